@@ -113,8 +113,14 @@ enum {
                                   outputs are incomplete                 */
   CCONV_DERR_ROW_INDEX = 16,   /* fused entry points / checkpoint export: a
                                   logical row maps outside [0, num_rows) */
-  CCONV_DERR_CHECKPOINT = 32   /* checkpoint export: request, offset or
+  CCONV_DERR_CHECKPOINT = 32,  /* checkpoint export: request, offset or
                                   slot out of range                      */
+  CCONV_DERR_POSITION = 64,    /* attn_norm_rope_cache: positions[t] or
+                                  slot_mapping[t] out of range           */
+  CCONV_DERR_PAGE = 128,       /* attn_decode: a block_table entry that a
+                                  request's length reaches is out of range */
+  CCONV_DERR_SEQ_LEN = 256     /* attn_decode: seq_lens[s] negative or beyond
+                                  the block table                        */
 };
 
 /* [slot, channel, column] view of a conv-state pool (element strides). */
@@ -434,6 +440,192 @@ CCONV_API int cca_qk_conv_noalloc(const void* qk, int64_t qk_row_stride, const v
                         int32_t Cqk, int32_t dtype, void* out_qk, int64_t out_qk_row_stride,
                         void* out_delayed_prev, int64_t out_delayed_prev_row_stride,
                         int32_t* dev_err, cconv_stream_t stream);
+
+/*
+ * State pool of the gated delta rule: a [slot, value head, dk, dv] view whose
+ * last two dimensions are contiguous (dv fastest).
+ */
+typedef struct gdn_state {
+  void* p;           /* 16-byte aligned                                      */
+  int64_t s_slot;    /* element strides of slots and heads (multiples of the */
+  int64_t s_head;    /* 16-byte vector; s_head >= dk * dv)                   */
+  int32_t num_slots;
+  int32_t dtype;     /* CCONV_DTYPE_F32 or CCONV_DTYPE_BF16                  */
+} gdn_state_t;
+
+/*
+ * gdn_fwd_varlen -- the gated delta rule over a packed varlen batch, reading
+ * and writing each sequence's state: the step after the GDN layer's short
+ * convolution (prefill, and decodes passed as one-token sequences).
+ *
+ * Defined by: the gated delta rule (Yang, Kautz, Hatamizadeh, "Gated Delta
+ * Networks", 2024) with the gates of its layers. The GDN page calls the core
+ * after its conv (_spec_aware_nonspec: gating, then the chunked rule for
+ * prefills and the recurrent one for decodes) and leaves its arithmetic out.
+ *
+ * For token t and value head h, with k and q of head h / (num_v_heads /
+ * num_k_heads):
+ *   alpha = exp(-exp(A_log[h]) * softplus(a[t,h] + dt_bias[h])),
+ *   beta  = sigmoid(b[t,h]),
+ *   q, k  divided by sqrt(sum of squares + 1e-6) if qk_l2norm,
+ *   S     = alpha * S;  S += beta * k (v - S^T k)^T;   out = scale * S^T q
+ * over the state S [dk, dv] of slot state_idx[s] (zeros if !has_init[s]), which
+ * then holds the last token's S. Everything between the loads and the stores
+ * is held in fp32 or in sums of two bf16 terms (about 16 bits); the state is
+ * rounded once, when it is stored.
+ *
+ *   q, k         [num_tokens, num_k_heads * dk]; v, out [num_tokens,
+ *                num_v_heads * dv]; row strides in elements (>= the row,
+ *                multiples of the 16-byte vector); 16-byte aligned. Views of
+ *                one row of channels, as the conv writes it, are fine. out
+ *                must not alias the inputs.
+ *   a, b         [num_tokens, num_v_heads] with row strides (any >= num_v_heads),
+ *                of the call's dtype
+ *   A_log, dt_bias  fp32 [num_v_heads]
+ *   states       pool, read and written in place; its type is its own
+ *   state_idx, cu_seqlens, has_init   as cconv_fwd_varlen (a padding row
+ *                starts from zeros and stores no state)
+ *   num_v_heads  a multiple of num_k_heads; dk, dv each 64 or 128 (others
+ *                return CCONV_ERR_UNSUPPORTED)
+ * An empty sequence leaves its slot as it is with has_init, zeros without.
+ * Errors on the device: CCONV_DERR_SLOT_RANGE, CCONV_DERR_CU_SEQLENS,
+ * CCONV_DERR_TIMEOUT.
+ */
+CCONV_API int gdn_fwd_varlen(const void* q, int64_t q_row_stride, const void* k,
+                   int64_t k_row_stride, const void* v, int64_t v_row_stride, const void* a,
+                   int64_t a_row_stride, const void* b, int64_t b_row_stride,
+                   const float* A_log, const float* dt_bias, gdn_state_t states,
+                   const int32_t* state_idx, const int32_t* cu_seqlens,
+                   const uint8_t* has_init, int32_t num_seqs, int32_t num_tokens,
+                   int32_t num_k_heads, int32_t num_v_heads, int32_t dk, int32_t dv,
+                   float scale, int32_t qk_l2norm, int32_t dtype, void* out,
+                   int64_t out_row_stride, int32_t* dev_err, cconv_stream_t stream);
+
+/*
+ * gdn_update -- the same rule for decode (n_spec == 0) or speculative decode
+ * (n_spec > 0: q_len = 1 + n_spec tokens per request, rows [s*q_len,
+ * s*q_len + q_len)).
+ *
+ * Defined by: the same; the GDN page's _spec_forward runs a "multi-slot"
+ * recurrence, one state slot a draft token, so that a rejected draft is undone
+ * by starting from an earlier slot.
+ *
+ *   state_idx    int32 [num_seqs, 1 + n_spec]: the state after token i is
+ *                stored in slot state_idx[s][i] (not where that is negative);
+ *                the request starts from slot state_idx[s][num_accepted[s] - 1]
+ *                (zeros if that is negative or !has_init[s]). Non-negative
+ *                entries of different requests must differ.
+ *   num_accepted int32 [num_seqs] in [1, 1 + n_spec]; required when n_spec > 0,
+ *                else ignored
+ *   n_spec       0..7
+ * Other arguments as gdn_fwd_varlen. Errors on the device:
+ * CCONV_DERR_SLOT_RANGE, CCONV_DERR_NUM_ACCEPTED (the request is skipped).
+ */
+CCONV_API int gdn_update(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride,
+               const void* v, int64_t v_row_stride, const void* a, int64_t a_row_stride,
+               const void* b, int64_t b_row_stride, const float* A_log, const float* dt_bias,
+               gdn_state_t states, const int32_t* state_idx, int32_t num_seqs, int32_t n_spec,
+               const int32_t* num_accepted, const uint8_t* has_init, int32_t num_k_heads,
+               int32_t num_v_heads, int32_t dk, int32_t dv, float scale, int32_t qk_l2norm,
+               int32_t dtype, void* out, int64_t out_row_stride, int32_t* dev_err,
+               cconv_stream_t stream);
+
+/*
+ * Paged key-value cache: k and v as [page, token of the page, kv head,
+ * head_dim] views of the same strides (elements; multiples of the 16-byte
+ * vector; head_dim contiguous). Both [pages, page_size, heads, dim] and
+ * [pages, heads, page_size, dim] storage are such views. Strides and page
+ * numbers are combined in 64 bits.
+ */
+typedef struct kv_cache {
+  void* k;           /* 16-byte aligned */
+  void* v;
+  int64_t s_page, s_token, s_head;
+  int32_t num_pages, page_size, num_kv_heads, head_dim;
+  int32_t dtype;     /* the call's dtype (another one: CCONV_ERR_UNSUPPORTED) */
+} kv_cache_t;
+
+/*
+ * attn_norm_rope_cache -- per-head RMS norm of queries and keys, their
+ * rotation by position, and the write of keys and values into the paged cache,
+ * in one pass over [query | key | value] rows as cca_qk_conv_fused writes them.
+ *
+ * Defined by: RMS norm (Zhang, Sennrich 2019) and rotary position embedding
+ * (Su et al. 2021). For each token t and head, x the head's head_dim values:
+ *   y = x / sqrt(mean(x^2) + eps) * weight           (q_weight or k_weight;
+ *                                                     y = x where it is NULL)
+ *   then over the first rot_dim values, with c_i, s_i = cos_sin[positions[t]]
+ *   [i], [rot_dim/2 + i], i < rot_dim/2, for the pair (y_i, y_{i + rot_dim/2})
+ *   or, if interleaved, (y_2i, y_{2i+1}):
+ *     (y0, y1) -> (y0 c - y1 s, y1 c + y0 s)
+ * computed in fp32 and rounded once. q goes to q_out, k to the cache's k and v
+ * unchanged to its v at slot_mapping[t] = page * page_size + token of the page.
+ *
+ *   q            [num_tokens, num_q_heads * head_dim], k, v [num_tokens,
+ *                num_kv_heads * head_dim] with row strides (multiples of the
+ *                16-byte vector); q_out like q (it may be q itself)
+ *   q_weight, k_weight  [head_dim] of the call's dtype, or NULL
+ *   cos_sin      fp32 [max_position, rot_dim] contiguous; positions int32
+ *   rot_dim      0..head_dim, even; when not interleaved a multiple of two
+ *                16-byte vectors (16 bf16, 8 fp32)
+ *   slot_mapping int32 [num_tokens], distinct; negative: a padding row, whose
+ *                q_out is written and whose k and v are not
+ *   head_dim     64, 128 or 256
+ * A position outside [0, max_position) or a slot beyond the cache sets
+ * CCONV_DERR_POSITION and that token is skipped.
+ */
+CCONV_API int attn_norm_rope_cache(const void* q, int64_t q_row_stride, const void* k,
+                         int64_t k_row_stride, const void* v, int64_t v_row_stride,
+                         const void* q_weight, const void* k_weight, float eps,
+                         const float* cos_sin, int32_t max_position, int32_t rot_dim,
+                         int32_t interleaved, const int32_t* positions, kv_cache_t cache,
+                         const int32_t* slot_mapping, int32_t num_tokens,
+                         int32_t num_q_heads, int32_t dtype, void* q_out,
+                         int64_t q_out_row_stride, int32_t* dev_err, cconv_stream_t stream);
+
+/*
+ * attn_decode -- attention of the new token of each request (or of its
+ * q_len = 1 + n_spec tokens) over a paged cache, split over the cached length
+ * and joined.
+ *
+ * Defined by: softmax attention with shared key-value heads. Query row i of
+ * request s (rows [s*q_len, s*q_len + q_len) of q and out) is at position
+ * seq_lens[s] - q_len + i and sees the cached positions up to its own, n_i =
+ * seq_lens[s] - (q_len - 1 - i) of them; position j lies in page
+ * block_table[s][j / page_size]. Per query head h over kv head h / (num_q_heads
+ * / num_kv_heads):
+ *   out = sum_j softmax_j(scale * q.k_j) v_j,  lse = log sum_j exp(scale * q.k_j)
+ * Scores, softmax statistics and sums are fp32; the bf16 kernel rounds the
+ * softmax weights to bf16 for the product with v. A row that sees nothing gets
+ * out = 0 and lse = -inf.
+ *
+ *   q, out       [num_seqs * q_len, num_q_heads * head_dim], row strides
+ *   block_table  int32 [num_seqs, table_width] with row stride
+ *                block_table_row_stride; entries beyond a request's length are
+ *                not read
+ *   seq_lens     int32 [num_seqs]: cached tokens, the new ones included
+ *   lse          fp32 [num_seqs * q_len, num_q_heads] or NULL
+ *   n_spec       0..7; head_dim 64, 128 or 256; (num_q_heads / num_kv_heads) *
+ *                q_len <= 64
+ *   workspace    attn_decode_workspace_bytes() of device memory, 16-byte
+ *                aligned; holds nothing between calls, and calls that may
+ *                overlap need one each
+ * A page number outside the cache sets CCONV_DERR_PAGE, and the positions of
+ * that page are left out; a seq_lens entry that is negative or longer than the
+ * block table sets CCONV_DERR_SEQ_LEN, and the request is skipped.
+ */
+CCONV_API int attn_decode(const void* q, int64_t q_row_stride, kv_cache_t cache,
+                const int32_t* block_table, int64_t block_table_row_stride, int32_t table_width,
+                const int32_t* seq_lens, int32_t num_seqs, int32_t n_spec, int32_t num_q_heads,
+                float scale, int32_t dtype, void* out, int64_t out_row_stride, float* lse,
+                void* workspace, int64_t workspace_bytes, int32_t* dev_err,
+                cconv_stream_t stream);
+
+/* Workspace of an attn_decode call of these sizes on the current device; a
+ * negative status where they are out of range. */
+CCONV_API int64_t attn_decode_workspace_bytes(int32_t num_seqs, int32_t n_spec,
+                                              int32_t num_q_heads, int32_t num_kv_heads,
+                                              int32_t head_dim);
 
 /* Static English text for a status code. */
 CCONV_API const char* cconv_status_string(int status);

@@ -22,6 +22,7 @@ DTYPE_F32, DTYPE_BF16 = 0, 1
 ACT_NONE, ACT_SILU = 0, 1
 DERR_SLOT_RANGE, DERR_CU_SEQLENS, DERR_NUM_ACCEPTED, DERR_TIMEOUT = 1, 2, 4, 8
 DERR_ROW_INDEX, DERR_CHECKPOINT = 16, 32
+DERR_POSITION, DERR_PAGE, DERR_SEQ_LEN = 64, 128, 256
 
 _lock = threading.Lock()
 _lib = None
@@ -43,6 +44,21 @@ class Pool(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
+class GdnState(ctypes.Structure):
+    """gdn_state_t: [slot, value head, dk, dv] view of a gated-delta-rule state pool."""
+    _fields_ = [("p", ctypes.c_void_p), ("s_slot", ctypes.c_int64), ("s_head", ctypes.c_int64),
+                ("num_slots", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class KvCache(ctypes.Structure):
+    """kv_cache_t: [page, token, kv head, head_dim] views of a paged k and v cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("s_page", ctypes.c_int64),
+                ("s_token", ctypes.c_int64), ("s_head", ctypes.c_int64),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
 class CConvError(RuntimeError):
     def __init__(self, fn, status):
         super().__init__(f"{fn}: status {status} ({status_string(status)})")
@@ -52,6 +68,8 @@ class CConvError(RuntimeError):
 def load():
     """Load libcconv.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -84,6 +102,22 @@ def load():
                                           P, I64, Pool, P, I64, P, P, P, I32, I32, I32, I32, P,
                                           I64, P, P]
         lib.cca_qk_conv_fused.restype = ctypes.c_int
+        F32 = ctypes.c_float
+        lib.gdn_fwd_varlen.argtypes = [P, I64, P, I64, P, I64, P, I64, P, I64, P, P, GdnState, P,
+                                       P, P, I32, I32, I32, I32, I32, I32, F32, I32, I32, P,
+                                       I64, P, P]
+        lib.gdn_fwd_varlen.restype = ctypes.c_int
+        lib.gdn_update.argtypes = [P, I64, P, I64, P, I64, P, I64, P, I64, P, P, GdnState, P, I32,
+                                   I32, P, P, I32, I32, I32, I32, F32, I32, I32, P, I64, P, P]
+        lib.gdn_update.restype = ctypes.c_int
+        lib.attn_norm_rope_cache.argtypes = [P, I64, P, I64, P, I64, P, P, F32, P, I32, I32, I32,
+                                             P, KvCache, P, I32, I32, I32, P, I64, P, P]
+        lib.attn_norm_rope_cache.restype = ctypes.c_int
+        lib.attn_decode.argtypes = [P, I64, KvCache, P, I64, I32, P, I32, I32, I32, F32, I32, P,
+                                    I64, P, P, I64, P, P]
+        lib.attn_decode.restype = ctypes.c_int
+        lib.attn_decode_workspace_bytes.argtypes = [I32, I32, I32, I32, I32]
+        lib.attn_decode_workspace_bytes.restype = I64
         lib.cconv_status_string.argtypes = [ctypes.c_int]
         lib.cconv_status_string.restype = ctypes.c_char_p
         lib.cconv_abi_version.argtypes = []
@@ -323,3 +357,225 @@ def cca_qk_conv_fused(qk, w_dw, b_dw, w_gr, b_gr, groups, num_q_heads, t0, t1, d
         _ptr(out), _rows(out), _ptr(dev_err), _stream(stream))
     _check("cca_qk_conv_fused", rc)
 
+
+
+# ---- the mixers behind the convolutions --------------------------------------
+# A decode step's calls are short, so these read each tensor's sizes and strides
+# once, check them, and hand plain integers to the library.
+
+_CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _raw(*tensors):
+    """Device addresses (None for None)."""
+    got = []
+    for t in tensors:
+        if t is None:
+            got.append(None)
+        elif t.is_cuda:
+            got.append(t.data_ptr())
+        else:
+            raise ValueError("tensors passed to libcconv must live on the GPU")
+    return got
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _heads(t, name, dtype, rows, heads=None, dim=None):
+    """(heads, dim, row stride) of a [rows, heads, dim] tensor whose rows are contiguous."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must have the call's dtype")
+    s, st = t.shape, t.stride()
+    if len(s) != 3 or st[2] != 1 or (st[1] != s[2] and s[1] > 1):
+        raise ValueError(f"{name} must be [rows, heads, dim] with contiguous rows")
+    n, h, d = s
+    if n < rows or (heads is not None and (h != heads or d != dim)):
+        raise ValueError(f"{name} has the wrong rows, heads or head size")
+    return h, d, (st[0] if n > 1 else max(st[0], h * d))
+
+
+def _vector(t, name, dtype, n):
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n}")
+
+
+def _gates(t, name, dtype, rows, hv):
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must have the call's dtype")
+    s, st = t.shape, t.stride()
+    if len(s) != 2 or s[0] < rows or s[1] != hv or (hv > 1 and st[1] != 1):
+        raise ValueError(f"{name} must be [rows, value heads] with contiguous rows")
+    return st[0] if s[0] > 1 else max(st[0], hv)
+
+
+def _gdn_call(fn, q, k, v, a, b, A_log, dt_bias, states, out, rows, scale, l2norm, stream, dev_err,
+              index, middle):
+    """index: the int32/uint8 tensors after the pool; middle(addresses) -> the C arguments between
+    the pool and the head counts."""
+    dtype = k.dtype
+    hk, dk, ks = _heads(k, "k", dtype, rows)
+    hv, dv, vs = _heads(v, "v", dtype, rows)
+    qs = _heads(q, "q", dtype, rows, hk, dk)[2]
+    os_ = _heads(out, "out", dtype, rows, hv, dv)[2]
+    a_s, b_s = _gates(a, "a", dtype, rows, hv), _gates(b, "b", dtype, rows, hv)
+    _vector(A_log, "A_log", torch.float32, hv)
+    _vector(dt_bias, "dt_bias", torch.float32, hv)
+    s, st = states.shape, states.stride()
+    if len(s) != 4 or s[1] != hv or s[2] != dk or s[3] != dv or st[3] != 1 or st[2] != dv:
+        raise ValueError("states must be [slots, value heads, dk, dv], the last two contiguous")
+    code, st_code = _CODES.get(dtype), _CODES.get(states.dtype)
+    if code is None or st_code is None:
+        raise TypeError(f"unsupported dtype {dtype} or {states.dtype}")
+    P = _raw(q, k, v, a, b, A_log, dt_bias, states, out, dev_err, *index)
+    # a pool of one slot or one head may carry any stride there
+    pool = GdnState(P[7], st[0] if s[0] > 1 else max(st[0], hv * dk * dv),
+                    st[1] if hv > 1 else max(st[1], dk * dv), s[0], st_code)
+    rc = getattr(load(), fn)(P[0], qs, P[1], ks, P[2], vs, P[3], a_s, P[4], b_s, P[5], P[6], pool,
+                             *middle(P[10:]), hk, hv, dk, dv, scale, l2norm, code, P[8], os_, P[9],
+                             _raw_stream(stream))
+    if rc != OK:
+        raise CConvError(fn, rc)
+
+
+def gdn_fwd_varlen(q, k, v, a, b, A_log, dt_bias, states, state_idx, cu_seqlens, has_init, scale,
+                   out, qk_l2norm=True, dev_err=None, stream=None, num_tokens=None):
+    """Gated delta rule over a packed varlen batch (see gdn_fwd_varlen in cconv.h).
+
+    q, k: [T, Hk, dk]; v, out: [T, Hv, dv]; a, b: [T, Hv] raw gate projections; A_log,
+    dt_bias: fp32 [Hv]; states: [slots, Hv, dk, dv] fp32 or bf16, updated in place;
+    state_idx/cu_seqlens: int32; has_init: uint8/bool or None.
+    """
+    _i32(state_idx, "state_idx")
+    _i32(cu_seqlens, "cu_seqlens")
+    _u8(has_init, "has_init")
+    T = q.shape[0] if num_tokens is None else int(num_tokens)
+    B = state_idx.shape[0]
+    if cu_seqlens.shape[0] != B + 1:
+        raise ValueError("cu_seqlens must have one entry more than state_idx")
+    _gdn_call("gdn_fwd_varlen", q, k, v, a, b, A_log, dt_bias, states, out, T, scale,
+              1 if qk_l2norm else 0, stream, dev_err, (state_idx, cu_seqlens, has_init),
+              lambda P: (P[0], P[1], P[2], B, T))
+
+
+def gdn_update(q, k, v, a, b, A_log, dt_bias, states, state_idx, n_spec, num_accepted, has_init,
+               scale, out, qk_l2norm=True, dev_err=None, stream=None):
+    """Gated delta rule for decode / speculative decode (see gdn_update in cconv.h).
+
+    Rows [s*(1+n_spec), (s+1)*(1+n_spec)) belong to request s; state_idx: int32 [B, 1+n_spec]
+    (or [B] when n_spec is 0), the slot of the state after each token; num_accepted: int32 [B]
+    when n_spec > 0.
+    """
+    _i32(state_idx, "state_idx")
+    _i32(num_accepted, "num_accepted")
+    _u8(has_init, "has_init")
+    B = state_idx.shape[0]
+    if state_idx.numel() != B * (1 + n_spec) or not state_idx.is_contiguous():
+        raise ValueError("state_idx must be a contiguous [requests, 1 + n_spec]")
+    _gdn_call("gdn_update", q, k, v, a, b, A_log, dt_bias, states, out, B * (1 + n_spec), scale,
+              1 if qk_l2norm else 0, stream, dev_err, (state_idx, num_accepted, has_init),
+              lambda P: (P[0], B, n_spec, P[1], P[2]))
+
+
+def _cache(k_cache, v_cache, dtype):
+    """(shape, strides, dtype code) of a paged cache's two views."""
+    s, st = k_cache.shape, k_cache.stride()
+    if len(s) != 4 or v_cache.shape != s or st[3] != 1:
+        raise ValueError("caches must be [pages, page_size, kv heads, head_dim] of one shape")
+    if v_cache.stride() != st:
+        raise ValueError("k_cache and v_cache must have the same strides")
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
+        raise TypeError("the caches must have q's dtype")
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    # a dimension of one entry may carry any stride
+    st = [x if n > 1 else max(x, s[3]) for x, n in zip(st, s)]
+    return s, st, code
+
+
+def attn_norm_rope_cache(q, k, v, q_weight, k_weight, eps, cos_sin, positions, interleaved,
+                         k_cache, v_cache, slot_mapping, q_out, dev_err=None, stream=None):
+    """Head norm, rotation and cache write (see attn_norm_rope_cache in cconv.h).
+
+    q, q_out: [T, Hq, D]; k, v: [T, Hkv, D]; q_weight, k_weight: [D] or None; cos_sin: fp32
+    [max_position, rot_dim], the cosines then the sines; caches: [pages, page_size, Hkv, D]
+    views (any order of storage with contiguous D); positions, slot_mapping: int32 [T].
+    """
+    _i32(positions, "positions")
+    _i32(slot_mapping, "slot_mapping")
+    dtype = q.dtype
+    (pages, page, hkv, dim), st, code = _cache(k_cache, v_cache, dtype)
+    T, hq = q.shape[0], q.shape[1]
+    qs = _heads(q, "q", dtype, T, hq, dim)[2]
+    ks = _heads(k, "k", dtype, T, hkv, dim)[2]
+    vs = _heads(v, "v", dtype, T, hkv, dim)[2]
+    os_ = _heads(q_out, "q_out", dtype, T, hq, dim)[2]
+    if positions.shape[0] < T or slot_mapping.shape[0] < T:
+        raise ValueError("positions and slot_mapping must have q's rows")
+    if q_weight is not None:
+        _vector(q_weight, "q_weight", dtype, dim)
+    if k_weight is not None:
+        _vector(k_weight, "k_weight", dtype, dim)
+    if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise TypeError("cos_sin must be contiguous float32 [max_position, rot_dim]")
+    P = _raw(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_cache, slot_mapping, q_out,
+             dev_err)
+    cache = KvCache(P[7], P[8], st[0], st[1], st[2], pages, page, hkv, dim, code)
+    rc = load().attn_norm_rope_cache(P[0], qs, P[1], ks, P[2], vs, P[3], P[4], eps, P[5],
+                                     cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0,
+                                     P[6], cache, P[9], T, hq, code, P[10], os_, P[11],
+                                     _raw_stream(stream))
+    if rc != OK:
+        raise CConvError("attn_norm_rope_cache", rc)
+
+
+def attn_decode_workspace_bytes(num_seqs, n_spec, num_q_heads, num_kv_heads, head_dim):
+    """Bytes of workspace of an attn_decode call of these sizes."""
+    n = load().attn_decode_workspace_bytes(num_seqs, n_spec, num_q_heads, num_kv_heads, head_dim)
+    if n < 0:
+        raise CConvError("attn_decode_workspace_bytes", n)
+    return n
+
+
+def attn_decode(q, k_cache, v_cache, block_table, seq_lens, n_spec, scale, out, lse=None,
+                workspace=None, dev_err=None, stream=None):
+    """Attention of new tokens over a paged cache (see attn_decode in cconv.h).
+
+    q, out: [B*(1+n_spec), Hq, D]; block_table: int32 [B, width]; seq_lens: int32 [B], the
+    cached tokens with the new ones; lse: fp32 [B*(1+n_spec), Hq] or None; workspace: a uint8
+    tensor of attn_decode_workspace_bytes() or None (allocated for the call).
+    """
+    _i32(block_table, "block_table")
+    _i32(seq_lens, "seq_lens")
+    dtype = q.dtype
+    (pages, page, hkv, dim), st, code = _cache(k_cache, v_cache, dtype)
+    B = seq_lens.shape[0]
+    rows, hq = B * (1 + n_spec), q.shape[1]
+    qs = _heads(q, "q", dtype, rows, hq, dim)[2]
+    os_ = _heads(out, "out", dtype, rows, hq, dim)[2]
+    ts, tst = block_table.shape, block_table.stride()
+    if len(ts) != 2 or ts[0] < B or (ts[1] > 1 and tst[1] != 1):
+        raise ValueError("block_table must be [requests, width] with contiguous rows")
+    if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous()
+                            or lse.shape[0] < rows or lse.shape[1:] != (hq,)):
+        raise ValueError("lse must be contiguous float32 [rows, heads]")
+    P = _raw(q, k_cache, v_cache, block_table, seq_lens, out, lse, workspace, dev_err)
+    if workspace is None:
+        need = attn_decode_workspace_bytes(B, n_spec, hq, hkv, dim)
+        if stream is None:
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        else:
+            with torch.cuda.stream(stream):     # the call's stream owns it
+                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        P[7] = workspace.data_ptr()
+    cache = KvCache(P[1], P[2], st[0], st[1], st[2], pages, page, hkv, dim, code)
+    rc = load().attn_decode(P[0], qs, cache, P[3], tst[0] if ts[0] > 1 else max(tst[0], ts[1]),
+                            ts[1], P[4], B, n_spec, hq, scale, code, P[5], os_, P[6], P[7],
+                            workspace.numel() * workspace.element_size(), P[8],
+                            _raw_stream(stream))
+    if rc != OK:
+        raise CConvError("attn_decode", rc)
