@@ -45,4 +45,8 @@ __device__ __forceinline__ bool gdn_bounds(const GdnArgs& a, int s, int& st, int
 cudaError_t gdn_launch_step(const GdnArgs& a, int dtype, int state_dtype, int dk, int dv,
                             cudaStream_t st);
 
+// Chunked kernel (bf16, dk = dv = 128) over the sequences longer than
+// a.max_len; see gdn_chunk.cu.
+cudaError_t gdn_launch_chunk(const GdnArgs& a, int state_dtype, cudaStream_t st);
+
 }  // namespace cconv

@@ -39,6 +39,7 @@ namespace {
 constexpr int kCols = 32;      // state columns of a block
 constexpr int kTok = 8;        // tokens staged at a time
 constexpr int kStepThreads = 128;
+constexpr int kStepMax = 8;    // longest sequence of this kernel where the chunked one serves
 
 template <typename T, typename ST, int DK>
 __global__ void __launch_bounds__(kStepThreads)
@@ -313,9 +314,17 @@ extern "C" int gdn_fwd_varlen(const void* q, int64_t q_row_stride, const void* k
   o.cu = cu_seqlens;
   o.num_acc = nullptr;
   o.q_len = 0;
-  const cudaError_t e = gdn_launch_step(o, dtype, states.dtype, dk, dv,
-                                        reinterpret_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // sequences of more than kStepMax tokens go chunk by chunk where there is a
+  // kernel for it; a call of no more tokens than that has none
+  const bool chunked = dtype == CCONV_DTYPE_BF16 && dk == 128 && dv == 128 &&
+                       num_tokens > kStepMax;
+  if (chunked) {
+    o.max_len = kStepMax;
+    if (gdn_launch_chunk(o, states.dtype, st) != cudaSuccess) return CCONV_ERR_LAUNCH;
+  }
+  return gdn_launch_step(o, dtype, states.dtype, dk, dv, st) == cudaSuccess ? CCONV_OK
+                                                                           : CCONV_ERR_LAUNCH;
 }
 
 extern "C" int gdn_update(const void* q, int64_t q_row_stride, const void* k,
