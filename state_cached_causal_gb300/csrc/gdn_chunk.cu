@@ -54,37 +54,51 @@ namespace {
 constexpr int kC = 64;                       // tokens of a chunk
 constexpr int kD = 128;                      // dk = dv
 constexpr int kStages = 3;
-constexpr int kScanWarps = 8, kPrepWarps = 4;
-constexpr int kWarpPrep0 = kScanWarps, kWarpMma = kWarpPrep0 + kPrepWarps,
-              kWarpLoad = kWarpMma + 1;
+// Warpgroups: two on the chain, one for A and the scores, and one of two warps
+// for T, one that issues the tensor products and one that loads; registers a
+// thread of each (their sum is the block's 512 x 128).
+constexpr int kScanWarps = 8, kPrepWarps = 4, kInvWarps = 2;
+constexpr int kWarpPrep0 = kScanWarps, kWarpInv0 = kWarpPrep0 + kPrepWarps,
+              kWarpMma = kWarpInv0 + kInvWarps, kWarpLoad = kWarpMma + 1;
 constexpr int kThreadsC = (kWarpLoad + 1) * 32;
+constexpr int kRegsScan = 160, kRegsPrep = 104, kRegsRest = 88;
+static_assert(kThreadsC == 512 && 2 * kRegsScan + kRegsPrep + kRegsRest <= 4 * 128,
+              "a split over the block's own registers would wait forever");
 
 constexpr uint32_t kPanel = 128 * 128;       // 64 dk of [K; Q]: 128 rows x 128 bytes
 constexpr uint32_t kKQBytes = 2 * kPanel;
-constexpr uint32_t kVBytes = kC * kD * 2;
+constexpr uint32_t kVPanel = kC * 128;       // 64 dv of V
+constexpr uint32_t kVBytes = kC * kD * 2;    // V, later the chunk's outputs [64][128]
 constexpr uint32_t kStageBytes = kKQBytes + kVBytes;
 constexpr uint32_t kTBytes = kC * kC * 2;    // one 64 x 64 bf16 operand
 constexpr uint32_t kTP = 3 * kTBytes;        // T hi, T lo, scores
 constexpr int kAPitch = 68;                  // fp32 rows of A (16-byte aligned)
+constexpr int kB = 16;                       // blocks of T
+constexpr int kBPitch = 20;                  // fp32 rows of 16 (16-byte aligned)
 
-constexpr uint32_t kColS = 0, kColKS = 128, kColQS = 192, kColR = 256, kColN = 320, kColO = 352,
-                   kColD1 = 416;
+constexpr uint32_t kColS = 0, kColKS = 128, kColN = kColKS, kColQS = 192, kColR = 256,
+                   kColVN = 320, kColO = 384, kColD1 = 448;
 
 // A wait that has run out of this many clocks (seconds) gives the block up.
 constexpr long long kWaitClocks = 4000000000LL;
 
-struct alignas(16) Gates {   // read four at a time
-  float rb[kC];      // beta
-  float rc[kC];      // beta e^G / |k|
+// Per-token factors of a chunk for the warps on the chain (read four at a time).
+struct alignas(16) Coef {
+  float rc[kC];      // -e^G / |k|
   float vd[kC];      // e^{G_C - G} / |k|
   float o1[kC];      // scale e^G / |q|
   float o2[kC];      // scale / |q|
   float ec;          // e^{G_C}
 };
+// Gates of a chunk: sum of log2 decays (whole part, remainder) and beta.
+struct alignas(16) Gate {
+  float hi[kC], lo[kC], beta[kC];
+};
 
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
-  uint64_t d1_full, g_full, t_full, tp_empty[2], arr_empty[2];
+  uint64_t gate_empty[2], tp_empty[2], coef_full[2], coef_empty[2];
+  uint64_t d1_full, a_full, a_empty, t_full, prep_meet, inv_meet;
   uint64_t s_full, ks_full, qs_done, r_full, vn_full, vd_full, sd_full, o_full, o_empty, fin;
   uint32_t tmem;
   volatile int abort;
@@ -94,20 +108,22 @@ struct Smem {
   unsigned char stage[kStages][kStageBytes];   // 1024-byte aligned
   unsigned char tp[2][kTP];
   alignas(16) float A[kC][kAPitch];
-  alignas(16) float X[32][36];            // A21 T11 of the block step
-  Gates gates[2];
-  alignas(16) float rk[kC];
-  alignas(16) float g_hi[kC];
-  alignas(16) float g_lo[kC];
+  alignas(16) float Td[4][kB][kBPitch];        // inverses of the diagonal blocks
+  alignas(16) float ed[kC][kBPitch];           // e^{G_i - G_j} / |k_j|, j in the block of i
+  alignas(16) float tab[4][kC];                // e^{G_(16I-1) - G_j} / |k_j|, j < 16 I
+  alignas(16) float rn[2 * kC];                // 1 / |k|, 1 / |q|
+  Coef coef[2];
+  Gate gate[2];
   Ctl ctl;
 };
 static_assert(offsetof(Smem, tp) % 1024 == 0 && kStageBytes % 1024 == 0 && kTP % 1024 == 0 &&
-                  kTBytes % 1024 == 0,
+                  kTBytes % 1024 == 0 && kVPanel % 1024 == 0,
               "swizzled tiles start on 1024 bytes");
-static_assert(sizeof(Gates) % 16 == 0 && offsetof(Smem, A) % 16 == 0 &&
-                  offsetof(Smem, X) % 16 == 0 && offsetof(Smem, gates) % 16 == 0 &&
-                  offsetof(Smem, rk) % 16 == 0 && offsetof(Smem, g_hi) % 16 == 0 &&
-                  offsetof(Smem, g_lo) % 16 == 0 && offsetof(Smem, ctl) % 8 == 0,
+static_assert(sizeof(Coef) % 16 == 0 && sizeof(Gate) % 16 == 0 && offsetof(Smem, A) % 16 == 0 &&
+                  offsetof(Smem, Td) % 16 == 0 && offsetof(Smem, ed) % 16 == 0 &&
+                  offsetof(Smem, tab) % 16 == 0 && offsetof(Smem, rn) % 16 == 0 &&
+                  offsetof(Smem, coef) % 16 == 0 && offsetof(Smem, gate) % 16 == 0 &&
+                  offsetof(Smem, ctl) % 8 == 0,
               "16-byte accesses");
 
 __device__ __forceinline__ uint32_t sw128(int row, int unit) {
@@ -117,25 +133,27 @@ __device__ __forceinline__ uint32_t sw128(int row, int unit) {
 struct Wait {
   Ctl* ctl;
   int32_t* err;
-  // Called by whole warps. False when the block is giving up.
+  // Called by whole warps. False when the block is giving up. In line: a call
+  // would spill the state's registers around it.
   __device__ __forceinline__ bool operator()(uint64_t* bar, int phase) const {
-    const bool done = mbar_try(bar, phase & 1);
-    if (__any_sync(0xffffffffu, done)) return true;
-    return loop(bar, phase & 1);
-  }
-  __device__ __noinline__ bool loop(uint64_t* bar, uint32_t parity) const {
-    const long long t0 = clock64();
-    for (uint32_t it = 0;; ++it) {
-      if (__any_sync(0xffffffffu, mbar_try(bar, parity))) return true;
-      if ((it & 63u) == 63u) {
-        if (__any_sync(0xffffffffu, ctl->abort != 0)) return false;
-        if (__any_sync(0xffffffffu, clock64() - t0 > kWaitClocks)) {
-          ctl->abort = 1;
-          if ((threadIdx.x & 31) == 0) flag_error(err, CCONV_DERR_TIMEOUT);
+    const uint32_t parity = phase & 1;
+    long long t0 = 0;
+#pragma unroll 1
+    for (uint32_t it = 1; !__any_sync(0xffffffffu, mbar_try(bar, parity)); ++it) {
+      if ((it & 63u) == 0) {
+        const long long now = clock64();
+        if (t0 == 0) t0 = now;
+        const bool late = now - t0 > kWaitClocks;
+        if (__any_sync(0xffffffffu, late || ctl->abort != 0)) {
+          if (late) {
+            ctl->abort = 1;
+            if ((threadIdx.x & 31) == 0) flag_error(err, CCONV_DERR_TIMEOUT);
+          }
           return false;
         }
       }
     }
+    return true;
   }
 };
 
@@ -143,223 +161,362 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
-__device__ __forceinline__ void prep_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kPrepWarps * 32) : "memory");
+// Meeting point of a role's warps (a barrier of the block that can be given up).
+struct Meet {
+  uint64_t* bar;
+  int phase;
+  __device__ __forceinline__ bool operator()(const Wait& wait) {
+    warp_arrive(bar);
+    return wait(bar, phase++);
+  }
+};
+template <int N>
+__device__ __forceinline__ void more_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// ---- the warps that look one chunk ahead ----------------------------------
+// ---- the warp that loads K, Q and V and works the gates out -----------------
 
-// Gates, norms, A, T and scores of every chunk. Thread p < 64 holds row p of
-// K K^T and token p's gates, thread 64 + p row p of Q K^T.
-__device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait& wait, int row0,
-                                          int len, int h, int chunks, uint32_t tmem) {
-  const int p = threadIdx.x - kWarpPrep0 * 32, lane = p & 31, warp = p >> 5;
-  const bool is_k = p < kC;
-  const int r = is_k ? p : p - kC;               // the thread's row
+// Per chunk: requests its rows, works its gates out while they come, and says
+// so when both are there (stages free up a chunk's time apart, which is longer
+// than a load takes). Gates: two tokens a lane (lane, lane + 32); their sums are
+// kept as whole part and remainder in (-1, 0], exact to 2^-24 of the remainder
+// however long the sum.
+__device__ __forceinline__ void load_role(const GdnArgs& a, Smem& sm, const Wait& wait, int row0,
+                                          int len, int h, int chunks) {
+  const int lane = threadIdx.x & 31, u = lane & 15, r2 = lane >> 4;
+  const int hk = h / (a.Hv / a.Hk);
+  const char* kp = a.k + ((int64_t)row0 * a.k_rs + (int64_t)hk * kD) * 2 + u * 16;
+  const char* qp = a.q + ((int64_t)row0 * a.q_rs + (int64_t)hk * kD) * 2 + u * 16;
+  const char* vp = a.v + ((int64_t)row0 * a.v_rs + (int64_t)h * kD) * 2 + u * 16;
   const float A_log2 = -expf(a.A_log[h]) * 1.4426950408889634f;
   const float dtb = a.dt_bias[h];
   const __nv_bfloat16* ga = reinterpret_cast<const __nv_bfloat16*>(a.a) + h;
   const __nv_bfloat16* gb = reinterpret_cast<const __nv_bfloat16*>(a.b) + h;
-  float na = 0.0f, nb = 0.0f;                    // the next chunk's gate inputs
-  if (is_k && r < len) {
-    na = elem(ga, (int64_t)(row0 + r) * a.a_rs);
-    nb = elem(gb, (int64_t)(row0 + r) * a.b_rs);
+  for (int n = 0; n < chunks; ++n) {
+    const int st = n % kStages;
+    if (n >= kStages && !wait(&sm.ctl.empty[st], n / kStages - 1)) return;
+    const uint32_t base = smem_addr(sm.stage[st]) + (u >> 3) * kPanel;
+    const uint32_t vbase = smem_addr(sm.stage[st]) + kKQBytes + (u >> 3) * kVPanel;
+    float na[2], nb[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = n * kC + i * 32 + lane;
+      na[i] = t < len ? elem(ga, (int64_t)(row0 + t) * a.a_rs) : 0.0f;
+      nb[i] = t < len ? elem(gb, (int64_t)(row0 + t) * a.b_rs) : 0.0f;
+    }
+#pragma unroll 8
+    for (int i = 0; i < kC / 2; ++i) {
+      const int r = i * 2 + r2;
+      const int64_t t = (int64_t)n * kC + r;
+      const bool in = t < len;
+      const int64_t tt = in ? t : 0;
+      cp_async16(base + sw128(r, u & 7), kp + tt * a.k_rs * 2, in);
+      cp_async16(base + sw128(kC + r, u & 7), qp + tt * a.q_rs * 2, in);
+      cp_async16(vbase + sw128(r, u & 7), vp + tt * a.v_rs * 2, in);
+    }
+    cp_async_commit();
+    float w[2], f[2], be[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool in = n * kC + i * 32 + lane < len;
+      const float x = na[i] + dtb;
+      float g = A_log2 * (fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))));
+      // a decay below 2^-150 is zero in fp32 whatever follows (a NaN stays one)
+      g = in ? (g < -150.0f ? -150.0f : g) : 0.0f;
+      be[i] = in ? gdn_beta(nb[i]) : 0.0f;
+      w[i] = truncf(g);
+      f[i] = g - w[i];
+    }
+    auto add = [](float& w0, float& f0, float w1, float f1) {
+      const float s = f0 + f1, c = truncf(s);
+      w0 += w1 + c;
+      f0 = s - c;
+    };
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float ow = __shfl_up_sync(0xffffffffu, w[i], d);
+        const float of = __shfl_up_sync(0xffffffffu, f[i], d);
+        if (lane >= d) add(w[i], f[i], ow, of);
+      }
+    add(w[1], f[1], __shfl_sync(0xffffffffu, w[0], 31), __shfl_sync(0xffffffffu, f[0], 31));
+    if (n >= 2 && !wait(&sm.ctl.gate_empty[n & 1], (n >> 1) - 1)) {
+      cp_async_wait<0>();      // nothing lands after the block ends
+      return;
+    }
+    Gate& G = sm.gate[n & 1];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      G.hi[i * 32 + lane] = w[i];
+      G.lo[i * 32 + lane] = f[i];
+      G.beta[i * 32 + lane] = be[i];
+    }
+    cp_async_wait<0>();
+    fence_proxy_async();
+    warp_arrive(&sm.ctl.full[st]);
   }
+}
+
+// ---- the warps that look one chunk ahead ------------------------------------
+
+// Element (i, j) of T times beta_j, as bf16 hi and lo.
+__device__ __forceinline__ void put_t(unsigned char* tp, int i, int j, float v) {
+  const uint32_t at = sw128(i, j >> 3) + (j & 7) * 2;
+  const uint32_t hb = pack_bf16x2(v, 0.0f);
+  *reinterpret_cast<uint16_t*>(tp + at) = (uint16_t)hb;
+  *reinterpret_cast<uint16_t*>(tp + kTBytes + at) =
+      (uint16_t)pack_bf16x2(v - __uint_as_float(hb << 16), 0.0f);
+}
+
+// The 16 x 16 blocks of T below diagonal block J. With U = T^T,
+//   U_Ji = -(sum_{J <= k < i} U_Jk A_ik^T) U_ii,
+// so that each result is the left operand of the next product, where the
+// output layout of one warp product is the input layout of the next, and A and
+// T_ii are read from shared memory along their rows. Products of hi and lo
+// parts as everywhere (lo * lo left out).
+template <int J>
+__device__ __forceinline__ void t_blocks(const Smem& sm, unsigned char* tp, const float* beta) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = (lane & 3) * 2;
+  uint32_t uh[4][4], ul[4][4];      // U_Jk as left operands
+  const float b0 = beta[J * kB + r], b1 = beta[J * kB + r + 8];
+  {
+    const float(*t)[kBPitch] = sm.Td[J];
+    tc::split2(t[c][r], t[c + 1][r], uh[J][0], ul[J][0]);
+    tc::split2(t[c][r + 8], t[c + 1][r + 8], uh[J][1], ul[J][1]);
+    tc::split2(t[c + 8][r], t[c + 9][r], uh[J][2], ul[J][2]);
+    tc::split2(t[c + 8][r + 8], t[c + 9][r + 8], uh[J][3], ul[J][3]);
+  }
+  // two sums, of the hi * hi and of the mixed products: shorter chains
+  auto times = [&](float(&acc)[2][4], float(&mix)[2][4], const uint32_t(&ah)[4],
+                   const uint32_t(&al)[4], const float* base, int pitch) {
+    // (rows n of `base` along k)
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      const float* q = base + (nt * 8 + r) * pitch + c;
+      const float2 x = *reinterpret_cast<const float2*>(q);
+      const float2 y = *reinterpret_cast<const float2*>(q + 8);
+      uint32_t h0, l0, h1, l1;
+      tc::split2(x.x, x.y, h0, l0);
+      tc::split2(y.x, y.y, h1, l1);
+      tc::mma16(acc[nt], ah, h0, h1);
+      tc::mma16(mix[nt], ah, l0, l1);
+      tc::mma16(mix[nt], al, h0, h1);
+    }
+  };
+#pragma unroll
+  for (int i = J + 1; i < 4; ++i) {
+    float x[2][4] = {}, xm[2][4] = {};
+#pragma unroll
+    for (int k = J; k < i; ++k) times(x, xm, uh[k], ul[k], &sm.A[i * kB][k * kB], kAPitch);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e >> 2][e & 3] += xm[e >> 2][e & 3];
+    uint32_t xh[4], xl[4];
+    tc::split2(x[0][0], x[0][1], xh[0], xl[0]);
+    tc::split2(x[0][2], x[0][3], xh[1], xl[1]);
+    tc::split2(x[1][0], x[1][1], xh[2], xl[2]);
+    tc::split2(x[1][2], x[1][3], xh[3], xl[3]);
+    float y[2][4] = {}, ym[2][4] = {};
+    times(y, ym, xh, xl, &sm.Td[i][0][0], kBPitch);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e >> 2][e & 3] += ym[e >> 2][e & 3];
+    if (i < 3) {
+      tc::split2(-y[0][0], -y[0][1], uh[i][0], ul[i][0]);
+      tc::split2(-y[0][2], -y[0][3], uh[i][1], ul[i][1]);
+      tc::split2(-y[1][0], -y[1][1], uh[i][2], ul[i][2]);
+      tc::split2(-y[1][2], -y[1][3], uh[i][3], ul[i][3]);
+    }
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)   // y[nt][e] = -U_Ji[m][n]
+        put_t(tp, i * kB + nt * 8 + c + (e & 1), J * kB + r + (e >> 1) * 8,
+              -y[nt][e] * ((e >> 1) ? b1 : b0));
+  }
+}
+
+// Norms, factors, A, scores and T of every chunk. Thread p < 64 holds row p of
+// K K^T, thread 64 + p row p of Q K^T.
+__device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait& wait,
+                                          int chunks, uint32_t tmem) {
+  const int p = threadIdx.x - kWarpPrep0 * 32, warp = p >> 5;
+  const bool is_k = p < kC;
+  const int r = p & (kC - 1), blk = r / kB;       // the thread's row and its block
+  Meet meet{&sm.ctl.prep_meet, 0};
   for (int n = 0; n < chunks; ++n) {
     const int st = n % kStages, bf = n & 1;
-    const int left = len - n * kC;                // tokens of this chunk (>= 64: whole)
-    Gates& G = sm.gates[bf];
-    // ---- gates (64 threads: two warps scan 64 tokens)
-    double g = 0.0;
-    float beta = 0.0f;
-    if (is_k && r < left) {
-      const float x = na + dtb;
-      const float d = A_log2 * (fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))));
-      // a decay below 2^-150 is zero in fp32 whatever follows (a NaN stays one)
-      g = (double)(d < -150.0f ? -150.0f : d);
-      beta = gdn_beta(nb);
-    }
-    if (is_k && left - kC > r) {
-      na = elem(ga, (int64_t)(row0 + (n + 1) * kC + r) * a.a_rs);
-      nb = elem(gb, (int64_t)(row0 + (n + 1) * kC + r) * a.b_rs);
-    }
-    if (warp < 2) {
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const double o = __shfl_up_sync(0xffffffffu, g, d);
-        if (lane >= d) g += o;
-      }
-      if (p == 31) {      // the first warp's sum, for the second one
-        const double w = trunc(g);
-        sm.X[0][0] = (float)w;
-        sm.X[0][1] = (float)(g - w);
-      }
-    }
-    // ---- the row's sum of squares
+    Coef& C = sm.coef[bf];
+    const Gate& G = sm.gate[bf];
+    // ---- norms
     if (!wait(&sm.ctl.full[st], n / kStages)) return;
-    float ss = 0.0f;
-    {
-      const unsigned char* base = sm.stage[st];
-      const int row = is_k ? r : kC + r;
+    float rn = 1.0f;
+    if (a.l2norm) {
+      float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll
       for (int u = 0; u < 16; ++u) {
-        float f[8];
-        unpack16<__nv_bfloat16>(
-            *reinterpret_cast<const uint4*>(base + (u >> 3) * kPanel + sw128(row, u & 7)), f);
+        const uint4 x = *reinterpret_cast<const uint4*>(sm.stage[st] + (u >> 3) * kPanel +
+                                                        sw128(p, u & 7));
+        const uint32_t q[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
+        for (int e = 0; e < 4; e += 2) {
+          const float a0 = __uint_as_float(q[e] << 16), a1 = __uint_as_float(q[e] & 0xffff0000u);
+          const float b0 = __uint_as_float(q[e + 1] << 16),
+                      b1 = __uint_as_float(q[e + 1] & 0xffff0000u);
+          fma_x2(s0, s1, a0, a1, a0, a1, s0, s1);
+          fma_x2(s2, s3, b0, b1, b0, b1, s2, s3);
+        }
+      }
+      rn = 1.0f / sqrtf((s0 + s1) + (s2 + s3) + kGdnNormEps);
+    }
+    sm.rn[p] = rn;
+    // the factors of two chunks ago have been read
+    if (n >= 2 && !wait(&sm.ctl.coef_empty[bf], (n >> 1) - 1)) return;
+    if (!meet(wait)) return;
+    // ---- factors
+    const float hi = G.hi[r], lo = G.lo[r];
+    const float eg = tc::ex2(hi + lo);
+    if (is_k) {
+      C.rc[r] = -eg * rn;
+      C.vd[r] = rn * tc::ex2((G.hi[kC - 1] - hi) + (G.lo[kC - 1] - lo));
+      if (r == kC - 1) C.ec = eg;
+    } else {
+      C.o1[r] = a.scale * rn * eg;
+      C.o2[r] = a.scale * rn;
+    }
+    {
+      const float rk = sm.rn[r];
+#pragma unroll
+      for (int I = 1; I < 4; ++I)
+        if ((I == 3) == is_k && r < I * kB)
+          sm.tab[I][r] = rk * tc::ex2((G.hi[I * kB - 1] - hi) + (G.lo[I * kB - 1] - lo));
+      const int c0 = is_k ? 0 : 8;
+#pragma unroll
+      for (int c4 = 0; c4 < 8; c4 += 4) {
+        const int j = blk * kB + c0 + c4;
+        const float4 h4 = *reinterpret_cast<const float4*>(&G.hi[j]);
+        const float4 l4 = *reinterpret_cast<const float4*>(&G.lo[j]);
+        const float4 k4 = *reinterpret_cast<const float4*>(&sm.rn[j]);
+        *reinterpret_cast<float4*>(&sm.ed[r][c0 + c4]) =
+            make_float4(j <= r ? k4.x * tc::ex2((hi - h4.x) + (lo - l4.x)) : 0.0f,
+                        j + 1 <= r ? k4.y * tc::ex2((hi - h4.y) + (lo - l4.y)) : 0.0f,
+                        j + 2 <= r ? k4.z * tc::ex2((hi - h4.z) + (lo - l4.z)) : 0.0f,
+                        j + 3 <= r ? k4.w * tc::ex2((hi - h4.w) + (lo - l4.w)) : 0.0f);
       }
     }
-    const float rn = a.l2norm ? 1.0f / sqrtf(ss + kGdnNormEps) : 1.0f;
-    // the arrays of two chunks ago have been read
-    if (n >= 2 && !wait(&sm.ctl.arr_empty[bf], (n >> 1) - 1)) return;
-    prep_sync();
-    if (is_k) {
-      if (warp == 1) g += (double)sm.X[0][0] + (double)sm.X[0][1];
-      const double w = trunc(g);
-      sm.g_hi[r] = (float)w;
-      sm.g_lo[r] = (float)(g - w);
-      sm.rk[r] = rn;
-      const float eg = exp2f((float)g);
-      G.rb[r] = beta;
-      G.rc[r] = beta * eg * rn;
-    } else {
-      G.o2[r] = a.scale * rn;
-    }
-    prep_sync();
-    const float hi = sm.g_hi[r], lo = sm.g_lo[r];
-    if (is_k)
-      G.vd[r] = rn * exp2f((sm.g_hi[kC - 1] - hi) + (sm.g_lo[kC - 1] - lo));
-    else
-      G.o1[r] = a.scale * rn * exp2f(hi + lo);
-    if (p == 0) G.ec = exp2f(sm.g_hi[kC - 1] + sm.g_lo[kC - 1]);
-    warp_arrive(&sm.ctl.g_full);
-    // ---- A and the scores from [K; Q] K^T
+    const float fac = is_k ? G.beta[r] * rn : 1.0f;
+    const float off =
+        blk > 0 ? fac * tc::ex2((hi - G.hi[blk * kB - 1]) + (lo - G.lo[blk * kB - 1])) : 0.0f;
+    warp_arrive(&sm.ctl.coef_full[bf]);
+    if (!meet(wait)) return;
+    // ---- A and the scores from [K; Q] K^T: row r times the factors of its
+    // columns, e^{G_i - G_j} as two factors at most 1 around the block's start
     if (!wait(&sm.ctl.d1_full, n)) return;
     tc::fence_after();
-    if (n >= 2 && !wait(&sm.ctl.tp_empty[bf], (n >> 1) - 1)) return;
+    if (is_k ? n >= 1 && !wait(&sm.ctl.a_empty, n - 1)
+             : n >= 2 && !wait(&sm.ctl.tp_empty[bf], (n >> 1) - 1))
+      return;
     unsigned char* const tp = sm.tp[bf];
     const uint32_t d1 = tmem + kColD1 + ((uint32_t)(warp * 32) << 16);
-    const float fac = is_k ? beta * rn : 1.0f;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       uint32_t x[32];
       tc::ld32(d1 + hf * 32, x);
       tc::wait_ld(x);
-      float y[32];
 #pragma unroll
-      for (int j4 = 0; j4 < 8; ++j4) {
-        const int j = hf * 32 + j4 * 4;
-        const float4 rk4 = *reinterpret_cast<const float4*>(&sm.rk[j]);
-        const float4 h4 = *reinterpret_cast<const float4*>(&sm.g_hi[j]);
-        const float4 l4 = *reinterpret_cast<const float4*>(&sm.g_lo[j]);
-        const float rkv[4] = {rk4.x, rk4.y, rk4.z, rk4.w}, hv[4] = {h4.x, h4.y, h4.z, h4.w},
-                    lv[4] = {l4.x, l4.y, l4.z, l4.w};
+      for (int jb = 0; jb < 2; ++jb) {
+        const int J = hf * 2 + jb;
+        const float m = J < blk ? off : J == blk ? fac : 0.0f;
+        const float* q = J == blk ? sm.ed[r] : &sm.tab[blk][J * kB];
+        float y[16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int jj = j + e;
-          const bool in = is_k ? jj < r : jj <= r;
-          const float d = in ? exp2f((hi - hv[e]) + (lo - lv[e])) : 0.0f;
-          y[j4 * 4 + e] = in ? fac * rkv[e] * d * __uint_as_float(x[j4 * 4 + e]) : 0.0f;
+        for (int j4 = 0; j4 < 4; ++j4) {
+          // blocks right of the diagonal are zero and their factors not set
+          const float4 t = J <= blk ? *reinterpret_cast<const float4*>(q + j4 * 4)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+          const int e = jb * 16 + j4 * 4;
+          mul_x2(y[j4 * 4], y[j4 * 4 + 1], m * t.x, m * t.y, __uint_as_float(x[e]),
+                 __uint_as_float(x[e + 1]));
+          mul_x2(y[j4 * 4 + 2], y[j4 * 4 + 3], m * t.z, m * t.w, __uint_as_float(x[e + 2]),
+                 __uint_as_float(x[e + 3]));
         }
-      }
-      if (is_k) {
+        if (is_k) {
 #pragma unroll
-        for (int j4 = 0; j4 < 8; ++j4)
-          *reinterpret_cast<float4*>(&sm.A[r][hf * 32 + j4 * 4]) =
-              make_float4(y[j4 * 4], y[j4 * 4 + 1], y[j4 * 4 + 2], y[j4 * 4 + 3]);
-      } else {
+          for (int j4 = 0; j4 < 4; ++j4)
+            *reinterpret_cast<float4*>(&sm.A[r][J * kB + j4 * 4]) =
+                make_float4(y[j4 * 4], y[j4 * 4 + 1], y[j4 * 4 + 2], y[j4 * 4 + 3]);
+        } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          *reinterpret_cast<uint4*>(tp + 2 * kTBytes + sw128(r, hf * 4 + u)) =
-              make_uint4(pack_bf16x2(y[u * 8], y[u * 8 + 1]),
-                         pack_bf16x2(y[u * 8 + 2], y[u * 8 + 3]),
-                         pack_bf16x2(y[u * 8 + 4], y[u * 8 + 5]),
-                         pack_bf16x2(y[u * 8 + 6], y[u * 8 + 7]));
+          for (int u = 0; u < 2; ++u)
+            *reinterpret_cast<uint4*>(tp + 2 * kTBytes + sw128(r, J * 2 + u)) =
+                make_uint4(pack_bf16x2(y[u * 8], y[u * 8 + 1]),
+                           pack_bf16x2(y[u * 8 + 2], y[u * 8 + 3]),
+                           pack_bf16x2(y[u * 8 + 4], y[u * 8 + 5]),
+                           pack_bf16x2(y[u * 8 + 6], y[u * 8 + 7]));
+        }
       }
     }
     tc::fence_before();
-    prep_sync();
-    // ---- T: diagonal blocks (warps 0 and 1, a thread a column), stored as bf16
-    // hi and lo; fp32 copies for the block step stay in A's own blocks
-    auto put = [&](int i, int j, float v) {
-      const uint32_t at = sw128(i, j >> 3) + (j & 7) * 2;
-      const uint32_t hb = pack_bf16x2(v, 0.0f);
-      *reinterpret_cast<uint16_t*>(tp + at) = (uint16_t)hb;
-      *reinterpret_cast<uint16_t*>(tp + kTBytes + at) =
-          (uint16_t)pack_bf16x2(v - __uint_as_float(hb << 16), 0.0f);
-    };
-    if (warp < 2) {
-      const int b0 = warp * 32;
-      float t[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        float acc[4] = {lane == i ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int k4 = 0; k4 < i; k4 += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(&sm.A[b0 + i][b0 + k4]);
-          acc[0] = fmaf(-v.x, t[k4], acc[0]);
-          if (k4 + 1 < i) acc[1] = fmaf(-v.y, t[k4 + 1], acc[1]);
-          if (k4 + 2 < i) acc[2] = fmaf(-v.z, t[k4 + 2], acc[2]);
-          if (k4 + 3 < i) acc[3] = fmaf(-v.w, t[k4 + 3], acc[3]);
-        }
-        t[i] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-      }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        sm.A[b0 + i][b0 + lane] = t[i];
-        put(b0 + i, b0 + lane, t[i]);
-      }
+    if (is_k) {
+      warp_arrive(&sm.ctl.a_full);
+    } else {
+      fence_proxy_async();
+      warp_arrive(&sm.ctl.t_full);
     }
-    prep_sync();
-    // ---- T21 = -T22 (A21 T11): 8 outputs a thread, 2 rows x 4 columns
-    {
-      const int i0 = (p >> 3) * 2, j0 = (p & 7) * 4;
-      float x[2][4] = {};
+    warp_arrive(&sm.ctl.gate_empty[bf]);
+    if (!meet(wait)) return;     // ed, tab and rn are free for the next chunk
+  }
+}
+
+// T of every chunk, by two warps: forward substitution of the four diagonal
+// blocks (a lane a column, two blocks a warp), then the blocks below them, nine
+// block products by the first warp and seven by the second.
+__device__ __forceinline__ void inv_role(Smem& sm, const Wait& wait, int chunks) {
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kWarpInv0;
+  const int blk = warp * 2 + (lane >> 4), c = lane & (kB - 1), b0 = blk * kB;
+  Meet meet{&sm.ctl.inv_meet, 0};
+  for (int n = 0; n < chunks; ++n) {
+    const int bf = n & 1;
+    const Gate& G = sm.gate[bf];
+    unsigned char* const tp = sm.tp[bf];
+    if (!wait(&sm.ctl.a_full, n)) return;
+    if (n >= 2 && !wait(&sm.ctl.tp_empty[bf], (n >> 1) - 1)) return;
+    float t[kB];
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const float4 t = *reinterpret_cast<const float4*>(&sm.A[k][j0]);
+    for (int i = 0; i < kB; ++i) {
+      float acc[4] = {c == i ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float v = sm.A[32 + i0 + e][k];
-          x[e][0] = fmaf(v, t.x, x[e][0]);
-          x[e][1] = fmaf(v, t.y, x[e][1]);
-          x[e][2] = fmaf(v, t.z, x[e][2]);
-          x[e][3] = fmaf(v, t.w, x[e][3]);
-        }
+      for (int k4 = 0; k4 < i; k4 += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(&sm.A[b0 + i][b0 + k4]);
+        acc[0] = fmaf(-v.x, t[k4], acc[0]);
+        if (k4 + 1 < i) acc[1] = fmaf(-v.y, t[k4 + 1], acc[1]);
+        if (k4 + 2 < i) acc[2] = fmaf(-v.z, t[k4 + 2], acc[2]);
+        if (k4 + 3 < i) acc[3] = fmaf(-v.w, t[k4 + 3], acc[3]);
       }
+      t[i] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    }
+    const float be = G.beta[b0 + c];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        *reinterpret_cast<float4*>(&sm.X[i0 + e][j0]) =
-            make_float4(x[e][0], x[e][1], x[e][2], x[e][3]);
-      prep_sync();
-      float y[2][4] = {};
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const float4 t = *reinterpret_cast<const float4*>(&sm.X[k][j0]);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float v = -sm.A[32 + i0 + e][32 + k];
-          y[e][0] = fmaf(v, t.x, y[e][0]);
-          y[e][1] = fmaf(v, t.y, y[e][1]);
-          y[e][2] = fmaf(v, t.z, y[e][2]);
-          y[e][3] = fmaf(v, t.w, y[e][3]);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t h0, h1, l0, l1;
-        tc::split2(y[e][0], y[e][1], h0, l0);
-        tc::split2(y[e][2], y[e][3], h1, l1);
-        const uint32_t at = sw128(32 + i0 + e, j0 >> 3) + (j0 & 7) * 2;
-        *reinterpret_cast<uint2*>(tp + at) = make_uint2(h0, h1);
-        *reinterpret_cast<uint2*>(tp + kTBytes + at) = make_uint2(l0, l1);
-      }
+    for (int i = 0; i < kB; ++i) {
+      sm.Td[blk][i][c] = t[i];
+      put_t(tp, b0 + i, b0 + c, t[i] * be);
+    }
+    if (!meet(wait)) return;
+    if (warp == 0) {
+      t_blocks<0>(sm, tp, G.beta);
+    } else {
+      t_blocks<1>(sm, tp, G.beta);
+      t_blocks<2>(sm, tp, G.beta);
     }
     fence_proxy_async();
     warp_arrive(&sm.ctl.t_full);
-    prep_sync();     // X and A are free for the next chunk
+    warp_arrive(&sm.ctl.a_empty);
+    warp_arrive(&sm.ctl.gate_empty[bf]);
+    if (!meet(wait)) return;     // the diagonal blocks have been read
   }
 }
 
@@ -367,8 +524,7 @@ __device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait
 
 template <typename ST>
 __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait& wait, int row0,
-                                          int len, int h, int chunks, uint32_t tmem, bool init,
-                                          int slot) {
+                                          int len, int h, int chunks, uint32_t tmem, bool init, int slot) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int qd = warp & 3, hf = warp >> 2;
   const int col = qd * 32 + lane;                       // the thread's column of S
@@ -378,9 +534,11 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
   float S[64];                                          // dk hf * 64 + [0, 64)
 #pragma unroll
   for (int i = 0; i < 64; ++i) S[i] = init ? elem(sp, i * kD) : 0.0f;
-  __nv_bfloat16* const op = reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)h * kD + col;
 
-  // outputs of chunk n
+  // outputs of chunk n: 32 tokens by 32 columns of each warp, turned round in 2
+  // KB of the chunk's V, which has been used, and stored in 16-byte units
+  char* const op = a.out + ((int64_t)row0 * a.out_rs + (int64_t)h * kD + qd * 32) * 2 +
+                   (lane & 3) * 16;
   auto outputs = [&](int n) -> bool {
     if (!wait(&sm.ctl.o_full, n)) return false;
     tc::fence_after();
@@ -391,22 +549,39 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
     tc::wait_ld(y);
     tc::fence_before();
     warp_arrive(&sm.ctl.o_empty);
-    const Gates& G = sm.gates[n & 1];
-    const int t0 = n * kC + hf * 32;
-    __nv_bfloat16* o = op + (int64_t)(row0 + t0) * a.out_rs;
+    const Coef& C = sm.coef[n & 1];
+    unsigned char* const box = sm.stage[n % kStages] + kKQBytes + warp * 2048;
+    uint16_t* const o = reinterpret_cast<uint16_t*>(box) + lane;
 #pragma unroll
     for (int i4 = 0; i4 < 8; ++i4) {
-      const float4 c1 = *reinterpret_cast<const float4*>(&G.o1[hf * 32 + i4 * 4]);
-      const float4 c2 = *reinterpret_cast<const float4*>(&G.o2[hf * 32 + i4 * 4]);
-      const float u[4] = {c1.x, c1.y, c1.z, c1.w}, w[4] = {c2.x, c2.y, c2.z, c2.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = i4 * 4 + e;
-        const float v = fmaf(u[e], __uint_as_float(x[i]), w[e] * __uint_as_float(y[i]));
-        if (t0 + i < len) o[(int64_t)i * a.out_rs] = __float2bfloat16_rn(v);
-      }
+      const float4 c1 = *reinterpret_cast<const float4*>(&C.o1[hf * 32 + i4 * 4]);
+      const float4 c2 = *reinterpret_cast<const float4*>(&C.o2[hf * 32 + i4 * 4]);
+      float v[4];
+      mul_x2(v[0], v[1], c2.x, c2.y, __uint_as_float(y[i4 * 4]), __uint_as_float(y[i4 * 4 + 1]));
+      mul_x2(v[2], v[3], c2.z, c2.w, __uint_as_float(y[i4 * 4 + 2]),
+             __uint_as_float(y[i4 * 4 + 3]));
+      fma_x2(v[0], v[1], c1.x, c1.y, __uint_as_float(x[i4 * 4]), __uint_as_float(x[i4 * 4 + 1]),
+             v[0], v[1]);
+      fma_x2(v[2], v[3], c1.z, c1.w, __uint_as_float(x[i4 * 4 + 2]),
+             __uint_as_float(x[i4 * 4 + 3]), v[2], v[3]);
+      const uint32_t p0 = pack_bf16x2(v[0], v[1]), p1 = pack_bf16x2(v[2], v[3]);
+      o[(i4 * 4) * 32] = (uint16_t)p0;
+      o[(i4 * 4 + 1) * 32] = (uint16_t)(p0 >> 16);
+      o[(i4 * 4 + 2) * 32] = (uint16_t)p1;
+      o[(i4 * 4 + 3) * 32] = (uint16_t)(p1 >> 16);
     }
-    warp_arrive(&sm.ctl.arr_empty[n & 1]);
+    warp_arrive(&sm.ctl.coef_empty[n & 1]);
+    uint4 q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      q[i] = *reinterpret_cast<const uint4*>(box + (i * 32 + lane) * 16);
+    fence_proxy_async();
+    warp_arrive(&sm.ctl.empty[n % kStages]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = (int64_t)n * kC + hf * 32 + i * 8 + (lane >> 2);
+      if (t < len) *reinterpret_cast<uint4*>(op + t * a.out_rs * 2) = q[i];
+    }
     return true;
   };
   // S = e^{G_C} S + update of chunk n
@@ -414,14 +589,15 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
     uint32_t x[32];
     tc::ld32(tl + kColS + hf * 64 + part * 32, x);
     tc::wait_ld(x);
-    const float ec = sm.gates[n & 1].ec;
+    const float ec = sm.coef[n & 1].ec;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      S[part * 32 + i] = fmaf(ec, S[part * 32 + i], __uint_as_float(x[i]));
+    for (int i = 0; i < 32; i += 2)
+      fma_x2(S[part * 32 + i], S[part * 32 + i + 1], ec, ec, S[part * 32 + i],
+             S[part * 32 + i + 1], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
   };
 
   for (int n = 0; n < chunks; ++n) {
-    const int st = n % kStages, bf = n & 1;
+    const Coef& C = sm.coef[n & 1];
     // ---- S: add the last chunk's update, split, hand to the tensor cores
     if (n > 0) {
       if (!wait(&sm.ctl.sd_full, n - 1)) return;
@@ -443,30 +619,22 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
     warp_arrive(&sm.ctl.s_full);
     if (n > 0 && !outputs(n - 1)) return;
     // ---- R
-    if (!wait(&sm.ctl.g_full, n) || !wait(&sm.ctl.full[st], n / kStages) ||
-        !wait(&sm.ctl.ks_full, n))
-      return;
+    if (!wait(&sm.ctl.coef_full[n & 1], n >> 1) || !wait(&sm.ctl.ks_full, n)) return;
     tc::fence_after();
-    const Gates& G = sm.gates[bf];
     {
       uint32_t x[32], hi[16], lo[16];
       tc::ld32(tl + kColKS + hf * 32, x);
       tc::wait_ld(x);
-      const uint16_t* v = reinterpret_cast<const uint16_t*>(sm.stage[st] + kKQBytes) +
-                          hf * 32 * kD + col;
 #pragma unroll
       for (int i4 = 0; i4 < 8; ++i4) {
-        const float4 b4 = *reinterpret_cast<const float4*>(&G.rb[hf * 32 + i4 * 4]);
-        const float4 c4 = *reinterpret_cast<const float4*>(&G.rc[hf * 32 + i4 * 4]);
-        const float b[4] = {b4.x, b4.y, b4.z, b4.w}, c[4] = {c4.x, c4.y, c4.z, c4.w};
-        float r[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float vv = __uint_as_float((uint32_t)v[(i4 * 4 + e) * kD] << 16);
-          r[e] = fmaf(-c[e], __uint_as_float(x[i4 * 4 + e]), b[e] * vv);
-        }
-        tc::split2(r[0], r[1], hi[i4 * 2], lo[i4 * 2]);
-        tc::split2(r[2], r[3], hi[i4 * 2 + 1], lo[i4 * 2 + 1]);
+        const float4 c4 = *reinterpret_cast<const float4*>(&C.rc[hf * 32 + i4 * 4]);
+        float q[4];
+        mul_x2(q[0], q[1], c4.x, c4.y, __uint_as_float(x[i4 * 4]),
+               __uint_as_float(x[i4 * 4 + 1]));
+        mul_x2(q[2], q[3], c4.z, c4.w, __uint_as_float(x[i4 * 4 + 2]),
+               __uint_as_float(x[i4 * 4 + 3]));
+        tc::split2(q[0], q[1], hi[i4 * 2], lo[i4 * 2]);
+        tc::split2(q[2], q[3], hi[i4 * 2 + 1], lo[i4 * 2 + 1]);
       }
       tc::st16(tl + kColR + hf * 16, hi);
       tc::st16(tl + kColR + 32 + hf * 16, lo);
@@ -479,17 +647,20 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
     tc::fence_after();
     {
       uint32_t x[32], hi[16], lo[16], on[16];
-      tc::ld32(tl + kColKS + hf * 32, x);
+      tc::ld32(tl + kColVN + hf * 32, x);
       tc::wait_ld(x);
 #pragma unroll
       for (int i4 = 0; i4 < 8; ++i4) {
-        const float4 d4 = *reinterpret_cast<const float4*>(&G.vd[hf * 32 + i4 * 4]);
+        const float4 d4 = *reinterpret_cast<const float4*>(&C.vd[hf * 32 + i4 * 4]);
         const float v0 = __uint_as_float(x[i4 * 4]), v1 = __uint_as_float(x[i4 * 4 + 1]),
                     v2 = __uint_as_float(x[i4 * 4 + 2]), v3 = __uint_as_float(x[i4 * 4 + 3]);
         on[i4 * 2] = pack_bf16x2(v0, v1);
         on[i4 * 2 + 1] = pack_bf16x2(v2, v3);
-        tc::split2(d4.x * v0, d4.y * v1, hi[i4 * 2], lo[i4 * 2]);
-        tc::split2(d4.z * v2, d4.w * v3, hi[i4 * 2 + 1], lo[i4 * 2 + 1]);
+        float q[4];
+        mul_x2(q[0], q[1], d4.x, d4.y, v0, v1);
+        mul_x2(q[2], q[3], d4.z, d4.w, v2, v3);
+        tc::split2(q[0], q[1], hi[i4 * 2], lo[i4 * 2]);
+        tc::split2(q[2], q[3], hi[i4 * 2 + 1], lo[i4 * 2 + 1]);
       }
       tc::st16(tl + kColR + hf * 16, hi);
       tc::st16(tl + kColR + 32 + hf * 16, lo);
@@ -503,135 +674,138 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
   tc::fence_after();
   advance(chunks - 1, 0);
   advance(chunks - 1, 1);
+  if (!outputs(chunks - 1)) return;
   if (slot >= 0)
 #pragma unroll
     for (int i = 0; i < 64; ++i) {
       const auto raw = f32_to_raw<ST>(S[i]);
       *reinterpret_cast<std::remove_const_t<decltype(raw)>*>(sp + i * kD) = raw;
     }
-  outputs(chunks - 1);
 }
 
 // ---- the warp that issues the tensor products -------------------------------
 
+// On the chain: S^T k (16 products of N = 64, 512 clocks), T R (12, 384), the
+// update (8 of N = 128, 512). Beside it: S^T q, in-chunk outputs, and, while
+// the chain's warps work on S, T V of this chunk and the scores of the next.
 __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks, uint32_t tmem) {
-  const int lane = threadIdx.x & 31;
-  constexpr uint32_t kId64 = tc::idesc(128, 64), kIdUpd = tc::idesc(128, 128, true);
+  constexpr uint32_t kId = tc::idesc(128, 64), kIdV = tc::idesc(128, 64, true),
+                     kIdUpd = tc::idesc(128, 128, false, true);
+  const uint32_t stage0 = smem_addr(sm.stage[0]), tp0 = smem_addr(sm.tp[0]);
   auto panel = [&](int st, int ks, int row) {   // 16 dk of rows [row, ..) of [K; Q]
-    return smem_addr(sm.stage[st]) + (ks >> 2) * kPanel + (ks & 3) * 32 + row * 128;
+    return stage0 + st * kStageBytes + (ks >> 2) * kPanel + (ks & 3) * 32 + row * 128;
   };
   auto scores = [&](int n) -> bool {            // [K; Q] K^T of chunk n
     const int st = n % kStages;
     if (!wait(&sm.ctl.full[st], n / kStages)) return false;
     tc::fence_after();
-    if (lane == 0) {
+    if (tc::elect()) {
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
         const uint64_t d = tc::desc_sw128(panel(st, ks, 0), 16);
-        tc::mma_ss(tmem + kColD1, d, d, kId64, ks > 0);
+        tc::mma_ss(tmem + kColD1, d, d, kId, ks > 0);
       }
       tc::commit(&sm.ctl.d1_full);
     }
     __syncwarp();
     return true;
   };
+  auto tv = [&](int n) -> bool {                // (T V)^T of chunk n: V read along dv
+    if (!wait(&sm.ctl.t_full, n)) return false;
+    tc::fence_after();
+    const uint32_t tp = tp0 + (n & 1) * kTP, v = stage0 + (n % kStages) * kStageBytes + kKQBytes;
+    if (tc::elect()) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          tc::mma_ss(tmem + kColVN, tc::desc_sw128(v + ks * 2048, kVPanel),
+                     tc::desc_sw128(tp + t * kTBytes + ks * 32, 16), kIdV, (t | ks) > 0);
+    }
+    __syncwarp();
+    return true;
+  };
   if (!scores(0)) return;
+  int scored = 1, tved = 0;                     // chunks whose products are issued
   for (int n = 0; n < chunks; ++n) {
     const int st = n % kStages, bf = n & 1;
-    const uint32_t tp = smem_addr(sm.tp[bf]);
+    const uint32_t tp = tp0 + bf * kTP;
     if (!wait(&sm.ctl.s_full, n)) return;
+    // N of the last chunk lies where S^T k goes
+    if (n > 0 && !wait(&sm.ctl.o_full, n - 1)) return;
     tc::fence_after();
-    if (lane == 0) {
+    if (tc::elect()) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)               // S hi, S lo
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
           tc::mma_ts(tmem + kColKS, tmem + kColS + (ks >> 2) * 64 + t * 32 + (ks & 3) * 8,
-                     tc::desc_sw128(panel(st, ks, 0), 16), kId64, (t | ks) > 0);
+                     tc::desc_sw128(panel(st, ks, 0), 16), kId, (t | ks) > 0);
       tc::commit(&sm.ctl.ks_full);
     }
     __syncwarp();
     if (n > 0 && !wait(&sm.ctl.o_empty, n - 1)) return;
     tc::fence_after();
-    if (lane == 0) {
+    if (tc::elect()) {
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks)
         tc::mma_ts(tmem + kColQS, tmem + kColS + (ks >> 2) * 64 + (ks & 3) * 8,
-                   tc::desc_sw128(panel(st, ks, kC), 16), kId64, ks > 0);
+                   tc::desc_sw128(panel(st, ks, kC), 16), kId, ks > 0);
       tc::commit(&sm.ctl.qs_done);
     }
     __syncwarp();
-    if (!wait(&sm.ctl.r_full, n) || !wait(&sm.ctl.t_full, n)) return;
+    if (tved == n) {
+      if (!tv(n)) return;
+      ++tved;
+    }
+    if (!wait(&sm.ctl.r_full, n)) return;
     tc::fence_after();
-    if (lane == 0) {
+    if (tc::elect()) {
 #pragma unroll
       for (int t = 0; t < 3; ++t)               // R hi T hi, R lo T hi, R hi T lo
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          tc::mma_ts(tmem + kColKS, tmem + kColR + (t == 1 ? 32 : 0) + ks * 8,
-                     tc::desc_sw128(tp + (t == 2 ? kTBytes : 0) + ks * 32, 16), kId64,
-                     (t | ks) > 0);
+          tc::mma_ts(tmem + kColVN, tmem + kColR + (t == 1 ? 32 : 0) + ks * 8,
+                     tc::desc_sw128(tp + (t == 2 ? kTBytes : 0) + ks * 32, 16), kId, true);
       tc::commit(&sm.ctl.vn_full);
     }
     __syncwarp();
-    if (n + 1 < chunks && !scores(n + 1)) return;
+    if (scored == n + 1 && n + 1 < chunks) {
+      if (!scores(n + 1)) return;
+      ++scored;
+    }
     if (!wait(&sm.ctl.vd_full, n) || !wait(&sm.ctl.qs_done, n)) return;
     tc::fence_after();
-    if (lane == 0) {
+    if (tc::elect()) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)               // K read along dk: 16 tokens a step
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           tc::mma_ts(tmem + kColS, tmem + kColR + t * 32 + ks * 8,
-                     tc::desc_sw128(smem_addr(sm.stage[st]) + ks * 2048, kPanel), kIdUpd,
+                     tc::desc_sw128(stage0 + st * kStageBytes + ks * 2048, kPanel), kIdUpd,
                      (t | ks) > 0);
       tc::commit(&sm.ctl.sd_full);
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
         tc::mma_ts(tmem + kColO, tmem + kColN + ks * 8,
-                   tc::desc_sw128(tp + 2 * kTBytes + ks * 32, 16), kId64, ks > 0);
+                   tc::desc_sw128(tp + 2 * kTBytes + ks * 32, 16), kId, ks > 0);
       tc::commit(&sm.ctl.o_full);
       tc::commit(&sm.ctl.empty[st]);
       tc::commit(&sm.ctl.tp_empty[bf]);
     }
     __syncwarp();
-  }
-}
-
-// ---- the warp that stages K, Q and V ----------------------------------------
-
-__device__ __forceinline__ void load_role(const GdnArgs& a, Smem& sm, const Wait& wait, int row0,
-                                          int len, int h, int chunks) {
-  const int lane = threadIdx.x & 31, u = lane & 15, r2 = lane >> 4;
-  const int hk = h / (a.Hv / a.Hk);
-  const char* kp = a.k + ((int64_t)row0 * a.k_rs + (int64_t)hk * kD) * 2 + u * 16;
-  const char* qp = a.q + ((int64_t)row0 * a.q_rs + (int64_t)hk * kD) * 2 + u * 16;
-  const char* vp = a.v + ((int64_t)row0 * a.v_rs + (int64_t)h * kD) * 2 + u * 16;
-  for (int n = 0; n < chunks; ++n) {
-    const int st = n % kStages;
-    if (n >= kStages && !wait(&sm.ctl.empty[st], n / kStages - 1)) break;
-    const uint32_t base = smem_addr(sm.stage[st]) + (u >> 3) * kPanel;
-    const uint32_t vbase = smem_addr(sm.stage[st]) + kKQBytes + u * 16;
-#pragma unroll 8
-    for (int i = 0; i < kC / 2; ++i) {
-      const int r = i * 2 + r2;
-      const int64_t t = (int64_t)n * kC + r;
-      const bool in = t < len;
-      const int64_t tt = in ? t : 0;
-      cp_async16(base + sw128(r, u & 7), kp + tt * a.k_rs * 2, in);
-      cp_async16(base + sw128(kC + r, u & 7), qp + tt * a.q_rs * 2, in);
-      cp_async16(vbase + r * (kD * 2), vp + tt * a.v_rs * 2, in);
-    }
-    cp_async_commit();
-    if (n > 0) {
-      cp_async_wait<1>();
-      fence_proxy_async();
-      warp_arrive(&sm.ctl.full[(n - 1) % kStages]);
+    // if T of the next chunk is there already, its product with V and the
+    // scores of the chunk behind run while S is worked on
+    if (n + 1 < chunks && __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.t_full, (n + 1) & 1))) {
+      if (!tv(n + 1)) return;
+      ++tved;
+      if (n + 2 < chunks && __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.full[(n + 2) % kStages],
+                                                                 ((n + 2) / kStages) & 1))) {
+        if (!scores(n + 2)) return;
+        ++scored;
+      }
     }
   }
-  cp_async_wait<0>();      // also when giving up: nothing lands after the block ends
-  fence_proxy_async();
-  warp_arrive(&sm.ctl.full[(chunks - 1) % kStages]);
 }
 
 template <typename ST>
@@ -641,7 +815,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
       gdn_dyn + ((1024u - (smem_addr(gdn_dyn) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5;
   const int h = blockIdx.x % a.Hv, s = blockIdx.x / a.Hv;
-  // sequences that the recurrent kernel skips with an error are skipped there
+  // (a bad cu_seqlens entry is reported by the recurrent kernel)
   int row0, len;
   if (!gdn_bounds(a, s, row0, len) || len <= a.max_len) return;
   const int slot = a.state_idx[s];
@@ -656,15 +830,20 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
     Ctl& c = sm.ctl;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&c.full[i], 1);
-      mbar_init(&c.empty[i], 1);
+      mbar_init(&c.empty[i], 1 + kScanWarps);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.gate_empty[i], kPrepWarps + kInvWarps);
       mbar_init(&c.tp_empty[i], 1);
-      mbar_init(&c.arr_empty[i], kScanWarps);
+      mbar_init(&c.coef_full[i], kPrepWarps);
+      mbar_init(&c.coef_empty[i], kScanWarps);
     }
     mbar_init(&c.d1_full, 1);
-    mbar_init(&c.g_full, kPrepWarps);
-    mbar_init(&c.t_full, kPrepWarps);
+    mbar_init(&c.prep_meet, kPrepWarps);
+    mbar_init(&c.inv_meet, kInvWarps);
+    mbar_init(&c.a_full, 2);
+    mbar_init(&c.a_empty, kInvWarps);
+    mbar_init(&c.t_full, 2 + kInvWarps);     // scores, T
     mbar_init(&c.s_full, kScanWarps);
     mbar_init(&c.ks_full, 1);
     mbar_init(&c.qs_done, 1);
@@ -678,11 +857,13 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
     c.abort = 0;
     fence_mbar_init();
   }
-  // the upper right quarter of T is zero in both buffers
-  for (int i = tid; i < 2 * 2 * 32 * 4; i += kThreadsC) {
-    const int u = i & 3, r = (i >> 2) & 31, m = (i >> 7) & 1, b = i >> 8;
-    *reinterpret_cast<uint4*>(sm.tp[b] + m * kTBytes + sw128(r, 4 + u)) =
-        make_uint4(0u, 0u, 0u, 0u);
+  // blocks of T right of the diagonal are zero in both buffers: rows [0, 48),
+  // units from the row's next block on
+  for (int i = tid; i < 2 * 2 * 48 * 8; i += kThreadsC) {
+    const int u = i & 7, r = (i >> 3) % 48, m = (i / 384) & 1, b = i / 768;
+    if (u >= (r / kB + 1) * 2)
+      *reinterpret_cast<uint4*>(sm.tp[b] + m * kTBytes + sw128(r, u)) =
+          make_uint4(0u, 0u, 0u, 0u);
   }
   fence_proxy_async();
   if (warp == kWarpMma) {
@@ -698,22 +879,29 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
   const Wait wait{&sm.ctl, a.dev_err};
 
   if (warp < kScanWarps) {
+    more_regs<kRegsScan>();
     scan_role<ST>(a, sm, wait, row0, len, h, chunks, tmem, init, slot);
-  } else if (warp < kWarpMma) {
-    prep_role(a, sm, wait, row0, len, h, chunks, tmem);
-  } else if (warp == kWarpMma) {
-    mma_role(sm, wait, chunks, tmem);
-    // every product that was issued ends before tensor memory is given back
-    if ((tid & 31) == 0) tc::commit(&sm.ctl.fin);
-    __syncwarp();
-    const long long t0 = clock64();
-    while (!mbar_try(&sm.ctl.fin, 0))
-      if (clock64() - t0 > kWaitClocks) {
-        flag_error(a.dev_err, CCONV_DERR_TIMEOUT);
-        break;
-      }
+  } else if (warp < kWarpInv0) {
+    fewer_regs<kRegsPrep>();
+    prep_role(a, sm, wait, chunks, tmem);
   } else {
-    load_role(a, sm, wait, row0, len, h, chunks);
+    fewer_regs<kRegsRest>();
+    if (warp < kWarpMma) {
+      inv_role(sm, wait, chunks);
+    } else if (warp == kWarpMma) {
+      mma_role(sm, wait, chunks, tmem);
+      // every product that was issued ends before tensor memory is given back
+      if (tc::elect()) tc::commit(&sm.ctl.fin);
+      __syncwarp();
+      const long long t0 = clock64();
+      while (!mbar_try(&sm.ctl.fin, 0))
+        if (clock64() - t0 > kWaitClocks) {
+          flag_error(a.dev_err, CCONV_DERR_TIMEOUT);
+          break;
+        }
+    } else {
+      load_role(a, sm, wait, row0, len, h, chunks);
+    }
   }
   tc::fence_before();
   __syncthreads();

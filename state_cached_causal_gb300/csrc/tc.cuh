@@ -48,9 +48,10 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo) {
          (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
          (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-// kind::f16: fp32 D, bf16 A and B, A K-major, B K-major or (b_mn) MN-major.
-__host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn = false) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) |
+// kind::f16: fp32 D, bf16 A and B, each K-major or MN-major.
+__host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn = false, bool b_mn = false) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
@@ -90,7 +91,57 @@ __device__ __forceinline__ void wait_st() {
 // hi = bf16(x), lo = bf16(x - hi) of two values, each pair packed (x0 low).
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   hi = pack_bf16x2(x0, x1);
-  lo = pack_bf16x2(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
+  float l0, l1;
+  fma_x2(l0, l1, __uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u), -1.0f, -1.0f, x0,
+         x1);
+  lo = pack_bf16x2(l0, l1);
+}
+
+// 2^x by the hardware (2 ulp, results under 2^-126 are zero).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Phase test that returns at once (a try_wait may keep the warp for a while).
+__device__ __forceinline__ bool mbar_ready(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// One lane of a converged warp. tcgen05.mma takes its operands from uniform
+// registers: behind this predicate the compiler keeps them there, behind a
+// test of the lane number it moves them at every instruction (110 against 32
+// clocks for M = 128, N = 64, K = 16).
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+               : "=r"(r));
+  return r != 0;
+}
+
+// Warp-level products of 16 x 16 blocks (tcgen05 has no tile this small):
+// m16n8k16, bf16 in, fp32 out, and the four 8 x 8 matrices of one A operand.
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                      uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 
 }  // namespace tc
