@@ -43,7 +43,10 @@
 // of dk; the state update's accumulator takes the same columns once S has been
 // read) 0-127, S^T k 128-191 (then N), S^T q 192-255, R then the decayed N
 // (hi, lo) 256-319, N 320-351, in-chunk output 352-415, [K; Q] K^T 416-479.
+#include <cuda.h>
 #include <stddef.h>
+
+#include <mutex>
 
 #include "gdn.cuh"
 #include "tc.cuh"
@@ -54,15 +57,16 @@ namespace {
 constexpr int kC = 64;                       // tokens of a chunk
 constexpr int kD = 128;                      // dk = dv
 constexpr int kStages = 3;
-// Warpgroups: two on the chain, one for A and the scores, and one of two warps
-// for T, one that issues the tensor products and one that loads; registers a
-// thread of each (their sum is the block's 512 x 128).
-constexpr int kScanWarps = 8, kPrepWarps = 4, kInvWarps = 2;
+// Warpgroups: two on the chain, one for A and the scores, one of two warps for
+// T, one that issues the tensor products and one that loads, and one for the
+// outputs; registers a thread of each (their sum is the block's 640 x 96).
+constexpr int kScanWarps = 8, kPrepWarps = 4, kInvWarps = 2, kOutWarps = 4;
 constexpr int kWarpPrep0 = kScanWarps, kWarpInv0 = kWarpPrep0 + kPrepWarps,
-              kWarpMma = kWarpInv0 + kInvWarps, kWarpLoad = kWarpMma + 1;
-constexpr int kThreadsC = (kWarpLoad + 1) * 32;
-constexpr int kRegsScan = 160, kRegsPrep = 104, kRegsRest = 88;
-static_assert(kThreadsC == 512 && 2 * kRegsScan + kRegsPrep + kRegsRest <= 4 * 128,
+              kWarpMma = kWarpInv0 + kInvWarps, kWarpLoad = kWarpMma + 1,
+              kWarpOut0 = kWarpLoad + 1;
+constexpr int kThreadsC = (kWarpOut0 + kOutWarps) * 32;
+constexpr int kRegsScan = 136, kRegsPrep = 88, kRegsRest = 72, kRegsOut = 48;
+static_assert(kThreadsC == 640 && 2 * kRegsScan + kRegsPrep + kRegsRest + kRegsOut <= 5 * 96,
               "a split over the block's own registers would wait forever");
 
 constexpr uint32_t kPanel = 128 * 128;       // 64 dk of [K; Q]: 128 rows x 128 bytes
@@ -72,9 +76,10 @@ constexpr uint32_t kVBytes = kC * kD * 2;    // V, later the chunk's outputs [64
 constexpr uint32_t kStageBytes = kKQBytes + kVBytes;
 constexpr uint32_t kTBytes = kC * kC * 2;    // one 64 x 64 bf16 operand
 constexpr uint32_t kTP = 3 * kTBytes;        // T hi, T lo, scores
-constexpr int kAPitch = 68;                  // fp32 rows of A (16-byte aligned)
-constexpr int kB = 16;                       // blocks of T
-constexpr int kBPitch = 20;                  // fp32 rows of 16 (16-byte aligned)
+constexpr int kB = 16;                       // blocks of A and T
+constexpr int kBPitch = 20;                  // fp32 rows of 16: 80 bytes
+constexpr int kAPitch = 56;                  // bf16 rows of 48: 112 bytes
+constexpr int kUPitch = 24;                  // bf16 rows of 16: 48 bytes
 
 constexpr uint32_t kColS = 0, kColKS = 128, kColN = kColKS, kColQS = 192, kColR = 256,
                    kColVN = 320, kColO = 384, kColD1 = 448;
@@ -95,11 +100,16 @@ struct alignas(16) Gate {
   float hi[kC], lo[kC], beta[kC];
 };
 
+struct Maps {
+  CUtensorMap k, q, v;   // [tokens, heads * 128], boxes of 64 x 64 in the 128-byte swizzle
+};
+
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
   uint64_t gate_empty[2], tp_empty[2], coef_full[2], coef_empty[2];
-  uint64_t d1_full, a_full, a_empty, t_full, prep_meet, inv_meet;
-  uint64_t s_full, ks_full, qs_done, r_full, vn_full, vd_full, sd_full, o_full, o_empty, fin;
+  uint64_t d1_full, d1_empty, a_full, a_empty, t_full, prep_meet, inv_meet;
+  uint64_t s_full[2], sd_full[2];
+  uint64_t ks_full, qs_done, r_full, vn_full, vd_full, o_full, o_empty, fin;
   uint32_t tmem;
   volatile int abort;
 };
@@ -107,8 +117,11 @@ struct Ctl {
 struct Smem {
   unsigned char stage[kStages][kStageBytes];   // 1024-byte aligned
   unsigned char tp[2][kTP];
-  alignas(16) float A[kC][kAPitch];
-  alignas(16) float Td[4][kB][kBPitch];        // inverses of the diagonal blocks
+  alignas(16) float Ad[kC][kBPitch];           // A: diagonal blocks
+  alignas(16) uint16_t Ah[kC - kB][kAPitch];   // and rows 16 .. of the blocks left of them,
+  alignas(16) uint16_t Al[kC - kB][kAPitch];   // bf16 hi and lo
+  alignas(16) uint16_t Uh[kC][kUPitch];        // transposed inverses of the diagonal blocks
+  alignas(16) uint16_t Ul[kC][kUPitch];
   alignas(16) float ed[kC][kBPitch];           // e^{G_i - G_j} / |k_j|, j in the block of i
   alignas(16) float tab[4][kC];                // e^{G_(16I-1) - G_j} / |k_j|, j < 16 I
   alignas(16) float rn[2 * kC];                // 1 / |k|, 1 / |q|
@@ -119,8 +132,9 @@ struct Smem {
 static_assert(offsetof(Smem, tp) % 1024 == 0 && kStageBytes % 1024 == 0 && kTP % 1024 == 0 &&
                   kTBytes % 1024 == 0 && kVPanel % 1024 == 0,
               "swizzled tiles start on 1024 bytes");
-static_assert(sizeof(Coef) % 16 == 0 && sizeof(Gate) % 16 == 0 && offsetof(Smem, A) % 16 == 0 &&
-                  offsetof(Smem, Td) % 16 == 0 && offsetof(Smem, ed) % 16 == 0 &&
+static_assert(sizeof(Coef) % 16 == 0 && sizeof(Gate) % 16 == 0 && offsetof(Smem, Ad) % 16 == 0 &&
+                  offsetof(Smem, Ah) % 16 == 0 && offsetof(Smem, Al) % 16 == 0 &&
+                  offsetof(Smem, Uh) % 16 == 0 && offsetof(Smem, Ul) % 16 == 0 && offsetof(Smem, ed) % 16 == 0 &&
                   offsetof(Smem, tab) % 16 == 0 && offsetof(Smem, rn) % 16 == 0 &&
                   offsetof(Smem, coef) % 16 == 0 && offsetof(Smem, gate) % 16 == 0 &&
                   offsetof(Smem, ctl) % 8 == 0,
@@ -179,15 +193,26 @@ __device__ __forceinline__ void fewer_regs() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Waits for a phase while giving up: bounded by time alone.
+__device__ __forceinline__ void drain(uint64_t* bar, int phase, int32_t* err) {
+  const long long t0 = clock64();
+  while (!mbar_try(bar, phase & 1))
+    if (clock64() - t0 > kWaitClocks) {
+      flag_error(err, CCONV_DERR_TIMEOUT);
+      return;
+    }
+}
+
 // ---- the warp that loads K, Q and V and works the gates out -----------------
 
-// Per chunk: requests its rows, works its gates out while they come, and says
-// so when both are there (stages free up a chunk's time apart, which is longer
-// than a load takes). Gates: two tokens a lane (lane, lane + 32); their sums are
+// Per chunk: requests its rows, works its gates out while they come. Whole
+// chunks come as tensor-map boxes; the last, partial one row by row, with
+// zeros behind the sequence's end. Gates: two tokens a lane (lane, lane + 32); their sums are
 // kept as whole part and remainder in (-1, 0], exact to 2^-24 of the remainder
 // however long the sum.
-__device__ __forceinline__ void load_role(const GdnArgs& a, Smem& sm, const Wait& wait, int row0,
-                                          int len, int h, int chunks) {
+__device__ __forceinline__ void load_role(const GdnArgs& a, const Maps& maps, Smem& sm,
+                                          const Wait& wait, int row0, int len, int h,
+                                          int chunks) {
   const int lane = threadIdx.x & 31, u = lane & 15, r2 = lane >> 4;
   const int hk = h / (a.Hv / a.Hk);
   const char* kp = a.k + ((int64_t)row0 * a.k_rs + (int64_t)hk * kD) * 2 + u * 16;
@@ -197,9 +222,10 @@ __device__ __forceinline__ void load_role(const GdnArgs& a, Smem& sm, const Wait
   const float dtb = a.dt_bias[h];
   const __nv_bfloat16* ga = reinterpret_cast<const __nv_bfloat16*>(a.a) + h;
   const __nv_bfloat16* gb = reinterpret_cast<const __nv_bfloat16*>(a.b) + h;
-  for (int n = 0; n < chunks; ++n) {
+  int boxed = 0, n = 0;     // chunks requested as boxes; this chunk
+  for (; n < chunks; ++n) {
     const int st = n % kStages;
-    if (n >= kStages && !wait(&sm.ctl.empty[st], n / kStages - 1)) return;
+    if (n >= kStages && !wait(&sm.ctl.empty[st], n / kStages - 1)) break;
     const uint32_t base = smem_addr(sm.stage[st]) + (u >> 3) * kPanel;
     const uint32_t vbase = smem_addr(sm.stage[st]) + kKQBytes + (u >> 3) * kVPanel;
     float na[2], nb[2];
@@ -209,17 +235,35 @@ __device__ __forceinline__ void load_role(const GdnArgs& a, Smem& sm, const Wait
       na[i] = t < len ? elem(ga, (int64_t)(row0 + t) * a.a_rs) : 0.0f;
       nb[i] = t < len ? elem(gb, (int64_t)(row0 + t) * a.b_rs) : 0.0f;
     }
-#pragma unroll 8
-    for (int i = 0; i < kC / 2; ++i) {
-      const int r = i * 2 + r2;
-      const int64_t t = (int64_t)n * kC + r;
-      const bool in = t < len;
-      const int64_t tt = in ? t : 0;
-      cp_async16(base + sw128(r, u & 7), kp + tt * a.k_rs * 2, in);
-      cp_async16(base + sw128(kC + r, u & 7), qp + tt * a.q_rs * 2, in);
-      cp_async16(vbase + sw128(r, u & 7), vp + tt * a.v_rs * 2, in);
+    const bool whole = len - n * kC >= kC;
+    if (whole) {
+      boxed = n + 1;
+      if (lane == 0) {
+        const uint32_t at = smem_addr(sm.stage[st]);
+        const int y = row0 + n * kC;
+        mbar_arrive_tx(&sm.ctl.full[st], kStageBytes);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          tc::tma_load_2d(at + p * kPanel, &maps.k, hk * kD + p * 64, y, &sm.ctl.full[st]);
+          tc::tma_load_2d(at + p * kPanel + kC * 128, &maps.q, hk * kD + p * 64, y,
+                          &sm.ctl.full[st]);
+          tc::tma_load_2d(at + kKQBytes + p * kVPanel, &maps.v, h * kD + p * 64, y,
+                          &sm.ctl.full[st]);
+        }
+      }
+    } else {
+#pragma unroll 4
+      for (int i = 0; i < kC / 2; ++i) {
+        const int r = i * 2 + r2;
+        const int64_t t = (int64_t)n * kC + r;
+        const bool in = t < len;
+        const int64_t tt = in ? t : 0;
+        cp_async16(base + sw128(r, u & 7), kp + tt * a.k_rs * 2, in);
+        cp_async16(base + sw128(kC + r, u & 7), qp + tt * a.q_rs * 2, in);
+        cp_async16(vbase + sw128(r, u & 7), vp + tt * a.v_rs * 2, in);
+      }
+      cp_async_commit();
     }
-    cp_async_commit();
     float w[2], f[2], be[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -247,8 +291,8 @@ __device__ __forceinline__ void load_role(const GdnArgs& a, Smem& sm, const Wait
       }
     add(w[1], f[1], __shfl_sync(0xffffffffu, w[0], 31), __shfl_sync(0xffffffffu, f[0], 31));
     if (n >= 2 && !wait(&sm.ctl.gate_empty[n & 1], (n >> 1) - 1)) {
-      cp_async_wait<0>();      // nothing lands after the block ends
-      return;
+      warp_arrive(&sm.ctl.full[st]);
+      break;
     }
     Gate& G = sm.gate[n & 1];
 #pragma unroll
@@ -257,86 +301,88 @@ __device__ __forceinline__ void load_role(const GdnArgs& a, Smem& sm, const Wait
       G.lo[i * 32 + lane] = f[i];
       G.beta[i * 32 + lane] = be[i];
     }
-    cp_async_wait<0>();
-    fence_proxy_async();
+    if (!whole) {
+      cp_async_wait<0>();
+      fence_proxy_async();
+      if (lane == 0) mbar_arrive(&sm.ctl.full[st]);
+    }
     warp_arrive(&sm.ctl.full[st]);
+  }
+  if (n < chunks) {         // given up: no copy lands after the block ends
+    cp_async_wait<0>();
+    for (int i = max(boxed - kStages, 0); i < boxed; ++i)
+      drain(&sm.ctl.full[i % kStages], i / kStages, a.dev_err);
   }
 }
 
 // ---- the warps that look one chunk ahead ------------------------------------
 
-// Element (i, j) of T times beta_j, as bf16 hi and lo.
-__device__ __forceinline__ void put_t(unsigned char* tp, int i, int j, float v) {
-  const uint32_t at = sw128(i, j >> 3) + (j & 7) * 2;
-  const uint32_t hb = pack_bf16x2(v, 0.0f);
-  *reinterpret_cast<uint16_t*>(tp + at) = (uint16_t)hb;
-  *reinterpret_cast<uint16_t*>(tp + kTBytes + at) =
-      (uint16_t)pack_bf16x2(v - __uint_as_float(hb << 16), 0.0f);
+// Four pairs of fp32 as bf16 hi and lo.
+__device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
+  tc::split2(x[0], x[1], hi.x, lo.x);
+  tc::split2(x[2], x[3], hi.y, lo.y);
+  tc::split2(x[4], x[5], hi.z, lo.z);
+  tc::split2(x[6], x[7], hi.w, lo.w);
 }
 
-// The 16 x 16 blocks of T below diagonal block J. With U = T^T,
+// The 16 x 16 blocks of T below diagonal block J. With U = T^T, which is also
+// how T is stored for the tensor cores,
 //   U_Ji = -(sum_{J <= k < i} U_Jk A_ik^T) U_ii,
 // so that each result is the left operand of the next product, where the
-// output layout of one warp product is the input layout of the next, and A and
-// T_ii are read from shared memory along their rows. Products of hi and lo
-// parts as everywhere (lo * lo left out).
+// output layout of one warp product is the input layout of the next, and the
+// right operands come from shared memory as they lie there. Products of hi and
+// lo parts as everywhere (lo * lo left out), the mixed ones in a sum of their
+// own: shorter chains. Row j of the stored U is scaled by beta_j.
 template <int J>
 __device__ __forceinline__ void t_blocks(const Smem& sm, unsigned char* tp, const float* beta) {
   const int lane = threadIdx.x & 31, r = lane >> 2, c = (lane & 3) * 2;
-  uint32_t uh[4][4], ul[4][4];      // U_Jk as left operands
+  const int lrow = lane & 15, lcol = (lane >> 4) * 8;    // ldmatrix: row and column of the lane
+  uint32_t uh[4][4], ul[4][4];                           // U_Jk as left operands
   const float b0 = beta[J * kB + r], b1 = beta[J * kB + r + 8];
-  {
-    const float(*t)[kBPitch] = sm.Td[J];
-    tc::split2(t[c][r], t[c + 1][r], uh[J][0], ul[J][0]);
-    tc::split2(t[c][r + 8], t[c + 1][r + 8], uh[J][1], ul[J][1]);
-    tc::split2(t[c + 8][r], t[c + 9][r], uh[J][2], ul[J][2]);
-    tc::split2(t[c + 8][r + 8], t[c + 9][r + 8], uh[J][3], ul[J][3]);
-  }
-  // two sums, of the hi * hi and of the mixed products: shorter chains
-  auto times = [&](float(&acc)[2][4], float(&mix)[2][4], const uint32_t(&ah)[4],
-                   const uint32_t(&al)[4], const float* base, int pitch) {
-    // (rows n of `base` along k)
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      const float* q = base + (nt * 8 + r) * pitch + c;
-      const float2 x = *reinterpret_cast<const float2*>(q);
-      const float2 y = *reinterpret_cast<const float2*>(q + 8);
-      uint32_t h0, l0, h1, l1;
-      tc::split2(x.x, x.y, h0, l0);
-      tc::split2(y.x, y.y, h1, l1);
-      tc::mma16(acc[nt], ah, h0, h1);
-      tc::mma16(mix[nt], ah, l0, l1);
-      tc::mma16(mix[nt], al, h0, h1);
-    }
-  };
+  tc::ldmatrix4(uh[J], smem_addr(&sm.Uh[J * kB + lrow][lcol]));
+  tc::ldmatrix4(ul[J], smem_addr(&sm.Ul[J * kB + lrow][lcol]));
 #pragma unroll
   for (int i = J + 1; i < 4; ++i) {
     float x[2][4] = {}, xm[2][4] = {};
 #pragma unroll
-    for (int k = J; k < i; ++k) times(x, xm, uh[k], ul[k], &sm.A[i * kB][k * kB], kAPitch);
+    for (int k = J; k < i; ++k) {
+      uint32_t h[4], l[4];      // n-tile nt: registers nt and nt + 2
+      tc::ldmatrix4(h, smem_addr(&sm.Ah[(i - 1) * kB + lrow][k * kB + lcol]));
+      tc::ldmatrix4(l, smem_addr(&sm.Al[(i - 1) * kB + lrow][k * kB + lcol]));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e >> 2][e & 3] += xm[e >> 2][e & 3];
+      for (int nt = 0; nt < 2; ++nt) {
+        tc::mma16(x[nt], uh[k], h[nt], h[nt + 2]);
+        tc::mma16(xm[nt], uh[k], l[nt], l[nt + 2]);
+        tc::mma16(xm[nt], ul[k], h[nt], h[nt + 2]);
+      }
+    }
     uint32_t xh[4], xl[4];
-    tc::split2(x[0][0], x[0][1], xh[0], xl[0]);
-    tc::split2(x[0][2], x[0][3], xh[1], xl[1]);
-    tc::split2(x[1][0], x[1][1], xh[2], xl[2]);
-    tc::split2(x[1][2], x[1][3], xh[3], xl[3]);
-    float y[2][4] = {}, ym[2][4] = {};
-    times(y, ym, xh, xl, &sm.Td[i][0][0], kBPitch);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e >> 2][e & 3] += ym[e >> 2][e & 3];
-    if (i < 3) {
-      tc::split2(-y[0][0], -y[0][1], uh[i][0], ul[i][0]);
-      tc::split2(-y[0][2], -y[0][3], uh[i][1], ul[i][1]);
-      tc::split2(-y[1][0], -y[1][1], uh[i][2], ul[i][2]);
-      tc::split2(-y[1][2], -y[1][3], uh[i][3], ul[i][3]);
+    for (int e = 0; e < 4; ++e)
+      tc::split2(x[e >> 1][(e & 1) * 2] + xm[e >> 1][(e & 1) * 2],
+                 x[e >> 1][(e & 1) * 2 + 1] + xm[e >> 1][(e & 1) * 2 + 1], xh[e], xl[e]);
+    float y[2][4] = {}, ym[2][4] = {};
+    uint32_t h[4], l[4];        // n-tile nt: registers 2 nt and 2 nt + 1
+    tc::ldmatrix4_trans(h, smem_addr(&sm.Uh[i * kB + lrow][lcol]));
+    tc::ldmatrix4_trans(l, smem_addr(&sm.Ul[i * kB + lrow][lcol]));
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      tc::mma16(y[nt], xh, h[2 * nt], h[2 * nt + 1]);
+      tc::mma16(ym[nt], xh, l[2 * nt], l[2 * nt + 1]);
+      tc::mma16(ym[nt], xl, h[2 * nt], h[2 * nt + 1]);
     }
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)   // y[nt][e] = -U_Ji[m][n]
-        put_t(tp, i * kB + nt * 8 + c + (e & 1), J * kB + r + (e >> 1) * 8,
-              -y[nt][e] * ((e >> 1) ? b1 : b0));
+    for (int e = 0; e < 4; ++e) {   // rows r, r + 8 (e & 1) of n-tile e >> 1
+      const float u0 = -(y[e >> 1][(e & 1) * 2] + ym[e >> 1][(e & 1) * 2]);
+      const float u1 = -(y[e >> 1][(e & 1) * 2 + 1] + ym[e >> 1][(e & 1) * 2 + 1]);
+      if (i < 3) tc::split2(u0, u1, uh[i][e], ul[i][e]);
+      const float be = (e & 1) ? b1 : b0;
+      uint32_t sh, sl;
+      tc::split2(be * u0, be * u1, sh, sl);
+      const uint32_t at = sw128(J * kB + r + (e & 1) * 8, i * 2 + (e >> 1)) + c * 2;
+      *reinterpret_cast<uint32_t*>(tp + at) = sh;
+      *reinterpret_cast<uint32_t*>(tp + kTBytes + at) = sl;
+    }
   }
 }
 
@@ -420,47 +466,53 @@ __device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait
     if (is_k ? n >= 1 && !wait(&sm.ctl.a_empty, n - 1)
              : n >= 2 && !wait(&sm.ctl.tp_empty[bf], (n >> 1) - 1))
       return;
-    unsigned char* const tp = sm.tp[bf];
+    unsigned char* const scores = sm.tp[bf] + 2 * kTBytes;
     const uint32_t d1 = tmem + kColD1 + ((uint32_t)(warp * 32) << 16);
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      uint32_t x[32];
-      tc::ld32(d1 + hf * 32, x);
+    for (int J = 0; J < 4; ++J) {
+      uint32_t x[16];
+      tc::ld16(d1 + J * 16, x);
       tc::wait_ld(x);
+      // blocks right of the diagonal are zero and their factors not set
+      const float m = J < blk ? off : fac;
+      const float* q = J == blk ? sm.ed[r] : &sm.tab[blk][J * kB];
+      float y[16];
 #pragma unroll
-      for (int jb = 0; jb < 2; ++jb) {
-        const int J = hf * 2 + jb;
-        const float m = J < blk ? off : J == blk ? fac : 0.0f;
-        const float* q = J == blk ? sm.ed[r] : &sm.tab[blk][J * kB];
-        float y[16];
+      for (int j4 = 0; j4 < 16; j4 += 4) {
+        const float4 t = J <= blk ? *reinterpret_cast<const float4*>(q + j4)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        mul_x2(y[j4], y[j4 + 1], m * t.x, m * t.y, __uint_as_float(x[j4]),
+               __uint_as_float(x[j4 + 1]));
+        mul_x2(y[j4 + 2], y[j4 + 3], m * t.z, m * t.w, __uint_as_float(x[j4 + 2]),
+               __uint_as_float(x[j4 + 3]));
+      }
+      if (is_k) {
+        if (J < blk) {
 #pragma unroll
-        for (int j4 = 0; j4 < 4; ++j4) {
-          // blocks right of the diagonal are zero and their factors not set
-          const float4 t = J <= blk ? *reinterpret_cast<const float4*>(q + j4 * 4)
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-          const int e = jb * 16 + j4 * 4;
-          mul_x2(y[j4 * 4], y[j4 * 4 + 1], m * t.x, m * t.y, __uint_as_float(x[e]),
-                 __uint_as_float(x[e + 1]));
-          mul_x2(y[j4 * 4 + 2], y[j4 * 4 + 3], m * t.z, m * t.w, __uint_as_float(x[e + 2]),
-                 __uint_as_float(x[e + 3]));
+          for (int u = 0; u < 2; ++u) {
+            uint4 h, l;
+            split8(y + u * 8, h, l);
+            *reinterpret_cast<uint4*>(&sm.Ah[r - kB][J * kB + u * 8]) = h;
+            *reinterpret_cast<uint4*>(&sm.Al[r - kB][J * kB + u * 8]) = l;
+          }
+        } else if (J == blk) {
+#pragma unroll
+          for (int j4 = 0; j4 < 16; j4 += 4)
+            *reinterpret_cast<float4*>(&sm.Ad[r][j4]) =
+                make_float4(y[j4], y[j4 + 1], y[j4 + 2], y[j4 + 3]);
         }
-        if (is_k) {
+      } else {
 #pragma unroll
-          for (int j4 = 0; j4 < 4; ++j4)
-            *reinterpret_cast<float4*>(&sm.A[r][J * kB + j4 * 4]) =
-                make_float4(y[j4 * 4], y[j4 * 4 + 1], y[j4 * 4 + 2], y[j4 * 4 + 3]);
-        } else {
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            *reinterpret_cast<uint4*>(tp + 2 * kTBytes + sw128(r, J * 2 + u)) =
-                make_uint4(pack_bf16x2(y[u * 8], y[u * 8 + 1]),
-                           pack_bf16x2(y[u * 8 + 2], y[u * 8 + 3]),
-                           pack_bf16x2(y[u * 8 + 4], y[u * 8 + 5]),
-                           pack_bf16x2(y[u * 8 + 6], y[u * 8 + 7]));
-        }
+        for (int u = 0; u < 2; ++u)
+          *reinterpret_cast<uint4*>(scores + sw128(r, J * 2 + u)) =
+              make_uint4(pack_bf16x2(y[u * 8], y[u * 8 + 1]),
+                         pack_bf16x2(y[u * 8 + 2], y[u * 8 + 3]),
+                         pack_bf16x2(y[u * 8 + 4], y[u * 8 + 5]),
+                         pack_bf16x2(y[u * 8 + 6], y[u * 8 + 7]));
       }
     }
     tc::fence_before();
+    warp_arrive(&sm.ctl.d1_empty);
     if (is_k) {
       warp_arrive(&sm.ctl.a_full);
     } else {
@@ -491,7 +543,7 @@ __device__ __forceinline__ void inv_role(Smem& sm, const Wait& wait, int chunks)
       float acc[4] = {c == i ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int k4 = 0; k4 < i; k4 += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(&sm.A[b0 + i][b0 + k4]);
+        const float4 v = *reinterpret_cast<const float4*>(&sm.Ad[b0 + i][k4]);
         acc[0] = fmaf(-v.x, t[k4], acc[0]);
         if (k4 + 1 < i) acc[1] = fmaf(-v.y, t[k4 + 1], acc[1]);
         if (k4 + 2 < i) acc[2] = fmaf(-v.z, t[k4 + 2], acc[2]);
@@ -501,9 +553,16 @@ __device__ __forceinline__ void inv_role(Smem& sm, const Wait& wait, int chunks)
     }
     const float be = G.beta[b0 + c];
 #pragma unroll
-    for (int i = 0; i < kB; ++i) {
-      sm.Td[blk][i][c] = t[i];
-      put_t(tp, b0 + i, b0 + c, t[i] * be);
+    for (int u = 0; u < 2; ++u) {
+      uint4 h, l;
+      split8(t + u * 8, h, l);
+      *reinterpret_cast<uint4*>(&sm.Uh[b0 + c][u * 8]) = h;
+      *reinterpret_cast<uint4*>(&sm.Ul[b0 + c][u * 8]) = l;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[u * 8 + i] *= be;
+      split8(t + u * 8, h, l);
+      *reinterpret_cast<uint4*>(tp + sw128(b0 + c, blk * 2 + u)) = h;
+      *reinterpret_cast<uint4*>(tp + kTBytes + sw128(b0 + c, blk * 2 + u)) = l;
     }
     if (!meet(wait)) return;
     if (warp == 0) {
@@ -522,122 +581,79 @@ __device__ __forceinline__ void inv_role(Smem& sm, const Wait& wait, int chunks)
 
 // ---- the warps on the chain -------------------------------------------------
 
+// Thread: column `col` of S, dk (i / 32) * 64 + hf * 32 + i % 32 in S[i]: the
+// first 32 lie in the first half of dk for both warps of a column, so that the
+// two halves of S pass through the update and the split one after the other,
+// while the tensor cores work on the other one.
 template <typename ST>
-__device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait& wait, int row0,
-                                          int len, int h, int chunks, uint32_t tmem, bool init, int slot) {
+__device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait& wait, int h,
+                                          int chunks, uint32_t tmem, bool init, int slot) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int qd = warp & 3, hf = warp >> 2;
-  const int col = qd * 32 + lane;                       // the thread's column of S
+  const int col = qd * 32 + lane;
   const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
   ST* const sp = reinterpret_cast<ST*>(a.st) + (int64_t)(slot < 0 ? 0 : slot) * a.st_slot +
-                 (int64_t)h * a.st_head + (int64_t)hf * 64 * kD + col;
-  float S[64];                                          // dk hf * 64 + [0, 64)
+                 (int64_t)h * a.st_head + (int64_t)hf * 32 * kD + col;
+  float S[64];
 #pragma unroll
-  for (int i = 0; i < 64; ++i) S[i] = init ? elem(sp, i * kD) : 0.0f;
+  for (int i = 0; i < 64; ++i)
+    S[i] = init ? elem(sp, ((i >> 5) * 64 + (i & 31)) * kD) : 0.0f;
 
-  // outputs of chunk n: 32 tokens by 32 columns of each warp, turned round in 2
-  // KB of the chunk's V, which has been used, and stored in 16-byte units
-  char* const op = a.out + ((int64_t)row0 * a.out_rs + (int64_t)h * kD + qd * 32) * 2 +
-                   (lane & 3) * 16;
-  auto outputs = [&](int n) -> bool {
-    if (!wait(&sm.ctl.o_full, n)) return false;
+  // S = e^{G_C} S + update of chunk n, one half
+  auto advance = [&](int n, int part) -> bool {
+    if (!wait(&sm.ctl.sd_full[part], n)) return false;
     tc::fence_after();
-    uint32_t x[32], y[32];
-    tc::ld32(tl + kColQS + hf * 32, x);
-    tc::ld32(tl + kColO + hf * 32, y);
-    tc::wait_ld(x);
-    tc::wait_ld(y);
-    tc::fence_before();
-    warp_arrive(&sm.ctl.o_empty);
-    const Coef& C = sm.coef[n & 1];
-    unsigned char* const box = sm.stage[n % kStages] + kKQBytes + warp * 2048;
-    uint16_t* const o = reinterpret_cast<uint16_t*>(box) + lane;
-#pragma unroll
-    for (int i4 = 0; i4 < 8; ++i4) {
-      const float4 c1 = *reinterpret_cast<const float4*>(&C.o1[hf * 32 + i4 * 4]);
-      const float4 c2 = *reinterpret_cast<const float4*>(&C.o2[hf * 32 + i4 * 4]);
-      float v[4];
-      mul_x2(v[0], v[1], c2.x, c2.y, __uint_as_float(y[i4 * 4]), __uint_as_float(y[i4 * 4 + 1]));
-      mul_x2(v[2], v[3], c2.z, c2.w, __uint_as_float(y[i4 * 4 + 2]),
-             __uint_as_float(y[i4 * 4 + 3]));
-      fma_x2(v[0], v[1], c1.x, c1.y, __uint_as_float(x[i4 * 4]), __uint_as_float(x[i4 * 4 + 1]),
-             v[0], v[1]);
-      fma_x2(v[2], v[3], c1.z, c1.w, __uint_as_float(x[i4 * 4 + 2]),
-             __uint_as_float(x[i4 * 4 + 3]), v[2], v[3]);
-      const uint32_t p0 = pack_bf16x2(v[0], v[1]), p1 = pack_bf16x2(v[2], v[3]);
-      o[(i4 * 4) * 32] = (uint16_t)p0;
-      o[(i4 * 4 + 1) * 32] = (uint16_t)(p0 >> 16);
-      o[(i4 * 4 + 2) * 32] = (uint16_t)p1;
-      o[(i4 * 4 + 3) * 32] = (uint16_t)(p1 >> 16);
-    }
-    warp_arrive(&sm.ctl.coef_empty[n & 1]);
-    uint4 q[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      q[i] = *reinterpret_cast<const uint4*>(box + (i * 32 + lane) * 16);
-    fence_proxy_async();
-    warp_arrive(&sm.ctl.empty[n % kStages]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t t = (int64_t)n * kC + hf * 32 + i * 8 + (lane >> 2);
-      if (t < len) *reinterpret_cast<uint4*>(op + t * a.out_rs * 2) = q[i];
-    }
-    return true;
-  };
-  // S = e^{G_C} S + update of chunk n
-  auto advance = [&](int n, int part) {
     uint32_t x[32];
-    tc::ld32(tl + kColS + hf * 64 + part * 32, x);
-    tc::wait_ld(x);
+    tc::ld32(tl + kColS + part * 64 + hf * 32, x);
     const float ec = sm.coef[n & 1].ec;
+    tc::wait_ld(x);
 #pragma unroll
     for (int i = 0; i < 32; i += 2)
       fma_x2(S[part * 32 + i], S[part * 32 + i + 1], ec, ec, S[part * 32 + i],
              S[part * 32 + i + 1], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+    return true;
   };
 
   for (int n = 0; n < chunks; ++n) {
     const Coef& C = sm.coef[n & 1];
     // ---- S: add the last chunk's update, split, hand to the tensor cores
-    if (n > 0) {
-      if (!wait(&sm.ctl.sd_full, n - 1)) return;
-      tc::fence_after();
-      advance(n - 1, 0);
-      advance(n - 1, 1);
-    }
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
+      if (n > 0 && !advance(n - 1, part)) return;
       uint32_t hi[16], lo[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         tc::split2(S[part * 32 + 2 * i], S[part * 32 + 2 * i + 1], hi[i], lo[i]);
-      tc::st16(tl + kColS + hf * 64 + part * 16, hi);
-      tc::st16(tl + kColS + hf * 64 + 32 + part * 16, lo);
+      tc::st16(tl + kColS + part * 64 + hf * 32, hi);
+      tc::st16(tl + kColS + part * 64 + hf * 32 + 16, lo);
+      tc::wait_st();
+      tc::fence_before();
+      warp_arrive(&sm.ctl.s_full[part]);
     }
-    tc::wait_st();
-    tc::fence_before();
-    warp_arrive(&sm.ctl.s_full);
-    if (n > 0 && !outputs(n - 1)) return;
+    if (n > 0) warp_arrive(&sm.ctl.coef_empty[(n - 1) & 1]);
     // ---- R
     if (!wait(&sm.ctl.coef_full[n & 1], n >> 1) || !wait(&sm.ctl.ks_full, n)) return;
     tc::fence_after();
     {
-      uint32_t x[32], hi[16], lo[16];
+      uint32_t x[32];
       tc::ld32(tl + kColKS + hf * 32, x);
       tc::wait_ld(x);
 #pragma unroll
-      for (int i4 = 0; i4 < 8; ++i4) {
-        const float4 c4 = *reinterpret_cast<const float4*>(&C.rc[hf * 32 + i4 * 4]);
-        float q[4];
-        mul_x2(q[0], q[1], c4.x, c4.y, __uint_as_float(x[i4 * 4]),
-               __uint_as_float(x[i4 * 4 + 1]));
-        mul_x2(q[2], q[3], c4.z, c4.w, __uint_as_float(x[i4 * 4 + 2]),
-               __uint_as_float(x[i4 * 4 + 3]));
-        tc::split2(q[0], q[1], hi[i4 * 2], lo[i4 * 2]);
-        tc::split2(q[2], q[3], hi[i4 * 2 + 1], lo[i4 * 2 + 1]);
+      for (int g = 0; g < 2; ++g) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const int t = g * 16 + i * 2;
+          const float4 c4 = *reinterpret_cast<const float4*>(&C.rc[hf * 32 + t]);
+          float q[4];
+          mul_x2(q[0], q[1], c4.x, c4.y, __uint_as_float(x[t]), __uint_as_float(x[t + 1]));
+          mul_x2(q[2], q[3], c4.z, c4.w, __uint_as_float(x[t + 2]), __uint_as_float(x[t + 3]));
+          tc::split2(q[0], q[1], hi[i], lo[i]);
+          tc::split2(q[2], q[3], hi[i + 1], lo[i + 1]);
+        }
+        tc::st8(tl + kColR + hf * 16 + g * 8, hi);
+        tc::st8(tl + kColR + 32 + hf * 16 + g * 8, lo);
       }
-      tc::st16(tl + kColR + hf * 16, hi);
-      tc::st16(tl + kColR + 32 + hf * 16, lo);
     }
     tc::wait_st();
     tc::fence_before();
@@ -646,118 +662,192 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
     if (!wait(&sm.ctl.vn_full, n)) return;
     tc::fence_after();
     {
-      uint32_t x[32], hi[16], lo[16], on[16];
+      uint32_t x[32];
       tc::ld32(tl + kColVN + hf * 32, x);
       tc::wait_ld(x);
 #pragma unroll
-      for (int i4 = 0; i4 < 8; ++i4) {
-        const float4 d4 = *reinterpret_cast<const float4*>(&C.vd[hf * 32 + i4 * 4]);
-        const float v0 = __uint_as_float(x[i4 * 4]), v1 = __uint_as_float(x[i4 * 4 + 1]),
-                    v2 = __uint_as_float(x[i4 * 4 + 2]), v3 = __uint_as_float(x[i4 * 4 + 3]);
-        on[i4 * 2] = pack_bf16x2(v0, v1);
-        on[i4 * 2 + 1] = pack_bf16x2(v2, v3);
-        float q[4];
-        mul_x2(q[0], q[1], d4.x, d4.y, v0, v1);
-        mul_x2(q[2], q[3], d4.z, d4.w, v2, v3);
-        tc::split2(q[0], q[1], hi[i4 * 2], lo[i4 * 2]);
-        tc::split2(q[2], q[3], hi[i4 * 2 + 1], lo[i4 * 2 + 1]);
+      for (int g = 0; g < 2; ++g) {
+        uint32_t hi[8], lo[8], on[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const int t = g * 16 + i * 2;
+          const float4 d4 = *reinterpret_cast<const float4*>(&C.vd[hf * 32 + t]);
+          const float v0 = __uint_as_float(x[t]), v1 = __uint_as_float(x[t + 1]),
+                      v2 = __uint_as_float(x[t + 2]), v3 = __uint_as_float(x[t + 3]);
+          on[i] = pack_bf16x2(v0, v1);
+          on[i + 1] = pack_bf16x2(v2, v3);
+          float q[4];
+          mul_x2(q[0], q[1], d4.x, d4.y, v0, v1);
+          mul_x2(q[2], q[3], d4.z, d4.w, v2, v3);
+          tc::split2(q[0], q[1], hi[i], lo[i]);
+          tc::split2(q[2], q[3], hi[i + 1], lo[i + 1]);
+        }
+        tc::st8(tl + kColR + hf * 16 + g * 8, hi);
+        tc::st8(tl + kColR + 32 + hf * 16 + g * 8, lo);
+        tc::st8(tl + kColN + hf * 16 + g * 8, on);
       }
-      tc::st16(tl + kColR + hf * 16, hi);
-      tc::st16(tl + kColR + 32 + hf * 16, lo);
-      tc::st16(tl + kColN + hf * 16, on);
     }
     tc::wait_st();
     tc::fence_before();
     warp_arrive(&sm.ctl.vd_full);
   }
-  if (!wait(&sm.ctl.sd_full, chunks - 1)) return;
-  tc::fence_after();
-  advance(chunks - 1, 0);
-  advance(chunks - 1, 1);
-  if (!outputs(chunks - 1)) return;
+  if (!advance(chunks - 1, 0) || !advance(chunks - 1, 1)) return;
   if (slot >= 0)
 #pragma unroll
     for (int i = 0; i < 64; ++i) {
       const auto raw = f32_to_raw<ST>(S[i]);
-      *reinterpret_cast<std::remove_const_t<decltype(raw)>*>(sp + i * kD) = raw;
+      *reinterpret_cast<std::remove_const_t<decltype(raw)>*>(
+          sp + ((i >> 5) * 64 + (i & 31)) * kD) = raw;
     }
+}
+
+// Outputs: a warp takes 32 columns, 16 tokens at a time, turns them round in
+// the chunk's V, which has been used, and stores 16-byte units.
+__device__ __forceinline__ void out_role(const GdnArgs& a, Smem& sm, const Wait& wait, int row0,
+                                         int len, int h, int chunks, uint32_t tmem) {
+  const int qd = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
+  char* const op = a.out + ((int64_t)row0 * a.out_rs + (int64_t)h * kD + qd * 32) * 2 +
+                   (lane & 3) * 16;
+  for (int n = 0; n < chunks; ++n) {
+    if (!wait(&sm.ctl.o_full, n)) return;
+    tc::fence_after();
+    const Coef& C = sm.coef[n & 1];
+    unsigned char* const box = sm.stage[n % kStages] + kKQBytes + qd * 4096;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      uint32_t x[16], y[16];
+      tc::ld16(tl + kColQS + g * 16, x);
+      tc::ld16(tl + kColO + g * 16, y);
+      tc::wait_ld(x);
+      tc::wait_ld(y);
+      if (g == 3) {
+        tc::fence_before();
+        warp_arrive(&sm.ctl.o_empty);
+      }
+      uint16_t* const o = reinterpret_cast<uint16_t*>(box + g * 1024) + lane;
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float2 c1 = *reinterpret_cast<const float2*>(&C.o1[g * 16 + i]);
+        const float2 c2 = *reinterpret_cast<const float2*>(&C.o2[g * 16 + i]);
+        float v0, v1;
+        mul_x2(v0, v1, c2.x, c2.y, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+        fma_x2(v0, v1, c1.x, c1.y, __uint_as_float(x[i]), __uint_as_float(x[i + 1]), v0, v1);
+        const uint32_t p = pack_bf16x2(v0, v1);
+        o[i * 32] = (uint16_t)p;
+        o[(i + 1) * 32] = (uint16_t)(p >> 16);
+      }
+    }
+    warp_arrive(&sm.ctl.coef_empty[n & 1]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 q = *reinterpret_cast<const uint4*>(box + (i * 32 + lane) * 16);
+      const int64_t t = (int64_t)n * kC + i * 8 + (lane >> 2);
+      if (t < len) *reinterpret_cast<uint4*>(op + t * a.out_rs * 2) = q;
+    }
+    fence_proxy_async();
+    warp_arrive(&sm.ctl.empty[n % kStages]);
+  }
 }
 
 // ---- the warp that issues the tensor products -------------------------------
 
 // On the chain: S^T k (16 products of N = 64, 512 clocks), T R (12, 384), the
-// update (8 of N = 128, 512). Beside it: S^T q, in-chunk outputs, and, while
-// the chain's warps work on S, T V of this chunk and the scores of the next.
+// update (16, 512). Beside it: S^T q, in-chunk outputs, and, while the chain's
+// warps work on S, T V of this chunk and the scores of the next ones.
 __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks, uint32_t tmem) {
-  constexpr uint32_t kId = tc::idesc(128, 64), kIdV = tc::idesc(128, 64, true),
-                     kIdUpd = tc::idesc(128, 128, false, true);
+  constexpr uint32_t kId = tc::idesc(128, 64), kIdT = tc::idesc(128, 64, false, true),
+                     kIdV = tc::idesc(128, 64, true, true);
   const uint32_t stage0 = smem_addr(sm.stage[0]), tp0 = smem_addr(sm.tp[0]);
   auto panel = [&](int st, int ks, int row) {   // 16 dk of rows [row, ..) of [K; Q]
     return stage0 + st * kStageBytes + (ks >> 2) * kPanel + (ks & 3) * 32 + row * 128;
   };
-  auto scores = [&](int n) -> bool {            // [K; Q] K^T of chunk n
-    const int st = n % kStages;
-    if (!wait(&sm.ctl.full[st], n / kStages)) return false;
+  auto s_col = [&](int ks, int t) {             // 16 dk of S, hi or lo
+    return tmem + kColS + (ks >> 1) * 32 + t * 16 + (ks & 1) * 8;
+  };
+  int scored = 0, tved = 0;                     // chunks whose products are issued
+  auto scores = [&]() {                         // [K; Q] K^T of chunk `scored`
     tc::fence_after();
     if (tc::elect()) {
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
-        const uint64_t d = tc::desc_sw128(panel(st, ks, 0), 16);
+        const uint64_t d = tc::desc_sw128(panel(scored % kStages, ks, 0), 16);
         tc::mma_ss(tmem + kColD1, d, d, kId, ks > 0);
       }
       tc::commit(&sm.ctl.d1_full);
     }
     __syncwarp();
-    return true;
+    ++scored;
   };
-  auto tv = [&](int n) -> bool {                // (T V)^T of chunk n: V read along dv
-    if (!wait(&sm.ctl.t_full, n)) return false;
+  auto scores_if_ready = [&]() {
+    if (scored < chunks &&
+        __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.full[scored % kStages],
+                                               (scored / kStages) & 1)) &&
+        (scored == 0 ||
+         __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.d1_empty, (scored - 1) & 1))))
+      scores();
+  };
+  auto tv = [&]() {                             // (T V)^T of chunk `tved`: V read along dv
     tc::fence_after();
-    const uint32_t tp = tp0 + (n & 1) * kTP, v = stage0 + (n % kStages) * kStageBytes + kKQBytes;
+    const uint32_t tp = tp0 + (tved & 1) * kTP,
+                   v = stage0 + (tved % kStages) * kStageBytes + kKQBytes;
     if (tc::elect()) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           tc::mma_ss(tmem + kColVN, tc::desc_sw128(v + ks * 2048, kVPanel),
-                     tc::desc_sw128(tp + t * kTBytes + ks * 32, 16), kIdV, (t | ks) > 0);
+                     tc::desc_sw128(tp + t * kTBytes + ks * 2048, kTBytes), kIdV, (t | ks) > 0);
     }
     __syncwarp();
-    return true;
+    ++tved;
   };
-  if (!scores(0)) return;
-  int scored = 1, tved = 0;                     // chunks whose products are issued
   for (int n = 0; n < chunks; ++n) {
     const int st = n % kStages, bf = n & 1;
     const uint32_t tp = tp0 + bf * kTP;
-    if (!wait(&sm.ctl.s_full, n)) return;
-    // N of the last chunk lies where S^T k goes
-    if (n > 0 && !wait(&sm.ctl.o_full, n - 1)) return;
-    tc::fence_after();
-    if (tc::elect()) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)               // S hi, S lo
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tc::mma_ts(tmem + kColKS, tmem + kColS + (ks >> 2) * 64 + t * 32 + (ks & 3) * 8,
-                     tc::desc_sw128(panel(st, ks, 0), 16), kId, (t | ks) > 0);
-      tc::commit(&sm.ctl.ks_full);
+    if (n == 0) {
+      if (!wait(&sm.ctl.full[0], 0)) return;
+      scores();
     }
-    __syncwarp();
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      if (!wait(&sm.ctl.s_full[part], n)) return;
+      // N of the last chunk lies where S^T k goes
+      if (part == 0 && n > 0 && !wait(&sm.ctl.o_full, n - 1)) return;
+      tc::fence_after();
+      if (tc::elect()) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)             // S hi, S lo
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4)
+            tc::mma_ts(tmem + kColKS, s_col(part * 4 + k4, t),
+                       tc::desc_sw128(panel(st, part * 4 + k4, 0), 16), kId,
+                       (part | t | k4) > 0);
+        if (part == 1) tc::commit(&sm.ctl.ks_full);
+      }
+      __syncwarp();
+    }
     if (n > 0 && !wait(&sm.ctl.o_empty, n - 1)) return;
     tc::fence_after();
     if (tc::elect()) {
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks)
-        tc::mma_ts(tmem + kColQS, tmem + kColS + (ks >> 2) * 64 + (ks & 3) * 8,
-                   tc::desc_sw128(panel(st, ks, kC), 16), kId, ks > 0);
+        tc::mma_ts(tmem + kColQS, s_col(ks, 0), tc::desc_sw128(panel(st, ks, kC), 16), kId,
+                   ks > 0);
       tc::commit(&sm.ctl.qs_done);
     }
     __syncwarp();
     if (tved == n) {
-      if (!tv(n)) return;
-      ++tved;
+      while (scored <= n) {
+        if (!wait(&sm.ctl.full[scored % kStages], scored / kStages) ||
+            (scored > 0 && !wait(&sm.ctl.d1_empty, scored - 1)))
+          return;
+        scores();
+      }
+      if (!wait(&sm.ctl.t_full, n)) return;
+      tv();
     }
+    scores_if_ready();
     if (!wait(&sm.ctl.r_full, n)) return;
     tc::fence_after();
     if (tc::elect()) {
@@ -766,25 +856,27 @@ __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks,
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           tc::mma_ts(tmem + kColVN, tmem + kColR + (t == 1 ? 32 : 0) + ks * 8,
-                     tc::desc_sw128(tp + (t == 2 ? kTBytes : 0) + ks * 32, 16), kId, true);
+                     tc::desc_sw128(tp + (t == 2 ? kTBytes : 0) + ks * 2048, kTBytes), kIdT,
+                     true);
       tc::commit(&sm.ctl.vn_full);
     }
     __syncwarp();
-    if (scored == n + 1 && n + 1 < chunks) {
-      if (!scores(n + 1)) return;
-      ++scored;
-    }
+    scores_if_ready();
     if (!wait(&sm.ctl.vd_full, n) || !wait(&sm.ctl.qs_done, n)) return;
     tc::fence_after();
     if (tc::elect()) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)               // K read along dk: 16 tokens a step
+      for (int part = 0; part < 2; ++part) {    // K read along dk, 64 at a time
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          tc::mma_ts(tmem + kColS, tmem + kColR + t * 32 + ks * 8,
-                     tc::desc_sw128(stage0 + st * kStageBytes + ks * 2048, kPanel), kIdUpd,
-                     (t | ks) > 0);
-      tc::commit(&sm.ctl.sd_full);
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            tc::mma_ts(tmem + kColS + part * 64, tmem + kColR + t * 32 + ks * 8,
+                       tc::desc_sw128(stage0 + st * kStageBytes + part * kPanel + ks * 2048,
+                                      kPanel),
+                       kIdT, (t | ks) > 0);
+        tc::commit(&sm.ctl.sd_full[part]);
+      }
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
         tc::mma_ts(tmem + kColO, tmem + kColN + ks * 8,
@@ -794,22 +886,16 @@ __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks,
       tc::commit(&sm.ctl.tp_empty[bf]);
     }
     __syncwarp();
-    // if T of the next chunk is there already, its product with V and the
-    // scores of the chunk behind run while S is worked on
-    if (n + 1 < chunks && __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.t_full, (n + 1) & 1))) {
-      if (!tv(n + 1)) return;
-      ++tved;
-      if (n + 2 < chunks && __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.full[(n + 2) % kStages],
-                                                                 ((n + 2) / kStages) & 1))) {
-        if (!scores(n + 2)) return;
-        ++scored;
-      }
-    }
+    // T of the next chunk, if it is there already: its product with V runs
+    // while S is worked on
+    scores_if_ready();
+    if (n + 1 < chunks && __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.t_full, (n + 1) & 1)))
+      tv();
   }
 }
 
 template <typename ST>
-__global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a) {
+__global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a, const __grid_constant__ Maps maps) {
   extern __shared__ __align__(1024) unsigned char gdn_dyn[];
   Smem& sm = *reinterpret_cast<Smem*>(
       gdn_dyn + ((1024u - (smem_addr(gdn_dyn) & 1023u)) & 1023u));
@@ -829,14 +915,16 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
   if (tid == 0) {
     Ctl& c = sm.ctl;
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&c.full[i], 1);
-      mbar_init(&c.empty[i], 1 + kScanWarps);
+      mbar_init(&c.full[i], 2);                // rows, gates
+      mbar_init(&c.empty[i], 1 + kOutWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.gate_empty[i], kPrepWarps + kInvWarps);
       mbar_init(&c.tp_empty[i], 1);
       mbar_init(&c.coef_full[i], kPrepWarps);
-      mbar_init(&c.coef_empty[i], kScanWarps);
+      mbar_init(&c.coef_empty[i], kScanWarps + kOutWarps);
+      mbar_init(&c.s_full[i], kScanWarps);
+      mbar_init(&c.sd_full[i], 1);
     }
     mbar_init(&c.d1_full, 1);
     mbar_init(&c.prep_meet, kPrepWarps);
@@ -844,24 +932,23 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
     mbar_init(&c.a_full, 2);
     mbar_init(&c.a_empty, kInvWarps);
     mbar_init(&c.t_full, 2 + kInvWarps);     // scores, T
-    mbar_init(&c.s_full, kScanWarps);
+    mbar_init(&c.d1_empty, kPrepWarps);
     mbar_init(&c.ks_full, 1);
     mbar_init(&c.qs_done, 1);
     mbar_init(&c.r_full, kScanWarps);
     mbar_init(&c.vn_full, 1);
     mbar_init(&c.vd_full, kScanWarps);
-    mbar_init(&c.sd_full, 1);
     mbar_init(&c.o_full, 1);
-    mbar_init(&c.o_empty, kScanWarps);
+    mbar_init(&c.o_empty, kOutWarps);
     mbar_init(&c.fin, 1);
     c.abort = 0;
     fence_mbar_init();
   }
-  // blocks of T right of the diagonal are zero in both buffers: rows [0, 48),
-  // units from the row's next block on
+  // blocks of U left of the diagonal are zero in both buffers: rows [16, 64),
+  // units before the row's block
   for (int i = tid; i < 2 * 2 * 48 * 8; i += kThreadsC) {
-    const int u = i & 7, r = (i >> 3) % 48, m = (i / 384) & 1, b = i / 768;
-    if (u >= (r / kB + 1) * 2)
+    const int u = i & 7, r = kB + (i >> 3) % 48, m = (i / 384) & 1, b = i / 768;
+    if (u < r / kB * 2)
       *reinterpret_cast<uint4*>(sm.tp[b] + m * kTBytes + sw128(r, u)) =
           make_uint4(0u, 0u, 0u, 0u);
   }
@@ -880,11 +967,11 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
 
   if (warp < kScanWarps) {
     more_regs<kRegsScan>();
-    scan_role<ST>(a, sm, wait, row0, len, h, chunks, tmem, init, slot);
+    scan_role<ST>(a, sm, wait, h, chunks, tmem, init, slot);
   } else if (warp < kWarpInv0) {
     fewer_regs<kRegsPrep>();
     prep_role(a, sm, wait, chunks, tmem);
-  } else {
+  } else if (warp < kWarpOut0) {
     fewer_regs<kRegsRest>();
     if (warp < kWarpMma) {
       inv_role(sm, wait, chunks);
@@ -893,21 +980,50 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
       // every product that was issued ends before tensor memory is given back
       if (tc::elect()) tc::commit(&sm.ctl.fin);
       __syncwarp();
-      const long long t0 = clock64();
-      while (!mbar_try(&sm.ctl.fin, 0))
-        if (clock64() - t0 > kWaitClocks) {
-          flag_error(a.dev_err, CCONV_DERR_TIMEOUT);
-          break;
-        }
+      drain(&sm.ctl.fin, 0, a.dev_err);
     } else {
-      load_role(a, sm, wait, row0, len, h, chunks);
+      load_role(a, maps, sm, wait, row0, len, h, chunks);
     }
+  } else {
+    fewer_regs<kRegsOut>();
+    out_role(a, sm, wait, row0, len, h, chunks, tmem);
   }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   if (warp == kWarpMma)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+bool encode_rows(CUtensorMap* m, const char* p, int64_t cols, int64_t rows, int64_t stride) {
+  const EncodeTiledFn enc = encode_fn();
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+  const cuuint32_t box[2] = {64u, (cuuint32_t)kC};
+  const cuuint32_t step[2] = {1u, 1u};
+  return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<char*>(p), dims, strides,
+                    box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename ST>
@@ -917,7 +1033,12 @@ cudaError_t launch_chunk(const GdnArgs& a, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(
       gdn_chunk_kernel<ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  gdn_chunk_kernel<ST><<<(unsigned)(a.B * a.Hv), kThreadsC, smem, st>>>(a);
+  Maps maps;
+  if (!encode_rows(&maps.k, a.k, (int64_t)a.Hk * kD, a.T, a.k_rs) ||
+      !encode_rows(&maps.q, a.q, (int64_t)a.Hk * kD, a.T, a.q_rs) ||
+      !encode_rows(&maps.v, a.v, (int64_t)a.Hv * kD, a.T, a.v_rs))
+    return cudaErrorInvalidValue;
+  gdn_chunk_kernel<ST><<<(unsigned)(a.B * a.Hv), kThreadsC, smem, st>>>(a, maps);
   return cudaGetLastError();
 }
 
