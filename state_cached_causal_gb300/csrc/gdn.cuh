@@ -15,6 +15,7 @@ struct GdnArgs {
   char* st;
   int64_t st_slot, st_head;   // elements
   int32_t num_slots;
+  int32_t st_bytes;           // of a state element (chunked kernel)
   const int32_t* state_idx;
   const int32_t* cu;          // NULL: rows [s*q_len, s*q_len + q_len)
   const int32_t* num_acc;

@@ -76,6 +76,7 @@ constexpr uint32_t kVBytes = kC * kD * 2;    // V, later the chunk's outputs [64
 constexpr uint32_t kStageBytes = kKQBytes + kVBytes;
 constexpr uint32_t kTBytes = kC * kC * 2;    // one 64 x 64 bf16 operand
 constexpr uint32_t kTP = 3 * kTBytes;        // T hi, T lo, scores
+constexpr int kMaxSeqs = 640;                // sequences of a launch
 constexpr int kB = 16;                       // blocks of A and T
 constexpr int kBPitch = 20;                  // fp32 rows of 16: 80 bytes
 constexpr int kAPitch = 56;                  // bf16 rows of 48: 112 bytes
@@ -127,6 +128,8 @@ struct Smem {
   alignas(16) float rn[2 * kC];                // 1 / |k|, 1 / |q|
   Coef coef[2];
   Gate gate[2];
+  uint16_t order[kMaxSeqs];   // the launch's long sequences, longest first
+  int count, total;           // how many; chunks of this block's chains
   Ctl ctl;
 };
 static_assert(offsetof(Smem, tp) % 1024 == 0 && kStageBytes % 1024 == 0 && kTP % 1024 == 0 &&
@@ -203,6 +206,66 @@ __device__ __forceinline__ void drain(uint64_t* bar, int phase, int32_t* err) {
     }
 }
 
+// ---- which chains a block takes ----------------------------------------------
+
+// The chains of a launch, longest sequence first, a head after the other, are
+// dealt to the blocks back and forth, so that each gets some of every length.
+// Neighbouring heads, which share K and Q, run at the same time.
+struct Chain {
+  int row0, len, chunks, h, slot;
+  bool init;
+};
+__device__ __forceinline__ bool chain_at(const GdnArgs& a, const Smem& sm, int k, Chain& c) {
+  const uint32_t i = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  if (i >= (uint32_t)sm.count * a.Hv) return false;   // (less than 2^31: a host check)
+  const uint32_t r = i / (uint32_t)a.Hv;
+  const int s = sm.order[r];
+  c.h = (int)(i - r * a.Hv);
+  c.row0 = a.cu[s];
+  c.len = a.cu[s + 1] - c.row0;
+  c.chunks = (c.len + kC - 1) / kC;
+  c.slot = a.state_idx[s];
+  c.init = c.slot >= 0 && (!a.has_init || a.has_init[s]);
+  return true;
+}
+
+// Fills order, count and total. All threads; `lens` is scratch of kMaxSeqs.
+__device__ __forceinline__ void order_chains(const GdnArgs& a, Smem& sm, int* lens) {
+  const int s = threadIdx.x;
+  static_assert(kThreadsC >= kMaxSeqs, "a thread a sequence");
+  int len = 0;
+  if (s < a.B) {
+    int row0;
+    // (a bad cu_seqlens entry is reported by the recurrent kernel)
+    if (!gdn_bounds(a, s, row0, len) || len <= a.max_len) len = 0;
+    if (len > 0 && a.state_idx[s] >= a.num_slots) {
+      if (blockIdx.x == 0) flag_error(a.dev_err, CCONV_DERR_SLOT_RANGE);
+      len = 0;
+    }
+  }
+  if (s < kMaxSeqs) lens[s] = len;
+  const int count = __syncthreads_count(len > 0);
+  if (len > 0) {
+    int rank = 0;
+    for (int i = 0; i < a.B; ++i) {
+      const int o = lens[i];
+      rank += o > len || (o == len && i < s);
+    }
+    sm.order[rank] = (uint16_t)s;
+  }
+  if (s == 0) sm.count = count;
+  __syncthreads();
+  if (s < 32) {
+    int sum = 0;
+    Chain c;
+    for (int k = s; chain_at(a, sm, k, c); k += 32) sum += c.chunks;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (s == 0) sm.total = sum;
+  }
+  __syncthreads();
+}
+
 // ---- the warp that loads K, Q and V and works the gates out -----------------
 
 // Per chunk: requests its rows, works its gates out while they come. Whole
@@ -211,21 +274,30 @@ __device__ __forceinline__ void drain(uint64_t* bar, int phase, int32_t* err) {
 // kept as whole part and remainder in (-1, 0], exact to 2^-24 of the remainder
 // however long the sum.
 __device__ __forceinline__ void load_role(const GdnArgs& a, const Maps& maps, Smem& sm,
-                                          const Wait& wait, int row0, int len, int h,
-                                          int chunks) {
+                                          const Wait& wait) {
   const int lane = threadIdx.x & 31, u = lane & 15, r2 = lane >> 4;
+  const __nv_bfloat16* const ga0 = reinterpret_cast<const __nv_bfloat16*>(a.a);
+  const __nv_bfloat16* const gb0 = reinterpret_cast<const __nv_bfloat16*>(a.b);
+  int boxed = 0, g = 0;     // chunks requested as boxes; chunks of the block so far
+  Chain c;
+  for (int k = 0; chain_at(a, sm, k, c); ++k) {
+  const int row0 = c.row0, len = c.len, h = c.h;
   const int hk = h / (a.Hv / a.Hk);
   const char* kp = a.k + ((int64_t)row0 * a.k_rs + (int64_t)hk * kD) * 2 + u * 16;
   const char* qp = a.q + ((int64_t)row0 * a.q_rs + (int64_t)hk * kD) * 2 + u * 16;
   const char* vp = a.v + ((int64_t)row0 * a.v_rs + (int64_t)h * kD) * 2 + u * 16;
   const float A_log2 = -expf(a.A_log[h]) * 1.4426950408889634f;
   const float dtb = a.dt_bias[h];
-  const __nv_bfloat16* ga = reinterpret_cast<const __nv_bfloat16*>(a.a) + h;
-  const __nv_bfloat16* gb = reinterpret_cast<const __nv_bfloat16*>(a.b) + h;
-  int boxed = 0, n = 0;     // chunks requested as boxes; this chunk
-  for (; n < chunks; ++n) {
-    const int st = n % kStages;
-    if (n >= kStages && !wait(&sm.ctl.empty[st], n / kStages - 1)) break;
+  const __nv_bfloat16* ga = ga0 + h;
+  const __nv_bfloat16* gb = gb0 + h;
+  if (c.init) {             // the chain's state, for the warps that will read it
+    const char* sp = a.st + ((int64_t)c.slot * a.st_slot + (int64_t)h * a.st_head) * a.st_bytes;
+    for (int i = lane * 128; i < kD * kD * a.st_bytes; i += 32 * 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(sp + i));
+  }
+  for (int n = 0; n < c.chunks; ++n, ++g) {
+    const int st = g % kStages;
+    if (g >= kStages && !wait(&sm.ctl.empty[st], g / kStages - 1)) goto quit;
     const uint32_t base = smem_addr(sm.stage[st]) + (u >> 3) * kPanel;
     const uint32_t vbase = smem_addr(sm.stage[st]) + kKQBytes + (u >> 3) * kVPanel;
     float na[2], nb[2];
@@ -237,7 +309,7 @@ __device__ __forceinline__ void load_role(const GdnArgs& a, const Maps& maps, Sm
     }
     const bool whole = len - n * kC >= kC;
     if (whole) {
-      boxed = n + 1;
+      boxed = g + 1;
       if (lane == 0) {
         const uint32_t at = smem_addr(sm.stage[st]);
         const int y = row0 + n * kC;
@@ -252,7 +324,7 @@ __device__ __forceinline__ void load_role(const GdnArgs& a, const Maps& maps, Sm
         }
       }
     } else {
-#pragma unroll 4
+#pragma unroll 1
       for (int i = 0; i < kC / 2; ++i) {
         const int r = i * 2 + r2;
         const int64_t t = (int64_t)n * kC + r;
@@ -290,11 +362,11 @@ __device__ __forceinline__ void load_role(const GdnArgs& a, const Maps& maps, Sm
         if (lane >= d) add(w[i], f[i], ow, of);
       }
     add(w[1], f[1], __shfl_sync(0xffffffffu, w[0], 31), __shfl_sync(0xffffffffu, f[0], 31));
-    if (n >= 2 && !wait(&sm.ctl.gate_empty[n & 1], (n >> 1) - 1)) {
+    if (g >= 2 && !wait(&sm.ctl.gate_empty[g & 1], (g >> 1) - 1)) {
       warp_arrive(&sm.ctl.full[st]);
-      break;
+      goto quit;
     }
-    Gate& G = sm.gate[n & 1];
+    Gate& G = sm.gate[g & 1];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       G.hi[i * 32 + lane] = w[i];
@@ -308,11 +380,12 @@ __device__ __forceinline__ void load_role(const GdnArgs& a, const Maps& maps, Sm
     }
     warp_arrive(&sm.ctl.full[st]);
   }
-  if (n < chunks) {         // given up: no copy lands after the block ends
-    cp_async_wait<0>();
-    for (int i = max(boxed - kStages, 0); i < boxed; ++i)
-      drain(&sm.ctl.full[i % kStages], i / kStages, a.dev_err);
   }
+  return;
+quit:                       // given up: no copy lands after the block ends
+  cp_async_wait<0>();
+  for (int i = max(boxed - kStages, 0); i < boxed; ++i)
+    drain(&sm.ctl.full[i % kStages], i / kStages, a.dev_err);
 }
 
 // ---- the warps that look one chunk ahead ------------------------------------
@@ -325,46 +398,45 @@ __device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
   tc::split2(x[6], x[7], hi.w, lo.w);
 }
 
-// The 16 x 16 blocks of T below diagonal block J. With U = T^T, which is also
-// how T is stored for the tensor cores,
+// The 16 x 16 blocks of T below diagonal block J. With U = T^T, which is how T
+// is stored for the tensor cores,
 //   U_Ji = -(sum_{J <= k < i} U_Jk A_ik^T) U_ii,
-// so that each result is the left operand of the next product, where the
-// output layout of one warp product is the input layout of the next, and the
-// right operands come from shared memory as they lie there. Products of hi and
-// lo parts as everywhere (lo * lo left out), the mixed ones in a sum of their
-// own: shorter chains. Row j of the stored U is scaled by beta_j.
-template <int J>
-__device__ __forceinline__ void t_blocks(const Smem& sm, unsigned char* tp, const float* beta) {
+// and the same with every row j of the left factors scaled by beta_j, as the
+// stored U is: the stored blocks are the left operands, A and the diagonal
+// blocks the right ones, all as they lie in shared memory. The sum passes to
+// the second product in registers, where the output layout of one warp product
+// is the input layout of the next. Products of hi and lo parts as everywhere
+// (lo * lo left out), the mixed ones in a sum of their own: shorter chains.
+__device__ __forceinline__ void t_blocks(const Smem& sm, unsigned char* tp, int J) {
   const int lane = threadIdx.x & 31, r = lane >> 2, c = (lane & 3) * 2;
   const int lrow = lane & 15, lcol = (lane >> 4) * 8;    // ldmatrix: row and column of the lane
-  uint32_t uh[4][4], ul[4][4];                           // U_Jk as left operands
-  const float b0 = beta[J * kB + r], b1 = beta[J * kB + r + 8];
-  tc::ldmatrix4(uh[J], smem_addr(&sm.Uh[J * kB + lrow][lcol]));
-  tc::ldmatrix4(ul[J], smem_addr(&sm.Ul[J * kB + lrow][lcol]));
-#pragma unroll
+  const uint32_t u0 = smem_addr(tp) + (J * kB + lrow) * 128;
+#pragma unroll 1
   for (int i = J + 1; i < 4; ++i) {
     float x[2][4] = {}, xm[2][4] = {};
-#pragma unroll
+#pragma unroll 1
     for (int k = J; k < i; ++k) {
-      uint32_t h[4], l[4];      // n-tile nt: registers nt and nt + 2
+      uint32_t uh[4], ul[4], h[4], l[4];      // right operand of n-tile nt: registers nt, nt + 2
+      const uint32_t at = u0 + (((k * 2 + (lane >> 4)) ^ (lrow & 7)) << 4);
+      tc::ldmatrix4(uh, at);
+      tc::ldmatrix4(ul, at + kTBytes);
       tc::ldmatrix4(h, smem_addr(&sm.Ah[(i - 1) * kB + lrow][k * kB + lcol]));
       tc::ldmatrix4(l, smem_addr(&sm.Al[(i - 1) * kB + lrow][k * kB + lcol]));
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
-        tc::mma16(x[nt], uh[k], h[nt], h[nt + 2]);
-        tc::mma16(xm[nt], uh[k], l[nt], l[nt + 2]);
-        tc::mma16(xm[nt], ul[k], h[nt], h[nt + 2]);
+        tc::mma16(x[nt], uh, h[nt], h[nt + 2]);
+        tc::mma16(xm[nt], uh, l[nt], l[nt + 2]);
+        tc::mma16(xm[nt], ul, h[nt], h[nt + 2]);
       }
     }
-    uint32_t xh[4], xl[4];
+    uint32_t xh[4], xl[4], h[4], l[4];        // right operand of n-tile nt: 2 nt, 2 nt + 1
+    tc::ldmatrix4_trans(h, smem_addr(&sm.Uh[i * kB + lrow][lcol]));
+    tc::ldmatrix4_trans(l, smem_addr(&sm.Ul[i * kB + lrow][lcol]));
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       tc::split2(x[e >> 1][(e & 1) * 2] + xm[e >> 1][(e & 1) * 2],
                  x[e >> 1][(e & 1) * 2 + 1] + xm[e >> 1][(e & 1) * 2 + 1], xh[e], xl[e]);
     float y[2][4] = {}, ym[2][4] = {};
-    uint32_t h[4], l[4];        // n-tile nt: registers 2 nt and 2 nt + 1
-    tc::ldmatrix4_trans(h, smem_addr(&sm.Uh[i * kB + lrow][lcol]));
-    tc::ldmatrix4_trans(l, smem_addr(&sm.Ul[i * kB + lrow][lcol]));
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
       tc::mma16(y[nt], xh, h[2 * nt], h[2 * nt + 1]);
@@ -373,16 +445,14 @@ __device__ __forceinline__ void t_blocks(const Smem& sm, unsigned char* tp, cons
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {   // rows r, r + 8 (e & 1) of n-tile e >> 1
-      const float u0 = -(y[e >> 1][(e & 1) * 2] + ym[e >> 1][(e & 1) * 2]);
-      const float u1 = -(y[e >> 1][(e & 1) * 2 + 1] + ym[e >> 1][(e & 1) * 2 + 1]);
-      if (i < 3) tc::split2(u0, u1, uh[i][e], ul[i][e]);
-      const float be = (e & 1) ? b1 : b0;
       uint32_t sh, sl;
-      tc::split2(be * u0, be * u1, sh, sl);
+      tc::split2(-(y[e >> 1][(e & 1) * 2] + ym[e >> 1][(e & 1) * 2]),
+                 -(y[e >> 1][(e & 1) * 2 + 1] + ym[e >> 1][(e & 1) * 2 + 1]), sh, sl);
       const uint32_t at = sw128(J * kB + r + (e & 1) * 8, i * 2 + (e >> 1)) + c * 2;
       *reinterpret_cast<uint32_t*>(tp + at) = sh;
       *reinterpret_cast<uint32_t*>(tp + kTBytes + at) = sl;
     }
+    __syncwarp();
   }
 }
 
@@ -468,7 +538,7 @@ __device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait
       return;
     unsigned char* const scores = sm.tp[bf] + 2 * kTBytes;
     const uint32_t d1 = tmem + kColD1 + ((uint32_t)(warp * 32) << 16);
-#pragma unroll
+#pragma unroll 1
     for (int J = 0; J < 4; ++J) {
       uint32_t x[16];
       tc::ld16(d1 + J * 16, x);
@@ -565,12 +635,8 @@ __device__ __forceinline__ void inv_role(Smem& sm, const Wait& wait, int chunks)
       *reinterpret_cast<uint4*>(tp + kTBytes + sw128(b0 + c, blk * 2 + u)) = l;
     }
     if (!meet(wait)) return;
-    if (warp == 0) {
-      t_blocks<0>(sm, tp, G.beta);
-    } else {
-      t_blocks<1>(sm, tp, G.beta);
-      t_blocks<2>(sm, tp, G.beta);
-    }
+#pragma unroll 1
+    for (int J = warp; J < 1 + 2 * warp; ++J) t_blocks(sm, tp, J);   // 0, and 1 with 2
     fence_proxy_async();
     warp_arrive(&sm.ctl.t_full);
     warp_arrive(&sm.ctl.a_empty);
@@ -586,19 +652,13 @@ __device__ __forceinline__ void inv_role(Smem& sm, const Wait& wait, int chunks)
 // two halves of S pass through the update and the split one after the other,
 // while the tensor cores work on the other one.
 template <typename ST>
-__device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait& wait, int h,
-                                          int chunks, uint32_t tmem, bool init, int slot) {
+__device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait& wait,
+                                          uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int qd = warp & 3, hf = warp >> 2;
   const int col = qd * 32 + lane;
   const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
-  ST* const sp = reinterpret_cast<ST*>(a.st) + (int64_t)(slot < 0 ? 0 : slot) * a.st_slot +
-                 (int64_t)h * a.st_head + (int64_t)hf * 32 * kD + col;
   float S[64];
-#pragma unroll
-  for (int i = 0; i < 64; ++i)
-    S[i] = init ? elem(sp, ((i >> 5) * 64 + (i & 31)) * kD) : 0.0f;
-
   // S = e^{G_C} S + update of chunk n, one half
   auto advance = [&](int n, int part) -> bool {
     if (!wait(&sm.ctl.sd_full[part], n)) return false;
@@ -614,12 +674,20 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
     return true;
   };
 
-  for (int n = 0; n < chunks; ++n) {
+  int n = 0;                                      // chunks of the block so far
+  Chain ch;
+  for (int k = 0; chain_at(a, sm, k, ch); ++k) {
+  ST* const sp = reinterpret_cast<ST*>(a.st) + (int64_t)(ch.slot < 0 ? 0 : ch.slot) * a.st_slot +
+                 (int64_t)ch.h * a.st_head + (int64_t)hf * 32 * kD + col;
+#pragma unroll
+  for (int i = 0; i < 64; ++i)
+    S[i] = ch.init ? elem(sp, ((i >> 5) * 64 + (i & 31)) * kD) : 0.0f;
+  for (int m = 0; m < ch.chunks; ++m, ++n) {
     const Coef& C = sm.coef[n & 1];
     // ---- S: add the last chunk's update, split, hand to the tensor cores
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
-      if (n > 0 && !advance(n - 1, part)) return;
+      if (m > 0 && !advance(n - 1, part)) return;
       uint32_t hi[16], lo[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i)
@@ -630,7 +698,7 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
       tc::fence_before();
       warp_arrive(&sm.ctl.s_full[part]);
     }
-    if (n > 0) warp_arrive(&sm.ctl.coef_empty[(n - 1) & 1]);
+    if (m > 0) warp_arrive(&sm.ctl.coef_empty[(n - 1) & 1]);
     // ---- R
     if (!wait(&sm.ctl.coef_full[n & 1], n >> 1) || !wait(&sm.ctl.ks_full, n)) return;
     tc::fence_after();
@@ -691,30 +759,35 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
     tc::fence_before();
     warp_arrive(&sm.ctl.vd_full);
   }
-  if (!advance(chunks - 1, 0) || !advance(chunks - 1, 1)) return;
-  if (slot >= 0)
+  if (!advance(n - 1, 0) || !advance(n - 1, 1)) return;
+  warp_arrive(&sm.ctl.coef_empty[(n - 1) & 1]);
+  if (ch.slot >= 0)
 #pragma unroll
     for (int i = 0; i < 64; ++i) {
       const auto raw = f32_to_raw<ST>(S[i]);
       *reinterpret_cast<std::remove_const_t<decltype(raw)>*>(
           sp + ((i >> 5) * 64 + (i & 31)) * kD) = raw;
     }
+  }
 }
 
 // Outputs: a warp takes 32 columns, 16 tokens at a time, turns them round in
 // the chunk's V, which has been used, and stores 16-byte units.
-__device__ __forceinline__ void out_role(const GdnArgs& a, Smem& sm, const Wait& wait, int row0,
-                                         int len, int h, int chunks, uint32_t tmem) {
+__device__ __forceinline__ void out_role(const GdnArgs& a, Smem& sm, const Wait& wait,
+                                         uint32_t tmem) {
   const int qd = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
-  char* const op = a.out + ((int64_t)row0 * a.out_rs + (int64_t)h * kD + qd * 32) * 2 +
+  int n = 0;                                      // chunks of the block so far
+  Chain ch;
+  for (int k = 0; chain_at(a, sm, k, ch); ++k) {
+  char* const op = a.out + ((int64_t)ch.row0 * a.out_rs + (int64_t)ch.h * kD + qd * 32) * 2 +
                    (lane & 3) * 16;
-  for (int n = 0; n < chunks; ++n) {
+  for (int m = 0; m < ch.chunks; ++m, ++n) {
     if (!wait(&sm.ctl.o_full, n)) return;
     tc::fence_after();
     const Coef& C = sm.coef[n & 1];
     unsigned char* const box = sm.stage[n % kStages] + kKQBytes + qd * 4096;
-#pragma unroll
+#pragma unroll 1
     for (int g = 0; g < 4; ++g) {
       uint32_t x[16], y[16];
       tc::ld16(tl + kColQS + g * 16, x);
@@ -742,11 +815,12 @@ __device__ __forceinline__ void out_role(const GdnArgs& a, Smem& sm, const Wait&
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint4 q = *reinterpret_cast<const uint4*>(box + (i * 32 + lane) * 16);
-      const int64_t t = (int64_t)n * kC + i * 8 + (lane >> 2);
-      if (t < len) *reinterpret_cast<uint4*>(op + t * a.out_rs * 2) = q;
+      const int64_t t = (int64_t)m * kC + i * 8 + (lane >> 2);
+      if (t < ch.len) *reinterpret_cast<uint4*>(op + t * a.out_rs * 2) = q;
     }
     fence_proxy_async();
     warp_arrive(&sm.ctl.empty[n % kStages]);
+  }
   }
 }
 
@@ -758,139 +832,131 @@ __device__ __forceinline__ void out_role(const GdnArgs& a, Smem& sm, const Wait&
 __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks, uint32_t tmem) {
   constexpr uint32_t kId = tc::idesc(128, 64), kIdT = tc::idesc(128, 64, false, true),
                      kIdV = tc::idesc(128, 64, true, true);
-  const uint32_t stage0 = smem_addr(sm.stage[0]), tp0 = smem_addr(sm.tp[0]);
-  auto panel = [&](int st, int ks, int row) {   // 16 dk of rows [row, ..) of [K; Q]
-    return stage0 + st * kStageBytes + (ks >> 2) * kPanel + (ks & 3) * 32 + row * 128;
+  // descriptors of the first stage and T buffer; others lie a constant further
+  // (their addresses are counted in units of 16 bytes). K, Q, scores: K-major;
+  // K for the update: 64 dk of 16 tokens, MN-major, like V and U.
+  const uint64_t kq0 = tc::desc_sw128(smem_addr(sm.stage[0]), 16);
+  const uint64_t v0 = tc::desc_sw128(smem_addr(sm.stage[0]) + kKQBytes, kVPanel);
+  const uint64_t t0 = tc::desc_sw128(smem_addr(sm.tp[0]), 16);
+  auto panel = [](int ks, int row) {            // 16 dk of rows [row, ..) of [K; Q]
+    return ((ks >> 2) * kPanel + (ks & 3) * 32 + row * 128) >> 4;
   };
-  auto s_col = [&](int ks, int t) {             // 16 dk of S, hi or lo
-    return tmem + kColS + (ks >> 1) * 32 + t * 16 + (ks & 1) * 8;
-  };
+  // Steps of a chunk: S^T k of the first half of dk, of the second (with S^T q),
+  // T R, update. Before each, what runs beside the chain is issued if its
+  // operands are there: the scores of the next chunk that has none, and T V of
+  // this chunk.
   int scored = 0, tved = 0;                     // chunks whose products are issued
-  auto scores = [&]() {                         // [K; Q] K^T of chunk `scored`
-    tc::fence_after();
-    if (tc::elect()) {
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        const uint64_t d = tc::desc_sw128(panel(scored % kStages, ks, 0), 16);
-        tc::mma_ss(tmem + kColD1, d, d, kId, ks > 0);
+#pragma unroll 1
+  for (int step = 0; step < 4 * chunks; ++step) {
+    const int n = step >> 2, sub = step & 3, st = n % kStages;
+    const uint64_t kq = kq0 + ((st * kStageBytes) >> 4), tp = t0 + (((n & 1) * kTP) >> 4);
+    const bool must = sub == 2 && tved == n;    // T R needs T V before it
+#pragma unroll 1
+    do {
+      uint64_t* const full = &sm.ctl.full[scored % kStages];
+      if (scored < chunks && (must && scored <= n)) {
+        if (!wait(full, scored / kStages) || (scored > 0 && !wait(&sm.ctl.d1_empty, scored - 1)))
+          return;
       }
-      tc::commit(&sm.ctl.d1_full);
-    }
-    __syncwarp();
-    ++scored;
-  };
-  auto scores_if_ready = [&]() {
-    if (scored < chunks &&
-        __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.full[scored % kStages],
-                                               (scored / kStages) & 1)) &&
-        (scored == 0 ||
-         __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.d1_empty, (scored - 1) & 1))))
-      scores();
-  };
-  auto tv = [&]() {                             // (T V)^T of chunk `tved`: V read along dv
-    tc::fence_after();
-    const uint32_t tp = tp0 + (tved & 1) * kTP,
-                   v = stage0 + (tved % kStages) * kStageBytes + kKQBytes;
-    if (tc::elect()) {
+      if (scored < chunks &&
+          __any_sync(0xffffffffu, tc::mbar_ready(full, (scored / kStages) & 1)) &&
+          (scored == 0 ||
+           __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.d1_empty, (scored - 1) & 1)))) {
+        tc::fence_after();
+        const uint64_t d = kq0 + (((scored % kStages) * kStageBytes) >> 4);
+        if (tc::elect()) {                      // [K; Q] K^T
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+          for (int ks = 0; ks < 8; ++ks)
+            tc::mma_ss(tmem + kColD1, d + panel(ks, 0), d + panel(ks, 0), kId, ks > 0);
+          tc::commit(&sm.ctl.d1_full);
+        }
+        __syncwarp();
+        ++scored;
+      }
+      // (chunk n - 1's N has been read: its update, which needed it, is issued)
+      if (must && scored > n && !wait(&sm.ctl.t_full, n)) return;
+      if (tved == n && scored > n &&
+          __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.t_full, tved & 1))) {
+        tc::fence_after();
+        const uint64_t v = v0 + ((st * kStageBytes) >> 4);
+        if (tc::elect()) {                      // (T V)^T, V read along dv
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          tc::mma_ss(tmem + kColVN, tc::desc_sw128(v + ks * 2048, kVPanel),
-                     tc::desc_sw128(tp + t * kTBytes + ks * 2048, kTBytes), kIdV, (t | ks) > 0);
-    }
-    __syncwarp();
-    ++tved;
-  };
-  for (int n = 0; n < chunks; ++n) {
-    const int st = n % kStages, bf = n & 1;
-    const uint32_t tp = tp0 + bf * kTP;
-    if (n == 0) {
-      if (!wait(&sm.ctl.full[0], 0)) return;
-      scores();
-    }
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      if (!wait(&sm.ctl.s_full[part], n)) return;
+            for (int ks = 0; ks < 4; ++ks)
+              tc::mma_ss(tmem + kColVN, v + ((ks * 2048) >> 4),
+                         tp + ((t * kTBytes + ks * 2048) >> 4), kIdV, (t | ks) > 0);
+        }
+        __syncwarp();
+        ++tved;
+      }
+    } while (must && tved == n);
+    if (sub < 2) {
+      if (!wait(&sm.ctl.full[st], n / kStages) || !wait(&sm.ctl.s_full[sub], n)) return;
       // N of the last chunk lies where S^T k goes
-      if (part == 0 && n > 0 && !wait(&sm.ctl.o_full, n - 1)) return;
+      if (sub == 0 && n > 0 && !wait(&sm.ctl.o_full, n - 1)) return;
       tc::fence_after();
+      const uint32_t s0 = tmem + kColS + sub * 64;
+      const uint64_t kp = kq + ((sub * kPanel) >> 4);
       if (tc::elect()) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)             // S hi, S lo
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4)
-            tc::mma_ts(tmem + kColKS, s_col(part * 4 + k4, t),
-                       tc::desc_sw128(panel(st, part * 4 + k4, 0), 16), kId,
-                       (part | t | k4) > 0);
-        if (part == 1) tc::commit(&sm.ctl.ks_full);
+            tc::mma_ts(tmem + kColKS, s0 + t * 16 + (k4 >> 1) * 32 + (k4 & 1) * 8,
+                       kp + panel(k4, 0), kId, (sub | t | k4) > 0);
+        if (sub == 1) tc::commit(&sm.ctl.ks_full);
+      }
+      __syncwarp();
+      if (sub == 1) {
+        if (n > 0 && !wait(&sm.ctl.o_empty, n - 1)) return;
+        tc::fence_after();
+        if (tc::elect()) {
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            tc::mma_ts(tmem + kColQS, tmem + kColS + (ks >> 1) * 32 + (ks & 1) * 8,
+                       kq + panel(ks, kC), kId, ks > 0);
+          tc::commit(&sm.ctl.qs_done);
+        }
+        __syncwarp();
+      }
+    } else if (sub == 2) {
+      if (!wait(&sm.ctl.r_full, n)) return;
+      tc::fence_after();
+      if (tc::elect()) {
+#pragma unroll
+        for (int t = 0; t < 3; ++t)             // R hi T hi, R lo T hi, R hi T lo
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            tc::mma_ts(tmem + kColVN, tmem + kColR + (t == 1 ? 32 : 0) + ks * 8,
+                       tp + (((t == 2 ? kTBytes : 0) + ks * 2048) >> 4), kIdT, true);
+        tc::commit(&sm.ctl.vn_full);
+      }
+      __syncwarp();
+    } else {
+      if (!wait(&sm.ctl.vd_full, n) || !wait(&sm.ctl.qs_done, n)) return;
+      tc::fence_after();
+      if (tc::elect()) {
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {  // K read along dk, 64 at a time
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              tc::mma_ts(tmem + kColS + part * 64, tmem + kColR + t * 32 + ks * 8,
+                         kq + ((part * kPanel + ks * 2048) >> 4), kIdT, (t | ks) > 0);
+          tc::commit(&sm.ctl.sd_full[part]);
+        }
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          tc::mma_ts(tmem + kColO, tmem + kColN + ks * 8,
+                     tp + ((2 * kTBytes + ks * 32) >> 4), kId, ks > 0);
+        tc::commit(&sm.ctl.o_full);
+        tc::commit(&sm.ctl.empty[st]);
+        tc::commit(&sm.ctl.tp_empty[n & 1]);
       }
       __syncwarp();
     }
-    if (n > 0 && !wait(&sm.ctl.o_empty, n - 1)) return;
-    tc::fence_after();
-    if (tc::elect()) {
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
-        tc::mma_ts(tmem + kColQS, s_col(ks, 0), tc::desc_sw128(panel(st, ks, kC), 16), kId,
-                   ks > 0);
-      tc::commit(&sm.ctl.qs_done);
-    }
-    __syncwarp();
-    if (tved == n) {
-      while (scored <= n) {
-        if (!wait(&sm.ctl.full[scored % kStages], scored / kStages) ||
-            (scored > 0 && !wait(&sm.ctl.d1_empty, scored - 1)))
-          return;
-        scores();
-      }
-      if (!wait(&sm.ctl.t_full, n)) return;
-      tv();
-    }
-    scores_if_ready();
-    if (!wait(&sm.ctl.r_full, n)) return;
-    tc::fence_after();
-    if (tc::elect()) {
-#pragma unroll
-      for (int t = 0; t < 3; ++t)               // R hi T hi, R lo T hi, R hi T lo
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          tc::mma_ts(tmem + kColVN, tmem + kColR + (t == 1 ? 32 : 0) + ks * 8,
-                     tc::desc_sw128(tp + (t == 2 ? kTBytes : 0) + ks * 2048, kTBytes), kIdT,
-                     true);
-      tc::commit(&sm.ctl.vn_full);
-    }
-    __syncwarp();
-    scores_if_ready();
-    if (!wait(&sm.ctl.vd_full, n) || !wait(&sm.ctl.qs_done, n)) return;
-    tc::fence_after();
-    if (tc::elect()) {
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {    // K read along dk, 64 at a time
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            tc::mma_ts(tmem + kColS + part * 64, tmem + kColR + t * 32 + ks * 8,
-                       tc::desc_sw128(stage0 + st * kStageBytes + part * kPanel + ks * 2048,
-                                      kPanel),
-                       kIdT, (t | ks) > 0);
-        tc::commit(&sm.ctl.sd_full[part]);
-      }
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        tc::mma_ts(tmem + kColO, tmem + kColN + ks * 8,
-                   tc::desc_sw128(tp + 2 * kTBytes + ks * 32, 16), kId, ks > 0);
-      tc::commit(&sm.ctl.o_full);
-      tc::commit(&sm.ctl.empty[st]);
-      tc::commit(&sm.ctl.tp_empty[bf]);
-    }
-    __syncwarp();
-    // T of the next chunk, if it is there already: its product with V runs
-    // while S is worked on
-    scores_if_ready();
-    if (n + 1 < chunks && __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.t_full, (n + 1) & 1)))
-      tv();
   }
 }
 
@@ -900,17 +966,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
   Smem& sm = *reinterpret_cast<Smem*>(
       gdn_dyn + ((1024u - (smem_addr(gdn_dyn) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5;
-  const int h = blockIdx.x % a.Hv, s = blockIdx.x / a.Hv;
-  // (a bad cu_seqlens entry is reported by the recurrent kernel)
-  int row0, len;
-  if (!gdn_bounds(a, s, row0, len) || len <= a.max_len) return;
-  const int slot = a.state_idx[s];
-  if (slot >= a.num_slots) {
-    if (h == 0 && tid == 0) flag_error(a.dev_err, CCONV_DERR_SLOT_RANGE);
-    return;
-  }
-  const bool init = slot >= 0 && (!a.has_init || a.has_init[s]);
-  const int chunks = (len + kC - 1) / kC;
+  order_chains(a, sm, reinterpret_cast<int*>(sm.stage[0]));
+  const int chunks = sm.total;
+  if (chunks == 0) return;
 
   if (tid == 0) {
     Ctl& c = sm.ctl;
@@ -967,7 +1025,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
 
   if (warp < kScanWarps) {
     more_regs<kRegsScan>();
-    scan_role<ST>(a, sm, wait, h, chunks, tmem, init, slot);
+    scan_role<ST>(a, sm, wait, tmem);
   } else if (warp < kWarpInv0) {
     fewer_regs<kRegsPrep>();
     prep_role(a, sm, wait, chunks, tmem);
@@ -982,11 +1040,11 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
       __syncwarp();
       drain(&sm.ctl.fin, 0, a.dev_err);
     } else {
-      load_role(a, maps, sm, wait, row0, len, h, chunks);
+      load_role(a, maps, sm, wait);
     }
   } else {
     fewer_regs<kRegsOut>();
-    out_role(a, sm, wait, row0, len, h, chunks, tmem);
+    out_role(a, sm, wait, tmem);
   }
   tc::fence_before();
   __syncthreads();
@@ -1038,8 +1096,21 @@ cudaError_t launch_chunk(const GdnArgs& a, cudaStream_t st) {
       !encode_rows(&maps.q, a.q, (int64_t)a.Hk * kD, a.T, a.q_rs) ||
       !encode_rows(&maps.v, a.v, (int64_t)a.Hv * kD, a.T, a.v_rs))
     return cudaErrorInvalidValue;
-  gdn_chunk_kernel<ST><<<(unsigned)(a.B * a.Hv), kThreadsC, smem, st>>>(a, maps);
-  return cudaGetLastError();
+  const int sms = mix_sm_count();
+  if (sms <= 0) return cudaErrorInvalidValue;
+  GdnArgs b = a;
+  b.st_bytes = sizeof(ST);
+  for (int s = 0; s < a.B; s += kMaxSeqs) {     // a launch orders at most kMaxSeqs sequences
+    b.B = std::min(kMaxSeqs, a.B - s);
+    b.state_idx = a.state_idx + s;
+    b.cu = a.cu + s;
+    b.has_init = a.has_init ? a.has_init + s : nullptr;
+    const int grid = (int)std::min<int64_t>(sms, (int64_t)b.B * a.Hv);
+    gdn_chunk_kernel<ST><<<grid, kThreadsC, smem, st>>>(b, maps);
+    const cudaError_t le = cudaGetLastError();
+    if (le != cudaSuccess) return le;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
