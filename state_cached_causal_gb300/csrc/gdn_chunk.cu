@@ -965,9 +965,12 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
   extern __shared__ __align__(1024) unsigned char gdn_dyn[];
   Smem& sm = *reinterpret_cast<Smem*>(
       gdn_dyn + ((1024u - (smem_addr(gdn_dyn) & 1023u)) & 1023u));
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x;
+  // (read from one lane: values that the compiler then knows to be the same in
+  // the whole warp, and keeps in uniform registers, where tcgen05.mma wants them)
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   order_chains(a, sm, reinterpret_cast<int*>(sm.stage[0]));
-  const int chunks = sm.total;
+  const int chunks = __shfl_sync(0xffffffffu, sm.total, 0);
   if (chunks == 0) return;
 
   if (tid == 0) {
@@ -1020,7 +1023,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
   }
   __syncthreads();
   tc::fence_after();
-  const uint32_t tmem = sm.ctl.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.ctl.tmem, 0);
   const Wait wait{&sm.ctl, a.dev_err};
 
   if (warp < kScanWarps) {
