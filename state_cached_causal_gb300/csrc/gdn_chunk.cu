@@ -57,16 +57,16 @@ namespace {
 constexpr int kC = 64;                       // tokens of a chunk
 constexpr int kD = 128;                      // dk = dv
 constexpr int kStages = 3;
-// Warpgroups: two on the chain, one for A and the scores, one of two warps for
+// Warpgroups: four on the chain, one for A and the scores, one of two warps for
 // T, one that issues the tensor products and one that loads, and one for the
-// outputs; registers a thread of each (their sum is the block's 640 x 96).
-constexpr int kScanWarps = 8, kPrepWarps = 4, kInvWarps = 2, kOutWarps = 4;
+// outputs; registers a thread of each (their sum is the block's 896 x 72).
+constexpr int kScanWarps = 16, kPrepWarps = 4, kInvWarps = 2, kOutWarps = 4;
 constexpr int kWarpPrep0 = kScanWarps, kWarpInv0 = kWarpPrep0 + kPrepWarps,
               kWarpMma = kWarpInv0 + kInvWarps, kWarpLoad = kWarpMma + 1,
               kWarpOut0 = kWarpLoad + 1;
 constexpr int kThreadsC = (kWarpOut0 + kOutWarps) * 32;
-constexpr int kRegsScan = 136, kRegsPrep = 88, kRegsRest = 72, kRegsOut = 48;
-static_assert(kThreadsC == 640 && 2 * kRegsScan + kRegsPrep + kRegsRest + kRegsOut <= 5 * 96,
+constexpr int kRegsScan = 72, kRegsPrep = 88, kRegsRest = 72, kRegsOut = 56;
+static_assert(kThreadsC == 896 && 4 * kRegsScan + kRegsPrep + kRegsRest + kRegsOut <= 7 * 72,
               "a split over the block's own registers would wait forever");
 
 constexpr uint32_t kPanel = 128 * 128;       // 64 dk of [K; Q]: 128 rows x 128 bytes
@@ -80,7 +80,7 @@ constexpr int kMaxSeqs = 640;                // sequences of a launch
 constexpr int kB = 16;                       // blocks of A and T
 constexpr int kBPitch = 20;                  // fp32 rows of 16: 80 bytes
 constexpr int kAPitch = 56;                  // bf16 rows of 48: 112 bytes
-constexpr int kUPitch = 24;                  // bf16 rows of 16: 48 bytes
+constexpr int kOut = 4;                      // chunks whose output factors are kept
 
 constexpr uint32_t kColS = 0, kColKS = 128, kColN = kColKS, kColQS = 192, kColR = 256,
                    kColVN = 320, kColO = 384, kColD1 = 448;
@@ -92,8 +92,6 @@ constexpr long long kWaitClocks = 4000000000LL;
 struct alignas(16) Coef {
   float rc[kC];      // -e^G / |k|
   float vd[kC];      // e^{G_C - G} / |k|
-  float o1[kC];      // scale e^G / |q|
-  float o2[kC];      // scale / |q|
   float ec;          // e^{G_C}
 };
 // Gates of a chunk: sum of log2 decays (whole part, remainder) and beta.
@@ -107,7 +105,7 @@ struct Maps {
 
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
-  uint64_t gate_empty[2], tp_empty[2], coef_full[2], coef_empty[2];
+  uint64_t gate_empty[2], tp_empty[2], coef_full[2], coef_empty[2], o1_empty[kOut];
   uint64_t d1_full, d1_empty, a_full, a_empty, t_full, prep_meet, inv_meet;
   uint64_t s_full[2], sd_full[2];
   uint64_t ks_full, qs_done, r_full, vn_full, vd_full, o_full, o_empty, fin;
@@ -121,11 +119,10 @@ struct Smem {
   alignas(16) float Ad[kC][kBPitch];           // A: diagonal blocks
   alignas(16) uint16_t Ah[kC - kB][kAPitch];   // and rows 16 .. of the blocks left of them,
   alignas(16) uint16_t Al[kC - kB][kAPitch];   // bf16 hi and lo
-  alignas(16) uint16_t Uh[kC][kUPitch];        // transposed inverses of the diagonal blocks
-  alignas(16) uint16_t Ul[kC][kUPitch];
   alignas(16) float ed[kC][kBPitch];           // e^{G_i - G_j} / |k_j|, j in the block of i
   alignas(16) float tab[4][kC];                // e^{G_(16I-1) - G_j} / |k_j|, j < 16 I
   alignas(16) float rn[2 * kC];                // 1 / |k|, 1 / |q|
+  alignas(16) float o1[kOut][kC];              // scale e^G / |q|
   Coef coef[2];
   Gate gate[2];
   uint16_t order[kMaxSeqs];   // the launch's long sequences, longest first
@@ -137,7 +134,7 @@ static_assert(offsetof(Smem, tp) % 1024 == 0 && kStageBytes % 1024 == 0 && kTP %
               "swizzled tiles start on 1024 bytes");
 static_assert(sizeof(Coef) % 16 == 0 && sizeof(Gate) % 16 == 0 && offsetof(Smem, Ad) % 16 == 0 &&
                   offsetof(Smem, Ah) % 16 == 0 && offsetof(Smem, Al) % 16 == 0 &&
-                  offsetof(Smem, Uh) % 16 == 0 && offsetof(Smem, Ul) % 16 == 0 && offsetof(Smem, ed) % 16 == 0 &&
+                  offsetof(Smem, o1) % 16 == 0 && offsetof(Smem, ed) % 16 == 0 &&
                   offsetof(Smem, tab) % 16 == 0 && offsetof(Smem, rn) % 16 == 0 &&
                   offsetof(Smem, coef) % 16 == 0 && offsetof(Smem, gate) % 16 == 0 &&
                   offsetof(Smem, ctl) % 8 == 0,
@@ -400,13 +397,11 @@ __device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
 
 // The 16 x 16 blocks of T below diagonal block J. With U = T^T, which is how T
 // is stored for the tensor cores,
-//   U_Ji = -(sum_{J <= k < i} U_Jk A_ik^T) U_ii,
-// and the same with every row j of the left factors scaled by beta_j, as the
-// stored U is: the stored blocks are the left operands, A and the diagonal
-// blocks the right ones, all as they lie in shared memory. The sum passes to
-// the second product in registers, where the output layout of one warp product
-// is the input layout of the next. Products of hi and lo parts as everywhere
-// (lo * lo left out), the mixed ones in a sum of their own: shorter chains.
+//   U_Ji = -(sum_{J <= k < i} U_Jk A_ik^T) U_ii:
+// both factors and A as they lie in shared memory. The sum passes to the second
+// product in registers, where the output layout of one warp product is the
+// input layout of the next. Products of hi and lo parts as everywhere (lo * lo
+// left out), the mixed ones in a sum of their own: shorter chains.
 __device__ __forceinline__ void t_blocks(const Smem& sm, unsigned char* tp, int J) {
   const int lane = threadIdx.x & 31, r = lane >> 2, c = (lane & 3) * 2;
   const int lrow = lane & 15, lcol = (lane >> 4) * 8;    // ldmatrix: row and column of the lane
@@ -430,8 +425,9 @@ __device__ __forceinline__ void t_blocks(const Smem& sm, unsigned char* tp, int 
       }
     }
     uint32_t xh[4], xl[4], h[4], l[4];        // right operand of n-tile nt: 2 nt, 2 nt + 1
-    tc::ldmatrix4_trans(h, smem_addr(&sm.Uh[i * kB + lrow][lcol]));
-    tc::ldmatrix4_trans(l, smem_addr(&sm.Ul[i * kB + lrow][lcol]));
+    const uint32_t ui = smem_addr(tp) + sw128(i * kB + lrow, i * 2 + (lane >> 4));
+    tc::ldmatrix4_trans(h, ui);
+    tc::ldmatrix4_trans(l, ui + kTBytes);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       tc::split2(x[e >> 1][(e & 1) * 2] + xm[e >> 1][(e & 1) * 2],
@@ -490,8 +486,9 @@ __device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait
       rn = 1.0f / sqrtf((s0 + s1) + (s2 + s3) + kGdnNormEps);
     }
     sm.rn[p] = rn;
-    // the factors of two chunks ago have been read
+    // the factors of two (four) chunks ago have been read
     if (n >= 2 && !wait(&sm.ctl.coef_empty[bf], (n >> 1) - 1)) return;
+    if (n >= kOut && !wait(&sm.ctl.o1_empty[n % kOut], n / kOut - 1)) return;
     if (!meet(wait)) return;
     // ---- factors
     const float hi = G.hi[r], lo = G.lo[r];
@@ -501,8 +498,7 @@ __device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait
       C.vd[r] = rn * tc::ex2((G.hi[kC - 1] - hi) + (G.lo[kC - 1] - lo));
       if (r == kC - 1) C.ec = eg;
     } else {
-      C.o1[r] = a.scale * rn * eg;
-      C.o2[r] = a.scale * rn;
+      sm.o1[n % kOut][r] = a.scale * rn * eg;
     }
     {
       const float rk = sm.rn[r];
@@ -524,7 +520,7 @@ __device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait
                         j + 3 <= r ? k4.w * tc::ex2((hi - h4.w) + (lo - l4.w)) : 0.0f);
       }
     }
-    const float fac = is_k ? G.beta[r] * rn : 1.0f;
+    const float fac = is_k ? rn : a.scale * rn;
     const float off =
         blk > 0 ? fac * tc::ex2((hi - G.hi[blk * kB - 1]) + (lo - G.lo[blk * kB - 1])) : 0.0f;
     warp_arrive(&sm.ctl.coef_full[bf]);
@@ -596,7 +592,9 @@ __device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait
 
 // T of every chunk, by two warps: forward substitution of the four diagonal
 // blocks (a lane a column, two blocks a warp), then the blocks below them, nine
-// block products by the first warp and seven by the second.
+// block products by the first warp and seven by the second. What is built is T
+// with its columns scaled by beta, (diag(1 / beta) + A)^-1 for the A without
+// beta that the scores' warps wrote: rows t_i = beta_i (e_i - sum_k A_ik t_k).
 __device__ __forceinline__ void inv_role(Smem& sm, const Wait& wait, int chunks) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kWarpInv0;
   const int blk = warp * 2 + (lane >> 4), c = lane & (kB - 1), b0 = blk * kB;
@@ -619,17 +617,11 @@ __device__ __forceinline__ void inv_role(Smem& sm, const Wait& wait, int chunks)
         if (k4 + 2 < i) acc[2] = fmaf(-v.z, t[k4 + 2], acc[2]);
         if (k4 + 3 < i) acc[3] = fmaf(-v.w, t[k4 + 3], acc[3]);
       }
-      t[i] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      t[i] = G.beta[b0 + i] * ((acc[0] + acc[1]) + (acc[2] + acc[3]));
     }
-    const float be = G.beta[b0 + c];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       uint4 h, l;
-      split8(t + u * 8, h, l);
-      *reinterpret_cast<uint4*>(&sm.Uh[b0 + c][u * 8]) = h;
-      *reinterpret_cast<uint4*>(&sm.Ul[b0 + c][u * 8]) = l;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[u * 8 + i] *= be;
       split8(t + u * 8, h, l);
       *reinterpret_cast<uint4*>(tp + sw128(b0 + c, blk * 2 + u)) = h;
       *reinterpret_cast<uint4*>(tp + kTBytes + sw128(b0 + c, blk * 2 + u)) = l;
@@ -647,127 +639,112 @@ __device__ __forceinline__ void inv_role(Smem& sm, const Wait& wait, int chunks)
 
 // ---- the warps on the chain -------------------------------------------------
 
-// Thread: column `col` of S, dk (i / 32) * 64 + hf * 32 + i % 32 in S[i]: the
-// first 32 lie in the first half of dk for both warps of a column, so that the
-// two halves of S pass through the update and the split one after the other,
-// while the tensor cores work on the other one.
+// Thread: column `col` of S, dk p * 64 + qt * 16 + [0, 16) in S[p * 16 ..], p =
+// 0, 1: the two halves of dk pass through the update and the split one after
+// the other, while the tensor cores work on the other one. Of a chunk's tokens
+// the thread has qt * 16 + [0, 16). (Four warps a quadrant of lanes: what a warp
+// does between two products is short then; with two, the chain was a third
+// longer.)
 template <typename ST>
 __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait& wait,
                                           uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int qd = warp & 3, hf = warp >> 2;
+  const int qd = warp & 3, qt = warp >> 2;
   const int col = qd * 32 + lane;
   const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
-  float S[64];
+  const uint32_t ts = tl + kColS + qt * 16;
+  float S[32];
+
   // S = e^{G_C} S + update of chunk n, one half
-  auto advance = [&](int n, int part) -> bool {
-    if (!wait(&sm.ctl.sd_full[part], n)) return false;
+  auto advance = [&](int n, int p) -> bool {
+    if (!wait(&sm.ctl.sd_full[p], n)) return false;
     tc::fence_after();
-    uint32_t x[32];
-    tc::ld32(tl + kColS + part * 64 + hf * 32, x);
+    uint32_t x[16];
+    tc::ld16(ts + p * 64, x);
     const float ec = sm.coef[n & 1].ec;
     tc::wait_ld(x);
 #pragma unroll
-    for (int i = 0; i < 32; i += 2)
-      fma_x2(S[part * 32 + i], S[part * 32 + i + 1], ec, ec, S[part * 32 + i],
-             S[part * 32 + i + 1], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+    for (int i = 0; i < 16; i += 2)
+      fma_x2(S[p * 16 + i], S[p * 16 + i + 1], ec, ec, S[p * 16 + i], S[p * 16 + i + 1],
+             __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
     return true;
+  };
+  // the thread's 16 tokens times their factors, split, to kColR
+  auto scaled = [&](const uint32_t(&x)[16], const float* f) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const float4 c = *reinterpret_cast<const float4*>(f + qt * 16 + i);
+      float q[4];
+      mul_x2(q[0], q[1], c.x, c.y, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+      mul_x2(q[2], q[3], c.z, c.w, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+      tc::split2(q[0], q[1], hi[i / 2], lo[i / 2]);
+      tc::split2(q[2], q[3], hi[i / 2 + 1], lo[i / 2 + 1]);
+    }
+    tc::st8(tl + kColR + qt * 8, hi);
+    tc::st8(tl + kColR + 32 + qt * 8, lo);
   };
 
   int n = 0;                                      // chunks of the block so far
   Chain ch;
   for (int k = 0; chain_at(a, sm, k, ch); ++k) {
-  ST* const sp = reinterpret_cast<ST*>(a.st) + (int64_t)(ch.slot < 0 ? 0 : ch.slot) * a.st_slot +
-                 (int64_t)ch.h * a.st_head + (int64_t)hf * 32 * kD + col;
+    ST* const sp = reinterpret_cast<ST*>(a.st) +
+                   (int64_t)(ch.slot < 0 ? 0 : ch.slot) * a.st_slot + (int64_t)ch.h * a.st_head +
+                   (int64_t)qt * 16 * kD + col;
 #pragma unroll
-  for (int i = 0; i < 64; ++i)
-    S[i] = ch.init ? elem(sp, ((i >> 5) * 64 + (i & 31)) * kD) : 0.0f;
-  for (int m = 0; m < ch.chunks; ++m, ++n) {
-    const Coef& C = sm.coef[n & 1];
-    // ---- S: add the last chunk's update, split, hand to the tensor cores
+    for (int i = 0; i < 32; ++i)
+      S[i] = ch.init ? elem(sp, ((i >> 4) * 64 + (i & 15)) * kD) : 0.0f;
+    for (int m = 0; m < ch.chunks; ++m, ++n) {
+      const Coef& C = sm.coef[n & 1];
+      // ---- S: add the last chunk's update, split, hand to the tensor cores
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      if (m > 0 && !advance(n - 1, part)) return;
-      uint32_t hi[16], lo[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        tc::split2(S[part * 32 + 2 * i], S[part * 32 + 2 * i + 1], hi[i], lo[i]);
-      tc::st16(tl + kColS + part * 64 + hf * 32, hi);
-      tc::st16(tl + kColS + part * 64 + hf * 32 + 16, lo);
-      tc::wait_st();
-      tc::fence_before();
-      warp_arrive(&sm.ctl.s_full[part]);
-    }
-    if (m > 0) warp_arrive(&sm.ctl.coef_empty[(n - 1) & 1]);
-    // ---- R
-    if (!wait(&sm.ctl.coef_full[n & 1], n >> 1) || !wait(&sm.ctl.ks_full, n)) return;
-    tc::fence_after();
-    {
-      uint32_t x[32];
-      tc::ld32(tl + kColKS + hf * 32, x);
-      tc::wait_ld(x);
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
+      for (int p = 0; p < 2; ++p) {
+        if (m > 0 && !advance(n - 1, p)) return;
         uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const int t = g * 16 + i * 2;
-          const float4 c4 = *reinterpret_cast<const float4*>(&C.rc[hf * 32 + t]);
-          float q[4];
-          mul_x2(q[0], q[1], c4.x, c4.y, __uint_as_float(x[t]), __uint_as_float(x[t + 1]));
-          mul_x2(q[2], q[3], c4.z, c4.w, __uint_as_float(x[t + 2]), __uint_as_float(x[t + 3]));
-          tc::split2(q[0], q[1], hi[i], lo[i]);
-          tc::split2(q[2], q[3], hi[i + 1], lo[i + 1]);
-        }
-        tc::st8(tl + kColR + hf * 16 + g * 8, hi);
-        tc::st8(tl + kColR + 32 + hf * 16 + g * 8, lo);
+        for (int i = 0; i < 8; ++i)
+          tc::split2(S[p * 16 + 2 * i], S[p * 16 + 2 * i + 1], hi[i], lo[i]);
+        tc::st8(ts + p * 64, hi);
+        tc::st8(ts + p * 64 + 8, lo);
+        tc::wait_st();
+        tc::fence_before();
+        warp_arrive(&sm.ctl.s_full[p]);
       }
-    }
-    tc::wait_st();
-    tc::fence_before();
-    warp_arrive(&sm.ctl.r_full);
-    // ---- N
-    if (!wait(&sm.ctl.vn_full, n)) return;
-    tc::fence_after();
-    {
-      uint32_t x[32];
-      tc::ld32(tl + kColVN + hf * 32, x);
+      if (m > 0) warp_arrive(&sm.ctl.coef_empty[(n - 1) & 1]);
+      // ---- R
+      if (!wait(&sm.ctl.coef_full[n & 1], n >> 1) || !wait(&sm.ctl.ks_full, n)) return;
+      tc::fence_after();
+      uint32_t x[16];
+      tc::ld16(tl + kColKS + qt * 16, x);
       tc::wait_ld(x);
+      scaled(x, C.rc);
+      tc::wait_st();
+      tc::fence_before();
+      warp_arrive(&sm.ctl.r_full);
+      // ---- N
+      if (!wait(&sm.ctl.vn_full, n)) return;
+      tc::fence_after();
+      tc::ld16(tl + kColVN + qt * 16, x);
+      tc::wait_ld(x);
+      scaled(x, C.vd);
+      uint32_t on[8];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint32_t hi[8], lo[8], on[8];
+      for (int i = 0; i < 8; ++i)
+        on[i] = pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+      tc::st8(tl + kColN + qt * 8, on);
+      tc::wait_st();
+      tc::fence_before();
+      warp_arrive(&sm.ctl.vd_full);
+    }
+    if (!advance(n - 1, 0) || !advance(n - 1, 1)) return;
+    warp_arrive(&sm.ctl.coef_empty[(n - 1) & 1]);
+    if (ch.slot >= 0)
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const int t = g * 16 + i * 2;
-          const float4 d4 = *reinterpret_cast<const float4*>(&C.vd[hf * 32 + t]);
-          const float v0 = __uint_as_float(x[t]), v1 = __uint_as_float(x[t + 1]),
-                      v2 = __uint_as_float(x[t + 2]), v3 = __uint_as_float(x[t + 3]);
-          on[i] = pack_bf16x2(v0, v1);
-          on[i + 1] = pack_bf16x2(v2, v3);
-          float q[4];
-          mul_x2(q[0], q[1], d4.x, d4.y, v0, v1);
-          mul_x2(q[2], q[3], d4.z, d4.w, v2, v3);
-          tc::split2(q[0], q[1], hi[i], lo[i]);
-          tc::split2(q[2], q[3], hi[i + 1], lo[i + 1]);
-        }
-        tc::st8(tl + kColR + hf * 16 + g * 8, hi);
-        tc::st8(tl + kColR + 32 + hf * 16 + g * 8, lo);
-        tc::st8(tl + kColN + hf * 16 + g * 8, on);
+      for (int i = 0; i < 32; ++i) {
+        const auto raw = f32_to_raw<ST>(S[i]);
+        *reinterpret_cast<std::remove_const_t<decltype(raw)>*>(
+            sp + ((i >> 4) * 64 + (i & 15)) * kD) = raw;
       }
-    }
-    tc::wait_st();
-    tc::fence_before();
-    warp_arrive(&sm.ctl.vd_full);
-  }
-  if (!advance(n - 1, 0) || !advance(n - 1, 1)) return;
-  warp_arrive(&sm.ctl.coef_empty[(n - 1) & 1]);
-  if (ch.slot >= 0)
-#pragma unroll
-    for (int i = 0; i < 64; ++i) {
-      const auto raw = f32_to_raw<ST>(S[i]);
-      *reinterpret_cast<std::remove_const_t<decltype(raw)>*>(
-          sp + ((i >> 5) * 64 + (i & 31)) * kD) = raw;
-    }
   }
 }
 
@@ -780,47 +757,52 @@ __device__ __forceinline__ void out_role(const GdnArgs& a, Smem& sm, const Wait&
   int n = 0;                                      // chunks of the block so far
   Chain ch;
   for (int k = 0; chain_at(a, sm, k, ch); ++k) {
-  char* const op = a.out + ((int64_t)ch.row0 * a.out_rs + (int64_t)ch.h * kD + qd * 32) * 2 +
-                   (lane & 3) * 16;
-  for (int m = 0; m < ch.chunks; ++m, ++n) {
-    if (!wait(&sm.ctl.o_full, n)) return;
-    tc::fence_after();
-    const Coef& C = sm.coef[n & 1];
-    unsigned char* const box = sm.stage[n % kStages] + kKQBytes + qd * 4096;
+    char* const op = a.out + ((int64_t)ch.row0 * a.out_rs + (int64_t)ch.h * kD + qd * 32) * 2 +
+                     (lane & 3) * 16;
+    for (int m = 0; m < ch.chunks; ++m, ++n) {
+      if (!wait(&sm.ctl.o_full, n)) return;
+      tc::fence_after();
+      unsigned char* const box = sm.stage[n % kStages] + kKQBytes + qd * 4096;
 #pragma unroll 1
-    for (int g = 0; g < 4; ++g) {
-      uint32_t x[16], y[16];
-      tc::ld16(tl + kColQS + g * 16, x);
-      tc::ld16(tl + kColO + g * 16, y);
-      tc::wait_ld(x);
-      tc::wait_ld(y);
-      if (g == 3) {
-        tc::fence_before();
-        warp_arrive(&sm.ctl.o_empty);
-      }
-      uint16_t* const o = reinterpret_cast<uint16_t*>(box + g * 1024) + lane;
+      for (int g = 0; g < 4; ++g) {
+        uint32_t x[16], y[16];
+        tc::ld16(tl + kColQS + g * 16, x);
+        tc::ld16(tl + kColO + g * 16, y);
+        tc::wait_ld(x);
+        tc::wait_ld(y);
+        if (g == 3) {
+          tc::fence_before();
+          warp_arrive(&sm.ctl.o_empty);
+        }
+        uint16_t* const o = reinterpret_cast<uint16_t*>(box + g * 1024) + lane;
+        const float* f = sm.o1[n % kOut] + g * 16;
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const float2 c1 = *reinterpret_cast<const float2*>(&C.o1[g * 16 + i]);
-        const float2 c2 = *reinterpret_cast<const float2*>(&C.o2[g * 16 + i]);
-        float v0, v1;
-        mul_x2(v0, v1, c2.x, c2.y, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
-        fma_x2(v0, v1, c1.x, c1.y, __uint_as_float(x[i]), __uint_as_float(x[i + 1]), v0, v1);
-        const uint32_t p = pack_bf16x2(v0, v1);
-        o[i * 32] = (uint16_t)p;
-        o[(i + 1) * 32] = (uint16_t)(p >> 16);
+        for (int i = 0; i < 16; i += 4) {
+          const float4 c = *reinterpret_cast<const float4*>(f + i);
+          float v[4];
+          fma_x2(v[0], v[1], c.x, c.y, __uint_as_float(x[i]), __uint_as_float(x[i + 1]),
+                 __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+          fma_x2(v[2], v[3], c.z, c.w, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]),
+                 __uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]));
+          const uint32_t p0 = pack_bf16x2(v[0], v[1]), p1 = pack_bf16x2(v[2], v[3]);
+          o[i * 32] = (uint16_t)p0;
+          o[(i + 1) * 32] = (uint16_t)(p0 >> 16);
+          o[(i + 2) * 32] = (uint16_t)p1;
+          o[(i + 3) * 32] = (uint16_t)(p1 >> 16);
+        }
       }
-    }
-    warp_arrive(&sm.ctl.coef_empty[n & 1]);
+      warp_arrive(&sm.ctl.o1_empty[n % kOut]);
+      char* ot = op + ((int64_t)m * kC + (lane >> 2)) * a.out_rs * 2;
+      const int left = ch.len - m * kC - (lane >> 2);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint4 q = *reinterpret_cast<const uint4*>(box + (i * 32 + lane) * 16);
-      const int64_t t = (int64_t)m * kC + i * 8 + (lane >> 2);
-      if (t < ch.len) *reinterpret_cast<uint4*>(op + t * a.out_rs * 2) = q;
+      for (int i = 0; i < 8; ++i) {
+        const uint4 q = *reinterpret_cast<const uint4*>(box + (i * 32 + lane) * 16);
+        if (i * 8 < left) *reinterpret_cast<uint4*>(ot) = q;
+        ot += a.out_rs * 16;
+      }
+      fence_proxy_async();
+      warp_arrive(&sm.ctl.empty[n % kStages]);
     }
-    fence_proxy_async();
-    warp_arrive(&sm.ctl.empty[n % kStages]);
-  }
   }
 }
 
@@ -842,19 +824,27 @@ __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks,
     return ((ks >> 2) * kPanel + (ks & 3) * 32 + row * 128) >> 4;
   };
   // Steps of a chunk: S^T k of the first half of dk, of the second (with S^T q),
-  // T R, update. Before each, what runs beside the chain is issued if its
-  // operands are there: the scores of the next chunk that has none, and T V of
-  // this chunk.
+  // T R, update. While S is worked on, the pipe is free: the scores of the next
+  // chunk that has none and T V of this one are issued then, as soon as their
+  // operands are there (and at the latest before T R, which needs both).
   int scored = 0, tved = 0;                     // chunks whose products are issued
 #pragma unroll 1
   for (int step = 0; step < 4 * chunks; ++step) {
     const int n = step >> 2, sub = step & 3, st = n % kStages;
     const uint64_t kq = kq0 + ((st * kStageBytes) >> 4), tp = t0 + (((n & 1) * kTP) >> 4);
-    const bool must = sub == 2 && tved == n;    // T R needs T V before it
+    const bool must = sub == 2;
+    // polls: bounded like the waits, by the one behind this loop or, before T R,
+    // by those inside
 #pragma unroll 1
-    do {
+    for (int poll = 0;
+         must ? tved == n
+              : sub == 0 && (step == 0 ? scored == 0
+                                       : poll == 0 || poll < 4096 && !__any_sync(0xffffffffu,
+                                                                    tc::mbar_ready(&sm.ctl.s_full[0],
+                                                                                   n & 1)));
+         ++poll) {
       uint64_t* const full = &sm.ctl.full[scored % kStages];
-      if (scored < chunks && (must && scored <= n)) {
+      if ((must || step == 0) && scored <= n) {
         if (!wait(full, scored / kStages) || (scored > 0 && !wait(&sm.ctl.d1_empty, scored - 1)))
           return;
       }
@@ -890,7 +880,7 @@ __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks,
         __syncwarp();
         ++tved;
       }
-    } while (must && tved == n);
+    }
     if (sub < 2) {
       if (!wait(&sm.ctl.full[st], n / kStages) || !wait(&sm.ctl.s_full[sub], n)) return;
       // N of the last chunk lies where S^T k goes
@@ -903,7 +893,7 @@ __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks,
         for (int t = 0; t < 2; ++t)             // S hi, S lo
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4)
-            tc::mma_ts(tmem + kColKS, s0 + t * 16 + (k4 >> 1) * 32 + (k4 & 1) * 8,
+            tc::mma_ts(tmem + kColKS, s0 + k4 * 16 + t * 8,
                        kp + panel(k4, 0), kId, (sub | t | k4) > 0);
         if (sub == 1) tc::commit(&sm.ctl.ks_full);
       }
@@ -914,8 +904,7 @@ __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks,
         if (tc::elect()) {
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            tc::mma_ts(tmem + kColQS, tmem + kColS + (ks >> 1) * 32 + (ks & 1) * 8,
-                       kq + panel(ks, kC), kId, ks > 0);
+            tc::mma_ts(tmem + kColQS, tmem + kColS + ks * 16, kq + panel(ks, kC), kId, ks > 0);
           tc::commit(&sm.ctl.qs_done);
         }
         __syncwarp();
@@ -983,11 +972,12 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
       mbar_init(&c.gate_empty[i], kPrepWarps + kInvWarps);
       mbar_init(&c.tp_empty[i], 1);
       mbar_init(&c.coef_full[i], kPrepWarps);
-      mbar_init(&c.coef_empty[i], kScanWarps + kOutWarps);
+      mbar_init(&c.coef_empty[i], kScanWarps);
       mbar_init(&c.s_full[i], kScanWarps);
       mbar_init(&c.sd_full[i], 1);
     }
     mbar_init(&c.d1_full, 1);
+    for (int i = 0; i < kOut; ++i) mbar_init(&c.o1_empty[i], kOutWarps);
     mbar_init(&c.prep_meet, kPrepWarps);
     mbar_init(&c.inv_meet, kInvWarps);
     mbar_init(&c.a_full, 2);
@@ -1027,13 +1017,11 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
   const Wait wait{&sm.ctl, a.dev_err};
 
   if (warp < kScanWarps) {
-    more_regs<kRegsScan>();
     scan_role<ST>(a, sm, wait, tmem);
   } else if (warp < kWarpInv0) {
-    fewer_regs<kRegsPrep>();
+    more_regs<kRegsPrep>();
     prep_role(a, sm, wait, chunks, tmem);
   } else if (warp < kWarpOut0) {
-    fewer_regs<kRegsRest>();
     if (warp < kWarpMma) {
       inv_role(sm, wait, chunks);
     } else if (warp == kWarpMma) {
