@@ -80,7 +80,7 @@ constexpr int kMaxSeqs = 640;                // sequences of a launch
 constexpr int kB = 16;                       // blocks of A and T
 constexpr int kBPitch = 20;                  // fp32 rows of 16: 80 bytes
 constexpr int kAPitch = 56;                  // bf16 rows of 48: 112 bytes
-constexpr int kOut = 4;                      // chunks whose output factors are kept
+constexpr int kCoefs = 4;                    // chunks whose factors are kept
 
 constexpr uint32_t kColS = 0, kColKS = 128, kColN = kColKS, kColQS = 192, kColR = 256,
                    kColVN = 320, kColO = 384, kColD1 = 448;
@@ -92,6 +92,7 @@ constexpr long long kWaitClocks = 4000000000LL;
 struct alignas(16) Coef {
   float rc[kC];      // -e^G / |k|
   float vd[kC];      // e^{G_C - G} / |k|
+  float o1[kC];      // scale e^G / |q|
   float ec;          // e^{G_C}
 };
 // Gates of a chunk: sum of log2 decays (whole part, remainder) and beta.
@@ -105,7 +106,8 @@ struct Maps {
 
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
-  uint64_t gate_empty[2], tp_empty[2], coef_full[2], coef_empty[2], o1_empty[kOut];
+  uint64_t gate_empty[2], tp_empty[2], coef_full[kCoefs], coef_empty[kCoefs];
+  uint64_t v_full[kStages], v_empty[kStages];
   uint64_t d1_full, d1_empty, a_full, a_empty, t_full, prep_meet, inv_meet;
   uint64_t s_full[2], sd_full[2];
   uint64_t ks_full, qs_done, r_full, vn_full, vd_full, o_full, o_empty, fin;
@@ -122,8 +124,7 @@ struct Smem {
   alignas(16) float ed[kC][kBPitch];           // e^{G_i - G_j} / |k_j|, j in the block of i
   alignas(16) float tab[4][kC];                // e^{G_(16I-1) - G_j} / |k_j|, j < 16 I
   alignas(16) float rn[2 * kC];                // 1 / |k|, 1 / |q|
-  alignas(16) float o1[kOut][kC];              // scale e^G / |q|
-  Coef coef[2];
+  Coef coef[kCoefs];
   Gate gate[2];
   uint16_t order[kMaxSeqs];   // the launch's long sequences, longest first
   int count, total;           // how many; chunks of this block's chains
@@ -133,8 +134,7 @@ static_assert(offsetof(Smem, tp) % 1024 == 0 && kStageBytes % 1024 == 0 && kTP %
                   kTBytes % 1024 == 0 && kVPanel % 1024 == 0,
               "swizzled tiles start on 1024 bytes");
 static_assert(sizeof(Coef) % 16 == 0 && sizeof(Gate) % 16 == 0 && offsetof(Smem, Ad) % 16 == 0 &&
-                  offsetof(Smem, Ah) % 16 == 0 && offsetof(Smem, Al) % 16 == 0 &&
-                  offsetof(Smem, o1) % 16 == 0 && offsetof(Smem, ed) % 16 == 0 &&
+                  offsetof(Smem, Ah) % 16 == 0 && offsetof(Smem, Al) % 16 == 0 && offsetof(Smem, ed) % 16 == 0 &&
                   offsetof(Smem, tab) % 16 == 0 && offsetof(Smem, rn) % 16 == 0 &&
                   offsetof(Smem, coef) % 16 == 0 && offsetof(Smem, gate) % 16 == 0 &&
                   offsetof(Smem, ctl) % 8 == 0,
@@ -275,7 +275,7 @@ __device__ __forceinline__ void load_role(const GdnArgs& a, const Maps& maps, Sm
   const int lane = threadIdx.x & 31, u = lane & 15, r2 = lane >> 4;
   const __nv_bfloat16* const ga0 = reinterpret_cast<const __nv_bfloat16*>(a.a);
   const __nv_bfloat16* const gb0 = reinterpret_cast<const __nv_bfloat16*>(a.b);
-  int boxed = 0, g = 0;     // chunks requested as boxes; chunks of the block so far
+  int boxed = 0, v_boxed = 0, g = 0;   // last chunks that came as boxes; chunks of the block so far
   Chain c;
   for (int k = 0; chain_at(a, sm, k, c); ++k) {
   const int row0 = c.row0, len = c.len, h = c.h;
@@ -295,8 +295,6 @@ __device__ __forceinline__ void load_role(const GdnArgs& a, const Maps& maps, Sm
   for (int n = 0; n < c.chunks; ++n, ++g) {
     const int st = g % kStages;
     if (g >= kStages && !wait(&sm.ctl.empty[st], g / kStages - 1)) goto quit;
-    const uint32_t base = smem_addr(sm.stage[st]) + (u >> 3) * kPanel;
-    const uint32_t vbase = smem_addr(sm.stage[st]) + kKQBytes + (u >> 3) * kVPanel;
     float na[2], nb[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -304,33 +302,33 @@ __device__ __forceinline__ void load_role(const GdnArgs& a, const Maps& maps, Sm
       na[i] = t < len ? elem(ga, (int64_t)(row0 + t) * a.a_rs) : 0.0f;
       nb[i] = t < len ? elem(gb, (int64_t)(row0 + t) * a.b_rs) : 0.0f;
     }
+    // K and Q, then, when the outputs have left its place, V
     const bool whole = len - n * kC >= kC;
-    if (whole) {
-      boxed = g + 1;
-      if (lane == 0) {
-        const uint32_t at = smem_addr(sm.stage[st]);
-        const int y = row0 + n * kC;
-        mbar_arrive_tx(&sm.ctl.full[st], kStageBytes);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          tc::tma_load_2d(at + p * kPanel, &maps.k, hk * kD + p * 64, y, &sm.ctl.full[st]);
-          tc::tma_load_2d(at + p * kPanel + kC * 128, &maps.q, hk * kD + p * 64, y,
-                          &sm.ctl.full[st]);
-          tc::tma_load_2d(at + kKQBytes + p * kVPanel, &maps.v, h * kD + p * 64, y,
-                          &sm.ctl.full[st]);
-        }
-      }
-    } else {
+    const int y = row0 + n * kC;
+    const uint32_t at = smem_addr(sm.stage[st]);
+    auto rows = [&](uint32_t dst, uint32_t pitch, const char* src, int64_t stride) {
 #pragma unroll 1
       for (int i = 0; i < kC / 2; ++i) {
         const int r = i * 2 + r2;
         const int64_t t = (int64_t)n * kC + r;
         const bool in = t < len;
-        const int64_t tt = in ? t : 0;
-        cp_async16(base + sw128(r, u & 7), kp + tt * a.k_rs * 2, in);
-        cp_async16(base + sw128(kC + r, u & 7), qp + tt * a.q_rs * 2, in);
-        cp_async16(vbase + sw128(r, u & 7), vp + tt * a.v_rs * 2, in);
+        cp_async16(dst + (u >> 3) * pitch + sw128(r, u & 7), src + (in ? t : 0) * stride * 2, in);
       }
+    };
+    if (whole) {
+      boxed = g + 1;
+      if (lane == 0) {
+        mbar_arrive_tx(&sm.ctl.full[st], kKQBytes);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          tc::tma_load_2d(at + p * kPanel, &maps.k, hk * kD + p * 64, y, &sm.ctl.full[st]);
+          tc::tma_load_2d(at + p * kPanel + kC * 128, &maps.q, hk * kD + p * 64, y,
+                          &sm.ctl.full[st]);
+        }
+      }
+    } else {
+      rows(at, kPanel, kp, a.k_rs);
+      rows(at + kC * 128, kPanel, qp, a.q_rs);
       cp_async_commit();
     }
     float w[2], f[2], be[2];
@@ -376,6 +374,23 @@ __device__ __forceinline__ void load_role(const GdnArgs& a, const Maps& maps, Sm
       if (lane == 0) mbar_arrive(&sm.ctl.full[st]);
     }
     warp_arrive(&sm.ctl.full[st]);
+    if (g >= kStages && !wait(&sm.ctl.v_empty[st], g / kStages - 1)) goto quit;
+    if (whole) {
+      v_boxed = g + 1;
+      if (lane == 0) {
+        mbar_arrive_tx(&sm.ctl.v_full[st], kVBytes);
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          tc::tma_load_2d(at + kKQBytes + p * kVPanel, &maps.v, h * kD + p * 64, y,
+                          &sm.ctl.v_full[st]);
+      }
+    } else {
+      rows(at + kKQBytes, kVPanel, vp, a.v_rs);
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_proxy_async();
+      warp_arrive(&sm.ctl.v_full[st]);
+    }
   }
   }
   return;
@@ -383,6 +398,8 @@ quit:                       // given up: no copy lands after the block ends
   cp_async_wait<0>();
   for (int i = max(boxed - kStages, 0); i < boxed; ++i)
     drain(&sm.ctl.full[i % kStages], i / kStages, a.dev_err);
+  for (int i = max(v_boxed - kStages, 0); i < v_boxed; ++i)
+    drain(&sm.ctl.v_full[i % kStages], i / kStages, a.dev_err);
 }
 
 // ---- the warps that look one chunk ahead ------------------------------------
@@ -462,7 +479,7 @@ __device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait
   Meet meet{&sm.ctl.prep_meet, 0};
   for (int n = 0; n < chunks; ++n) {
     const int st = n % kStages, bf = n & 1;
-    Coef& C = sm.coef[bf];
+    Coef& C = sm.coef[n % kCoefs];
     const Gate& G = sm.gate[bf];
     // ---- norms
     if (!wait(&sm.ctl.full[st], n / kStages)) return;
@@ -486,9 +503,7 @@ __device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait
       rn = 1.0f / sqrtf((s0 + s1) + (s2 + s3) + kGdnNormEps);
     }
     sm.rn[p] = rn;
-    // the factors of two (four) chunks ago have been read
-    if (n >= 2 && !wait(&sm.ctl.coef_empty[bf], (n >> 1) - 1)) return;
-    if (n >= kOut && !wait(&sm.ctl.o1_empty[n % kOut], n / kOut - 1)) return;
+    if (n >= kCoefs && !wait(&sm.ctl.coef_empty[n % kCoefs], n / kCoefs - 1)) return;
     if (!meet(wait)) return;
     // ---- factors
     const float hi = G.hi[r], lo = G.lo[r];
@@ -498,7 +513,7 @@ __device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait
       C.vd[r] = rn * tc::ex2((G.hi[kC - 1] - hi) + (G.lo[kC - 1] - lo));
       if (r == kC - 1) C.ec = eg;
     } else {
-      sm.o1[n % kOut][r] = a.scale * rn * eg;
+      C.o1[r] = a.scale * rn * eg;
     }
     {
       const float rk = sm.rn[r];
@@ -523,7 +538,7 @@ __device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait
     const float fac = is_k ? rn : a.scale * rn;
     const float off =
         blk > 0 ? fac * tc::ex2((hi - G.hi[blk * kB - 1]) + (lo - G.lo[blk * kB - 1])) : 0.0f;
-    warp_arrive(&sm.ctl.coef_full[bf]);
+    warp_arrive(&sm.ctl.coef_full[n % kCoefs]);
     if (!meet(wait)) return;
     // ---- A and the scores from [K; Q] K^T: row r times the factors of its
     // columns, e^{G_i - G_j} as two factors at most 1 around the block's start
@@ -661,7 +676,7 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
     tc::fence_after();
     uint32_t x[16];
     tc::ld16(ts + p * 64, x);
-    const float ec = sm.coef[n & 1].ec;
+    const float ec = sm.coef[n % kCoefs].ec;
     tc::wait_ld(x);
 #pragma unroll
     for (int i = 0; i < 16; i += 2)
@@ -695,7 +710,7 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
     for (int i = 0; i < 32; ++i)
       S[i] = ch.init ? elem(sp, ((i >> 4) * 64 + (i & 15)) * kD) : 0.0f;
     for (int m = 0; m < ch.chunks; ++m, ++n) {
-      const Coef& C = sm.coef[n & 1];
+      const Coef& C = sm.coef[n % kCoefs];
       // ---- S: add the last chunk's update, split, hand to the tensor cores
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
@@ -710,9 +725,9 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
         tc::fence_before();
         warp_arrive(&sm.ctl.s_full[p]);
       }
-      if (m > 0) warp_arrive(&sm.ctl.coef_empty[(n - 1) & 1]);
+      if (m > 0) warp_arrive(&sm.ctl.coef_empty[(n - 1) % kCoefs]);
       // ---- R
-      if (!wait(&sm.ctl.coef_full[n & 1], n >> 1) || !wait(&sm.ctl.ks_full, n)) return;
+      if (!wait(&sm.ctl.coef_full[n % kCoefs], n / kCoefs) || !wait(&sm.ctl.ks_full, n)) return;
       tc::fence_after();
       uint32_t x[16];
       tc::ld16(tl + kColKS + qt * 16, x);
@@ -737,7 +752,7 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
       warp_arrive(&sm.ctl.vd_full);
     }
     if (!advance(n - 1, 0) || !advance(n - 1, 1)) return;
-    warp_arrive(&sm.ctl.coef_empty[(n - 1) & 1]);
+    warp_arrive(&sm.ctl.coef_empty[(n - 1) % kCoefs]);
     if (ch.slot >= 0)
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
@@ -775,7 +790,7 @@ __device__ __forceinline__ void out_role(const GdnArgs& a, Smem& sm, const Wait&
           warp_arrive(&sm.ctl.o_empty);
         }
         uint16_t* const o = reinterpret_cast<uint16_t*>(box + g * 1024) + lane;
-        const float* f = sm.o1[n % kOut] + g * 16;
+        const float* f = sm.coef[n % kCoefs].o1 + g * 16;
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const float4 c = *reinterpret_cast<const float4*>(f + i);
@@ -791,7 +806,7 @@ __device__ __forceinline__ void out_role(const GdnArgs& a, Smem& sm, const Wait&
           o[(i + 3) * 32] = (uint16_t)(p1 >> 16);
         }
       }
-      warp_arrive(&sm.ctl.o1_empty[n % kOut]);
+      warp_arrive(&sm.ctl.coef_empty[n % kCoefs]);
       char* ot = op + ((int64_t)m * kC + (lane >> 2)) * a.out_rs * 2;
       const int left = ch.len - m * kC - (lane >> 2);
 #pragma unroll
@@ -801,7 +816,7 @@ __device__ __forceinline__ void out_role(const GdnArgs& a, Smem& sm, const Wait&
         ot += a.out_rs * 16;
       }
       fence_proxy_async();
-      warp_arrive(&sm.ctl.empty[n % kStages]);
+      warp_arrive(&sm.ctl.v_empty[n % kStages]);
     }
   }
 }
@@ -864,9 +879,12 @@ __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks,
         ++scored;
       }
       // (chunk n - 1's N has been read: its update, which needed it, is issued)
-      if (must && scored > n && !wait(&sm.ctl.t_full, n)) return;
+      if (must && scored > n &&
+          (!wait(&sm.ctl.t_full, n) || !wait(&sm.ctl.v_full[st], n / kStages)))
+        return;
       if (tved == n && scored > n &&
-          __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.t_full, tved & 1))) {
+          __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.t_full, n & 1)) &&
+          __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.v_full[st], (n / kStages) & 1))) {
         tc::fence_after();
         const uint64_t v = v0 + ((st * kStageBytes) >> 4);
         if (tc::elect()) {                      // (T V)^T, V read along dv
@@ -936,12 +954,12 @@ __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks,
                          kq + ((part * kPanel + ks * 2048) >> 4), kIdT, (t | ks) > 0);
           tc::commit(&sm.ctl.sd_full[part]);
         }
+        tc::commit(&sm.ctl.empty[st]);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           tc::mma_ts(tmem + kColO, tmem + kColN + ks * 8,
                      tp + ((2 * kTBytes + ks * 32) >> 4), kId, ks > 0);
         tc::commit(&sm.ctl.o_full);
-        tc::commit(&sm.ctl.empty[st]);
         tc::commit(&sm.ctl.tp_empty[n & 1]);
       }
       __syncwarp();
@@ -966,18 +984,21 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
     Ctl& c = sm.ctl;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&c.full[i], 2);                // rows, gates
-      mbar_init(&c.empty[i], 1 + kOutWarps);
+      mbar_init(&c.empty[i], 1);
+      mbar_init(&c.v_full[i], 1);
+      mbar_init(&c.v_empty[i], kOutWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.gate_empty[i], kPrepWarps + kInvWarps);
       mbar_init(&c.tp_empty[i], 1);
-      mbar_init(&c.coef_full[i], kPrepWarps);
-      mbar_init(&c.coef_empty[i], kScanWarps);
       mbar_init(&c.s_full[i], kScanWarps);
       mbar_init(&c.sd_full[i], 1);
     }
     mbar_init(&c.d1_full, 1);
-    for (int i = 0; i < kOut; ++i) mbar_init(&c.o1_empty[i], kOutWarps);
+    for (int i = 0; i < kCoefs; ++i) {
+      mbar_init(&c.coef_full[i], kPrepWarps);
+      mbar_init(&c.coef_empty[i], kScanWarps + kOutWarps);
+    }
     mbar_init(&c.prep_meet, kPrepWarps);
     mbar_init(&c.inv_meet, kInvWarps);
     mbar_init(&c.a_full, 2);
