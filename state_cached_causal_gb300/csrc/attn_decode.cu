@@ -245,9 +245,17 @@ struct AttnPlan {
 };
 AttnPlan plan(int dtype, int sms, int64_t B, int q_len, int G, int Hkv, int D) {
   AttnPlan p;
-  p.rows = kRows;
-  p.rblocks = (G * q_len + kRows - 1) / kRows;
-  p.grid = sms * 2;
+  const int rows = G * q_len;
+  if (dtype == CCONV_DTYPE_F32) {
+    p.rows = kRows;
+    p.grid = sms * 2;
+  } else {
+    // row tiles whose sums fit in registers; blocks that an SM holds at once, by
+    // their shared memory (70 to 218 KB) and registers
+    p.rows = rows <= 16 || D == 256 ? 16 : 32;
+    p.grid = sms * (D * p.rows >= 4096 ? 1 : D * p.rows >= 2048 ? 2 : 3);
+  }
+  p.rblocks = (rows + p.rows - 1) / p.rows;
   p.meta_bytes = (B * Hkv * p.rblocks * 8 + 15) / 16 * 16;
   p.bytes = p.meta_bytes + (int64_t)p.grid * 2 * p.rows * (D + 2) * 4;
   return p;
@@ -316,6 +324,9 @@ extern "C" int attn_decode(const void* q, int64_t q_row_stride, kv_cache_t cache
   a.vc = static_cast<const char*>(cache.v);
   a.s_page = cache.s_page, a.s_tok = cache.s_token, a.s_head = cache.s_head;
   a.num_pages = cache.num_pages, a.page_size = cache.page_size;
+  a.page_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if (cache.page_size == 1 << s) a.page_shift = s;
   a.table = block_table;
   a.table_rs = block_table_row_stride;
   a.table_width = table_width;
@@ -341,9 +352,7 @@ extern "C" int attn_decode(const void* q, int64_t q_row_stride, kv_cache_t cache
           : D == 128 ? launch_attn<float, 128>(a, p.grid, st)
                      : launch_attn<float, 256>(a, p.grid, st);
   else
-    err = D == 64 ? launch_attn<__nv_bfloat16, 64>(a, p.grid, st)
-          : D == 128 ? launch_attn<__nv_bfloat16, 128>(a, p.grid, st)
-                     : launch_attn<__nv_bfloat16, 256>(a, p.grid, st);
+    err = attn_launch_mma(a, D, p.grid, st);
   if (err != cudaSuccess) return CCONV_ERR_LAUNCH;
   const dim3 grid((unsigned)(num_seqs * cache.num_kv_heads * p.rblocks),
                   (unsigned)std::min(8, p.rows));

@@ -23,6 +23,7 @@ struct AttnArgs {
   const char *kc, *vc;
   int64_t s_page, s_tok, s_head;
   int32_t num_pages, page_size;
+  int32_t page_shift;   // log2(page_size), -1 if it is no power of two
   const int32_t* table;
   int64_t table_rs;
   int32_t table_width;
