@@ -15,6 +15,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kTile = 32;
 constexpr int kRows = 8;          // query rows of a block
+constexpr int kMaxGrid = 4096;    // blocks of the split kernels
 
 template <typename T, int D>
 struct AttnSmem {
@@ -187,46 +188,89 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const AttnArgs a) {
   }
 }
 
-// Joins the parts of a cut unit, one block a unit: a thread a column, rows in
-// turn. Part i (block c0 + i) is slot 1 of block c0 and slot 0 of the others.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, const int D) {
-  const int u = blockIdx.x % (a.Hkv * a.rblocks), b = blockIdx.x / (a.Hkv * a.rblocks);
-  const int c0 = a.meta[(int64_t)blockIdx.x * 2], c1 = a.meta[(int64_t)blockIdx.x * 2 + 1];
+// Joins the parts of a cut unit, one block a row of a unit. Part i (block c0 +
+// i) is slot 1 of block c0 and slot 0 of the others. The threads first turn the
+// parts' maxima and sums into weights, then take a column each and every
+// kGroups-th part, sixteen loads in flight. (It is launched to overlap the end
+// of the kernel before, whose results it waits for.) Few units have many parts
+// each and get 512 threads a row, many units few parts and 256.
+template <typename T, int D, int kJoinThreads>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
+  constexpr int kGroups = kJoinThreads / D;
+  __shared__ float wt[kMaxGrid];
+  __shared__ float red[2][kJoinThreads / 32];
+  __shared__ float sums[kGroups][D];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int rows = a.hw * a.rows, used = min(a.rows, a.G * a.q_len);
+  const int64_t bu = blockIdx.x;                    // request and unit
+  const int row = blockIdx.y / used * a.rows + blockIdx.y % used;
+  const int c0 = a.meta[bu * 2], c1 = a.meta[bu * 2 + 1];
   if (c0 < 0) return;
-  const int hkv = u / a.rblocks, r0 = u % a.rblocks * a.rows;
-  const int nr = min(a.rows, a.G * a.q_len - r0);
-  const int64_t one = (int64_t)a.rows * (D + 2);
-  auto slot = [&](int c) { return a.part + ((int64_t)c * 2 + (c == c0)) * one; };
-  for (int r = blockIdx.y; r < nr; r += gridDim.y) {
-    float m = -INFINITY;
-    for (int c = c0; c <= c1; ++c) m = fmaxf(m, slot(c)[r * (D + 2) + D]);
-    float l = 0.0f, acc[2] = {0.0f, 0.0f};
-    if (m > -INFINITY)
-      for (int c = c0; c <= c1; ++c) {
-        const float* p = slot(c) + r * (D + 2);
-        const float w = expf(p[D] - m);
-        l = fmaf(w, p[D + 1], l);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if ((int)threadIdx.x + i * kThreads < D)
-            acc[i] = fmaf(w, p[threadIdx.x + i * kThreads], acc[i]);
-      }
-    const int rr = r0 + r;
-    const int64_t row = (int64_t)b * a.q_len + rr / a.G;
-    const int h = hkv * a.G + rr % a.G;
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if ((int)threadIdx.x + i * kThreads < D) {
-        const auto raw = f32_to_raw<T>(acc[i] * inv);
-        *reinterpret_cast<std::remove_const_t<decltype(raw)>*>(
-            reinterpret_cast<T*>(a.out) + row * a.out_rs + (int64_t)h * D + threadIdx.x +
-            i * kThreads) = raw;
-      }
-    if (a.lse && threadIdx.x == 0)
-      a.lse[row * a.Hq + h] = l > 0.0f ? m + logf(l) : -INFINITY;
+  const int b = (int)(bu / a.units), u = (int)(bu % a.units);
+  const int hkv = u / a.rblocks * a.hw + row / a.rows;
+  const int rr = u % a.rblocks * a.rows + row % a.rows;
+  if (rr >= a.G * a.q_len) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, parts = c1 - c0 + 1;
+  const int64_t one = (int64_t)rows * (D + 2);
+  auto part = [&](int i) {
+    return a.part + ((int64_t)(c0 + i) * 2 + (i == 0)) * one + row * (D + 2);
+  };
+  float m = -INFINITY;
+  for (int i = tid; i < parts; i += kJoinThreads) {
+    const float x = part(i)[D];
+    wt[i] = x;
+    m = fmaxf(m, x);
   }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  if (lane == 0) red[0][warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[0][w]);
+  float l = 0.0f;
+  for (int i = tid; i < parts; i += kJoinThreads) {
+    const float w = m == -INFINITY ? 0.0f : expf(wt[i] - m);
+    wt[i] = w;
+    l = fmaf(w, part(i)[D + 1], l);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  if (lane == 0) red[1][warp] = l;
+  __syncthreads();
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) l += red[1][w];
+  const int c = tid % D, g = tid / D;
+  float acc = 0.0f;
+#pragma unroll 16
+  for (int i = g; i < parts; i += kGroups) acc = fmaf(wt[i], part(i)[c], acc);
+  sums[g][c] = acc;
+  __syncthreads();
+  if (g > 0) return;
+#pragma unroll
+  for (int k = 1; k < kGroups; ++k) acc += sums[k][c];
+  const int64_t orow = (int64_t)b * a.q_len + rr / a.G;
+  const int h = hkv * a.G + rr % a.G;
+  const auto raw = f32_to_raw<T>(l > 0.0f ? acc / l : 0.0f);
+  *reinterpret_cast<std::remove_const_t<decltype(raw)>*>(reinterpret_cast<T*>(a.out) +
+                                                         orow * a.out_rs + (int64_t)h * D + c) = raw;
+  if (a.lse && c == 0) a.lse[orow * a.Hq + h] = l > 0.0f ? m + logf(l) : -INFINITY;
+}
+
+template <typename T, int D>
+cudaError_t launch_join(const AttnArgs& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.B * a.units), (unsigned)(a.hw * std::min(a.rows, a.G * a.q_len)));
+  const bool few = (int64_t)cfg.gridDim.x * cfg.gridDim.y <= 1024;
+  cfg.blockDim = dim3(few ? 512 : 256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return few ? cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D, 512>, a)
+             : cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D, 256>, a);
 }
 
 template <typename T, int D>
@@ -240,12 +284,13 @@ cudaError_t launch_attn(const AttnArgs& a, int grid, cudaStream_t st) {
 }
 
 struct AttnPlan {
-  int rblocks, rows, grid;
+  int hw, rblocks, rows, units, grid;
   int64_t meta_bytes, bytes;
 };
 AttnPlan plan(int dtype, int sms, int64_t B, int q_len, int G, int Hkv, int D) {
   AttnPlan p;
   const int rows = G * q_len;
+  p.hw = 1;
   if (dtype == CCONV_DTYPE_F32) {
     p.rows = kRows;
     p.grid = sms * 2;
@@ -253,11 +298,14 @@ AttnPlan plan(int dtype, int sms, int64_t B, int q_len, int G, int Hkv, int D) {
     // row tiles whose sums fit in registers; blocks that an SM holds at once, by
     // their shared memory (70 to 218 KB) and registers
     p.rows = rows <= 16 || D == 256 ? 16 : 32;
+    p.hw = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
     p.grid = sms * (D * p.rows >= 4096 ? 1 : D * p.rows >= 2048 ? 2 : 3);
   }
+  p.grid = std::min(p.grid, kMaxGrid);
   p.rblocks = (rows + p.rows - 1) / p.rows;
-  p.meta_bytes = (B * Hkv * p.rblocks * 8 + 15) / 16 * 16;
-  p.bytes = p.meta_bytes + (int64_t)p.grid * 2 * p.rows * (D + 2) * 4;
+  p.units = Hkv / p.hw * p.rblocks;
+  p.meta_bytes = (B * p.units * 8 + 15) / 16 * 16;
+  p.bytes = p.meta_bytes + (int64_t)p.grid * 2 * p.hw * p.rows * (D + 2) * 4;
   return p;
 }
 
@@ -267,7 +315,7 @@ int check_sizes(int32_t num_seqs, int32_t n_spec, int32_t Hq, int32_t Hkv, int32
   if (n_spec > kMaxSpec || (int64_t)(Hq / Hkv) * (1 + n_spec) > 64 ||
       (D != 64 && D != 128 && D != 256))
     return CCONV_ERR_UNSUPPORTED;
-  if ((int64_t)num_seqs * Hkv * 8 > INT32_MAX || (int64_t)num_seqs * (1 + n_spec) > INT32_MAX)
+  if ((int64_t)num_seqs * Hkv * 128 > INT32_MAX || (int64_t)num_seqs * (1 + n_spec) > INT32_MAX)
     return CCONV_ERR_INVALID;
   return CCONV_OK;
 }
@@ -342,8 +390,10 @@ extern "C" int attn_decode(const void* q, int64_t q_row_stride, kv_cache_t cache
   a.lse = lse;
   a.meta = static_cast<int32_t*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.meta_bytes);
+  a.hw = p.hw;
   a.rblocks = p.rblocks;
   a.rows = p.rows;
+  a.units = p.units;
   a.dev_err = dev_err;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t err;
@@ -354,11 +404,12 @@ extern "C" int attn_decode(const void* q, int64_t q_row_stride, kv_cache_t cache
   else
     err = attn_launch_mma(a, D, p.grid, st);
   if (err != cudaSuccess) return CCONV_ERR_LAUNCH;
-  const dim3 grid((unsigned)(num_seqs * cache.num_kv_heads * p.rblocks),
-                  (unsigned)std::min(8, p.rows));
   if (dtype == CCONV_DTYPE_F32)
-    attn_join_kernel<float><<<grid, kThreads, 0, st>>>(a, D);
+    err = D == 64 ? launch_join<float, 64>(a, st) : D == 128 ? launch_join<float, 128>(a, st)
+                                                             : launch_join<float, 256>(a, st);
   else
-    attn_join_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a, D);
-  return cudaGetLastError() == cudaSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
+    err = D == 64 ? launch_join<__nv_bfloat16, 64>(a, st)
+          : D == 128 ? launch_join<__nv_bfloat16, 128>(a, st)
+                     : launch_join<__nv_bfloat16, 256>(a, st);
+  return err == cudaSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
 }

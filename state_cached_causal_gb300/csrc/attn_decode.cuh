@@ -1,16 +1,16 @@
 // Paged attention of new tokens: work split, partial results and arguments
-// shared by the kernels of attn_decode (attn_decode.cu).
+// shared by the kernels of attn_decode (attn_decode.cu, attn_mma.cu).
 //
-// The cached tokens of a request and kv head are cut into tiles of `tile`
-// positions. All tiles of the call form one line -- request by request, head
-// by head, tile by tile -- which the grid's blocks cut into equal runs,
-// whatever the requests' lengths: the work is K and V bytes, and equal runs of
-// them end together. A block walks its run as segments, one per request and
-// head. A segment that holds all the tiles of its request and head is written
-// out at once; of one that is cut the block stores the running maximum, sum
-// and weighted values, at most two a block (its first segment if that began in
-// another block, its last if that goes on in the next), and attn_join_kernel
-// joins them.
+// A unit is a request with a group of `hw` kv heads (and a block of `rows` query
+// rows of each); its cached tokens are cut into tiles of `tile` positions. All
+// tiles of the call form one line -- request by request, unit by unit, tile by
+// tile -- which the grid's blocks cut into equal runs, whatever the requests'
+// lengths: the work is K and V bytes, and equal runs of them end together. A
+// block walks its run as segments, one per unit. A segment that holds all the
+// tiles of its unit is written out at once; of one that is cut the block stores
+// the running maximum, sum and weighted values, at most two a block (its first
+// segment if that began in another block, its last if that goes on in the
+// next), and attn_join_kernel joins them.
 #pragma once
 
 #include "mixer.cuh"
@@ -33,10 +33,12 @@ struct AttnArgs {
   char* out;
   int64_t out_rs;
   float* lse;
-  int32_t* meta;     // [B * Hkv * row blocks][2]: first and last block of a cut unit, or -1
-  float* part;       // [grid][2][rows][D + 2]: weighted values, maximum, sum
-  int32_t rblocks;   // row blocks of a unit (rows of G * q_len taken separately)
+  int32_t* meta;     // [B * units][2]: first and last block of a cut unit, or -1
+  float* part;       // [grid][2][hw * rows][D + 2]: weighted values, maximum, sum
+  int32_t hw;        // kv heads of a unit
+  int32_t rblocks;   // row blocks of a head (rows of G * q_len taken separately)
   int32_t rows;      // rows of a block
+  int32_t units;     // of a request: Hkv / hw * rblocks
   int32_t* dev_err;
 };
 
@@ -85,7 +87,7 @@ __device__ __forceinline__ bool attn_split(const AttnArgs& a, int tile, int64_t 
     sum += sm[w];
   }
   incl += base;
-  const int64_t units = (int64_t)a.Hkv * a.rblocks;
+  const int64_t units = a.units;
   r.total = sum * units;
   // no run is empty: where there are fewer tiles than blocks, the blocks past
   // the tiles' number have none
@@ -124,7 +126,7 @@ struct AttnSeg {
 };
 __device__ __forceinline__ AttnSeg attn_segment(const AttnArgs& a, int tile, const AttnRun& r) {
   AttnSeg s;
-  const int64_t units = (int64_t)a.Hkv * a.rblocks;
+  const int64_t units = a.units;
   s.b = r.b;
   s.len = attn_len(a, r.b);
   s.tiles = attn_tiles(a, r.b, tile);
@@ -138,7 +140,7 @@ __device__ __forceinline__ AttnSeg attn_segment(const AttnArgs& a, int tile, con
 }
 __device__ __forceinline__ void attn_advance(const AttnArgs& a, const AttnSeg& s, AttnRun& r) {
   r.p += s.j1 - s.j0;
-  if (s.j1 == s.tiles && s.unit == a.Hkv * a.rblocks - 1) {
+  if (s.j1 == s.tiles && s.unit == a.units - 1) {
     r.before += s.tiles;
     ++r.b;
   }
@@ -147,11 +149,11 @@ __device__ __forceinline__ void attn_advance(const AttnArgs& a, const AttnSeg& s
 // Where the block's part of a cut segment goes (see above), and the note for
 // the join, written by the block that holds the unit's first tile.
 __device__ __forceinline__ float* attn_part(const AttnArgs& a, const AttnSeg& s, int D) {
-  return a.part + ((int64_t)blockIdx.x * 2 + (s.j0 == 0 ? 1 : 0)) * a.rows * (D + 2);
+  return a.part + ((int64_t)blockIdx.x * 2 + (s.j0 == 0 ? 1 : 0)) * a.hw * a.rows * (D + 2);
 }
 __device__ __forceinline__ void attn_note(const AttnArgs& a, const AttnSeg& s, const AttnRun& r) {
   if (s.j0 != 0) return;
-  int32_t* m = a.meta + ((int64_t)s.b * a.Hkv * a.rblocks + s.unit) * 2;
+  int32_t* m = a.meta + ((int64_t)s.b * a.units + s.unit) * 2;
   const bool cut = !s.whole && s.len >= 0;
   m[0] = cut ? attn_block_of(s.line, r) : -1;
   m[1] = cut ? attn_block_of(s.line + s.tiles - 1, r) : -1;

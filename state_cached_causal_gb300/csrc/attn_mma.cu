@@ -10,12 +10,14 @@
 //
 // A block of 4 warps keeps a ring of tiles of K and V in shared memory, filled
 // by cp.async (16 bytes a request, rows swizzled by 16-byte unit so that
-// ldmatrix meets no bank conflict), several tiles ahead. Each warp takes 16 of
-// a tile's 64 positions: scores = Q K^T (Q held in registers), running maximum
-// and sum of its own, weights to bf16 in registers (the score layout of one
-// product is the weight layout of the next), weighted values += P V. No barrier
-// between warps but the ring's; the four partial results are joined once per
-// segment, through shared memory.
+// ldmatrix meets no bank conflict), several tiles ahead. A tile is 64 rows: 64 /
+// hw positions of hw kv heads, since the heads of a token lie side by side in
+// the usual cache and one head alone would take 256 bytes of every kilobyte
+// (3.96 TB/s so, against @HW@ with four heads together). Each warp takes 16
+// rows, of one head: scores = Q K^T, running maximum and sum of its own, weights
+// to bf16 in registers (the score layout of one product is the weight layout of
+// the next), weighted values += P V. No barrier between warps but the ring's;
+// warps of one head join their parts once per segment, through shared memory.
 //
 // Positions of a tile that lie behind the length or on a bad page are filled
 // with zeros and masked.
@@ -28,7 +30,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 64;           // positions of a tile; 16 a warp
+constexpr int kTile = 64;           // rows of a tile (positions x heads); 16 a warp
 
 template <int D>
 struct Cfg {
@@ -36,7 +38,7 @@ struct Cfg {
   static constexpr int kUnits = D / 8;                       // 16-byte units a row
   static constexpr int kTileBytes = kTile * kRowBytes;       // K or V of a tile
   static constexpr int kStages = D == 64 ? 4 : 3;
-  static constexpr int kSmem = kStages * 2 * kTileBytes;
+  static constexpr int kRing = kStages * 2 * kTileBytes;
 };
 
 // Byte of 16-byte unit u of row r: units are permuted within groups of eight.
@@ -78,29 +80,35 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
   constexpr bool kQRegs = MT * D <= 128;
   extern __shared__ __align__(128) unsigned char attn_dyn[];
   __shared__ int64_t scan[kThreads + 4];
-  __shared__ __align__(16) unsigned char sq[kQRegs ? 16 : MT * 16 * D * 2];
   __shared__ __align__(4) unsigned char there[C::kStages][kTile];   // positions that hold a token
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t smem = smem_addr(attn_dyn);
+  // behind the ring: the joins of at most two heads, or the warps' own Q before
+  float* const join = reinterpret_cast<float*>(attn_dyn + C::kRing);
+  unsigned char* const sq = attn_dyn + C::kRing + warp * (MT * 16 * D * 2);
   AttnRun run;
-  if (!attn_split<kThreads>(a, kTile, scan, run)) return;
+  const int hw_shift = a.hw == 4 ? 2 : a.hw >> 1, tpos = kTile >> hw_shift;   // positions a tile
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!attn_split<kThreads>(a, tpos, scan, run)) return;
   const int rows_all = a.G * a.q_len;
   const float sl2 = a.scale * 1.4426950408889634f;
 
   // ---- loads: thread tid copies unit tid % kUnits of rows tid / kUnits + ..
   constexpr int kRowsAtOnce = kThreads / C::kUnits, kCopies = kTile / kRowsAtOnce;
   AttnRun ld = run;               // the load side runs ahead of the compute side
-  AttnSeg ls = attn_segment(a, kTile, ld);
+  AttnSeg ls = attn_segment(a, tpos, ld);
   int lj = ls.j0;
   auto load_tile = [&](int stage) {
     if (ld.p < ld.end) {
       const uint32_t kb = smem + stage * 2 * C::kTileBytes, vb = kb + C::kTileBytes;
       const int u = tid % C::kUnits, r0 = tid / C::kUnits;
-      const int hkv = ls.unit / a.rblocks;
+      const int hkv0 = ls.unit / a.rblocks * a.hw;
       const int32_t* tab = a.table + (int64_t)ls.b * a.table_rs;
 #pragma unroll
       for (int i = 0; i < kCopies; ++i) {
-        const int r = r0 + i * kRowsAtOnce, pos = lj * kTile + r;
+        // copies in the order of the cache: position by position, its heads
+        const int k = r0 + i * kRowsAtOnce, hl = k & (a.hw - 1), pl = k >> hw_shift;
+        const int r = hl * tpos + pl, pos = lj * tpos + pl;
         int page = -1;
         if (pos < ls.len) {
           page = tab[a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size];
@@ -112,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
         const bool in = page >= 0;
         const int tok = a.page_shift >= 0 ? pos & (a.page_size - 1) : pos % a.page_size;
         const int64_t off = in ? ((int64_t)page * a.s_page + (int64_t)tok * a.s_tok +
-                                  (int64_t)hkv * a.s_head + u * 8) * 2
+                                  (int64_t)(hkv0 + hl) * a.s_head + u * 8) * 2
                                : 0;
         if (u == 0) there[stage][r] = in;
         cp_async16(kb + at<D>(r, u), a.kc + off, in);
@@ -121,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
       if (++lj == ls.j1) {
         attn_advance(a, ls, ld);
         if (ld.p < ld.end) {
-          ls = attn_segment(a, kTile, ld);
+          ls = attn_segment(a, tpos, ld);
           lj = ls.j0;
         }
       }
@@ -133,13 +141,15 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
   int stage = 0;
 
   while (run.p < run.end) {
-    const AttnSeg sg = attn_segment(a, kTile, run);
+    const AttnSeg sg = attn_segment(a, tpos, run);
     if (tid == 0) {
       attn_note(a, sg, run);
       if (sg.len < 0) flag_error(a.dev_err, CCONV_DERR_SEQ_LEN);
     }
     attn_advance(a, sg, run);
-    const int hkv = sg.unit / a.rblocks, r0 = sg.unit % a.rblocks * (MT * 16);
+    // the warp's head and its first position of a tile
+    const int hkv = sg.unit / a.rblocks * a.hw + warp * 16 / tpos;
+    const int p0 = warp * 16 % tpos, r0 = sg.unit % a.rblocks * (MT * 16);
     const int rows = min(MT * 16, rows_all - r0);
     // ---- Q as left operands: row r is token (r0 + r) / G, head hkv * G + (r0 + r) % G
     auto q_row = [&](int r) {
@@ -164,13 +174,13 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
                   in ? *reinterpret_cast<const uint32_t*>(p + (ks * 16 + e * 8) * 2) : 0u;
         }
     } else {
-      for (int i = tid; i < MT * 16 * C::kUnits; i += kThreads) {
+      for (int i = lane; i < MT * 16 * C::kUnits; i += 32) {
         const int r = i / C::kUnits, u = i % C::kUnits;
         const bool in = r < rows && sg.len > 0;
         *reinterpret_cast<uint4*>(sq + at<D>(r, u)) =
             in ? ldg16(q_row(r) + u * 16) : make_uint4(0u, 0u, 0u, 0u);
       }
-      // (the first tile's barrier makes it visible)
+      __syncwarp();
     }
     float m[MT][2], l[MT][2], o[MT][D / 8][4];
 #pragma unroll
@@ -208,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
         }
       }
       // ---- mask, running maximum, weights
-      const int pos0 = j * kTile + warp * 16 + (lane & 3) * 2;   // + 8 n + {0, 1}
+      const int pos0 = j * tpos + p0 + (lane & 3) * 2;   // + 8 n + {0, 1}
       const unsigned char* tr = there[cur] + warp * 16 + (lane & 3) * 2;
       const uint32_t th = (uint32_t)*reinterpret_cast<const uint16_t*>(tr) |
                           ((uint32_t)*reinterpret_cast<const uint16_t*>(tr + 8) << 16);
@@ -258,112 +268,113 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
         }
       }
     }
-    // ---- join the warps' parts: maxima and sums, then the values through
-    // shared memory of their own
-    __shared__ float sml[kWarps][MT * 16][2];
-    __shared__ float so[MT * 16][D + 4];
+    // ---- the row sums over the quad, then the warps of one head join: those
+    // behind the head's first one leave their part in shared memory, in turn
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        float t = l[mt][half];
-        t += __shfl_xor_sync(0xffffffffu, t, 1);
-        t += __shfl_xor_sync(0xffffffffu, t, 2);
-        if ((lane & 3) == 0) {
-          sml[warp][mt * 16 + half * 8 + (lane >> 2)][0] = m[mt][half];
-          sml[warp][mt * 16 + half * 8 + (lane >> 2)][1] = t;
-        }
+        l[mt][half] += __shfl_xor_sync(0xffffffffu, l[mt][half], 1);
+        l[mt][half] += __shfl_xor_sync(0xffffffffu, l[mt][half], 2);
       }
-    __syncthreads();
-    float mj[MT][2], lj2[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int r = mt * 16 + half * 8 + (lane >> 2);
-        float mm = -INFINITY, ll = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sml[w][r][0]);
-        const float base = mm == -INFINITY ? 0.0f : mm;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) ll = fmaf(ex2(sml[w][r][0] - base), sml[w][r][1], ll);
-        mj[mt][half] = mm;
-        lj2[mt][half] = ll;
-        const float f = ex2(m[mt][half] - base);
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          o[mt][n][half * 2] *= f;
-          o[mt][n][half * 2 + 1] *= f;
-        }
-      }
+    const int per = kWarps >> hw_shift;              // warps of a head
+    if (!kQRegs && per > 1) __syncthreads();         // every warp is done with its Q
 #pragma unroll 1
-    for (int w = 0; w < kWarps; ++w) {
-      if (warp == w) {
+    for (int w = 1; w < per; ++w) {
+      float* const so = join + (warp / per) * (MT * 16 * (D + 4));
+      if (warp % per == w) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
+          for (int half = 0; half < 2; ++half) {
+            float* p = so + (mt * 16 + half * 8 + (lane >> 2)) * (D + 4) + (lane & 3) * 2;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+              *reinterpret_cast<float2*>(p + n * 8) =
+                  make_float2(o[mt][n][half * 2], o[mt][n][half * 2 + 1]);
+            if ((lane & 3) == 0) {
+              p[D] = m[mt][half];
+              p[D + 1] = l[mt][half];
+            }
+          }
+      }
+      __syncthreads();
+      if (warp % per == 0) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const float* row = so + (mt * 16 + half * 8 + (lane >> 2)) * (D + 4);
+            const float mo = row[D], lo = row[D + 1];
+            const float mm = fmaxf(m[mt][half], mo), base = mm == -INFINITY ? 0.0f : mm;
+            const float f = ex2(m[mt][half] - base), fo = ex2(mo - base);
+            m[mt][half] = mm;
+            l[mt][half] = fmaf(l[mt][half], f, lo * fo);
 #pragma unroll
             for (int n = 0; n < D / 8; ++n) {
-              float2* p = reinterpret_cast<float2*>(
-                  &so[mt * 16 + half * 8 + (lane >> 2)][n * 8 + (lane & 3) * 2]);
-              float2 v = make_float2(o[mt][n][half * 2], o[mt][n][half * 2 + 1]);
-              if (w > 0) {
-                const float2 t = *p;
-                v.x += t.x;
-                v.y += t.y;
-              }
-              *p = v;
+              const float2 v = *reinterpret_cast<const float2*>(row + n * 8 + (lane & 3) * 2);
+              o[mt][n][half * 2] = fmaf(o[mt][n][half * 2], f, v.x * fo);
+              o[mt][n][half * 2 + 1] = fmaf(o[mt][n][half * 2 + 1], f, v.y * fo);
             }
-        if (w == 0 && (lane & 3) == 0)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              so[mt * 16 + half * 8 + (lane >> 2)][D] = mj[mt][half];
-              so[mt * 16 + half * 8 + (lane >> 2)][D + 1] = lj2[mt][half];
-            }
+          }
       }
       __syncthreads();
     }
-    if (sg.len >= 0) {
-      if (sg.whole) {
-        for (int i = tid; i < rows * (D / 2); i += kThreads) {
-          const int r = i / (D / 2), c = i % (D / 2) * 2;
-          const float ll = so[r][D + 1], inv = ll > 0.0f ? 1.0f / ll : 0.0f;
-          *reinterpret_cast<uint32_t*>(
-              a.out + (((int64_t)sg.b * a.q_len + (r0 + r) / a.G) * a.out_rs +
-                       (int64_t)(hkv * a.G + (r0 + r) % a.G) * D + c) * 2) =
-              pack_bf16x2(so[r][c] * inv, so[r][c + 1] * inv);
-        }
-        if (a.lse && tid < rows)
-          a.lse[((int64_t)sg.b * a.q_len + (r0 + tid) / a.G) * a.Hq + hkv * a.G +
-                (r0 + tid) % a.G] =
-              so[tid][D + 1] > 0.0f ? so[tid][D] * 0.6931471805599453f + logf(so[tid][D + 1])
-                                    : -INFINITY;
-      } else {
-        float* part = attn_part(a, sg, D);
-        for (int i = tid; i < rows * D; i += kThreads)
-          part[i / D * (D + 2) + i % D] = so[i / D][i % D];
-        if (tid < rows) {
-          part[tid * (D + 2) + D] = so[tid][D] * 0.6931471805599453f;   // natural logarithm
-          part[tid * (D + 2) + D + 1] = so[tid][D + 1];
+    if (sg.len < 0 || warp % per != 0) continue;
+    float* const part = attn_part(a, sg, D) + (warp / per) * (MT * 16) * (D + 2);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int r = mt * 16 + half * 8 + (lane >> 2), c = (lane & 3) * 2;
+        if (r >= rows) continue;
+        const float ll = l[mt][half], mn = m[mt][half] * 0.6931471805599453f;   // natural
+        if (sg.whole) {
+          const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+          const int64_t tok = (int64_t)sg.b * a.q_len + (r0 + r) / a.G;
+          const int h = hkv * a.G + (r0 + r) % a.G;
+          char* p = a.out + (tok * a.out_rs + (int64_t)h * D + c) * 2;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n)
+            *reinterpret_cast<uint32_t*>(p + n * 16) =
+                pack_bf16x2(o[mt][n][half * 2] * inv, o[mt][n][half * 2 + 1] * inv);
+          if (a.lse && c == 0) a.lse[tok * a.Hq + h] = ll > 0.0f ? mn + logf(ll) : -INFINITY;
+        } else {
+          float* p = part + r * (D + 2);
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n)
+            *reinterpret_cast<float2*>(p + n * 8 + c) =
+                make_float2(o[mt][n][half * 2], o[mt][n][half * 2 + 1]);
+          if (c == 0) {
+            p[D] = mn;
+            p[D + 1] = ll;
+          }
         }
       }
-    }
-    __syncthreads();
   }
   cp_async_wait<0>();
 }
 
+static_assert(kTile == 16 * kWarps, "a warp takes 16 rows");
+
+// Ring, and behind it the joins (none with a head a warp) or the warps' Q.
+template <int D, int MT>
+int smem_bytes(int hw) {
+  const int join = (hw == 4 ? 0 : hw) * MT * 16 * (D + 4) * 4;
+  const int q = MT * D <= 128 ? 0 : kWarps * MT * 16 * D * 2;
+  return Cfg<D>::kRing + std::max(join, q);
+}
+
 template <int D, int MT>
 cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
+  const int smem = smem_bytes<D, MT>(a.hw);
   const cudaError_t e = cudaFuncSetAttribute(
-      attn_mma_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+      attn_mma_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  attn_mma_kernel<D, MT><<<grid, kThreads, Cfg<D>::kSmem, st>>>(a);
+  attn_mma_kernel<D, MT><<<grid, kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
+
 }  // namespace
 
 cudaError_t attn_launch_mma(const AttnArgs& a, int D, int grid, cudaStream_t st) {
