@@ -8,19 +8,24 @@
 // are, keeps the softmax in the registers of the warp that made the scores, and
 // the tensor pipe is mostly idle either way.
 //
-// A block of 4 warps keeps a ring of tiles of K and V in shared memory, filled
-// by cp.async (16 bytes a request, rows swizzled by 16-byte unit so that
-// ldmatrix meets no bank conflict), several tiles ahead. A tile is 64 rows: 64 /
-// hw positions of hw kv heads, since the heads of a token lie side by side in
-// the usual cache and one head alone would take 256 bytes of every kilobyte
-// (3.96 TB/s so, against @HW@ with four heads together). Each warp takes 16
-// rows, of one head: scores = Q K^T, running maximum and sum of its own, weights
-// to bf16 in registers (the score layout of one product is the weight layout of
-// the next), weighted values += P V. No barrier between warps but the ring's;
-// warps of one head join their parts once per segment, through shared memory.
+// A block of 4 warps keeps a ring of tiles of K and V in shared memory, several
+// tiles ahead. A tile is 64 rows: 64 / hw positions of hw kv heads, since the
+// heads of a token lie side by side in the usual cache: a position then comes in
+// one bulk copy of hw * D values (else in hw of D values), a copy a thread. The
+// copies cost a handful of instructions a tile; the first form, per-thread
+// 16-byte copies of swizzled rows, took two thirds of the kernel's instructions
+// and held it at 4.2 TB/s. Positions are 16 bytes further apart than their
+// length, so that ldmatrix meets no bank conflict. Each warp takes 16 rows, of
+// one head: scores = Q K^T, running maximum and sum of its own, weights to bf16
+// in registers (the score layout of one product is the weight layout of the
+// next), weighted values += P V. No barrier between warps but the ring's; warps
+// of one head join their parts once per segment, through shared memory.
 //
-// Positions of a tile that lie behind the length or on a bad page are filled
-// with zeros and masked.
+// V of positions that lie behind the length or on a bad page is filled with
+// zeros; their scores are masked, as are those that a draft token's row does not
+// see. A tile that every row sees whole skips the masks, and sums are rescaled
+// only when a maximum has risen.
+#include "async.cuh"
 #include "attn_decode.cuh"
 
 #include <math.h>
@@ -32,20 +37,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 64;           // rows of a tile (positions x heads); 16 a warp
 
-template <int D>
-struct Cfg {
-  static constexpr int kRowBytes = D * 2;
-  static constexpr int kUnits = D / 8;                       // 16-byte units a row
-  static constexpr int kTileBytes = kTile * kRowBytes;       // K or V of a tile
-  static constexpr int kStages = D == 64 ? 4 : 3;
-  static constexpr int kRing = kStages * 2 * kTileBytes;
-};
-
-// Byte of 16-byte unit u of row r: units are permuted within groups of eight.
-template <int D>
-__device__ __forceinline__ uint32_t at(int r, int u) {
-  return (uint32_t)(r * Cfg<D>::kRowBytes + ((u ^ (r & 7)) << 4));
-}
+constexpr int kMaxStages = 4;
+constexpr long long kWaitClocks = 4000000000LL;   // seconds; a copy takes microseconds
 
 __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -72,73 +65,99 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Bounded wait of a whole warp.
+__device__ __forceinline__ bool wait_full(uint64_t* bar, int phase, int32_t* err) {
+  long long t0 = 0;
+#pragma unroll 1
+  for (uint32_t it = 1; !__any_sync(0xffffffffu, mbar_try(bar, phase)); ++it) {
+    if ((it & 255u) == 0) {
+      const long long now = clock64();
+      if (t0 == 0) t0 = now;
+      if (__any_sync(0xffffffffu, now - t0 > kWaitClocks)) {
+        flag_error(err, CCONV_DERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
 // MT row tiles of 16. Q stays in registers where it fits beside the sums, else
-// in shared memory (swizzled like K).
+// in shared memory.
 template <int D, int MT>
-__global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
-  using C = Cfg<D>;
-  constexpr bool kQRegs = MT * D <= 128;
+__global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, const int stages) {
+  constexpr bool kQRegs = MT == 1;
+  constexpr int kQPitch = D * 2 + 16;
   extern __shared__ __align__(128) unsigned char attn_dyn[];
   __shared__ int64_t scan[kThreads + 4];
-  __shared__ __align__(4) unsigned char there[C::kStages][kTile];   // positions that hold a token
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ __align__(16) unsigned char there[kMaxStages][kTile];   // positions that hold a token
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t smem = smem_addr(attn_dyn);
-  // behind the ring: the joins of at most two heads, or the warps' own Q before
-  float* const join = reinterpret_cast<float*>(attn_dyn + C::kRing);
-  unsigned char* const sq = attn_dyn + C::kRing + warp * (MT * 16 * D * 2);
-  AttnRun run;
+  const uint32_t pitch = a.hw * D * 2 + 16;
   const int hw_shift = a.hw == 4 ? 2 : a.hw >> 1, tpos = kTile >> hw_shift;   // positions a tile
+  const uint32_t half_stage = tpos * pitch;     // K, then V
+  // behind the ring: the joins of at most two heads, or the warps' own Q before
+  unsigned char* const behind = attn_dyn + stages * 2 * half_stage;
+  float* const join = reinterpret_cast<float*>(behind);
+  unsigned char* const sq = behind + warp * (MT * 16 * kQPitch);
+  if (tid == 0) {
+    for (int i = 0; i < kMaxStages; ++i) mbar_init(&full[i], kThreads);
+    fence_mbar_init();
+  }
+  AttnRun run;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!attn_split<kThreads>(a, tpos, scan, run)) return;
   const int rows_all = a.G * a.q_len;
   const float sl2 = a.scale * 1.4426950408889634f;
 
-  // ---- loads: thread tid copies unit tid % kUnits of rows tid / kUnits + ..
-  constexpr int kRowsAtOnce = kThreads / C::kUnits, kCopies = kTile / kRowsAtOnce;
+  // ---- loads: thread tid has the copies tid, tid + 128, .. of a tile: K and V of
+  // each position, whole or head by head
+  const bool joined = a.s_head == D;
+  const int pieces = joined ? 1 : a.hw, copies = 2 * tpos * pieces;
+  const uint32_t bytes = (joined ? a.hw : 1) * D * 2;
   AttnRun ld = run;               // the load side runs ahead of the compute side
   AttnSeg ls = attn_segment(a, tpos, ld);
   int lj = ls.j0;
   auto load_tile = [&](int stage) {
-    if (ld.p < ld.end) {
-      const uint32_t kb = smem + stage * 2 * C::kTileBytes, vb = kb + C::kTileBytes;
-      const int u = tid % C::kUnits, r0 = tid / C::kUnits;
-      const int hkv0 = ls.unit / a.rblocks * a.hw;
-      const int32_t* tab = a.table + (int64_t)ls.b * a.table_rs;
-#pragma unroll
-      for (int i = 0; i < kCopies; ++i) {
-        // copies in the order of the cache: position by position, its heads
-        const int k = r0 + i * kRowsAtOnce, hl = k & (a.hw - 1), pl = k >> hw_shift;
-        const int r = hl * tpos + pl, pos = lj * tpos + pl;
-        int page = -1;
-        if (pos < ls.len) {
-          page = tab[a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size];
-          if (page < 0 || page >= a.num_pages) {
-            flag_error(a.dev_err, CCONV_DERR_PAGE);
-            page = -1;
-          }
+    if (ld.p >= ld.end) return;
+    unsigned char* const kb = attn_dyn + stage * 2 * half_stage;
+    const int32_t* tab = a.table + (int64_t)ls.b * a.table_rs;
+    for (int c = tid; c < copies; c += kThreads) {
+      const int isv = c & 1, pl = (c >> 1) / pieces, piece = (c >> 1) - pl * pieces;
+      const int pos = lj * tpos + pl;
+      int page = -1;
+      if (pos < ls.len) {
+        page = tab[a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size];
+        if (page < 0 || page >= a.num_pages) {
+          flag_error(a.dev_err, CCONV_DERR_PAGE);
+          page = -1;
         }
-        const bool in = page >= 0;
-        const int tok = a.page_shift >= 0 ? pos & (a.page_size - 1) : pos % a.page_size;
-        const int64_t off = in ? ((int64_t)page * a.s_page + (int64_t)tok * a.s_tok +
-                                  (int64_t)(hkv0 + hl) * a.s_head + u * 8) * 2
-                               : 0;
-        if (u == 0) there[stage][r] = in;
-        cp_async16(kb + at<D>(r, u), a.kc + off, in);
-        cp_async16(vb + at<D>(r, u), a.vc + off, in);
       }
-      if (++lj == ls.j1) {
-        attn_advance(a, ls, ld);
-        if (ld.p < ld.end) {
-          ls = attn_segment(a, tpos, ld);
-          lj = ls.j0;
-        }
+      unsigned char* const dst = kb + isv * half_stage + pl * pitch + piece * (D * 2);
+      if (isv == 0 && piece == 0) there[stage][pl] = page >= 0;
+      if (page >= 0) {
+        const int tok = a.page_shift >= 0 ? pos & (a.page_size - 1) : pos % a.page_size;
+        const int64_t off = ((int64_t)page * a.s_page + (int64_t)tok * a.s_tok +
+                             (int64_t)(ls.unit / a.rblocks * a.hw + piece) * a.s_head) * 2;
+        mbar_expect(&full[stage], bytes);
+        bulk_load(dst, (isv ? a.vc : a.kc) + off, bytes, &full[stage]);
+      } else if (isv) {
+        for (uint32_t i = 0; i < bytes; i += 16)
+          *reinterpret_cast<uint4*>(dst + i) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async();      // before a later copy into the same place
       }
     }
-    cp_async_commit();
+    mbar_arrive(&full[stage]);
+    if (++lj == ls.j1) {
+      attn_advance(a, ls, ld);
+      if (ld.p < ld.end) {
+        ls = attn_segment(a, tpos, ld);
+        lj = ls.j0;
+      }
+    }
   };
-#pragma unroll
-  for (int s = 0; s < C::kStages - 1; ++s) load_tile(s);
-  int stage = 0;
+  for (int s = 0; s < stages - 1; ++s) load_tile(s);
+  int stage = 0, phase = 0;
 
   while (run.p < run.end) {
     const AttnSeg sg = attn_segment(a, tpos, run);
@@ -148,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
     }
     attn_advance(a, sg, run);
     // the warp's head and its first position of a tile
-    const int hkv = sg.unit / a.rblocks * a.hw + warp * 16 / tpos;
+    const int hl = warp * 16 / tpos, hkv = sg.unit / a.rblocks * a.hw + hl;
     const int p0 = warp * 16 % tpos, r0 = sg.unit % a.rblocks * (MT * 16);
     const int rows = min(MT * 16, rows_all - r0);
     // ---- Q as left operands: row r is token (r0 + r) / G, head hkv * G + (r0 + r) % G
@@ -174,10 +193,10 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
                   in ? *reinterpret_cast<const uint32_t*>(p + (ks * 16 + e * 8) * 2) : 0u;
         }
     } else {
-      for (int i = lane; i < MT * 16 * C::kUnits; i += 32) {
-        const int r = i / C::kUnits, u = i % C::kUnits;
+      for (int i = lane; i < MT * 16 * (D / 8); i += 32) {
+        const int r = i / (D / 8), u = i % (D / 8);
         const bool in = r < rows && sg.len > 0;
-        *reinterpret_cast<uint4*>(sq + at<D>(r, u)) =
+        *reinterpret_cast<uint4*>(sq + r * kQPitch + u * 16) =
             in ? ldg16(q_row(r) + u * 16) : make_uint4(0u, 0u, 0u, 0u);
       }
       __syncwarp();
@@ -191,19 +210,22 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
       for (int n = 0; n < D / 8; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.0f;
     }
     for (int j = sg.j0; j < sg.j1; ++j) {
-      cp_async_wait<C::kStages - 2>();
-      __syncthreads();                 // the tile is there; the oldest one has been read
-      load_tile((stage + C::kStages - 1) % C::kStages);
-      const uint32_t kb = smem + stage * 2 * C::kTileBytes, vb = kb + C::kTileBytes;
-      const int cur = stage;
-      stage = (stage + 1) % C::kStages;
+      // the tile is there; the one before it has been read by all
+      if (!wait_full(&full[stage], phase, a.dev_err)) return;
+      __syncthreads();
+      load_tile(stage == 0 ? stages - 1 : stage - 1);
+      const uint32_t kb = smem_addr(attn_dyn) + stage * 2 * half_stage + p0 * pitch + hl * (D * 2);
+      const uint32_t vb = kb + half_stage;
+      const unsigned char* tr = there[stage] + p0;
+      if (++stage == stages) stage = 0, phase ^= 1;
       // ---- scores of the warp's 16 positions: two n-tiles of 8
       float s[MT][2][4] = {};
-      const int kr = warp * 16 + (lane & 7) + ((lane >> 4) << 3), ku = (lane >> 3) & 1;
+      const uint32_t ka =
+          kb + ((lane & 7) + ((lane >> 4) << 3)) * pitch + ((lane >> 3) & 1) * 16;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         uint32_t b[4];                 // positions 0-7: k 0-7, k 8-15; positions 8-15: the same
-        ldm4(b, kb + at<D>(kr, ks * 2 + ku));
+        ldm4(b, ka + ks * 32);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           if constexpr (kQRegs) {
@@ -211,58 +233,71 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
             mma(s[mt][1], q[mt][ks], b[2], b[3]);
           } else {
             uint32_t qa[4];
-            ldm4(qa, smem_addr(sq) + at<D>(mt * 16 + (lane & 15), ks * 2 + (lane >> 4)));
+            ldm4(qa, smem_addr(sq) + (mt * 16 + (lane & 15)) * kQPitch + ks * 32 + (lane >> 4) * 16);
             mma(s[mt][0], qa, b[0], b[1]);
             mma(s[mt][1], qa, b[2], b[3]);
           }
         }
       }
-      // ---- mask, running maximum, weights
-      const int pos0 = j * tpos + p0 + (lane & 3) * 2;   // + 8 n + {0, 1}
-      const unsigned char* tr = there[cur] + warp * 16 + (lane & 3) * 2;
-      const uint32_t th = (uint32_t)*reinterpret_cast<const uint16_t*>(tr) |
-                          ((uint32_t)*reinterpret_cast<const uint16_t*>(tr + 8) << 16);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[mt][i >> 2][i & 3] *= sl2;
+      // ---- masks, running maximum, weights
+      const int pos0 = j * tpos + p0;              // the warp's first position
+      const uint4 all = *reinterpret_cast<const uint4*>(tr);
+      if (pos0 + 15 > sg.len - a.q_len ||
+          (all.x & all.y & all.z & all.w) != 0x01010101u) {
+        const int q0 = (lane & 3) * 2;             // + 8 n + {0, 1}
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int r = mt * 16 + half * 8 + (lane >> 2);
+            const int seen = r < rows ? sg.len - a.q_len + 1 + (r0 + r) / a.G : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int q = q0 + (i >> 1) * 8 + (i & 1);
+              if (!tr[q] || pos0 + q >= seen) s[mt][i >> 1][half * 2 + (i & 1)] = -INFINITY;
+            }
+          }
+      }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         uint32_t pw[4];
+        float corr[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int r = mt * 16 + half * 8 + (lane >> 2);
-          const int seen = r < rows ? sg.len - a.q_len + 1 + (r0 + r) / a.G : 0;
-          float x[4], mx = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int pos = pos0 + (i >> 1) * 8 + (i & 1);
-            x[i] = ((th >> (i * 8)) & 1u) && pos < seen ? sl2 * s[mt][i >> 1][half * 2 + (i & 1)]
-                                                     : -INFINITY;
-            mx = fmaxf(mx, x[i]);
-          }
+          const float s0 = s[mt][0][half * 2], s1 = s[mt][0][half * 2 + 1],
+                      s2 = s[mt][1][half * 2], s3 = s[mt][1][half * 2 + 1];
+          float mx = fmaxf(fmaxf(s0, s1), fmaxf(s2, s3));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           const float mn = fmaxf(m[mt][half], mx);
           const float base = mn == -INFINITY ? 0.0f : mn;
-          const float corr = ex2(m[mt][half] - base);
+          corr[half] = ex2(m[mt][half] - base);
           m[mt][half] = mn;
-          float sum = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = ex2(x[i] - base);
-            sum += x[i];
-          }
-          l[mt][half] = fmaf(l[mt][half], corr, sum);
-          pw[half] = pack_bf16x2(x[0], x[1]);
-          pw[2 + half] = pack_bf16x2(x[2], x[3]);
+          const float x0 = ex2(s0 - base), x1 = ex2(s1 - base), x2 = ex2(s2 - base),
+                      x3 = ex2(s3 - base);
+          l[mt][half] = fmaf(l[mt][half], corr[half], (x0 + x1) + (x2 + x3));
+          pw[half] = pack_bf16x2(x0, x1);
+          pw[2 + half] = pack_bf16x2(x2, x3);
+        }
+        if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
 #pragma unroll
           for (int n = 0; n < D / 8; ++n) {
-            o[mt][n][half * 2] *= corr;
-            o[mt][n][half * 2 + 1] *= corr;
+            o[mt][n][0] *= corr[0];
+            o[mt][n][1] *= corr[0];
+            o[mt][n][2] *= corr[1];
+            o[mt][n][3] *= corr[1];
           }
         }
         // ---- weighted values
+        const uint32_t va = vb + (lane & 15) * pitch + (lane >> 4) * 16;
 #pragma unroll
         for (int n = 0; n < D / 16; ++n) {
           uint32_t b[4];               // dims 0-7: positions 0-7, 8-15; dims 8-15: the same
-          ldm4t(b, vb + at<D>(warp * 16 + (lane & 15), n * 2 + (lane >> 4)));
+          ldm4t(b, va + n * 32);
           mma(o[mt][2 * n], pw, b[0], b[1]);
           mma(o[mt][2 * n + 1], pw, b[2], b[3]);
         }
@@ -352,26 +387,23 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
         }
       }
   }
-  cp_async_wait<0>();
 }
 
 static_assert(kTile == 16 * kWarps, "a warp takes 16 rows");
 
-// Ring, and behind it the joins (none with a head a warp) or the warps' Q.
-template <int D, int MT>
-int smem_bytes(int hw) {
-  const int join = (hw == 4 ? 0 : hw) * MT * 16 * (D + 4) * 4;
-  const int q = MT * D <= 128 ? 0 : kWarps * MT * 16 * D * 2;
-  return Cfg<D>::kRing + std::max(join, q);
-}
-
 template <int D, int MT>
 cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
-  const int smem = smem_bytes<D, MT>(a.hw);
+  // the ring, and behind it the joins (none with a head a warp) or the warps' Q
+  const int stage = 2 * kTile / a.hw * (a.hw * D * 2 + 16);
+  const int join = (a.hw == 4 ? 0 : a.hw) * MT * 16 * (D + 4) * 4;
+  const int q = MT == 1 ? 0 : kWarps * MT * 16 * (D * 2 + 16);
+  int stages = D == 64 ? 4 : 3;
+  while (stages > 2 && stages * stage + std::max(join, q) > 224 * 1024) --stages;
+  const int smem = stages * stage + std::max(join, q);
   const cudaError_t e = cudaFuncSetAttribute(
       attn_mma_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  attn_mma_kernel<D, MT><<<grid, kThreads, smem, st>>>(a);
+  attn_mma_kernel<D, MT><<<grid, kThreads, smem, st>>>(a, stages);
   return cudaGetLastError();
 }
 
