@@ -188,18 +188,19 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const AttnArgs a) {
   }
 }
 
-// Joins the parts of a cut unit, one block a row of a unit. Part i (block c0 +
-// i) is slot 1 of block c0 and slot 0 of the others. The threads first turn the
-// parts' maxima and sums into weights, then take a column each and every
-// kGroups-th part, sixteen loads in flight. (It is launched to overlap the end
-// of the kernel before, whose results it waits for.) Few units have many parts
-// each and get 512 threads a row, many units few parts and 256.
-template <typename T, int D, int kJoinThreads>
+// Joins the parts of a cut unit, one block a row of a unit and CC of its columns.
+// Part i (block c0 + i) is slot 1 of block c0 and slot 0 of the others. The
+// threads first turn the parts' maxima and sums into weights, then take a column
+// each and every kGroups-th part, with many loads in flight. (It is launched to
+// overlap the end of the kernel before, whose results it waits for.) A few units
+// have many parts each -- one long context has one of every block -- and get 16
+// groups of 32 columns; many units have few and get whole rows.
+template <typename T, int D, int CC, int kJoinThreads>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
-  constexpr int kGroups = kJoinThreads / D;
+  constexpr int kGroups = kJoinThreads / CC;
   __shared__ float wt[kMaxGrid];
   __shared__ float red[2][kJoinThreads / 32];
-  __shared__ float sums[kGroups][D];
+  __shared__ float sums[kGroups][CC];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int rows = a.hw * a.rows, used = min(a.rows, a.G * a.q_len);
   const int64_t bu = blockIdx.x;                    // request and unit
@@ -240,15 +241,15 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   l = 0.0f;
 #pragma unroll
   for (int w = 0; w < kJoinThreads / 32; ++w) l += red[1][w];
-  const int c = tid % D, g = tid / D;
+  const int cl = tid % CC, g = tid / CC, c = blockIdx.z * CC + cl;
   float acc = 0.0f;
-#pragma unroll 16
+#pragma unroll 10
   for (int i = g; i < parts; i += kGroups) acc = fmaf(wt[i], part(i)[c], acc);
-  sums[g][c] = acc;
+  sums[g][cl] = acc;
   __syncthreads();
   if (g > 0) return;
 #pragma unroll
-  for (int k = 1; k < kGroups; ++k) acc += sums[k][c];
+  for (int k = 1; k < kGroups; ++k) acc += sums[k][cl];
   const int64_t orow = (int64_t)b * a.q_len + rr / a.G;
   const int h = hkv * a.G + rr % a.G;
   const auto raw = f32_to_raw<T>(l > 0.0f ? acc / l : 0.0f);
@@ -261,7 +262,8 @@ template <typename T, int D>
 cudaError_t launch_join(const AttnArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.B * a.units), (unsigned)(a.hw * std::min(a.rows, a.G * a.q_len)));
-  const bool few = (int64_t)cfg.gridDim.x * cfg.gridDim.y <= 1024;
+  const bool few = (int64_t)cfg.gridDim.x * cfg.gridDim.y <= 512;
+  cfg.gridDim.z = few ? D / 32 : 1;
   cfg.blockDim = dim3(few ? 512 : 256);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -269,8 +271,8 @@ cudaError_t launch_join(const AttnArgs& a, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D, 512>, a)
-             : cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D, 256>, a);
+  return few ? cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D, 32, 512>, a)
+             : cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D, D, 256>, a);
 }
 
 template <typename T, int D>

@@ -61,8 +61,8 @@ struct AttnRun {
   int64_t before;       // tiles (of one unit) of the requests before b
 };
 
-// Splits the line over the grid. Every thread of the block calls it (a power
-// of two of at most 256 threads); `sm` is shared scratch. Each thread counts a
+// Splits the line over the grid. Every thread of the block calls it; `sm` is
+// shared scratch. Each thread counts a
 // run of requests, and a scan over the threads places the block's start.
 template <int THREADS>
 __device__ __forceinline__ bool attn_split(const AttnArgs& a, int tile, int64_t (&sm)[THREADS + 4],

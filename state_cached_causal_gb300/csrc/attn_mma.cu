@@ -34,7 +34,7 @@ namespace cconv {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kThreads = (kWarps + 1) * 32;   // and one warp that loads
 constexpr int kTile = 64;           // rows of a tile (positions x heads); 16 a warp
 
 constexpr int kMaxStages = 4;
@@ -65,8 +65,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The warps that compute, among themselves.
+__device__ __forceinline__ void warps_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+}
 // Bounded wait of a whole warp.
-__device__ __forceinline__ bool wait_full(uint64_t* bar, int phase, int32_t* err) {
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, int phase, int32_t* err) {
   long long t0 = 0;
 #pragma unroll 1
   for (uint32_t it = 1; !__any_sync(0xffffffffu, mbar_try(bar, phase)); ++it) {
@@ -90,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
   constexpr int kQPitch = D * 2 + 16;
   extern __shared__ __align__(128) unsigned char attn_dyn[];
   __shared__ int64_t scan[kThreads + 4];
-  __shared__ uint64_t full[kMaxStages];
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
   __shared__ __align__(16) unsigned char there[kMaxStages][kTile];   // positions that hold a token
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t pitch = a.hw * D * 2 + 16;
@@ -101,7 +105,10 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
   float* const join = reinterpret_cast<float*>(behind);
   unsigned char* const sq = behind + warp * (MT * 16 * kQPitch);
   if (tid == 0) {
-    for (int i = 0; i < kMaxStages; ++i) mbar_init(&full[i], kThreads);
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kWarps);
+    }
     fence_mbar_init();
   }
   AttnRun run;
@@ -110,53 +117,58 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
   const int rows_all = a.G * a.q_len;
   const float sl2 = a.scale * 1.4426950408889634f;
 
-  // ---- loads: thread tid has the copies tid, tid + 128, .. of a tile: K and V of
-  // each position, whole or head by head
-  const bool joined = a.s_head == D;
-  const int pieces = joined ? 1 : a.hw, copies = 2 * tpos * pieces;
-  const uint32_t bytes = (joined ? a.hw : 1) * D * 2;
-  AttnRun ld = run;               // the load side runs ahead of the compute side
-  AttnSeg ls = attn_segment(a, tpos, ld);
-  int lj = ls.j0;
-  auto load_tile = [&](int stage) {
-    if (ld.p >= ld.end) return;
-    unsigned char* const kb = attn_dyn + stage * 2 * half_stage;
-    const int32_t* tab = a.table + (int64_t)ls.b * a.table_rs;
-    for (int c = tid; c < copies; c += kThreads) {
-      const int isv = c & 1, pl = (c >> 1) / pieces, piece = (c >> 1) - pl * pieces;
-      const int pos = lj * tpos + pl;
-      int page = -1;
-      if (pos < ls.len) {
-        page = tab[a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size];
-        if (page < 0 || page >= a.num_pages) {
-          flag_error(a.dev_err, CCONV_DERR_PAGE);
-          page = -1;
+  if (warp == kWarps) {
+    // ---- loads: lane l has the copies l, l + 32, .. of a tile: K and V of each
+    // position, whole or head by head. The pages of the next tile are looked up
+    // before the wait for its place.
+    const bool joined = a.s_head == D;
+    const int pieces = joined ? 1 : a.hw, copies = 2 * tpos * pieces;
+    const uint32_t bytes = (joined ? a.hw : 1) * D * 2;
+    int st = 0, ph = 1;               // (the first round's places are free)
+    while (run.p < run.end) {
+      const AttnSeg s = attn_segment(a, tpos, run);
+      attn_advance(a, s, run);
+      const int32_t* tab = a.table + (int64_t)s.b * a.table_rs;
+      const int64_t head = (int64_t)(s.unit / a.rblocks * a.hw) * a.s_head;
+      for (int j = s.j0; j < s.j1; ++j) {
+        unsigned char* const kb = attn_dyn + st * 2 * half_stage;
+        bool waited = false;
+        for (int c0 = 0; c0 < copies; c0 += 32) {
+          const int c = c0 + lane, isv = c & 1, pl = (c >> 1) / pieces,
+                    piece = (c >> 1) - pl * pieces;
+          const int pos = j * tpos + pl;
+          int page = -1;
+          if (c < copies && pos < s.len) {
+            page = tab[a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size];
+            if (page < 0 || page >= a.num_pages) {
+              flag_error(a.dev_err, CCONV_DERR_PAGE);
+              page = -1;
+            }
+          }
+          const int tok = a.page_shift >= 0 ? pos & (a.page_size - 1) : pos % a.page_size;
+          const int64_t off = (page * a.s_page + tok * a.s_tok + head + piece * a.s_head) * 2;
+          if (!waited && !wait_bar(&empty[st], ph, a.dev_err)) return;
+          waited = true;
+          if (c < copies) {
+            unsigned char* const dst = kb + isv * half_stage + pl * pitch + piece * (D * 2);
+            if (isv == 0 && piece == 0) there[st][pl] = page >= 0;
+            if (page >= 0) {
+              mbar_expect(&full[st], bytes);
+              bulk_load(dst, (isv ? a.vc : a.kc) + off, bytes, &full[st]);
+            } else if (isv) {
+              for (uint32_t i = 0; i < bytes; i += 16)
+                *reinterpret_cast<uint4*>(dst + i) = make_uint4(0u, 0u, 0u, 0u);
+              fence_proxy_async();      // before a later copy into the same place
+            }
+          }
         }
-      }
-      unsigned char* const dst = kb + isv * half_stage + pl * pitch + piece * (D * 2);
-      if (isv == 0 && piece == 0) there[stage][pl] = page >= 0;
-      if (page >= 0) {
-        const int tok = a.page_shift >= 0 ? pos & (a.page_size - 1) : pos % a.page_size;
-        const int64_t off = ((int64_t)page * a.s_page + (int64_t)tok * a.s_tok +
-                             (int64_t)(ls.unit / a.rblocks * a.hw + piece) * a.s_head) * 2;
-        mbar_expect(&full[stage], bytes);
-        bulk_load(dst, (isv ? a.vc : a.kc) + off, bytes, &full[stage]);
-      } else if (isv) {
-        for (uint32_t i = 0; i < bytes; i += 16)
-          *reinterpret_cast<uint4*>(dst + i) = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async();      // before a later copy into the same place
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+        if (++st == stages) st = 0, ph ^= 1;
       }
     }
-    mbar_arrive(&full[stage]);
-    if (++lj == ls.j1) {
-      attn_advance(a, ls, ld);
-      if (ld.p < ld.end) {
-        ls = attn_segment(a, tpos, ld);
-        lj = ls.j0;
-      }
-    }
-  };
-  for (int s = 0; s < stages - 1; ++s) load_tile(s);
+    return;
+  }
   int stage = 0, phase = 0;
 
   while (run.p < run.end) {
@@ -210,13 +222,11 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
       for (int n = 0; n < D / 8; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.0f;
     }
     for (int j = sg.j0; j < sg.j1; ++j) {
-      // the tile is there; the one before it has been read by all
-      if (!wait_full(&full[stage], phase, a.dev_err)) return;
-      __syncthreads();
-      load_tile(stage == 0 ? stages - 1 : stage - 1);
+      if (!wait_bar(&full[stage], phase, a.dev_err)) return;
       const uint32_t kb = smem_addr(attn_dyn) + stage * 2 * half_stage + p0 * pitch + hl * (D * 2);
       const uint32_t vb = kb + half_stage;
       const unsigned char* tr = there[stage] + p0;
+      uint64_t* const read = &empty[stage];
       if (++stage == stages) stage = 0, phase ^= 1;
       // ---- scores of the warp's 16 positions: two n-tiles of 8
       float s[MT][2][4] = {};
@@ -302,6 +312,8 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
           mma(o[mt][2 * n + 1], pw, b[2], b[3]);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(read);
     }
     // ---- the row sums over the quad, then the warps of one head join: those
     // behind the head's first one leave their part in shared memory, in turn
@@ -313,7 +325,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
         l[mt][half] += __shfl_xor_sync(0xffffffffu, l[mt][half], 2);
       }
     const int per = kWarps >> hw_shift;              // warps of a head
-    if (!kQRegs && per > 1) __syncthreads();         // every warp is done with its Q
+    if (!kQRegs && per > 1) warps_sync();         // every warp is done with its Q
 #pragma unroll 1
     for (int w = 1; w < per; ++w) {
       float* const so = join + (warp / per) * (MT * 16 * (D + 4));
@@ -333,7 +345,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
             }
           }
       }
-      __syncthreads();
+      warps_sync();
       if (warp % per == 0) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -353,7 +365,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
             }
           }
       }
-      __syncthreads();
+      warps_sync();
     }
     if (sg.len < 0 || warp % per != 0) continue;
     float* const part = attn_part(a, sg, D) + (warp / per) * (MT * 16) * (D + 2);
