@@ -565,7 +565,8 @@ typedef struct kv_cache {
  *                num_kv_heads * head_dim] with row strides (multiples of the
  *                16-byte vector); q_out like q (it may be q itself)
  *   q_weight, k_weight  [head_dim] of the call's dtype, or NULL
- *   cos_sin      fp32 [max_position, rot_dim] contiguous; positions int32
+ *   cos_sin      fp32 [max_position, rot_dim] contiguous, 16-byte aligned;
+ *                positions int32
  *   rot_dim      0..head_dim, even; when not interleaved a multiple of two
  *                16-byte vectors (16 bf16, 8 fp32)
  *   slot_mapping int32 [num_tokens], distinct; negative: a padding row, whose

@@ -2,19 +2,22 @@
 // position, and the write of k and v into the paged cache, in one pass.
 //
 // The pass reads every row once and writes every row once, with about 10
-// flops a value: it is bound by HBM. A head is a run of 16-byte units, one per
-// lane (LPH lanes a head, 32/LPH heads a warp at a time). A warp keeps one
-// token: its lanes hold the same columns of every head, so the token's cosines
-// and sines and the norm weights are loaded once into registers and serve all
-// its heads; heads go in groups of kUnroll whose loads are in flight together.
-// When there are few tokens a token's heads are spread over several warps.
+// flops a value: it is bound by HBM as long as the instructions around those
+// flops stay few. A lane holds two 16-byte units of a head, in the half-split
+// rotation unit u of the first half and unit u of the second, so that both
+// values of every rotated pair are in one lane (with one unit a lane the partner
+// came by shuffles, 8 for 8 values). A warp takes one token after the other: its
+// lanes hold the same columns of every head, so a token's cosines and sines, and
+// for all tokens the norm weights, are in registers and serve all heads. When
+// there are few tokens a token's heads are spread over several warps.
 #include "mixer.cuh"
 
 namespace cconv {
 namespace {
 
 constexpr int kNrThreads = 128;
-constexpr int kUnroll = 4;
+constexpr int kNrBlocks = 5;    // of an SM
+constexpr int kUnroll = 2;      // groups of heads whose loads are in flight together
 
 struct NrArgs {
   const char *q, *k, *v;
@@ -35,160 +38,173 @@ struct NrArgs {
   int32_t* dev_err;
 };
 
-// U units of a head per lane (2 when a head has more than 32 units).
 template <typename T, int D, bool PAIRS>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NrArgs a) {
+__global__ void __launch_bounds__(kNrThreads, kNrBlocks) norm_rope_kernel(const NrArgs a) {
   constexpr int V = Elem<T>::V, E = Elem<T>::bytes;
-  constexpr int UNITS = D / V;
-  constexpr int U = UNITS > 32 ? UNITS / 32 : 1;
-  constexpr int LPH = UNITS / U;              // lanes a head
+  constexpr int LPH = D / V / 2;              // lanes a head, two units each
   constexpr int HPW = 32 / LPH;               // heads a warp at a time
   const int lane = threadIdx.x & 31;
-  const int64_t wid = (int64_t)blockIdx.x * (kNrThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = wid / a.parts;
-  const int part = (int)(wid % a.parts);
-  if (t >= a.T) return;
-  const int pos = a.pos[t];
-  const int slot = a.slots[t];
-  if (pos < 0 || pos >= a.max_pos || slot >= a.num_slots) {
-    if (part == 0 && lane == 0) flag_error(a.dev_err, CCONV_DERR_POSITION);
-    return;
-  }
-  const int sub = lane / LPH, hl = lane % LPH;   // head of the group, lane of the head
-  // the lane's unit u holds columns u * LPH * V + hl * V + [0, V)
-  float c[U][V], s[U][V];
-  const int half = a.rot / 2;
-  const float* cs = a.cs + (int64_t)pos * a.rot;
+  const int wid = blockIdx.x * (kNrThreads / 32) + (threadIdx.x >> 5);
+  const int part = wid % a.parts;
+  const int step = gridDim.x * (kNrThreads / 32) / a.parts;   // tokens at a time
+  const int sub = lane / LPH, l = lane % LPH;    // head of the group, lane of the head
+  // columns [c0, c0 + V) and [c1, c1 + V): partners half a rotation apart, or
+  // neighbours where nothing is rotated (and in the interleaved rotation)
+  const int half = a.rot / 2, hu = PAIRS ? 0 : half / V;
+  // unit at column c of a weight vector (of any alignment)
+  auto load_w = [](const char* w, int c) {
+    float f[V];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
+    for (int e = 0; e < V; ++e) f[e] = load_f32<T>(w, c + e);
+    return pack16<T>(f);
+  };
+  const int c0 = (l < hu ? l : 2 * l) * V, c1 = (l < hu ? l + hu : 2 * l + 1) * V;
+  uint4 wq[2] = {}, wk[2] = {};   // the lane's norm weights
+  if (a.qw) wq[0] = load_w(a.qw, c0), wq[1] = load_w(a.qw, c1);
+  if (a.kw) wk[0] = load_w(a.kw, c0), wk[1] = load_w(a.kw, c1);
+  int t = wid / a.parts;
+  if (t >= step) return;        // (a last, incomplete row of warps)
+  int pos = t < a.T ? a.pos[t] : 0, slot = t < a.T ? a.slots[t] : 0;
+#pragma unroll 1
+  for (; t < a.T;) {
+  const int p = pos, sl = slot, tok = t;
+  t += step;
+  if (t < a.T) {                // the next token's, while this one is worked on
+    pos = a.pos[t];
+    slot = a.slots[t];
+  }
+  if (p < 0 || p >= a.max_pos || sl >= a.num_slots) {
+    if (part == 0 && lane == 0) flag_error(a.dev_err, CCONV_DERR_POSITION);
+    continue;
+  }
+  // factors of the lane's V pairs: (x0[e], x1[e]), or (x0[2i], x0[2i+1]) then
+  // (x1[2i], x1[2i+1])
+  float c[V], s[V];
+  const float* cs = a.cs + (int64_t)p * a.rot;
+  if constexpr (PAIRS) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const int col = (u * LPH + hl) * V + e;
-      c[u][e] = 1.0f;
-      s[u][e] = 0.0f;
-      if (col < a.rot) {
-        const int i = PAIRS ? col >> 1 : (col < half ? col : col - half);
-        const bool lo = PAIRS ? (col & 1) == 0 : col < half;
-        c[u][e] = __ldg(cs + i);
-        s[u][e] = lo ? -__ldg(cs + half + i) : __ldg(cs + half + i);
-      }
+      const int i = e < V / 2 ? c0 / 2 + e : c1 / 2 + e - V / 2;
+      const bool in = 2 * i < a.rot;
+      c[e] = in ? __ldg(cs + i) : 1.0f;
+      s[e] = in ? __ldg(cs + half + i) : 0.0f;
     }
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; e += 4) {
+      const float4 one = make_float4(1.f, 1.f, 1.f, 1.f), zero = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 x = l < hu ? __ldg(reinterpret_cast<const float4*>(cs + c0 + e)) : one;
+      const float4 y = l < hu ? __ldg(reinterpret_cast<const float4*>(cs + half + c0 + e)) : zero;
+      c[e] = x.x, c[e + 1] = x.y, c[e + 2] = x.z, c[e + 3] = x.w;
+      s[e] = y.x, s[e + 1] = y.y, s[e + 2] = y.z, s[e + 3] = y.w;
+    }
+  }
   char *kdst = nullptr, *vdst = nullptr;
-  if (slot >= 0) {
-    const int64_t page = slot / a.page_size, tok = slot % a.page_size;
-    const int64_t off = (page * a.s_page + tok * a.s_tok) * E;
+  if (sl >= 0) {
+    const int page = sl / a.page_size;
+    const int64_t off = (page * a.s_page + (int64_t)(sl - page * a.page_size) * a.s_tok) * E;
     kdst = a.kc + off;
     vdst = a.vc + off;
   }
-  // heads [0, Hq) of q, then Hkv of k (both normalised and rotated)
-  auto rotate_heads = [&](int h_begin, int h_end, const char* src, const char* w, char* dst,
-                          int64_t dst_head) {
-    float wt[U][V];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        wt[u][e] = w ? load_f32<T>(w, (u * LPH + hl) * V + e) : 1.0f;
+  auto rotate_heads = [&](int h_begin, int h_end, const char* src, const char* w,
+                          const uint4 (&wu)[2], char* dst, int64_t dst_head) {
+    float w0[V], w1[V];
+    unpack16<T>(wu[0], w0);
+    unpack16<T>(wu[1], w1);
+#pragma unroll 1
     for (int h0 = h_begin; h0 < h_end; h0 += HPW * kUnroll) {
-      uint4 raw[kUnroll][U];
+      uint4 r0[kUnroll], r1[kUnroll];
 #pragma unroll
       for (int j = 0; j < kUnroll; ++j) {
         const int h = h0 + j * HPW + sub;
-        if (h < h_end)
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            raw[j][u] = *reinterpret_cast<const uint4*>(
-                src + ((int64_t)h * D + (u * LPH + hl) * V) * E);
-        else
-#pragma unroll
-          for (int u = 0; u < U; ++u) raw[j][u] = make_uint4(0u, 0u, 0u, 0u);
+        r0[j] = r1[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (h < h_end) {
+          const char* p = src + (int64_t)h * (D * E);
+          r0[j] = *reinterpret_cast<const uint4*>(p + c0 * E);
+          r1[j] = *reinterpret_cast<const uint4*>(p + c1 * E);
+        }
       }
 #pragma unroll
       for (int j = 0; j < kUnroll; ++j) {
         if (h0 + j * HPW >= h_end) break;            // warp-uniform
         const int h = h0 + j * HPW + sub;
-        float x[U][V], sum = 0.0f;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          unpack16<T>(raw[j][u], x[u]);
-#pragma unroll
-          for (int e = 0; e < V; ++e) sum = fmaf(x[u][e], x[u][e], sum);
-        }
+        float x0[V], x1[V];
+        unpack16<T>(r0[j], x0);
+        unpack16<T>(r1[j], x1);
         if (w) {
+          float q0 = 0.0f, q1 = 0.0f, q2 = 0.0f, q3 = 0.0f;
+#pragma unroll
+          for (int e = 0; e < V; e += 2) {
+            fma_x2(q0, q1, x0[e], x0[e + 1], x0[e], x0[e + 1], q0, q1);
+            fma_x2(q2, q3, x1[e], x1[e + 1], x1[e], x1[e + 1], q2, q3);
+          }
+          float sum = (q0 + q1) + (q2 + q3);
 #pragma unroll
           for (int d = LPH / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-          const float r = 1.0f / sqrtf(sum * (1.0f / D) + a.eps);
+          const float r = rsqrtf(fmaf(sum, 1.0f / D, a.eps));
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int e = 0; e < V; ++e) x[u][e] *= r * wt[u][e];
-        }
-        float y[U][V];
-        if constexpr (PAIRS) {
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int e = 0; e < V; ++e) y[u][e] = fmaf(x[u][e ^ 1], s[u][e], x[u][e] * c[u][e]);
-        } else {
-          // the partner column is half columns away: half is a whole number of
-          // units, so the same element of another lane's unit
-          const int hu = half / V;
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int unit = u * LPH + hl;
-            int pu = unit;
-            if (unit < 2 * hu) pu = unit < hu ? unit + hu : unit - hu;
-            const int pl = (lane - hl) + pu % LPH;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              float other = __shfl_sync(0xffffffffu, x[0][e], pl);
-              if constexpr (U == 2) {
-                const float hi = __shfl_sync(0xffffffffu, x[1][e], pl);
-                if (pu >= LPH) other = hi;
-              }
-              y[u][e] = fmaf(other, s[u][e], x[u][e] * c[u][e]);
-            }
+          for (int e = 0; e < V; e += 2) {
+            mul_x2(x0[e], x0[e + 1], x0[e], x0[e + 1], r * w0[e], r * w0[e + 1]);
+            mul_x2(x1[e], x1[e + 1], x1[e], x1[e + 1], r * w1[e], r * w1[e + 1]);
           }
         }
-        if (h < h_end && dst) {
+        float y0[V], y1[V];
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            stg16(dst + ((int64_t)h * dst_head + (u * LPH + hl) * V) * E, pack16<T>(y[u]));
+        for (int e = 0; e < V; ++e) {
+          if constexpr (PAIRS) {
+            float* y = e < V / 2 ? y0 + 2 * e : y1 + 2 * e - V;
+            const float* x = e < V / 2 ? x0 + 2 * e : x1 + 2 * e - V;
+            y[0] = fmaf(-x[1], s[e], x[0] * c[e]);
+            y[1] = fmaf(x[0], s[e], x[1] * c[e]);
+          } else {
+            y0[e] = fmaf(-x1[e], s[e], x0[e] * c[e]);
+            y1[e] = fmaf(x0[e], s[e], x1[e] * c[e]);
+          }
+        }
+        if (h < h_end) {
+          char* p = dst + (int64_t)h * dst_head * E;
+          stg16(p + c0 * E, pack16<T>(y0));
+          stg16(p + c1 * E, pack16<T>(y1));
         }
       }
     }
   };
   // this warp's share of the heads, in whole groups of HPW
-  const int gq = (a.Hq + HPW - 1) / HPW, gk = (a.Hkv + HPW - 1) / HPW;
-  auto share = [&](int groups, int heads, int& b, int& e) {
-    b = min(heads, (int)((int64_t)groups * part / a.parts) * HPW);
-    e = min(heads, (int)((int64_t)groups * (part + 1) / a.parts) * HPW);
+  auto share = [&](int heads, int& b, int& e) {
+    const int groups = (heads + HPW - 1) / HPW;
+    b = min(heads, groups * part / a.parts * HPW);
+    e = min(heads, groups * (part + 1) / a.parts * HPW);
   };
   int hb, he;
-  share(gq, a.Hq, hb, he);
+  share(a.Hq, hb, he);
   if (hb < he)
-    rotate_heads(hb, he, a.q + t * a.q_rs * E, a.qw, a.qo + t * a.qo_rs * E, D);
-  if (!kdst) return;
-  share(gk, a.Hkv, hb, he);
+    rotate_heads(hb, he, a.q + tok * a.q_rs * E, a.qw, wq, a.qo + tok * a.qo_rs * E, D);
+  if (!kdst) continue;
+  share(a.Hkv, hb, he);
   if (hb < he) {
     // the values first: their loads run while the keys are worked on
-    const char* vs = a.v + t * a.v_rs * E;
+    const char* vs = a.v + tok * a.v_rs * E;
     for (int h0 = hb; h0 < he; h0 += HPW) {
       const int h = h0 + sub;
-      if (h < he)
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          stg16(vdst + ((int64_t)h * a.s_head + (u * LPH + hl) * V) * E,
-                *reinterpret_cast<const uint4*>(vs + ((int64_t)h * D + (u * LPH + hl) * V) * E));
+      if (h < he) {
+        const char* p = vs + (int64_t)h * (D * E) + l * 16;
+        char* q = vdst + (int64_t)h * a.s_head * E + l * 16;
+        const uint4 u0 = *reinterpret_cast<const uint4*>(p);
+        const uint4 u1 = *reinterpret_cast<const uint4*>(p + LPH * 16);
+        stg16(q, u0);
+        stg16(q + LPH * 16, u1);
+      }
     }
-    rotate_heads(hb, he, a.k + t * a.k_rs * E, a.kw, kdst, a.s_head);
+    rotate_heads(hb, he, a.k + tok * a.k_rs * E, a.kw, wk, kdst, a.s_head);
+  }
   }
 }
 
 template <typename T, int D>
-cudaError_t launch_nr(const NrArgs& a, bool pairs, cudaStream_t st) {
-  const int64_t warps = (int64_t)a.T * a.parts;
-  const unsigned grid = (unsigned)((warps + kNrThreads / 32 - 1) / (kNrThreads / 32));
+cudaError_t launch_nr(const NrArgs& a, bool pairs, int sms, cudaStream_t st) {
+  const int64_t warps = (int64_t)a.T * a.parts, per = kNrThreads / 32;
+  const unsigned grid =
+      (unsigned)std::min<int64_t>((warps + per - 1) / per, (int64_t)sms * kNrBlocks);
   if (pairs)
     norm_rope_kernel<T, D, true><<<grid, kNrThreads, 0, st>>>(a);
   else
@@ -197,10 +213,10 @@ cudaError_t launch_nr(const NrArgs& a, bool pairs, cudaStream_t st) {
 }
 
 template <typename T>
-cudaError_t launch_nr_d(const NrArgs& a, int D, bool pairs, cudaStream_t st) {
-  if (D == 64) return launch_nr<T, 64>(a, pairs, st);
-  if (D == 128) return launch_nr<T, 128>(a, pairs, st);
-  return launch_nr<T, 256>(a, pairs, st);
+cudaError_t launch_nr_d(const NrArgs& a, int D, bool pairs, int sms, cudaStream_t st) {
+  if (D == 64) return launch_nr<T, 64>(a, pairs, sms, st);
+  if (D == 128) return launch_nr<T, 128>(a, pairs, sms, st);
+  return launch_nr<T, 256>(a, pairs, sms, st);
 }
 
 }  // namespace
@@ -223,7 +239,7 @@ extern "C" int attn_norm_rope_cache(const void* q, int64_t q_row_stride, const v
   if (rc != CCONV_OK) return rc;
   const int V = 16 / e, D = cache.head_dim;
   if (rot_dim < 0 || rot_dim > D || rot_dim % 2 || (!interleaved && rot_dim % (2 * V)) ||
-      max_position <= 0 || (rot_dim > 0 && !cos_sin) || !(eps >= 0.0f))
+      max_position <= 0 || (rot_dim > 0 && (!cos_sin || !mix_aligned16(cos_sin))) || !(eps >= 0.0f))
     return CCONV_ERR_INVALID;
   if (reinterpret_cast<uintptr_t>(q_weight) % e || reinterpret_cast<uintptr_t>(k_weight) % e)
     return CCONV_ERR_INVALID;
@@ -260,14 +276,13 @@ extern "C" int attn_norm_rope_cache(const void* q, int64_t q_row_stride, const v
   a.Hkv = cache.num_kv_heads;
   a.qo = static_cast<char*>(q_out);
   a.dev_err = dev_err;
-  // several warps a token while there are fewer than 16 warps an SM
-  a.parts = (int32_t)std::max<int64_t>(
-      1, std::min<int64_t>(8, (int64_t)sms * 16 / std::max(1, num_tokens)));
-  if (((int64_t)num_tokens * a.parts) / (kNrThreads / 32) + 1 > INT32_MAX)
-    return CCONV_ERR_INVALID;
+  // several warps a token while there are fewer than 16 warps an SM: 1, 2, 4 or 8,
+  // so that a block's four warps, and the grid's, fall into whole tokens
+  a.parts = 1;
+  while (a.parts < 8 && (int64_t)num_tokens * a.parts * 2 <= (int64_t)sms * 16) a.parts *= 2;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t err = dtype == CCONV_DTYPE_F32
-                              ? launch_nr_d<float>(a, D, interleaved != 0, st)
-                              : launch_nr_d<__nv_bfloat16>(a, D, interleaved != 0, st);
+                              ? launch_nr_d<float>(a, D, interleaved != 0, sms, st)
+                              : launch_nr_d<__nv_bfloat16>(a, D, interleaved != 0, sms, st);
   return err == cudaSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
 }
