@@ -1,7 +1,8 @@
 """Build libcconv.so (sm_103a) in-tree with nvcc.
 
 Each ``csrc/*.cu`` translation unit compiles in parallel to an object under
-``_build/``; the objects link into ``state_cached_causal_gb300/libcconv.so``.
+``_build/``; the objects link into ``state_cached_causal_gb300/libcconv.so``. The
+binding's C module ``_fast.so`` is built beside it with the host compiler.
 An object is rebuilt when its source, a header it may include, or the flags
 change.
 """
@@ -12,6 +13,7 @@ import hashlib
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcconv.so")
+FAST = os.path.join(PKG, "_fast.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -74,11 +77,34 @@ def _compile(nvcc, src, extra_flags, verbose):
     return obj
 
 
+def _build_fast(verbose):
+    """The binding's C module (csrc/fast.c), with the host compiler and Python's headers."""
+    src = os.path.join(CSRC, "fast.c")
+    stamp = os.path.join(BUILD, "fast." + _digest(src, [sysconfig.get_config_var("SOABI") or ""]))
+    if os.path.exists(FAST) and os.path.exists(stamp):
+        return
+    cc = os.environ.get("CC") or shutil.which("gcc") or "cc"
+    tmp = FAST + f".{os.getpid()}.tmp"
+    cmd = [cc, "-O2", "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-I",
+           sysconfig.get_paths()["include"], src, "-o", tmp, "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cc} failed on {src}:\n{r.stdout}\n{r.stderr}")
+    if verbose and (r.stdout or r.stderr):
+        print(r.stdout + r.stderr)
+    os.replace(tmp, FAST)
+    for f in os.listdir(BUILD):
+        if f.startswith("fast."):
+            os.remove(os.path.join(BUILD, f))
+    open(stamp, "w").close()
+
+
 def build(verbose: bool = False, extra_flags=None, jobs: int | None = None) -> str:
     """Compile every CUDA source and link libcconv.so; return its path."""
     extra_flags = list(extra_flags or [])
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
+    _build_fast(verbose)
     srcs = _sources()
     jobs = jobs or min(len(srcs), os.cpu_count() or 4)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:

@@ -16,8 +16,8 @@ namespace cconv {
 namespace {
 
 constexpr int kNrThreads = 128;
-constexpr int kNrBlocks = 5;    // of an SM
-constexpr int kUnroll = 2;      // groups of heads whose loads are in flight together
+constexpr int kNrBlocks = 4;    // of an SM
+constexpr int kUnroll = 4;      // groups of heads whose loads are in flight together
 
 struct NrArgs {
   const char *q, *k, *v;

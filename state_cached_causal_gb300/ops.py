@@ -26,6 +26,7 @@ DERR_POSITION, DERR_PAGE, DERR_SEQ_LEN = 64, 128, 256
 
 _lock = threading.Lock()
 _lib = None
+_fast = None    # csrc/fast.c: the mixer calls' marshalling in C, set by load()
 
 
 class Epilogue(ctypes.Structure):
@@ -67,7 +68,7 @@ class CConvError(RuntimeError):
 
 def load():
     """Load libcconv.so (raises if it has not been built)."""
-    global _lib
+    global _lib, _fast
     if _lib is not None:
         return _lib
     with _lock:
@@ -122,8 +123,31 @@ def load():
         lib.cconv_status_string.restype = ctypes.c_char_p
         lib.cconv_abi_version.argtypes = []
         lib.cconv_abi_version.restype = ctypes.c_int
+        _fast = _load_fast(lib)
         _lib = lib
         return lib
+
+
+def _load_fast(lib):
+    """The C module with the library's entry points, or None where a part it stands on is
+    missing (the functions below then marshal by themselves)."""
+    try:
+        from . import _fast as mod
+        raw = torch._C._cuda_getCurrentRawStream
+    except (ImportError, AttributeError):
+        return None
+    mod.init(lib._handle, (torch.float32, torch.bfloat16, torch.int32, torch.uint8, torch.bool),
+             raw)
+    return mod
+
+
+def _served(fn, rc):
+    """What the C module answered: True for a call made, False for one left to Python."""
+    if rc is None:
+        return False
+    if rc != OK:
+        raise CConvError(fn, rc)
+    return True
 
 
 def status_string(status: int) -> str:
@@ -360,8 +384,9 @@ def cca_qk_conv_fused(qk, w_dw, b_dw, w_gr, b_gr, groups, num_q_heads, t0, t1, d
 
 
 # ---- the mixers behind the convolutions --------------------------------------
-# A decode step's calls are short, so these read each tensor's sizes and strides
-# once, check them, and hand plain integers to the library.
+# A decode step's calls are short, so their plain cases are marshalled in C (csrc/fast.c);
+# what that leaves -- another stream, anything unusual, whatever is wrong -- is checked and
+# marshalled here, where each tensor's sizes and strides are read once.
 
 _CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 
@@ -449,6 +474,11 @@ def gdn_fwd_varlen(q, k, v, a, b, A_log, dt_bias, states, state_idx, cu_seqlens,
     dt_bias: fp32 [Hv]; states: [slots, Hv, dk, dv] fp32 or bf16, updated in place;
     state_idx/cu_seqlens: int32; has_init: uint8/bool or None.
     """
+    if stream is None and (_lib or load()) and _fast is not None and _served(
+            "gdn_fwd_varlen", _fast.gdn_fwd_varlen(
+                q, k, v, a, b, A_log, dt_bias, states, state_idx, cu_seqlens, has_init, scale, out,
+                qk_l2norm, dev_err, num_tokens)):
+        return
     _i32(state_idx, "state_idx")
     _i32(cu_seqlens, "cu_seqlens")
     _u8(has_init, "has_init")
@@ -469,6 +499,11 @@ def gdn_update(q, k, v, a, b, A_log, dt_bias, states, state_idx, n_spec, num_acc
     (or [B] when n_spec is 0), the slot of the state after each token; num_accepted: int32 [B]
     when n_spec > 0.
     """
+    if stream is None and (_lib or load()) and _fast is not None and _served(
+            "gdn_update", _fast.gdn_update(
+                q, k, v, a, b, A_log, dt_bias, states, state_idx, n_spec, num_accepted, has_init,
+                scale, out, qk_l2norm, dev_err)):
+        return
     _i32(state_idx, "state_idx")
     _i32(num_accepted, "num_accepted")
     _u8(has_init, "has_init")
@@ -505,6 +540,11 @@ def attn_norm_rope_cache(q, k, v, q_weight, k_weight, eps, cos_sin, positions, i
     [max_position, rot_dim], the cosines then the sines; caches: [pages, page_size, Hkv, D]
     views (any order of storage with contiguous D); positions, slot_mapping: int32 [T].
     """
+    if stream is None and (_lib or load()) and _fast is not None and _served(
+            "attn_norm_rope_cache", _fast.attn_norm_rope_cache(
+                q, k, v, q_weight, k_weight, eps, cos_sin, positions, interleaved, k_cache,
+                v_cache, slot_mapping, q_out, dev_err)):
+        return
     _i32(positions, "positions")
     _i32(slot_mapping, "slot_mapping")
     dtype = q.dtype
@@ -549,6 +589,16 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, n_spec, scale, out, 
     cached tokens with the new ones; lse: fp32 [B*(1+n_spec), Hq] or None; workspace: a uint8
     tensor of attn_decode_workspace_bytes() or None (allocated for the call).
     """
+    if (stream is None and q.is_cuda and q.dim() == 3 and k_cache.dim() == 4
+            and (_lib or load()) and _fast is not None):
+        ws = workspace
+        if ws is None:
+            ws = q.new_empty(max(attn_decode_workspace_bytes(seq_lens.shape[0], n_spec, q.shape[1],
+                                                             k_cache.shape[2], q.shape[2]), 16),
+                             dtype=torch.uint8)
+        if _served("attn_decode", _fast.attn_decode(q, k_cache, v_cache, block_table, seq_lens,
+                                                    n_spec, scale, out, lse, ws, dev_err)):
+            return
     _i32(block_table, "block_table")
     _i32(seq_lens, "seq_lens")
     dtype = q.dtype
