@@ -7,10 +7,13 @@
 // in registers from its load to its store, and takes its tokens past it.
 //
 // The state's columns are independent of each other: column c of S needs k, q
-// and element c of v alone. A block takes 32 columns (kCols) of one head of one
-// sequence, all dk rows, 128 threads of 4 columns by dk/16 rows; blocks of 16
-// KB keep enough loads in flight on an SM (16 blocks of 128 threads) and give
-// one request of 32 heads 128 blocks.
+// and element c of v alone. An item is 32 columns (kCols) of one head of one
+// sequence, all dk rows, 128 threads of 4 columns by dk/16 rows: one request of
+// 32 heads is 128 items. Blocks, eight an SM, take one item after the other, and
+// request the next item's state (cp.async, each thread into its own place in
+// shared memory, so that no barrier is needed) before they work on this one:
+// 128 KB are on their way to an SM at any time. Without that, one block an item
+// and as many a SM, a decode step of 64 requests took 57.8 us (4.7 TB/s).
 //
 // Per token one reduction over the rows gives both products with the old
 // state, x = S^T k and y = S^T q, and the rest follows from them:
@@ -37,14 +40,71 @@ int mix_sm_count() {
 namespace {
 
 constexpr int kCols = 32;      // state columns of a block
-constexpr int kTok = 8;        // tokens staged at a time
+constexpr int kTok = 4;        // tokens staged at a time
+constexpr int kStepBlocks = 8; // of an SM
 constexpr int kStepThreads = 128;
 constexpr int kStepMax = 8;    // longest sequence of this kernel where the chunked one serves
 
+struct StepItem {
+  int s, h, blk, row0, len, slot_in, slot_out;
+  bool skip, init;
+};
+// Item i: its sequence, head and columns, and the slots to start from and (not
+// for gdn_update, which has one for each token) to end in. Reports bad indices.
+__device__ __forceinline__ void step_item(const GdnArgs& a, int i, int nblk, StepItem& t) {
+  t.blk = i % nblk;
+  t.h = i / nblk % a.Hv;
+  t.s = i / nblk / a.Hv;
+  t.skip = true;
+  t.init = false;
+  const bool first = t.blk == 0 && t.h == 0 && threadIdx.x == 0;
+  if (!gdn_bounds(a, t.s, t.row0, t.len)) {
+    if (first) flag_error(a.dev_err, CCONV_DERR_CU_SEQLENS);
+    return;
+  }
+  if (a.max_len > 0 && t.len > a.max_len) return;
+  bool bad = false;
+  if (a.cu) {
+    t.slot_in = t.slot_out = a.state_idx[t.s];
+    bad = t.slot_in >= a.num_slots;
+  } else {
+    const int32_t* idx = a.state_idx + (int64_t)t.s * a.q_len;
+    int acc = 1;
+    if (a.q_len > 1) {
+      acc = a.num_acc[t.s];
+      if (acc < 1 || acc > a.q_len) {
+        if (first) flag_error(a.dev_err, CCONV_DERR_NUM_ACCEPTED);
+        return;
+      }
+    }
+    for (int k = 0; k < a.q_len; ++k) bad |= idx[k] >= a.num_slots;
+    t.slot_in = idx[acc - 1];
+    t.slot_out = -1;
+  }
+  if (bad) {
+    if (first) flag_error(a.dev_err, CCONV_DERR_SLOT_RANGE);
+    return;
+  }
+  t.init = t.slot_in >= 0 && (!a.has_init || a.has_init[t.s]);
+  // an empty sequence leaves its slot, or clears it
+  t.skip = t.len == 0 && (t.init || t.slot_out < 0);
+}
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
+                 : "memory");
+}
+
 template <typename T, typename ST, int DK>
-__global__ void __launch_bounds__(kStepThreads)
-gdn_step_kernel(const GdnArgs a, const int dv) {
+__global__ void __launch_bounds__(kStepThreads, kStepBlocks)
+gdn_step_kernel(const GdnArgs a, const int dv, const int items) {
   constexpr int R = DK / 16;                     // rows of a thread
+  constexpr int kUnit = 4 * sizeof(ST);          // bytes of its 4 columns of a row
+  __shared__ __align__(16) unsigned char stage[R][kStepThreads][kUnit];
   __shared__ float sk[kTok][DK], sq[kTok][DK];   // raw k and q of the staged tokens
   __shared__ float sv[kTok][kCols];
   __shared__ float spart[2][3][4][kTok];          // sums of squares and q.k by warp
@@ -52,172 +112,167 @@ gdn_step_kernel(const GdnArgs a, const int dv) {
   __shared__ float4 sred[2][2][4][8];            // [token parity][x, y][warp][column quad]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nblk = dv / kCols;
-  const int blk = blockIdx.x % nblk;
-  const int h = (blockIdx.x / nblk) % a.Hv;
-  const int s = blockIdx.x / nblk / a.Hv;
-  int row0, len;
-  if (!gdn_bounds(a, s, row0, len)) {
-    if (blk == 0 && h == 0 && tid == 0) flag_error(a.dev_err, CCONV_DERR_CU_SEQLENS);
-    return;
-  }
-  if (a.max_len > 0 && len > a.max_len) return;
-  // slots: the one to start from, and (update) one for each token
-  int slot_in, slot_out;
-  bool bad = false;
-  if (a.cu) {
-    slot_in = slot_out = a.state_idx[s];
-    bad = slot_in >= a.num_slots;
-  } else {
-    int acc = 1;
-    if (a.q_len > 1) {
-      acc = a.num_acc[s];
-      if (acc < 1 || acc > a.q_len) {
-        if (blk == 0 && h == 0 && tid == 0) flag_error(a.dev_err, CCONV_DERR_NUM_ACCEPTED);
-        return;
-      }
-    }
-    for (int i = 0; i < a.q_len; ++i) bad |= a.state_idx[(int64_t)s * a.q_len + i] >= a.num_slots;
-    slot_in = a.state_idx[(int64_t)s * a.q_len + acc - 1];
-    slot_out = -1;
-  }
-  if (bad) {
-    if (blk == 0 && h == 0 && tid == 0) flag_error(a.dev_err, CCONV_DERR_SLOT_RANGE);
-    return;
-  }
-  const bool init = slot_in >= 0 && (!a.has_init || a.has_init[s]);
-  if (len == 0 && (init || slot_out < 0)) return;   // nothing to compute, nothing to clear
-
-  const int c0 = blk * kCols + (lane & 7) * 4;       // the thread's 4 columns
+  const int cq = (lane & 7) * 4;                     // the thread's 4 columns of the item
   const int rg = warp * 4 + (lane >> 3);             // rows rg + 16 i
-  ST* const base = reinterpret_cast<ST*>(a.st) + (int64_t)h * a.st_head + c0;
-  float S[R][4];
-  if (init) {
-    const ST* p = base + (int64_t)slot_in * a.st_slot;
+  auto state_of = [&](const StepItem& t, int slot) {
+    return reinterpret_cast<ST*>(a.st) + (int64_t)slot * a.st_slot + (int64_t)t.h * a.st_head +
+           t.blk * kCols + cq + (int64_t)rg * dv;
+  };
+  auto request = [&](const StepItem& t) {
+    if (t.skip || !t.init) return;
+    const ST* p = state_of(t, t.slot_in);
 #pragma unroll
-    for (int i = 0; i < R; ++i) load4<ST>(p + (rg + 16 * i) * dv, S[i]);
-  } else {
+    for (int i = 0; i < R; ++i) cp_async_small<kUnit>(smem_addr(stage[i][tid]), p + 16 * i * dv);
+  };
+  StepItem it, nx;
+  step_item(a, blockIdx.x, nblk, nx);
+  request(nx);
+  int pb = 0;
+#pragma unroll 1
+  for (int i = blockIdx.x; i < items; i += gridDim.x) {
+    it = nx;
+    cp_async_commit();
+    cp_async_wait<0>();
+    float S[R][4];
 #pragma unroll
-    for (int i = 0; i < R; ++i) S[i][0] = S[i][1] = S[i][2] = S[i][3] = 0.0f;
-  }
-
-  const T* const qp = reinterpret_cast<const T*>(a.q) + (int64_t)(h / (a.Hv / a.Hk)) * DK;
-  const T* const kp = reinterpret_cast<const T*>(a.k) + (int64_t)(h / (a.Hv / a.Hk)) * DK;
-  const T* const vp = reinterpret_cast<const T*>(a.v) + (int64_t)h * dv + blk * kCols;
-  for (int t0 = 0; t0 < len; t0 += kTok) {
-    const int n = min(kTok, len - t0);
-    const int pb = (t0 / kTok) & 1;
-    __syncthreads();   // the last tokens' reads are done
-    for (int t = 0; t < n; ++t) {
-      const int64_t row = (int64_t)row0 + t0 + t;
-      float kk = 0.0f, qq = 0.0f, qk = 0.0f;
-      for (int i = tid; i < DK; i += kStepThreads) {
-        const float kv = elem<T>(kp, row * a.k_rs + i), qv = elem<T>(qp, row * a.q_rs + i);
-        sk[t][i] = kv;
-        sq[t][i] = qv;
-        kk = fmaf(kv, kv, kk);
-        qq = fmaf(qv, qv, qq);
-        qk = fmaf(qv, kv, qk);
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        kk += __shfl_xor_sync(0xffffffffu, kk, d);
-        qq += __shfl_xor_sync(0xffffffffu, qq, d);
-        qk += __shfl_xor_sync(0xffffffffu, qk, d);
-      }
-      if (lane == 0) {
-        spart[pb][0][warp][t] = kk;
-        spart[pb][1][warp][t] = qq;
-        spart[pb][2][warp][t] = qk;
-      }
+    for (int r = 0; r < R; ++r) {
+      if (it.init)
+        load4<ST>(reinterpret_cast<const ST*>(stage[r][tid]), S[r]);
+      else
+        S[r][0] = S[r][1] = S[r][2] = S[r][3] = 0.0f;
     }
-    for (int i = tid; i < n * kCols; i += kStepThreads)
-      sv[i / kCols][i % kCols] = elem<T>(vp, ((int64_t)row0 + t0 + i / kCols) * a.v_rs + i % kCols);
-    if (tid < n) {
-      const int64_t row = (int64_t)row0 + t0 + tid;
-      sgate[tid][0] = expf(gdn_log_decay(elem<T>(reinterpret_cast<const T*>(a.a), row * a.a_rs + h),
-                                         a.A_log[h], a.dt_bias[h]));
-      sgate[tid][1] = gdn_beta(elem<T>(reinterpret_cast<const T*>(a.b), row * a.b_rs + h));
+    if (i + (int)gridDim.x < items) {
+      step_item(a, i + gridDim.x, nblk, nx);
+      request(nx);
     }
-    __syncthreads();
-    for (int t = 0; t < n; ++t) {
-      float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f}, kr[R];
+    if (it.skip) continue;
+    const int hk = it.h / (a.Hv / a.Hk);
+    const T* const qp = reinterpret_cast<const T*>(a.q) + (int64_t)hk * DK;
+    const T* const kp = reinterpret_cast<const T*>(a.k) + (int64_t)hk * DK;
+    const T* const vp = reinterpret_cast<const T*>(a.v) + (int64_t)it.h * dv + it.blk * kCols;
+#pragma unroll 1
+    for (int t0 = 0; t0 < it.len; t0 += kTok) {
+      const int n = min(kTok, it.len - t0);
+      pb ^= 1;
+      __syncthreads();   // the last tokens' reads are done
+#pragma unroll 1
+      for (int t = 0; t < n; ++t) {
+        const int64_t row = (int64_t)it.row0 + t0 + t;
+        float kk = 0.0f, qq = 0.0f, qk = 0.0f;
+        if (DK == kStepThreads || tid < DK) {
+          const float kv = elem<T>(kp, row * a.k_rs + tid), qv = elem<T>(qp, row * a.q_rs + tid);
+          sk[t][tid] = kv;
+          sq[t][tid] = qv;
+          kk = kv * kv;
+          qq = qv * qv;
+          qk = qv * kv;
+        }
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        kr[i] = sk[t][rg + 16 * i];
-        const float qv = sq[t][rg + 16 * i];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          x[c] = fmaf(kr[i], S[i][c], x[c]);
-          y[c] = fmaf(qv, S[i][c], y[c]);
+        for (int d = 16; d > 0; d >>= 1) {
+          kk += __shfl_xor_sync(0xffffffffu, kk, d);
+          qq += __shfl_xor_sync(0xffffffffu, qq, d);
+          qk += __shfl_xor_sync(0xffffffffu, qk, d);
+        }
+        if (lane == 0) {
+          spart[pb][0][warp][t] = kk;
+          spart[pb][1][warp][t] = qq;
+          spart[pb][2][warp][t] = qk;
         }
       }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        x[c] += __shfl_xor_sync(0xffffffffu, x[c], 8);
-        y[c] += __shfl_xor_sync(0xffffffffu, y[c], 8);
-        x[c] += __shfl_xor_sync(0xffffffffu, x[c], 16);
-        y[c] += __shfl_xor_sync(0xffffffffu, y[c], 16);
-      }
-      // two copies of the exchange by token parity: one barrier a token
-      if (lane < 8) {
-        sred[t & 1][0][warp][lane] = make_float4(x[0], x[1], x[2], x[3]);
-        sred[t & 1][1][warp][lane] = make_float4(y[0], y[1], y[2], y[3]);
+      if (tid < n * kCols)
+        sv[tid / kCols][tid % kCols] =
+            elem<T>(vp, ((int64_t)it.row0 + t0 + tid / kCols) * a.v_rs + tid % kCols);
+      if (tid < n) {
+        const int64_t row = (int64_t)it.row0 + t0 + tid;
+        sgate[tid][0] = expf(gdn_log_decay(
+            elem<T>(reinterpret_cast<const T*>(a.a), row * a.a_rs + it.h), a.A_log[it.h],
+            a.dt_bias[it.h]));
+        sgate[tid][1] = gdn_beta(elem<T>(reinterpret_cast<const T*>(a.b), row * a.b_rs + it.h));
       }
       __syncthreads();
-      float4 X = make_float4(0.f, 0.f, 0.f, 0.f), Y = X;
-      float kk = 0.0f, qq = 0.0f, qk = 0.0f;
+#pragma unroll 1
+      for (int t = 0; t < n; ++t) {
+        float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f}, kr[R];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float4 u = sred[t & 1][0][w][lane & 7], z = sred[t & 1][1][w][lane & 7];
-        X.x += u.x, X.y += u.y, X.z += u.z, X.w += u.w;
-        Y.x += z.x, Y.y += z.y, Y.z += z.z, Y.w += z.w;
-        kk += spart[pb][0][w][t];
-        qq += spart[pb][1][w][t];
-        qk += spart[pb][2][w][t];
-      }
-      const float rk = a.l2norm ? 1.0f / sqrtf(kk + kGdnNormEps) : 1.0f;
-      const float rq = (a.l2norm ? 1.0f / sqrtf(qq + kGdnNormEps) : 1.0f) * a.scale;
-      const float al = sgate[t][0], be = sgate[t][1];
-      const float ark = al * rk, arq = al * rq, kq = rq * rk * qk;
-      const float* vt = &sv[t][(lane & 7) * 4];
-      const float r[4] = {be * (vt[0] - ark * X.x), be * (vt[1] - ark * X.y),
-                          be * (vt[2] - ark * X.z), be * (vt[3] - ark * X.w)};
+        for (int r = 0; r < R; ++r) {
+          kr[r] = sk[t][rg + 16 * r];
+          const float qv = sq[t][rg + 16 * r];
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const float kn = kr[i] * rk;
+          for (int c = 0; c < 4; ++c) {
+            x[c] = fmaf(kr[r], S[r][c], x[c]);
+            y[c] = fmaf(qv, S[r][c], y[c]);
+          }
+        }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) S[i][c] = fmaf(kn, r[c], al * S[i][c]);
-      }
-      if (tid < 8) {
-        const float o[4] = {fmaf(kq, r[0], arq * Y.x), fmaf(kq, r[1], arq * Y.y),
-                            fmaf(kq, r[2], arq * Y.z), fmaf(kq, r[3], arq * Y.w)};
-        store4<T>(reinterpret_cast<T*>(a.out) + ((int64_t)row0 + t0 + t) * a.out_rs +
-                      (int64_t)h * dv + c0, o);
-      }
-      if (!a.cu) {
-        const int so = a.state_idx[(int64_t)s * a.q_len + t0 + t];
+        for (int c = 0; c < 4; ++c) {
+          x[c] += __shfl_xor_sync(0xffffffffu, x[c], 8);
+          y[c] += __shfl_xor_sync(0xffffffffu, y[c], 8);
+          x[c] += __shfl_xor_sync(0xffffffffu, x[c], 16);
+          y[c] += __shfl_xor_sync(0xffffffffu, y[c], 16);
+        }
+        // two copies of the exchange by token parity: one barrier a token
+        if (lane < 8) {
+          sred[t & 1][0][warp][lane] = make_float4(x[0], x[1], x[2], x[3]);
+          sred[t & 1][1][warp][lane] = make_float4(y[0], y[1], y[2], y[3]);
+        }
+        __syncthreads();
+        float4 X = make_float4(0.f, 0.f, 0.f, 0.f), Y = X;
+        float kk = 0.0f, qq = 0.0f, qk = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float4 u = sred[t & 1][0][w][lane & 7], z = sred[t & 1][1][w][lane & 7];
+          X.x += u.x, X.y += u.y, X.z += u.z, X.w += u.w;
+          Y.x += z.x, Y.y += z.y, Y.z += z.z, Y.w += z.w;
+          kk += spart[pb][0][w][t];
+          qq += spart[pb][1][w][t];
+          qk += spart[pb][2][w][t];
+        }
+        const float rk = a.l2norm ? 1.0f / sqrtf(kk + kGdnNormEps) : 1.0f;
+        const float rq = (a.l2norm ? 1.0f / sqrtf(qq + kGdnNormEps) : 1.0f) * a.scale;
+        const float al = sgate[t][0], be = sgate[t][1];
+        const float ark = al * rk, arq = al * rq, kq = rq * rk * qk;
+        const float* vt = &sv[t][cq];
+        const float r4[4] = {be * (vt[0] - ark * X.x), be * (vt[1] - ark * X.y),
+                             be * (vt[2] - ark * X.z), be * (vt[3] - ark * X.w)};
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float kn = kr[r] * rk;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) S[r][c] = fmaf(kn, r4[c], al * S[r][c]);
+        }
+        if (tid < 8) {
+          const float o[4] = {fmaf(kq, r4[0], arq * Y.x), fmaf(kq, r4[1], arq * Y.y),
+                              fmaf(kq, r4[2], arq * Y.z), fmaf(kq, r4[3], arq * Y.w)};
+          store4<T>(reinterpret_cast<T*>(a.out) + ((int64_t)it.row0 + t0 + t) * a.out_rs +
+                        (int64_t)it.h * dv + it.blk * kCols + cq, o);
+        }
+        const int so = a.cu ? (t0 + t + 1 == it.len ? it.slot_out : -1)
+                            : a.state_idx[(int64_t)it.s * a.q_len + t0 + t];
         if (so >= 0) {
-          ST* p = base + (int64_t)so * a.st_slot;
+          ST* p = state_of(it, so);
 #pragma unroll
-          for (int i = 0; i < R; ++i) store4<ST>(p + (rg + 16 * i) * dv, S[i]);
+          for (int r = 0; r < R; ++r) store4<ST>(p + 16 * r * dv, S[r]);
         }
       }
     }
-  }
-  if (slot_out >= 0) {
-    ST* p = base + (int64_t)slot_out * a.st_slot;
+    if (it.len == 0) {      // cleared
+      ST* p = state_of(it, it.slot_out);
 #pragma unroll
-    for (int i = 0; i < R; ++i) store4<ST>(p + (rg + 16 * i) * dv, S[i]);
+      for (int r = 0; r < R; ++r) store4<ST>(p + 16 * r * dv, S[r]);
+    }
   }
 }
 
 template <typename T, typename ST>
 cudaError_t launch_step_t(const GdnArgs& a, int dk, int dv, cudaStream_t st) {
-  const unsigned grid = (unsigned)((int64_t)a.B * a.Hv * (dv / kCols));
+  const int sms = mix_sm_count();
+  if (sms <= 0) return cudaErrorInvalidValue;
+  const int items = a.B * a.Hv * (dv / kCols);     // (at most 2^31 - 1: a host check)
+  const int grid = std::min(items, sms * kStepBlocks);
   if (dk == 64)
-    gdn_step_kernel<T, ST, 64><<<grid, kStepThreads, 0, st>>>(a, dv);
+    gdn_step_kernel<T, ST, 64><<<grid, kStepThreads, 0, st>>>(a, dv, items);
   else
-    gdn_step_kernel<T, ST, 128><<<grid, kStepThreads, 0, st>>>(a, dv);
+    gdn_step_kernel<T, ST, 128><<<grid, kStepThreads, 0, st>>>(a, dv, items);
   return cudaGetLastError();
 }
 
@@ -262,8 +317,8 @@ static int gdn_args(const void* q, int64_t q_rs, const void* k, int64_t k_rs, co
   if (!st.p || !mix_aligned16(st.p) || st.num_slots <= 0 || st.s_head < (int64_t)dk * dv ||
       st.s_slot <= 0 || st.s_head % (16 / se) || st.s_slot % (16 / se))
     return CCONV_ERR_INVALID;
-  // the grid's blocks: num_seqs * Hv * dv / 32
-  if ((int64_t)num_seqs * Hv * (dv / kCols) > INT32_MAX) return CCONV_ERR_INVALID;
+  // items of the recurrent kernel (and a grid more) are counted in 32 bits
+  if ((int64_t)num_seqs * Hv * (dv / kCols) > INT32_MAX / 2) return CCONV_ERR_INVALID;
   o.q = static_cast<const char*>(q);
   o.k = static_cast<const char*>(k);
   o.v = static_cast<const char*>(v);
