@@ -85,8 +85,8 @@ constexpr int kCoefs = 4;                    // chunks whose factors are kept
 constexpr uint32_t kColS = 0, kColKS = 128, kColN = kColKS, kColQS = 192, kColR = 256,
                    kColVN = 320, kColO = 384, kColD1 = 448;
 
-// A wait that has run out of this many clocks (seconds) gives the block up.
-constexpr long long kWaitClocks = 4000000000LL;
+// A wait of this many nanoseconds gives the block up.
+constexpr long long kWaitNs = 2000000000LL;
 
 // Per-token factors of a chunk for the warps on the chain (read four at a time).
 struct alignas(16) Coef {
@@ -112,7 +112,6 @@ struct Ctl {
   uint64_t s_full[2], sd_full[2];
   uint64_t ks_full, qs_done, r_full, vn_full, vd_full, o_full, o_empty, fin;
   uint32_t tmem;
-  volatile int abort;
 };
 
 struct Smem {
@@ -144,30 +143,32 @@ __device__ __forceinline__ uint32_t sw128(int row, int unit) {
   return (uint32_t)(row * 128 + ((unit ^ (row & 7)) << 4));
 }
 
+// A wait of a whole warp on a phase: false when it has run out of time, and the
+// role gives up (what waits for it runs out of time in turn). Few instructions,
+// and in line: the block's code is larger than the instruction caches near the
+// schedulers, so every role pays for the size of all; and a call would spill
+// the state's registers around it.
 struct Wait {
-  Ctl* ctl;
-  int32_t* err;
-  // Called by whole warps. False when the block is giving up. In line: a call
-  // would spill the state's registers around it.
   __device__ __forceinline__ bool operator()(uint64_t* bar, int phase) const {
-    const uint32_t parity = phase & 1;
-    long long t0 = 0;
-#pragma unroll 1
-    for (uint32_t it = 1; !__any_sync(0xffffffffu, mbar_try(bar, parity)); ++it) {
-      if ((it & 63u) == 0) {
-        const long long now = clock64();
-        if (t0 == 0) t0 = now;
-        const bool late = now - t0 > kWaitClocks;
-        if (__any_sync(0xffffffffu, late || ctl->abort != 0)) {
-          if (late) {
-            ctl->abort = 1;
-            if ((threadIdx.x & 31) == 0) flag_error(err, CCONV_DERR_TIMEOUT);
-          }
-          return false;
-        }
-      }
-    }
-    return true;
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 t0, t1;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "mov.u64 t0, %globaltimer;\n"
+        "AGAIN:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "mov.u64 t1, %globaltimer;\n\t"
+        "sub.u64 t1, t1, t0;\n\t"
+        "setp.lt.u64 q, t1, %3;\n\t"
+        "@q bra AGAIN;\n"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"((uint32_t)(phase & 1)), "n"(kWaitNs)
+        : "memory");
+    return __all_sync(0xffffffffu, ok != 0);
   }
 };
 
@@ -191,16 +192,6 @@ __device__ __forceinline__ void more_regs() {
 template <int N>
 __device__ __forceinline__ void fewer_regs() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// Waits for a phase while giving up: bounded by time alone.
-__device__ __forceinline__ void drain(uint64_t* bar, int phase, int32_t* err) {
-  const long long t0 = clock64();
-  while (!mbar_try(bar, phase & 1))
-    if (clock64() - t0 > kWaitClocks) {
-      flag_error(err, CCONV_DERR_TIMEOUT);
-      return;
-    }
 }
 
 // ---- which chains a block takes ----------------------------------------------
@@ -270,7 +261,7 @@ __device__ __forceinline__ void order_chains(const GdnArgs& a, Smem& sm, int* le
 // zeros behind the sequence's end. Gates: two tokens a lane (lane, lane + 32); their sums are
 // kept as whole part and remainder in (-1, 0], exact to 2^-24 of the remainder
 // however long the sum.
-__device__ __forceinline__ void load_role(const GdnArgs& a, const Maps& maps, Smem& sm,
+__device__ __forceinline__ bool load_role(const GdnArgs& a, const Maps& maps, Smem& sm,
                                           const Wait& wait) {
   const int lane = threadIdx.x & 31, u = lane & 15, r2 = lane >> 4;
   const __nv_bfloat16* const ga0 = reinterpret_cast<const __nv_bfloat16*>(a.a);
@@ -393,13 +384,13 @@ __device__ __forceinline__ void load_role(const GdnArgs& a, const Maps& maps, Sm
     }
   }
   }
-  return;
+  return true;
 quit:                       // given up: no copy lands after the block ends
   cp_async_wait<0>();
-  for (int i = max(boxed - kStages, 0); i < boxed; ++i)
-    drain(&sm.ctl.full[i % kStages], i / kStages, a.dev_err);
+  for (int i = max(boxed - kStages, 0); i < boxed; ++i) wait(&sm.ctl.full[i % kStages], i / kStages);
   for (int i = max(v_boxed - kStages, 0); i < v_boxed; ++i)
-    drain(&sm.ctl.v_full[i % kStages], i / kStages, a.dev_err);
+    wait(&sm.ctl.v_full[i % kStages], i / kStages);
+  return false;
 }
 
 // ---- the warps that look one chunk ahead ------------------------------------
@@ -471,7 +462,7 @@ __device__ __forceinline__ void t_blocks(const Smem& sm, unsigned char* tp, int 
 
 // Norms, factors, A, scores and T of every chunk. Thread p < 64 holds row p of
 // K K^T, thread 64 + p row p of Q K^T.
-__device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait& wait,
+__device__ __forceinline__ bool prep_role(const GdnArgs& a, Smem& sm, const Wait& wait,
                                           int chunks, uint32_t tmem) {
   const int p = threadIdx.x - kWarpPrep0 * 32, warp = p >> 5;
   const bool is_k = p < kC;
@@ -482,7 +473,7 @@ __device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait
     Coef& C = sm.coef[n % kCoefs];
     const Gate& G = sm.gate[bf];
     // ---- norms
-    if (!wait(&sm.ctl.full[st], n / kStages)) return;
+    if (!wait(&sm.ctl.full[st], n / kStages)) return false;
     float rn = 1.0f;
     if (a.l2norm) {
       float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
@@ -503,8 +494,8 @@ __device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait
       rn = 1.0f / sqrtf((s0 + s1) + (s2 + s3) + kGdnNormEps);
     }
     sm.rn[p] = rn;
-    if (n >= kCoefs && !wait(&sm.ctl.coef_empty[n % kCoefs], n / kCoefs - 1)) return;
-    if (!meet(wait)) return;
+    if (n >= kCoefs && !wait(&sm.ctl.coef_empty[n % kCoefs], n / kCoefs - 1)) return false;
+    if (!meet(wait)) return false;
     // ---- factors
     const float hi = G.hi[r], lo = G.lo[r];
     const float eg = tc::ex2(hi + lo);
@@ -539,14 +530,14 @@ __device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait
     const float off =
         blk > 0 ? fac * tc::ex2((hi - G.hi[blk * kB - 1]) + (lo - G.lo[blk * kB - 1])) : 0.0f;
     warp_arrive(&sm.ctl.coef_full[n % kCoefs]);
-    if (!meet(wait)) return;
+    if (!meet(wait)) return false;
     // ---- A and the scores from [K; Q] K^T: row r times the factors of its
     // columns, e^{G_i - G_j} as two factors at most 1 around the block's start
-    if (!wait(&sm.ctl.d1_full, n)) return;
+    if (!wait(&sm.ctl.d1_full, n)) return false;
     tc::fence_after();
     if (is_k ? n >= 1 && !wait(&sm.ctl.a_empty, n - 1)
              : n >= 2 && !wait(&sm.ctl.tp_empty[bf], (n >> 1) - 1))
-      return;
+      return false;
     unsigned char* const scores = sm.tp[bf] + 2 * kTBytes;
     const uint32_t d1 = tmem + kColD1 + ((uint32_t)(warp * 32) << 16);
 #pragma unroll 1
@@ -601,8 +592,9 @@ __device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait
       warp_arrive(&sm.ctl.t_full);
     }
     warp_arrive(&sm.ctl.gate_empty[bf]);
-    if (!meet(wait)) return;     // ed, tab and rn are free for the next chunk
+    if (!meet(wait)) return false;     // ed, tab and rn are free for the next chunk
   }
+  return true;
 }
 
 // T of every chunk, by two warps: forward substitution of the four diagonal
@@ -610,7 +602,7 @@ __device__ __forceinline__ void prep_role(const GdnArgs& a, Smem& sm, const Wait
 // block products by the first warp and seven by the second. What is built is T
 // with its columns scaled by beta, (diag(1 / beta) + A)^-1 for the A without
 // beta that the scores' warps wrote: rows t_i = beta_i (e_i - sum_k A_ik t_k).
-__device__ __forceinline__ void inv_role(Smem& sm, const Wait& wait, int chunks) {
+__device__ __forceinline__ bool inv_role(Smem& sm, const Wait& wait, int chunks) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kWarpInv0;
   const int blk = warp * 2 + (lane >> 4), c = lane & (kB - 1), b0 = blk * kB;
   Meet meet{&sm.ctl.inv_meet, 0};
@@ -618,8 +610,8 @@ __device__ __forceinline__ void inv_role(Smem& sm, const Wait& wait, int chunks)
     const int bf = n & 1;
     const Gate& G = sm.gate[bf];
     unsigned char* const tp = sm.tp[bf];
-    if (!wait(&sm.ctl.a_full, n)) return;
-    if (n >= 2 && !wait(&sm.ctl.tp_empty[bf], (n >> 1) - 1)) return;
+    if (!wait(&sm.ctl.a_full, n)) return false;
+    if (n >= 2 && !wait(&sm.ctl.tp_empty[bf], (n >> 1) - 1)) return false;
     float t[kB];
 #pragma unroll
     for (int i = 0; i < kB; ++i) {
@@ -641,15 +633,16 @@ __device__ __forceinline__ void inv_role(Smem& sm, const Wait& wait, int chunks)
       *reinterpret_cast<uint4*>(tp + sw128(b0 + c, blk * 2 + u)) = h;
       *reinterpret_cast<uint4*>(tp + kTBytes + sw128(b0 + c, blk * 2 + u)) = l;
     }
-    if (!meet(wait)) return;
+    if (!meet(wait)) return false;
 #pragma unroll 1
     for (int J = warp; J < 1 + 2 * warp; ++J) t_blocks(sm, tp, J);   // 0, and 1 with 2
     fence_proxy_async();
     warp_arrive(&sm.ctl.t_full);
     warp_arrive(&sm.ctl.a_empty);
     warp_arrive(&sm.ctl.gate_empty[bf]);
-    if (!meet(wait)) return;     // the diagonal blocks have been read
+    if (!meet(wait)) return false;     // the diagonal blocks have been read
   }
+  return true;
 }
 
 // ---- the warps on the chain -------------------------------------------------
@@ -661,7 +654,7 @@ __device__ __forceinline__ void inv_role(Smem& sm, const Wait& wait, int chunks)
 // does between two products is short then; with two, the chain was a third
 // longer.)
 template <typename ST>
-__device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait& wait,
+__device__ __forceinline__ bool scan_role(const GdnArgs& a, Smem& sm, const Wait& wait,
                                           uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int qd = warp & 3, qt = warp >> 2;
@@ -714,7 +707,7 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
       // ---- S: add the last chunk's update, split, hand to the tensor cores
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        if (m > 0 && !advance(n - 1, p)) return;
+        if (m > 0 && !advance(n - 1, p)) return false;
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -727,7 +720,7 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
       }
       if (m > 0) warp_arrive(&sm.ctl.coef_empty[(n - 1) % kCoefs]);
       // ---- R
-      if (!wait(&sm.ctl.coef_full[n % kCoefs], n / kCoefs) || !wait(&sm.ctl.ks_full, n)) return;
+      if (!wait(&sm.ctl.coef_full[n % kCoefs], n / kCoefs) || !wait(&sm.ctl.ks_full, n)) return false;
       tc::fence_after();
       uint32_t x[16];
       tc::ld16(tl + kColKS + qt * 16, x);
@@ -737,7 +730,7 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
       tc::fence_before();
       warp_arrive(&sm.ctl.r_full);
       // ---- N
-      if (!wait(&sm.ctl.vn_full, n)) return;
+      if (!wait(&sm.ctl.vn_full, n)) return false;
       tc::fence_after();
       tc::ld16(tl + kColVN + qt * 16, x);
       tc::wait_ld(x);
@@ -751,7 +744,7 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
       tc::fence_before();
       warp_arrive(&sm.ctl.vd_full);
     }
-    if (!advance(n - 1, 0) || !advance(n - 1, 1)) return;
+    if (!advance(n - 1, 0) || !advance(n - 1, 1)) return false;
     warp_arrive(&sm.ctl.coef_empty[(n - 1) % kCoefs]);
     if (ch.slot >= 0)
 #pragma unroll
@@ -761,11 +754,12 @@ __device__ __forceinline__ void scan_role(const GdnArgs& a, Smem& sm, const Wait
             sp + ((i >> 4) * 64 + (i & 15)) * kD) = raw;
       }
   }
+  return true;
 }
 
 // Outputs: a warp takes 32 columns, 16 tokens at a time, turns them round in
 // the chunk's V, which has been used, and stores 16-byte units.
-__device__ __forceinline__ void out_role(const GdnArgs& a, Smem& sm, const Wait& wait,
+__device__ __forceinline__ bool out_role(const GdnArgs& a, Smem& sm, const Wait& wait,
                                          uint32_t tmem) {
   const int qd = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
@@ -775,7 +769,7 @@ __device__ __forceinline__ void out_role(const GdnArgs& a, Smem& sm, const Wait&
     char* const op = a.out + ((int64_t)ch.row0 * a.out_rs + (int64_t)ch.h * kD + qd * 32) * 2 +
                      (lane & 3) * 16;
     for (int m = 0; m < ch.chunks; ++m, ++n) {
-      if (!wait(&sm.ctl.o_full, n)) return;
+      if (!wait(&sm.ctl.o_full, n)) return false;
       tc::fence_after();
       unsigned char* const box = sm.stage[n % kStages] + kKQBytes + qd * 4096;
 #pragma unroll 1
@@ -819,6 +813,7 @@ __device__ __forceinline__ void out_role(const GdnArgs& a, Smem& sm, const Wait&
       warp_arrive(&sm.ctl.v_empty[n % kStages]);
     }
   }
+  return true;
 }
 
 // ---- the warp that issues the tensor products -------------------------------
@@ -826,7 +821,7 @@ __device__ __forceinline__ void out_role(const GdnArgs& a, Smem& sm, const Wait&
 // On the chain: S^T k (16 products of N = 64, 512 clocks), T R (12, 384), the
 // update (16, 512). Beside it: S^T q, in-chunk outputs, and, while the chain's
 // warps work on S, T V of this chunk and the scores of the next ones.
-__device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks, uint32_t tmem) {
+__device__ __forceinline__ bool mma_role(Smem& sm, const Wait& wait, int chunks, uint32_t tmem) {
   constexpr uint32_t kId = tc::idesc(128, 64), kIdT = tc::idesc(128, 64, false, true),
                      kIdV = tc::idesc(128, 64, true, true);
   // descriptors of the first stage and T buffer; others lie a constant further
@@ -861,7 +856,7 @@ __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks,
       uint64_t* const full = &sm.ctl.full[scored % kStages];
       if ((must || step == 0) && scored <= n) {
         if (!wait(full, scored / kStages) || (scored > 0 && !wait(&sm.ctl.d1_empty, scored - 1)))
-          return;
+          return false;
       }
       if (scored < chunks &&
           __any_sync(0xffffffffu, tc::mbar_ready(full, (scored / kStages) & 1)) &&
@@ -881,7 +876,7 @@ __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks,
       // (chunk n - 1's N has been read: its update, which needed it, is issued)
       if (must && scored > n &&
           (!wait(&sm.ctl.t_full, n) || !wait(&sm.ctl.v_full[st], n / kStages)))
-        return;
+        return false;
       if (tved == n && scored > n &&
           __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.t_full, n & 1)) &&
           __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.v_full[st], (n / kStages) & 1))) {
@@ -900,9 +895,9 @@ __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks,
       }
     }
     if (sub < 2) {
-      if (!wait(&sm.ctl.full[st], n / kStages) || !wait(&sm.ctl.s_full[sub], n)) return;
+      if (!wait(&sm.ctl.full[st], n / kStages) || !wait(&sm.ctl.s_full[sub], n)) return false;
       // N of the last chunk lies where S^T k goes
-      if (sub == 0 && n > 0 && !wait(&sm.ctl.o_full, n - 1)) return;
+      if (sub == 0 && n > 0 && !wait(&sm.ctl.o_full, n - 1)) return false;
       tc::fence_after();
       const uint32_t s0 = tmem + kColS + sub * 64;
       const uint64_t kp = kq + ((sub * kPanel) >> 4);
@@ -917,7 +912,7 @@ __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks,
       }
       __syncwarp();
       if (sub == 1) {
-        if (n > 0 && !wait(&sm.ctl.o_empty, n - 1)) return;
+        if (n > 0 && !wait(&sm.ctl.o_empty, n - 1)) return false;
         tc::fence_after();
         if (tc::elect()) {
 #pragma unroll
@@ -928,7 +923,7 @@ __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks,
         __syncwarp();
       }
     } else if (sub == 2) {
-      if (!wait(&sm.ctl.r_full, n)) return;
+      if (!wait(&sm.ctl.r_full, n)) return false;
       tc::fence_after();
       if (tc::elect()) {
 #pragma unroll
@@ -941,7 +936,7 @@ __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks,
       }
       __syncwarp();
     } else {
-      if (!wait(&sm.ctl.vd_full, n) || !wait(&sm.ctl.qs_done, n)) return;
+      if (!wait(&sm.ctl.vd_full, n) || !wait(&sm.ctl.qs_done, n)) return false;
       tc::fence_after();
       if (tc::elect()) {
 #pragma unroll
@@ -965,6 +960,7 @@ __device__ __forceinline__ void mma_role(Smem& sm, const Wait& wait, int chunks,
       __syncwarp();
     }
   }
+  return true;
 }
 
 template <typename ST>
@@ -1013,7 +1009,6 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
     mbar_init(&c.o_full, 1);
     mbar_init(&c.o_empty, kOutWarps);
     mbar_init(&c.fin, 1);
-    c.abort = 0;
     fence_mbar_init();
   }
   // blocks of U left of the diagonal are zero in both buffers: rows [16, 64),
@@ -1035,29 +1030,31 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm.ctl.tmem, 0);
-  const Wait wait{&sm.ctl, a.dev_err};
+  const Wait wait;
+  bool ok = true;
 
   if (warp < kScanWarps) {
-    scan_role<ST>(a, sm, wait, tmem);
+    ok = scan_role<ST>(a, sm, wait, tmem);
   } else if (warp < kWarpInv0) {
     more_regs<kRegsPrep>();
-    prep_role(a, sm, wait, chunks, tmem);
+    ok = prep_role(a, sm, wait, chunks, tmem);
   } else if (warp < kWarpOut0) {
     if (warp < kWarpMma) {
-      inv_role(sm, wait, chunks);
+      ok = inv_role(sm, wait, chunks);
     } else if (warp == kWarpMma) {
-      mma_role(sm, wait, chunks, tmem);
+      ok = mma_role(sm, wait, chunks, tmem);
       // every product that was issued ends before tensor memory is given back
       if (tc::elect()) tc::commit(&sm.ctl.fin);
       __syncwarp();
-      drain(&sm.ctl.fin, 0, a.dev_err);
+      if (!wait(&sm.ctl.fin, 0)) ok = false;
     } else {
-      load_role(a, maps, sm, wait);
+      ok = load_role(a, maps, sm, wait);
     }
   } else {
     fewer_regs<kRegsOut>();
-    out_role(a, sm, wait, tmem);
+    ok = out_role(a, sm, wait, tmem);
   }
+  if (!ok && (tid & 31) == 0) flag_error(a.dev_err, CCONV_DERR_TIMEOUT);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
