@@ -286,10 +286,11 @@ __device__ __forceinline__ bool load_role(const GdnArgs& a, const Maps& maps, Sm
   for (int n = 0; n < c.chunks; ++n, ++g) {
     const int st = g % kStages;
     if (g >= kStages && !wait(&sm.ctl.empty[st], g / kStages - 1)) goto quit;
+    const int tok = n * kC + lane;
     float na[2], nb[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int t = n * kC + i * 32 + lane;
+      const int t = tok + i * 32;
       na[i] = t < len ? elem(ga, (int64_t)(row0 + t) * a.a_rs) : 0.0f;
       nb[i] = t < len ? elem(gb, (int64_t)(row0 + t) * a.b_rs) : 0.0f;
     }
@@ -299,11 +300,10 @@ __device__ __forceinline__ bool load_role(const GdnArgs& a, const Maps& maps, Sm
     const uint32_t at = smem_addr(sm.stage[st]);
     auto rows = [&](uint32_t dst, uint32_t pitch, const char* src, int64_t stride) {
 #pragma unroll 1
-      for (int i = 0; i < kC / 2; ++i) {
-        const int r = i * 2 + r2;
-        const int64_t t = (int64_t)n * kC + r;
-        const bool in = t < len;
-        cp_async16(dst + (u >> 3) * pitch + sw128(r, u & 7), src + (in ? t : 0) * stride * 2, in);
+      for (int i = r2; i < kC; i += 2) {
+        const bool in = n * kC + i < len;
+        cp_async16(dst + (u >> 3) * pitch + sw128(i, u & 7),
+                   src + (int64_t)(in ? n * kC + i : 0) * stride * 2, in);
       }
     };
     if (whole) {
@@ -322,42 +322,38 @@ __device__ __forceinline__ bool load_role(const GdnArgs& a, const Maps& maps, Sm
       rows(at + kC * 128, kPanel, qp, a.q_rs);
       cp_async_commit();
     }
-    float w[2], f[2], be[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const bool in = n * kC + i * 32 + lane < len;
-      const float x = na[i] + dtb;
-      float g = A_log2 * (fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))));
-      // a decay below 2^-150 is zero in fp32 whatever follows (a NaN stays one)
-      g = in ? (g < -150.0f ? -150.0f : g) : 0.0f;
-      be[i] = in ? gdn_beta(nb[i]) : 0.0f;
-      w[i] = truncf(g);
-      f[i] = g - w[i];
-    }
-    auto add = [](float& w0, float& f0, float w1, float f1) {
-      const float s = f0 + f1, c = truncf(s);
-      w0 += w1 + c;
-      f0 = s - c;
-    };
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float ow = __shfl_up_sync(0xffffffffu, w[i], d);
-        const float of = __shfl_up_sync(0xffffffffu, f[i], d);
-        if (lane >= d) add(w[i], f[i], ow, of);
-      }
-    add(w[1], f[1], __shfl_sync(0xffffffffu, w[0], 31), __shfl_sync(0xffffffffu, f[0], 31));
     if (g >= 2 && !wait(&sm.ctl.gate_empty[g & 1], (g >> 1) - 1)) {
       warp_arrive(&sm.ctl.full[st]);
       goto quit;
     }
     Gate& G = sm.gate[g & 1];
-#pragma unroll
+    float w0 = 0.0f, f0 = 0.0f;                    // sums so far
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
-      G.hi[i * 32 + lane] = w[i];
-      G.lo[i * 32 + lane] = f[i];
-      G.beta[i * 32 + lane] = be[i];
+      const bool in = tok + i * 32 < len;
+      const float x = (i == 0 ? na[0] : na[1]) + dtb;
+      float gl = A_log2 * (fmaxf(x, 0.0f) + log1pf(__expf(-fabsf(x))));
+      // a decay below 2^-150 is zero in fp32 whatever follows (a NaN stays one)
+      gl = in ? (gl < -150.0f ? -150.0f : gl) : 0.0f;
+      float w = truncf(gl), f = gl - w;
+      auto add = [&](float ow, float of) {
+        const float s = f + of, c = truncf(s);
+        w += ow + c;
+        f = s - c;
+      };
+#pragma unroll 1
+      for (int d = 1; d < 32; d <<= 1) {
+        const float ow = __shfl_up_sync(0xffffffffu, w, d);
+        const float of = __shfl_up_sync(0xffffffffu, f, d);
+        if (lane >= d) add(ow, of);
+      }
+      add(w0, f0);
+      w0 = __shfl_sync(0xffffffffu, w, 31);
+      f0 = __shfl_sync(0xffffffffu, f, 31);
+      G.hi[i * 32 + lane] = w;
+      G.lo[i * 32 + lane] = f;
+      G.beta[i * 32 + lane] =
+          in ? __fdividef(1.0f, 1.0f + __expf(-(i == 0 ? nb[0] : nb[1]))) : 0.0f;
     }
     if (!whole) {
       cp_async_wait<0>();
@@ -477,7 +473,7 @@ __device__ __forceinline__ bool prep_role(const GdnArgs& a, Smem& sm, const Wait
     float rn = 1.0f;
     if (a.l2norm) {
       float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
-#pragma unroll
+#pragma unroll 4
       for (int u = 0; u < 16; ++u) {
         const uint4 x = *reinterpret_cast<const uint4*>(sm.stage[st] + (u >> 3) * kPanel +
                                                         sw128(p, u & 7));
@@ -491,7 +487,7 @@ __device__ __forceinline__ bool prep_role(const GdnArgs& a, Smem& sm, const Wait
           fma_x2(s2, s3, b0, b1, b0, b1, s2, s3);
         }
       }
-      rn = 1.0f / sqrtf((s0 + s1) + (s2 + s3) + kGdnNormEps);
+      rn = rsqrtf((s0 + s1) + (s2 + s3) + kGdnNormEps);
     }
     sm.rn[p] = rn;
     if (n >= kCoefs && !wait(&sm.ctl.coef_empty[n % kCoefs], n / kCoefs - 1)) return false;
