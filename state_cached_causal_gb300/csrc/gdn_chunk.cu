@@ -79,7 +79,6 @@ constexpr uint32_t kTP = 3 * kTBytes;        // T hi, T lo, scores
 constexpr int kMaxSeqs = 640;                // sequences of a launch
 constexpr int kB = 16;                       // blocks of A and T
 constexpr int kBPitch = 20;                  // fp32 rows of 16: 80 bytes
-constexpr int kAPitch = 56;                  // bf16 rows of 48: 112 bytes
 constexpr int kCoefs = 4;                    // chunks whose factors are kept
 
 constexpr uint32_t kColS = 0, kColKS = 128, kColN = kColKS, kColQS = 192, kColR = 256,
@@ -104,11 +103,26 @@ struct Maps {
   CUtensorMap k, q, v;   // [tokens, heads * 128], boxes of 64 x 64 in the 128-byte swizzle
 };
 
+// A of a chunk: diagonal blocks in fp32, the blocks left of them as bf16 hi and
+// lo (block (i, k) at i (i - 1) / 2 + k); 16-byte units permuted by row so that
+// rows written or read together fall into different banks.
+struct alignas(16) Blocks {
+  float d[kC * kB];
+  uint16_t hi[6 * kB * kB], lo[6 * kB * kB];
+};
+__device__ __forceinline__ int a_diag(int row, int unit) {          // index of 4 floats
+  return row * kB + ((unit ^ ((row >> 1) & 3)) << 2);
+}
+__device__ __forceinline__ int a_left(int i, int k, int row, int unit) {   // of 8 bf16
+  return ((i * (i - 1) / 2 + k) * kB + row) * kB + ((unit ^ ((row >> 2) & 1)) << 3);
+}
+
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
   uint64_t gate_empty[2], tp_empty[2], coef_full[kCoefs], coef_empty[kCoefs];
   uint64_t v_full[kStages], v_empty[kStages];
-  uint64_t d1_full, d1_empty, a_full, a_empty, t_full, prep_meet, inv_meet;
+  uint64_t a_full[2], a_empty[2];
+  uint64_t d1_full, d1_empty, t_full, prep_meet, inv_meet;
   uint64_t s_full[2], sd_full[2];
   uint64_t ks_full, qs_done, r_full, vn_full, vd_full, o_full, o_empty, fin;
   uint32_t tmem;
@@ -117,9 +131,7 @@ struct Ctl {
 struct Smem {
   unsigned char stage[kStages][kStageBytes];   // 1024-byte aligned
   unsigned char tp[2][kTP];
-  alignas(16) float Ad[kC][kBPitch];           // A: diagonal blocks
-  alignas(16) uint16_t Ah[kC - kB][kAPitch];   // and rows 16 .. of the blocks left of them,
-  alignas(16) uint16_t Al[kC - kB][kAPitch];   // bf16 hi and lo
+  Blocks A[2];
   alignas(16) float ed[kC][kBPitch];           // e^{G_i - G_j} / |k_j|, j in the block of i
   alignas(16) float tab[4][kC];                // e^{G_(16I-1) - G_j} / |k_j|, j < 16 I
   alignas(16) float rn[2 * kC];                // 1 / |k|, 1 / |q|
@@ -132,8 +144,8 @@ struct Smem {
 static_assert(offsetof(Smem, tp) % 1024 == 0 && kStageBytes % 1024 == 0 && kTP % 1024 == 0 &&
                   kTBytes % 1024 == 0 && kVPanel % 1024 == 0,
               "swizzled tiles start on 1024 bytes");
-static_assert(sizeof(Coef) % 16 == 0 && sizeof(Gate) % 16 == 0 && offsetof(Smem, Ad) % 16 == 0 &&
-                  offsetof(Smem, Ah) % 16 == 0 && offsetof(Smem, Al) % 16 == 0 && offsetof(Smem, ed) % 16 == 0 &&
+static_assert(sizeof(Coef) % 16 == 0 && sizeof(Gate) % 16 == 0 && sizeof(Blocks) % 16 == 0 &&
+                  offsetof(Smem, A) % 16 == 0 && offsetof(Smem, ed) % 16 == 0 &&
                   offsetof(Smem, tab) % 16 == 0 && offsetof(Smem, rn) % 16 == 0 &&
                   offsetof(Smem, coef) % 16 == 0 && offsetof(Smem, gate) % 16 == 0 &&
                   offsetof(Smem, ctl) % 8 == 0,
@@ -399,61 +411,110 @@ __device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
   tc::split2(x[6], x[7], hi.w, lo.w);
 }
 
-// The 16 x 16 blocks of T below diagonal block J. With U = T^T, which is how T
-// is stored for the tensor cores,
-//   U_Ji = -(sum_{J <= k < i} U_Jk A_ik^T) U_ii:
-// both factors and A as they lie in shared memory. The sum passes to the second
-// product in registers, where the output layout of one warp product is the
-// input layout of the next. Products of hi and lo parts as everywhere (lo * lo
-// left out), the mixed ones in a sum of their own: shorter chains.
-__device__ __forceinline__ void t_blocks(const Smem& sm, unsigned char* tp, int J) {
-  const int lane = threadIdx.x & 31, r = lane >> 2, c = (lane & 3) * 2;
-  const int lrow = lane & 15, lcol = (lane >> 4) * 8;    // ldmatrix: row and column of the lane
-  const uint32_t u0 = smem_addr(tp) + (J * kB + lrow) * 128;
-#pragma unroll 1
-  for (int i = J + 1; i < 4; ++i) {
-    float x[2][4] = {}, xm[2][4] = {};
-#pragma unroll 1
-    for (int k = J; k < i; ++k) {
-      uint32_t uh[4], ul[4], h[4], l[4];      // right operand of n-tile nt: registers nt, nt + 2
-      const uint32_t at = u0 + (((k * 2 + (lane >> 4)) ^ (lrow & 7)) << 4);
-      tc::ldmatrix4(uh, at);
-      tc::ldmatrix4(ul, at + kTBytes);
-      tc::ldmatrix4(h, smem_addr(&sm.Ah[(i - 1) * kB + lrow][k * kB + lcol]));
-      tc::ldmatrix4(l, smem_addr(&sm.Al[(i - 1) * kB + lrow][k * kB + lcol]));
+// The 16 x 16 blocks of T below the diagonal, by two warps. With U = T^T, which
+// is how T is stored for the tensor cores,
+//   U_Ji = -(sum_{J <= k < i} U_Jk A_ik^T) U_ii
+// is taken in two levels of 32 x 32 blocks: first U_01 (warp 0) and U_23 (warp 1),
+// then, for J = 0 and 1, X_2 = sum_k U_Jk A_2k^T and X_3 = sum_k U_Jk A_3k^T over k =
+// J .. 1, and U_J2 = -X_2 U_22, U_J3 = -(X_2 U_23 + X_3 U_33). Factors and A are
+// read as they lie in shared memory; X passes to its second product in
+// registers, where the output layout of one warp product is the input layout
+// of the next. Products of hi and lo parts as everywhere (lo * lo left out), the
+// mixed ones in a sum of their own: shorter chains.
+struct Sum {
+  float x[2][4], m[2][4];       // hi * hi, mixed; two tiles of 8 columns
+};
+template <bool PAIRS>
+__device__ __forceinline__ void mul_add(Sum& s, const uint32_t (&ah)[4], const uint32_t (&al)[4],
+                                        const uint32_t (&bh)[4], const uint32_t (&bl)[4]) {
+  // right operand of tile nt: registers 2 nt, 2 nt + 1 (PAIRS) or nt, nt + 2
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        tc::mma16(x[nt], uh, h[nt], h[nt + 2]);
-        tc::mma16(xm[nt], uh, l[nt], l[nt + 2]);
-        tc::mma16(xm[nt], ul, h[nt], h[nt + 2]);
-      }
-    }
-    uint32_t xh[4], xl[4], h[4], l[4];        // right operand of n-tile nt: 2 nt, 2 nt + 1
-    const uint32_t ui = smem_addr(tp) + sw128(i * kB + lrow, i * 2 + (lane >> 4));
-    tc::ldmatrix4_trans(h, ui);
-    tc::ldmatrix4_trans(l, ui + kTBytes);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      tc::split2(x[e >> 1][(e & 1) * 2] + xm[e >> 1][(e & 1) * 2],
-                 x[e >> 1][(e & 1) * 2 + 1] + xm[e >> 1][(e & 1) * 2 + 1], xh[e], xl[e]);
-    float y[2][4] = {}, ym[2][4] = {};
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      tc::mma16(y[nt], xh, h[2 * nt], h[2 * nt + 1]);
-      tc::mma16(ym[nt], xh, l[2 * nt], l[2 * nt + 1]);
-      tc::mma16(ym[nt], xl, h[2 * nt], h[2 * nt + 1]);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {   // rows r, r + 8 (e & 1) of n-tile e >> 1
-      uint32_t sh, sl;
-      tc::split2(-(y[e >> 1][(e & 1) * 2] + ym[e >> 1][(e & 1) * 2]),
-                 -(y[e >> 1][(e & 1) * 2 + 1] + ym[e >> 1][(e & 1) * 2 + 1]), sh, sl);
-      const uint32_t at = sw128(J * kB + r + (e & 1) * 8, i * 2 + (e >> 1)) + c * 2;
-      *reinterpret_cast<uint32_t*>(tp + at) = sh;
-      *reinterpret_cast<uint32_t*>(tp + kTBytes + at) = sl;
-    }
-    __syncwarp();
+  for (int nt = 0; nt < 2; ++nt) {
+    const int i0 = PAIRS ? 2 * nt : nt, i1 = PAIRS ? 2 * nt + 1 : nt + 2;
+    tc::mma16(s.x[nt], ah, bh[i0], bh[i1]);
+    tc::mma16(s.m[nt], ah, bl[i0], bl[i1]);
+    tc::mma16(s.m[nt], al, bh[i0], bh[i1]);
   }
+}
+// The sum times `sign` as a left operand, hi and lo.
+__device__ __forceinline__ void to_left(const Sum& s, float sign, uint32_t (&h)[4],
+                                        uint32_t (&l)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    tc::split2(sign * (s.x[e >> 1][(e & 1) * 2] + s.m[e >> 1][(e & 1) * 2]),
+               sign * (s.x[e >> 1][(e & 1) * 2 + 1] + s.m[e >> 1][(e & 1) * 2 + 1]), h[e], l[e]);
+}
+struct TWarp {
+  const Blocks& A;
+  unsigned char* tp;
+  int lane, lrow, lu;           // lane; its row and unit of a block for ldmatrix
+  __device__ __forceinline__ void left(int J, int k, uint32_t (&h)[4], uint32_t (&l)[4]) const {
+    const uint32_t at = smem_addr(tp) + sw128(J * kB + lrow, k * 2 + lu);       // U_Jk
+    tc::ldmatrix4(h, at);
+    tc::ldmatrix4(l, at + kTBytes);
+  }
+  __device__ __forceinline__ void right(int i, int k, uint32_t (&h)[4], uint32_t (&l)[4]) const {
+    const uint32_t at = smem_addr(tp) + sw128(i * kB + lrow, k * 2 + lu);       // U_ik
+    tc::ldmatrix4_trans(h, at);
+    tc::ldmatrix4_trans(l, at + kTBytes);
+  }
+  __device__ __forceinline__ void a_right(int i, int k, uint32_t (&h)[4],
+                                          uint32_t (&l)[4]) const {             // A_ik^T
+    const int at = a_left(i, k, lrow, lu);
+    tc::ldmatrix4(h, smem_addr(&A.hi[at]));
+    tc::ldmatrix4(l, smem_addr(&A.lo[at]));
+  }
+  // U_Ji, from its left-operand form
+  __device__ __forceinline__ void put(int J, int i, const uint32_t (&h)[4],
+                                      const uint32_t (&l)[4]) const {
+    const int r = lane >> 2, c = (lane & 3) * 2;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {      // rows r, r + 8 (e & 1) of tile e >> 1
+      const uint32_t at = sw128(J * kB + r + (e & 1) * 8, i * 2 + (e >> 1)) + c * 2;
+      *reinterpret_cast<uint32_t*>(tp + at) = h[e];
+      *reinterpret_cast<uint32_t*>(tp + kTBytes + at) = l[e];
+    }
+  }
+};
+__device__ __forceinline__ bool t_blocks(const TWarp& w, int warp, Meet& meet, const Wait& wait) {
+  uint32_t uh[4], ul[4], bh[4], bl[4], xh[4], xl[4];
+  {                                    // U_01 or U_23
+    const int J = warp * 2;
+    Sum x = {}, y = {};
+    w.left(J, J, uh, ul);
+    w.a_right(J + 1, J, bh, bl);
+    mul_add<false>(x, uh, ul, bh, bl);
+    w.right(J + 1, J + 1, bh, bl);
+    to_left(x, 1.0f, xh, xl);
+    mul_add<true>(y, xh, xl, bh, bl);
+    to_left(y, -1.0f, xh, xl);
+    w.put(J, J + 1, xh, xl);
+  }
+  if (!meet(wait)) return false;
+  const int J = warp;
+  Sum x2 = {}, x3 = {};
+#pragma unroll 1
+  for (int k = J; k < 2; ++k) {
+    w.left(J, k, uh, ul);
+    w.a_right(2, k, bh, bl);
+    mul_add<false>(x2, uh, ul, bh, bl);
+    w.a_right(3, k, bh, bl);
+    mul_add<false>(x3, uh, ul, bh, bl);
+  }
+  Sum y2 = {}, y3 = {};
+  to_left(x2, 1.0f, xh, xl);
+  w.right(2, 2, bh, bl);
+  mul_add<true>(y2, xh, xl, bh, bl);
+  w.right(2, 3, bh, bl);
+  mul_add<true>(y3, xh, xl, bh, bl);
+  to_left(x3, 1.0f, uh, ul);
+  w.right(3, 3, bh, bl);
+  mul_add<true>(y3, uh, ul, bh, bl);
+  to_left(y2, -1.0f, xh, xl);
+  w.put(J, 2, xh, xl);
+  to_left(y3, -1.0f, xh, xl);
+  w.put(J, 3, xh, xl);
+  return true;
 }
 
 // Norms, factors, A, scores and T of every chunk. Thread p < 64 holds row p of
@@ -531,8 +592,7 @@ __device__ __forceinline__ bool prep_role(const GdnArgs& a, Smem& sm, const Wait
     // columns, e^{G_i - G_j} as two factors at most 1 around the block's start
     if (!wait(&sm.ctl.d1_full, n)) return false;
     tc::fence_after();
-    if (is_k ? n >= 1 && !wait(&sm.ctl.a_empty, n - 1)
-             : n >= 2 && !wait(&sm.ctl.tp_empty[bf], (n >> 1) - 1))
+    if (n >= 2 && !wait(is_k ? &sm.ctl.a_empty[bf] : &sm.ctl.tp_empty[bf], (n >> 1) - 1))
       return false;
     unsigned char* const scores = sm.tp[bf] + 2 * kTBytes;
     const uint32_t d1 = tmem + kColD1 + ((uint32_t)(warp * 32) << 16);
@@ -560,13 +620,14 @@ __device__ __forceinline__ bool prep_role(const GdnArgs& a, Smem& sm, const Wait
           for (int u = 0; u < 2; ++u) {
             uint4 h, l;
             split8(y + u * 8, h, l);
-            *reinterpret_cast<uint4*>(&sm.Ah[r - kB][J * kB + u * 8]) = h;
-            *reinterpret_cast<uint4*>(&sm.Al[r - kB][J * kB + u * 8]) = l;
+            const int at = a_left(blk, J, r & (kB - 1), u);
+            *reinterpret_cast<uint4*>(&sm.A[bf].hi[at]) = h;
+            *reinterpret_cast<uint4*>(&sm.A[bf].lo[at]) = l;
           }
         } else if (J == blk) {
 #pragma unroll
           for (int j4 = 0; j4 < 16; j4 += 4)
-            *reinterpret_cast<float4*>(&sm.Ad[r][j4]) =
+            *reinterpret_cast<float4*>(&sm.A[bf].d[a_diag(r, j4 >> 2)]) =
                 make_float4(y[j4], y[j4 + 1], y[j4 + 2], y[j4 + 3]);
         }
       } else {
@@ -582,7 +643,7 @@ __device__ __forceinline__ bool prep_role(const GdnArgs& a, Smem& sm, const Wait
     tc::fence_before();
     warp_arrive(&sm.ctl.d1_empty);
     if (is_k) {
-      warp_arrive(&sm.ctl.a_full);
+      warp_arrive(&sm.ctl.a_full[bf]);
     } else {
       fence_proxy_async();
       warp_arrive(&sm.ctl.t_full);
@@ -594,9 +655,8 @@ __device__ __forceinline__ bool prep_role(const GdnArgs& a, Smem& sm, const Wait
 }
 
 // T of every chunk, by two warps: forward substitution of the four diagonal
-// blocks (a lane a column, two blocks a warp), then the blocks below them, nine
-// block products by the first warp and seven by the second. What is built is T
-// with its columns scaled by beta, (diag(1 / beta) + A)^-1 for the A without
+// blocks (a lane a column, two blocks a warp), then the blocks below them. What
+// is built is T with its columns scaled by beta, (diag(1 / beta) + A)^-1 for the A without
 // beta that the scores' warps wrote: rows t_i = beta_i (e_i - sum_k A_ik t_k).
 __device__ __forceinline__ bool inv_role(Smem& sm, const Wait& wait, int chunks) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kWarpInv0;
@@ -606,15 +666,16 @@ __device__ __forceinline__ bool inv_role(Smem& sm, const Wait& wait, int chunks)
     const int bf = n & 1;
     const Gate& G = sm.gate[bf];
     unsigned char* const tp = sm.tp[bf];
-    if (!wait(&sm.ctl.a_full, n)) return false;
+    if (!wait(&sm.ctl.a_full[bf], n >> 1)) return false;
     if (n >= 2 && !wait(&sm.ctl.tp_empty[bf], (n >> 1) - 1)) return false;
+    const Blocks& A = sm.A[bf];
     float t[kB];
 #pragma unroll
     for (int i = 0; i < kB; ++i) {
       float acc[4] = {c == i ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int k4 = 0; k4 < i; k4 += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(&sm.Ad[b0 + i][k4]);
+        const float4 v = *reinterpret_cast<const float4*>(&A.d[a_diag(b0 + i, k4 >> 2)]);
         acc[0] = fmaf(-v.x, t[k4], acc[0]);
         if (k4 + 1 < i) acc[1] = fmaf(-v.y, t[k4 + 1], acc[1]);
         if (k4 + 2 < i) acc[2] = fmaf(-v.z, t[k4 + 2], acc[2]);
@@ -629,14 +690,12 @@ __device__ __forceinline__ bool inv_role(Smem& sm, const Wait& wait, int chunks)
       *reinterpret_cast<uint4*>(tp + sw128(b0 + c, blk * 2 + u)) = h;
       *reinterpret_cast<uint4*>(tp + kTBytes + sw128(b0 + c, blk * 2 + u)) = l;
     }
-    if (!meet(wait)) return false;
-#pragma unroll 1
-    for (int J = warp; J < 1 + 2 * warp; ++J) t_blocks(sm, tp, J);   // 0, and 1 with 2
+    __syncwarp();     // (the first level reads the warp's own blocks)
+    if (!t_blocks(TWarp{A, tp, lane, lane & 15, lane >> 4}, warp, meet, wait)) return false;
     fence_proxy_async();
     warp_arrive(&sm.ctl.t_full);
-    warp_arrive(&sm.ctl.a_empty);
+    warp_arrive(&sm.ctl.a_empty[bf]);
     warp_arrive(&sm.ctl.gate_empty[bf]);
-    if (!meet(wait)) return false;     // the diagonal blocks have been read
   }
   return true;
 }
@@ -983,6 +1042,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.gate_empty[i], kPrepWarps + kInvWarps);
       mbar_init(&c.tp_empty[i], 1);
+      mbar_init(&c.a_full[i], 2);
+      mbar_init(&c.a_empty[i], kInvWarps);
       mbar_init(&c.s_full[i], kScanWarps);
       mbar_init(&c.sd_full[i], 1);
     }
@@ -993,8 +1054,6 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
     }
     mbar_init(&c.prep_meet, kPrepWarps);
     mbar_init(&c.inv_meet, kInvWarps);
-    mbar_init(&c.a_full, 2);
-    mbar_init(&c.a_empty, kInvWarps);
     mbar_init(&c.t_full, 2 + kInvWarps);     // scores, T
     mbar_init(&c.d1_empty, kPrepWarps);
     mbar_init(&c.ks_full, 1);
