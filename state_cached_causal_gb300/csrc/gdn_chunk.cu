@@ -120,9 +120,9 @@ __device__ __forceinline__ int a_left(int i, int k, int row, int unit) {   // of
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
   uint64_t gate_empty[2], tp_empty[2], coef_full[kCoefs], coef_empty[kCoefs];
-  uint64_t v_full[kStages], v_empty[kStages];
-  uint64_t a_full[2], a_empty[2];
-  uint64_t d1_full, d1_empty, t_full, prep_meet, inv_meet;
+  uint64_t rn_full[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t a_full[2], a_empty[2], t_full[2], p_full[2];
+  uint64_t d1_full, d1_empty, prep_meet, inv_meet;
   uint64_t s_full[2], sd_full[2];
   uint64_t ks_full, qs_done, r_full, vn_full, vd_full, o_full, o_empty, fin;
   uint32_t tmem;
@@ -134,7 +134,7 @@ struct Smem {
   Blocks A[2];
   alignas(16) float ed[kC][kBPitch];           // e^{G_i - G_j} / |k_j|, j in the block of i
   alignas(16) float tab[4][kC];                // e^{G_(16I-1) - G_j} / |k_j|, j < 16 I
-  alignas(16) float rn[2 * kC];                // 1 / |k|, 1 / |q|
+  alignas(16) float rn[kStages][2 * kC];        // 1 / |k|, 1 / |q|
   Coef coef[kCoefs];
   Gate gate[2];
   uint16_t order[kMaxSeqs];   // the launch's long sequences, longest first
@@ -529,30 +529,11 @@ __device__ __forceinline__ bool prep_role(const GdnArgs& a, Smem& sm, const Wait
     const int st = n % kStages, bf = n & 1;
     Coef& C = sm.coef[n % kCoefs];
     const Gate& G = sm.gate[bf];
-    // ---- norms
-    if (!wait(&sm.ctl.full[st], n / kStages)) return false;
-    float rn = 1.0f;
-    if (a.l2norm) {
-      float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
-#pragma unroll 4
-      for (int u = 0; u < 16; ++u) {
-        const uint4 x = *reinterpret_cast<const uint4*>(sm.stage[st] + (u >> 3) * kPanel +
-                                                        sw128(p, u & 7));
-        const uint32_t q[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const float a0 = __uint_as_float(q[e] << 16), a1 = __uint_as_float(q[e] & 0xffff0000u);
-          const float b0 = __uint_as_float(q[e + 1] << 16),
-                      b1 = __uint_as_float(q[e + 1] & 0xffff0000u);
-          fma_x2(s0, s1, a0, a1, a0, a1, s0, s1);
-          fma_x2(s2, s3, b0, b1, b0, b1, s2, s3);
-        }
-      }
-      rn = rsqrtf((s0 + s1) + (s2 + s3) + kGdnNormEps);
-    }
-    sm.rn[p] = rn;
+    if (!wait(&sm.ctl.full[st], n / kStages) || !wait(&sm.ctl.rn_full[n % kStages], n / kStages))
+      return false;
+    const float* const rns = sm.rn[n % kStages];
+    const float rn = rns[p];
     if (n >= kCoefs && !wait(&sm.ctl.coef_empty[n % kCoefs], n / kCoefs - 1)) return false;
-    if (!meet(wait)) return false;
     // ---- factors
     const float hi = G.hi[r], lo = G.lo[r];
     const float eg = tc::ex2(hi + lo);
@@ -564,7 +545,7 @@ __device__ __forceinline__ bool prep_role(const GdnArgs& a, Smem& sm, const Wait
       C.o1[r] = a.scale * rn * eg;
     }
     {
-      const float rk = sm.rn[r];
+      const float rk = rns[r];
 #pragma unroll
       for (int I = 1; I < 4; ++I)
         if ((I == 3) == is_k && r < I * kB)
@@ -575,7 +556,7 @@ __device__ __forceinline__ bool prep_role(const GdnArgs& a, Smem& sm, const Wait
         const int j = blk * kB + c0 + c4;
         const float4 h4 = *reinterpret_cast<const float4*>(&G.hi[j]);
         const float4 l4 = *reinterpret_cast<const float4*>(&G.lo[j]);
-        const float4 k4 = *reinterpret_cast<const float4*>(&sm.rn[j]);
+        const float4 k4 = *reinterpret_cast<const float4*>(&rns[j]);
         *reinterpret_cast<float4*>(&sm.ed[r][c0 + c4]) =
             make_float4(j <= r ? k4.x * tc::ex2((hi - h4.x) + (lo - l4.x)) : 0.0f,
                         j + 1 <= r ? k4.y * tc::ex2((hi - h4.y) + (lo - l4.y)) : 0.0f,
@@ -646,7 +627,7 @@ __device__ __forceinline__ bool prep_role(const GdnArgs& a, Smem& sm, const Wait
       warp_arrive(&sm.ctl.a_full[bf]);
     } else {
       fence_proxy_async();
-      warp_arrive(&sm.ctl.t_full);
+      warp_arrive(&sm.ctl.p_full[bf]);
     }
     warp_arrive(&sm.ctl.gate_empty[bf]);
     if (!meet(wait)) return false;     // ed, tab and rn are free for the next chunk
@@ -693,7 +674,7 @@ __device__ __forceinline__ bool inv_role(Smem& sm, const Wait& wait, int chunks)
     __syncwarp();     // (the first level reads the warp's own blocks)
     if (!t_blocks(TWarp{A, tp, lane, lane & 15, lane >> 4}, warp, meet, wait)) return false;
     fence_proxy_async();
-    warp_arrive(&sm.ctl.t_full);
+    warp_arrive(&sm.ctl.t_full[bf]);
     warp_arrive(&sm.ctl.a_empty[bf]);
     warp_arrive(&sm.ctl.gate_empty[bf]);
   }
@@ -813,11 +794,39 @@ __device__ __forceinline__ bool scan_role(const GdnArgs& a, Smem& sm, const Wait
 }
 
 // Outputs: a warp takes 32 columns, 16 tokens at a time, turns them round in
-// the chunk's V, which has been used, and stores 16-byte units.
+// the chunk's V, which has been used, and stores 16-byte units. In between the
+// same warps take the norms of the chunk three further on (a thread a row).
 __device__ __forceinline__ bool out_role(const GdnArgs& a, Smem& sm, const Wait& wait,
-                                         uint32_t tmem) {
+                                         int chunks, uint32_t tmem) {
   const int qd = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
+  auto norms = [&](int m) -> bool {
+    if (m >= chunks) return true;
+    if (!wait(&sm.ctl.full[m % kStages], m / kStages)) return false;
+    const int p = threadIdx.x - kWarpOut0 * 32;         // row of [K; Q]
+    float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+    if (a.l2norm) {
+#pragma unroll 4
+      for (int u = 0; u < 16; ++u) {
+        const uint4 x = *reinterpret_cast<const uint4*>(sm.stage[m % kStages] + (u >> 3) * kPanel +
+                                                        sw128(p, u & 7));
+        const uint32_t q[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          const float a0 = __uint_as_float(q[e] << 16), a1 = __uint_as_float(q[e] & 0xffff0000u);
+          const float b0 = __uint_as_float(q[e + 1] << 16),
+                      b1 = __uint_as_float(q[e + 1] & 0xffff0000u);
+          fma_x2(s0, s1, a0, a1, a0, a1, s0, s1);
+          fma_x2(s2, s3, b0, b1, b0, b1, s2, s3);
+        }
+      }
+    }
+    sm.rn[m % kStages][p] = a.l2norm ? rsqrtf((s0 + s1) + (s2 + s3) + kGdnNormEps) : 1.0f;
+    warp_arrive(&sm.ctl.rn_full[m % kStages]);
+    return true;
+  };
+  for (int m = 0; m < kStages; ++m)
+    if (!norms(m)) return false;
   int n = 0;                                      // chunks of the block so far
   Chain ch;
   for (int k = 0; chain_at(a, sm, k, ch); ++k) {
@@ -866,6 +875,7 @@ __device__ __forceinline__ bool out_role(const GdnArgs& a, Smem& sm, const Wait&
       }
       fence_proxy_async();
       warp_arrive(&sm.ctl.v_empty[n % kStages]);
+      if (!norms(n + kStages)) return false;
     }
   }
   return true;
@@ -889,9 +899,11 @@ __device__ __forceinline__ bool mma_role(Smem& sm, const Wait& wait, int chunks,
     return ((ks >> 2) * kPanel + (ks & 3) * 32 + row * 128) >> 4;
   };
   // Steps of a chunk: S^T k of the first half of dk, of the second (with S^T q),
-  // T R, update. While S is worked on, the pipe is free: the scores of the next
-  // chunk that has none and T V of this one are issued then, as soon as their
-  // operands are there (and at the latest before T R, which needs both).
+  // T R, update. The pipe is free while the chain's warps work: T V of this chunk
+  // is issued while S is worked on, the scores of the next chunk that has none
+  // while R or N is, each as soon as its operands are there (and at the latest
+  // before T R, which needs both). Issued before S^T k, the scores held it up by
+  // 500 clocks.
   int scored = 0, tved = 0;                     // chunks whose products are issued
 #pragma unroll 1
   for (int step = 0; step < 4 * chunks; ++step) {
@@ -900,20 +912,15 @@ __device__ __forceinline__ bool mma_role(Smem& sm, const Wait& wait, int chunks,
     const bool must = sub == 2;
     // polls: bounded like the waits, by the one behind this loop or, before T R,
     // by those inside
+    bool again = sub != 1;
 #pragma unroll 1
-    for (int poll = 0;
-         must ? tved == n
-              : sub == 0 && (step == 0 ? scored == 0
-                                       : poll == 0 || poll < 4096 && !__any_sync(0xffffffffu,
-                                                                    tc::mbar_ready(&sm.ctl.s_full[0],
-                                                                                   n & 1)));
-         ++poll) {
+    for (int poll = 0; again; ++poll) {
       uint64_t* const full = &sm.ctl.full[scored % kStages];
       if ((must || step == 0) && scored <= n) {
         if (!wait(full, scored / kStages) || (scored > 0 && !wait(&sm.ctl.d1_empty, scored - 1)))
           return false;
       }
-      if (scored < chunks &&
+      if (scored < chunks && (sub >= 2 || step == 0 || poll > 0) &&
           __any_sync(0xffffffffu, tc::mbar_ready(full, (scored / kStages) & 1)) &&
           (scored == 0 ||
            __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.d1_empty, (scored - 1) & 1)))) {
@@ -930,10 +937,10 @@ __device__ __forceinline__ bool mma_role(Smem& sm, const Wait& wait, int chunks,
       }
       // (chunk n - 1's N has been read: its update, which needed it, is issued)
       if (must && scored > n &&
-          (!wait(&sm.ctl.t_full, n) || !wait(&sm.ctl.v_full[st], n / kStages)))
+          (!wait(&sm.ctl.t_full[n & 1], n >> 1) || !wait(&sm.ctl.v_full[st], n / kStages)))
         return false;
       if (tved == n && scored > n &&
-          __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.t_full, n & 1)) &&
+          __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.t_full[n & 1], (n >> 1) & 1)) &&
           __any_sync(0xffffffffu, tc::mbar_ready(&sm.ctl.v_full[st], (n / kStages) & 1))) {
         tc::fence_after();
         const uint64_t v = v0 + ((st * kStageBytes) >> 4);
@@ -948,6 +955,10 @@ __device__ __forceinline__ bool mma_role(Smem& sm, const Wait& wait, int chunks,
         __syncwarp();
         ++tved;
       }
+      again = must ? tved == n
+                   : sub == 0 && (step == 0 ? scored == 0
+                                            : poll < 4096 && !__any_sync(0xffffffffu,
+                                                  tc::mbar_ready(&sm.ctl.s_full[0], n & 1)));
     }
     if (sub < 2) {
       if (!wait(&sm.ctl.full[st], n / kStages) || !wait(&sm.ctl.s_full[sub], n)) return false;
@@ -991,7 +1002,9 @@ __device__ __forceinline__ bool mma_role(Smem& sm, const Wait& wait, int chunks,
       }
       __syncwarp();
     } else {
-      if (!wait(&sm.ctl.vd_full, n) || !wait(&sm.ctl.qs_done, n)) return false;
+      if (!wait(&sm.ctl.p_full[n & 1], n >> 1) || !wait(&sm.ctl.vd_full, n) ||
+          !wait(&sm.ctl.qs_done, n))
+        return false;
       tc::fence_after();
       if (tc::elect()) {
 #pragma unroll
@@ -1037,12 +1050,15 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
       mbar_init(&c.full[i], 2);                // rows, gates
       mbar_init(&c.empty[i], 1);
       mbar_init(&c.v_full[i], 1);
+      mbar_init(&c.rn_full[i], kOutWarps);
       mbar_init(&c.v_empty[i], kOutWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.gate_empty[i], kPrepWarps + kInvWarps);
       mbar_init(&c.tp_empty[i], 1);
       mbar_init(&c.a_full[i], 2);
+      mbar_init(&c.p_full[i], 2);
+      mbar_init(&c.t_full[i], kInvWarps);
       mbar_init(&c.a_empty[i], kInvWarps);
       mbar_init(&c.s_full[i], kScanWarps);
       mbar_init(&c.sd_full[i], 1);
@@ -1054,7 +1070,6 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
     }
     mbar_init(&c.prep_meet, kPrepWarps);
     mbar_init(&c.inv_meet, kInvWarps);
-    mbar_init(&c.t_full, 2 + kInvWarps);     // scores, T
     mbar_init(&c.d1_empty, kPrepWarps);
     mbar_init(&c.ks_full, 1);
     mbar_init(&c.qs_done, 1);
@@ -1107,7 +1122,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a
     }
   } else {
     fewer_regs<kRegsOut>();
-    ok = out_role(a, sm, wait, tmem);
+    ok = out_role(a, sm, wait, chunks, tmem);
   }
   if (!ok && (tid & 31) == 0) flag_error(a.dev_err, CCONV_DERR_TIMEOUT);
   tc::fence_before();

@@ -99,6 +99,12 @@ def test_head_layouts(hk, hv):
     check_fwd(12, [90, 20], hk, hv, 128, 128, BF16, BF16)
 
 
+def test_more_chains_than_blocks():
+    """9 sequences of 32 heads: 256 or more chains, several for each block of the persistent kernel,
+    of whole and partial chunks in turn."""
+    check_fwd(21, [70, 9, 128, 1, 64, 33, 130, 12, 65], 16, 32, 128, 128, BF16, F32)
+
+
 @pytest.mark.parametrize("keys,gates", [("equal", "normal"), ("zero", "normal"), ("silu", "ends")])
 @pytest.mark.parametrize("lens", [[130], [5]])
 def test_hard_values(keys, gates, lens):
