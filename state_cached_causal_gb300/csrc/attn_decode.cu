@@ -253,8 +253,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   const int64_t orow = (int64_t)b * a.q_len + rr / a.G;
   const int h = hkv * a.G + rr % a.G;
   const auto raw = f32_to_raw<T>(l > 0.0f ? acc / l : 0.0f);
-  *reinterpret_cast<std::remove_const_t<decltype(raw)>*>(reinterpret_cast<T*>(a.out) +
-                                                         orow * a.out_rs + (int64_t)h * D + c) = raw;
+  T* const o = reinterpret_cast<T*>(a.out) + orow * a.out_rs + (int64_t)h * D + c;
+  *reinterpret_cast<std::remove_const_t<decltype(raw)>*>(o) = raw;
   if (a.lse && c == 0) a.lse[orow * a.Hq + h] = l > 0.0f ? m + logf(l) : -INFINITY;
 }
 

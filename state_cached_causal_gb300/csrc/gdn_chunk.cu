@@ -7,10 +7,10 @@
 //   R_i  = b_i (v_i - e^{G_i} S^T k_i),          N = T R,
 //   o_i  = scale (e^{G_i} S^T q_i + sum_{j<=i} e^{G_i - G_j} (q_i.k_j) N_j),
 //   S'   = e^{G_C} S + sum_j e^{G_C - G_j} k_j N_j^T,
-// one chain of chunks per sequence and head. A block owns one chain. Everything
-// that does not need S -- gates, norms, A, T, q.k -- is worked out one chunk
-// ahead by four warps, so that the chain itself is four tensor products and
-// the element-wise work between them.
+// one chain of chunks per sequence and head. Everything that does not need S --
+// gates, norms, A, T, T V, q.k -- is worked out ahead of the chain by other
+// warps, so that a link of it is three tensor products, one after the other
+// (S^T k, T R, the update), and the element-wise work between them.
 //
 // Orientation. All products with S are taken transposed, with the 128 columns
 // of S (dv) as the M rows of the tensor-core instruction and the tokens (or dk)
@@ -19,30 +19,52 @@
 // operand there and never passes it through shared memory. The B operands are
 // the staged tiles themselves: K and Q (rows = tokens) for S^T k and S^T q, the
 // same K tile read along its other dimension for the state update, T and the
-// scores for the two products inside the chunk.
+// scores for the two products inside the chunk. V enters once, as (T V)^T, with
+// V as the A operand from shared memory and before the chain arrives; T R then
+// adds -T e^G S^T k to it.
 //
 // Precision. k, q and v are bf16 and exact. fp32 factors (S, R, T, N) enter as
 // sums of two bf16 terms (about 16 bits; products lo * lo are left out), since
 // the state must keep more than 8 bits over thousands of tokens: its error is
-// 4e-6 of its norm against 64 bits where single bf16 factors give 2e-3. The
-// two products that only feed the output, which is rounded to bf16 itself,
-// take one term (2e-3). S is held in fp32 registers from the first chunk to
-// the last. l2 norms enter as factors of the rows, so that raw rows are
-// multiplied. G is kept as whole part + remainder (in powers of two): chunks
-// with strong decays reach sums of several hundred, whose differences fp32
-// alone would round by 1e-5.
+// 4e-6 of its norm against 64 bits, where single bf16 factors give 2e-3. The
+// outputs are rounded to bf16 themselves (1.7e-3 of their norm): their products
+// take S in S^T q and the scores with one term (2.3e-3 in all; with one term
+// for N too, 2.6e-3, and no faster: 889 us at 16384 tokens either way. A second
+// term for S there makes 2.2e-3, and 907 us). S is held in fp32 registers from
+// the first chunk to the last. l2 norms enter as factors of the rows, so that
+// raw rows are multiplied. G is kept as whole part + remainder (in powers of
+// two): chunks with strong decays reach sums of several hundred, whose
+// differences fp32 alone would round by 1e-5.
 //
-// T is built by forward substitution of the two 32 x 32 diagonal blocks
-// (a thread a column) and one block step for the rest, all in fp32: stable for
-// any keys, unlike sums of powers of A, whose terms cancel for equal keys.
+// T is built by forward substitution of its four 16 x 16 diagonal blocks, in
+// fp32, and products of blocks for the rest: stable for any keys, unlike sums
+// of powers of A, whose terms cancel for equal keys.
+//
+// Roles (28 warps, registers dealt by setmaxnreg): 16 scan warps hold S and the
+// chain, four work out A and the scores, two T, one issues every tcgen05.mma,
+// one loads and works the gates out, four write the outputs and take the norms.
+// They meet at mbarriers alone, each wait with a time limit, after which the
+// block gives up and the launch reports it.
 //
 // Layout. K and Q of a chunk form one 128-row tile in the 128-byte swizzle (two
-// panels of 64 dk each); rows behind the sequence's end are filled with zeros
-// by the copies themselves (cp.async), so nothing of the neighbouring request
-// -- NaN, say -- enters a product. Tensor memory columns: S (hi, lo by halves
-// of dk; the state update's accumulator takes the same columns once S has been
-// read) 0-127, S^T k 128-191 (then N), S^T q 192-255, R then the decayed N
-// (hi, lo) 256-319, N 320-351, in-chunk output 352-415, [K; Q] K^T 416-479.
+// panels of 64 dk each). Whole chunks come as tensor-map boxes; in a sequence's
+// last, partial one the rows behind its end are filled with zeros by the copies
+// themselves (cp.async), so nothing of the neighbouring request -- NaN, say --
+// enters a product. Tensor memory columns: S 0-127, per 16 dk 8 columns hi and 8
+// lo (the update's accumulator takes the same columns once S has been read),
+// S^T k 128-191 (then N hi, lo), S^T q 192-255, R and then the decayed N (hi,
+// lo) 256-319, T V + T R 320-383, in-chunk output 384-447, [K; Q] K^T 448-511.
+//
+// What bounds it. A chain is serial: at 16384 tokens of one request 256 links of
+// 3.5 us, 0.89 ms, on 32 of the SMs (one a head); its bytes would take 0.06 ms
+// and its products less. With 16 requests of up to 2048 tokens and 32 heads the
+// 512 chains fill the GPU: 0.26 ms, where bytes take 0.10; the longest chains and
+// the whole work weigh alike there. Inside a link every wait is short, and the
+// roles' code together (72 KB) is larger than the instruction caches near the
+// schedulers, so code size counts: unrolled loops and waits of 161 KB took 0.61
+// ms for the 16 requests and 128 single tokens that take 0.36 now, and what is
+// not on the chain stays rolled. Token by token (gdn_step.cu) the long chain
+// takes 21.5 ms.
 #include <cuda.h>
 #include <stddef.h>
 
@@ -270,132 +292,134 @@ __device__ __forceinline__ void order_chains(const GdnArgs& a, Smem& sm, int* le
 
 // Per chunk: requests its rows, works its gates out while they come. Whole
 // chunks come as tensor-map boxes; the last, partial one row by row, with
-// zeros behind the sequence's end. Gates: two tokens a lane (lane, lane + 32); their sums are
-// kept as whole part and remainder in (-1, 0], exact to 2^-24 of the remainder
-// however long the sum.
+// zeros behind the sequence's end. Gates: two tokens a lane (lane, lane + 32);
+// their sums are kept as whole part and remainder in (-1, 0], exact to 2^-24 of
+// the remainder however long the sum.
 __device__ __forceinline__ bool load_role(const GdnArgs& a, const Maps& maps, Smem& sm,
                                           const Wait& wait) {
   const int lane = threadIdx.x & 31, u = lane & 15, r2 = lane >> 4;
   const __nv_bfloat16* const ga0 = reinterpret_cast<const __nv_bfloat16*>(a.a);
   const __nv_bfloat16* const gb0 = reinterpret_cast<const __nv_bfloat16*>(a.b);
-  int boxed = 0, v_boxed = 0, g = 0;   // last chunks that came as boxes; chunks of the block so far
+  int boxed = 0, v_boxed = 0;   // last chunks that came as boxes
+  int g = 0;                    // chunks of the block so far
   Chain c;
   for (int k = 0; chain_at(a, sm, k, c); ++k) {
-  const int row0 = c.row0, len = c.len, h = c.h;
-  const int hk = h / (a.Hv / a.Hk);
-  const char* kp = a.k + ((int64_t)row0 * a.k_rs + (int64_t)hk * kD) * 2 + u * 16;
-  const char* qp = a.q + ((int64_t)row0 * a.q_rs + (int64_t)hk * kD) * 2 + u * 16;
-  const char* vp = a.v + ((int64_t)row0 * a.v_rs + (int64_t)h * kD) * 2 + u * 16;
-  const float A_log2 = -expf(a.A_log[h]) * 1.4426950408889634f;
-  const float dtb = a.dt_bias[h];
-  const __nv_bfloat16* ga = ga0 + h;
-  const __nv_bfloat16* gb = gb0 + h;
-  if (c.init) {             // the chain's state, for the warps that will read it
-    const char* sp = a.st + ((int64_t)c.slot * a.st_slot + (int64_t)h * a.st_head) * a.st_bytes;
-    for (int i = lane * 128; i < kD * kD * a.st_bytes; i += 32 * 128)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(sp + i));
-  }
-  for (int n = 0; n < c.chunks; ++n, ++g) {
-    const int st = g % kStages;
-    if (g >= kStages && !wait(&sm.ctl.empty[st], g / kStages - 1)) goto quit;
-    const int tok = n * kC + lane;
-    float na[2], nb[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int t = tok + i * 32;
-      na[i] = t < len ? elem(ga, (int64_t)(row0 + t) * a.a_rs) : 0.0f;
-      nb[i] = t < len ? elem(gb, (int64_t)(row0 + t) * a.b_rs) : 0.0f;
+    const int row0 = c.row0, len = c.len, h = c.h;
+    const int hk = h / (a.Hv / a.Hk);
+    const char* kp = a.k + ((int64_t)row0 * a.k_rs + (int64_t)hk * kD) * 2 + u * 16;
+    const char* qp = a.q + ((int64_t)row0 * a.q_rs + (int64_t)hk * kD) * 2 + u * 16;
+    const char* vp = a.v + ((int64_t)row0 * a.v_rs + (int64_t)h * kD) * 2 + u * 16;
+    const float A_log2 = -expf(a.A_log[h]) * 1.4426950408889634f;
+    const float dtb = a.dt_bias[h];
+    const __nv_bfloat16* ga = ga0 + h;
+    const __nv_bfloat16* gb = gb0 + h;
+    if (c.init) {             // the chain's state, for the warps that will read it
+      const char* sp = a.st + ((int64_t)c.slot * a.st_slot + (int64_t)h * a.st_head) * a.st_bytes;
+      for (int i = lane * 128; i < kD * kD * a.st_bytes; i += 32 * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(sp + i));
     }
-    // K and Q, then, when the outputs have left its place, V
-    const bool whole = len - n * kC >= kC;
-    const int y = row0 + n * kC;
-    const uint32_t at = smem_addr(sm.stage[st]);
-    auto rows = [&](uint32_t dst, uint32_t pitch, const char* src, int64_t stride) {
-#pragma unroll 1
-      for (int i = r2; i < kC; i += 2) {
-        const bool in = n * kC + i < len;
-        cp_async16(dst + (u >> 3) * pitch + sw128(i, u & 7),
-                   src + (int64_t)(in ? n * kC + i : 0) * stride * 2, in);
-      }
-    };
-    if (whole) {
-      boxed = g + 1;
-      if (lane == 0) {
-        mbar_arrive_tx(&sm.ctl.full[st], kKQBytes);
+    for (int n = 0; n < c.chunks; ++n, ++g) {
+      const int st = g % kStages;
+      if (g >= kStages && !wait(&sm.ctl.empty[st], g / kStages - 1)) goto quit;
+      const int tok = n * kC + lane;
+      float na[2], nb[2];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          tc::tma_load_2d(at + p * kPanel, &maps.k, hk * kD + p * 64, y, &sm.ctl.full[st]);
-          tc::tma_load_2d(at + p * kPanel + kC * 128, &maps.q, hk * kD + p * 64, y,
-                          &sm.ctl.full[st]);
+      for (int i = 0; i < 2; ++i) {
+        const int t = tok + i * 32;
+        na[i] = t < len ? elem(ga, (int64_t)(row0 + t) * a.a_rs) : 0.0f;
+        nb[i] = t < len ? elem(gb, (int64_t)(row0 + t) * a.b_rs) : 0.0f;
+      }
+      // K and Q, then, when the outputs have left its place, V
+      const bool whole = len - n * kC >= kC;
+      const int y = row0 + n * kC;
+      const uint32_t at = smem_addr(sm.stage[st]);
+      auto rows = [&](uint32_t dst, uint32_t pitch, const char* src, int64_t stride) {
+#pragma unroll 1
+        for (int i = r2; i < kC; i += 2) {
+          const bool in = n * kC + i < len;
+          cp_async16(dst + (u >> 3) * pitch + sw128(i, u & 7),
+                     src + (int64_t)(in ? n * kC + i : 0) * stride * 2, in);
         }
-      }
-    } else {
-      rows(at, kPanel, kp, a.k_rs);
-      rows(at + kC * 128, kPanel, qp, a.q_rs);
-      cp_async_commit();
-    }
-    if (g >= 2 && !wait(&sm.ctl.gate_empty[g & 1], (g >> 1) - 1)) {
-      warp_arrive(&sm.ctl.full[st]);
-      goto quit;
-    }
-    Gate& G = sm.gate[g & 1];
-    float w0 = 0.0f, f0 = 0.0f;                    // sums so far
-#pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-      const bool in = tok + i * 32 < len;
-      const float x = (i == 0 ? na[0] : na[1]) + dtb;
-      float gl = A_log2 * (fmaxf(x, 0.0f) + log1pf(__expf(-fabsf(x))));
-      // a decay below 2^-150 is zero in fp32 whatever follows (a NaN stays one)
-      gl = in ? (gl < -150.0f ? -150.0f : gl) : 0.0f;
-      float w = truncf(gl), f = gl - w;
-      auto add = [&](float ow, float of) {
-        const float s = f + of, c = truncf(s);
-        w += ow + c;
-        f = s - c;
       };
-#pragma unroll 1
-      for (int d = 1; d < 32; d <<= 1) {
-        const float ow = __shfl_up_sync(0xffffffffu, w, d);
-        const float of = __shfl_up_sync(0xffffffffu, f, d);
-        if (lane >= d) add(ow, of);
-      }
-      add(w0, f0);
-      w0 = __shfl_sync(0xffffffffu, w, 31);
-      f0 = __shfl_sync(0xffffffffu, f, 31);
-      G.hi[i * 32 + lane] = w;
-      G.lo[i * 32 + lane] = f;
-      G.beta[i * 32 + lane] =
-          in ? __fdividef(1.0f, 1.0f + __expf(-(i == 0 ? nb[0] : nb[1]))) : 0.0f;
-    }
-    if (!whole) {
-      cp_async_wait<0>();
-      fence_proxy_async();
-      if (lane == 0) mbar_arrive(&sm.ctl.full[st]);
-    }
-    warp_arrive(&sm.ctl.full[st]);
-    if (g >= kStages && !wait(&sm.ctl.v_empty[st], g / kStages - 1)) goto quit;
-    if (whole) {
-      v_boxed = g + 1;
-      if (lane == 0) {
-        mbar_arrive_tx(&sm.ctl.v_full[st], kVBytes);
+      if (whole) {
+        boxed = g + 1;
+        if (lane == 0) {
+          mbar_arrive_tx(&sm.ctl.full[st], kKQBytes);
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-          tc::tma_load_2d(at + kKQBytes + p * kVPanel, &maps.v, h * kD + p * 64, y,
-                          &sm.ctl.v_full[st]);
+          for (int p = 0; p < 2; ++p) {
+            tc::tma_load_2d(at + p * kPanel, &maps.k, hk * kD + p * 64, y, &sm.ctl.full[st]);
+            tc::tma_load_2d(at + p * kPanel + kC * 128, &maps.q, hk * kD + p * 64, y,
+                            &sm.ctl.full[st]);
+          }
+        }
+      } else {
+        rows(at, kPanel, kp, a.k_rs);
+        rows(at + kC * 128, kPanel, qp, a.q_rs);
+        cp_async_commit();
       }
-    } else {
-      rows(at + kKQBytes, kVPanel, vp, a.v_rs);
-      cp_async_commit();
-      cp_async_wait<0>();
-      fence_proxy_async();
-      warp_arrive(&sm.ctl.v_full[st]);
+      if (g >= 2 && !wait(&sm.ctl.gate_empty[g & 1], (g >> 1) - 1)) {
+        warp_arrive(&sm.ctl.full[st]);
+        goto quit;
+      }
+      Gate& G = sm.gate[g & 1];
+      float w0 = 0.0f, f0 = 0.0f;                    // sums so far
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        const bool in = tok + i * 32 < len;
+        const float x = (i == 0 ? na[0] : na[1]) + dtb;
+        float gl = A_log2 * (fmaxf(x, 0.0f) + log1pf(__expf(-fabsf(x))));
+        // a decay below 2^-150 is zero in fp32 whatever follows (a NaN stays one)
+        gl = in ? (gl < -150.0f ? -150.0f : gl) : 0.0f;
+        float w = truncf(gl), f = gl - w;
+        auto add = [&](float ow, float of) {
+          const float s = f + of, c = truncf(s);
+          w += ow + c;
+          f = s - c;
+        };
+#pragma unroll 1
+        for (int d = 1; d < 32; d <<= 1) {
+          const float ow = __shfl_up_sync(0xffffffffu, w, d);
+          const float of = __shfl_up_sync(0xffffffffu, f, d);
+          if (lane >= d) add(ow, of);
+        }
+        add(w0, f0);
+        w0 = __shfl_sync(0xffffffffu, w, 31);
+        f0 = __shfl_sync(0xffffffffu, f, 31);
+        G.hi[i * 32 + lane] = w;
+        G.lo[i * 32 + lane] = f;
+        G.beta[i * 32 + lane] =
+            in ? __fdividef(1.0f, 1.0f + __expf(-(i == 0 ? nb[0] : nb[1]))) : 0.0f;
+      }
+      if (!whole) {
+        cp_async_wait<0>();
+        fence_proxy_async();
+        if (lane == 0) mbar_arrive(&sm.ctl.full[st]);
+      }
+      warp_arrive(&sm.ctl.full[st]);
+      if (g >= kStages && !wait(&sm.ctl.v_empty[st], g / kStages - 1)) goto quit;
+      if (whole) {
+        v_boxed = g + 1;
+        if (lane == 0) {
+          mbar_arrive_tx(&sm.ctl.v_full[st], kVBytes);
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            tc::tma_load_2d(at + kKQBytes + p * kVPanel, &maps.v, h * kD + p * 64, y,
+                            &sm.ctl.v_full[st]);
+        }
+      } else {
+        rows(at + kKQBytes, kVPanel, vp, a.v_rs);
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_proxy_async();
+        warp_arrive(&sm.ctl.v_full[st]);
+      }
     }
-  }
   }
   return true;
 quit:                       // given up: no copy lands after the block ends
   cp_async_wait<0>();
-  for (int i = max(boxed - kStages, 0); i < boxed; ++i) wait(&sm.ctl.full[i % kStages], i / kStages);
+  for (int i = max(boxed - kStages, 0); i < boxed; ++i)
+    wait(&sm.ctl.full[i % kStages], i / kStages);
   for (int i = max(v_boxed - kStages, 0); i < v_boxed; ++i)
     wait(&sm.ctl.v_full[i % kStages], i / kStages);
   return false;
@@ -517,8 +541,8 @@ __device__ __forceinline__ bool t_blocks(const TWarp& w, int warp, Meet& meet, c
   return true;
 }
 
-// Norms, factors, A, scores and T of every chunk. Thread p < 64 holds row p of
-// K K^T, thread 64 + p row p of Q K^T.
+// Factors, A and the scores of every chunk. Thread p < 64 holds row p of K K^T,
+// thread 64 + p row p of Q K^T.
 __device__ __forceinline__ bool prep_role(const GdnArgs& a, Smem& sm, const Wait& wait,
                                           int chunks, uint32_t tmem) {
   const int p = threadIdx.x - kWarpPrep0 * 32, warp = p >> 5;
@@ -637,8 +661,9 @@ __device__ __forceinline__ bool prep_role(const GdnArgs& a, Smem& sm, const Wait
 
 // T of every chunk, by two warps: forward substitution of the four diagonal
 // blocks (a lane a column, two blocks a warp), then the blocks below them. What
-// is built is T with its columns scaled by beta, (diag(1 / beta) + A)^-1 for the A without
-// beta that the scores' warps wrote: rows t_i = beta_i (e_i - sum_k A_ik t_k).
+// is built is T with its columns scaled by beta, (diag(1 / beta) + A)^-1 for the
+// A without beta that the scores' warps wrote: rows t_i = beta_i (e_i - sum_k
+// A_ik t_k), without a division, so that beta = 0 needs nothing of its own.
 __device__ __forceinline__ bool inv_role(Smem& sm, const Wait& wait, int chunks) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kWarpInv0;
   const int blk = warp * 2 + (lane >> 4), c = lane & (kB - 1), b0 = blk * kB;
@@ -756,7 +781,8 @@ __device__ __forceinline__ bool scan_role(const GdnArgs& a, Smem& sm, const Wait
       }
       if (m > 0) warp_arrive(&sm.ctl.coef_empty[(n - 1) % kCoefs]);
       // ---- R
-      if (!wait(&sm.ctl.coef_full[n % kCoefs], n / kCoefs) || !wait(&sm.ctl.ks_full, n)) return false;
+      if (!wait(&sm.ctl.coef_full[n % kCoefs], n / kCoefs) || !wait(&sm.ctl.ks_full, n))
+        return false;
       tc::fence_after();
       uint32_t x[16];
       tc::ld16(tl + kColKS + qt * 16, x);
@@ -771,11 +797,12 @@ __device__ __forceinline__ bool scan_role(const GdnArgs& a, Smem& sm, const Wait
       tc::ld16(tl + kColVN + qt * 16, x);
       tc::wait_ld(x);
       scaled(x, C.vd);
-      uint32_t on[8];
+      uint32_t hi[8], lo[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        on[i] = pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-      tc::st8(tl + kColN + qt * 8, on);
+        tc::split2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), hi[i], lo[i]);
+      tc::st8(tl + kColN + qt * 8, hi);
+      tc::st8(tl + kColN + 32 + qt * 8, lo);
       tc::wait_st();
       tc::fence_before();
       warp_arrive(&sm.ctl.vd_full);
@@ -982,7 +1009,7 @@ __device__ __forceinline__ bool mma_role(Smem& sm, const Wait& wait, int chunks,
         tc::fence_after();
         if (tc::elect()) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
+          for (int ks = 0; ks < 8; ++ks)        // S hi
             tc::mma_ts(tmem + kColQS, tmem + kColS + ks * 16, kq + panel(ks, kC), kId, ks > 0);
           tc::commit(&sm.ctl.qs_done);
         }
@@ -1019,9 +1046,11 @@ __device__ __forceinline__ bool mma_role(Smem& sm, const Wait& wait, int chunks,
         }
         tc::commit(&sm.ctl.empty[st]);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          tc::mma_ts(tmem + kColO, tmem + kColN + ks * 8,
-                     tp + ((2 * kTBytes + ks * 32) >> 4), kId, ks > 0);
+        for (int t = 0; t < 2; ++t)             // N hi, N lo
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            tc::mma_ts(tmem + kColO, tmem + kColN + t * 32 + ks * 8,
+                       tp + ((2 * kTBytes + ks * 32) >> 4), kId, (t | ks) > 0);
         tc::commit(&sm.ctl.o_full);
         tc::commit(&sm.ctl.tp_empty[n & 1]);
       }
@@ -1032,7 +1061,8 @@ __device__ __forceinline__ bool mma_role(Smem& sm, const Wait& wait, int chunks,
 }
 
 template <typename ST>
-__global__ void __launch_bounds__(kThreadsC, 1) gdn_chunk_kernel(const GdnArgs a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(kThreadsC, 1)
+    gdn_chunk_kernel(const GdnArgs a, const __grid_constant__ Maps maps) {
   extern __shared__ __align__(1024) unsigned char gdn_dyn[];
   Smem& sm = *reinterpret_cast<Smem*>(
       gdn_dyn + ((1024u - (smem_addr(gdn_dyn) & 1023u)) & 1023u));
