@@ -1070,6 +1070,10 @@ __global__ void __launch_bounds__(kThreadsC, 1)
   // (read from one lane: values that the compiler then knows to be the same in
   // the whole warp, and keeps in uniform registers, where tcgen05.mma wants them)
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  // the short sequences' kernel, which needs nothing of this one, may start as
+  // SMs become free (22.5 -> 20.1 us for one request of 77 tokens; SMs kept free
+  // for it from the start took as much from the chains as it gained)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   order_chains(a, sm, reinterpret_cast<int*>(sm.stage[0]));
   const int chunks = __shfl_sync(0xffffffffu, sm.total, 0);
   if (chunks == 0) return;
