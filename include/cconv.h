@@ -14,6 +14,9 @@
  *   - Zaya CCA's two-stage q/k conv and the one-token-delayed half of v
  *     (page "vllm.model_executor.models.zaya", ZayaCCA.__init__ and
  *     _mix_with_state).
+ * Behind the convolutions stand the mixers of such layers: the gated delta
+ * rule over a state pool (gdn_fwd_varlen, gdn_update), and attention over a
+ * paged cache (attn_norm_rope_cache, attn_decode).
  *
  * Conventions shared by every entry point
  * ---------------------------------------

@@ -1,4 +1,4 @@
-"""State-cached causal short convolution on GB300 (sm_103a).
+"""State-cached causal short convolution, and the mixers behind it, on GB300 (sm_103a).
 
 The compute path is ``libcconv.so`` (hand-written CUDA, C ABI, declared in
 ``include/cconv.h``); ``state_cached_causal_gb300.ops`` is the thin ctypes

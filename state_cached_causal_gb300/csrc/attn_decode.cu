@@ -15,7 +15,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kTile = 32;
 constexpr int kRows = 8;          // query rows of a block
-constexpr int kMaxGrid = 4096;    // blocks of the split kernels
+constexpr int kMaxGrid = 1024;    // blocks of the split kernels
 
 template <typename T, int D>
 struct AttnSmem {
@@ -189,16 +189,18 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const AttnArgs a) {
 }
 
 // Joins the parts of a cut unit, one block a row of a unit and CC of its columns.
-// Part i (block c0 + i) is slot 1 of block c0 and slot 0 of the others. The
-// threads first turn the parts' maxima and sums into weights, then take a column
-// each and every kGroups-th part, with many loads in flight. (It is launched to
-// overlap the end of the kernel before, whose results it waits for.) A few units
-// have many parts each -- one long context has one of every block -- and get 16
-// groups of 32 columns; many units have few and get whole rows.
+// Part i (block c0 + i) is slot 1 of block c0 and slot 0 of the others. A thread
+// takes a column and every kGroups-th part. It requests its first kPre values,
+// then the threads turn the parts' maxima and sums into weights: the whole join
+// is two round trips to the L2. (It is launched to overlap the end of the kernel
+// before, whose results it waits for.) A few units have many parts each -- one
+// long context has one of every block -- and get 32 groups of 16 columns; many
+// units have few and get whole rows.
 template <typename T, int D, int CC, int kJoinThreads>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
   constexpr int kGroups = kJoinThreads / CC;
-  __shared__ float wt[kMaxGrid];
+  constexpr int kPre = 10;
+  __shared__ float wt[kMaxGrid], lt[kMaxGrid];
   __shared__ float red[2][kJoinThreads / 32];
   __shared__ float sums[kGroups][CC];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -216,11 +218,17 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   auto part = [&](int i) {
     return a.part + ((int64_t)(c0 + i) * 2 + (i == 0)) * one + row * (D + 2);
   };
+  const int cl = tid % CC, g = tid / CC, c = blockIdx.z * CC + cl;
+  float x[kPre];
+#pragma unroll
+  for (int k = 0; k < kPre; ++k)
+    x[k] = g + k * kGroups < parts ? part(g + k * kGroups)[c] : 0.0f;
   float m = -INFINITY;
   for (int i = tid; i < parts; i += kJoinThreads) {
-    const float x = part(i)[D];
-    wt[i] = x;
-    m = fmaxf(m, x);
+    const float2 ml = *reinterpret_cast<const float2*>(part(i) + D);
+    wt[i] = ml.x;
+    lt[i] = ml.y;
+    m = fmaxf(m, ml.x);
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -232,7 +240,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   for (int i = tid; i < parts; i += kJoinThreads) {
     const float w = m == -INFINITY ? 0.0f : expf(wt[i] - m);
     wt[i] = w;
-    l = fmaf(w, part(i)[D + 1], l);
+    l = fmaf(w, lt[i], l);
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
@@ -241,10 +249,11 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   l = 0.0f;
 #pragma unroll
   for (int w = 0; w < kJoinThreads / 32; ++w) l += red[1][w];
-  const int cl = tid % CC, g = tid / CC, c = blockIdx.z * CC + cl;
   float acc = 0.0f;
-#pragma unroll 10
-  for (int i = g; i < parts; i += kGroups) acc = fmaf(wt[i], part(i)[c], acc);
+#pragma unroll
+  for (int k = 0; k < kPre; ++k)
+    if (g + k * kGroups < parts) acc = fmaf(wt[g + k * kGroups], x[k], acc);
+  for (int i = g + kPre * kGroups; i < parts; i += kGroups) acc = fmaf(wt[i], part(i)[c], acc);
   sums[g][cl] = acc;
   __syncthreads();
   if (g > 0) return;
@@ -263,7 +272,7 @@ cudaError_t launch_join(const AttnArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.B * a.units), (unsigned)(a.hw * std::min(a.rows, a.G * a.q_len)));
   const bool few = (int64_t)cfg.gridDim.x * cfg.gridDim.y <= 512;
-  cfg.gridDim.z = few ? D / 32 : 1;
+  cfg.gridDim.z = few ? D / 16 : 1;
   cfg.blockDim = dim3(few ? 512 : 256);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -271,15 +280,15 @@ cudaError_t launch_join(const AttnArgs& a, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D, 32, 512>, a)
+  return few ? cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D, 16, 512>, a)
              : cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D, D, 256>, a);
 }
 
 template <typename T, int D>
 cudaError_t launch_attn(const AttnArgs& a, int grid, cudaStream_t st) {
   const size_t smem = sizeof(AttnSmem<T, D>);
-  const cudaError_t e = cudaFuncSetAttribute(
-      attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> full;
+  const cudaError_t e = mix_full_smem(reinterpret_cast<const void*>(attn_kernel<T, D>), full);
   if (e != cudaSuccess) return e;
   attn_kernel<T, D><<<grid, kThreads, smem, st>>>(a);
   return cudaGetLastError();

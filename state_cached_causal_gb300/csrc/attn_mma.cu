@@ -417,8 +417,8 @@ cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
   int stages = D == 64 ? 4 : 3;
   while (stages > 2 && stages * stage + std::max(join, q) > 224 * 1024) --stages;
   const int smem = stages * stage + std::max(join, q);
-  const cudaError_t e = cudaFuncSetAttribute(
-      attn_mma_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> full;
+  const cudaError_t e = mix_full_smem(reinterpret_cast<const void*>(attn_mma_kernel<D, MT>), full);
   if (e != cudaSuccess) return e;
   attn_mma_kernel<D, MT><<<grid, kThreads, smem, st>>>(a, stages);
   return cudaGetLastError();

@@ -4,9 +4,10 @@
  * sizes, strides and addresses from Python took 20 us a call, in C it takes 3
  * to 4. The functions here take the arguments of the functions of the same
  * name in ops.py, check that everything is as the plain case has it -- tensor
- * types, layouts, sizes, device -- and make the call of libcconv.so on the current
- * stream. They return its status, or None where anything is not plain; ops.py then takes its
- * own way, which either serves the case or raises what is wrong with it.
+ * types, layouts, sizes, device -- and make the call of libcconv.so on the
+ * current stream. They return its status, or None where anything is not plain;
+ * ops.py then takes its own way, which either serves the case or raises what is
+ * wrong with it.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -18,6 +19,7 @@ enum { F32 = 0, BF16 = 1, I32 = 2, U8 = 3, NDT = 5 };
 static PyObject* dtypes[NDT]; /* float32, bfloat16, int32, uint8, bool */
 static PyObject *s_dtype, *s_is_cuda, *s_shape, *s_stride, *s_data_ptr, *s_get_device;
 static PyObject* raw_stream; /* device index -> cudaStream_t as an int */
+static PyObject* new_bytes;  /* (tensor, n) -> n bytes beside it */
 
 static int (*p_fwd)(const void*, int64_t, const void*, int64_t, const void*, int64_t, const void*,
                     int64_t, const void*, int64_t, const float*, const float*, gdn_state_t,
@@ -36,6 +38,8 @@ static int (*p_norm)(const void*, int64_t, const void*, int64_t, const void*, in
 static int (*p_attn)(const void*, int64_t, kv_cache_t, const int32_t*, int64_t, int32_t,
                      const int32_t*, int32_t, int32_t, int32_t, float, int32_t, void*, int64_t,
                      float*, void*, int64_t, int32_t*, cconv_stream_t);
+
+static int64_t (*p_need)(int32_t, int32_t, int32_t, int32_t, int32_t);
 
 typedef struct {
   void* p;
@@ -258,7 +262,8 @@ static PyObject* f_attn(PyObject* self, PyObject* const* x, Py_ssize_t n) {
   const double scale = PyFloat_AsDouble(x[6]);
   if (PyErr_Occurred() || ns < 0 || !cache(x[1], x[2], q.dt, &c) || !need(x[3], &tab, I32) ||
       !need(x[4], &len, I32) || !need(x[7], &out, q.dt) || !maybe(x[8], &lse, F32) ||
-      !need(x[9], &ws, U8) || !maybe(x[10], &err, I32) || !flat(&len) || !flat(&ws))
+      !maybe(x[9], &ws, U8) || !maybe(x[10], &err, I32) || !flat(&len) ||
+      (ws.nd >= 0 && !flat(&ws)))
     return not_plain();
   const int64_t B = len.n[0], rows = B * (1 + ns);
   if (q.n[2] != c.head_dim || !heads(&q, rows, q.n[1], q.n[2], &qs) ||
@@ -269,15 +274,30 @@ static PyObject* f_attn(PyObject* self, PyObject* const* x, Py_ssize_t n) {
       !stream_of(x[0], &st))
     return not_plain();
   const int64_t ts = tab.n[0] > 1 || tab.s[0] > tab.n[1] ? tab.s[0] : tab.n[1];
-  return PyLong_FromLong(p_attn(q.p, qs, c, tab.p, ts, (int32_t)tab.n[1], len.p, (int32_t)B,
-                                (int32_t)ns, (int32_t)q.n[1], (float)scale, q.dt, out.p, os, lse.p,
-                                ws.p, ws.n[0], err.p, st));
+  PyObject* own = NULL; /* the call's workspace, if it brought none */
+  if (ws.nd < 0) {
+    const int64_t need = p_need((int32_t)B, (int32_t)ns, (int32_t)q.n[1], c.num_kv_heads,
+                                c.head_dim);
+    if (need < 0) return not_plain();
+    own = PyObject_CallFunction(new_bytes, "OL", x[0], (long long)(need > 16 ? need : 16));
+    if (!own) return NULL;
+    if (!get(own, &ws) || ws.nd != 1) {
+      Py_DECREF(own);
+      return not_plain();
+    }
+  }
+  const int rc = p_attn(q.p, qs, c, tab.p, ts, (int32_t)tab.n[1], len.p, (int32_t)B,
+                        (int32_t)ns, (int32_t)q.n[1], (float)scale, q.dt, out.p, os, lse.p, ws.p,
+                        ws.n[0], err.p, st);
+  Py_XDECREF(own);
+  return PyLong_FromLong(rc);
 }
 
-/* init(handle of libcconv.so, (float32, bfloat16, int32, uint8, bool), raw stream function) */
+/* init(handle of libcconv.so, (float32, bfloat16, int32, uint8, bool), raw stream function,
+ *      function (tensor, n) -> n bytes on its device and the current stream) */
 static PyObject* f_init(PyObject* self, PyObject* const* x, Py_ssize_t n) {
-  if (n != 3 || !PyTuple_Check(x[1]) || PyTuple_GET_SIZE(x[1]) != NDT) {
-    PyErr_SetString(PyExc_TypeError, "init(handle, dtypes, raw_stream)");
+  if (n != 4 || !PyTuple_Check(x[1]) || PyTuple_GET_SIZE(x[1]) != NDT) {
+    PyErr_SetString(PyExc_TypeError, "init(handle, dtypes, raw_stream, new_bytes)");
     return NULL;
   }
   void* h = PyLong_AsVoidPtr(x[0]);
@@ -286,12 +306,14 @@ static PyObject* f_init(PyObject* self, PyObject* const* x, Py_ssize_t n) {
   *(void**)&p_upd = dlsym(h, "gdn_update");
   *(void**)&p_norm = dlsym(h, "attn_norm_rope_cache");
   *(void**)&p_attn = dlsym(h, "attn_decode");
-  if (!p_fwd || !p_upd || !p_norm || !p_attn) {
+  *(void**)&p_need = dlsym(h, "attn_decode_workspace_bytes");
+  if (!p_fwd || !p_upd || !p_norm || !p_attn || !p_need) {
     PyErr_SetString(PyExc_RuntimeError, "libcconv.so lacks an entry point");
     return NULL;
   }
   for (int i = 0; i < NDT; ++i) Py_XSETREF(dtypes[i], Py_NewRef(PyTuple_GET_ITEM(x[1], i)));
   Py_XSETREF(raw_stream, Py_NewRef(x[2]));
+  Py_XSETREF(new_bytes, Py_NewRef(x[3]));
   Py_RETURN_NONE;
 }
 

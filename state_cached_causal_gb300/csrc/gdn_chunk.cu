@@ -1201,8 +1201,8 @@ template <typename ST>
 cudaError_t launch_chunk(const GdnArgs& a, cudaStream_t st) {
   constexpr size_t smem = sizeof(Smem) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory of a block");
-  const cudaError_t e = cudaFuncSetAttribute(
-      gdn_chunk_kernel<ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> full;
+  const cudaError_t e = mix_full_smem(reinterpret_cast<const void*>(gdn_chunk_kernel<ST>), full);
   if (e != cudaSuccess) return e;
   Maps maps;
   if (!encode_rows(&maps.k, a.k, (int64_t)a.Hk * kD, a.T, a.k_rs) ||

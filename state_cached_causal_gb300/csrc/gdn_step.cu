@@ -46,6 +46,22 @@ int mix_sm_count() {
   return count[dev];
 }
 
+cudaError_t mix_full_smem(const void* f, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && (done.load() >> dev & 1))) return e;
+  cudaFuncAttributes at;
+  e = cudaFuncGetAttributes(&at, f);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             227 * 1024 - (int)at.sharedSizeBytes);
+  if (e != cudaSuccess)
+    cudaGetLastError();                  // this call's error, not the next one's
+  else if (dev < 64)
+    done |= 1ull << dev;
+  return e;
+}
+
 namespace {
 
 constexpr int kCols = 32;      // state columns of a block

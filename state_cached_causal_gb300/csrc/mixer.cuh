@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 
@@ -35,6 +36,9 @@ inline int mix_check_cache(const kv_cache_t& c, int dtype) {
 
 // SMs of the current device (looked up once per device), 0 on an error.
 int mix_sm_count();
+// Lets kernel `f` take as much shared memory as a block can have, once per
+// device; `done` is the kernel's own.
+cudaError_t mix_full_smem(const void* f, std::atomic<uint64_t>& done);
 
 // 4 consecutive elements of storage type T <-> fp32.
 template <typename T>

@@ -137,7 +137,7 @@ def _load_fast(lib):
     except (ImportError, AttributeError):
         return None
     mod.init(lib._handle, (torch.float32, torch.bfloat16, torch.int32, torch.uint8, torch.bool),
-             raw)
+             raw, lambda beside, n: beside.new_empty(n, dtype=torch.uint8))
     return mod
 
 
@@ -589,16 +589,11 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, n_spec, scale, out, 
     cached tokens with the new ones; lse: fp32 [B*(1+n_spec), Hq] or None; workspace: a uint8
     tensor of attn_decode_workspace_bytes() or None (allocated for the call).
     """
-    if (stream is None and q.is_cuda and q.dim() == 3 and k_cache.dim() == 4
-            and (_lib or load()) and _fast is not None):
-        ws = workspace
-        if ws is None:
-            ws = q.new_empty(max(attn_decode_workspace_bytes(seq_lens.shape[0], n_spec, q.shape[1],
-                                                             k_cache.shape[2], q.shape[2]), 16),
-                             dtype=torch.uint8)
-        if _served("attn_decode", _fast.attn_decode(q, k_cache, v_cache, block_table, seq_lens,
-                                                    n_spec, scale, out, lse, ws, dev_err)):
-            return
+    if stream is None and (_lib or load()) and _fast is not None and _served(
+            "attn_decode", _fast.attn_decode(
+                q, k_cache, v_cache, block_table, seq_lens, n_spec, scale, out, lse, workspace,
+                dev_err)):
+        return
     _i32(block_table, "block_table")
     _i32(seq_lens, "seq_lens")
     dtype = q.dtype
