@@ -148,3 +148,63 @@ def test_binding_checks():
                      (dict(k_cache=z(5, 16, 2, 32)), ValueError), (dict(), ValueError)):
         with pytest.raises(err):
             ops.attn_decode(**{**dec, **bad})
+
+
+# ---- the marshalling in C takes the same calls as the one in Python ---------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["fwd", "update", "norm", "attn"])
+def test_both_marshallings_agree(what, monkeypatch):
+    dev, bf = torch.device("cuda"), torch.bfloat16
+    g = torch.Generator(device=dev).manual_seed(3)
+
+    def rnd(*shape, dtype=bf):
+        return torch.randn(*shape, generator=g, device=dev).to(dtype)
+
+    def ints(*v):
+        return torch.tensor(v, dtype=torch.int32, device=dev)
+
+    rows = rnd(6, (2 + 2 + 4) * 64)
+    q, k, v = (t.unflatten(1, (-1, 64)) for t in rows.split([128, 128, 256], 1))
+    gates, A, dt = rnd(6, 8), rnd(4, dtype=torch.float32), rnd(4, dtype=torch.float32)
+    states, cache = rnd(8, 4, 64, 64, dtype=torch.float32), rnd(4, 2, 16, 2, 64)
+    cos = rnd(32, 64, dtype=torch.float32)
+
+    def call():
+        st, c = states.clone(), cache.clone()
+        out = torch.zeros(6, 4, 64, device=dev, dtype=bf)
+        lse = torch.zeros(6, 4, device=dev)
+        if what == "fwd":
+            ops.gdn_fwd_varlen(q, k, v, gates[:, :4], gates[:, 4:], A, dt, st, ints(2, 5),
+                               ints(0, 1, 6), None, 0.125, out)
+        elif what == "update":
+            ops.gdn_update(q, k, v, gates[:, :4], gates[:, 4:], A, dt, st, ints(1, 2, 3, 4, 5, 6)
+                           .view(3, 2), 1, ints(1, 2, 1), None, 0.125, out)
+        elif what == "norm":
+            ops.attn_norm_rope_cache(v, k, q, rnd(64) * 0 + 1, None, 1e-6, cos,
+                                     ints(0, 1, 2, 3, 4, 5), True, c[:, 0], c[:, 1],
+                                     ints(9, 30, -1, 0, 17, 63), out)
+        else:
+            ops.attn_decode(v, c[:, 0], c[:, 1], ints(1, 0, 3, 2).view(2, 2), ints(19, 3), 2, 0.125,
+                            out, lse)
+        torch.cuda.synchronize()
+        return st, c, out, lse
+
+    ops.load()
+    served = []
+    if ops._fast is not None:
+        name = {"fwd": "gdn_fwd_varlen", "update": "gdn_update", "norm": "attn_norm_rope_cache",
+                "attn": "attn_decode"}[what]
+        real, plain = ops._fast, getattr(ops._fast, name)
+
+        class Spy:
+            def __getattr__(self, n):
+                return (lambda *x: served.append(plain(*x)) or served[-1]) if n == name else \
+                    getattr(real, n)
+
+        monkeypatch.setattr(ops, "_fast", Spy())
+    one = call()
+    assert ops._fast is None or served == [0]
+    monkeypatch.setattr(ops, "_fast", None)
+    for a, b in zip(one, call()):
+        assert torch.equal(a, b)
