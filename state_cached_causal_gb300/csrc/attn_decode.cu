@@ -188,17 +188,17 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const AttnArgs a) {
   }
 }
 
-// Joins the parts of a cut unit, one block a row of a unit and CC of its columns.
-// Part i (block c0 + i) is slot 1 of block c0 and slot 0 of the others. A thread
-// takes a column and every kGroups-th part. It requests its first kPre values,
-// then the threads turn the parts' maxima and sums into weights: the whole join
-// is two round trips to the L2. (It is launched to overlap the end of the kernel
-// before, whose results it waits for.) A few units have many parts each -- one
-// long context has one of every block -- and get 32 groups of 16 columns; many
-// units have few and get whole rows.
-template <typename T, int D, int CC, int kJoinThreads>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
-  constexpr int kGroups = kJoinThreads / CC;
+// The joins of the parts of cut units. Part i (block c0 + i) is slot 1 of block
+// c0 and slot 0 of the others. (Both kernels are launched to overlap the end of
+// the kernel before, whose results they wait for.)
+//
+// A few rows have many parts each -- one long context has one of every block:
+// a block a row and CC of its columns. A thread takes a column and every
+// kGroups-th part; it requests its first kPre values, then the threads turn the
+// parts' maxima and sums into weights: two round trips to the L2 in all.
+template <typename T, int D>
+__global__ void __launch_bounds__(512) attn_join_kernel(const AttnArgs a) {
+  constexpr int kJoinThreads = 512, CC = 16, kGroups = kJoinThreads / CC;
   constexpr int kPre = 10;
   __shared__ float wt[kMaxGrid], lt[kMaxGrid];
   __shared__ float red[2][kJoinThreads / 32];
@@ -267,12 +267,88 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   if (a.lse && c == 0) a.lse[orow * a.Hq + h] = l > 0.0f ? m + logf(l) : -INFINITY;
 }
 
+// Many rows have few parts each: a warp a row. (A block a row took 4096 blocks,
+// four rounds of them, for 64 requests of 64 rows: 66 us in all, 56 so.)
+template <typename T, int D>
+__global__ void __launch_bounds__(256) attn_join_rows_kernel(const AttnArgs a, const int64_t n) {
+  constexpr int kPairs = D / 64, kAhead = 4;
+  const int lane = threadIdx.x & 31;
+  const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (at >= n) return;
+  const int rows = a.hw * a.rows, used = min(a.rows, a.G * a.q_len), y = a.hw * used;
+  const int64_t bu = at / y;                        // request and unit
+  const int row = (int)(at % y) / used * a.rows + (int)(at % y) % used;
+  const int c0 = a.meta[bu * 2], c1 = a.meta[bu * 2 + 1];
+  if (c0 < 0) return;
+  const int b = (int)(bu / a.units), u = (int)(bu % a.units);
+  const int hkv = u / a.rblocks * a.hw + row / a.rows;
+  const int rr = u % a.rblocks * a.rows + row % a.rows;
+  if (rr >= a.G * a.q_len) return;
+  const int parts = c1 - c0 + 1;
+  const int64_t one = (int64_t)rows * (D + 2);
+  auto part = [&](int i) {
+    return a.part + ((int64_t)(c0 + i) * 2 + (i == 0)) * one + row * (D + 2);
+  };
+  auto stats = [&](int i) {
+    return i < parts ? *reinterpret_cast<const float2*>(part(i) + D)
+                     : make_float2(-INFINITY, 0.0f);
+  };
+  const float2 first = stats(lane);
+  float m = first.x;
+  for (int i = lane + 32; i < parts; i += 32) m = fmaxf(m, stats(i).x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  float l = 0.0f, acc[kPairs][2] = {};
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    const float2 ml = i0 == 0 ? first : stats(i0 + lane);
+    const float w = ml.x == -INFINITY ? 0.0f : expf(ml.x - m);
+    l = fmaf(w, ml.y, l);
+    const int end = min(32, parts - i0);
+    for (int k0 = 0; k0 < end; k0 += kAhead) {
+      float2 x[kAhead][kPairs];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j)
+          x[k][j] = k0 + k < end ? *reinterpret_cast<const float2*>(part(i0 + k0 + k) + j * 64 +
+                                                                    lane * 2)
+                                 : make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k0 + k);   // (0 behind the last part)
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          acc[j][0] = fmaf(wk, x[k][j].x, acc[j][0]);
+          acc[j][1] = fmaf(wk, x[k][j].y, acc[j][1]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  const int64_t orow = (int64_t)b * a.q_len + rr / a.G;
+  const int h = hkv * a.G + rr % a.G;
+  T* const o = reinterpret_cast<T*>(a.out) + orow * a.out_rs + (int64_t)h * D + lane * 2;
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+  for (int j = 0; j < kPairs; ++j) {
+    const float v0 = acc[j][0] * inv, v1 = acc[j][1] * inv;
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float2*>(o + j * 64) = make_float2(v0, v1);
+    else
+      *reinterpret_cast<uint32_t*>(o + j * 64) = pack_bf16x2(v0, v1);
+  }
+  if (a.lse && lane == 0) a.lse[orow * a.Hq + h] = l > 0.0f ? m + logf(l) : -INFINITY;
+}
+
 template <typename T, int D>
 cudaError_t launch_join(const AttnArgs& a, cudaStream_t st) {
+  const int y = a.hw * std::min(a.rows, a.G * a.q_len);
+  const int64_t units = (int64_t)a.B * a.units, n = units * y;
+  const bool few = n <= 512;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.B * a.units), (unsigned)(a.hw * std::min(a.rows, a.G * a.q_len)));
-  const bool few = (int64_t)cfg.gridDim.x * cfg.gridDim.y <= 512;
-  cfg.gridDim.z = few ? D / 16 : 1;
+  cfg.gridDim = few ? dim3((unsigned)units, (unsigned)y, D / 16) : dim3((unsigned)((n + 7) / 8));
   cfg.blockDim = dim3(few ? 512 : 256);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -280,8 +356,8 @@ cudaError_t launch_join(const AttnArgs& a, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D, 16, 512>, a)
-             : cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D, D, 256>, a);
+  return few ? cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D>, a)
+             : cudaLaunchKernelEx(&cfg, attn_join_rows_kernel<T, D>, a, n);
 }
 
 template <typename T, int D>

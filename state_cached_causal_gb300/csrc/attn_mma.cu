@@ -22,8 +22,8 @@
 // of one head join their parts once per segment, through shared memory.
 //
 // Measured, heads of 128, 4 kv heads, 16 query heads: 256 requests of 1 to 8192
-// positions (2.1 GB) 332 us, 6.4 TB/s; one of 131072 (270 MB) 47 us and 8 more
-// for the join; 64 requests of up to 4096 with 4 tokens each (0.25 GB) 65 us.
+// positions (2.1 GB) 325 us, 6.5 TB/s; one of 131072 (270 MB) 47 us and 8 more
+// for the join; 64 requests of up to 4096 with 4 tokens each (0.25 GB) 56 us.
 //
 // V of positions that lie behind the length or on a bad page is filled with
 // zeros; their scores are masked, as are those that a draft token's row does not

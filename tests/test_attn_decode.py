@@ -92,6 +92,12 @@ def test_many_requests():
     assert check(*case(6, lens, 2, 1, 64, 16, 1, BF16), 1) == 0
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_rows_of_many_parts(dtype):
+    """A join of hundreds of rows, those of one request cut into more parts than a warp has lanes."""
+    assert check(*case(12, [6000, 8, 9, 33, 10], 16, 2, 64, 16, 8, dtype), 8) == 0
+
+
 def test_other_stream_and_callers_workspace():
     c = case(7, [500, 20], 16, 4, 128, 16, 1, BF16)
     ws = torch.full((ops.attn_decode_workspace_bytes(2, 0, 16, 4, 128),), 255, dtype=torch.uint8,
