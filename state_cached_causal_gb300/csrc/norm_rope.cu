@@ -11,11 +11,13 @@
 // for all tokens the norm weights, are in registers and serve all heads. When
 // there are few tokens a token's heads are spread over several warps.
 //
-// Four groups of heads have their loads in flight together, and four blocks an
-// SM take the tokens one after the other, the next token's position and slot
-// read ahead. 33024 tokens of 16 + 4 + 4 heads of 128 in bf16: 78.7 us for 422
-// MB, 5.4 TB/s (one unit a lane: 98.7 us; two groups in flight: 80.4 us). 61
-// tokens: 3.0 us, the latency of a few dependent loads.
+// Four groups of query heads have their loads in flight together, beside the
+// first group of keys and values, and four blocks an SM take the tokens one after
+// the other, the next token's position and slot read ahead. 33024 tokens of
+// 16 + 4 + 4 heads of 128 in bf16: 75.9 us for 422 MB, 5.6 TB/s (keys after the
+// queries, values after the keys: 78.7 us; three blocks, whose 168 registers
+// spill nothing: 78.1 us; one unit a lane: 98.7 us). 61 tokens: 3.0 us, the
+// latency of a few dependent loads.
 #include "mixer.cuh"
 
 namespace cconv {
@@ -112,67 +114,52 @@ __global__ void __launch_bounds__(kNrThreads, kNrBlocks) norm_rope_kernel(const 
       kdst = a.kc + off;
       vdst = a.vc + off;
     }
-    auto rotate_heads = [&](int h_begin, int h_end, const char* src, const char* w,
-                            const uint4 (&wu)[2], char* dst, int64_t dst_head) {
-      float w0[V], w1[V];
-      unpack16<T>(wu[0], w0);
-      unpack16<T>(wu[1], w1);
-#pragma unroll 1
-      for (int h0 = h_begin; h0 < h_end; h0 += HPW * kUnroll) {
-        uint4 r0[kUnroll], r1[kUnroll];
+    // one group of heads: norm, rotation, store (`in`: the lane's head exists)
+    auto rotate = [&](const uint4& u0, const uint4& u1, const float (&w0)[V], const float (&w1)[V],
+                      bool norm, char* dst, bool in) {
+      float x0[V], x1[V];
+      unpack16<T>(u0, x0);
+      unpack16<T>(u1, x1);
+      if (norm) {
+        float q0 = 0.0f, q1 = 0.0f, q2 = 0.0f, q3 = 0.0f;
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-          const int h = h0 + j * HPW + sub;
-          r0[j] = r1[j] = make_uint4(0u, 0u, 0u, 0u);
-          if (h < h_end) {
-            const char* p = src + (int64_t)h * (D * E);
-            r0[j] = *reinterpret_cast<const uint4*>(p + c0 * E);
-            r1[j] = *reinterpret_cast<const uint4*>(p + c1 * E);
-          }
+        for (int e = 0; e < V; e += 2) {
+          fma_x2(q0, q1, x0[e], x0[e + 1], x0[e], x0[e + 1], q0, q1);
+          fma_x2(q2, q3, x1[e], x1[e + 1], x1[e], x1[e + 1], q2, q3);
         }
+        float sum = (q0 + q1) + (q2 + q3);
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-          if (h0 + j * HPW >= h_end) break;            // warp-uniform
-          const int h = h0 + j * HPW + sub;
-          float x0[V], x1[V];
-          unpack16<T>(r0[j], x0);
-          unpack16<T>(r1[j], x1);
-          if (w) {
-            float q0 = 0.0f, q1 = 0.0f, q2 = 0.0f, q3 = 0.0f;
+        for (int d = LPH / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        const float r = rsqrtf(fmaf(sum, 1.0f / D, a.eps));
 #pragma unroll
-            for (int e = 0; e < V; e += 2) {
-              fma_x2(q0, q1, x0[e], x0[e + 1], x0[e], x0[e + 1], q0, q1);
-              fma_x2(q2, q3, x1[e], x1[e + 1], x1[e], x1[e + 1], q2, q3);
-            }
-            float sum = (q0 + q1) + (q2 + q3);
-#pragma unroll
-            for (int d = LPH / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            const float r = rsqrtf(fmaf(sum, 1.0f / D, a.eps));
-#pragma unroll
-            for (int e = 0; e < V; e += 2) {
-              mul_x2(x0[e], x0[e + 1], x0[e], x0[e + 1], r * w0[e], r * w0[e + 1]);
-              mul_x2(x1[e], x1[e + 1], x1[e], x1[e + 1], r * w1[e], r * w1[e + 1]);
-            }
-          }
-          float y0[V], y1[V];
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            if constexpr (PAIRS) {
-              float* y = e < V / 2 ? y0 + 2 * e : y1 + 2 * e - V;
-              const float* x = e < V / 2 ? x0 + 2 * e : x1 + 2 * e - V;
-              y[0] = fmaf(-x[1], s[e], x[0] * c[e]);
-              y[1] = fmaf(x[0], s[e], x[1] * c[e]);
-            } else {
-              y0[e] = fmaf(-x1[e], s[e], x0[e] * c[e]);
-              y1[e] = fmaf(x0[e], s[e], x1[e] * c[e]);
-            }
-          }
-          if (h < h_end) {
-            char* p = dst + (int64_t)h * dst_head * E;
-            stg16(p + c0 * E, pack16<T>(y0));
-            stg16(p + c1 * E, pack16<T>(y1));
-          }
+        for (int e = 0; e < V; e += 2) {
+          mul_x2(x0[e], x0[e + 1], x0[e], x0[e + 1], r * w0[e], r * w0[e + 1]);
+          mul_x2(x1[e], x1[e + 1], x1[e], x1[e + 1], r * w1[e], r * w1[e + 1]);
         }
+      }
+      float y0[V], y1[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if constexpr (PAIRS) {
+          float* y = e < V / 2 ? y0 + 2 * e : y1 + 2 * e - V;
+          const float* x = e < V / 2 ? x0 + 2 * e : x1 + 2 * e - V;
+          y[0] = fmaf(-x[1], s[e], x[0] * c[e]);
+          y[1] = fmaf(x[0], s[e], x[1] * c[e]);
+        } else {
+          y0[e] = fmaf(-x1[e], s[e], x0[e] * c[e]);
+          y1[e] = fmaf(x0[e], s[e], x1[e] * c[e]);
+        }
+      }
+      if (in) {
+        stg16(dst + c0 * E, pack16<T>(y0));
+        stg16(dst + c1 * E, pack16<T>(y1));
+      }
+    };
+    auto load = [&](const char* p, bool in, uint4& u0, uint4& u1, int b0, int b1) {
+      u0 = u1 = make_uint4(0u, 0u, 0u, 0u);
+      if (in) {
+        u0 = *reinterpret_cast<const uint4*>(p + b0);
+        u1 = *reinterpret_cast<const uint4*>(p + b1);
       }
     };
     // this warp's share of the heads, in whole groups of HPW
@@ -181,27 +168,54 @@ __global__ void __launch_bounds__(kNrThreads, kNrBlocks) norm_rope_kernel(const 
       b = min(heads, groups * part / a.parts * HPW);
       e = min(heads, groups * (part + 1) / a.parts * HPW);
     };
-    int hb, he;
-    share(a.Hq, hb, he);
-    if (hb < he)
-      rotate_heads(hb, he, a.q + tok * a.q_rs * E, a.qw, wq, a.qo + tok * a.qo_rs * E, D);
-    if (!kdst) continue;
-    share(a.Hkv, hb, he);
-    if (hb < he) {
-      // the values first: their loads run while the keys are worked on
-      const char* vs = a.v + tok * a.v_rs * E;
-      for (int h0 = hb; h0 < he; h0 += HPW) {
-        const int h = h0 + sub;
-        if (h < he) {
-          const char* p = vs + (int64_t)h * (D * E) + l * 16;
-          char* q = vdst + (int64_t)h * a.s_head * E + l * 16;
-          const uint4 u0 = *reinterpret_cast<const uint4*>(p);
-          const uint4 u1 = *reinterpret_cast<const uint4*>(p + LPH * 16);
-          stg16(q, u0);
-          stg16(q + LPH * 16, u1);
-        }
+    int qb, qe, kb, ke;
+    share(a.Hq, qb, qe);
+    share(a.Hkv, kb, ke);
+    if (!kdst) ke = kb;
+    const char* const qs = a.q + tok * a.q_rs * E;
+    const char* const ks = a.k + tok * a.k_rs * E;
+    const char* const vs = a.v + tok * a.v_rs * E;
+    char* const qd = a.qo + tok * a.qo_rs * E;
+    // values pass as they are: two units a lane, side by side over the lanes
+    const int v0 = l * 16, v1 = (LPH + l) * 16;
+    // the first group of keys and values comes while the queries are worked on
+    uint4 ku0, ku1, vu0, vu1;
+    const int64_t at0 = (int64_t)(kb + sub) * (D * E);
+    load(ks + at0, kb + sub < ke, ku0, ku1, c0 * E, c1 * E);
+    load(vs + at0, kb + sub < ke, vu0, vu1, v0, v1);
+    float w0[V], w1[V];
+    unpack16<T>(wq[0], w0);
+    unpack16<T>(wq[1], w1);
+#pragma unroll 1
+    for (int h0 = qb; h0 < qe; h0 += HPW * kUnroll) {
+      uint4 u0[kUnroll], u1[kUnroll];
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        const int h = h0 + j * HPW + sub;
+        load(qs + (int64_t)h * (D * E), h < qe, u0[j], u1[j], c0 * E, c1 * E);
       }
-      rotate_heads(hb, he, a.k + tok * a.k_rs * E, a.kw, wk, kdst, a.s_head);
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        if (h0 + j * HPW >= qe) break;              // warp-uniform
+        const int h = h0 + j * HPW + sub;
+        rotate(u0[j], u1[j], w0, w1, a.qw != nullptr, qd + (int64_t)h * (D * E), h < qe);
+      }
+    }
+    unpack16<T>(wk[0], w0);
+    unpack16<T>(wk[1], w1);
+#pragma unroll 1
+    for (int h0 = kb; h0 < ke; h0 += HPW) {
+      const int h = h0 + sub;
+      const int64_t to = (int64_t)h * a.s_head * E;
+      if (h < ke) {
+        stg16(vdst + to + v0, vu0);
+        stg16(vdst + to + v1, vu1);
+      }
+      const uint4 k0 = ku0, k1 = ku1;
+      const int64_t next = (int64_t)(h + HPW) * (D * E);
+      load(ks + next, h + HPW < ke, ku0, ku1, c0 * E, c1 * E);
+      load(vs + next, h + HPW < ke, vu0, vu1, v0, v1);
+      rotate(k0, k1, w0, w1, a.kw != nullptr, kdst + to, h < ke);
     }
   }
 }
