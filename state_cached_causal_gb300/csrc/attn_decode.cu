@@ -119,8 +119,8 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const AttnArgs a) {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
         const float mn = fmaxf(m[i], mx);
-        const float p = mn == -INFINITY ? 0.0f : expf(x - mn);
-        const float corr = mn == -INFINITY ? 1.0f : expf(m[i] - mn);
+        const float base = mn == -INFINITY ? 0.0f : mn;   // (a NaN score stays one)
+        const float p = expf(x - base), corr = expf(m[i] - base);
         float ps = p;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, d);
@@ -136,7 +136,10 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const AttnArgs a) {
 #pragma unroll
         for (int c = 0; c < CD; ++c) acc[c][r] *= corr;
       }
-      if (tid < D)
+      // (a weight of zero does not hide an infinity or NaN among the values of
+      // a draft token from the rows before it: there the rows choose)
+      const int drafts = sg.len - a.q_len + 1 - t0;   // positions that all rows see
+      if (tid < D && drafts >= kTile) {
 #pragma unroll 4
         for (int t = 0; t < kTile; ++t)
 #pragma unroll
@@ -145,6 +148,17 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const AttnArgs a) {
 #pragma unroll
             for (int r = 0; r < kRows; ++r) acc[c][r] = fmaf(sm.p[r][t], v, acc[c][r]);
           }
+      } else if (tid < D) {
+#pragma unroll 1
+        for (int t = 0; t < kTile; ++t)
+#pragma unroll
+          for (int c = 0; c < CD; ++c) {
+            const float v = sm.v[t][tid + c * kThreads];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+              if (t < drafts + (r0 + r) / a.G) acc[c][r] = fmaf(sm.p[r][t], v, acc[c][r]);
+          }
+      }
     }
     if (sg.whole) {
       __syncthreads();
@@ -158,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const AttnArgs a) {
         for (int r = 0; r < kRows; ++r)
           if (r < nr) {
             const int rr = r0 + r;
-            const float inv = sm.corr[r] > 0.0f ? 1.0f / sm.corr[r] : 0.0f;
+            const float inv = sm.corr[r] != 0.0f ? 1.0f / sm.corr[r] : 0.0f;
             T* o = reinterpret_cast<T*>(a.out) + ((int64_t)sg.b * a.q_len + rr / a.G) * a.out_rs +
                    (int64_t)(hkv * a.G + rr % a.G) * D;
 #pragma unroll
@@ -171,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const AttnArgs a) {
         const int r = warp * 2 + lane, rr = r0 + r;
         if (r < nr)
           a.lse[((int64_t)sg.b * a.q_len + rr / a.G) * a.Hq + hkv * a.G + rr % a.G] =
-              l[lane] > 0.0f ? m[lane] + logf(l[lane]) : -INFINITY;
+              l[lane] != 0.0f ? m[lane] + logf(l[lane]) : -INFINITY;
       }
     } else {
       float* part = attn_part(a, sg, D);
@@ -261,10 +275,10 @@ __global__ void __launch_bounds__(512) attn_join_kernel(const AttnArgs a) {
   for (int k = 1; k < kGroups; ++k) acc += sums[k][cl];
   const int64_t orow = (int64_t)b * a.q_len + rr / a.G;
   const int h = hkv * a.G + rr % a.G;
-  const auto raw = f32_to_raw<T>(l > 0.0f ? acc / l : 0.0f);
+  const auto raw = f32_to_raw<T>(l != 0.0f ? acc / l : 0.0f);
   T* const o = reinterpret_cast<T*>(a.out) + orow * a.out_rs + (int64_t)h * D + c;
   *reinterpret_cast<std::remove_const_t<decltype(raw)>*>(o) = raw;
-  if (a.lse && c == 0) a.lse[orow * a.Hq + h] = l > 0.0f ? m + logf(l) : -INFINITY;
+  if (a.lse && c == 0) a.lse[orow * a.Hq + h] = l != 0.0f ? m + logf(l) : -INFINITY;
 }
 
 // Many rows have few parts each: a warp a row. (A block a row took 4096 blocks,
@@ -330,7 +344,7 @@ __global__ void __launch_bounds__(256) attn_join_rows_kernel(const AttnArgs a, c
   const int64_t orow = (int64_t)b * a.q_len + rr / a.G;
   const int h = hkv * a.G + rr % a.G;
   T* const o = reinterpret_cast<T*>(a.out) + orow * a.out_rs + (int64_t)h * D + lane * 2;
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
   for (int j = 0; j < kPairs; ++j) {
     const float v0 = acc[j][0] * inv, v1 = acc[j][1] * inv;
@@ -339,7 +353,7 @@ __global__ void __launch_bounds__(256) attn_join_rows_kernel(const AttnArgs a, c
     else
       *reinterpret_cast<uint32_t*>(o + j * 64) = pack_bf16x2(v0, v1);
   }
-  if (a.lse && lane == 0) a.lse[orow * a.Hq + h] = l > 0.0f ? m + logf(l) : -INFINITY;
+  if (a.lse && lane == 0) a.lse[orow * a.Hq + h] = l != 0.0f ? m + logf(l) : -INFINITY;
 }
 
 template <typename T, int D>

@@ -69,6 +69,17 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+// All ones in the halves of a bf16 pair that are infinite or NaN.
+__device__ __forceinline__ uint32_t not_finite(uint32_t v) {
+  return ((v & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) |
+         ((v & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+}
+
 // The warps that compute, among themselves.
 __device__ __forceinline__ void warps_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
@@ -260,6 +271,18 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
         for (int i = 0; i < 8; ++i) s[mt][i >> 2][i & 3] *= sl2;
       // ---- masks, running maximum, weights
       const int pos0 = j * tpos + p0;              // the warp's first position
+      // Draft tokens' positions are hidden from the rows before them by a weight
+      // of zero, which an infinity or NaN among their values would get through:
+      // such values (`wild`) are kept out of the product and added to the rows
+      // that see them.
+      const int x0 = max(0, sg.len - a.q_len + 1 - pos0), x1 = min(16, sg.len - pos0);
+      bool wild = false;
+      if (x0 < x1) {
+        for (int x = x0; x < x1; ++x)
+          for (int i = lane; i < D / 2; i += 32)
+            wild |= not_finite(lds32(vb + x * pitch + i * 4)) != 0;
+        wild = __any_sync(0xffffffffu, wild);
+      }
       const uint4 all = *reinterpret_cast<const uint4*>(tr);
       if (pos0 + 15 > sg.len - a.q_len ||
           (all.x & all.y & all.z & all.w) != 0x01010101u) {
@@ -309,12 +332,43 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
         }
         // ---- weighted values
         const uint32_t va = vb + (lane & 15) * pitch + (lane >> 4) * 16;
+        if (!wild) {
 #pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-          uint32_t b[4];               // dims 0-7: positions 0-7, 8-15; dims 8-15: the same
-          ldm4t(b, va + n * 32);
-          mma(o[mt][2 * n], pw, b[0], b[1]);
-          mma(o[mt][2 * n + 1], pw, b[2], b[3]);
+          for (int n = 0; n < D / 16; ++n) {
+            uint32_t b[4];             // dims 0-7: positions 0-7, 8-15; dims 8-15: the same
+            ldm4t(b, va + n * 32);
+            mma(o[mt][2 * n], pw, b[0], b[1]);
+            mma(o[mt][2 * n + 1], pw, b[2], b[3]);
+          }
+        } else {
+          const int q0 = (lane & 3) * 2;
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n) {
+            uint32_t b[4];
+            ldm4t(b, va + n * 32);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {          // positions q0 + 8 (i & 1) + {0, 1}
+              const int x = q0 + (i & 1) * 8;
+              const uint32_t hidden = (x >= x0 ? 0xffffu : 0u) | (x + 1 >= x0 ? 0xffff0000u : 0u);
+              b[i] &= ~(not_finite(b[i]) & hidden);
+            }
+            mma(o[mt][2 * n], pw, b[0], b[1]);
+            mma(o[mt][2 * n + 1], pw, b[2], b[3]);
+          }
+#pragma unroll 1
+          for (int x = x0; x < x1; ++x)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int r = mt * 16 + half * 8 + (lane >> 2);
+              if (r >= rows || pos0 + x >= sg.len - a.q_len + 1 + (r0 + r) / a.G) continue;
+#pragma unroll
+              for (int n = 0; n < D / 8; ++n) {
+                uint32_t v = lds32(vb + x * pitch + (n * 8 + q0) * 2);
+                v &= not_finite(v);
+                o[mt][n][half * 2] += __uint_as_float(v << 16);
+                o[mt][n][half * 2 + 1] += __uint_as_float(v & 0xffff0000u);
+              }
+            }
         }
       }
       __syncwarp();
@@ -382,7 +436,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
         if (r >= rows) continue;
         const float ll = l[mt][half], mn = m[mt][half] * 0.6931471805599453f;   // natural
         if (sg.whole) {
-          const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+          const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
           const int64_t tok = (int64_t)sg.b * a.q_len + (r0 + r) / a.G;
           const int h = hkv * a.G + (r0 + r) % a.G;
           char* p = a.out + (tok * a.out_rs + (int64_t)h * D + c) * 2;
@@ -390,7 +444,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
           for (int n = 0; n < D / 8; ++n)
             *reinterpret_cast<uint32_t*>(p + n * 16) =
                 pack_bf16x2(o[mt][n][half * 2] * inv, o[mt][n][half * 2 + 1] * inv);
-          if (a.lse && c == 0) a.lse[tok * a.Hq + h] = ll > 0.0f ? mn + logf(ll) : -INFINITY;
+          if (a.lse && c == 0) a.lse[tok * a.Hq + h] = ll != 0.0f ? mn + logf(ll) : -INFINITY;
         } else {
           float* p = part + r * (D + 2);
 #pragma unroll

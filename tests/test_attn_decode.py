@@ -118,6 +118,28 @@ def test_the_same_every_time():
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("hq,hkv,D", [(4, 2, 64), (16, 4, 128), (12, 1, 128), (4, 2, 256)])
+def test_draft_values_that_are_not_finite(dtype, hq, hkv, D):
+    """Infinities and NaN in a draft token's key and values reach its own row and those after it only."""
+    n = 4
+    q, kc, vc, table, lens = case(13, [18, 4, 100, 65], hq, hkv, D, 16, n, dtype)
+    bad = [float("inf"), float("-inf"), float("nan"), float("inf")]
+    for b, length in enumerate(lens.tolist()):
+        last = length - 1 - (b % 2)                       # the last draft token, or the one before
+        page = int(table[b, last // 16])
+        vc[page, last % 16, :, 3 + 2 * b] = bad[b]
+        vc[page, last % 16, 0, D - 1 - b] = bad[(b + 1) % 4]
+    kc[int(table[2, 99 // 16]), 99 % 16] = float("nan")
+    out = torch.zeros(q.shape, device=DEV, dtype=dtype)
+    ops.attn_decode(q, kc, vc, table, lens, n - 1, D ** -0.5, out)
+    torch.cuda.synchronize()
+    want, _ = attn_ref(q.cpu(), kc.cpu(), vc.cpu(), table.cpu(), lens.tolist(), n, D ** -0.5)
+    nan = torch.isnan(want)
+    assert nan.any() and torch.isinf(want).any() and torch.equal(torch.isnan(out.cpu()), nan)
+    assert_close(out.nan_to_num(0, float("inf"), -float("inf")), want.masked_fill(nan, 0), "out")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_a_bad_page_is_left_out(dtype):
     q, kc, vc, table, lens = case(9, [100, 40], 4, 2, 128, 16, 1, dtype)
     table[0, 2], table[1, 0] = -1, kc.shape[0]
