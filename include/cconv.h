@@ -490,7 +490,9 @@ typedef struct gdn_state {
  *                starts from zeros and stores no state)
  *   num_v_heads  a multiple of num_k_heads; dk, dv each 64 or 128 (others
  *                return CCONV_ERR_UNSUPPORTED)
- * An empty sequence leaves its slot as it is with has_init, zeros without.
+ * An empty sequence leaves its slot as it is with has_init, zeros without. An
+ * infinity or NaN in a token's row spreads to its own sequence alone, where
+ * sequences are taken by chunks from the start of its chunk of 64 tokens on.
  * Errors on the device: CCONV_DERR_SLOT_RANGE, CCONV_DERR_CU_SEQLENS,
  * CCONV_DERR_TIMEOUT.
  */

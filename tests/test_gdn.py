@@ -178,6 +178,66 @@ def test_fwd_is_the_same_every_time():
     assert all(torch.equal(o, got[0][0]) and torch.equal(s, got[0][1]) for o, s in got[1:])
 
 
+def _fwd(inp, lens, st):
+    out = torch.zeros(sum(lens), inp[2].shape[1], 128, device=DEV, dtype=BF16)
+    ops.gdn_fwd_varlen(*inp, st, torch.arange(len(lens), dtype=torch.int32, device=DEV),
+                       synth.cu_from_lens(lens, DEV), None, 0.1, out)
+    return out
+
+
+@pytest.mark.parametrize("where", ["q", "k", "v", "a", "state"])
+def test_what_is_not_finite_stays_in_its_sequence(where):
+    """Several chains a block, every other sequence with an infinity or NaN: the others keep their
+    bits, and so do the chunks of 64 tokens before it."""
+    lens = [130 + 7 * (i % 5) for i in range(58)] + [1, 3, 1, 2]
+    inp = inputs(23, sum(lens), 2, 8, 128, 128, BF16, spare=0)
+    st = pool(23, len(lens), 8, 128, 128, F32)
+    good_st = st.clone()
+    good = _fwd(inp, lens, good_st)
+    at = 0
+    for i, n in enumerate(lens):
+        if i % 2:
+            bad = (float("nan"), float("inf"), -float("inf"))[i // 2 % 3]
+            if where == "state":
+                st[i, :, 5, 17] = bad
+            else:
+                inp[dict(q=0, k=1, v=2, a=3)[where]][at + (100 if n > 100 else 0)] = bad
+        at += n
+    out = _fwd(inp, lens, st)
+    torch.cuda.synchronize()
+    at = 0
+    for i, n in enumerate(lens):
+        keep = n if i % 2 == 0 else 64 if n > 100 and where != "state" else 0
+        assert torch.equal(out[at:at + keep], good[at:at + keep]), i
+        if i % 2 == 0:
+            assert torch.equal(st[i], good_st[i]), i
+        at += n
+
+
+def test_captured_in_a_graph():
+    """Both kernels of a call, replayed: what follows in the graph sees both results."""
+    lens = [200, 1, 2000, 5, 64]
+    inp = inputs(24, sum(lens), 2, 4, 128, 128, BF16, spare=0)
+    start = pool(24, len(lens), 4, 128, 128, F32)
+    want_st = start.clone()
+    want = _fwd(inp, lens, want_st)
+    st, idx, cu = start.clone(), torch.arange(5, dtype=torch.int32, device=DEV), synth.cu_from_lens(lens, DEV)
+    out, copies = torch.zeros_like(want), (torch.zeros_like(want), torch.zeros_like(start))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        st.copy_(start)
+        ops.gdn_fwd_varlen(*inp, st, idx, cu, None, 0.1, out)
+        copies[0].copy_(out)
+        copies[1].copy_(st)
+    for _ in range(3):
+        for c in copies:
+            c.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(copies[0], want) and torch.equal(copies[1], want_st)
+
+
 def test_fwd_device_errors_skip_the_sequence():
     inp = inputs(20, 80, 1, 1, 128, 128, BF16, spare=0)
     for idx, cu, bit in (([0, 5], [0, 70, 80], ops.DERR_SLOT_RANGE),
