@@ -396,11 +396,10 @@ AttnPlan plan(int dtype, int sms, int64_t B, int q_len, int G, int Hkv, int D) {
     p.rows = kRows;
     p.grid = sms * 2;
   } else {
-    // row tiles whose sums fit in registers; blocks that an SM holds at once, by
-    // their shared memory (70 to 218 KB) and registers
+    // row tiles whose sums fit in registers
     p.rows = rows <= 16 || D == 256 ? 16 : 32;
     p.hw = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
-    p.grid = sms * (D * p.rows >= 4096 ? 1 : D * p.rows >= 2048 ? 2 : 3);
+    p.grid = sms * attn_mma_blocks(D, p.rows);
   }
   p.grid = std::min(p.grid, kMaxGrid);
   p.rblocks = (rows + p.rows - 1) / p.rows;
@@ -492,6 +491,12 @@ extern "C" int attn_decode(const void* q, int64_t q_row_stride, kv_cache_t cache
   a.meta = static_cast<int32_t*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.meta_bytes);
   a.hw = p.hw;
+  // positions that follow one another in memory come together, up to 1 KB or four
+  a.group_shift = 0;
+  if (cache.s_token == (int64_t)p.hw * D && (p.hw == 1 || cache.s_head == D))
+    while (a.group_shift < 2 && (p.hw * D * 2 << a.group_shift) < 1024 &&
+           cache.page_size % (2 << a.group_shift) == 0)
+      ++a.group_shift;
   a.rblocks = p.rblocks;
   a.rows = p.rows;
   a.units = p.units;

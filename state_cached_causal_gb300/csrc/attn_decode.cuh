@@ -36,11 +36,18 @@ struct AttnArgs {
   int32_t* meta;     // [B * units][2]: first and last block of a cut unit, or -1
   float* part;       // [grid][2][hw * rows][D + 2]: weighted values, maximum, sum
   int32_t hw;        // kv heads of a unit
+  int32_t group_shift;  // log2 of the positions that one copy brings (attn_mma.cu)
   int32_t rblocks;   // row blocks of a head (rows of G * q_len taken separately)
   int32_t rows;      // rows of a block
   int32_t units;     // of a request: Hkv / hw * rblocks
   int32_t* dev_err;
 };
+
+// Blocks of the bf16 kernel that an SM holds at once, by their registers and
+// shared memory (50 to 218 KB).
+inline int attn_mma_blocks(int D, int rows) {
+  return D * rows >= 4096 ? 1 : D * rows >= 2048 ? 2 : 3;
+}
 
 // Tiles of request b: at least one (an empty request still writes its rows).
 // len < 0 marks a request that is skipped.

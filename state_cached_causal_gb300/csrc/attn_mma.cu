@@ -14,16 +14,21 @@
 // one bulk copy of hw * D values (else in hw of D values), a copy a thread. The
 // copies cost a handful of instructions a tile; the first form, per-thread
 // 16-byte copies of swizzled rows, took two thirds of the kernel's instructions
-// and held it at 4.2 TB/s. Positions are 16 bytes further apart than their
-// length, so that ldmatrix meets no bank conflict. Each warp takes 16 rows, of
+// and held it at 4.2 TB/s. Where a position is less than 1 KB and the next one lies
+// behind it in memory, a copy brings two or four. Copies are 16 bytes further
+// apart than their length, so that ldmatrix meets no bank conflict, or one of two
+// or four positions: with a copy a position the copies were what bounded small
+// rows. Each warp takes 16 rows, of
 // one head: scores = Q K^T, running maximum and sum of its own, weights to bf16
 // in registers (the score layout of one product is the weight layout of the
 // next), weighted values += P V. No barrier between warps but the ring's; warps
 // of one head join their parts once per segment, through shared memory.
 //
 // Measured, heads of 128, 4 kv heads, 16 query heads: 256 requests of 1 to 8192
-// positions (2.1 GB) 325 us, 6.5 TB/s; one of 131072 (270 MB) 47 us and 8 more
-// for the join; 64 requests of up to 4096 with 4 tokens each (0.25 GB) 56 us.
+// positions (2.1 GB) 331 us, 6.4 TB/s; one of 131072 (270 MB) 47 us and 8 more
+// for the join; 64 requests of up to 4096 with 4 tokens each (0.25 GB) 56 us. With
+// 2 kv heads, 256 requests (1.06 GB): 179 us, 5.9 TB/s; with a copy a position,
+// and a ring that left the grid's second block of an SM no room, 354 us.
 //
 // V of positions that lie behind the length or on a bad page is filled with
 // zeros; their scores are masked, as are those that a draft token's row does not
@@ -112,9 +117,11 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
   __shared__ __align__(16) unsigned char there[kMaxStages][kTile];   // positions that hold a token
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t pitch = a.hw * D * 2 + 16;
+  // position x of a tile lies at off(x) of its place: rows of a group side by side
+  const int rowb = a.hw * D * 2, gs = a.group_shift, group = 1 << gs;
+  auto off = [&](int x) { return (uint32_t)(x * rowb + (x >> gs) * 16); };
   const int hw_shift = a.hw == 4 ? 2 : a.hw >> 1, tpos = kTile >> hw_shift;   // positions a tile
-  const uint32_t half_stage = tpos * pitch;     // K, then V
+  const uint32_t half_stage = off(tpos);        // K, then V
   // behind the ring: the joins of at most two heads, or the warps' own Q before
   unsigned char* const behind = attn_dyn + stages * 2 * half_stage;
   float* const join = reinterpret_cast<float*>(behind);
@@ -134,44 +141,55 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
 
   if (warp == kWarps) {
     // ---- loads: lane l has the copies l, l + 32, .. of a tile: K and V of each
-    // position, whole or head by head. The pages of the next tile are looked up
-    // before the wait for its place.
-    const bool joined = a.s_head == D;
-    const int pieces = joined ? 1 : a.hw, copies = 2 * tpos * pieces;
-    const uint32_t bytes = (joined ? a.hw : 1) * D * 2;
+    // group of positions, whole or head by head. The pages of the copies after
+    // these are looked up while these are issued.
+    const int ps = a.s_head == D ? 0 : hw_shift;      // log2 of the copies of a position
+    const uint32_t bytes = rowb >> ps;                // of a copy and position
+    // the lane's copies: K or V, a head or all, positions pl0, pl0 + dpl, ..
+    const int isv = lane & 1, piece = (lane >> 1) & ((1 << ps) - 1);
+    const int pl0 = lane >> (1 + ps) << gs, dpl = 16 >> ps << gs;
+    unsigned char* const dst0 = attn_dyn + isv * half_stage + piece * (D * 2);
+    const bool notes = isv == 0 && piece == 0;
     int st = 0, ph = 1;               // (the first round's places are free)
     while (run.p < run.end) {
       const AttnSeg s = attn_segment(a, tpos, run);
       attn_advance(a, s, run);
       const int32_t* tab = a.table + (int64_t)s.b * a.table_rs;
-      const int64_t head = (int64_t)(s.unit / a.rblocks * a.hw) * a.s_head;
+      const char* const src0 =
+          (isv ? a.vc : a.kc) +
+          ((int64_t)(s.unit / a.rblocks * a.hw) * a.s_head + piece * a.s_head) * 2;
+      // page of position pos, as the table has it
+      auto look = [&](int pos, bool in) {
+        return in && pos < s.len ? tab[a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size]
+                                 : -1;
+      };
+      int ahead = look(s.j0 * tpos + pl0, pl0 < tpos);
       for (int j = s.j0; j < s.j1; ++j) {
-        unsigned char* const kb = attn_dyn + st * 2 * half_stage;
-        bool waited = false;
-        for (int c0 = 0; c0 < copies; c0 += 32) {
-          const int c = c0 + lane, isv = c & 1, pl = (c >> 1) / pieces,
-                    piece = (c >> 1) - pl * pieces;
-          const int pos = j * tpos + pl;
-          int page = -1;
-          if (c < copies && pos < s.len) {
-            page = tab[a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size];
-            if (page < 0 || page >= a.num_pages) {
-              flag_error(a.dev_err, CCONV_DERR_PAGE);
-              page = -1;
-            }
+        const uint32_t place = st * 2 * half_stage;
+        const int t0 = j * tpos;
+        int pl = pl0;
+        for (int p = 0; p < tpos; p += dpl, pl += dpl) {       // (p: of lane 0)
+          const int pos = t0 + pl, page = ahead;
+          const bool in = pl < tpos;
+          ahead = p + dpl < tpos ? look(pos + dpl, pl + dpl < tpos)
+                                 : look(t0 + tpos + pl0, j + 1 < s.j1 && pl0 < tpos);
+          int held = in ? min(group, max(s.len - pos, 0)) : 0;   // positions with a token
+          if (held > 0 && (uint32_t)page >= (uint32_t)a.num_pages) {
+            flag_error(a.dev_err, CCONV_DERR_PAGE);
+            held = 0;
           }
-          const int tok = a.page_shift >= 0 ? pos & (a.page_size - 1) : pos % a.page_size;
-          const int64_t off = (page * a.s_page + tok * a.s_tok + head + piece * a.s_head) * 2;
-          if (!waited && !wait_bar(&empty[st], ph, a.dev_err)) return;
-          waited = true;
-          if (c < copies) {
-            unsigned char* const dst = kb + isv * half_stage + pl * pitch + piece * (D * 2);
-            if (isv == 0 && piece == 0) there[st][pl] = page >= 0;
-            if (page >= 0) {
-              mbar_expect(&full[st], bytes);
-              bulk_load(dst, (isv ? a.vc : a.kc) + off, bytes, &full[st]);
-            } else if (isv) {
-              for (uint32_t i = 0; i < bytes; i += 16)
+          if (p == 0 && !wait_bar(&empty[st], ph, a.dev_err)) return;
+          if (in) {
+            if (notes)
+              for (int k = 0; k < group; ++k) there[st][pl + k] = k < held;
+            unsigned char* const dst = dst0 + place + off(pl);
+            if (held > 0) {
+              const int tok = a.page_shift >= 0 ? pos & (a.page_size - 1) : pos % a.page_size;
+              mbar_expect(&full[st], held * bytes);
+              bulk_load(dst, src0 + (page * a.s_page + tok * a.s_tok) * 2, held * bytes, &full[st]);
+            }
+            if (isv && held < group) {
+              for (uint32_t i = held * bytes; i < group * bytes; i += 16)
                 *reinterpret_cast<uint4*>(dst + i) = make_uint4(0u, 0u, 0u, 0u);
               fence_proxy_async();      // before a later copy into the same place
             }
@@ -238,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
     }
     for (int j = sg.j0; j < sg.j1; ++j) {
       if (!wait_bar(&full[stage], phase, a.dev_err)) return;
-      const uint32_t kb = smem_addr(attn_dyn) + stage * 2 * half_stage + p0 * pitch + hl * (D * 2);
+      const uint32_t kb = smem_addr(attn_dyn) + stage * 2 * half_stage + off(p0) + hl * (D * 2);
       const uint32_t vb = kb + half_stage;
       const unsigned char* tr = there[stage] + p0;
       uint64_t* const read = &empty[stage];
@@ -246,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
       // ---- scores of the warp's 16 positions: two n-tiles of 8
       float s[MT][2][4] = {};
       const uint32_t ka =
-          kb + ((lane & 7) + ((lane >> 4) << 3)) * pitch + ((lane >> 3) & 1) * 16;
+          kb + off((lane & 7) + ((lane >> 4) << 3)) + ((lane >> 3) & 1) * 16;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         uint32_t b[4];                 // positions 0-7: k 0-7, k 8-15; positions 8-15: the same
@@ -280,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
       if (x0 < x1) {
         for (int x = x0; x < x1; ++x)
           for (int i = lane; i < D / 2; i += 32)
-            wild |= not_finite(lds32(vb + x * pitch + i * 4)) != 0;
+            wild |= not_finite(lds32(vb + off(x) + i * 4)) != 0;
         wild = __any_sync(0xffffffffu, wild);
       }
       const uint4 all = *reinterpret_cast<const uint4*>(tr);
@@ -331,7 +349,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
           }
         }
         // ---- weighted values
-        const uint32_t va = vb + (lane & 15) * pitch + (lane >> 4) * 16;
+        const uint32_t va = vb + off(lane & 15) + (lane >> 4) * 16;
         if (!wild) {
 #pragma unroll
           for (int n = 0; n < D / 16; ++n) {
@@ -363,7 +381,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
               if (r >= rows || pos0 + x >= sg.len - a.q_len + 1 + (r0 + r) / a.G) continue;
 #pragma unroll
               for (int n = 0; n < D / 8; ++n) {
-                uint32_t v = lds32(vb + x * pitch + (n * 8 + q0) * 2);
+                uint32_t v = lds32(vb + off(x) + (n * 8 + q0) * 2);
                 v &= not_finite(v);
                 o[mt][n][half * 2] += __uint_as_float(v << 16);
                 o[mt][n][half * 2 + 1] += __uint_as_float(v & 0xffff0000u);
@@ -465,11 +483,14 @@ static_assert(kTile == 16 * kWarps, "a warp takes 16 rows");
 template <int D, int MT>
 cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
   // the ring, and behind it the joins (none with a head a warp) or the warps' Q
-  const int stage = 2 * kTile / a.hw * (a.hw * D * 2 + 16);
+  const int tpos = kTile / a.hw, stage = 2 * (tpos * a.hw * D * 2 + (tpos >> a.group_shift) * 16);
   const int join = (a.hw == 4 ? 0 : a.hw) * MT * 16 * (D + 4) * 4;
   const int q = MT == 1 ? 0 : kWarps * MT * 16 * (D * 2 + 16);
   int stages = D == 64 ? 4 : 3;
-  while (stages > 2 && stages * stage + std::max(join, q) > 224 * 1024) --stages;
+  // as many as let the grid's blocks of an SM all be there (228 KB, less what the
+  // kernel has besides)
+  const int most = 228 * 1024 / attn_mma_blocks(D, MT * 16) - 3 * 1024;
+  while (stages > 2 && stages * stage + std::max(join, q) > most) --stages;
   const int smem = stages * stage + std::max(join, q);
   static std::atomic<uint64_t> full;
   const cudaError_t e = mix_full_smem(reinterpret_cast<const void*>(attn_mma_kernel<D, MT>), full);
