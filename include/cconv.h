@@ -601,9 +601,10 @@ CCONV_API int attn_norm_rope_cache(const void* q, int64_t q_row_stride, const vo
  * block_table[s][j / page_size]. Per query head h over kv head h / (num_q_heads
  * / num_kv_heads):
  *   out = sum_j softmax_j(scale * q.k_j) v_j,  lse = log sum_j exp(scale * q.k_j)
- * Scores, softmax statistics and sums are fp32; the bf16 kernel rounds the
- * softmax weights to bf16 for the product with v. A row that sees nothing gets
- * out = 0 and lse = -inf.
+ * Scores, softmax statistics and sums are fp32; the bf16 kernel takes the
+ * softmax weights as sums of two bf16 terms (about 16 bits) for the product with
+ * v, and rounds the result once. A row that sees nothing gets out = 0 and lse =
+ * -inf.
  *
  *   q, out       [num_seqs * q_len, num_q_heads * head_dim], row strides
  *   block_table  int32 [num_seqs, table_width] with row stride

@@ -19,14 +19,14 @@
 // apart than their length, so that ldmatrix meets no bank conflict, or one of two
 // or four positions: with a copy a position the copies were what bounded small
 // rows. Each warp takes 16 rows, of
-// one head: scores = Q K^T, running maximum and sum of its own, weights to bf16
-// in registers (the score layout of one product is the weight layout of the
-// next), weighted values += P V. No barrier between warps but the ring's; warps
+// one head: scores = Q K^T, running maximum and sum of its own, weights to two
+// bf16 terms in registers (the score layout of one product is the weight layout of
+// the next), weighted values += P V. No barrier between warps but the ring's; warps
 // of one head join their parts once per segment, through shared memory.
 //
 // Measured, heads of 128, 4 kv heads, 16 query heads: 256 requests of 1 to 8192
-// positions (2.1 GB) 331 us, 6.4 TB/s; one of 131072 (270 MB) 47 us and 8 more
-// for the join; 64 requests of up to 4096 with 4 tokens each (0.25 GB) 56 us. With
+// positions (2.1 GB) 339 us, 6.3 TB/s; one of 131072 (270 MB) 57 us with its join;
+// 64 requests of up to 4096 with 4 tokens each (0.25 GB) 57 us. With
 // 2 kv heads, 256 requests (1.06 GB): 179 us, 5.9 TB/s; with a copy a position,
 // and a ring that left the grid's second block of an SM no room, 354 us.
 //
@@ -78,6 +78,19 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+// Two weights as two bf16 terms, each pair packed (x0 low): 16 bits of them, so
+// that the one rounding of a result is its last. With one term (331 us for the 256
+// requests) the results were 2.1e-3 of their norm off instead of 1.7e-3. The first term is cut, not rounded:
+// the second one then is not negative, and is kept above zero for a weight that is,
+// since otherwise the terms' products with an infinite value would make NaN.
+__device__ __forceinline__ float rest(float x) {
+  const float r = x - __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+  return fmaxf(r, fminf(x, 0x1p-126f));
+}
+__device__ __forceinline__ void split_weights(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  hi = __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632);
+  lo = pack_bf16x2(rest(x0), rest(x1));
 }
 // All ones in the halves of a bf16 pair that are infinite or NaN.
 __device__ __forceinline__ uint32_t not_finite(uint32_t v) {
@@ -320,7 +333,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        uint32_t pw[4];
+        uint32_t pw[4], pl[4];
         float corr[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -336,8 +349,8 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
           const float x0 = ex2(s0 - base), x1 = ex2(s1 - base), x2 = ex2(s2 - base),
                       x3 = ex2(s3 - base);
           l[mt][half] = fmaf(l[mt][half], corr[half], (x0 + x1) + (x2 + x3));
-          pw[half] = pack_bf16x2(x0, x1);
-          pw[2 + half] = pack_bf16x2(x2, x3);
+          split_weights(x0, x1, pw[half], pl[half]);
+          split_weights(x2, x3, pw[2 + half], pl[2 + half]);
         }
         if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
 #pragma unroll
@@ -352,11 +365,18 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
         const uint32_t va = vb + off(lane & 15) + (lane >> 4) * 16;
         if (!wild) {
 #pragma unroll
-          for (int n = 0; n < D / 16; ++n) {
-            uint32_t b[4];             // dims 0-7: positions 0-7, 8-15; dims 8-15: the same
+          for (int n = 0; n < D / 16; n += 2) {
+            uint32_t b[4], c[4];       // dims 0-7: positions 0-7, 8-15; dims 8-15: the same
             ldm4t(b, va + n * 32);
+            ldm4t(c, va + n * 32 + 32);
             mma(o[mt][2 * n], pw, b[0], b[1]);
             mma(o[mt][2 * n + 1], pw, b[2], b[3]);
+            mma(o[mt][2 * n + 2], pw, c[0], c[1]);
+            mma(o[mt][2 * n + 3], pw, c[2], c[3]);
+            mma(o[mt][2 * n], pl, b[0], b[1]);
+            mma(o[mt][2 * n + 1], pl, b[2], b[3]);
+            mma(o[mt][2 * n + 2], pl, c[0], c[1]);
+            mma(o[mt][2 * n + 3], pl, c[2], c[3]);
           }
         } else {
           const int q0 = (lane & 3) * 2;
@@ -372,6 +392,8 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
             }
             mma(o[mt][2 * n], pw, b[0], b[1]);
             mma(o[mt][2 * n + 1], pw, b[2], b[3]);
+            mma(o[mt][2 * n], pl, b[0], b[1]);
+            mma(o[mt][2 * n + 1], pl, b[2], b[3]);
           }
 #pragma unroll 1
           for (int x = x0; x < x1; ++x)
