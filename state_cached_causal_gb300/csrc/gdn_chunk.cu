@@ -23,15 +23,14 @@
 // V as the A operand from shared memory and before the chain arrives; T R then
 // adds -T e^G S^T k to it.
 //
-// Precision. k, q and v are bf16 and exact. fp32 factors (S, R, T, N) enter as
-// sums of two bf16 terms (about 16 bits; products lo * lo are left out), since
-// the state must keep more than 8 bits over thousands of tokens: its error is
-// 4e-6 of its norm against 64 bits, where single bf16 factors give 2e-3. The
-// outputs are rounded to bf16 themselves (1.7e-3 of their norm): their products
-// take S in S^T q and the scores with one term (2.3e-3 in all; with one term
-// for N too, 2.6e-3, and no faster: 889 us at 16384 tokens either way. A second
-// term for S there makes 2.2e-3, and 907 us). S is held in fp32 registers from
-// the first chunk to the last. l2 norms enter as factors of the rows, so that
+// Precision. k, q and v are bf16 and exact. fp32 factors (S, R, T, N, the scores)
+// enter as sums of two bf16 terms (about 16 bits; products lo * lo are left out),
+// since the state must keep more than 8 bits over thousands of tokens: its error
+// is 4e-6 of its norm against 64 bits, where single bf16 factors give 2e-3. The
+// outputs are rounded once, when they are stored: 1.7e-3 of their norm against 64
+// bits, 1.4e-4 against the rounded ones of 64 bits. (With one term for the scores
+// and for S in S^T q they were 2.3e-3 off; 887 us at 16384 tokens then, 926 now.)
+// S is held in fp32 registers from the first chunk to the last. l2 norms enter as factors of the rows, so that
 // raw rows are multiplied. G is kept as whole part + remainder (in powers of
 // two): chunks with strong decays reach sums of several hundred, whose
 // differences fp32 alone would round by 1e-5.
@@ -56,16 +55,17 @@
 // lo) 256-319, T V + T R 320-383, in-chunk output 384-447, [K; Q] K^T 448-511.
 //
 // What bounds it. A chain is serial: at 16384 tokens of one request 256 links of
-// 3.5 us, 0.89 ms, on 32 of the SMs (one a head); its bytes would take 0.06 ms
+// 3.6 us, 0.93 ms, on 32 of the SMs (one a head); its bytes would take 0.06 ms
 // and its products less. With 16 requests of up to 2048 tokens and 32 heads the
-// 512 chains fill the GPU: 0.26 ms, where bytes take 0.10; the longest chains and
+// 512 chains fill the GPU: 0.28 ms, where bytes take 0.07; the longest chains and
 // the whole work weigh alike there. Inside a link every wait is short, and the
 // roles' code together (72 KB) is larger than the instruction caches near the
 // schedulers, so code size counts: unrolled loops and waits of 161 KB took 0.61
-// ms for the 16 requests and 128 single tokens that take 0.36 now, and what is
+// ms for the 16 requests and 128 single tokens that take 0.37 now, and what is
 // not on the chain stays rolled. Token by token (gdn_step.cu) the long chain
 // takes 21.5 ms.
 #include <cuda.h>
+#include <math.h>
 #include <stddef.h>
 
 #include <mutex>
@@ -97,10 +97,10 @@ constexpr uint32_t kVPanel = kC * 128;       // 64 dv of V
 constexpr uint32_t kVBytes = kC * kD * 2;    // V, later the chunk's outputs [64][128]
 constexpr uint32_t kStageBytes = kKQBytes + kVBytes;
 constexpr uint32_t kTBytes = kC * kC * 2;    // one 64 x 64 bf16 operand
-constexpr uint32_t kTP = 3 * kTBytes;        // T hi, T lo, scores
+constexpr uint32_t kDiagBytes = 16 * 128;    // four 16 x 16 blocks side by side
+constexpr uint32_t kTP = 3 * kTBytes + kDiagBytes;   // T hi, T lo, scores (see p_lo)
 constexpr int kMaxSeqs = 640;                // sequences of a launch
 constexpr int kB = 16;                       // blocks of A and T
-constexpr int kBPitch = 20;                  // fp32 rows of 16: 80 bytes
 constexpr int kCoefs = 4;                    // chunks whose factors are kept
 
 constexpr uint32_t kColS = 0, kColKS = 128, kColN = kColKS, kColQS = 192, kColR = 256,
@@ -139,6 +139,21 @@ __device__ __forceinline__ int a_left(int i, int k, int row, int unit) {   // of
   return ((i * (i - 1) / 2 + k) * kB + row) * kB + ((unit ^ ((row >> 2) & 1)) << 3);
 }
 
+__device__ __forceinline__ uint32_t sw128(int row, int unit) {
+  return (uint32_t)(row * 128 + ((unit ^ (row & 7)) << 4));
+}
+
+// Scores: 10 blocks of 16 x 16 on and below the diagonal, in two bf16 terms. The
+// first terms lie where they belong, block (I, J) in rows I and columns J of the
+// tile; the second ones of the six blocks below the diagonal in the tile's free
+// half, (I, J) in rows I - J - 1 and columns 3 - J, so that those of one J lie one
+// below the other, as a product takes them; the second ones of the diagonal in a
+// tile of 16 rows behind. Offset of row `row`, unit `unit` of a second term:
+__device__ __forceinline__ uint32_t p_lo(int I, int J, int row, int unit) {
+  return J < I ? sw128((I - J - 1) * kB + row, (3 - J) * 2 + unit)
+               : kTBytes + sw128(row, J * 2 + unit);
+}
+
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
   uint64_t gate_empty[2], tp_empty[2], coef_full[kCoefs], coef_empty[kCoefs];
@@ -154,7 +169,6 @@ struct Smem {
   unsigned char stage[kStages][kStageBytes];   // 1024-byte aligned
   unsigned char tp[2][kTP];
   Blocks A[2];
-  alignas(16) float ed[kC][kBPitch];           // e^{G_i - G_j} / |k_j|, j in the block of i
   alignas(16) float tab[4][kC];                // e^{G_(16I-1) - G_j} / |k_j|, j < 16 I
   alignas(16) float rn[kStages][2 * kC];        // 1 / |k|, 1 / |q|
   Coef coef[kCoefs];
@@ -167,15 +181,11 @@ static_assert(offsetof(Smem, tp) % 1024 == 0 && kStageBytes % 1024 == 0 && kTP %
                   kTBytes % 1024 == 0 && kVPanel % 1024 == 0,
               "swizzled tiles start on 1024 bytes");
 static_assert(sizeof(Coef) % 16 == 0 && sizeof(Gate) % 16 == 0 && sizeof(Blocks) % 16 == 0 &&
-                  offsetof(Smem, A) % 16 == 0 && offsetof(Smem, ed) % 16 == 0 &&
+                  offsetof(Smem, A) % 16 == 0 &&
                   offsetof(Smem, tab) % 16 == 0 && offsetof(Smem, rn) % 16 == 0 &&
                   offsetof(Smem, coef) % 16 == 0 && offsetof(Smem, gate) % 16 == 0 &&
                   offsetof(Smem, ctl) % 8 == 0,
               "16-byte accesses");
-
-__device__ __forceinline__ uint32_t sw128(int row, int unit) {
-  return (uint32_t)(row * 128 + ((unit ^ (row & 7)) << 4));
-}
 
 // A wait of a whole warp on a phase: false when it has run out of time, and the
 // role gives up (what waits for it runs out of time in turn). Few instructions,
@@ -574,76 +584,85 @@ __device__ __forceinline__ bool prep_role(const GdnArgs& a, Smem& sm, const Wait
       for (int I = 1; I < 4; ++I)
         if ((I == 3) == is_k && r < I * kB)
           sm.tab[I][r] = rk * tc::ex2((G.hi[I * kB - 1] - hi) + (G.lo[I * kB - 1] - lo));
-      const int c0 = is_k ? 0 : 8;
-#pragma unroll
-      for (int c4 = 0; c4 < 8; c4 += 4) {
-        const int j = blk * kB + c0 + c4;
-        const float4 h4 = *reinterpret_cast<const float4*>(&G.hi[j]);
-        const float4 l4 = *reinterpret_cast<const float4*>(&G.lo[j]);
-        const float4 k4 = *reinterpret_cast<const float4*>(&rns[j]);
-        *reinterpret_cast<float4*>(&sm.ed[r][c0 + c4]) =
-            make_float4(j <= r ? k4.x * tc::ex2((hi - h4.x) + (lo - l4.x)) : 0.0f,
-                        j + 1 <= r ? k4.y * tc::ex2((hi - h4.y) + (lo - l4.y)) : 0.0f,
-                        j + 2 <= r ? k4.z * tc::ex2((hi - h4.z) + (lo - l4.z)) : 0.0f,
-                        j + 3 <= r ? k4.w * tc::ex2((hi - h4.w) + (lo - l4.w)) : 0.0f);
-      }
     }
     const float fac = is_k ? rn : a.scale * rn;
     const float off =
         blk > 0 ? fac * tc::ex2((hi - G.hi[blk * kB - 1]) + (lo - G.lo[blk * kB - 1])) : 0.0f;
     warp_arrive(&sm.ctl.coef_full[n % kCoefs]);
+    // the row's factors of the diagonal block, zero above it (in registers: worked
+    // out where they are used, in half of a warp's lanes at a time, they made 16384
+    // tokens 1317 us)
+    float e[kB];
+#pragma unroll
+    for (int j4 = 0; j4 < kB; j4 += 4) {
+      const int j = blk * kB + j4;
+      const float4 h4 = *reinterpret_cast<const float4*>(&G.hi[j]);
+      const float4 l4 = *reinterpret_cast<const float4*>(&G.lo[j]);
+      const float4 k4 = *reinterpret_cast<const float4*>(&rns[j]);
+      float d[4], f[4];
+      fma_x2(d[0], d[1], l4.x, l4.y, -1.0f, -1.0f, lo, lo);
+      fma_x2(d[2], d[3], l4.z, l4.w, -1.0f, -1.0f, lo, lo);
+      fma_x2(f[0], f[1], h4.x, h4.y, -1.0f, -1.0f, hi, hi);
+      fma_x2(f[2], f[3], h4.z, h4.w, -1.0f, -1.0f, hi, hi);
+      fma_x2(d[0], d[1], f[0], f[1], 1.0f, 1.0f, d[0], d[1]);
+      fma_x2(d[2], d[3], f[2], f[3], 1.0f, 1.0f, d[2], d[3]);
+      mul_x2(f[0], f[1], k4.x, k4.y, fac, fac);
+      mul_x2(f[2], f[3], k4.z, k4.w, fac, fac);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] = tc::ex2(j + i <= r ? d[i] : -INFINITY);
+      mul_x2(e[j4], e[j4 + 1], d[0], d[1], f[0], f[1]);
+      mul_x2(e[j4 + 2], e[j4 + 3], d[2], d[3], f[2], f[3]);
+    }
     if (!meet(wait)) return false;
-    // ---- A and the scores from [K; Q] K^T: row r times the factors of its
-    // columns, e^{G_i - G_j} as two factors at most 1 around the block's start
+    // ---- A and the scores from [K; Q] K^T: row r times the factors of its columns
     if (!wait(&sm.ctl.d1_full, n)) return false;
     tc::fence_after();
     if (n >= 2 && !wait(is_k ? &sm.ctl.a_empty[bf] : &sm.ctl.tp_empty[bf], (n >> 1) - 1))
       return false;
     unsigned char* const scores = sm.tp[bf] + 2 * kTBytes;
     const uint32_t d1 = tmem + kColD1 + ((uint32_t)(warp * 32) << 16);
+    // (the last block that one of the warp's rows has)
+    const int last = (warp & 1) * 2 + 1;
 #pragma unroll 1
-    for (int J = 0; J < 4; ++J) {
+    for (int J = 0; J <= last; ++J) {
       uint32_t x[16];
       tc::ld16(d1 + J * 16, x);
       tc::wait_ld(x);
-      // blocks right of the diagonal are zero and their factors not set
-      const float m = J < blk ? off : fac;
-      const float* q = J == blk ? sm.ed[r] : &sm.tab[blk][J * kB];
-      float y[16];
+      if (J <= blk) {
+        // left of the diagonal: e^{G_i - G_j} as two factors at most 1 around the
+        // start of the row's block
+        float y[16];
 #pragma unroll
-      for (int j4 = 0; j4 < 16; j4 += 4) {
-        const float4 t = J <= blk ? *reinterpret_cast<const float4*>(q + j4)
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-        mul_x2(y[j4], y[j4 + 1], m * t.x, m * t.y, __uint_as_float(x[j4]),
-               __uint_as_float(x[j4 + 1]));
-        mul_x2(y[j4 + 2], y[j4 + 3], m * t.z, m * t.w, __uint_as_float(x[j4 + 2]),
-               __uint_as_float(x[j4 + 3]));
-      }
-      if (is_k) {
-        if (J < blk) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            uint4 h, l;
-            split8(y + u * 8, h, l);
-            const int at = a_left(blk, J, r & (kB - 1), u);
-            *reinterpret_cast<uint4*>(&sm.A[bf].hi[at]) = h;
-            *reinterpret_cast<uint4*>(&sm.A[bf].lo[at]) = l;
-          }
-        } else if (J == blk) {
+        for (int j4 = 0; j4 < 16; j4 += 4) {
+          const float4 t = *reinterpret_cast<const float4*>(&sm.tab[blk][J * kB + j4]);
+          const bool left = J < blk;
+          mul_x2(y[j4], y[j4 + 1], left ? off * t.x : e[j4], left ? off * t.y : e[j4 + 1],
+                 __uint_as_float(x[j4]), __uint_as_float(x[j4 + 1]));
+          mul_x2(y[j4 + 2], y[j4 + 3], left ? off * t.z : e[j4 + 2], left ? off * t.w : e[j4 + 3],
+                 __uint_as_float(x[j4 + 2]), __uint_as_float(x[j4 + 3]));
+        }
+        if (is_k && J == blk) {
 #pragma unroll
           for (int j4 = 0; j4 < 16; j4 += 4)
             *reinterpret_cast<float4*>(&sm.A[bf].d[a_diag(r, j4 >> 2)]) =
                 make_float4(y[j4], y[j4 + 1], y[j4 + 2], y[j4 + 3]);
-        }
-      } else {
+        } else {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-          *reinterpret_cast<uint4*>(scores + sw128(r, J * 2 + u)) =
-              make_uint4(pack_bf16x2(y[u * 8], y[u * 8 + 1]),
-                         pack_bf16x2(y[u * 8 + 2], y[u * 8 + 3]),
-                         pack_bf16x2(y[u * 8 + 4], y[u * 8 + 5]),
-                         pack_bf16x2(y[u * 8 + 6], y[u * 8 + 7]));
+          for (int u = 0; u < 2; ++u) {
+            uint4 h, l;
+            split8(y + u * 8, h, l);
+            if (is_k) {
+              const int at = a_left(blk, J, r & (kB - 1), u);
+              *reinterpret_cast<uint4*>(&sm.A[bf].hi[at]) = h;
+              *reinterpret_cast<uint4*>(&sm.A[bf].lo[at]) = l;
+            } else {
+              *reinterpret_cast<uint4*>(scores + sw128(r, J * 2 + u)) = h;
+              *reinterpret_cast<uint4*>(scores + p_lo(blk, J, r & (kB - 1), u)) = l;
+            }
+          }
+        }
       }
+      __syncwarp();
     }
     tc::fence_before();
     warp_arrive(&sm.ctl.d1_empty);
@@ -654,7 +673,7 @@ __device__ __forceinline__ bool prep_role(const GdnArgs& a, Smem& sm, const Wait
       warp_arrive(&sm.ctl.p_full[bf]);
     }
     warp_arrive(&sm.ctl.gate_empty[bf]);
-    if (!meet(wait)) return false;     // ed, tab and rn are free for the next chunk
+    if (!meet(wait)) return false;     // tab and rn are free for the next chunk
   }
   return true;
 }
@@ -1009,8 +1028,11 @@ __device__ __forceinline__ bool mma_role(Smem& sm, const Wait& wait, int chunks,
         tc::fence_after();
         if (tc::elect()) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)        // S hi
-            tc::mma_ts(tmem + kColQS, tmem + kColS + ks * 16, kq + panel(ks, kC), kId, ks > 0);
+          for (int t = 0; t < 2; ++t)           // S hi, S lo
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              tc::mma_ts(tmem + kColQS, tmem + kColS + ks * 16 + t * 8, kq + panel(ks, kC), kId,
+                         (t | ks) > 0);
           tc::commit(&sm.ctl.qs_done);
         }
         __syncwarp();
@@ -1045,12 +1067,24 @@ __device__ __forceinline__ bool mma_role(Smem& sm, const Wait& wait, int chunks,
           tc::commit(&sm.ctl.sd_full[part]);
         }
         tc::commit(&sm.ctl.empty[st]);
+        // in-chunk outputs: tokens j of a block ks reach the tokens i of that block
+        // and of those behind it, i.e. rows [16 ks, 64) of the scores
 #pragma unroll
-        for (int t = 0; t < 2; ++t)             // N hi, N lo
+        for (int t = 0; t < 2; ++t)             // N hi P hi, N lo P hi
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            tc::mma_ts(tmem + kColO, tmem + kColN + t * 32 + ks * 8,
-                       tp + ((2 * kTBytes + ks * 32) >> 4), kId, (t | ks) > 0);
+            tc::mma_ts(tmem + kColO + ks * kB, tmem + kColN + t * 32 + ks * 8,
+                       tp + ((2 * kTBytes + ks * (kB * 128 + 32)) >> 4),
+                       tc::idesc(128, kC - ks * kB), (t | ks) > 0);
+#pragma unroll
+        for (int ks = 0; ks < 3; ++ks)          // N hi P lo, below the diagonal
+          tc::mma_ts(tmem + kColO + (ks + 1) * kB, tmem + kColN + ks * 8,
+                     tp + ((2 * kTBytes + (3 - ks) * 32) >> 4),
+                     tc::idesc(128, kC - (ks + 1) * kB), true);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)          // on it
+          tc::mma_ts(tmem + kColO + ks * kB, tmem + kColN + ks * 8,
+                     tp + ((3 * kTBytes + ks * 32) >> 4), tc::idesc(128, kB), true);
         tc::commit(&sm.ctl.o_full);
         tc::commit(&sm.ctl.tp_empty[n & 1]);
       }
