@@ -29,7 +29,7 @@
 // is 4e-6 of its norm against 64 bits, where single bf16 factors give 2e-3. The
 // outputs are rounded once, when they are stored: 1.7e-3 of their norm against 64
 // bits, 1.4e-4 against the rounded ones of 64 bits. (With one term for the scores
-// and for S in S^T q they were 2.3e-3 off; 887 us at 16384 tokens then, 926 now.)
+// and for S in S^T q they were 2.3e-3 off; 887 us at 16384 tokens then, 929 now.)
 // S is held in fp32 registers from the first chunk to the last. l2 norms enter as factors of the rows, so that
 // raw rows are multiplied. G is kept as whole part + remainder (in powers of
 // two): chunks with strong decays reach sums of several hundred, whose
@@ -377,7 +377,7 @@ __device__ __forceinline__ bool load_role(const GdnArgs& a, const Maps& maps, Sm
       for (int i = 0; i < 2; ++i) {
         const bool in = tok + i * 32 < len;
         const float x = (i == 0 ? na[0] : na[1]) + dtb;
-        float gl = A_log2 * (fmaxf(x, 0.0f) + log1pf(__expf(-fabsf(x))));
+        float gl = A_log2 * gdn_softplus(x);
         // a decay below 2^-150 is zero in fp32 whatever follows (a NaN stays one)
         gl = in ? (gl < -150.0f ? -150.0f : gl) : 0.0f;
         float w = truncf(gl), f = gl - w;
@@ -397,8 +397,7 @@ __device__ __forceinline__ bool load_role(const GdnArgs& a, const Maps& maps, Sm
         f0 = __shfl_sync(0xffffffffu, f, 31);
         G.hi[i * 32 + lane] = w;
         G.lo[i * 32 + lane] = f;
-        G.beta[i * 32 + lane] =
-            in ? __fdividef(1.0f, 1.0f + __expf(-(i == 0 ? nb[0] : nb[1]))) : 0.0f;
+        G.beta[i * 32 + lane] = in ? gdn_beta(i == 0 ? nb[0] : nb[1]) : 0.0f;
       }
       if (!whole) {
         cp_async_wait<0>();

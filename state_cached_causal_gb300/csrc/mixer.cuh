@@ -67,9 +67,11 @@ __device__ __forceinline__ float elem(const T* p, int64_t i) {
 }
 
 // The gates of one token and value head: log decay and write strength.
+__device__ __forceinline__ float gdn_softplus(float x) {
+  return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
+}
 __device__ __forceinline__ float gdn_log_decay(float a, float A_log, float dt_bias) {
-  const float x = a + dt_bias;
-  return -expf(A_log) * (fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))));
+  return -expf(A_log) * gdn_softplus(a + dt_bias);
 }
 __device__ __forceinline__ float gdn_beta(float b) { return 1.0f / (1.0f + expf(-b)); }
 

@@ -5,6 +5,8 @@ fp32, and the state is off by a few of 2^-18, so that an output is off by 2^-15 
 its rounding; against the rounded result of 64 bits that makes 2^-11 of the norm (as in
 test_attn_rounding.py). One bf16 term for the scores or the state makes twice to four times that.
 """
+import math
+
 import pytest
 import torch
 
@@ -45,3 +47,28 @@ def test_one_rounding(lens, st_dtype):
 def test_one_rounding_with_gates_at_their_ends():
     worst = max(errors(52, [130, 70], 1, 2, F32, gates="ends"))
     assert worst <= 2.0 ** -11, f"{worst:.3g}"
+
+
+@pytest.mark.parametrize("n", [5, 9, 64, 130])
+def test_decays_are_those_of_64_bits(n):
+    """Keys of zero leave a state that only decays: its error is the gates' own. Gates far out (a softplus
+    of e^-80 under a rate of e^80) by either kernel. The log decay of a token is two exponentials, a
+    log1p and two products, each off by 1 or 2 of 2^-24: under 5e-7 of it. The n tokens' sum is 8, so
+    that the state is off by 4e-6, and 1e-6 for the last exponential; exponentials whose argument was
+    rounded after a product with log2(e) would make 8 * 80 * 2^-24 = 4e-5."""
+    hv = 4
+    inp = list(inputs(53, n, 2, hv, 128, 128, BF16, spare=0))
+    inp[1] = torch.zeros_like(inp[1])
+    inp[3] = torch.tensor([-80.0, -76.0, -60.0, -40.0], device=DEV).expand(n, hv).to(BF16).contiguous()
+    inp[5] = -inp[3][0].float() - math.log(n / 8)
+    inp[6] = torch.zeros(hv, device=DEV)
+    st = pool(53, 1, hv, 128, 128, F32)
+    S0 = st[0].double().cpu()
+    out = torch.zeros(n, hv, 128, device=DEV, dtype=BF16)
+    ops.gdn_fwd_varlen(*inp, st, torch.zeros(1, dtype=torch.int32, device=DEV),
+                       torch.tensor([0, n], dtype=torch.int32, device=DEV), None, 0.1, out)
+    torch.cuda.synchronize()
+    cpu = [t.double().cpu() for t in inp]
+    want = gdn_ref(*cpu, S0, 0.1)[1][-1]
+    err = (st[0].double().cpu() - want).flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1)
+    assert err.max().item() <= 1e-5, err
