@@ -428,6 +428,22 @@ def _vector(t, name, dtype, n):
         raise ValueError(f"{name} must be a contiguous vector of {n}")
 
 
+def _entries(t, name, n, flags=False):
+    """An index vector (or a vector of flags) whose first n entries the library reads side by side."""
+    if t is None:
+        return
+    (_u8 if flags else _i32)(t, name)
+    if t.dim() == 0 or t.numel() != t.shape[0] or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector")
+    if t.numel() < n:
+        raise ValueError(f"{name} must have {n} entries")
+
+
+def _error_word(dev_err):
+    if dev_err is not None and (_i32(dev_err, "dev_err").numel() < 1):
+        raise ValueError("dev_err must have an entry")
+
+
 def _gates(t, name, dtype, rows, hv):
     if t.dtype is not dtype:
         raise TypeError(f"{name} must have the call's dtype")
@@ -441,6 +457,7 @@ def _gdn_call(fn, q, k, v, a, b, A_log, dt_bias, states, out, rows, scale, l2nor
               index, middle):
     """index: the int32/uint8 tensors after the pool; middle(addresses) -> the C arguments between
     the pool and the head counts."""
+    _error_word(dev_err)
     dtype = k.dtype
     hk, dk, ks = _heads(k, "k", dtype, rows)
     hv, dv, vs = _heads(v, "v", dtype, rows)
@@ -479,11 +496,11 @@ def gdn_fwd_varlen(q, k, v, a, b, A_log, dt_bias, states, state_idx, cu_seqlens,
                 q, k, v, a, b, A_log, dt_bias, states, state_idx, cu_seqlens, has_init, scale, out,
                 qk_l2norm, dev_err, num_tokens)):
         return
-    _i32(state_idx, "state_idx")
-    _i32(cu_seqlens, "cu_seqlens")
-    _u8(has_init, "has_init")
+    _entries(state_idx, "state_idx", 0)
     T = q.shape[0] if num_tokens is None else int(num_tokens)
     B = state_idx.shape[0]
+    _entries(cu_seqlens, "cu_seqlens", B + 1)
+    _entries(has_init, "has_init", B, flags=True)
     if cu_seqlens.shape[0] != B + 1:
         raise ValueError("cu_seqlens must have one entry more than state_idx")
     _gdn_call("gdn_fwd_varlen", q, k, v, a, b, A_log, dt_bias, states, out, T, scale,
@@ -506,8 +523,10 @@ def gdn_update(q, k, v, a, b, A_log, dt_bias, states, state_idx, n_spec, num_acc
         return
     _i32(state_idx, "state_idx")
     _i32(num_accepted, "num_accepted")
-    _u8(has_init, "has_init")
     B = state_idx.shape[0]
+    _entries(has_init, "has_init", B, flags=True)
+    if n_spec > 0:                  # (else it is not read)
+        _entries(num_accepted, "num_accepted", B)
     if state_idx.numel() != B * (1 + n_spec) or not state_idx.is_contiguous():
         raise ValueError("state_idx must be a contiguous [requests, 1 + n_spec]")
     _gdn_call("gdn_update", q, k, v, a, b, A_log, dt_bias, states, out, B * (1 + n_spec), scale,
@@ -545,8 +564,9 @@ def attn_norm_rope_cache(q, k, v, q_weight, k_weight, eps, cos_sin, positions, i
                 q, k, v, q_weight, k_weight, eps, cos_sin, positions, interleaved, k_cache,
                 v_cache, slot_mapping, q_out, dev_err)):
         return
-    _i32(positions, "positions")
-    _i32(slot_mapping, "slot_mapping")
+    _entries(positions, "positions", q.shape[0])
+    _entries(slot_mapping, "slot_mapping", q.shape[0])
+    _error_word(dev_err)
     dtype = q.dtype
     (pages, page, hkv, dim), st, code = _cache(k_cache, v_cache, dtype)
     T, hq = q.shape[0], q.shape[1]
@@ -554,8 +574,6 @@ def attn_norm_rope_cache(q, k, v, q_weight, k_weight, eps, cos_sin, positions, i
     ks = _heads(k, "k", dtype, T, hkv, dim)[2]
     vs = _heads(v, "v", dtype, T, hkv, dim)[2]
     os_ = _heads(q_out, "q_out", dtype, T, hq, dim)[2]
-    if positions.shape[0] < T or slot_mapping.shape[0] < T:
-        raise ValueError("positions and slot_mapping must have q's rows")
     if q_weight is not None:
         _vector(q_weight, "q_weight", dtype, dim)
     if k_weight is not None:
@@ -595,7 +613,10 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, n_spec, scale, out, 
                 dev_err)):
         return
     _i32(block_table, "block_table")
-    _i32(seq_lens, "seq_lens")
+    _entries(seq_lens, "seq_lens", 0)
+    _error_word(dev_err)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     dtype = q.dtype
     (pages, page, hkv, dim), st, code = _cache(k_cache, v_cache, dtype)
     B = seq_lens.shape[0]

@@ -208,3 +208,59 @@ def test_both_marshallings_agree(what, monkeypatch):
     monkeypatch.setattr(ops, "_fast", None)
     for a, b in zip(one, call()):
         assert torch.equal(a, b)
+
+
+def _two():
+    """Two valid sets of arguments (host tensors): of the delta rule and of attention."""
+    z = torch.zeros
+    q, v, ab, c = z(4, 2, 64), z(4, 4, 64), z(4, 4), z(5, 16, 2, 64)
+    i = lambda *s: z(*s, dtype=torch.int32)                     # noqa: E731
+    gdn = dict(q=q, k=q, v=v, a=ab, b=ab, A_log=z(4), dt_bias=z(4), states=z(8, 4, 64, 64), scale=1.0, out=v)
+    norm = dict(q=v, k=q, v=q, q_weight=None, k_weight=None, eps=1e-6, cos_sin=z(9, 64), positions=i(4),
+                interleaved=False, k_cache=c, v_cache=c, slot_mapping=i(4), q_out=v)
+    attn = dict(q=v, k_cache=c, v_cache=c, block_table=i(4, 3), seq_lens=i(4), n_spec=0, scale=1.0, out=v)
+    return gdn, norm, attn, i
+
+
+def test_binding_refuses_short_and_strided_indices():
+    """Index and flag vectors are read as so many entries side by side: others are refused, by name."""
+    gdn, norm, attn, i = _two()
+    flags = torch.zeros(8, dtype=torch.uint8)
+    fwd = dict(gdn, state_idx=i(2), cu_seqlens=i(3), has_init=None)
+    upd = dict(gdn, state_idx=i(4), n_spec=0, num_accepted=None, has_init=None)
+    spec = dict(gdn, state_idx=i(2, 2), n_spec=1, num_accepted=i(2), has_init=None)
+    cases = [(ops.gdn_fwd_varlen, fwd, "state_idx", i(2, 4)[:, 0]), (ops.gdn_fwd_varlen, fwd, "state_idx", i(2, 4)),
+             (ops.gdn_fwd_varlen, fwd, "cu_seqlens", i(6)[::2]), (ops.gdn_fwd_varlen, fwd, "cu_seqlens", i(2)),
+             (ops.gdn_fwd_varlen, fwd, "has_init", flags[:1]), (ops.gdn_fwd_varlen, fwd, "has_init", flags[:4:2]),
+             (ops.gdn_update, upd, "state_idx", i(4, 2)[:, 0]), (ops.gdn_update, upd, "has_init", flags[:3]),
+             (ops.gdn_update, upd, "has_init", flags[::2]), (ops.gdn_update, spec, "num_accepted", i(1)),
+             (ops.gdn_update, spec, "num_accepted", i(4)[::2]),
+             (ops.attn_norm_rope_cache, norm, "positions", i(8)[::2]),
+             (ops.attn_norm_rope_cache, norm, "positions", i(3)),
+             (ops.attn_norm_rope_cache, norm, "slot_mapping", i(8)[::2]),
+             (ops.attn_norm_rope_cache, norm, "slot_mapping", i(3)),
+             (ops.attn_decode, attn, "seq_lens", i(4, 2)[:, 0]), (ops.attn_decode, attn, "seq_lens", i(4, 2)),
+             (ops.attn_decode, attn, "workspace", torch.zeros(64, 64, dtype=torch.uint8).t())]
+    for fn, call, name, bad in cases:
+        with pytest.raises(ValueError, match=name):
+            fn(**{**call, name: bad})
+    for fn, call in ((ops.gdn_fwd_varlen, fwd), (ops.gdn_update, upd), (ops.attn_norm_rope_cache, norm),
+                     (ops.attn_decode, attn)):
+        with pytest.raises(TypeError, match="dev_err"):
+            fn(**call, dev_err=torch.zeros(4, dtype=torch.uint8))
+        with pytest.raises(ValueError, match="dev_err"):
+            fn(**call, dev_err=i(0))
+
+
+def test_binding_takes_what_it_does_not_read():
+    """A short num_accepted without draft tokens, and vectors longer than needed, get as far as the check
+    of where the tensors live."""
+    gdn, norm, attn, i = _two()
+    flags = torch.zeros(8, dtype=torch.uint8)
+    for fn, call in ((ops.gdn_update, dict(gdn, state_idx=i(4), n_spec=0, num_accepted=i(1), has_init=flags)),
+                     (ops.gdn_update, dict(gdn, state_idx=i(4, 1), n_spec=0, num_accepted=None, has_init=None)),
+                     (ops.gdn_fwd_varlen, dict(gdn, state_idx=i(2, 1), cu_seqlens=i(3), has_init=flags)),
+                     (ops.attn_norm_rope_cache, {**norm, "positions": i(9), "slot_mapping": i(9)}),
+                     (ops.attn_decode, dict(attn, workspace=torch.zeros(9, dtype=torch.uint8)))):
+        with pytest.raises(ValueError, match="must live on the GPU"):
+            fn(**call)
