@@ -4,10 +4,10 @@
  * sizes, strides and addresses from Python took 20 us a call, in C it takes 3
  * to 4. The functions here take the arguments of the functions of the same
  * name in ops.py, check that everything is as the plain case has it -- tensor
- * types, layouts, sizes, device -- and make the call of libcconv.so on the
- * current stream. They return its status, or None where anything is not plain;
- * ops.py then takes its own way, which either serves the case or raises what is
- * wrong with it.
+ * types, layouts, sizes, all on the current device -- and make the call of
+ * libcconv.so on the current stream. They return its status, or None where
+ * anything is not plain; ops.py then takes its own way, which either serves the
+ * case or raises what is wrong with it.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -17,8 +17,9 @@
 
 enum { F32 = 0, BF16 = 1, I32 = 2, U8 = 3, NDT = 5 };
 static PyObject* dtypes[NDT]; /* float32, bfloat16, int32, uint8, bool */
-static PyObject *s_dtype, *s_is_cuda, *s_shape, *s_stride, *s_data_ptr, *s_get_device;
+static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device;
 static PyObject* raw_stream; /* device index -> cudaStream_t as an int */
+static PyObject* cur_device; /* () -> index of the current device */
 static PyObject* new_bytes;  /* (tensor, n) -> n bytes beside it */
 
 static int (*p_fwd)(const void*, int64_t, const void*, int64_t, const void*, int64_t, const void*,
@@ -47,8 +48,9 @@ typedef struct {
   int64_t n[4], s[4];
 } Ten;
 
-/* 1: a CUDA tensor of at most 4 dimensions and a known type, or None; 0: not. */
-static int get(PyObject* o, Ten* t) {
+/* 1: a CUDA tensor of at most 4 dimensions and a known type, or None; 0: not. *dev is the
+ * device of the call's tensors, -1 before the first one: another device is not plain. */
+static int get(PyObject* o, Ten* t, int* dev) {
   t->p = NULL;
   t->nd = -1;
   t->dt = -1;
@@ -59,11 +61,12 @@ static int get(PyObject* o, Ten* t) {
     if (d == dtypes[i]) t->dt = i == 4 ? U8 : i;
   Py_DECREF(d);
   if (t->dt < 0) return 0;
-  PyObject* c = PyObject_GetAttr(o, s_is_cuda);
+  PyObject* c = PyObject_CallMethodNoArgs(o, s_get_device);
   if (!c) return 0;
-  const int cuda = c == Py_True;
+  const long on = PyLong_AsLong(c);
   Py_DECREF(c);
-  if (!cuda) return 0;
+  if (on < 0 || (*dev >= 0 && on != *dev)) return 0; /* (a host tensor: -1) */
+  *dev = (int)on;
   PyObject* sh = PyObject_GetAttr(o, s_shape);
   if (!sh) return 0;
   PyObject* st = PyObject_CallMethodNoArgs(o, s_stride);
@@ -87,9 +90,13 @@ static int get(PyObject* o, Ten* t) {
 }
 
 /* A required tensor of this type. */
-static int need(PyObject* o, Ten* t, int dt) { return get(o, t) && t->nd >= 0 && t->dt == dt; }
+static int need(PyObject* o, Ten* t, int dt, int* dev) {
+  return get(o, t, dev) && t->nd >= 0 && t->dt == dt;
+}
 /* An optional one. */
-static int maybe(PyObject* o, Ten* t, int dt) { return get(o, t) && (t->nd < 0 || t->dt == dt); }
+static int maybe(PyObject* o, Ten* t, int dt, int* dev) {
+  return get(o, t, dev) && (t->nd < 0 || t->dt == dt);
+}
 
 /* [rows, heads, dim] with contiguous rows; *rs = row stride. */
 static int heads(const Ten* t, int64_t rows, int64_t h, int64_t d, int64_t* rs) {
@@ -109,10 +116,12 @@ static int vec(const Ten* t, int64_t n) {
 }
 static int flat(const Ten* t) { return t->nd == 1 && (t->n[0] <= 1 || t->s[0] == 1); }
 
-static int stream_of(PyObject* tensor, cconv_stream_t* st) {
-  PyObject* d = PyObject_CallMethodNoArgs(tensor, s_get_device);
+/* The current stream of device `dev`, which has to be the current device. */
+static int stream_of(int dev, cconv_stream_t* st) {
+  PyObject* d = PyObject_CallNoArgs(cur_device);
   if (!d) return 0;
-  PyObject* r = PyObject_CallOneArg(raw_stream, d);
+  const long cur = PyLong_AsLong(d);
+  PyObject* r = cur == dev && !PyErr_Occurred() ? PyObject_CallOneArg(raw_stream, d) : NULL;
   Py_DECREF(d);
   if (!r) return 0;
   *st = (cconv_stream_t)PyLong_AsVoidPtr(r);
@@ -128,17 +137,20 @@ static PyObject* not_plain(void) {
 typedef struct {
   Ten q, k, v, a, b, A, dtb, st, out, err;
   int64_t qs, ks, vs, as, bs, os, hk, hv, dk, dv;
+  int dev;
   gdn_state_t pool;
   cconv_stream_t stream;
 } Gdn;
 
-/* args: q k v a b A_log dt_bias states at 0..7 */
+/* args: q k v a b A_log dt_bias states at 0..7; g->dev is set */
 static int gdn(PyObject* const* x, PyObject* out, PyObject* err, int64_t rows, Gdn* g) {
-  if (!get(x[1], &g->k) || g->k.nd != 3 || (g->k.dt != F32 && g->k.dt != BF16)) return 0;
+  int* const dev = &g->dev;
+  if (!get(x[1], &g->k, dev) || g->k.nd != 3 || (g->k.dt != F32 && g->k.dt != BF16)) return 0;
   const int dt = g->k.dt;
-  if (!need(x[0], &g->q, dt) || !need(x[2], &g->v, dt) || !need(x[3], &g->a, dt) ||
-      !need(x[4], &g->b, dt) || !need(x[5], &g->A, F32) || !need(x[6], &g->dtb, F32) ||
-      !get(x[7], &g->st) || !need(out, &g->out, dt) || !maybe(err, &g->err, I32))
+  if (!need(x[0], &g->q, dt, dev) || !need(x[2], &g->v, dt, dev) ||
+      !need(x[3], &g->a, dt, dev) || !need(x[4], &g->b, dt, dev) ||
+      !need(x[5], &g->A, F32, dev) || !need(x[6], &g->dtb, F32, dev) ||
+      !get(x[7], &g->st, dev) || !need(out, &g->out, dt, dev) || !maybe(err, &g->err, I32, dev))
     return 0;
   if (g->v.nd != 3 || g->st.nd != 4 || (g->st.dt != F32 && g->st.dt != BF16)) return 0;
   g->hk = g->k.n[1], g->dk = g->k.n[2], g->hv = g->v.n[1], g->dv = g->v.n[2];
@@ -156,24 +168,25 @@ static int gdn(PyObject* const* x, PyObject* out, PyObject* err, int64_t rows, G
   g->pool.s_head = g->hv > 1 || s[1] > one ? s[1] : one;
   g->pool.num_slots = (int32_t)n[0];
   g->pool.dtype = g->st.dt;
-  return stream_of(x[0], &g->stream);
+  return stream_of(g->dev, &g->stream);
 }
 
 /* q k v a b A_log dt_bias states state_idx cu_seqlens has_init scale out l2norm dev_err rows */
 static PyObject* f_fwd(PyObject* self, PyObject* const* x, Py_ssize_t n) {
   Gdn g;
+  g.dev = -1;
   Ten idx, cu, hi;
   if (n != 16) return not_plain();
   const double scale = PyFloat_AsDouble(x[11]);
   const long l2 = PyObject_IsTrue(x[13]);
-  if (PyErr_Occurred() || !need(x[8], &idx, I32) || !need(x[9], &cu, I32) ||
-      !maybe(x[10], &hi, U8) || !flat(&idx) || !flat(&cu) || cu.n[0] != idx.n[0] + 1 ||
+  if (PyErr_Occurred() || !need(x[8], &idx, I32, &g.dev) || !need(x[9], &cu, I32, &g.dev) ||
+      !maybe(x[10], &hi, U8, &g.dev) || !flat(&idx) || !flat(&cu) || cu.n[0] != idx.n[0] + 1 ||
       (hi.nd >= 0 && (!flat(&hi) || hi.n[0] < idx.n[0])))
     return not_plain();
   Ten q;
   int64_t rows;
   if (x[15] == Py_None) {
-    if (!get(x[0], &q) || q.nd != 3) return not_plain();
+    if (!get(x[0], &q, &g.dev) || q.nd != 3) return not_plain();
     rows = q.n[0];
   } else {
     rows = PyLong_AsLongLong(x[15]);
@@ -190,13 +203,14 @@ static PyObject* f_fwd(PyObject* self, PyObject* const* x, Py_ssize_t n) {
 /* q k v a b A_log dt_bias states state_idx n_spec num_accepted has_init scale out l2norm dev_err */
 static PyObject* f_upd(PyObject* self, PyObject* const* x, Py_ssize_t n) {
   Gdn g;
+  g.dev = -1;
   Ten idx, acc, hi;
   if (n != 16) return not_plain();
   const long ns = PyLong_AsLong(x[9]);
   const double scale = PyFloat_AsDouble(x[12]);
   const long l2 = PyObject_IsTrue(x[14]);
-  if (PyErr_Occurred() || !need(x[8], &idx, I32) || !maybe(x[10], &acc, I32) ||
-      !maybe(x[11], &hi, U8) || idx.nd < 1 || idx.nd > 2 || ns < 0)
+  if (PyErr_Occurred() || !need(x[8], &idx, I32, &g.dev) || !maybe(x[10], &acc, I32, &g.dev) ||
+      !maybe(x[11], &hi, U8, &g.dev) || idx.nd < 1 || idx.nd > 2 || ns < 0)
     return not_plain();
   const int64_t B = idx.n[0], w = idx.nd == 2 ? idx.n[1] : 1;
   if (w != 1 + ns || (idx.nd == 2 && w > 1 && idx.s[1] != 1) || (B > 1 && idx.s[0] != w) ||
@@ -209,9 +223,10 @@ static PyObject* f_upd(PyObject* self, PyObject* const* x, Py_ssize_t n) {
       (int32_t)g.dv, (float)scale, (int32_t)l2, g.k.dt, g.out.p, g.os, g.err.p, g.stream));
 }
 
-static int cache(PyObject* ko, PyObject* vo, int dt, kv_cache_t* c) {
+static int cache(PyObject* ko, PyObject* vo, int dt, kv_cache_t* c, int* dev) {
   Ten k, v;
-  if (!need(ko, &k, dt) || !need(vo, &v, dt) || k.nd != 4 || v.nd != 4 || k.s[3] != 1) return 0;
+  if (!need(ko, &k, dt, dev) || !need(vo, &v, dt, dev) || k.nd != 4 || v.nd != 4 || k.s[3] != 1)
+    return 0;
   for (int i = 0; i < 4; ++i)
     if (k.n[i] != v.n[i] || k.s[i] != v.s[i]) return 0;
   int64_t s[3];
@@ -228,23 +243,26 @@ static int cache(PyObject* ko, PyObject* vo, int dt, kv_cache_t* c) {
 static PyObject* f_norm(PyObject* self, PyObject* const* x, Py_ssize_t n) {
   Ten q, k, v, qw, kw, cs, pos, sl, out, err;
   kv_cache_t c;
+  int dev = -1;
   int64_t qs, ks, vs, os;
   cconv_stream_t st;
-  if (n != 14 || !get(x[0], &q) || q.nd != 3 || (q.dt != F32 && q.dt != BF16)) return not_plain();
+  if (n != 14 || !get(x[0], &q, &dev) || q.nd != 3 || (q.dt != F32 && q.dt != BF16))
+    return not_plain();
   const int dt = q.dt;
   const int64_t T = q.n[0], hq = q.n[1], D = q.n[2];
   const double eps = PyFloat_AsDouble(x[5]);
   const long il = PyObject_IsTrue(x[8]);
-  if (PyErr_Occurred() || !cache(x[9], x[10], dt, &c) || c.head_dim != D ||
-      !need(x[1], &k, dt) || !need(x[2], &v, dt) || !maybe(x[3], &qw, dt) ||
-      !maybe(x[4], &kw, dt) || !need(x[6], &cs, F32) || !need(x[7], &pos, I32) ||
-      !need(x[11], &sl, I32) || !need(x[12], &out, dt) || !maybe(x[13], &err, I32))
+  if (PyErr_Occurred() || !cache(x[9], x[10], dt, &c, &dev) || c.head_dim != D ||
+      !need(x[1], &k, dt, &dev) || !need(x[2], &v, dt, &dev) || !maybe(x[3], &qw, dt, &dev) ||
+      !maybe(x[4], &kw, dt, &dev) || !need(x[6], &cs, F32, &dev) || !need(x[7], &pos, I32, &dev) ||
+      !need(x[11], &sl, I32, &dev) || !need(x[12], &out, dt, &dev) ||
+      !maybe(x[13], &err, I32, &dev))
     return not_plain();
   if (!heads(&q, T, hq, D, &qs) || !heads(&k, T, c.num_kv_heads, D, &ks) ||
       !heads(&v, T, c.num_kv_heads, D, &vs) || !heads(&out, T, hq, D, &os) ||
       (qw.nd >= 0 && !vec(&qw, D)) || (kw.nd >= 0 && !vec(&kw, D)) || !flat(&pos) || !flat(&sl) ||
       pos.n[0] < T || sl.n[0] < T || cs.nd != 2 || (cs.n[1] > 1 && cs.s[1] != 1) ||
-      (cs.n[0] > 1 && cs.s[0] != cs.n[1]) || !stream_of(x[0], &st))
+      (cs.n[0] > 1 && cs.s[0] != cs.n[1]) || !stream_of(dev, &st))
     return not_plain();
   return PyLong_FromLong(p_norm(q.p, qs, k.p, ks, v.p, vs, qw.p, kw.p, (float)eps, cs.p,
                                 (int32_t)cs.n[0], (int32_t)cs.n[1], (int32_t)il, pos.p, c, sl.p,
@@ -255,14 +273,17 @@ static PyObject* f_norm(PyObject* self, PyObject* const* x, Py_ssize_t n) {
 static PyObject* f_attn(PyObject* self, PyObject* const* x, Py_ssize_t n) {
   Ten q, tab, len, out, lse, ws, err;
   kv_cache_t c;
+  int dev = -1;
   int64_t qs, os;
   cconv_stream_t st;
-  if (n != 11 || !get(x[0], &q) || q.nd != 3 || (q.dt != F32 && q.dt != BF16)) return not_plain();
+  if (n != 11 || !get(x[0], &q, &dev) || q.nd != 3 || (q.dt != F32 && q.dt != BF16))
+    return not_plain();
   const long ns = PyLong_AsLong(x[5]);
   const double scale = PyFloat_AsDouble(x[6]);
-  if (PyErr_Occurred() || ns < 0 || !cache(x[1], x[2], q.dt, &c) || !need(x[3], &tab, I32) ||
-      !need(x[4], &len, I32) || !need(x[7], &out, q.dt) || !maybe(x[8], &lse, F32) ||
-      !maybe(x[9], &ws, U8) || !maybe(x[10], &err, I32) || !flat(&len) ||
+  if (PyErr_Occurred() || ns < 0 || !cache(x[1], x[2], q.dt, &c, &dev) ||
+      !need(x[3], &tab, I32, &dev) || !need(x[4], &len, I32, &dev) ||
+      !need(x[7], &out, q.dt, &dev) || !maybe(x[8], &lse, F32, &dev) ||
+      !maybe(x[9], &ws, U8, &dev) || !maybe(x[10], &err, I32, &dev) || !flat(&len) ||
       (ws.nd >= 0 && !flat(&ws)))
     return not_plain();
   const int64_t B = len.n[0], rows = B * (1 + ns);
@@ -271,7 +292,7 @@ static PyObject* f_attn(PyObject* self, PyObject* const* x, Py_ssize_t n) {
       (tab.n[1] > 1 && tab.s[1] != 1) ||
       (lse.nd >= 0 && (lse.nd != 2 || lse.n[0] < rows || lse.n[1] != q.n[1] ||
                        (lse.n[1] > 1 && lse.s[1] != 1) || (lse.n[0] > 1 && lse.s[0] != q.n[1]))) ||
-      !stream_of(x[0], &st))
+      !stream_of(dev, &st))
     return not_plain();
   const int64_t ts = tab.n[0] > 1 || tab.s[0] > tab.n[1] ? tab.s[0] : tab.n[1];
   PyObject* own = NULL; /* the call's workspace, if it brought none */
@@ -281,7 +302,7 @@ static PyObject* f_attn(PyObject* self, PyObject* const* x, Py_ssize_t n) {
     if (need < 0) return not_plain();
     own = PyObject_CallFunction(new_bytes, "OL", x[0], (long long)(need > 16 ? need : 16));
     if (!own) return NULL;
-    if (!get(own, &ws) || ws.nd != 1) {
+    if (!get(own, &ws, &dev) || ws.nd != 1) {
       Py_DECREF(own);
       return not_plain();
     }
@@ -294,10 +315,11 @@ static PyObject* f_attn(PyObject* self, PyObject* const* x, Py_ssize_t n) {
 }
 
 /* init(handle of libcconv.so, (float32, bfloat16, int32, uint8, bool), raw stream function,
- *      function (tensor, n) -> n bytes on its device and the current stream) */
+ *      function (tensor, n) -> n bytes on its device and the current stream, current device
+ *      function) */
 static PyObject* f_init(PyObject* self, PyObject* const* x, Py_ssize_t n) {
-  if (n != 4 || !PyTuple_Check(x[1]) || PyTuple_GET_SIZE(x[1]) != NDT) {
-    PyErr_SetString(PyExc_TypeError, "init(handle, dtypes, raw_stream, new_bytes)");
+  if (n != 5 || !PyTuple_Check(x[1]) || PyTuple_GET_SIZE(x[1]) != NDT) {
+    PyErr_SetString(PyExc_TypeError, "init(handle, dtypes, raw_stream, new_bytes, cur_device)");
     return NULL;
   }
   void* h = PyLong_AsVoidPtr(x[0]);
@@ -314,6 +336,7 @@ static PyObject* f_init(PyObject* self, PyObject* const* x, Py_ssize_t n) {
   for (int i = 0; i < NDT; ++i) Py_XSETREF(dtypes[i], Py_NewRef(PyTuple_GET_ITEM(x[1], i)));
   Py_XSETREF(raw_stream, Py_NewRef(x[2]));
   Py_XSETREF(new_bytes, Py_NewRef(x[3]));
+  Py_XSETREF(cur_device, Py_NewRef(x[4]));
   Py_RETURN_NONE;
 }
 
@@ -329,7 +352,6 @@ static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", NULL, -1, me
 
 PyMODINIT_FUNC PyInit__fast(void) {
   s_dtype = PyUnicode_InternFromString("dtype");
-  s_is_cuda = PyUnicode_InternFromString("is_cuda");
   s_shape = PyUnicode_InternFromString("shape");
   s_stride = PyUnicode_InternFromString("stride");
   s_data_ptr = PyUnicode_InternFromString("data_ptr");

@@ -133,11 +133,11 @@ def _load_fast(lib):
     missing (the functions below then marshal by themselves)."""
     try:
         from . import _fast as mod
-        raw = torch._C._cuda_getCurrentRawStream
+        raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     except (ImportError, AttributeError):
         return None
     mod.init(lib._handle, (torch.float32, torch.bfloat16, torch.int32, torch.uint8, torch.bool),
-             raw, lambda beside, n: beside.new_empty(n, dtype=torch.uint8))
+             raw, lambda beside, n: beside.new_empty(n, dtype=torch.uint8), device)
     return mod
 
 
@@ -392,20 +392,29 @@ _CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 
 
 def _raw(*tensors):
-    """Device addresses (None for None)."""
-    got = []
+    """Device addresses (None for None) of tensors that all live on the current device, whose stream
+    and SMs the library takes."""
+    got, on = [], None
     for t in tensors:
         if t is None:
             got.append(None)
-        elif t.is_cuda:
-            got.append(t.data_ptr())
-        else:
+            continue
+        if not t.is_cuda:
             raise ValueError("tensors passed to libcconv must live on the GPU")
+        if on is None:
+            on = torch.cuda.current_device()
+        if t.get_device() != on:
+            raise ValueError(f"tensors passed to libcconv must live on the current device ({on})")
+        got.append(t.data_ptr())
     return got
 
 
 def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    if stream.device.index != torch.cuda.current_device():
+        raise ValueError("the stream must be one of the current device")
+    return stream.cuda_stream
 
 
 def _heads(t, name, dtype, rows, heads=None, dim=None):

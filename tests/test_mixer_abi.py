@@ -264,3 +264,74 @@ def test_binding_takes_what_it_does_not_read():
                      (ops.attn_decode, dict(attn, workspace=torch.zeros(9, dtype=torch.uint8)))):
         with pytest.raises(ValueError, match="must live on the GPU"):
             fn(**call)
+
+
+class _Placed:
+    """A host tensor that says it lives on a GPU: its address goes to the library, which has none."""
+
+    def __init__(self, t, dev=0):
+        self.t, self.dev, self.is_cuda = t, dev, True
+
+    def get_device(self):
+        return self.dev
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def _placed_calls():
+    gdn, norm, attn, i = _two()
+    flags, err = torch.zeros(8, dtype=torch.uint8), i(1)
+    return [("gdn_fwd_varlen", dict(gdn, state_idx=i(2), cu_seqlens=i(3), has_init=flags, dev_err=err)),
+            ("gdn_update", dict(gdn, state_idx=i(2, 2), n_spec=1, num_accepted=i(2), has_init=flags, dev_err=err)),
+            ("attn_norm_rope_cache", dict(norm, q_weight=torch.zeros(64), k_weight=torch.zeros(64), dev_err=err)),
+            ("attn_decode", dict(attn, lse=torch.zeros(4, 4), workspace=torch.zeros(1 << 26, dtype=torch.uint8),
+                                 dev_err=err))]
+
+
+@no_gpu
+@pytest.mark.parametrize("in_c", [True, False])
+def test_tensors_of_a_call_share_the_current_device(in_c, monkeypatch):
+    """A call whose tensors lie on another device than the current one, whose stream and SMs it would take,
+    or on two, is refused; C leaves it to Python, which raises. (Without a GPU a call that is not refused
+    ends with the launch's status.)"""
+    lib = ops.load()
+    if in_c and ops._fast is None:
+        pytest.skip("the C module is not built")
+    current = [0]
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(ops, "_raw_stream", lambda stream: None)
+    seen = []
+    if in_c:
+        ops._fast.init(lib._handle, (torch.float32, torch.bfloat16, torch.int32, torch.uint8, torch.bool),
+                       lambda d: seen.append(d) or 0, None, lambda: current[0])
+    else:
+        monkeypatch.setattr(ops, "_fast", None)
+    try:
+        for fn, call in _placed_calls():
+            tensors = [n for n, t in call.items() if torch.is_tensor(t)]
+            here = {n: _Placed(t) if n in tensors else t for n, t in call.items()}
+            with pytest.raises(ops.CConvError, match=fn):
+                getattr(ops, fn)(**here)
+            assert not in_c or seen.pop() == 0
+            for n in tensors:
+                with pytest.raises(ValueError, match="current device"):
+                    getattr(ops, fn)(**{**here, n: _Placed(call[n], 1)})
+            current[0] = 1
+            with pytest.raises(ValueError, match="current device"):
+                getattr(ops, fn)(**here)
+            current[0] = 0
+            assert not seen
+    finally:
+        ops._load_fast(lib)
+
+
+@no_gpu
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 0
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="current device"):
+        ops._raw_stream(Stream())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    assert ops._raw_stream(Stream()) == 0
