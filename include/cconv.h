@@ -619,7 +619,9 @@ CCONV_API int attn_norm_rope_cache(const void* q, int64_t q_row_stride, const vo
  *                overlap need one each
  * A page number outside the cache sets CCONV_DERR_PAGE, and the positions of
  * that page are left out; a seq_lens entry that is negative or longer than the
- * block table sets CCONV_DERR_SEQ_LEN, and the request is skipped.
+ * block table sets CCONV_DERR_SEQ_LEN, and the request is skipped. The bf16
+ * kernel's waits have a time limit: CCONV_DERR_TIMEOUT (out and lse are then
+ * incomplete).
  */
 CCONV_API int attn_decode(const void* q, int64_t q_row_stride, kv_cache_t cache,
                 const int32_t* block_table, int64_t block_table_row_stride, int32_t table_width,

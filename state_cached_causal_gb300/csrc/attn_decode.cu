@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(512) attn_join_kernel(const AttnArgs a) {
   const int64_t bu = blockIdx.x;                    // request and unit
   const int row = blockIdx.y / used * a.rows + blockIdx.y % used;
   const int c0 = a.meta[bu * 2], c1 = a.meta[bu * 2 + 1];
-  if (c0 < 0) return;
+  if (!attn_joins(c0, c1, a.grid)) return;
   const int b = (int)(bu / a.units), u = (int)(bu % a.units);
   const int hkv = u / a.rblocks * a.hw + row / a.rows;
   const int rr = u % a.rblocks * a.rows + row % a.rows;
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(256) attn_join_rows_kernel(const AttnArgs a, c
   const int64_t bu = at / y;                        // request and unit
   const int row = (int)(at % y) / used * a.rows + (int)(at % y) % used;
   const int c0 = a.meta[bu * 2], c1 = a.meta[bu * 2 + 1];
-  if (c0 < 0) return;
+  if (!attn_joins(c0, c1, a.grid)) return;
   const int b = (int)(bu / a.units), u = (int)(bu % a.units);
   const int hkv = u / a.rblocks * a.hw + row / a.rows;
   const int rr = u % a.rblocks * a.rows + row % a.rows;
@@ -503,6 +503,7 @@ extern "C" int attn_decode(const void* q, int64_t q_row_stride, kv_cache_t cache
   a.rblocks = p.rblocks;
   a.rows = p.rows;
   a.units = p.units;
+  a.grid = p.grid;
   a.dev_err = dev_err;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t err;

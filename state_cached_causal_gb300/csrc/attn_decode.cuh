@@ -40,6 +40,7 @@ struct AttnArgs {
   int32_t rblocks;   // row blocks of a head (rows of G * q_len taken separately)
   int32_t rows;      // rows of a block
   int32_t units;     // of a request: Hkv / hw * rblocks
+  int32_t grid;      // blocks of the split kernel
   int32_t* dev_err;
 };
 
@@ -164,6 +165,12 @@ __device__ __forceinline__ void attn_note(const AttnArgs& a, const AttnSeg& s, c
   const bool cut = !s.whole && s.len >= 0;
   m[0] = cut ? attn_block_of(s.line, r) : -1;
   m[1] = cut ? attn_block_of(s.line + s.tiles - 1, r) : -1;
+}
+
+// Whether blocks c0 to c1 hold the parts of a cut unit: not if it was whole or
+// skipped (-1), nor if no note of it was written, since a block was given up.
+__host__ __device__ inline bool attn_joins(int32_t c0, int32_t c1, int32_t grid) {
+  return c0 >= 0 && c0 <= c1 && c1 < grid;
 }
 
 // bf16 kernel (attn_mma.cu)

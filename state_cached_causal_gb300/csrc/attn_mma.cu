@@ -25,7 +25,7 @@
 // of one head join their parts once per segment, through shared memory.
 //
 // Measured, heads of 128, 4 kv heads, 16 query heads: 256 requests of 1 to 8192
-// positions (2.1 GB) 339 us, 6.3 TB/s; one of 131072 (270 MB) 57 us with its join;
+// positions (2.1 GB) 340 us, 6.2 TB/s; one of 131072 (270 MB) 57 us with its join;
 // 64 requests of up to 4096 with 4 tokens each (0.25 GB) 57 us. With
 // 2 kv heads, 256 requests (1.06 GB): 179 us, 5.9 TB/s; with a copy a position,
 // and a ring that left the grid's second block of an SM no room, 354 us.
@@ -98,11 +98,9 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t v) {
          ((v & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
 }
 
-// The warps that compute, among themselves.
-__device__ __forceinline__ void warps_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-}
-// Bounded wait of a whole warp.
+// Bounded wait of a whole warp. A warp that it gives up leaves the kernel; what
+// waits for that warp is given up in turn, so no barrier behind the first of these
+// waits may be one without a limit.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, int phase, int32_t* err) {
   long long t0 = 0;
 #pragma unroll 1
@@ -116,7 +114,18 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, int phase, int32_t* err)
       }
     }
   }
+  __syncwarp();
   return true;
+}
+
+// What a warp that gives a wait up leaves the kernel by, so that no copy lands
+// behind the block's end: the last tiles of all places, those from `st` on in the
+// phase of parity ph, those before it in the next one. (A place that no such tile
+// came to: at once for the loading warp, whose phases are the last ones begun; for
+// the others when its time is up. Waiting here at the loading warp's usual end, too,
+// took 5 us of 340; it ends with copies on their way, which the others wait for.)
+__device__ __noinline__ void settle(uint64_t* full, int stages, int st, int ph, int32_t* err) {
+  for (int i = 0; i < stages; ++i) wait_bar(&full[i], i < st ? ph ^ 1 : ph, err);
 }
 
 // MT row tiles of 16. Q stays in registers where it fits beside the sums, else
@@ -127,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
   constexpr int kQPitch = D * 2 + 16;
   extern __shared__ __align__(128) unsigned char attn_dyn[];
   __shared__ int64_t scan[kThreads + 4];
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], met;
   __shared__ __align__(16) unsigned char there[kMaxStages][kTile];   // positions that hold a token
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // position x of a tile lies at off(x) of its place: rows of a group side by side
@@ -144,6 +153,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], kWarps);
     }
+    mbar_init(&met, kWarps);
     fence_mbar_init();
   }
   AttnRun run;
@@ -191,7 +201,8 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
             flag_error(a.dev_err, CCONV_DERR_PAGE);
             held = 0;
           }
-          if (p == 0 && !wait_bar(&empty[st], ph, a.dev_err)) return;
+          if (p == 0 && !wait_bar(&empty[st], ph, a.dev_err))
+            return settle(full, stages, st, ph, a.dev_err);
           if (in) {
             if (notes)
               for (int k = 0; k < group; ++k) there[st][pl + k] = k < held;
@@ -215,7 +226,13 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
     }
     return;
   }
-  int stage = 0, phase = 0;
+  int stage = 0, phase = 0, meets = 0;
+  // The warps that compute, among themselves.
+  auto meet = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&met);
+    return wait_bar(&met, meets++ & 1, a.dev_err);
+  };
 
   while (run.p < run.end) {
     const AttnSeg sg = attn_segment(a, tpos, run);
@@ -268,7 +285,8 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
       for (int n = 0; n < D / 8; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.0f;
     }
     for (int j = sg.j0; j < sg.j1; ++j) {
-      if (!wait_bar(&full[stage], phase, a.dev_err)) return;
+      if (!wait_bar(&full[stage], phase, a.dev_err))
+        return settle(full, stages, stage, phase, a.dev_err);
       const uint32_t kb = smem_addr(attn_dyn) + stage * 2 * half_stage + off(p0) + hl * (D * 2);
       const uint32_t vb = kb + half_stage;
       const unsigned char* tr = there[stage] + p0;
@@ -424,7 +442,8 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
         l[mt][half] += __shfl_xor_sync(0xffffffffu, l[mt][half], 2);
       }
     const int per = kWarps >> hw_shift;              // warps of a head
-    if (!kQRegs && per > 1) warps_sync();         // every warp is done with its Q
+    // (with Q in shared memory: every warp is done with its own)
+    if (!kQRegs && per > 1 && !meet()) return settle(full, stages, stage, phase, a.dev_err);
 #pragma unroll 1
     for (int w = 1; w < per; ++w) {
       float* const so = join + (warp / per) * (MT * 16 * (D + 4));
@@ -444,7 +463,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
             }
           }
       }
-      warps_sync();
+      if (!meet()) return settle(full, stages, stage, phase, a.dev_err);
       if (warp % per == 0) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -464,7 +483,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
             }
           }
       }
-      warps_sync();
+      if (!meet()) return settle(full, stages, stage, phase, a.dev_err);
     }
     if (sg.len < 0 || warp % per != 0) continue;
     float* const part = attn_part(a, sg, D) + (warp / per) * (MT * 16) * (D + 2);
