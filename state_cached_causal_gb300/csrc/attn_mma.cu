@@ -34,8 +34,8 @@
 // zeros; their scores are masked, as are those that a draft token's row does not
 // see. A tile that every row sees whole skips the masks, and sums are rescaled
 // only when a maximum has risen.
-#include "async.cuh"
 #include "attn_decode.cuh"
+#include "tc.cuh"
 
 #include <math.h>
 
@@ -48,31 +48,6 @@ constexpr int kTile = 64;           // rows of a tile (positions x heads); 16 a 
 
 constexpr int kMaxStages = 4;
 constexpr long long kWaitClocks = 4000000000LL;   // seconds; a copy takes microseconds
-
-__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                    uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
@@ -299,18 +274,18 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         uint32_t b[4];                 // positions 0-7: k 0-7, k 8-15; positions 8-15: the same
-        ldm4(b, ka + ks * 32);
+        tc::ldmatrix4(b, ka + ks * 32);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           if constexpr (kQRegs) {
-            mma(s[mt][0], q[mt][ks], b[0], b[1]);
-            mma(s[mt][1], q[mt][ks], b[2], b[3]);
+            tc::mma16(s[mt][0], q[mt][ks], b[0], b[1]);
+            tc::mma16(s[mt][1], q[mt][ks], b[2], b[3]);
           } else {
             uint32_t qa[4];
-            ldm4(qa, smem_addr(sq) + (mt * 16 + (lane & 15)) * kQPitch + ks * 32 +
+            tc::ldmatrix4(qa, smem_addr(sq) + (mt * 16 + (lane & 15)) * kQPitch + ks * 32 +
                          (lane >> 4) * 16);
-            mma(s[mt][0], qa, b[0], b[1]);
-            mma(s[mt][1], qa, b[2], b[3]);
+            tc::mma16(s[mt][0], qa, b[0], b[1]);
+            tc::mma16(s[mt][1], qa, b[2], b[3]);
           }
         }
       }
@@ -362,10 +337,10 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           const float mn = fmaxf(m[mt][half], mx);
           const float base = mn == -INFINITY ? 0.0f : mn;
-          corr[half] = ex2(m[mt][half] - base);
+          corr[half] = tc::ex2(m[mt][half] - base);
           m[mt][half] = mn;
-          const float x0 = ex2(s0 - base), x1 = ex2(s1 - base), x2 = ex2(s2 - base),
-                      x3 = ex2(s3 - base);
+          const float x0 = tc::ex2(s0 - base), x1 = tc::ex2(s1 - base), x2 = tc::ex2(s2 - base),
+                      x3 = tc::ex2(s3 - base);
           l[mt][half] = fmaf(l[mt][half], corr[half], (x0 + x1) + (x2 + x3));
           split_weights(x0, x1, pw[half], pl[half]);
           split_weights(x2, x3, pw[2 + half], pl[2 + half]);
@@ -385,33 +360,33 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
 #pragma unroll
           for (int n = 0; n < D / 16; n += 2) {
             uint32_t b[4], c[4];       // dims 0-7: positions 0-7, 8-15; dims 8-15: the same
-            ldm4t(b, va + n * 32);
-            ldm4t(c, va + n * 32 + 32);
-            mma(o[mt][2 * n], pw, b[0], b[1]);
-            mma(o[mt][2 * n + 1], pw, b[2], b[3]);
-            mma(o[mt][2 * n + 2], pw, c[0], c[1]);
-            mma(o[mt][2 * n + 3], pw, c[2], c[3]);
-            mma(o[mt][2 * n], pl, b[0], b[1]);
-            mma(o[mt][2 * n + 1], pl, b[2], b[3]);
-            mma(o[mt][2 * n + 2], pl, c[0], c[1]);
-            mma(o[mt][2 * n + 3], pl, c[2], c[3]);
+            tc::ldmatrix4_trans(b, va + n * 32);
+            tc::ldmatrix4_trans(c, va + n * 32 + 32);
+            tc::mma16(o[mt][2 * n], pw, b[0], b[1]);
+            tc::mma16(o[mt][2 * n + 1], pw, b[2], b[3]);
+            tc::mma16(o[mt][2 * n + 2], pw, c[0], c[1]);
+            tc::mma16(o[mt][2 * n + 3], pw, c[2], c[3]);
+            tc::mma16(o[mt][2 * n], pl, b[0], b[1]);
+            tc::mma16(o[mt][2 * n + 1], pl, b[2], b[3]);
+            tc::mma16(o[mt][2 * n + 2], pl, c[0], c[1]);
+            tc::mma16(o[mt][2 * n + 3], pl, c[2], c[3]);
           }
         } else {
           const int q0 = (lane & 3) * 2;
 #pragma unroll
           for (int n = 0; n < D / 16; ++n) {
             uint32_t b[4];
-            ldm4t(b, va + n * 32);
+            tc::ldmatrix4_trans(b, va + n * 32);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {          // positions q0 + 8 (i & 1) + {0, 1}
               const int x = q0 + (i & 1) * 8;
               const uint32_t hidden = (x >= x0 ? 0xffffu : 0u) | (x + 1 >= x0 ? 0xffff0000u : 0u);
               b[i] &= ~(not_finite(b[i]) & hidden);
             }
-            mma(o[mt][2 * n], pw, b[0], b[1]);
-            mma(o[mt][2 * n + 1], pw, b[2], b[3]);
-            mma(o[mt][2 * n], pl, b[0], b[1]);
-            mma(o[mt][2 * n + 1], pl, b[2], b[3]);
+            tc::mma16(o[mt][2 * n], pw, b[0], b[1]);
+            tc::mma16(o[mt][2 * n + 1], pw, b[2], b[3]);
+            tc::mma16(o[mt][2 * n], pl, b[0], b[1]);
+            tc::mma16(o[mt][2 * n + 1], pl, b[2], b[3]);
           }
 #pragma unroll 1
           for (int x = x0; x < x1; ++x)
@@ -472,7 +447,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
             const float* row = so + (mt * 16 + half * 8 + (lane >> 2)) * (D + 4);
             const float mo = row[D], lo = row[D + 1];
             const float mm = fmaxf(m[mt][half], mo), base = mm == -INFINITY ? 0.0f : mm;
-            const float f = ex2(m[mt][half] - base), fo = ex2(mo - base);
+            const float f = tc::ex2(m[mt][half] - base), fo = tc::ex2(mo - base);
             m[mt][half] = mm;
             l[mt][half] = fmaf(l[mt][half], f, lo * fo);
 #pragma unroll

@@ -31,11 +31,6 @@ struct GdnArgs {
 // Bounds of sequence s, or false (with the error flagged by the caller's
 // choice) for a bad cu_seqlens entry.
 __device__ __forceinline__ bool gdn_bounds(const GdnArgs& a, int s, int& st, int& len) {
-  if (!a.cu) {
-    st = s * a.q_len;
-    len = a.q_len;
-    return true;
-  }
   st = a.cu[s];
   const int en = a.cu[s + 1];
   len = en - st;

@@ -1,6 +1,7 @@
-// tcgen05 and tensor-memory wrappers for the chunked gated delta rule (sm_103a):
-// bf16 operands, fp32 accumulators in tensor memory, A from tensor or shared
-// memory, B from shared memory in the 128-byte swizzle.
+// Tensor-core wrappers of the mixers (sm_103a). tcgen05, for the chunked gated delta
+// rule: bf16 operands, fp32 accumulators in tensor memory, A from tensor or shared
+// memory, B from shared memory in the 128-byte swizzle. Warp-level products, for its
+// 16 x 16 blocks and for attention.
 #pragma once
 
 #include <cuda.h>
@@ -71,28 +72,13 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn = false, bo
                     "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
 #define TC_I8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), \
                     "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
-// 32 columns of the warp's 32 lanes.
-__device__ __forceinline__ void ld32(uint32_t addr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-      "%28, %29, %30, %31}, [%32];"
-      : TC_R8(r, 0), TC_R8(r, 8), TC_R8(r, 16), TC_R8(r, 24)
-      : "r"(addr)
-      : "memory");
-}
+// 16 columns of the warp's 32 lanes.
 __device__ __forceinline__ void ld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
       "%11, %12, %13, %14, %15}, [%16];"
       : TC_R8(r, 0), TC_R8(r, 8)
       : "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
-      "%10, %11, %12, %13, %14, %15};" ::TC_I8(r, 0), TC_I8(r, 8), "r"(addr)
       : "memory");
 }
 __device__ __forceinline__ void st8(uint32_t addr, const uint32_t (&r)[8]) {
@@ -154,8 +140,8 @@ __device__ __forceinline__ bool elect() {
   return r != 0;
 }
 
-// Warp-level products of 16 x 16 blocks (tcgen05 has no tile this small):
-// m16n8k16, bf16 in, fp32 out, and the four 8 x 8 matrices of one A operand.
+// Warp-level products of few rows (tcgen05 has no tile this small): m16n8k16, bf16
+// in, fp32 out, and the four 8 x 8 matrices of one operand.
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                       uint32_t b1) {
   asm(
