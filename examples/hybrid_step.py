@@ -13,6 +13,9 @@ and a decode step through
     cconv_update -> gdn_update
     cca_qk_conv_fused -> attn_norm_rope_cache -> attn_decode
 
+The attention of a prompt's tokens over each other is not part of the library: a prompt fills the cache
+here, and the tokens after it attend.
+
 Weights and inputs are random (seeded). Run it on a GPU: python examples/hybrid_step.py
 """
 import os

@@ -1,12 +1,15 @@
 // attn_decode in bf16: the same split as attn_decode.cuh, with the products on
 // the warp-level tensor instruction (m16n8k16).
 //
-// What bounds it is the cache's bytes: K and V are read once, for all query
-// rows of a kv head together, and a row pair of 16 x 128 products per 256 bytes
+// What bounds it is the cache's bytes: K and V are read once for up to 32 query
+// rows of a kv head (16 for heads of 256) together, and a row pair of 16 x 128 products per 256 bytes
 // is far below any arithmetic limit. tcgen05 would need 64 rows or a transposed
 // product to be fed; with 4 to 32 rows the warp-level form fits the rows as they
 // are, keeps the softmax in the registers of the warp that made the scores, and
-// the tensor pipe is mostly idle either way.
+// the tensor pipe is mostly idle either way. More rows are taken in blocks, and
+// each of them reads K and V again (64 rows of a kv head: twice, 281 us for 128
+// requests of up to 8192 positions and one kv head where 32 rows take 158; heads of
+// 256 with 32 rows, twice: 302 us for 60 requests and 2 kv heads).
 //
 // A block of 4 warps keeps a ring of tiles of K and V in shared memory, several
 // tiles ahead. A tile is 64 rows: 64 / hw positions of hw kv heads, since the
@@ -27,7 +30,7 @@
 // Measured, heads of 128, 4 kv heads, 16 query heads: 256 requests of 1 to 8192
 // positions (2.1 GB) 340 us, 6.2 TB/s; one of 131072 (270 MB) 57 us with its join;
 // 64 requests of up to 4096 with 4 tokens each (0.25 GB) 57 us. With
-// 2 kv heads, 256 requests (1.06 GB): 179 us, 5.9 TB/s; with a copy a position,
+// 2 kv heads, 256 requests (1.06 GB): 186 us, 5.7 TB/s; with a copy a position,
 // and a ring that left the grid's second block of an SM no room, 354 us.
 //
 // V of positions that lie behind the length or on a bad page is filled with
@@ -56,9 +59,10 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
 }
 // Two weights as two bf16 terms, each pair packed (x0 low): 16 bits of them, so
 // that the one rounding of a result is its last. With one term (331 us for the 256
-// requests) the results were 2.1e-3 of their norm off instead of 1.7e-3. The first term is cut, not rounded:
-// the second one then is not negative, and is kept above zero for a weight that is,
-// since otherwise the terms' products with an infinite value would make NaN.
+// requests) the results were 2.1e-3 of their norm off instead of 1.7e-3. The first
+// term is cut, not rounded: the second one then is not negative, and is kept above
+// zero for a weight that is, since otherwise the terms' products with an infinite
+// value would make NaN.
 __device__ __forceinline__ float rest(float x) {
   const float r = x - __uint_as_float(__float_as_uint(x) & 0xffff0000u);
   return fmaxf(r, fminf(x, 0x1p-126f));
