@@ -16,7 +16,9 @@
  *     _mix_with_state).
  * Behind the convolutions stand the mixers of such layers: the gated delta
  * rule over a state pool (gdn_fwd_varlen, gdn_update), and attention over a
- * paged cache (attn_norm_rope_cache, attn_decode).
+ * paged cache (attn_norm_rope_cache, attn_decode), whose rows may be 8-bit
+ * floats (attn_norm_rope_cache_q8, kv_cache_read_q8, attn_decode_q8) and whose
+ * first positions requests may share (attn_decode_shared, .._shared_q8).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -635,6 +637,73 @@ CCONV_API int attn_decode(const void* q, int64_t q_row_stride, kv_cache_t cache,
 CCONV_API int64_t attn_decode_workspace_bytes(int32_t num_seqs, int32_t n_spec,
                                               int32_t num_q_heads, int32_t num_kv_heads,
                                               int32_t head_dim);
+
+/*
+ * Paged key-value cache in 8 bits: as kv_cache, with values of e4m3 (one byte:
+ * sign, 4 bits of exponent, 3 of fraction; no infinities, 0x7f and 0xff are NaN)
+ * and, for each row of head_dim values, the power of two that multiplies them:
+ * scale byte b stands for 2^(b - 127), 1 <= b <= 254. k_scale and v_scale are
+ * [page, token of the page, kv head] views of the same strides (in bytes, any).
+ */
+typedef struct kv_cache_q8 {
+  void* k;           /* 16-byte aligned */
+  void* v;
+  int64_t s_page, s_token, s_head;      /* multiples of 16 */
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  int64_t c_page, c_token, c_head;
+  int32_t num_pages, page_size, num_kv_heads, head_dim;
+} kv_cache_q8_t;
+
+/*
+ * attn_norm_rope_cache_q8 -- attn_norm_rope_cache into a cache in 8 bits.
+ *
+ * The rows of k (after norm and rotation, in fp32) and of v are rounded once,
+ * from fp32 to e4m3 (nearest even): with m the largest finite |x| of a row,
+ *   e = the least integer with m <= 448 * 2^e, at least -126;
+ *   value = e4m3(x * 2^-e),  scale byte = e + 127.
+ * A power of two costs no precision over m / 448 (e4m3 values have a step that
+ * goes with their size) and multiplies without a rounding when it is read.
+ * Infinities and NaN are stored as NaN, and do not enter m.
+ * Other arguments and errors as attn_norm_rope_cache; dtype is that of q, k, v,
+ * the weights and q_out.
+ */
+CCONV_API int attn_norm_rope_cache_q8(const void* q, int64_t q_row_stride, const void* k,
+                            int64_t k_row_stride, const void* v, int64_t v_row_stride,
+                            const void* q_weight, const void* k_weight, float eps,
+                            const float* cos_sin, int32_t max_position, int32_t rot_dim,
+                            int32_t interleaved, const int32_t* positions, kv_cache_q8_t cache,
+                            const int32_t* slot_mapping, int32_t num_tokens,
+                            int32_t num_q_heads, int32_t dtype, void* q_out,
+                            int64_t q_out_row_stride, int32_t* dev_err, cconv_stream_t stream);
+
+/*
+ * kv_cache_read_q8 -- rows of a cache in 8 bits as fp32 or bf16: k_out[t] and
+ * v_out[t] [num_kv_heads * head_dim] are the keys and values of cache row
+ * slot_mapping[t] = page * page_size + token of the page (fp32: exact; bf16: exact
+ * but for magnitudes under 2^-126). Rows may be named more than once. A negative
+ * slot leaves its rows of k_out and v_out as they are; one beyond the cache does
+ * too, and sets CCONV_DERR_POSITION. head_dim is 64, 128 or 256.
+ */
+CCONV_API int kv_cache_read_q8(kv_cache_q8_t cache, const int32_t* slot_mapping,
+                     int32_t num_tokens, int32_t dtype, void* k_out, int64_t k_out_row_stride,
+                     void* v_out, int64_t v_out_row_stride, int32_t* dev_err,
+                     cconv_stream_t stream);
+
+/*
+ * attn_decode_q8 -- attn_decode over a cache in 8 bits: the same definition with
+ * k and v the values that the cache's bytes and scales stand for. Arguments,
+ * workspace (attn_decode_workspace_bytes) and errors as attn_decode. The bf16
+ * kernel multiplies the bytes as they are, as fp16 (exact), q as fp16 with a power
+ * of two a row (exact but for values 2^-38 below the row's largest), and takes the
+ * softmax weights, times their row's power of two, as fp16 (11 bits).
+ */
+CCONV_API int attn_decode_q8(const void* q, int64_t q_row_stride, kv_cache_q8_t cache,
+                   const int32_t* block_table, int64_t block_table_row_stride,
+                   int32_t table_width, const int32_t* seq_lens, int32_t num_seqs,
+                   int32_t n_spec, int32_t num_q_heads, float scale, int32_t dtype, void* out,
+                   int64_t out_row_stride, float* lse, void* workspace, int64_t workspace_bytes,
+                   int32_t* dev_err, cconv_stream_t stream);
 
 /* Static English text for a status code. */
 CCONV_API const char* cconv_status_string(int status);

@@ -1,5 +1,5 @@
-// Entry point attn_decode: host side, the plain-arithmetic kernel and the join
-// of split results. The split is described in attn_decode.cuh.
+// Entry points attn_decode and attn_decode_q8: host side, the plain-arithmetic
+// kernel and the join of split results. The split is described in attn_decode.cuh.
 //
 // attn_kernel keeps one softmax pass over the tiles: K and V of 32 positions go
 // to shared memory, each warp scores two of up to kRows query rows (lane =
@@ -11,6 +11,7 @@
 // of up to 8192 positions, 2 kv heads of 64: 123 us with seven (2.1 TB/s), 274
 // with two.
 #include "attn_decode.cuh"
+#include "q8.cuh"
 
 #include <math.h>
 
@@ -32,7 +33,7 @@ struct AttnSmem {
   int64_t scan[kThreads + 4];
 };
 
-template <typename T, int D>
+template <typename T, int D, bool Q8>
 __global__ void __launch_bounds__(kThreads) attn_kernel(const AttnArgs a) {
   constexpr int V = Elem<T>::V, E = Elem<T>::bytes;
   constexpr int CD = (D + kThreads - 1) / kThreads;   // columns of a thread
@@ -82,7 +83,20 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const AttnArgs a) {
           }
         }
         float fk[V], fv[V];
-        if (page >= 0) {
+        if (Q8 && page >= 0) {
+          const int64_t off = page * a.s_page + (pos % a.page_size) * a.s_tok +
+                              (int64_t)hkv * a.s_head + u * V;
+          const int64_t to = page * a.c_page + (pos % a.page_size) * a.c_tok + hkv * a.c_head;
+          const float ks = q8_scale(a.ksc[to]), vs = q8_scale(a.vsc[to]);
+#pragma unroll
+          for (int e = 0; e < V; e += 4) {
+            float yk[4], yv[4];
+            unpack_e4m3x4(*reinterpret_cast<const uint32_t*>(a.kc + off + e), yk);
+            unpack_e4m3x4(*reinterpret_cast<const uint32_t*>(a.vc + off + e), yv);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) fk[e + k] = yk[k] * ks, fv[e + k] = yv[k] * vs;
+          }
+        } else if (page >= 0) {
           const int64_t off = ((int64_t)page * a.s_page + (pos % a.page_size) * a.s_tok +
                                (int64_t)hkv * a.s_head + u * V) * E;
           unpack16<T>(ldg16(a.kc + off), fk);
@@ -379,14 +393,20 @@ cudaError_t launch_join(const AttnArgs& a, cudaStream_t st) {
              : cudaLaunchKernelEx(&cfg, attn_join_rows_kernel<T, D>, a, n);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool Q8>
 cudaError_t launch_attn(const AttnArgs& a, int grid, cudaStream_t st) {
   const size_t smem = sizeof(AttnSmem<T, D>);
   static std::atomic<uint64_t> full;
-  const cudaError_t e = mix_full_smem(reinterpret_cast<const void*>(attn_kernel<T, D>), full);
+  const cudaError_t e = mix_full_smem(reinterpret_cast<const void*>(attn_kernel<T, D, Q8>), full);
   if (e != cudaSuccess) return e;
-  attn_kernel<T, D><<<grid, kThreads, smem, st>>>(a);
+  attn_kernel<T, D, Q8><<<grid, kThreads, smem, st>>>(a);
   return cudaGetLastError();
+}
+template <typename T, bool Q8>
+cudaError_t launch_attn_d(const AttnArgs& a, int D, int grid, cudaStream_t st) {
+  return D == 64    ? launch_attn<T, 64, Q8>(a, grid, st)
+         : D == 128 ? launch_attn<T, 128, Q8>(a, grid, st)
+                    : launch_attn<T, 256, Q8>(a, grid, st);
 }
 
 struct AttnPlan {
@@ -425,6 +445,90 @@ int check_sizes(int32_t num_seqs, int32_t n_spec, int32_t Hq, int32_t Hkv, int32
   return CCONV_OK;
 }
 
+// What both entry points check and do; a's cache is set.
+int decode(AttnArgs& a, int D, bool q8, const void* q, int64_t q_row_stride,
+           const int32_t* block_table, int64_t block_table_row_stride, int32_t table_width,
+           const int32_t* seq_lens, int32_t num_seqs, int32_t n_spec, int32_t num_q_heads,
+           float scale, int32_t dtype, void* out, int64_t out_row_stride, float* lse,
+           void* workspace, int64_t workspace_bytes, int32_t* dev_err, cconv_stream_t stream) {
+  const int rc = check_sizes(num_seqs, n_spec, num_q_heads, a.Hkv, D);
+  if (rc != CCONV_OK) return rc;
+  if (num_seqs == 0) return CCONV_OK;
+  const int V = 16 / mix_dtype_bytes(dtype);
+  if (!mix_rows_ok(q, q_row_stride, (int64_t)num_q_heads * D, V) ||
+      !mix_rows_ok(out, out_row_stride, (int64_t)num_q_heads * D, V) || !seq_lens ||
+      table_width < 0 || (table_width > 0 && !block_table) ||
+      block_table_row_stride < table_width ||
+      (int64_t)table_width * a.page_size > INT32_MAX - 1024)
+    return CCONV_ERR_INVALID;
+  const int sms = mix_sm_count();
+  if (sms <= 0) return CCONV_ERR_LAUNCH;
+  const bool plain = dtype == CCONV_DTYPE_F32 || q8;
+  const AttnPlan p = plan(plain ? CCONV_DTYPE_F32 : CCONV_DTYPE_BF16, sms, num_seqs, 1 + n_spec,
+                          num_q_heads / a.Hkv, a.Hkv, D);
+  if (!workspace || !mix_aligned16(workspace) || workspace_bytes < p.bytes)
+    return CCONV_ERR_INVALID;
+  a.q = static_cast<const char*>(q);
+  a.q_rs = q_row_stride;
+  a.page_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if (a.page_size == 1 << s) a.page_shift = s;
+  a.table = block_table;
+  a.table_rs = block_table_row_stride;
+  a.table_width = table_width;
+  a.seq_lens = seq_lens;
+  a.B = num_seqs;
+  a.q_len = 1 + n_spec;
+  a.Hq = num_q_heads;
+  a.G = num_q_heads / a.Hkv;
+  a.scale = scale;
+  a.out = static_cast<char*>(out);
+  a.out_rs = out_row_stride;
+  a.lse = lse;
+  a.meta = static_cast<int32_t*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.meta_bytes);
+  a.hw = p.hw;
+  // positions that follow one another in memory come together, up to 1 KB or four
+  a.group_shift = 0;
+  if (a.s_tok == (int64_t)p.hw * D && (p.hw == 1 || a.s_head == D))
+    while (a.group_shift < 2 && (p.hw * D * 2 << a.group_shift) < 1024 &&
+           a.page_size % (2 << a.group_shift) == 0)
+      ++a.group_shift;
+  a.rblocks = p.rblocks;
+  a.rows = p.rows;
+  a.units = p.units;
+  a.grid = p.grid;
+  a.dev_err = dev_err;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t err;
+  if (dtype == CCONV_DTYPE_F32)
+    err = q8 ? launch_attn_d<float, true>(a, D, p.grid, st)
+             : launch_attn_d<float, false>(a, D, p.grid, st);
+  else
+    err = q8 ? launch_attn_d<__nv_bfloat16, true>(a, D, p.grid, st)
+             : attn_launch_mma(a, D, p.grid, st);
+  if (err != cudaSuccess) return CCONV_ERR_LAUNCH;
+  if (dtype == CCONV_DTYPE_F32)
+    err = D == 64 ? launch_join<float, 64>(a, st) : D == 128 ? launch_join<float, 128>(a, st)
+                                                             : launch_join<float, 256>(a, st);
+  else
+    err = D == 64 ? launch_join<__nv_bfloat16, 64>(a, st)
+          : D == 128 ? launch_join<__nv_bfloat16, 128>(a, st)
+                     : launch_join<__nv_bfloat16, 256>(a, st);
+  return err == cudaSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
+}
+
+template <typename C>
+AttnArgs cache_args(const C& cache) {
+  AttnArgs a = {};
+  a.kc = static_cast<const char*>(cache.k);
+  a.vc = static_cast<const char*>(cache.v);
+  a.s_page = cache.s_page, a.s_tok = cache.s_token, a.s_head = cache.s_head;
+  a.num_pages = cache.num_pages, a.page_size = cache.page_size;
+  a.Hkv = cache.num_kv_heads;
+  return a;
+}
+
 }  // namespace
 }  // namespace cconv
 
@@ -450,78 +554,29 @@ extern "C" int attn_decode(const void* q, int64_t q_row_stride, kv_cache_t cache
                            int32_t n_spec, int32_t num_q_heads, float scale, int32_t dtype,
                            void* out, int64_t out_row_stride, float* lse, void* workspace,
                            int64_t workspace_bytes, int32_t* dev_err, cconv_stream_t stream) {
-  const int e = mix_dtype_bytes(dtype);
-  if (e == 0) return CCONV_ERR_INVALID;
-  int rc = mix_check_cache(cache, dtype);
+  if (mix_dtype_bytes(dtype) == 0) return CCONV_ERR_INVALID;
+  const int rc = mix_check_cache(cache, dtype);
   if (rc != CCONV_OK) return rc;
-  rc = check_sizes(num_seqs, n_spec, num_q_heads, cache.num_kv_heads, cache.head_dim);
+  AttnArgs a = cache_args(cache);
+  return decode(a, cache.head_dim, false, q, q_row_stride, block_table, block_table_row_stride,
+                table_width, seq_lens, num_seqs, n_spec, num_q_heads, scale, dtype, out,
+                out_row_stride, lse, workspace, workspace_bytes, dev_err, stream);
+}
+
+extern "C" int attn_decode_q8(const void* q, int64_t q_row_stride, kv_cache_q8_t cache,
+                              const int32_t* block_table, int64_t block_table_row_stride,
+                              int32_t table_width, const int32_t* seq_lens, int32_t num_seqs,
+                              int32_t n_spec, int32_t num_q_heads, float scale, int32_t dtype,
+                              void* out, int64_t out_row_stride, float* lse, void* workspace,
+                              int64_t workspace_bytes, int32_t* dev_err, cconv_stream_t stream) {
+  if (mix_dtype_bytes(dtype) == 0) return CCONV_ERR_INVALID;
+  const int rc = mix_check_cache_q8(cache);
   if (rc != CCONV_OK) return rc;
-  if (num_seqs == 0) return CCONV_OK;
-  const int V = 16 / e, D = cache.head_dim;
-  if (!mix_rows_ok(q, q_row_stride, (int64_t)num_q_heads * D, V) ||
-      !mix_rows_ok(out, out_row_stride, (int64_t)num_q_heads * D, V) || !seq_lens ||
-      table_width < 0 || (table_width > 0 && !block_table) ||
-      block_table_row_stride < table_width ||
-      (int64_t)table_width * cache.page_size > INT32_MAX - 1024)
-    return CCONV_ERR_INVALID;
-  const int sms = mix_sm_count();
-  if (sms <= 0) return CCONV_ERR_LAUNCH;
-  const AttnPlan p = plan(dtype, sms, num_seqs, 1 + n_spec, num_q_heads / cache.num_kv_heads,
-                          cache.num_kv_heads, D);
-  if (!workspace || !mix_aligned16(workspace) || workspace_bytes < p.bytes)
-    return CCONV_ERR_INVALID;
-  AttnArgs a;
-  a.q = static_cast<const char*>(q);
-  a.q_rs = q_row_stride;
-  a.kc = static_cast<const char*>(cache.k);
-  a.vc = static_cast<const char*>(cache.v);
-  a.s_page = cache.s_page, a.s_tok = cache.s_token, a.s_head = cache.s_head;
-  a.num_pages = cache.num_pages, a.page_size = cache.page_size;
-  a.page_shift = -1;
-  for (int s = 0; s < 31; ++s)
-    if (cache.page_size == 1 << s) a.page_shift = s;
-  a.table = block_table;
-  a.table_rs = block_table_row_stride;
-  a.table_width = table_width;
-  a.seq_lens = seq_lens;
-  a.B = num_seqs;
-  a.q_len = 1 + n_spec;
-  a.Hq = num_q_heads;
-  a.Hkv = cache.num_kv_heads;
-  a.G = num_q_heads / cache.num_kv_heads;
-  a.scale = scale;
-  a.out = static_cast<char*>(out);
-  a.out_rs = out_row_stride;
-  a.lse = lse;
-  a.meta = static_cast<int32_t*>(workspace);
-  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.meta_bytes);
-  a.hw = p.hw;
-  // positions that follow one another in memory come together, up to 1 KB or four
-  a.group_shift = 0;
-  if (cache.s_token == (int64_t)p.hw * D && (p.hw == 1 || cache.s_head == D))
-    while (a.group_shift < 2 && (p.hw * D * 2 << a.group_shift) < 1024 &&
-           cache.page_size % (2 << a.group_shift) == 0)
-      ++a.group_shift;
-  a.rblocks = p.rblocks;
-  a.rows = p.rows;
-  a.units = p.units;
-  a.grid = p.grid;
-  a.dev_err = dev_err;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t err;
-  if (dtype == CCONV_DTYPE_F32)
-    err = D == 64 ? launch_attn<float, 64>(a, p.grid, st)
-          : D == 128 ? launch_attn<float, 128>(a, p.grid, st)
-                     : launch_attn<float, 256>(a, p.grid, st);
-  else
-    err = attn_launch_mma(a, D, p.grid, st);
-  if (err != cudaSuccess) return CCONV_ERR_LAUNCH;
-  if (dtype == CCONV_DTYPE_F32)
-    err = D == 64 ? launch_join<float, 64>(a, st) : D == 128 ? launch_join<float, 128>(a, st)
-                                                             : launch_join<float, 256>(a, st);
-  else
-    err = D == 64 ? launch_join<__nv_bfloat16, 64>(a, st)
-          : D == 128 ? launch_join<__nv_bfloat16, 128>(a, st)
-                     : launch_join<__nv_bfloat16, 256>(a, st);
-  return err == cudaSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
+  AttnArgs a = cache_args(cache);
+  a.ksc = cache.k_scale;
+  a.vsc = cache.v_scale;
+  a.c_page = cache.c_page, a.c_tok = cache.c_token, a.c_head = cache.c_head;
+  return decode(a, cache.head_dim, true, q, q_row_stride, block_table, block_table_row_stride,
+                table_width, seq_lens, num_seqs, n_spec, num_q_heads, scale, dtype, out,
+                out_row_stride, lse, workspace, workspace_bytes, dev_err, stream);
 }

@@ -42,6 +42,8 @@ struct AttnArgs {
   int32_t units;     // of a request: Hkv / hw * rblocks
   int32_t grid;      // blocks of the split kernel
   int32_t* dev_err;
+  const uint8_t *ksc, *vsc;   // scales of a cache in 8 bits
+  int64_t c_page, c_tok, c_head;
 };
 
 // Blocks of the bf16 kernel that an SM holds at once, by their registers and

@@ -15,8 +15,10 @@
 
 #include "cconv.h"
 
-enum { F32 = 0, BF16 = 1, I32 = 2, U8 = 3, NDT = 5 };
-static PyObject* dtypes[NDT]; /* float32, bfloat16, int32, uint8, bool */
+enum { F32 = 0, BF16 = 1, I32 = 2, U8 = 3, F8 = 5, F8S = 6, MIN_DT = 5, NDT = 7 };
+/* float32, bfloat16, int32, uint8, bool, and of a cache in 8 bits float8_e4m3fn,
+ * float8_e8m0fnu (taken as uint8); bool too is taken as uint8 */
+static PyObject* dtypes[NDT];
 static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device;
 static PyObject* raw_stream; /* device index -> cudaStream_t as an int */
 static PyObject* cur_device; /* () -> index of the current device */
@@ -40,6 +42,15 @@ static int (*p_attn)(const void*, int64_t, kv_cache_t, const int32_t*, int64_t, 
                      const int32_t*, int32_t, int32_t, int32_t, float, int32_t, void*, int64_t,
                      float*, void*, int64_t, int32_t*, cconv_stream_t);
 
+static int (*p_norm_q8)(const void*, int64_t, const void*, int64_t, const void*, int64_t,
+                        const void*, const void*, float, const float*, int32_t, int32_t, int32_t,
+                        const int32_t*, kv_cache_q8_t, const int32_t*, int32_t, int32_t, int32_t,
+                        void*, int64_t, int32_t*, cconv_stream_t);
+static int (*p_read_q8)(kv_cache_q8_t, const int32_t*, int32_t, int32_t, void*, int64_t, void*,
+                        int64_t, int32_t*, cconv_stream_t);
+static int (*p_attn_q8)(const void*, int64_t, kv_cache_q8_t, const int32_t*, int64_t, int32_t,
+                        const int32_t*, int32_t, int32_t, int32_t, float, int32_t, void*, int64_t,
+                        float*, void*, int64_t, int32_t*, cconv_stream_t);
 static int64_t (*p_need)(int32_t, int32_t, int32_t, int32_t, int32_t);
 
 typedef struct {
@@ -58,7 +69,7 @@ static int get(PyObject* o, Ten* t, int* dev) {
   PyObject* d = PyObject_GetAttr(o, s_dtype);
   if (!d) return 0;
   for (int i = 0; i < NDT; ++i)
-    if (d == dtypes[i]) t->dt = i == 4 ? U8 : i;
+    if (d == dtypes[i]) t->dt = i == 4 || i == F8S ? U8 : i;
   Py_DECREF(d);
   if (t->dt < 0) return 0;
   PyObject* c = PyObject_CallMethodNoArgs(o, s_get_device);
@@ -239,55 +250,114 @@ static int cache(PyObject* ko, PyObject* vo, int dt, kv_cache_t* c, int* dev) {
   return 1;
 }
 
-/* q k v q_weight k_weight eps cos_sin positions interleaved k_cache v_cache slots q_out dev_err */
-static PyObject* f_norm(PyObject* self, PyObject* const* x, Py_ssize_t n) {
+/* k_cache v_cache k_scale v_scale at x[0..3] */
+static int cache_q8(PyObject* const* x, kv_cache_q8_t* c, int* dev) {
+  kv_cache_t p;
+  Ten k, v;
+  if (!cache(x[0], x[1], F8, &p, dev) || !need(x[2], &k, U8, dev) || !need(x[3], &v, U8, dev) ||
+      k.nd != 3 || v.nd != 3)
+    return 0;
+  const int64_t n[3] = {p.num_pages, p.page_size, p.num_kv_heads};
+  int64_t s[3];
+  for (int i = 0; i < 3; ++i) {
+    if (k.n[i] != n[i] || v.n[i] != n[i] || k.s[i] != v.s[i]) return 0;
+    s[i] = n[i] > 1 || k.s[i] > 1 ? k.s[i] : 1;
+  }
+  c->k = p.k, c->v = p.v;
+  c->s_page = p.s_page, c->s_token = p.s_token, c->s_head = p.s_head;
+  c->k_scale = k.p, c->v_scale = v.p;
+  c->c_page = s[0], c->c_token = s[1], c->c_head = s[2];
+  c->num_pages = p.num_pages, c->page_size = p.page_size;
+  c->num_kv_heads = p.num_kv_heads, c->head_dim = p.head_dim;
+  return 1;
+}
+
+/* q k v q_weight k_weight eps cos_sin positions interleaved k_cache v_cache [k_scale v_scale]
+ * slots q_out dev_err */
+static PyObject* norm(PyObject* const* x, Py_ssize_t n, int q8) {
   Ten q, k, v, qw, kw, cs, pos, sl, out, err;
-  kv_cache_t c;
+  kv_cache_t c = {0};
+  kv_cache_q8_t c8 = {0};
   int dev = -1;
   int64_t qs, ks, vs, os;
   cconv_stream_t st;
-  if (n != 14 || !get(x[0], &q, &dev) || q.nd != 3 || (q.dt != F32 && q.dt != BF16))
+  if (n != (q8 ? 16 : 14) || !get(x[0], &q, &dev) || q.nd != 3 || (q.dt != F32 && q.dt != BF16))
     return not_plain();
   const int dt = q.dt;
   const int64_t T = q.n[0], hq = q.n[1], D = q.n[2];
   const double eps = PyFloat_AsDouble(x[5]);
   const long il = PyObject_IsTrue(x[8]);
-  if (PyErr_Occurred() || !cache(x[9], x[10], dt, &c, &dev) || c.head_dim != D ||
-      !need(x[1], &k, dt, &dev) || !need(x[2], &v, dt, &dev) || !maybe(x[3], &qw, dt, &dev) ||
-      !maybe(x[4], &kw, dt, &dev) || !need(x[6], &cs, F32, &dev) || !need(x[7], &pos, I32, &dev) ||
-      !need(x[11], &sl, I32, &dev) || !need(x[12], &out, dt, &dev) ||
-      !maybe(x[13], &err, I32, &dev))
+  PyObject* const* y = x + (q8 ? 13 : 11); /* slots q_out dev_err */
+  if (PyErr_Occurred() || !(q8 ? cache_q8(x + 9, &c8, &dev) : cache(x[9], x[10], dt, &c, &dev)))
     return not_plain();
-  if (!heads(&q, T, hq, D, &qs) || !heads(&k, T, c.num_kv_heads, D, &ks) ||
-      !heads(&v, T, c.num_kv_heads, D, &vs) || !heads(&out, T, hq, D, &os) ||
-      (qw.nd >= 0 && !vec(&qw, D)) || (kw.nd >= 0 && !vec(&kw, D)) || !flat(&pos) || !flat(&sl) ||
-      pos.n[0] < T || sl.n[0] < T || cs.nd != 2 || (cs.n[1] > 1 && cs.s[1] != 1) ||
-      (cs.n[0] > 1 && cs.s[0] != cs.n[1]) || !stream_of(dev, &st))
+  const int64_t hkv = q8 ? c8.num_kv_heads : c.num_kv_heads;
+  if ((q8 ? c8.head_dim : c.head_dim) != D || !need(x[1], &k, dt, &dev) ||
+      !need(x[2], &v, dt, &dev) || !maybe(x[3], &qw, dt, &dev) || !maybe(x[4], &kw, dt, &dev) ||
+      !need(x[6], &cs, F32, &dev) || !need(x[7], &pos, I32, &dev) || !need(y[0], &sl, I32, &dev) ||
+      !need(y[1], &out, dt, &dev) || !maybe(y[2], &err, I32, &dev))
     return not_plain();
-  return PyLong_FromLong(p_norm(q.p, qs, k.p, ks, v.p, vs, qw.p, kw.p, (float)eps, cs.p,
-                                (int32_t)cs.n[0], (int32_t)cs.n[1], (int32_t)il, pos.p, c, sl.p,
-                                (int32_t)T, (int32_t)hq, dt, out.p, os, err.p, st));
+  if (!heads(&q, T, hq, D, &qs) || !heads(&k, T, hkv, D, &ks) || !heads(&v, T, hkv, D, &vs) ||
+      !heads(&out, T, hq, D, &os) || (qw.nd >= 0 && !vec(&qw, D)) || (kw.nd >= 0 && !vec(&kw, D)) ||
+      !flat(&pos) || !flat(&sl) || pos.n[0] < T || sl.n[0] < T || cs.nd != 2 ||
+      (cs.n[1] > 1 && cs.s[1] != 1) || (cs.n[0] > 1 && cs.s[0] != cs.n[1]) ||
+      (err.nd >= 0 && (err.nd != 1 || err.n[0] < 1)) || !stream_of(dev, &st))
+    return not_plain();
+  return PyLong_FromLong(
+      q8 ? p_norm_q8(q.p, qs, k.p, ks, v.p, vs, qw.p, kw.p, (float)eps, cs.p, (int32_t)cs.n[0],
+                     (int32_t)cs.n[1], (int32_t)il, pos.p, c8, sl.p, (int32_t)T, (int32_t)hq, dt,
+                     out.p, os, err.p, st)
+         : p_norm(q.p, qs, k.p, ks, v.p, vs, qw.p, kw.p, (float)eps, cs.p, (int32_t)cs.n[0],
+                  (int32_t)cs.n[1], (int32_t)il, pos.p, c, sl.p, (int32_t)T, (int32_t)hq, dt,
+                  out.p, os, err.p, st));
+}
+static PyObject* f_norm(PyObject* self, PyObject* const* x, Py_ssize_t n) { return norm(x, n, 0); }
+static PyObject* f_norm_q8(PyObject* self, PyObject* const* x, Py_ssize_t n) {
+  return norm(x, n, 1);
 }
 
-/* q k_cache v_cache block_table seq_lens n_spec scale out lse workspace dev_err */
-static PyObject* f_attn(PyObject* self, PyObject* const* x, Py_ssize_t n) {
+/* k_cache v_cache k_scale v_scale slots k_out v_out dev_err */
+static PyObject* f_read_q8(PyObject* self, PyObject* const* x, Py_ssize_t n) {
+  Ten sl, ko, vo, err;
+  kv_cache_q8_t c;
+  int dev = -1;
+  int64_t ks, vs;
+  cconv_stream_t st;
+  if (n != 8 || !cache_q8(x, &c, &dev) || !need(x[4], &sl, I32, &dev) || !flat(&sl) ||
+      !get(x[5], &ko, &dev) || ko.nd != 3 || (ko.dt != F32 && ko.dt != BF16) ||
+      !need(x[6], &vo, ko.dt, &dev) || !maybe(x[7], &err, I32, &dev))
+    return not_plain();
+  const int64_t T = sl.n[0];
+  if (!heads(&ko, T, c.num_kv_heads, c.head_dim, &ks) ||
+      !heads(&vo, T, c.num_kv_heads, c.head_dim, &vs) ||
+      (err.nd >= 0 && (err.nd != 1 || err.n[0] < 1)) || !stream_of(dev, &st))
+    return not_plain();
+  return PyLong_FromLong(p_read_q8(c, sl.p, (int32_t)T, ko.dt, ko.p, ks, vo.p, vs, err.p, st));
+}
+
+/* q k_cache v_cache [k_scale v_scale] block_table seq_lens n_spec scale out lse workspace
+ * dev_err */
+static PyObject* attn(PyObject* const* x, Py_ssize_t n, int q8) {
   Ten q, tab, len, out, lse, ws, err;
-  kv_cache_t c;
+  kv_cache_t c = {0};
+  kv_cache_q8_t c8 = {0};
   int dev = -1;
   int64_t qs, os;
   cconv_stream_t st;
-  if (n != 11 || !get(x[0], &q, &dev) || q.nd != 3 || (q.dt != F32 && q.dt != BF16))
+  if (n != (q8 ? 13 : 11) || !get(x[0], &q, &dev) || q.nd != 3 || (q.dt != F32 && q.dt != BF16))
     return not_plain();
-  const long ns = PyLong_AsLong(x[5]);
-  const double scale = PyFloat_AsDouble(x[6]);
-  if (PyErr_Occurred() || ns < 0 || !cache(x[1], x[2], q.dt, &c, &dev) ||
-      !need(x[3], &tab, I32, &dev) || !need(x[4], &len, I32, &dev) ||
-      !need(x[7], &out, q.dt, &dev) || !maybe(x[8], &lse, F32, &dev) ||
-      !maybe(x[9], &ws, U8, &dev) || !maybe(x[10], &err, I32, &dev) || !flat(&len) ||
-      (ws.nd >= 0 && !flat(&ws)))
+  PyObject* const* y = x + (q8 ? 5 : 3); /* block_table .. */
+  const long ns = PyLong_AsLong(y[2]);
+  const double scale = PyFloat_AsDouble(y[3]);
+  if (PyErr_Occurred() || ns < 0 ||
+      !(q8 ? cache_q8(x + 1, &c8, &dev) : cache(x[1], x[2], q.dt, &c, &dev)) ||
+      !need(y[0], &tab, I32, &dev) || !need(y[1], &len, I32, &dev) ||
+      !need(y[4], &out, q.dt, &dev) || !maybe(y[5], &lse, F32, &dev) ||
+      !maybe(y[6], &ws, U8, &dev) || !maybe(y[7], &err, I32, &dev) || !flat(&len) ||
+      (ws.nd >= 0 && !flat(&ws)) || (err.nd >= 0 && (err.nd != 1 || err.n[0] < 1)))
     return not_plain();
   const int64_t B = len.n[0], rows = B * (1 + ns);
-  if (q.n[2] != c.head_dim || !heads(&q, rows, q.n[1], q.n[2], &qs) ||
+  const int32_t hkv = q8 ? c8.num_kv_heads : c.num_kv_heads, D = q8 ? c8.head_dim : c.head_dim;
+  if (q.n[2] != D || !heads(&q, rows, q.n[1], q.n[2], &qs) ||
       !heads(&out, rows, q.n[1], q.n[2], &os) || tab.nd != 2 || tab.n[0] < B ||
       (tab.n[1] > 1 && tab.s[1] != 1) ||
       (lse.nd >= 0 && (lse.nd != 2 || lse.n[0] < rows || lse.n[1] != q.n[1] ||
@@ -297,8 +367,7 @@ static PyObject* f_attn(PyObject* self, PyObject* const* x, Py_ssize_t n) {
   const int64_t ts = tab.n[0] > 1 || tab.s[0] > tab.n[1] ? tab.s[0] : tab.n[1];
   PyObject* own = NULL; /* the call's workspace, if it brought none */
   if (ws.nd < 0) {
-    const int64_t need = p_need((int32_t)B, (int32_t)ns, (int32_t)q.n[1], c.num_kv_heads,
-                                c.head_dim);
+    const int64_t need = p_need((int32_t)B, (int32_t)ns, (int32_t)q.n[1], hkv, D);
     if (need < 0) return not_plain();
     own = PyObject_CallFunction(new_bytes, "OL", x[0], (long long)(need > 16 ? need : 16));
     if (!own) return NULL;
@@ -307,18 +376,27 @@ static PyObject* f_attn(PyObject* self, PyObject* const* x, Py_ssize_t n) {
       return not_plain();
     }
   }
-  const int rc = p_attn(q.p, qs, c, tab.p, ts, (int32_t)tab.n[1], len.p, (int32_t)B,
-                        (int32_t)ns, (int32_t)q.n[1], (float)scale, q.dt, out.p, os, lse.p, ws.p,
-                        ws.n[0], err.p, st);
+  const int rc =
+      q8 ? p_attn_q8(q.p, qs, c8, tab.p, ts, (int32_t)tab.n[1], len.p, (int32_t)B, (int32_t)ns,
+                     (int32_t)q.n[1], (float)scale, q.dt, out.p, os, lse.p, ws.p, ws.n[0], err.p,
+                     st)
+         : p_attn(q.p, qs, c, tab.p, ts, (int32_t)tab.n[1], len.p, (int32_t)B, (int32_t)ns,
+                  (int32_t)q.n[1], (float)scale, q.dt, out.p, os, lse.p, ws.p, ws.n[0], err.p, st);
   Py_XDECREF(own);
   return PyLong_FromLong(rc);
 }
+static PyObject* f_attn(PyObject* self, PyObject* const* x, Py_ssize_t n) { return attn(x, n, 0); }
+static PyObject* f_attn_q8(PyObject* self, PyObject* const* x, Py_ssize_t n) {
+  return attn(x, n, 1);
+}
 
-/* init(handle of libcconv.so, (float32, bfloat16, int32, uint8, bool), raw stream function,
+/* init(handle of libcconv.so, (float32, bfloat16, int32, uint8, bool[, float8_e4m3fn,
+ *      float8_e8m0fnu: without them 8-bit caches are left to Python]), raw stream function,
  *      function (tensor, n) -> n bytes on its device and the current stream, current device
  *      function) */
 static PyObject* f_init(PyObject* self, PyObject* const* x, Py_ssize_t n) {
-  if (n != 5 || !PyTuple_Check(x[1]) || PyTuple_GET_SIZE(x[1]) != NDT) {
+  if (n != 5 || !PyTuple_Check(x[1]) ||
+      (PyTuple_GET_SIZE(x[1]) != MIN_DT && PyTuple_GET_SIZE(x[1]) != NDT)) {
     PyErr_SetString(PyExc_TypeError, "init(handle, dtypes, raw_stream, new_bytes, cur_device)");
     return NULL;
   }
@@ -329,11 +407,16 @@ static PyObject* f_init(PyObject* self, PyObject* const* x, Py_ssize_t n) {
   *(void**)&p_norm = dlsym(h, "attn_norm_rope_cache");
   *(void**)&p_attn = dlsym(h, "attn_decode");
   *(void**)&p_need = dlsym(h, "attn_decode_workspace_bytes");
-  if (!p_fwd || !p_upd || !p_norm || !p_attn || !p_need) {
+  *(void**)&p_norm_q8 = dlsym(h, "attn_norm_rope_cache_q8");
+  *(void**)&p_read_q8 = dlsym(h, "kv_cache_read_q8");
+  *(void**)&p_attn_q8 = dlsym(h, "attn_decode_q8");
+  if (!p_fwd || !p_upd || !p_norm || !p_attn || !p_need || !p_norm_q8 || !p_read_q8 ||
+      !p_attn_q8) {
     PyErr_SetString(PyExc_RuntimeError, "libcconv.so lacks an entry point");
     return NULL;
   }
-  for (int i = 0; i < NDT; ++i) Py_XSETREF(dtypes[i], Py_NewRef(PyTuple_GET_ITEM(x[1], i)));
+  for (int i = 0; i < NDT; ++i)
+    Py_XSETREF(dtypes[i], i < PyTuple_GET_SIZE(x[1]) ? Py_NewRef(PyTuple_GET_ITEM(x[1], i)) : NULL);
   Py_XSETREF(raw_stream, Py_NewRef(x[2]));
   Py_XSETREF(new_bytes, Py_NewRef(x[3]));
   Py_XSETREF(cur_device, Py_NewRef(x[4]));
@@ -346,6 +429,9 @@ static PyMethodDef methods[] = {FN("init", f_init),
                                 FN("gdn_update", f_upd),
                                 FN("attn_norm_rope_cache", f_norm),
                                 FN("attn_decode", f_attn),
+                                FN("attn_norm_rope_cache_q8", f_norm_q8),
+                                FN("kv_cache_read_q8", f_read_q8),
+                                FN("attn_decode_q8", f_attn_q8),
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", NULL, -1, methods,
                                     NULL, NULL, NULL, NULL};

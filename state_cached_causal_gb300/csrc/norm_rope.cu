@@ -1,5 +1,6 @@
-// Entry point attn_norm_rope_cache: per-head RMS norm of q and k, rotation by
-// position, and the write of k and v into the paged cache, in one pass.
+// Entry points attn_norm_rope_cache and attn_norm_rope_cache_q8: per-head RMS norm
+// of q and k, rotation by position, and the write of k and v into the paged cache,
+// in one pass.
 //
 // The pass reads every row once and writes every row once, with about 10
 // flops a value: it is bound by HBM as long as the instructions around those
@@ -18,7 +19,10 @@
 // queries, values after the keys: 78.7 us; three blocks, whose 168 registers
 // spill nothing: 78.1 us; one unit a lane: 98.7 us). 61 tokens: 3.0 us, the
 // latency of a few dependent loads.
-#include "mixer.cuh"
+//
+// Into a cache in 8 bits a row's largest magnitude is reduced over the head's lanes
+// as its sum of squares is, and a unit of 16 bytes becomes one of 8 (4 from fp32).
+#include "q8.cuh"
 
 namespace cconv {
 namespace {
@@ -44,9 +48,11 @@ struct NrArgs {
   int32_t parts;      // warps a token
   char* qo;
   int32_t* dev_err;
+  uint8_t *ksc, *vsc;   // of a cache in 8 bits
+  int64_t c_page, c_tok, c_head;
 };
 
-template <typename T, int D, bool PAIRS>
+template <typename T, int D, bool PAIRS, bool Q8>
 __global__ void __launch_bounds__(kNrThreads, kNrBlocks) norm_rope_kernel(const NrArgs a) {
   constexpr int V = Elem<T>::V, E = Elem<T>::bytes;
   constexpr int LPH = D / V / 2;              // lanes a head, two units each
@@ -108,15 +114,46 @@ __global__ void __launch_bounds__(kNrThreads, kNrBlocks) norm_rope_kernel(const 
       }
     }
     char *kdst = nullptr, *vdst = nullptr;
+    uint8_t *kscale = nullptr, *vscale = nullptr;
+    constexpr int CE = Q8 ? 1 : E;              // bytes of a cached value
     if (sl >= 0) {
       const int page = sl / a.page_size;
-      const int64_t off = (page * a.s_page + (int64_t)(sl - page * a.page_size) * a.s_tok) * E;
+      const int64_t off = (page * a.s_page + (int64_t)(sl - page * a.page_size) * a.s_tok) * CE;
       kdst = a.kc + off;
       vdst = a.vc + off;
+      if constexpr (Q8) {
+        const int64_t to = page * a.c_page + (int64_t)(sl - page * a.page_size) * a.c_tok;
+        kscale = a.ksc + to;
+        vscale = a.vsc + to;
+      }
     }
-    // one group of heads: norm, rotation, store (`in`: the lane's head exists)
+    // a head's row to 8 bits, of which the lane has columns from b0 and b1 on
+    auto store_q8 = [&](float (&x0)[V], float (&x1)[V], char* dst, int b0, int b1, uint8_t* scale,
+                        bool in) {
+      float m = 0.0f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        x0[e] = q8_in(x0[e]);
+        x1[e] = q8_in(x1[e]);
+        m = fmaxf(m, fmaxf(fabsf(x0[e]), fabsf(x1[e])));
+      }
+#pragma unroll
+      for (int d = LPH / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      const uint32_t byte = q8_byte(m);
+      const float f = q8_factor(byte);
+      if (!in) return;
+#pragma unroll
+      for (int e = 0; e < V; e += 4) {
+        *reinterpret_cast<uint32_t*>(dst + b0 + e) =
+            pack_e4m3x4(x0[e] * f, x0[e + 1] * f, x0[e + 2] * f, x0[e + 3] * f);
+        *reinterpret_cast<uint32_t*>(dst + b1 + e) =
+            pack_e4m3x4(x1[e] * f, x1[e + 1] * f, x1[e + 2] * f, x1[e + 3] * f);
+      }
+      if (l == 0) *scale = (uint8_t)byte;
+    };
+    // one group of heads: norm and rotation
     auto rotate = [&](const uint4& u0, const uint4& u1, const float (&w0)[V], const float (&w1)[V],
-                      bool norm, char* dst, bool in) {
+                      bool norm, float (&y0)[V], float (&y1)[V]) {
       float x0[V], x1[V];
       unpack16<T>(u0, x0);
       unpack16<T>(u1, x1);
@@ -137,7 +174,6 @@ __global__ void __launch_bounds__(kNrThreads, kNrBlocks) norm_rope_kernel(const 
           mul_x2(x1[e], x1[e + 1], x1[e], x1[e + 1], r * w1[e], r * w1[e + 1]);
         }
       }
-      float y0[V], y1[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         if constexpr (PAIRS) {
@@ -150,6 +186,9 @@ __global__ void __launch_bounds__(kNrThreads, kNrBlocks) norm_rope_kernel(const 
           y1[e] = fmaf(x0[e], s[e], x1[e] * c[e]);
         }
       }
+    };
+    // (`in`: the lane's head exists)
+    auto store = [&](const float (&y0)[V], const float (&y1)[V], char* dst, bool in) {
       if (in) {
         stg16(dst + c0 * E, pack16<T>(y0));
         stg16(dst + c1 * E, pack16<T>(y1));
@@ -198,7 +237,9 @@ __global__ void __launch_bounds__(kNrThreads, kNrBlocks) norm_rope_kernel(const 
       for (int j = 0; j < kUnroll; ++j) {
         if (h0 + j * HPW >= qe) break;              // warp-uniform
         const int h = h0 + j * HPW + sub;
-        rotate(u0[j], u1[j], w0, w1, a.qw != nullptr, qd + (int64_t)h * (D * E), h < qe);
+        float y0[V], y1[V];
+        rotate(u0[j], u1[j], w0, w1, a.qw != nullptr, y0, y1);
+        store(y0, y1, qd + (int64_t)h * (D * E), h < qe);
       }
     }
     unpack16<T>(wk[0], w0);
@@ -206,8 +247,13 @@ __global__ void __launch_bounds__(kNrThreads, kNrBlocks) norm_rope_kernel(const 
 #pragma unroll 1
     for (int h0 = kb; h0 < ke; h0 += HPW) {
       const int h = h0 + sub;
-      const int64_t to = (int64_t)h * a.s_head * E;
-      if (h < ke) {
+      const int64_t to = (int64_t)h * a.s_head * CE, sc = Q8 ? h * a.c_head : 0;
+      if constexpr (Q8) {
+        float x0[V], x1[V];
+        unpack16<T>(vu0, x0);
+        unpack16<T>(vu1, x1);
+        store_q8(x0, x1, vdst + to, l * V, (LPH + l) * V, vscale + sc, h < ke);
+      } else if (h < ke) {
         stg16(vdst + to + v0, vu0);
         stg16(vdst + to + v1, vu1);
       }
@@ -215,28 +261,98 @@ __global__ void __launch_bounds__(kNrThreads, kNrBlocks) norm_rope_kernel(const 
       const int64_t next = (int64_t)(h + HPW) * (D * E);
       load(ks + next, h + HPW < ke, ku0, ku1, c0 * E, c1 * E);
       load(vs + next, h + HPW < ke, vu0, vu1, v0, v1);
-      rotate(k0, k1, w0, w1, a.kw != nullptr, kdst + to, h < ke);
+      float y0[V], y1[V];
+      rotate(k0, k1, w0, w1, a.kw != nullptr, y0, y1);
+      if constexpr (Q8)
+        store_q8(y0, y1, kdst + to, c0, c1, kscale + sc, h < ke);
+      else
+        store(y0, y1, kdst + to, h < ke);
     }
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool Q8>
 cudaError_t launch_nr(const NrArgs& a, bool pairs, int sms, cudaStream_t st) {
   const int64_t warps = (int64_t)a.T * a.parts, per = kNrThreads / 32;
   const unsigned grid =
       (unsigned)std::min<int64_t>((warps + per - 1) / per, (int64_t)sms * kNrBlocks);
   if (pairs)
-    norm_rope_kernel<T, D, true><<<grid, kNrThreads, 0, st>>>(a);
+    norm_rope_kernel<T, D, true, Q8><<<grid, kNrThreads, 0, st>>>(a);
   else
-    norm_rope_kernel<T, D, false><<<grid, kNrThreads, 0, st>>>(a);
+    norm_rope_kernel<T, D, false, Q8><<<grid, kNrThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T>
+template <typename T, bool Q8>
 cudaError_t launch_nr_d(const NrArgs& a, int D, bool pairs, int sms, cudaStream_t st) {
-  if (D == 64) return launch_nr<T, 64>(a, pairs, sms, st);
-  if (D == 128) return launch_nr<T, 128>(a, pairs, sms, st);
-  return launch_nr<T, 256>(a, pairs, sms, st);
+  if (D == 64) return launch_nr<T, 64, Q8>(a, pairs, sms, st);
+  if (D == 128) return launch_nr<T, 128, Q8>(a, pairs, sms, st);
+  return launch_nr<T, 256, Q8>(a, pairs, sms, st);
+}
+
+// What both entry points check and fill in; a's cache, and D, are set.
+int norm_rope(NrArgs& a, int D, bool q8, const void* q, int64_t q_row_stride, const void* k,
+              int64_t k_row_stride, const void* v, int64_t v_row_stride, const void* q_weight,
+              const void* k_weight, float eps, const float* cos_sin, int32_t max_position,
+              int32_t rot_dim, int32_t interleaved, const int32_t* positions,
+              const int32_t* slot_mapping, int32_t num_tokens, int32_t num_q_heads, int32_t dtype,
+              void* q_out, int64_t q_out_row_stride, int32_t* dev_err, cconv_stream_t stream) {
+  const int e = mix_dtype_bytes(dtype), V = 16 / e;
+  if (rot_dim < 0 || rot_dim > D || rot_dim % 2 || (!interleaved && rot_dim % (2 * V)) ||
+      max_position <= 0 || (rot_dim > 0 && (!cos_sin || !mix_aligned16(cos_sin))) || !(eps >= 0.0f))
+    return CCONV_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(q_weight) % e || reinterpret_cast<uintptr_t>(k_weight) % e)
+    return CCONV_ERR_INVALID;
+  if (num_tokens == 0) return CCONV_OK;
+  if (!mix_rows_ok(q, q_row_stride, (int64_t)num_q_heads * D, V) ||
+      !mix_rows_ok(k, k_row_stride, (int64_t)a.Hkv * D, V) ||
+      !mix_rows_ok(v, v_row_stride, (int64_t)a.Hkv * D, V) ||
+      !mix_rows_ok(q_out, q_out_row_stride, (int64_t)num_q_heads * D, V) || !positions ||
+      !slot_mapping)
+    return CCONV_ERR_INVALID;
+  const int sms = mix_sm_count();
+  if (sms <= 0) return CCONV_ERR_LAUNCH;
+  a.q = static_cast<const char*>(q);
+  a.k = static_cast<const char*>(k);
+  a.v = static_cast<const char*>(v);
+  a.q_rs = q_row_stride, a.k_rs = k_row_stride, a.v_rs = v_row_stride;
+  a.qo_rs = q_out_row_stride;
+  a.qw = static_cast<const char*>(q_weight);
+  a.kw = static_cast<const char*>(k_weight);
+  a.eps = eps;
+  a.cs = cos_sin;
+  a.max_pos = max_position;
+  a.rot = rot_dim;
+  a.pos = positions;
+  a.slots = slot_mapping;
+  a.T = num_tokens;
+  a.Hq = num_q_heads;
+  a.qo = static_cast<char*>(q_out);
+  a.dev_err = dev_err;
+  // several warps a token while there are fewer than 16 warps an SM: 1, 2, 4 or 8,
+  // so that a block's four warps, and the grid's, fall into whole tokens
+  a.parts = 1;
+  while (a.parts < 8 && (int64_t)num_tokens * a.parts * 2 <= (int64_t)sms * 16) a.parts *= 2;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool pairs = interleaved != 0;
+  cudaError_t err;
+  if (dtype == CCONV_DTYPE_F32)
+    err = q8 ? launch_nr_d<float, true>(a, D, pairs, sms, st)
+             : launch_nr_d<float, false>(a, D, pairs, sms, st);
+  else
+    err = q8 ? launch_nr_d<__nv_bfloat16, true>(a, D, pairs, sms, st)
+             : launch_nr_d<__nv_bfloat16, false>(a, D, pairs, sms, st);
+  return err == cudaSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
+}
+
+template <typename C>
+void nr_cache(NrArgs& a, const C& cache) {
+  a.kc = static_cast<char*>(cache.k);
+  a.vc = static_cast<char*>(cache.v);
+  a.s_page = cache.s_page, a.s_tok = cache.s_token, a.s_head = cache.s_head;
+  a.page_size = cache.page_size;
+  a.num_slots = (int64_t)cache.num_pages * cache.page_size;
+  a.Hkv = cache.num_kv_heads;
 }
 
 }  // namespace
@@ -253,56 +369,36 @@ extern "C" int attn_norm_rope_cache(const void* q, int64_t q_row_stride, const v
                                     int32_t num_tokens, int32_t num_q_heads, int32_t dtype,
                                     void* q_out, int64_t q_out_row_stride, int32_t* dev_err,
                                     cconv_stream_t stream) {
-  const int e = mix_dtype_bytes(dtype);
-  if (e == 0 || num_tokens < 0 || num_q_heads <= 0) return CCONV_ERR_INVALID;
+  if (mix_dtype_bytes(dtype) == 0 || num_tokens < 0 || num_q_heads <= 0) return CCONV_ERR_INVALID;
   const int rc = mix_check_cache(cache, dtype);
   if (rc != CCONV_OK) return rc;
-  const int V = 16 / e, D = cache.head_dim;
-  if (rot_dim < 0 || rot_dim > D || rot_dim % 2 || (!interleaved && rot_dim % (2 * V)) ||
-      max_position <= 0 || (rot_dim > 0 && (!cos_sin || !mix_aligned16(cos_sin))) || !(eps >= 0.0f))
-    return CCONV_ERR_INVALID;
-  if (reinterpret_cast<uintptr_t>(q_weight) % e || reinterpret_cast<uintptr_t>(k_weight) % e)
-    return CCONV_ERR_INVALID;
-  if (num_tokens == 0) return CCONV_OK;
-  if (!mix_rows_ok(q, q_row_stride, (int64_t)num_q_heads * D, V) ||
-      !mix_rows_ok(k, k_row_stride, (int64_t)cache.num_kv_heads * D, V) ||
-      !mix_rows_ok(v, v_row_stride, (int64_t)cache.num_kv_heads * D, V) ||
-      !mix_rows_ok(q_out, q_out_row_stride, (int64_t)num_q_heads * D, V) || !positions ||
-      !slot_mapping)
-    return CCONV_ERR_INVALID;
-  const int sms = mix_sm_count();
-  if (sms <= 0) return CCONV_ERR_LAUNCH;
-  NrArgs a;
-  a.q = static_cast<const char*>(q);
-  a.k = static_cast<const char*>(k);
-  a.v = static_cast<const char*>(v);
-  a.q_rs = q_row_stride, a.k_rs = k_row_stride, a.v_rs = v_row_stride;
-  a.qo_rs = q_out_row_stride;
-  a.qw = static_cast<const char*>(q_weight);
-  a.kw = static_cast<const char*>(k_weight);
-  a.eps = eps;
-  a.cs = cos_sin;
-  a.max_pos = max_position;
-  a.rot = rot_dim;
-  a.pos = positions;
-  a.kc = static_cast<char*>(cache.k);
-  a.vc = static_cast<char*>(cache.v);
-  a.s_page = cache.s_page, a.s_tok = cache.s_token, a.s_head = cache.s_head;
-  a.page_size = cache.page_size;
-  a.num_slots = (int64_t)cache.num_pages * cache.page_size;
-  a.slots = slot_mapping;
-  a.T = num_tokens;
-  a.Hq = num_q_heads;
-  a.Hkv = cache.num_kv_heads;
-  a.qo = static_cast<char*>(q_out);
-  a.dev_err = dev_err;
-  // several warps a token while there are fewer than 16 warps an SM: 1, 2, 4 or 8,
-  // so that a block's four warps, and the grid's, fall into whole tokens
-  a.parts = 1;
-  while (a.parts < 8 && (int64_t)num_tokens * a.parts * 2 <= (int64_t)sms * 16) a.parts *= 2;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t err = dtype == CCONV_DTYPE_F32
-                              ? launch_nr_d<float>(a, D, interleaved != 0, sms, st)
-                              : launch_nr_d<__nv_bfloat16>(a, D, interleaved != 0, sms, st);
-  return err == cudaSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
+  NrArgs a = {};
+  nr_cache(a, cache);
+  return norm_rope(a, cache.head_dim, false, q, q_row_stride, k, k_row_stride, v, v_row_stride,
+                   q_weight, k_weight, eps, cos_sin, max_position, rot_dim, interleaved, positions,
+                   slot_mapping, num_tokens, num_q_heads, dtype, q_out, q_out_row_stride, dev_err,
+                   stream);
+}
+
+extern "C" int attn_norm_rope_cache_q8(const void* q, int64_t q_row_stride, const void* k,
+                                       int64_t k_row_stride, const void* v, int64_t v_row_stride,
+                                       const void* q_weight, const void* k_weight, float eps,
+                                       const float* cos_sin, int32_t max_position, int32_t rot_dim,
+                                       int32_t interleaved, const int32_t* positions,
+                                       kv_cache_q8_t cache, const int32_t* slot_mapping,
+                                       int32_t num_tokens, int32_t num_q_heads, int32_t dtype,
+                                       void* q_out, int64_t q_out_row_stride, int32_t* dev_err,
+                                       cconv_stream_t stream) {
+  if (mix_dtype_bytes(dtype) == 0 || num_tokens < 0 || num_q_heads <= 0) return CCONV_ERR_INVALID;
+  const int rc = mix_check_cache_q8(cache);
+  if (rc != CCONV_OK) return rc;
+  NrArgs a = {};
+  nr_cache(a, cache);
+  a.ksc = cache.k_scale;
+  a.vsc = cache.v_scale;
+  a.c_page = cache.c_page, a.c_tok = cache.c_token, a.c_head = cache.c_head;
+  return norm_rope(a, cache.head_dim, true, q, q_row_stride, k, k_row_stride, v, v_row_stride,
+                   q_weight, k_weight, eps, cos_sin, max_position, rot_dim, interleaved, positions,
+                   slot_mapping, num_tokens, num_q_heads, dtype, q_out, q_out_row_stride, dev_err,
+                   stream);
 }

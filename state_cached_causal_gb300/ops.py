@@ -24,6 +24,8 @@ DERR_SLOT_RANGE, DERR_CU_SEQLENS, DERR_NUM_ACCEPTED, DERR_TIMEOUT = 1, 2, 4, 8
 DERR_ROW_INDEX, DERR_CHECKPOINT = 16, 32
 DERR_POSITION, DERR_PAGE, DERR_SEQ_LEN = 64, 128, 256
 
+_F8, _F8_SCALE = torch.float8_e4m3fn, torch.float8_e8m0fnu    # of a cache in 8 bits
+
 _lock = threading.Lock()
 _lib = None
 _fast = None    # csrc/fast.c: the mixer calls' marshalling in C, set by load()
@@ -58,6 +60,16 @@ class KvCache(ctypes.Structure):
                 ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class KvCacheQ8(ctypes.Structure):
+    """kv_cache_q8_t: a paged cache of e4m3 rows and the [page, token, kv head] views of their scales."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("s_page", ctypes.c_int64),
+                ("s_token", ctypes.c_int64), ("s_head", ctypes.c_int64),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("c_page", ctypes.c_int64), ("c_token", ctypes.c_int64), ("c_head", ctypes.c_int64),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
 class CConvError(RuntimeError):
@@ -119,6 +131,12 @@ def load():
         lib.attn_decode.restype = ctypes.c_int
         lib.attn_decode_workspace_bytes.argtypes = [I32, I32, I32, I32, I32]
         lib.attn_decode_workspace_bytes.restype = I64
+        for name in ("attn_norm_rope_cache", "attn_decode"):
+            plain, q8 = getattr(lib, name), getattr(lib, name + "_q8")
+            q8.argtypes = [KvCacheQ8 if t is KvCache else t for t in plain.argtypes]
+            q8.restype = ctypes.c_int
+        lib.kv_cache_read_q8.argtypes = [KvCacheQ8, P, I32, I32, P, I64, P, I64, P, P]
+        lib.kv_cache_read_q8.restype = ctypes.c_int
         lib.cconv_status_string.argtypes = [ctypes.c_int]
         lib.cconv_status_string.restype = ctypes.c_char_p
         lib.cconv_abi_version.argtypes = []
@@ -136,8 +154,8 @@ def _load_fast(lib):
         raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     except (ImportError, AttributeError):
         return None
-    mod.init(lib._handle, (torch.float32, torch.bfloat16, torch.int32, torch.uint8, torch.bool),
-             raw, lambda beside, n: beside.new_empty(n, dtype=torch.uint8), device)
+    mod.init(lib._handle, (torch.float32, torch.bfloat16, torch.int32, torch.uint8, torch.bool,
+                           _F8, _F8_SCALE), raw, lambda beside, n: beside.new_empty(n, dtype=torch.uint8), device)
     return mod
 
 
@@ -560,6 +578,40 @@ def _cache(k_cache, v_cache, dtype):
     return s, st, code
 
 
+def _cache_q8(k_cache, v_cache, k_scale, v_scale):
+    """(shape, strides, scale strides) of an 8-bit cache's four views."""
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.dtype is not _F8:
+            raise TypeError(f"{name} must be float8_e4m3fn")
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t.dtype not in (torch.uint8, _F8_SCALE):
+            raise TypeError(f"{name} must be uint8 or float8_e8m0fnu")
+    s, st = k_cache.shape, k_cache.stride()
+    if len(s) != 4 or v_cache.shape != s or st[3] != 1:
+        raise ValueError("caches must be [pages, page_size, kv heads, head_dim] of one shape")
+    if v_cache.stride() != st:
+        raise ValueError("k_cache and v_cache must have the same strides")
+    if k_scale.shape != s[:3] or v_scale.shape != s[:3]:
+        raise ValueError("scales must be [pages, page_size, kv heads], as the caches")
+    ct = k_scale.stride()
+    if v_scale.stride() != ct:
+        raise ValueError("k_scale and v_scale must have the same strides")
+    # a dimension of one entry may carry any stride
+    st = [x if n > 1 else max(x, s[3]) for x, n in zip(st, s)]
+    return s, st, [x if n > 1 else max(x, 1) for x, n in zip(ct, s)]
+
+
+def _q8_struct(P, s, st, ct):
+    return KvCacheQ8(P[0], P[1], st[0], st[1], st[2], P[2], P[3], ct[0], ct[1], ct[2], *s)
+
+
+def _call_dtype(dtype):
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
 def attn_norm_rope_cache(q, k, v, q_weight, k_weight, eps, cos_sin, positions, interleaved,
                          k_cache, v_cache, slot_mapping, q_out, dev_err=None, stream=None):
     """Head norm, rotation and cache write (see attn_norm_rope_cache in cconv.h).
@@ -573,11 +625,19 @@ def attn_norm_rope_cache(q, k, v, q_weight, k_weight, eps, cos_sin, positions, i
                 q, k, v, q_weight, k_weight, eps, cos_sin, positions, interleaved, k_cache,
                 v_cache, slot_mapping, q_out, dev_err)):
         return
+    (pages, page, hkv, dim), st, code = _cache(k_cache, v_cache, q.dtype)
+    _norm_call("attn_norm_rope_cache", q, k, v, q_weight, k_weight, eps, cos_sin, positions,
+               interleaved, slot_mapping, q_out, dev_err, stream, hkv, dim, (k_cache, v_cache),
+               lambda P: KvCache(P[0], P[1], st[0], st[1], st[2], pages, page, hkv, dim, code))
+
+
+def _norm_call(fn, q, k, v, q_weight, k_weight, eps, cos_sin, positions, interleaved, slot_mapping,
+               q_out, dev_err, stream, hkv, dim, views, cache):
+    """views: the cache's tensors; cache(addresses) -> its C struct."""
     _entries(positions, "positions", q.shape[0])
     _entries(slot_mapping, "slot_mapping", q.shape[0])
     _error_word(dev_err)
-    dtype = q.dtype
-    (pages, page, hkv, dim), st, code = _cache(k_cache, v_cache, dtype)
+    dtype, code = q.dtype, _call_dtype(q.dtype)
     T, hq = q.shape[0], q.shape[1]
     qs = _heads(q, "q", dtype, T, hq, dim)[2]
     ks = _heads(k, "k", dtype, T, hkv, dim)[2]
@@ -589,15 +649,56 @@ def attn_norm_rope_cache(q, k, v, q_weight, k_weight, eps, cos_sin, positions, i
         _vector(k_weight, "k_weight", dtype, dim)
     if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
         raise TypeError("cos_sin must be contiguous float32 [max_position, rot_dim]")
-    P = _raw(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_cache, slot_mapping, q_out,
-             dev_err)
-    cache = KvCache(P[7], P[8], st[0], st[1], st[2], pages, page, hkv, dim, code)
-    rc = load().attn_norm_rope_cache(P[0], qs, P[1], ks, P[2], vs, P[3], P[4], eps, P[5],
-                                     cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0,
-                                     P[6], cache, P[9], T, hq, code, P[10], os_, P[11],
-                                     _raw_stream(stream))
+    P = _raw(q, k, v, q_weight, k_weight, cos_sin, positions, slot_mapping, q_out, dev_err, *views)
+    rc = getattr(load(), fn)(P[0], qs, P[1], ks, P[2], vs, P[3], P[4], eps, P[5], cos_sin.shape[0],
+                             cos_sin.shape[1], 1 if interleaved else 0, P[6], cache(P[10:]), P[7],
+                             T, hq, code, P[8], os_, P[9], _raw_stream(stream))
     if rc != OK:
-        raise CConvError("attn_norm_rope_cache", rc)
+        raise CConvError(fn, rc)
+
+
+def attn_norm_rope_cache_q8(q, k, v, q_weight, k_weight, eps, cos_sin, positions, interleaved,
+                            k_cache, v_cache, k_scale, v_scale, slot_mapping, q_out, dev_err=None,
+                            stream=None):
+    """attn_norm_rope_cache into a cache in 8 bits (see attn_norm_rope_cache_q8 in cconv.h).
+
+    caches: float8_e4m3fn [pages, page_size, Hkv, D] views; k_scale, v_scale: uint8 (or
+    float8_e8m0fnu) [pages, page_size, Hkv] views, the biased exponents of the rows' powers of two.
+    """
+    if stream is None and (_lib or load()) and _fast is not None and _served(
+            "attn_norm_rope_cache_q8", _fast.attn_norm_rope_cache_q8(
+                q, k, v, q_weight, k_weight, eps, cos_sin, positions, interleaved, k_cache,
+                v_cache, k_scale, v_scale, slot_mapping, q_out, dev_err)):
+        return
+    s, st, ct = _cache_q8(k_cache, v_cache, k_scale, v_scale)
+    _norm_call("attn_norm_rope_cache_q8", q, k, v, q_weight, k_weight, eps, cos_sin, positions,
+               interleaved, slot_mapping, q_out, dev_err, stream, s[2], s[3],
+               (k_cache, v_cache, k_scale, v_scale), lambda P: _q8_struct(P, s, st, ct))
+
+
+def kv_cache_read_q8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out, v_out, dev_err=None,
+                     stream=None):
+    """Rows of a cache in 8 bits as fp32 or bf16 (see kv_cache_read_q8 in cconv.h).
+
+    caches and scales as attn_norm_rope_cache_q8; slot_mapping: int32 [T], negative to leave a row
+    as it is; k_out, v_out: [T, Hkv, D].
+    """
+    if stream is None and (_lib or load()) and _fast is not None and _served(
+            "kv_cache_read_q8", _fast.kv_cache_read_q8(
+                k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out, v_out, dev_err)):
+        return
+    _entries(slot_mapping, "slot_mapping", 0)
+    _error_word(dev_err)
+    s, st, ct = _cache_q8(k_cache, v_cache, k_scale, v_scale)
+    T, dtype = slot_mapping.shape[0], k_out.dtype
+    code = _call_dtype(dtype)
+    ks = _heads(k_out, "k_out", dtype, T, s[2], s[3])[2]
+    vs = _heads(v_out, "v_out", dtype, T, s[2], s[3])[2]
+    P = _raw(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out, v_out, dev_err)
+    rc = load().kv_cache_read_q8(_q8_struct(P, s, st, ct), P[4], T, code, P[5], ks,
+                                 P[6], vs, P[7], _raw_stream(stream))
+    if rc != OK:
+        raise CConvError("kv_cache_read_q8", rc)
 
 
 def attn_decode_workspace_bytes(num_seqs, n_spec, num_q_heads, num_kv_heads, head_dim):
@@ -621,13 +722,21 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, n_spec, scale, out, 
                 q, k_cache, v_cache, block_table, seq_lens, n_spec, scale, out, lse, workspace,
                 dev_err)):
         return
+    (pages, page, hkv, dim), st, code = _cache(k_cache, v_cache, q.dtype)
+    _decode_call("attn_decode", q, block_table, seq_lens, n_spec, scale, out, lse, workspace, dev_err,
+                 stream, hkv, dim, (k_cache, v_cache),
+                 lambda P: KvCache(P[0], P[1], st[0], st[1], st[2], pages, page, hkv, dim, code))
+
+
+def _decode_call(fn, q, block_table, seq_lens, n_spec, scale, out, lse, workspace, dev_err, stream,
+                 hkv, dim, views, cache):
+    """views: the cache's tensors; cache(addresses) -> its C struct."""
     _i32(block_table, "block_table")
     _entries(seq_lens, "seq_lens", 0)
     _error_word(dev_err)
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    dtype = q.dtype
-    (pages, page, hkv, dim), st, code = _cache(k_cache, v_cache, dtype)
+    dtype, code = q.dtype, _call_dtype(q.dtype)
     B = seq_lens.shape[0]
     rows, hq = B * (1 + n_spec), q.shape[1]
     qs = _heads(q, "q", dtype, rows, hq, dim)[2]
@@ -638,7 +747,7 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, n_spec, scale, out, 
     if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous()
                             or lse.shape[0] < rows or lse.shape[1:] != (hq,)):
         raise ValueError("lse must be contiguous float32 [rows, heads]")
-    P = _raw(q, k_cache, v_cache, block_table, seq_lens, out, lse, workspace, dev_err)
+    P = _raw(q, block_table, seq_lens, out, lse, workspace, dev_err, *views)
     if workspace is None:
         need = attn_decode_workspace_bytes(B, n_spec, hq, hkv, dim)
         if stream is None:
@@ -646,11 +755,28 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, n_spec, scale, out, 
         else:
             with torch.cuda.stream(stream):     # the call's stream owns it
                 workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        P[7] = workspace.data_ptr()
-    cache = KvCache(P[1], P[2], st[0], st[1], st[2], pages, page, hkv, dim, code)
-    rc = load().attn_decode(P[0], qs, cache, P[3], tst[0] if ts[0] > 1 else max(tst[0], ts[1]),
-                            ts[1], P[4], B, n_spec, hq, scale, code, P[5], os_, P[6], P[7],
-                            workspace.numel() * workspace.element_size(), P[8],
-                            _raw_stream(stream))
+        P[5] = workspace.data_ptr()
+    rc = getattr(load(), fn)(P[0], qs, cache(P[7:]), P[1],
+                             tst[0] if ts[0] > 1 else max(tst[0], ts[1]), ts[1], P[2], B, n_spec, hq,
+                             scale, code, P[3], os_, P[4], P[5],
+                             workspace.numel() * workspace.element_size(), P[6],
+                             _raw_stream(stream))
     if rc != OK:
-        raise CConvError("attn_decode", rc)
+        raise CConvError(fn, rc)
+
+
+def attn_decode_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, n_spec, scale, out,
+                   lse=None, workspace=None, dev_err=None, stream=None):
+    """attn_decode over a cache in 8 bits (see attn_decode_q8 in cconv.h).
+
+    caches and scales as attn_norm_rope_cache_q8; the rest, and the workspace, as attn_decode.
+    """
+    if stream is None and (_lib or load()) and _fast is not None and _served(
+            "attn_decode_q8", _fast.attn_decode_q8(
+                q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, n_spec, scale, out,
+                lse, workspace, dev_err)):
+        return
+    s, st, ct = _cache_q8(k_cache, v_cache, k_scale, v_scale)
+    _decode_call("attn_decode_q8", q, block_table, seq_lens, n_spec, scale, out, lse, workspace,
+                 dev_err, stream, s[2], s[3], (k_cache, v_cache, k_scale, v_scale),
+                 lambda P: _q8_struct(P, s, st, ct))
