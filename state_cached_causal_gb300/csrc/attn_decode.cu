@@ -463,9 +463,7 @@ int decode(AttnArgs& a, int D, bool q8, const void* q, int64_t q_row_stride,
     return CCONV_ERR_INVALID;
   const int sms = mix_sm_count();
   if (sms <= 0) return CCONV_ERR_LAUNCH;
-  const bool plain = dtype == CCONV_DTYPE_F32 || q8;
-  const AttnPlan p = plan(plain ? CCONV_DTYPE_F32 : CCONV_DTYPE_BF16, sms, num_seqs, 1 + n_spec,
-                          num_q_heads / a.Hkv, a.Hkv, D);
+  const AttnPlan p = plan(dtype, sms, num_seqs, 1 + n_spec, num_q_heads / a.Hkv, a.Hkv, D);
   if (!workspace || !mix_aligned16(workspace) || workspace_bytes < p.bytes)
     return CCONV_ERR_INVALID;
   a.q = static_cast<const char*>(q);
@@ -491,7 +489,7 @@ int decode(AttnArgs& a, int D, bool q8, const void* q, int64_t q_row_stride,
   // positions that follow one another in memory come together, up to 1 KB or four
   a.group_shift = 0;
   if (a.s_tok == (int64_t)p.hw * D && (p.hw == 1 || a.s_head == D))
-    while (a.group_shift < 2 && (p.hw * D * 2 << a.group_shift) < 1024 &&
+    while (a.group_shift < 2 && (p.hw * D * (q8 ? 1 : 2) << a.group_shift) < 1024 &&
            a.page_size % (2 << a.group_shift) == 0)
       ++a.group_shift;
   a.rblocks = p.rblocks;
@@ -505,8 +503,8 @@ int decode(AttnArgs& a, int D, bool q8, const void* q, int64_t q_row_stride,
     err = q8 ? launch_attn_d<float, true>(a, D, p.grid, st)
              : launch_attn_d<float, false>(a, D, p.grid, st);
   else
-    err = q8 ? launch_attn_d<__nv_bfloat16, true>(a, D, p.grid, st)
-             : attn_launch_mma(a, D, p.grid, st);
+    err = q8 ? attn_launch_mma_q8(a, D, p.grid, false, st)
+             : attn_launch_mma(a, D, p.grid, false, st);
   if (err != cudaSuccess) return CCONV_ERR_LAUNCH;
   if (dtype == CCONV_DTYPE_F32)
     err = D == 64 ? launch_join<float, 64>(a, st) : D == 128 ? launch_join<float, 128>(a, st)

@@ -44,22 +44,64 @@ struct AttnArgs {
   int32_t* dev_err;
   const uint8_t *ksc, *vsc;   // scales of a cache in 8 bits
   int64_t c_page, c_tok, c_head;
+  const int32_t *cu_groups, *prefix_lens;   // of attn_decode_shared (attn_shared.cu)
+  int32_t groups;
 };
 
-// Blocks of the bf16 kernel that an SM holds at once, by their registers and
+// Blocks of the bf16 kernels that an SM holds at once, by their registers and
 // shared memory (50 to 218 KB).
-inline int attn_mma_blocks(int D, int rows) {
+__host__ __device__ constexpr int attn_mma_blocks(int D, int rows) {
   return D * rows >= 4096 ? 1 : D * rows >= 2048 ? 2 : 3;
 }
 
-// Tiles of request b: at least one (an empty request still writes its rows).
-// len < 0 marks a request that is skipped.
+// Length of request b; -1 for one that is skipped.
 __device__ __forceinline__ int attn_len(const AttnArgs& a, int b) {
   const int n = a.seq_lens[b];
   return (n < 0 || n > (int64_t)a.table_width * a.page_size) ? -1 : n;
 }
+
+// attn_decode_shared: the group that request b is of (-1: none), and the prefix of
+// group g (0 where its bounds or its prefix are out of range).
+__device__ __forceinline__ int attn_group(const AttnArgs& a, int b) {
+  int lo = 0, hi = a.groups;              // the last group that begins at b or before
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (a.cu_groups[mid] <= b)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  const int g = lo - 1;
+  return g >= 0 && a.cu_groups[g + 1] > b ? g : -1;
+}
+__device__ __forceinline__ bool attn_group_ok(const AttnArgs& a, int first, int end, int prefix) {
+  return first >= 0 && first <= end && end <= a.B && prefix >= 0 &&
+         prefix <= (int64_t)a.table_width * a.page_size;
+}
+__device__ __forceinline__ int attn_prefix(const AttnArgs& a, int g) {
+  const int first = a.cu_groups[g], end = a.cu_groups[g + 1], p = a.prefix_lens[g];
+  return attn_group_ok(a, first, end, p) ? p : 0;
+}
+// The positions of request b that the shared kernel takes (the rest begins there):
+// its group's prefix if all its rows see the whole of that, else none.
+__device__ __forceinline__ int attn_start(const AttnArgs& a, int b) {
+  const int g = attn_group(a, b);
+  if (g < 0) return 0;
+  const int p = attn_prefix(a, g);
+  return attn_len(a, b) - (a.q_len - 1) >= p ? p : 0;
+}
+
+// The position that tile 0 of request b begins at, and its tiles: at least one (an
+// empty request still writes its rows). A copy of several positions begins at a
+// multiple of them.
+template <bool SHARED>
+__device__ __forceinline__ int attn_base(const AttnArgs& a, int start) {
+  return SHARED ? start >> a.group_shift << a.group_shift : 0;
+}
+template <bool SHARED>
 __device__ __forceinline__ int attn_tiles(const AttnArgs& a, int b, int tile) {
-  const int n = attn_len(a, b);
+  int n = attn_len(a, b);
+  if (SHARED && n > 0) n -= attn_base<SHARED>(a, attn_start(a, b));
   return n <= 0 ? 1 : (n + tile - 1) / tile;
 }
 
@@ -74,14 +116,14 @@ struct AttnRun {
 // Splits the line over the grid. Every thread of the block calls it; `sm` is
 // shared scratch. Each thread counts a
 // run of requests, and a scan over the threads places the block's start.
-template <int THREADS>
+template <int THREADS, bool SHARED = false>
 __device__ __forceinline__ bool attn_split(const AttnArgs& a, int tile, int64_t (&sm)[THREADS + 4],
                                            AttnRun& r) {
   const int tid = threadIdx.x;
   const int per = (a.B + THREADS - 1) / THREADS;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += attn_tiles(a, b, tile);
+  for (int b = b0; b < b1; ++b) mine += attn_tiles<SHARED>(a, b, tile);
   int64_t incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -110,7 +152,7 @@ __device__ __forceinline__ bool attn_split(const AttnArgs& a, int tile, int64_t 
     int64_t before = incl - mine;
     int b = b0;
     for (;; ++b) {
-      const int n = attn_tiles(a, b, tile);
+      const int n = attn_tiles<SHARED>(a, b, tile);
       if (r.p < (before + n) * units) break;
       before += n;
     }
@@ -124,28 +166,32 @@ __device__ __forceinline__ bool attn_split(const AttnArgs& a, int tile, int64_t 
 }
 
 // The block of the grid whose run holds this tile of the line.
-__device__ __forceinline__ int attn_block_of(int64_t tile, const AttnRun& r) {
-  return (int)(((tile + 1) * r.grid - 1) / r.total);
+__device__ __forceinline__ int attn_block_of(int64_t tile, int64_t total, int64_t grid) {
+  return (int)(((tile + 1) * grid - 1) / total);
 }
 
-// One segment: unit `unit` of request b, tiles [j0, j1) of `tiles`.
+// One segment: unit `unit` of request b, tiles [j0, j1) of `tiles`; positions from
+// `start` on, tile 0 beginning at `base`.
 struct AttnSeg {
-  int b, unit, len, tiles, j0, j1;
+  int b, unit, len, tiles, j0, j1, start, base;
   bool whole;
   int64_t line;         // place of the unit's tile 0 on the line
 };
+template <bool SHARED = false>
 __device__ __forceinline__ AttnSeg attn_segment(const AttnArgs& a, int tile, const AttnRun& r) {
   AttnSeg s;
   const int64_t units = a.units;
   s.b = r.b;
   s.len = attn_len(a, r.b);
-  s.tiles = attn_tiles(a, r.b, tile);
+  s.start = SHARED && s.len > 0 ? attn_start(a, r.b) : 0;
+  s.base = attn_base<SHARED>(a, s.start);
+  s.tiles = s.len - s.base <= 0 ? 1 : (s.len - s.base + tile - 1) / tile;
   const int64_t rel = r.p - r.before * units;
   s.unit = (int)(rel / s.tiles);
   s.j0 = (int)(rel % s.tiles);
   s.j1 = (int)min((int64_t)s.tiles, s.j0 + (r.end - r.p));
   s.line = r.before * units + (int64_t)s.unit * s.tiles;
-  s.whole = s.j0 == 0 && s.j1 == s.tiles;
+  s.whole = !SHARED && s.j0 == 0 && s.j1 == s.tiles;
   return s;
 }
 __device__ __forceinline__ void attn_advance(const AttnArgs& a, const AttnSeg& s, AttnRun& r) {
@@ -156,17 +202,22 @@ __device__ __forceinline__ void attn_advance(const AttnArgs& a, const AttnSeg& s
   }
 }
 
-// Where the block's part of a cut segment goes (see above), and the note for
-// the join, written by the block that holds the unit's first tile.
+// Where the block's part of a cut segment goes (see above; attn_decode_shared joins
+// every segment: from one to the next on the line the unit's number or the block's
+// rises, so that their sum is a place of its own), and the note for the join,
+// written by the block that holds the unit's first tile.
+template <bool SHARED = false>
 __device__ __forceinline__ float* attn_part(const AttnArgs& a, const AttnSeg& s, int D) {
-  return a.part + ((int64_t)blockIdx.x * 2 + (s.j0 == 0 ? 1 : 0)) * a.hw * a.rows * (D + 2);
+  const int64_t place = SHARED ? (int64_t)s.b * a.units + s.unit + blockIdx.x
+                               : (int64_t)blockIdx.x * 2 + (s.j0 == 0 ? 1 : 0);
+  return a.part + place * a.hw * a.rows * (D + 2);
 }
 __device__ __forceinline__ void attn_note(const AttnArgs& a, const AttnSeg& s, const AttnRun& r) {
   if (s.j0 != 0) return;
   int32_t* m = a.meta + ((int64_t)s.b * a.units + s.unit) * 2;
   const bool cut = !s.whole && s.len >= 0;
-  m[0] = cut ? attn_block_of(s.line, r) : -1;
-  m[1] = cut ? attn_block_of(s.line + s.tiles - 1, r) : -1;
+  m[0] = cut ? attn_block_of(s.line, r.total, r.grid) : -1;
+  m[1] = cut ? attn_block_of(s.line + s.tiles - 1, r.total, r.grid) : -1;
 }
 
 // Whether blocks c0 to c1 hold the parts of a cut unit: not if it was whole or
@@ -175,7 +226,26 @@ __host__ __device__ inline bool attn_joins(int32_t c0, int32_t c1, int32_t grid)
   return c0 >= 0 && c0 <= c1 && c1 < grid;
 }
 
-// bf16 kernel (attn_mma.cu)
-cudaError_t attn_launch_mma(const AttnArgs& a, int D, int grid, cudaStream_t st);
+// bf16 kernels over a cache in bf16 (attn_mma.cu) and in 8 bits (attn_mma_q8.cu); with
+// `shared` they take each request from attn_start on, and all segments are joined.
+cudaError_t attn_launch_mma(const AttnArgs& a, int D, int grid, bool shared, cudaStream_t st);
+cudaError_t attn_launch_mma_q8(const AttnArgs& a, int D, int grid, bool shared, cudaStream_t st);
+
+// Launches a kernel of the shared form beside the end of the one before it.
+template <typename K, typename A>
+cudaError_t attn_launch_beside(K kernel, const A& a, int more, int grid, int threads, int smem,
+                               cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, more);
+}
 
 }  // namespace cconv

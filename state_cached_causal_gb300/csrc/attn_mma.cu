@@ -105,11 +105,19 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, int phase, int32_t* err)
 // took 5 us of 340; it ends with copies on their way, which the others wait for.)
 __device__ __noinline__ void settle(uint64_t* full, int stages, int st, int ph, int32_t* err) {
   for (int i = 0; i < stages; ++i) wait_bar(&full[i], i < st ? ph ^ 1 : ph, err);
+  asm volatile("griddepcontrol.wait;" ::: "memory");    // (as after_prefix)
+}
+
+// The shared form starts beside the end of the kernel that takes the prefixes and
+// needs nothing of it, but is not over before it: what follows joins both. (One block
+// waits; block 0 always has a run.)
+__device__ __forceinline__ void after_prefix() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // MT row tiles of 16. Q stays in registers where it fits beside the sums, else
 // in shared memory.
-template <int D, int MT>
+template <int D, int MT, bool SHARED>
 __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, const int stages) {
   constexpr bool kQRegs = MT == 1;
   constexpr int kQPitch = D * 2 + 16;
@@ -137,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
   }
   AttnRun run;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (!attn_split<kThreads>(a, tpos, scan, run)) return;
+  if (!attn_split<kThreads, SHARED>(a, tpos, scan, run)) return;
   const int rows_all = a.G * a.q_len;
   const float sl2 = a.scale * 1.4426950408889634f;
 
@@ -154,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
     const bool notes = isv == 0 && piece == 0;
     int st = 0, ph = 1;               // (the first round's places are free)
     while (run.p < run.end) {
-      const AttnSeg s = attn_segment(a, tpos, run);
+      const AttnSeg s = attn_segment<SHARED>(a, tpos, run);
       attn_advance(a, s, run);
       const int32_t* tab = a.table + (int64_t)s.b * a.table_rs;
       const char* const src0 =
@@ -165,10 +173,10 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
         return in && pos < s.len ? tab[a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size]
                                  : -1;
       };
-      int ahead = look(s.j0 * tpos + pl0, pl0 < tpos);
+      int ahead = look(s.base + s.j0 * tpos + pl0, pl0 < tpos);
       for (int j = s.j0; j < s.j1; ++j) {
         const uint32_t place = st * 2 * half_stage;
-        const int t0 = j * tpos;
+        const int t0 = s.base + j * tpos;
         int pl = pl0;
         for (int p = 0; p < tpos; p += dpl, pl += dpl) {       // (p: of lane 0)
           const int pos = t0 + pl, page = ahead;
@@ -183,17 +191,22 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
           if (p == 0 && !wait_bar(&empty[st], ph, a.dev_err))
             return settle(full, stages, st, ph, a.dev_err);
           if (in) {
+            // (positions before the request's first one are left out, too)
+            const int skip = SHARED ? min(max(s.start - pos, 0), held) : 0;
             if (notes)
-              for (int k = 0; k < group; ++k) there[st][pl + k] = k < held;
+              for (int k = 0; k < group; ++k) there[st][pl + k] = k >= skip && k < held;
             unsigned char* const dst = dst0 + place + off(pl);
-            if (held > 0) {
+            if (held > skip) {
               const int tok = a.page_shift >= 0 ? pos & (a.page_size - 1) : pos % a.page_size;
-              mbar_expect(&full[st], held * bytes);
-              bulk_load(dst, src0 + (page * a.s_page + tok * a.s_tok) * 2, held * bytes, &full[st]);
+              const uint32_t n = (held - skip) * bytes;
+              mbar_expect(&full[st], n);
+              bulk_load(dst + skip * bytes,
+                        src0 + (page * a.s_page + (tok + skip) * a.s_tok) * 2, n, &full[st]);
             }
-            if (isv && held < group) {
-              for (uint32_t i = held * bytes; i < group * bytes; i += 16)
-                *reinterpret_cast<uint4*>(dst + i) = make_uint4(0u, 0u, 0u, 0u);
+            if (isv && held - skip < group) {
+              for (uint32_t i = 0; i < group * bytes; i += 16)
+                if (i < skip * bytes || i >= held * bytes)
+                  *reinterpret_cast<uint4*>(dst + i) = make_uint4(0u, 0u, 0u, 0u);
               fence_proxy_async();      // before a later copy into the same place
             }
           }
@@ -203,6 +216,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
         if (++st == stages) st = 0, ph ^= 1;
       }
     }
+    if (SHARED && blockIdx.x == 0) after_prefix();
     return;
   }
   int stage = 0, phase = 0, meets = 0;
@@ -214,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
   };
 
   while (run.p < run.end) {
-    const AttnSeg sg = attn_segment(a, tpos, run);
+    const AttnSeg sg = attn_segment<SHARED>(a, tpos, run);
     if (tid == 0) {
       attn_note(a, sg, run);
       if (sg.len < 0) flag_error(a.dev_err, CCONV_DERR_SEQ_LEN);
@@ -298,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[mt][i >> 2][i & 3] *= sl2;
       // ---- masks, running maximum, weights
-      const int pos0 = j * tpos + p0;              // the warp's first position
+      const int pos0 = sg.base + j * tpos + p0;    // the warp's first position
       // Draft tokens' positions are hidden from the rows before them by a weight
       // of zero, which an infinity or NaN among their values would get through:
       // such values (`wild`) are kept out of the product and added to the rows
@@ -465,7 +479,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
       if (!meet()) return settle(full, stages, stage, phase, a.dev_err);
     }
     if (sg.len < 0 || warp % per != 0) continue;
-    float* const part = attn_part(a, sg, D) + (warp / per) * (MT * 16) * (D + 2);
+    float* const part = attn_part<SHARED>(a, sg, D) + (warp / per) * (MT * 16) * (D + 2);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -500,7 +514,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a, co
 
 static_assert(kTile == 16 * kWarps, "a warp takes 16 rows");
 
-template <int D, int MT>
+template <int D, int MT, bool SHARED>
 cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
   // the ring, and behind it the joins (none with a head a warp) or the warps' Q
   const int tpos = kTile / a.hw, stage = 2 * (tpos * a.hw * D * 2 + (tpos >> a.group_shift) * 16);
@@ -513,19 +527,30 @@ cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
   while (stages > 2 && stages * stage + std::max(join, q) > most) --stages;
   const int smem = stages * stage + std::max(join, q);
   static std::atomic<uint64_t> full;
-  const cudaError_t e = mix_full_smem(reinterpret_cast<const void*>(attn_mma_kernel<D, MT>), full);
+  const void* const f = reinterpret_cast<const void*>(attn_mma_kernel<D, MT, SHARED>);
+  const cudaError_t e = mix_full_smem(f, full);
   if (e != cudaSuccess) return e;
-  attn_mma_kernel<D, MT><<<grid, kThreads, smem, st>>>(a, stages);
-  return cudaGetLastError();
+  if constexpr (!SHARED) {
+    attn_mma_kernel<D, MT, SHARED><<<grid, kThreads, smem, st>>>(a, stages);
+    return cudaGetLastError();
+  } else {
+    return attn_launch_beside(attn_mma_kernel<D, MT, SHARED>, a, stages, grid, kThreads, smem, st);
+  }
+}
+
+template <bool SHARED>
+cudaError_t launch_d(const AttnArgs& a, int D, int grid, cudaStream_t st) {
+  if (a.rows == 16)
+    return D == 64    ? launch<64, 1, SHARED>(a, grid, st)
+           : D == 128 ? launch<128, 1, SHARED>(a, grid, st)
+                      : launch<256, 1, SHARED>(a, grid, st);
+  return D == 64 ? launch<64, 2, SHARED>(a, grid, st) : launch<128, 2, SHARED>(a, grid, st);
 }
 
 }  // namespace
 
-cudaError_t attn_launch_mma(const AttnArgs& a, int D, int grid, cudaStream_t st) {
-  if (a.rows == 16)
-    return D == 64 ? launch<64, 1>(a, grid, st) : D == 128 ? launch<128, 1>(a, grid, st)
-                                                          : launch<256, 1>(a, grid, st);
-  return D == 64 ? launch<64, 2>(a, grid, st) : launch<128, 2>(a, grid, st);
+cudaError_t attn_launch_mma(const AttnArgs& a, int D, int grid, bool shared, cudaStream_t st) {
+  return shared ? launch_d<true>(a, D, grid, st) : launch_d<false>(a, D, grid, st);
 }
 
 }  // namespace cconv
