@@ -124,8 +124,10 @@ enum {
                                   slot_mapping[t] out of range           */
   CCONV_DERR_PAGE = 128,       /* attn_decode: a block_table entry that a
                                   request's length reaches is out of range */
-  CCONV_DERR_SEQ_LEN = 256     /* attn_decode: seq_lens[s] negative or beyond
+  CCONV_DERR_SEQ_LEN = 256,    /* attn_decode: seq_lens[s] negative or beyond
                                   the block table                        */
+  CCONV_DERR_GROUP = 512       /* attn_decode_shared: cu_groups or prefix_lens
+                                  of a group out of range                */
 };
 
 /* [slot, channel, column] view of a conv-state pool (element strides). */
@@ -704,6 +706,59 @@ CCONV_API int attn_decode_q8(const void* q, int64_t q_row_stride, kv_cache_q8_t 
                    int32_t n_spec, int32_t num_q_heads, float scale, int32_t dtype, void* out,
                    int64_t out_row_stride, float* lse, void* workspace, int64_t workspace_bytes,
                    int32_t* dev_err, cconv_stream_t stream);
+
+/*
+ * attn_decode_shared -- attn_decode for requests that share their first positions
+ * in groups (one document or one set of instructions before all of them, several
+ * samples of one context): a group's prefix is read, and multiplied, once for all
+ * its requests. The results are those of attn_decode.
+ *
+ *   cu_groups    int32 [num_groups + 1]: group g holds the requests cu_groups[g] to
+ *                cu_groups[g + 1] - 1 (none of them: an empty group). Requests
+ *                before the first group and behind the last are attended as by
+ *                attn_decode.
+ *   prefix_lens  int32 [num_groups]: the first prefix_lens[g] positions are the
+ *                same for all of group g, in the same pages or in copies: those of
+ *                the block table of its first request are read. Any length,
+ *                whole pages or not; 0 for no prefix.
+ *   seq_lens     as attn_decode, the prefix included. A request of which some row
+ *                does not see the whole prefix (seq_lens[s] - n_spec <
+ *                prefix_lens[g]) attends over its own block table alone.
+ *   num_groups   0..num_seqs; with 0 cu_groups and prefix_lens may be NULL
+ *   workspace    attn_decode_shared_workspace_bytes() of device memory, 16-byte
+ *                aligned; holds nothing between calls, and calls that may overlap
+ *                need one each
+ *   dtype        CCONV_DTYPE_BF16 (fp32: CCONV_ERR_UNSUPPORTED)
+ * Other arguments and errors as attn_decode. A group that is out of range (bounds
+ * that fall or leave the batch, a prefix that is negative or longer than the block
+ * table) sets CCONV_DERR_GROUP and counts as one without a prefix; groups that
+ * overlap leave the rows of their requests unwritten where they have more rows than
+ * the call, with CCONV_DERR_GROUP.
+ */
+CCONV_API int attn_decode_shared(const void* q, int64_t q_row_stride, kv_cache_t cache,
+                       const int32_t* block_table, int64_t block_table_row_stride,
+                       int32_t table_width, const int32_t* seq_lens, int32_t num_seqs,
+                       const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
+                       int32_t n_spec, int32_t num_q_heads, float scale, int32_t dtype, void* out,
+                       int64_t out_row_stride, float* lse, void* workspace,
+                       int64_t workspace_bytes, int32_t* dev_err, cconv_stream_t stream);
+
+/* attn_decode_shared over a cache in 8 bits: the values that its bytes and scales
+ * stand for, which the prefix takes as bf16 (exactly). */
+CCONV_API int attn_decode_shared_q8(const void* q, int64_t q_row_stride, kv_cache_q8_t cache,
+                          const int32_t* block_table, int64_t block_table_row_stride,
+                          int32_t table_width, const int32_t* seq_lens, int32_t num_seqs,
+                          const int32_t* cu_groups, const int32_t* prefix_lens,
+                          int32_t num_groups, int32_t n_spec, int32_t num_q_heads, float scale,
+                          int32_t dtype, void* out, int64_t out_row_stride, float* lse,
+                          void* workspace, int64_t workspace_bytes, int32_t* dev_err,
+                          cconv_stream_t stream);
+
+/* Workspace of an attn_decode_shared call of these sizes on the current device; a
+ * negative status where they are out of range. */
+CCONV_API int64_t attn_decode_shared_workspace_bytes(int32_t num_seqs, int32_t num_groups,
+                                                     int32_t n_spec, int32_t num_q_heads,
+                                                     int32_t num_kv_heads, int32_t head_dim);
 
 /* Static English text for a status code. */
 CCONV_API const char* cconv_status_string(int status);

@@ -20,8 +20,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kTile = 32;
-constexpr int kRows = 8;          // query rows of a block
-constexpr int kMaxGrid = 2048;    // blocks of the split kernels
+constexpr int kRows = kAttnPlainRows;
+constexpr int kMaxGrid = kAttnMaxGrid;
 
 template <typename T, int D>
 struct AttnSmem {
@@ -409,94 +409,27 @@ cudaError_t launch_attn_d(const AttnArgs& a, int D, int grid, cudaStream_t st) {
                     : launch_attn<T, 256, Q8>(a, grid, st);
 }
 
-struct AttnPlan {
-  int hw, rblocks, rows, units, grid;
-  int64_t meta_bytes, bytes;
-};
-AttnPlan plan(int dtype, int sms, int64_t B, int q_len, int G, int Hkv, int D) {
-  AttnPlan p;
-  const int rows = G * q_len;
-  p.hw = 1;
-  if (dtype == CCONV_DTYPE_F32) {
-    p.rows = kRows;
-    p.grid = sms * (D == 64 ? 7 : D == 128 ? 5 : 2);   // blocks that an SM holds at once
-  } else {
-    // row tiles whose sums fit in registers
-    p.rows = rows <= 16 || D == 256 ? 16 : 32;
-    p.hw = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
-    p.grid = sms * attn_mma_blocks(D, p.rows);
-  }
-  p.grid = std::min(p.grid, kMaxGrid);
-  p.rblocks = (rows + p.rows - 1) / p.rows;
-  p.units = Hkv / p.hw * p.rblocks;
-  p.meta_bytes = (B * p.units * 8 + 15) / 16 * 16;
-  p.bytes = p.meta_bytes + (int64_t)p.grid * 2 * p.hw * p.rows * (D + 2) * 4;
-  return p;
-}
-
-int check_sizes(int32_t num_seqs, int32_t n_spec, int32_t Hq, int32_t Hkv, int32_t D) {
-  if (num_seqs < 0 || n_spec < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0)
-    return CCONV_ERR_INVALID;
-  if (n_spec > kMaxSpec || (int64_t)(Hq / Hkv) * (1 + n_spec) > 64 ||
-      (D != 64 && D != 128 && D != 256))
-    return CCONV_ERR_UNSUPPORTED;
-  if ((int64_t)num_seqs * Hkv * 128 > INT32_MAX || (int64_t)num_seqs * (1 + n_spec) > INT32_MAX)
-    return CCONV_ERR_INVALID;
-  return CCONV_OK;
-}
-
 // What both entry points check and do; a's cache is set.
 int decode(AttnArgs& a, int D, bool q8, const void* q, int64_t q_row_stride,
            const int32_t* block_table, int64_t block_table_row_stride, int32_t table_width,
            const int32_t* seq_lens, int32_t num_seqs, int32_t n_spec, int32_t num_q_heads,
            float scale, int32_t dtype, void* out, int64_t out_row_stride, float* lse,
            void* workspace, int64_t workspace_bytes, int32_t* dev_err, cconv_stream_t stream) {
-  const int rc = check_sizes(num_seqs, n_spec, num_q_heads, a.Hkv, D);
+  const int rc = attn_check_sizes(num_seqs, n_spec, num_q_heads, a.Hkv, D);
   if (rc != CCONV_OK) return rc;
   if (num_seqs == 0) return CCONV_OK;
-  const int V = 16 / mix_dtype_bytes(dtype);
-  if (!mix_rows_ok(q, q_row_stride, (int64_t)num_q_heads * D, V) ||
-      !mix_rows_ok(out, out_row_stride, (int64_t)num_q_heads * D, V) || !seq_lens ||
-      table_width < 0 || (table_width > 0 && !block_table) ||
-      block_table_row_stride < table_width ||
-      (int64_t)table_width * a.page_size > INT32_MAX - 1024)
+  if (!attn_rows_ok(a, D, dtype, q, q_row_stride, out, out_row_stride, num_q_heads, block_table,
+                    block_table_row_stride, table_width, seq_lens))
     return CCONV_ERR_INVALID;
   const int sms = mix_sm_count();
   if (sms <= 0) return CCONV_ERR_LAUNCH;
-  const AttnPlan p = plan(dtype, sms, num_seqs, 1 + n_spec, num_q_heads / a.Hkv, a.Hkv, D);
+  const AttnPlan p = attn_plan(dtype, sms, num_seqs, 1 + n_spec, num_q_heads / a.Hkv, a.Hkv, D);
   if (!workspace || !mix_aligned16(workspace) || workspace_bytes < p.bytes)
     return CCONV_ERR_INVALID;
-  a.q = static_cast<const char*>(q);
-  a.q_rs = q_row_stride;
-  a.page_shift = -1;
-  for (int s = 0; s < 31; ++s)
-    if (a.page_size == 1 << s) a.page_shift = s;
-  a.table = block_table;
-  a.table_rs = block_table_row_stride;
-  a.table_width = table_width;
-  a.seq_lens = seq_lens;
-  a.B = num_seqs;
-  a.q_len = 1 + n_spec;
-  a.Hq = num_q_heads;
-  a.G = num_q_heads / a.Hkv;
-  a.scale = scale;
-  a.out = static_cast<char*>(out);
-  a.out_rs = out_row_stride;
-  a.lse = lse;
+  attn_fill(a, p, D, q8 ? 1 : 2, q, q_row_stride, block_table, block_table_row_stride, table_width,
+            seq_lens, num_seqs, n_spec, num_q_heads, scale, out, out_row_stride, lse, dev_err);
   a.meta = static_cast<int32_t*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.meta_bytes);
-  a.hw = p.hw;
-  // positions that follow one another in memory come together, up to 1 KB or four
-  a.group_shift = 0;
-  if (a.s_tok == (int64_t)p.hw * D && (p.hw == 1 || a.s_head == D))
-    while (a.group_shift < 2 && (p.hw * D * (q8 ? 1 : 2) << a.group_shift) < 1024 &&
-           a.page_size % (2 << a.group_shift) == 0)
-      ++a.group_shift;
-  a.rblocks = p.rblocks;
-  a.rows = p.rows;
-  a.units = p.units;
-  a.grid = p.grid;
-  a.dev_err = dev_err;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t err;
   if (dtype == CCONV_DTYPE_F32)
@@ -516,17 +449,6 @@ int decode(AttnArgs& a, int D, bool q8, const void* q, int64_t q_row_stride,
   return err == cudaSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
 }
 
-template <typename C>
-AttnArgs cache_args(const C& cache) {
-  AttnArgs a = {};
-  a.kc = static_cast<const char*>(cache.k);
-  a.vc = static_cast<const char*>(cache.v);
-  a.s_page = cache.s_page, a.s_tok = cache.s_token, a.s_head = cache.s_head;
-  a.num_pages = cache.num_pages, a.page_size = cache.page_size;
-  a.Hkv = cache.num_kv_heads;
-  return a;
-}
-
 }  // namespace
 }  // namespace cconv
 
@@ -535,13 +457,13 @@ using namespace cconv;
 extern "C" int64_t attn_decode_workspace_bytes(int32_t num_seqs, int32_t n_spec,
                                                int32_t num_q_heads, int32_t num_kv_heads,
                                                int32_t head_dim) {
-  const int rc = check_sizes(num_seqs, n_spec, num_q_heads, num_kv_heads, head_dim);
+  const int rc = attn_check_sizes(num_seqs, n_spec, num_q_heads, num_kv_heads, head_dim);
   if (rc != CCONV_OK) return rc;
   const int sms = mix_sm_count();
   if (sms <= 0) return CCONV_ERR_LAUNCH;
   int64_t most = 0;
   for (const int dtype : {CCONV_DTYPE_F32, CCONV_DTYPE_BF16})
-    most = std::max(most, plan(dtype, sms, num_seqs, 1 + n_spec, num_q_heads / num_kv_heads,
+    most = std::max(most, attn_plan(dtype, sms, num_seqs, 1 + n_spec, num_q_heads / num_kv_heads,
                                num_kv_heads, head_dim).bytes);
   return most;
 }
@@ -555,7 +477,7 @@ extern "C" int attn_decode(const void* q, int64_t q_row_stride, kv_cache_t cache
   if (mix_dtype_bytes(dtype) == 0) return CCONV_ERR_INVALID;
   const int rc = mix_check_cache(cache, dtype);
   if (rc != CCONV_OK) return rc;
-  AttnArgs a = cache_args(cache);
+  AttnArgs a = attn_cache_args(cache);
   return decode(a, cache.head_dim, false, q, q_row_stride, block_table, block_table_row_stride,
                 table_width, seq_lens, num_seqs, n_spec, num_q_heads, scale, dtype, out,
                 out_row_stride, lse, workspace, workspace_bytes, dev_err, stream);
@@ -570,7 +492,7 @@ extern "C" int attn_decode_q8(const void* q, int64_t q_row_stride, kv_cache_q8_t
   if (mix_dtype_bytes(dtype) == 0) return CCONV_ERR_INVALID;
   const int rc = mix_check_cache_q8(cache);
   if (rc != CCONV_OK) return rc;
-  AttnArgs a = cache_args(cache);
+  AttnArgs a = attn_cache_args(cache);
   a.ksc = cache.k_scale;
   a.vsc = cache.v_scale;
   a.c_page = cache.c_page, a.c_tok = cache.c_token, a.c_head = cache.c_head;

@@ -231,6 +231,108 @@ __host__ __device__ inline bool attn_joins(int32_t c0, int32_t c1, int32_t grid)
 cudaError_t attn_launch_mma(const AttnArgs& a, int D, int grid, bool shared, cudaStream_t st);
 cudaError_t attn_launch_mma_q8(const AttnArgs& a, int D, int grid, bool shared, cudaStream_t st);
 
+// ---- host side ----------------------------------------------------------------
+
+constexpr int kAttnPlainRows = 8;     // query rows of a block of the plain kernel
+constexpr int kAttnMaxGrid = 2048;    // blocks of the split kernels
+
+struct AttnPlan {
+  int hw, rblocks, rows, units, grid;
+  int64_t meta_bytes, bytes;
+};
+inline AttnPlan attn_plan(int dtype, int sms, int64_t B, int q_len, int G, int Hkv, int D) {
+  AttnPlan p;
+  const int rows = G * q_len;
+  p.hw = 1;
+  if (dtype == CCONV_DTYPE_F32) {
+    p.rows = kAttnPlainRows;
+    p.grid = sms * (D == 64 ? 7 : D == 128 ? 5 : 2);   // blocks that an SM holds at once
+  } else {
+    // row tiles whose sums fit in registers
+    p.rows = rows <= 16 || D == 256 ? 16 : 32;
+    p.hw = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
+    p.grid = sms * attn_mma_blocks(D, p.rows);
+  }
+  p.grid = std::min(p.grid, kAttnMaxGrid);
+  p.rblocks = (rows + p.rows - 1) / p.rows;
+  p.units = Hkv / p.hw * p.rblocks;
+  p.meta_bytes = (B * p.units * 8 + 15) / 16 * 16;
+  p.bytes = p.meta_bytes + (int64_t)p.grid * 2 * p.hw * p.rows * (D + 2) * 4;
+  return p;
+}
+
+inline int attn_check_sizes(int32_t num_seqs, int32_t n_spec, int32_t Hq, int32_t Hkv, int32_t D) {
+  if (num_seqs < 0 || n_spec < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0)
+    return CCONV_ERR_INVALID;
+  if (n_spec > kMaxSpec || (int64_t)(Hq / Hkv) * (1 + n_spec) > 64 ||
+      (D != 64 && D != 128 && D != 256))
+    return CCONV_ERR_UNSUPPORTED;
+  if ((int64_t)num_seqs * Hkv * 128 > INT32_MAX || (int64_t)num_seqs * (1 + n_spec) > INT32_MAX)
+    return CCONV_ERR_INVALID;
+  return CCONV_OK;
+}
+
+template <typename C>
+AttnArgs attn_cache_args(const C& cache) {
+  AttnArgs a = {};
+  a.kc = static_cast<const char*>(cache.k);
+  a.vc = static_cast<const char*>(cache.v);
+  a.s_page = cache.s_page, a.s_tok = cache.s_token, a.s_head = cache.s_head;
+  a.num_pages = cache.num_pages, a.page_size = cache.page_size;
+  a.Hkv = cache.num_kv_heads;
+  return a;
+}
+
+inline bool attn_rows_ok(const AttnArgs& a, int D, int dtype, const void* q, int64_t q_row_stride,
+                         const void* out, int64_t out_row_stride, int32_t num_q_heads,
+                         const int32_t* block_table, int64_t block_table_row_stride,
+                         int32_t table_width, const int32_t* seq_lens) {
+  const int V = 16 / mix_dtype_bytes(dtype);
+  return mix_rows_ok(q, q_row_stride, (int64_t)num_q_heads * D, V) &&
+         mix_rows_ok(out, out_row_stride, (int64_t)num_q_heads * D, V) && seq_lens &&
+         table_width >= 0 && (table_width == 0 || block_table) &&
+         block_table_row_stride >= table_width &&
+         (int64_t)table_width * a.page_size <= INT32_MAX - 1024;
+}
+
+// Everything but the cache and the workspace; `bytes` of a cached value of the bf16
+// kernels.
+inline void attn_fill(AttnArgs& a, const AttnPlan& p, int D, int bytes, const void* q,
+                      int64_t q_row_stride, const int32_t* block_table,
+                      int64_t block_table_row_stride, int32_t table_width, const int32_t* seq_lens,
+                      int32_t num_seqs, int32_t n_spec, int32_t num_q_heads, float scale,
+                      void* out, int64_t out_row_stride, float* lse, int32_t* dev_err) {
+  a.q = static_cast<const char*>(q);
+  a.q_rs = q_row_stride;
+  a.page_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if (a.page_size == 1 << s) a.page_shift = s;
+  a.table = block_table;
+  a.table_rs = block_table_row_stride;
+  a.table_width = table_width;
+  a.seq_lens = seq_lens;
+  a.B = num_seqs;
+  a.q_len = 1 + n_spec;
+  a.Hq = num_q_heads;
+  a.G = num_q_heads / a.Hkv;
+  a.scale = scale;
+  a.out = static_cast<char*>(out);
+  a.out_rs = out_row_stride;
+  a.lse = lse;
+  a.hw = p.hw;
+  // positions that follow one another in memory come together, up to 1 KB or four
+  a.group_shift = 0;
+  if (a.s_tok == (int64_t)p.hw * D && (p.hw == 1 || a.s_head == D))
+    while (a.group_shift < 2 && (p.hw * D * bytes << a.group_shift) < 1024 &&
+           a.page_size % (2 << a.group_shift) == 0)
+      ++a.group_shift;
+  a.rblocks = p.rblocks;
+  a.rows = p.rows;
+  a.units = p.units;
+  a.grid = p.grid;
+  a.dev_err = dev_err;
+}
+
 // Launches a kernel of the shared form beside the end of the one before it.
 template <typename K, typename A>
 cudaError_t attn_launch_beside(K kernel, const A& a, int more, int grid, int threads, int smem,

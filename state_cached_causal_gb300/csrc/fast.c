@@ -51,7 +51,16 @@ static int (*p_read_q8)(kv_cache_q8_t, const int32_t*, int32_t, int32_t, void*, 
 static int (*p_attn_q8)(const void*, int64_t, kv_cache_q8_t, const int32_t*, int64_t, int32_t,
                         const int32_t*, int32_t, int32_t, int32_t, float, int32_t, void*, int64_t,
                         float*, void*, int64_t, int32_t*, cconv_stream_t);
+static int (*p_shared)(const void*, int64_t, kv_cache_t, const int32_t*, int64_t, int32_t,
+                       const int32_t*, int32_t, const int32_t*, const int32_t*, int32_t, int32_t,
+                       int32_t, float, int32_t, void*, int64_t, float*, void*, int64_t, int32_t*,
+                       cconv_stream_t);
+static int (*p_shared_q8)(const void*, int64_t, kv_cache_q8_t, const int32_t*, int64_t, int32_t,
+                          const int32_t*, int32_t, const int32_t*, const int32_t*, int32_t,
+                          int32_t, int32_t, float, int32_t, void*, int64_t, float*, void*, int64_t,
+                          int32_t*, cconv_stream_t);
 static int64_t (*p_need)(int32_t, int32_t, int32_t, int32_t, int32_t);
+static int64_t (*p_need_shared)(int32_t, int32_t, int32_t, int32_t, int32_t, int32_t);
 
 typedef struct {
   void* p;
@@ -334,40 +343,49 @@ static PyObject* f_read_q8(PyObject* self, PyObject* const* x, Py_ssize_t n) {
   return PyLong_FromLong(p_read_q8(c, sl.p, (int32_t)T, ko.dt, ko.p, ks, vo.p, vs, err.p, st));
 }
 
-/* q k_cache v_cache [k_scale v_scale] block_table seq_lens n_spec scale out lse workspace
- * dev_err */
-static PyObject* attn(PyObject* const* x, Py_ssize_t n, int q8) {
-  Ten q, tab, len, out, lse, ws, err;
+/* q k_cache v_cache [k_scale v_scale] block_table seq_lens [cu_groups prefix_lens] n_spec scale
+ * out lse workspace dev_err */
+static PyObject* attn(PyObject* const* x, Py_ssize_t n, int q8, int shared) {
+  Ten q, tab, len, cu, pre, out, lse, ws, err;
   kv_cache_t c = {0};
   kv_cache_q8_t c8 = {0};
   int dev = -1;
-  int64_t qs, os;
+  int64_t qs, os, G = 0;
   cconv_stream_t st;
-  if (n != (q8 ? 13 : 11) || !get(x[0], &q, &dev) || q.nd != 3 || (q.dt != F32 && q.dt != BF16))
+  if (n != 11 + 2 * q8 + 2 * shared || !get(x[0], &q, &dev) || q.nd != 3 ||
+      (q.dt != F32 && q.dt != BF16))
     return not_plain();
-  PyObject* const* y = x + (q8 ? 5 : 3); /* block_table .. */
-  const long ns = PyLong_AsLong(y[2]);
-  const double scale = PyFloat_AsDouble(y[3]);
+  PyObject* const* t = x + 3 + 2 * q8;  /* block_table seq_lens [cu_groups prefix_lens] */
+  PyObject* const* y = t + 2 + 2 * shared; /* n_spec .. */
+  const long ns = PyLong_AsLong(y[0]);
+  const double scale = PyFloat_AsDouble(y[1]);
   if (PyErr_Occurred() || ns < 0 ||
       !(q8 ? cache_q8(x + 1, &c8, &dev) : cache(x[1], x[2], q.dt, &c, &dev)) ||
-      !need(y[0], &tab, I32, &dev) || !need(y[1], &len, I32, &dev) ||
-      !need(y[4], &out, q.dt, &dev) || !maybe(y[5], &lse, F32, &dev) ||
-      !maybe(y[6], &ws, U8, &dev) || !maybe(y[7], &err, I32, &dev) || !flat(&len) ||
+      !need(t[0], &tab, I32, &dev) || !need(t[1], &len, I32, &dev) ||
+      !need(y[2], &out, q.dt, &dev) || !maybe(y[3], &lse, F32, &dev) ||
+      !maybe(y[4], &ws, U8, &dev) || !maybe(y[5], &err, I32, &dev) || !flat(&len) ||
       (ws.nd >= 0 && !flat(&ws)) || (err.nd >= 0 && (err.nd != 1 || err.n[0] < 1)))
     return not_plain();
+  if (shared) {
+    if (!need(t[2], &cu, I32, &dev) || !need(t[3], &pre, I32, &dev) || !flat(&cu) || !flat(&pre) ||
+        cu.n[0] != pre.n[0] + 1)
+      return not_plain();
+    G = pre.n[0];
+  }
   const int64_t B = len.n[0], rows = B * (1 + ns);
   const int32_t hkv = q8 ? c8.num_kv_heads : c.num_kv_heads, D = q8 ? c8.head_dim : c.head_dim;
-  if (q.n[2] != D || !heads(&q, rows, q.n[1], q.n[2], &qs) ||
-      !heads(&out, rows, q.n[1], q.n[2], &os) || tab.nd != 2 || tab.n[0] < B ||
-      (tab.n[1] > 1 && tab.s[1] != 1) ||
+  const int32_t hq = (int32_t)q.n[1];
+  if (q.n[2] != D || !heads(&q, rows, hq, D, &qs) || !heads(&out, rows, hq, D, &os) ||
+      tab.nd != 2 || tab.n[0] < B || (tab.n[1] > 1 && tab.s[1] != 1) ||
       (lse.nd >= 0 && (lse.nd != 2 || lse.n[0] < rows || lse.n[1] != q.n[1] ||
                        (lse.n[1] > 1 && lse.s[1] != 1) || (lse.n[0] > 1 && lse.s[0] != q.n[1]))) ||
       !stream_of(dev, &st))
     return not_plain();
   const int64_t ts = tab.n[0] > 1 || tab.s[0] > tab.n[1] ? tab.s[0] : tab.n[1];
+  const int32_t tw = (int32_t)tab.n[1], b = (int32_t)B, s = (int32_t)ns, g = (int32_t)G;
   PyObject* own = NULL; /* the call's workspace, if it brought none */
   if (ws.nd < 0) {
-    const int64_t need = p_need((int32_t)B, (int32_t)ns, (int32_t)q.n[1], hkv, D);
+    const int64_t need = shared ? p_need_shared(b, g, s, hq, hkv, D) : p_need(b, s, hq, hkv, D);
     if (need < 0) return not_plain();
     own = PyObject_CallFunction(new_bytes, "OL", x[0], (long long)(need > 16 ? need : 16));
     if (!own) return NULL;
@@ -376,19 +394,28 @@ static PyObject* attn(PyObject* const* x, Py_ssize_t n, int q8) {
       return not_plain();
     }
   }
-  const int rc =
-      q8 ? p_attn_q8(q.p, qs, c8, tab.p, ts, (int32_t)tab.n[1], len.p, (int32_t)B, (int32_t)ns,
-                     (int32_t)q.n[1], (float)scale, q.dt, out.p, os, lse.p, ws.p, ws.n[0], err.p,
-                     st)
-         : p_attn(q.p, qs, c, tab.p, ts, (int32_t)tab.n[1], len.p, (int32_t)B, (int32_t)ns,
-                  (int32_t)q.n[1], (float)scale, q.dt, out.p, os, lse.p, ws.p, ws.n[0], err.p, st);
+  int rc;
+  if (!shared)
+    rc = q8 ? p_attn_q8(q.p, qs, c8, tab.p, ts, tw, len.p, b, s, hq, (float)scale, q.dt, out.p, os,
+                        lse.p, ws.p, ws.n[0], err.p, st)
+            : p_attn(q.p, qs, c, tab.p, ts, tw, len.p, b, s, hq, (float)scale, q.dt, out.p, os,
+                     lse.p, ws.p, ws.n[0], err.p, st);
+  else
+    rc = q8 ? p_shared_q8(q.p, qs, c8, tab.p, ts, tw, len.p, b, cu.p, pre.p, g, s, hq,
+                          (float)scale, q.dt, out.p, os, lse.p, ws.p, ws.n[0], err.p, st)
+            : p_shared(q.p, qs, c, tab.p, ts, tw, len.p, b, cu.p, pre.p, g, s, hq, (float)scale,
+                       q.dt, out.p, os, lse.p, ws.p, ws.n[0], err.p, st);
   Py_XDECREF(own);
   return PyLong_FromLong(rc);
 }
-static PyObject* f_attn(PyObject* self, PyObject* const* x, Py_ssize_t n) { return attn(x, n, 0); }
-static PyObject* f_attn_q8(PyObject* self, PyObject* const* x, Py_ssize_t n) {
-  return attn(x, n, 1);
-}
+#define ATTN(name, q8, shared)                                                      \
+  static PyObject* name(PyObject* self, PyObject* const* x, Py_ssize_t n) {         \
+    return attn(x, n, q8, shared);                                                  \
+  }
+ATTN(f_attn, 0, 0)
+ATTN(f_attn_q8, 1, 0)
+ATTN(f_shared, 0, 1)
+ATTN(f_shared_q8, 1, 1)
 
 /* init(handle of libcconv.so, (float32, bfloat16, int32, uint8, bool[, float8_e4m3fn,
  *      float8_e8m0fnu: without them 8-bit caches are left to Python]), raw stream function,
@@ -410,8 +437,11 @@ static PyObject* f_init(PyObject* self, PyObject* const* x, Py_ssize_t n) {
   *(void**)&p_norm_q8 = dlsym(h, "attn_norm_rope_cache_q8");
   *(void**)&p_read_q8 = dlsym(h, "kv_cache_read_q8");
   *(void**)&p_attn_q8 = dlsym(h, "attn_decode_q8");
+  *(void**)&p_shared = dlsym(h, "attn_decode_shared");
+  *(void**)&p_shared_q8 = dlsym(h, "attn_decode_shared_q8");
+  *(void**)&p_need_shared = dlsym(h, "attn_decode_shared_workspace_bytes");
   if (!p_fwd || !p_upd || !p_norm || !p_attn || !p_need || !p_norm_q8 || !p_read_q8 ||
-      !p_attn_q8) {
+      !p_attn_q8 || !p_shared || !p_shared_q8 || !p_need_shared) {
     PyErr_SetString(PyExc_RuntimeError, "libcconv.so lacks an entry point");
     return NULL;
   }
@@ -432,6 +462,8 @@ static PyMethodDef methods[] = {FN("init", f_init),
                                 FN("attn_norm_rope_cache_q8", f_norm_q8),
                                 FN("kv_cache_read_q8", f_read_q8),
                                 FN("attn_decode_q8", f_attn_q8),
+                                FN("attn_decode_shared", f_shared),
+                                FN("attn_decode_shared_q8", f_shared_q8),
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", NULL, -1, methods,
                                     NULL, NULL, NULL, NULL};

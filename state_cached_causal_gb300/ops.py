@@ -22,7 +22,7 @@ DTYPE_F32, DTYPE_BF16 = 0, 1
 ACT_NONE, ACT_SILU = 0, 1
 DERR_SLOT_RANGE, DERR_CU_SEQLENS, DERR_NUM_ACCEPTED, DERR_TIMEOUT = 1, 2, 4, 8
 DERR_ROW_INDEX, DERR_CHECKPOINT = 16, 32
-DERR_POSITION, DERR_PAGE, DERR_SEQ_LEN = 64, 128, 256
+DERR_POSITION, DERR_PAGE, DERR_SEQ_LEN, DERR_GROUP = 64, 128, 256, 512
 
 _F8, _F8_SCALE = torch.float8_e4m3fn, torch.float8_e8m0fnu    # of a cache in 8 bits
 
@@ -131,7 +131,12 @@ def load():
         lib.attn_decode.restype = ctypes.c_int
         lib.attn_decode_workspace_bytes.argtypes = [I32, I32, I32, I32, I32]
         lib.attn_decode_workspace_bytes.restype = I64
-        for name in ("attn_norm_rope_cache", "attn_decode"):
+        lib.attn_decode_shared.argtypes = [P, I64, KvCache, P, I64, I32, P, I32, P, P, I32, I32, I32,
+                                           F32, I32, P, I64, P, P, I64, P, P]
+        lib.attn_decode_shared.restype = ctypes.c_int
+        lib.attn_decode_shared_workspace_bytes.argtypes = [I32, I32, I32, I32, I32, I32]
+        lib.attn_decode_shared_workspace_bytes.restype = I64
+        for name in ("attn_norm_rope_cache", "attn_decode", "attn_decode_shared"):
             plain, q8 = getattr(lib, name), getattr(lib, name + "_q8")
             q8.argtypes = [KvCacheQ8 if t is KvCache else t for t in plain.argtypes]
             q8.restype = ctypes.c_int
@@ -729,8 +734,9 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, n_spec, scale, out, 
 
 
 def _decode_call(fn, q, block_table, seq_lens, n_spec, scale, out, lse, workspace, dev_err, stream,
-                 hkv, dim, views, cache):
-    """views: the cache's tensors; cache(addresses) -> its C struct."""
+                 hkv, dim, views, cache, groups=None):
+    """views: the cache's tensors; cache(addresses) -> its C struct; groups: (cu_groups, prefix_lens)
+    of the shared form."""
     _i32(block_table, "block_table")
     _entries(seq_lens, "seq_lens", 0)
     _error_word(dev_err)
@@ -747,9 +753,18 @@ def _decode_call(fn, q, block_table, seq_lens, n_spec, scale, out, lse, workspac
     if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous()
                             or lse.shape[0] < rows or lse.shape[1:] != (hq,)):
         raise ValueError("lse must be contiguous float32 [rows, heads]")
-    P = _raw(q, block_table, seq_lens, out, lse, workspace, dev_err, *views)
+    more, G = (), 0
+    if groups is not None:
+        _entries(groups[1], "prefix_lens", 0)
+        G = groups[1].shape[0]
+        _entries(groups[0], "cu_groups", G + 1)
+        if groups[0].shape[0] != G + 1:
+            raise ValueError("cu_groups must have one entry more than prefix_lens")
+        more = groups
+    P = _raw(q, block_table, seq_lens, out, lse, workspace, dev_err, *views, *more)
     if workspace is None:
-        need = attn_decode_workspace_bytes(B, n_spec, hq, hkv, dim)
+        need = (attn_decode_workspace_bytes(B, n_spec, hq, hkv, dim) if groups is None else
+                attn_decode_shared_workspace_bytes(B, G, n_spec, hq, hkv, dim))
         if stream is None:
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
         else:
@@ -757,9 +772,9 @@ def _decode_call(fn, q, block_table, seq_lens, n_spec, scale, out, lse, workspac
                 workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
         P[5] = workspace.data_ptr()
     rc = getattr(load(), fn)(P[0], qs, cache(P[7:]), P[1],
-                             tst[0] if ts[0] > 1 else max(tst[0], ts[1]), ts[1], P[2], B, n_spec, hq,
-                             scale, code, P[3], os_, P[4], P[5],
-                             workspace.numel() * workspace.element_size(), P[6],
+                             tst[0] if ts[0] > 1 else max(tst[0], ts[1]), ts[1], P[2], B,
+                             *((P[-2], P[-1], G) if more else ()), n_spec, hq, scale, code, P[3],
+                             os_, P[4], P[5], workspace.numel() * workspace.element_size(), P[6],
                              _raw_stream(stream))
     if rc != OK:
         raise CConvError(fn, rc)
@@ -780,3 +795,53 @@ def attn_decode_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
     _decode_call("attn_decode_q8", q, block_table, seq_lens, n_spec, scale, out, lse, workspace,
                  dev_err, stream, s[2], s[3], (k_cache, v_cache, k_scale, v_scale),
                  lambda P: _q8_struct(P, s, st, ct))
+
+
+def attn_decode_shared_workspace_bytes(num_seqs, num_groups, n_spec, num_q_heads, num_kv_heads,
+                                       head_dim):
+    """Bytes of workspace of an attn_decode_shared (or .._q8) call of these sizes."""
+    n = load().attn_decode_shared_workspace_bytes(num_seqs, num_groups, n_spec, num_q_heads,
+                                                  num_kv_heads, head_dim)
+    if n < 0:
+        raise CConvError("attn_decode_shared_workspace_bytes", n)
+    return n
+
+
+def attn_decode_shared(q, k_cache, v_cache, block_table, seq_lens, cu_groups, prefix_lens, n_spec,
+                       scale, out, lse=None, workspace=None, dev_err=None, stream=None):
+    """Attention of new tokens of requests that share their first positions in groups (see
+    attn_decode_shared in cconv.h).
+
+    cu_groups: int32 [groups + 1], group g holds requests cu_groups[g] to cu_groups[g + 1] - 1;
+    prefix_lens: int32 [groups], the positions that it shares, read through the block table of its
+    first request; workspace: attn_decode_shared_workspace_bytes() or None (allocated for the
+    call). The rest as attn_decode, in bf16.
+    """
+    if stream is None and (_lib or load()) and _fast is not None and _served(
+            "attn_decode_shared", _fast.attn_decode_shared(
+                q, k_cache, v_cache, block_table, seq_lens, cu_groups, prefix_lens, n_spec, scale,
+                out, lse, workspace, dev_err)):
+        return
+    (pages, page, hkv, dim), st, code = _cache(k_cache, v_cache, q.dtype)
+    _decode_call("attn_decode_shared", q, block_table, seq_lens, n_spec, scale, out, lse, workspace,
+                 dev_err, stream, hkv, dim, (k_cache, v_cache),
+                 lambda P: KvCache(P[0], P[1], st[0], st[1], st[2], pages, page, hkv, dim, code),
+                 (cu_groups, prefix_lens))
+
+
+def attn_decode_shared_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_groups,
+                          prefix_lens, n_spec, scale, out, lse=None, workspace=None, dev_err=None,
+                          stream=None):
+    """attn_decode_shared over a cache in 8 bits (see attn_decode_shared_q8 in cconv.h).
+
+    caches and scales as attn_norm_rope_cache_q8; the rest as attn_decode_shared.
+    """
+    if stream is None and (_lib or load()) and _fast is not None and _served(
+            "attn_decode_shared_q8", _fast.attn_decode_shared_q8(
+                q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_groups,
+                prefix_lens, n_spec, scale, out, lse, workspace, dev_err)):
+        return
+    s, st, ct = _cache_q8(k_cache, v_cache, k_scale, v_scale)
+    _decode_call("attn_decode_shared_q8", q, block_table, seq_lens, n_spec, scale, out, lse,
+                 workspace, dev_err, stream, s[2], s[3], (k_cache, v_cache, k_scale, v_scale),
+                 lambda P: _q8_struct(P, s, st, ct), (cu_groups, prefix_lens))
