@@ -245,6 +245,12 @@ __device__ __forceinline__ uint32_t place(int r, int u) {
   return (u >> 3) * PANEL + r * 128 + (((u & 7) ^ (r & 7)) << 4);
 }
 
+// A lane's row of an item: where its values begin (-1: none, zeros), and its scale.
+struct Row {
+  int64_t at;
+  float f;
+};
+
 template <int D, bool Q8>
 __device__ __forceinline__ bool copy_role(const PrefixArgs& x, Run run, Ctl& c,
                                           unsigned char* ring, const Wait& wait) {
@@ -253,78 +259,116 @@ __device__ __forceinline__ bool copy_role(const PrefixArgs& x, Run run, Ctl& c,
   constexpr int kRowsW = S::kN / kCopyWarps;            // rows of a warp: lane r has row r's
   constexpr int kRowBytes = D * (Q8 ? 1 : 2), kLanes = kRowBytes / 16;   // of a row
   constexpr int kPer = 32 / kLanes, kPasses = kRowsW / kPer;
-  constexpr int kLag = 3;
-  // An item is announced kLag items later; the products may need the one behind the
-  // item whose place is waited for.
-  static_assert(kLag + 2 <= S::kStages, "");
+  // Copies of so many items are on their way before the first is waited for. (The
+  // products may need the item behind the one whose place is waited for.)
+  constexpr int kLag = S::kStages - 2;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kCopyWarp0;
   const int sub = lane / kLanes, u = lane % kLanes;
-  int it = 0, seq = 0;
+  int it = 0, seq = 0, told = 0;            // items issued, and announced
+  auto tell = [&]() {
+    fence_proxy_async();
+    mbar_arrive(&c.full[told++ % S::kStages]);
+  };
+  // Place of the next item: where it is still held, the items on their way are waited
+  // for, and announced, first.
+  auto acquire = [&]() {
+    uint64_t* const bar = &c.empty[it % S::kStages];
+    const int phase = (it / S::kStages & 1) ^ 1;
+    if (!Q8 && told < it && !__any_sync(0xffffffffu, tc::mbar_ready(bar, phase))) {
+      cp_async_wait<0>();
+      while (told < it) tell();
+    }
+    return wait(bar, phase);
+  };
   while (run.p < run.end) {
     const Seg s = segment<D>(x, run);
     const int n = s.j1 - s.j0;
     const bool two = S::NT == 2 && !s.pair;
     const int32_t* const tab = a.table + (int64_t)s.g.first * a.table_rs;
     const int64_t head = (int64_t)s.h * a.s_head;
-    // the lane's row of item i: its page and where that is
+    auto pos_of = [&](const Item& m) { return (s.j0 + m.tile) * S::kN + w * kRowsW + lane; };
+    // the lane's row of item i: its page
     auto look = [&](int i) {
-      const Item m = item_of(i, n, two);
-      const int pos = (s.j0 + m.tile) * S::kN + w * kRowsW + lane;
+      const int pos = pos_of(item_of(i, n, two));
       return i < 2 * n && lane < kRowsW && pos < s.g.prefix
                  ? tab[a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size]
                  : -1;
     };
-    int page = look(0), next = look(1);
-#pragma unroll 1
-    for (int i = 0; i < 2 * n; ++i, ++it) {
+    // and where that is
+    auto row_of = [&](int i, int page) {
       const Item m = item_of(i, n, two);
-      const int st = it % S::kStages;
-      const int pos = (s.j0 + m.tile) * S::kN + w * kRowsW + lane;
+      const int pos = pos_of(m);
+      const bool in = i < 2 * n && lane < kRowsW && pos < s.g.prefix;
+      Row r = {-1, 0.0f};
+      if (!in) return r;
+      if ((uint32_t)page >= (uint32_t)a.num_pages) {
+        if (!m.isv) flag_error(a.dev_err, CCONV_DERR_PAGE);
+        return r;
+      }
       const int tok = a.page_shift >= 0 ? pos & (a.page_size - 1) : pos % a.page_size;
-      const bool in = lane < kRowsW && pos < s.g.prefix;
-      const bool held = in && (uint32_t)page < (uint32_t)a.num_pages;
-      if (in && !held && !m.isv) flag_error(a.dev_err, CCONV_DERR_PAGE);
-      const int64_t row = held ? page * a.s_page + tok * a.s_tok + head : -1;
-      const char* const base = m.isv ? a.vc : a.kc;
-      float f = 0.0f;
-      if constexpr (Q8) {
-        if (held)
-          f = q8_scale((m.isv ? a.vsc : a.ksc)[page * a.c_page + tok * a.c_tok +
+      r.at = page * a.s_page + tok * a.s_tok + head;
+      if constexpr (Q8)
+        r.f = q8_scale((m.isv ? a.vsc : a.ksc)[page * a.c_page + tok * a.c_tok +
                                                (int64_t)s.h * a.c_head]);
-      }
-      page = next;
-      next = look(i + 2);
-      if (!wait(&c.empty[st], (it / S::kStages & 1) ^ 1)) return false;
-      if (!m.isv) {
-        const uint32_t mask = __ballot_sync(0xffffffffu, held);
-        if (lane == 0) c.mask[(seq + m.tile) % kMasks][w] = mask;
-      }
-      unsigned char* const dst = ring + st * S::kStage;
-      if constexpr (!Q8) {
+      return r;
+    };
+    auto note = [&](const Item& m, const Row& r) {
+      if (m.isv) return;
+      const uint32_t mask = __ballot_sync(0xffffffffu, r.at >= 0);
+      if (lane == 0) c.mask[(seq + m.tile) % kMasks][w] = mask;
+    };
+    if constexpr (!Q8) {
+      int page = look(0), next = look(1);
+#pragma unroll 1
+      for (int i = 0; i < 2 * n; ++i, ++it) {
+        const Item m = item_of(i, n, two);
+        const Row row = row_of(i, page);
+        const char* const base = m.isv ? a.vc : a.kc;
+        page = next;
+        next = look(i + 2);
+        if (!acquire()) return false;
+        note(m, row);
+        const uint32_t dst = smem_addr(ring) + it % S::kStages * S::kStage;
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
           const int r = p * kPer + sub;
-          const int64_t at = __shfl_sync(0xffffffffu, row, r);
-          cp_async16(smem_addr(dst) + place<S::kPanel>(w * kRowsW + r, u),
+          const int64_t at = __shfl_sync(0xffffffffu, row.at, r);
+          cp_async16(dst + place<S::kPanel>(w * kRowsW + r, u),
                      base + (at >= 0 ? at * 2 + u * 16 : 0), at >= 0);
         }
         cp_async_commit();
-        if (it >= kLag) {
+        if (it + 1 - told > kLag) {
           cp_async_wait<kLag>();
-          fence_proxy_async();
-          mbar_arrive(&c.full[(it - kLag) % S::kStages]);
+          tell();
         }
-      } else {
-        uint4 v[kPasses];
+      }
+    } else {
+      // An item's values are requested while the one before it is converted, their
+      // scales an item earlier, its pages another one.
+      uint4 v[kPasses];
+      auto fetch = [&](const Item& m, const Row& row) {
+        const char* const base = m.isv ? a.vc : a.kc;
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
-          const int64_t at = __shfl_sync(0xffffffffu, row, p * kPer + sub);
+          const int64_t at = __shfl_sync(0xffffffffu, row.at, p * kPer + sub);
           v[p] = at >= 0 ? ldg16(base + at + u * 16) : make_uint4(0u, 0u, 0u, 0u);
         }
+      };
+      int page0 = look(0), page1 = look(1), page2 = look(2);
+      Row row = row_of(0, page0), next = row_of(1, page1);
+      fetch(item_of(0, n, two), row);
+#pragma unroll 1
+      for (int i = 0; i < 2 * n; ++i, ++it) {
+        const Item m = item_of(i, n, two);
+        const Row after = row_of(i + 2, page2);
+        page2 = look(i + 3);
+        if (!acquire()) return false;
+        note(m, row);
+        unsigned char* const dst = ring + it % S::kStages * S::kStage;
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
           const int r = p * kPer + sub;
-          const float k = __shfl_sync(0xffffffffu, f, r);
+          const float k = __shfl_sync(0xffffffffu, row.f, r);
           uint32_t o[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -333,22 +377,21 @@ __device__ __forceinline__ bool copy_role(const PrefixArgs& x, Run run, Ctl& c,
             o[2 * e] = pack_bf16x2(y[0] * k, y[1] * k);
             o[2 * e + 1] = pack_bf16x2(y[2] * k, y[3] * k);
           }
-          unsigned char* const to = dst;
-          *reinterpret_cast<uint4*>(to + place<S::kPanel>(w * kRowsW + r, 2 * u)) =
+          *reinterpret_cast<uint4*>(dst + place<S::kPanel>(w * kRowsW + r, 2 * u)) =
               make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(to + place<S::kPanel>(w * kRowsW + r, 2 * u + 1)) =
+          *reinterpret_cast<uint4*>(dst + place<S::kPanel>(w * kRowsW + r, 2 * u + 1)) =
               make_uint4(o[4], o[5], o[6], o[7]);
         }
-        fence_proxy_async();
-        mbar_arrive(&c.full[st]);
+        tell();
+        row = next, next = after;
+        if (i + 1 < 2 * n) fetch(item_of(i + 1, n, two), row);
       }
     }
     seq += n;
   }
   if constexpr (!Q8) {
     cp_async_wait<0>();
-    fence_proxy_async();
-    for (int i = max(it - kLag, 0); i < it; ++i) mbar_arrive(&c.full[i % S::kStages]);
+    while (told < it) tell();
   }
   return true;
 }
@@ -457,6 +500,32 @@ __device__ __forceinline__ void empty_part(const PrefixArgs& x, const Seg& s, in
   x.ps[s.slot * S::kRowsU + stream * 128 + r] = make_float2(-INFINITY, 0.0f);
 }
 
+// Scores of positions without a row (behind the prefix, on a bad page) become -inf.
+template <int N>
+__device__ __noinline__ void hide(uint32_t sc, const uint32_t (&keep)[N / 32]) {
+#pragma unroll 1
+  for (int k = 0; k < N / 32; ++k) {
+    const uint32_t bits = k == 0 ? keep[0] : k == 1 ? keep[N > 32 ? 1 : 0]
+                                 : k == 2 ? keep[N > 64 ? 2 : 0] : keep[N > 96 ? 3 : 0];
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      uint32_t v[16], t[8];
+      tc::ld16(sc + k * 32 + h * 16, v);
+      tc::wait_ld(v);
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (!(bits >> (h * 16 + e) & 1u)) v[e] = 0xff800000u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] = v[e];
+      tc::st8(sc + k * 32 + h * 16, t);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] = v[8 + e];
+      tc::st8(sc + k * 32 + h * 16 + 8, t);
+    }
+  }
+  tc::wait_st();
+}
+
 template <int D>
 __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, unsigned char* q_all,
                                           const Wait& wait, uint32_t tmem, int stream) {
@@ -465,8 +534,9 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
   const int r = threadIdx.x & 127, rows_all = a.G * a.q_len;
   const uint32_t lanes = tmem + ((uint32_t)(r >> 5) << 21);
   const uint32_t sc = lanes + kColS + stream * 128, oc = lanes + kColO + stream * D;
-  // Q carries the scale's sign, so that the largest score has the largest weight
-  const float sl2 = fabsf(a.scale) * 1.4426950408889634f;
+  // Q carries the scale's sign, so that the largest score has the largest weight (and a
+  // scale of zero is the least normal number, which leaves hidden scores at -inf)
+  const float sl2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 0x1p-126f);
   const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
   int tiles_done = 0, segs = 0, seq = 0;
   bool ok = true;
@@ -500,6 +570,8 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
       fence_proxy_async();
       mbar_arrive(&c.q_full[stream]);
     }
+    const int valid = s.rows - (s.pair ? stream * 128 : 0);
+    const bool idle = (r & ~31) >= valid;    // no row of this warp's: nobody reads its sums
     float m = -INFINITY, l = 0.0f;          // (m: what the weights are relative to)
 #pragma unroll 1
     for (int t = t_first; t < n; t += step) {
@@ -508,6 +580,11 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
         break;
       }
       tc::fence_after();
+      if (idle) {
+        tc::fence_before();
+        mbar_arrive(&c.p_full[stream]);
+        continue;
+      }
       uint32_t keep[S::kN / 32];
       bool all = true;
 #pragma unroll
@@ -516,6 +593,7 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
         keep[k] = S::kN == 128 ? w[k] : w[2 * k] | w[2 * k + 1] << 16;
         all = all && keep[k] == 0xffffffffu;
       }
+      if (!all) hide<S::kN>(sc, keep);
       // ---- the largest score
       float mx = -INFINITY;
 #pragma unroll
@@ -526,13 +604,10 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
         tc::wait_ld(v0);
         tc::wait_ld(v1);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (!all && !(keep[k] >> e & 1u)) v0[e] = 0xff800000u;
-          if (!all && !(keep[k] >> (16 + e) & 1u)) v1[e] = 0xff800000u;
+        for (int e = 0; e < 16; ++e)
           mx = fmaxf(mx, fmaxf(__uint_as_float(v0[e]), __uint_as_float(v1[e])));
-        }
       }
-      const float top = mx == -INFINITY ? mx : mx * sl2;
+      const float top = mx * sl2;
       const bool rises = top > m + kSlack || (m == -INFINITY && top > m);
       if (__any_sync(0xffffffffu, rises)) {
         const float mn = rises ? top : m;
@@ -557,9 +632,9 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
           }
         }
       }
-      const float base = m == -INFINITY ? 0.0f : m;
+      const float base = m == -INFINITY ? 0.0f : -m;
       // ---- weights, in place of the scores: of 32 positions first terms, then second
-      float sum = 0.0f;
+      float sum = 0.0f, sum1 = 0.0f;
 #pragma unroll
       for (int k = 0; k < S::kN / 32; ++k) {
         uint32_t v0[16], v1[16];
@@ -571,11 +646,11 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           const uint32_t *w = e < 16 ? v0 + e : v1 + e - 16;
-          float p0 = tc::ex2(fmaf(__uint_as_float(w[0]), sl2, -base));
-          float p1 = tc::ex2(fmaf(__uint_as_float(w[1]), sl2, -base));
-          if (!all && !(keep[k] >> e & 1u)) p0 = 0.0f;
-          if (!all && !(keep[k] >> (e + 1) & 1u)) p1 = 0.0f;
-          sum += p0 + p1;
+          float p0, p1;
+          fma_x2(p0, p1, __uint_as_float(w[0]), __uint_as_float(w[1]), sl2, sl2, base, base);
+          p0 = tc::ex2(p0);
+          p1 = tc::ex2(p1);
+          fma_x2(sum, sum1, p0, p1, 1.0f, 1.0f, sum, sum1);
           // The first term is cut a little below the weight, so that the second is above
           // zero: terms of zero times an infinite value would make NaN.
           float c0, c1;
@@ -595,6 +670,7 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
           tc::st8(sc + k * 32 + q * 8, half);
         }
       }
+      sum += sum1;
       l += sum;
       tc::wait_st();
       tc::fence_before();
@@ -608,10 +684,10 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
     }
     tc::fence_after();
     const int64_t row = s.slot * S::kRowsU + stream * 128 + r;
-    const bool mine = r < s.rows - (s.pair ? stream * 128 : 0);
+    const bool mine = r < valid;
     float* const o = x.po + row * D;
 #pragma unroll 1
-    for (int k = 0; k < D; k += 16) {
+    for (int k = 0; k < (idle ? 0 : D); k += 16) {
       uint32_t v[16];
       tc::ld16(oc + k, v);
       tc::wait_ld(v);
@@ -692,38 +768,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
 template <int D, int W>
 __global__ void __launch_bounds__(256) attn_shared_join_kernel(const PrefixArgs x, const int n) {
   using S = Shape<D>;
-  constexpr int kPairs = D / 64, kAhead = 4, kRowsB = 8 / W;
+  constexpr int kPairs = D / 64, kAhead = D == 256 ? 4 : 8, kRowsB = 8 / W;
   const AttnArgs& a = x.a;
   __shared__ float sums[W > 1 ? 8 : 1][W > 1 ? D + 2 : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % W;
   const int64_t at = (int64_t)blockIdx.x * kRowsB + warp / W;   // request, kv head, row of it
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int rows_all = a.G * a.q_len;
   // (the warps of a row all go on or all leave)
-  if (at >= n) return;
+  if (at >= n) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int b = (int)(at / (a.Hkv * rows_all)), k = (int)(at % (a.Hkv * rows_all));
   const int h = k / rows_all, rr = k % rows_all;
-  // own positions
+  // what the call's arguments tell, before the kernels whose results are joined are done
   const int unit = h / a.hw * a.rblocks + rr / a.rows;
   const int64_t bu = (int64_t)b * a.units + unit;
-  const int c0 = a.meta[bu * 2], c1 = a.meta[bu * 2 + 1];
-  if (!attn_joins(c0, c1, a.grid)) return;
+  const int g = attn_start(a, b) > 0 ? attn_group(a, b) : -1;
+  Group s = {};
+  if (g >= 0) s = group_of<D>(a, g);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int2 c = *reinterpret_cast<const int2*>(a.meta + bu * 2);
+  Rec rec = {};
+  int64_t total = 0;
+  if (g >= 0) {
+    rec = x.rec[g];
+    total = x.rec[a.groups].line;
+  }
+  // own positions
+  if (!attn_joins(c.x, c.y, a.grid)) return;
   const int64_t one = (int64_t)a.hw * a.rows * (D + 2);
   const float* const own =
-      a.part + (bu + c0) * one + (int64_t)(h % a.hw * a.rows + rr % a.rows) * (D + 2);
-  const int owns = c1 - c0 + 1;
+      a.part + (bu + c.x) * one + (int64_t)(h % a.hw * a.rows + rr % a.rows) * (D + 2);
+  const int owns = c.y - c.x + 1;
   // the prefix
   int shared = 0;
   int64_t slot = 0;
   bool two = false;
-  if (attn_start(a, b) > 0) {
-    const int g = attn_group(a, b);
-    const Group s = group_of<D>(a, g);
-    const Rec rec = x.rec[g];
+  if (g >= 0) {
     if (rec.unit < 0) return;                     // (groups that overlap: reported)
     const int64_t R = (int64_t)(b - s.first) * rows_all + rr, mt = R / S::kRowsU;
     const int64_t u = mt * a.Hkv + h, line = rec.line + u * s.tiles;
-    const int64_t total = x.rec[a.groups].line;
     const int64_t grid = min((int64_t)x.grid, total);
     const int p0 = attn_block_of(line, total, grid);
     const int p1 = attn_block_of(line + s.tiles - 1, total, grid);
