@@ -73,7 +73,7 @@ struct Shape {
 
 struct Ctl {
   uint64_t full[8], empty[8];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], fin;
+  uint64_t q_full[2], s_full[2], p_full[2][4], o_full[2], fin;
   int64_t scan[2 * (kThreads / 32) + 4];
   uint32_t mask[kMasks][kCopyWarps];
   uint32_t tmem;
@@ -259,26 +259,11 @@ __device__ __forceinline__ bool copy_role(const PrefixArgs& x, Run run, Ctl& c,
   constexpr int kRowsW = S::kN / kCopyWarps;            // rows of a warp: lane r has row r's
   constexpr int kRowBytes = D * (Q8 ? 1 : 2), kLanes = kRowBytes / 16;   // of a row
   constexpr int kPer = 32 / kLanes, kPasses = kRowsW / kPer;
-  // Copies of so many items are on their way before the first is waited for. (The
-  // products may need the item behind the one whose place is waited for.)
-  constexpr int kLag = S::kStages - 2;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kCopyWarp0;
   const int sub = lane / kLanes, u = lane % kLanes;
-  int it = 0, seq = 0, told = 0;            // items issued, and announced
-  auto tell = [&]() {
-    fence_proxy_async();
-    mbar_arrive(&c.full[told++ % S::kStages]);
-  };
-  // Place of the next item: where it is still held, the items on their way are waited
-  // for, and announced, first.
+  int it = 0, seq = 0;                      // items, tiles of earlier segments
   auto acquire = [&]() {
-    uint64_t* const bar = &c.empty[it % S::kStages];
-    const int phase = (it / S::kStages & 1) ^ 1;
-    if (!Q8 && told < it && !__any_sync(0xffffffffu, tc::mbar_ready(bar, phase))) {
-      cp_async_wait<0>();
-      while (told < it) tell();
-    }
-    return wait(bar, phase);
+    return wait(&c.empty[it % S::kStages], (it / S::kStages & 1) ^ 1);
   };
   while (run.p < run.end) {
     const Seg s = segment<D>(x, run);
@@ -336,11 +321,11 @@ __device__ __forceinline__ bool copy_role(const PrefixArgs& x, Run run, Ctl& c,
           cp_async16(dst + place<S::kPanel>(w * kRowsW + r, u),
                      base + (at >= 0 ? at * 2 + u * 16 : 0), at >= 0);
         }
-        cp_async_commit();
-        if (it + 1 - told > kLag) {
-          cp_async_wait<kLag>();
-          tell();
-        }
+        // (arrives when the thread's copies have; the products' warp orders them
+        // before its own reads)
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                         smem_addr(&c.full[it % S::kStages]))
+                     : "memory");
       }
     } else {
       // An item's values are requested while the one before it is converted, their
@@ -382,16 +367,13 @@ __device__ __forceinline__ bool copy_role(const PrefixArgs& x, Run run, Ctl& c,
           *reinterpret_cast<uint4*>(dst + place<S::kPanel>(w * kRowsW + r, 2 * u + 1)) =
               make_uint4(o[4], o[5], o[6], o[7]);
         }
-        tell();
+        fence_proxy_async();
+        mbar_arrive(&c.full[it % S::kStages]);
         row = next, next = after;
         if (i + 1 < 2 * n) fetch(item_of(i + 1, n, two), row);
       }
     }
     seq += n;
-  }
-  if constexpr (!Q8) {
-    cp_async_wait<0>();
-    while (told < it) tell();
   }
   return true;
 }
@@ -399,6 +381,13 @@ __device__ __forceinline__ bool copy_role(const PrefixArgs& x, Run run, Ctl& c,
 // ---- products -------------------------------------------------------------------
 
 constexpr int kColS = 0, kColO = 256;      // of tensor memory: scores of both streams, sums
+
+// The order in which a softmax turns 32 scores after the other into weights: those first
+// that its first pass read last.
+template <int N>
+__host__ __device__ constexpr int chunk_at(int j) {
+  return N == 64 ? 1 - j : j < 2 ? 3 - j : j - 2;
+}
 
 template <int D>
 __device__ __forceinline__ bool mma_role(const PrefixArgs& x, Run run, Ctl& c, uint32_t q_addr,
@@ -408,7 +397,11 @@ __device__ __forceinline__ bool mma_role(const PrefixArgs& x, Run run, Ctl& c, u
   const uint64_t q0 = tc::desc_sw128(q_addr, 16);
   const uint64_t k0 = tc::desc_sw128(ring, 16), v0 = tc::desc_sw128(ring, S::kPanel);
   int it = 0, segs[2] = {0, 0}, ps[2] = {0, 0};
-  auto filled = [&](int i) { return wait(&c.full[i % S::kStages], i / S::kStages); };
+  auto filled = [&](int i) {
+    if (!wait(&c.full[i % S::kStages], i / S::kStages)) return false;
+    fence_proxy_async();          // (per-thread copies come by the generic proxy)
+    return true;
+  };
   // scores of stream s from item i, its Q being tile qt
   auto scores = [&](int s, int qt, int i) {
     const uint64_t q = q0 + ((qt * S::kQ) >> 4), k = k0 + ((i % S::kStages * S::kStage) >> 4);
@@ -421,22 +414,27 @@ __device__ __forceinline__ bool mma_role(const PrefixArgs& x, Run run, Ctl& c, u
     }
     __syncwarp();
   };
-  // sums of stream s: both terms of its weights times item i
+  // sums of stream s: both terms of its weights times item i, 32 positions after the
+  // other as the weights come
   auto values = [&](int s, int i, bool first, bool last) {
-    if (!wait(&c.p_full[s], ps[s]++)) return false;
-    tc::fence_after();
     const uint64_t v = v0 + ((i % S::kStages * S::kStage) >> 4);
-    if (tc::elect()) {
+    const int phase = ps[s]++;
 #pragma unroll
-      for (int ks = 0; ks < S::kN / 16; ++ks)
+    for (int j = 0; j < S::kN / 32; ++j) {
+      const int k = chunk_at<S::kN>(j);
+      if (!wait(&c.p_full[s][k], phase)) return false;
+      tc::fence_after();
+      if (tc::elect()) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          tc::mma_ts(tmem + kColO + s * D,
-                     tmem + kColS + s * 128 + (ks >> 1) * 32 + t * 16 + (ks & 1) * 8,
-                     v + ((ks * 2048) >> 4), kIdO, !first || ks > 0 || t > 0);
-      if (last) tc::commit(&c.o_full[s]);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            tc::mma_ts(tmem + kColO + s * D, tmem + kColS + s * 128 + k * 32 + t * 16 + h * 8,
+                       v + (((2 * k + h) * 2048) >> 4), kIdO, !first || j > 0 || h > 0 || t > 0);
+        if (last && j + 1 == S::kN / 32) tc::commit(&c.o_full[s]);
+      }
+      __syncwarp();
     }
-    __syncwarp();
     return true;
   };
   auto release = [&](int i) {
@@ -550,27 +548,37 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
       seq += n;
       continue;
     }
+    const int valid = s.rows - (two ? 0 : stream * 128);
     if (!two || stream == 0) {
+      // the warp's 32 rows: lane i knows where row i begins
       unsigned char* const to = q_all + stream * S::kQ;
-      const int64_t row0 = s.row0 + stream * 128;
-      const int rows = s.rows - stream * 128;
-      for (int i = r; i < 128 * (D / 8); i += 128) {
-        const int rr = i / (D / 8), u = i % (D / 8);
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (rr < rows) {
-          const int64_t R = row0 + rr;
-          const int64_t b = R / rows_all;
-          const int k = (int)(R - b * rows_all);
-          v = ldg16(a.q + (((s.g.first + b) * a.q_len + k / a.G) * a.q_rs +
-                           (int64_t)(s.h * a.G + k % a.G) * D) * 2 + u * 16);
-          v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+      const int lane = r & 31, w = r >> 5;
+      int64_t mine = -1;
+      if (r < valid) {
+        const int64_t R = s.row0 + stream * 128 + r, b = R / rows_all;
+        const int k = (int)(R - b * rows_all);
+        mine = ((s.g.first + b) * a.q_len + k / a.G) * a.q_rs + (int64_t)(s.h * a.G + k % a.G) * D;
+      }
+      constexpr int kLanes = D / 8, kPer = 32 / kLanes, kBatch = 8;
+#pragma unroll 1
+      for (int p0 = 0; p0 < 32 / kPer; p0 += kBatch) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int p = 0; p < kBatch; ++p) {
+          const int64_t at = __shfl_sync(0xffffffffu, mine, (p0 + p) * kPer + lane / kLanes);
+          v[p] = at >= 0 ? ldg16(a.q + at * 2 + lane % kLanes * 16) : make_uint4(0u, 0u, 0u, 0u);
         }
-        *reinterpret_cast<uint4*>(to + place<S::kPanelQ>(rr, u)) = v;
+#pragma unroll
+        for (int p = 0; p < kBatch; ++p) {
+          v[p].x ^= flip, v[p].y ^= flip, v[p].z ^= flip, v[p].w ^= flip;
+          const int row = w * 32 + (p0 + p) * kPer + lane / kLanes;
+          *reinterpret_cast<uint4*>(to + place<S::kPanelQ>(row, lane % kLanes)) = v[p];
+        }
       }
       fence_proxy_async();
-      mbar_arrive(&c.q_full[stream]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.q_full[stream]);
     }
-    const int valid = s.rows - (s.pair ? stream * 128 : 0);
     const bool idle = (r & ~31) >= valid;    // no row of this warp's: nobody reads its sums
     float m = -INFINITY, l = 0.0f;          // (m: what the weights are relative to)
 #pragma unroll 1
@@ -581,8 +589,8 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
       }
       tc::fence_after();
       if (idle) {
-        tc::fence_before();
-        mbar_arrive(&c.p_full[stream]);
+        if ((r & 31) == 0)
+          for (int k = 0; k < S::kN / 32; ++k) mbar_arrive(&c.p_full[stream][k]);
         continue;
       }
       uint32_t keep[S::kN / 32];
@@ -595,17 +603,17 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
       }
       if (!all) hide<S::kN>(sc, keep);
       // ---- the largest score
+      uint32_t v[2][32];                  // scores; of the last two chunks behind this pass
       float mx = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < S::kN / 32; ++k) {
-        uint32_t v0[16], v1[16];
-        tc::ld16(sc + k * 32, v0);
-        tc::ld16(sc + k * 32 + 16, v1);
-        tc::wait_ld(v0);
-        tc::wait_ld(v1);
+      for (int k = 0; k < S::kN / 32; k += 2) {
+        tc::ld32(sc + k * 32, v[0]);
+        tc::ld32(sc + k * 32 + 32, v[1]);
+        tc::wait_ld(v[0]);
+        tc::wait_ld(v[1]);
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          mx = fmaxf(mx, fmaxf(__uint_as_float(v0[e]), __uint_as_float(v1[e])));
+        for (int e = 0; e < 32; ++e)
+          mx = fmaxf(mx, fmaxf(__uint_as_float(v[0][e]), __uint_as_float(v[1][e])));
       }
       const float top = mx * sl2;
       const bool rises = top > m + kSlack || (m == -INFINITY && top > m);
@@ -636,45 +644,44 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
       // ---- weights, in place of the scores: of 32 positions first terms, then second
       float sum = 0.0f, sum1 = 0.0f;
 #pragma unroll
-      for (int k = 0; k < S::kN / 32; ++k) {
-        uint32_t v0[16], v1[16];
-        tc::ld16(sc + k * 32, v0);
-        tc::ld16(sc + k * 32 + 16, v1);
-        tc::wait_ld(v0);
-        tc::wait_ld(v1);
-        uint32_t hi[16], lo[16];
+      for (int j = 0; j < S::kN / 32; ++j) {
+        const int k = chunk_at<S::kN>(j);
+        uint32_t(&now)[32] = v[1 - (j & 1)];
+        if (j >= 2) tc::wait_ld(now);
+        // (the other buffer is free from the second chunk on)
+        if (j >= 1 && j + 1 < S::kN / 32)
+          tc::ld32(sc + chunk_at<S::kN>(j + 1 < S::kN / 32 ? j + 1 : j) * 32, v[j & 1]);
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const uint32_t *w = e < 16 ? v0 + e : v1 + e - 16;
-          float p0, p1;
-          fma_x2(p0, p1, __uint_as_float(w[0]), __uint_as_float(w[1]), sl2, sl2, base, base);
-          p0 = tc::ex2(p0);
-          p1 = tc::ex2(p1);
-          fma_x2(sum, sum1, p0, p1, 1.0f, 1.0f, sum, sum1);
-          // The first term is cut a little below the weight, so that the second is above
-          // zero: terms of zero times an infinite value would make NaN.
-          float c0, c1;
-          mul_x2(c0, c1, p0, p1, 0.99609375f, 0.99609375f);
-          const uint32_t h = __byte_perm(__float_as_uint(c0), __float_as_uint(c1), 0x7632);
-          float l0, l1;
-          fma_x2(l0, l1, __uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u), -1.0f, -1.0f,
-                 p0, p1);
-          hi[e / 2] = h;
-          lo[e / 2] = pack_bf16x2(l0, l1);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const uint32_t* w = now + h * 16 + e;
+            float p0, p1;
+            fma_x2(p0, p1, __uint_as_float(w[0]), __uint_as_float(w[1]), sl2, sl2, base, base);
+            p0 = tc::ex2(p0);
+            p1 = tc::ex2(p1);
+            fma_x2(sum, sum1, p0, p1, 1.0f, 1.0f, sum, sum1);
+            // The first term is cut a little below the weight, so that the second is above
+            // zero: terms of zero times an infinite value would make NaN.
+            float c0, c1;
+            mul_x2(c0, c1, p0, p1, 0.99609375f, 0.99609375f);
+            const uint32_t first = __byte_perm(__float_as_uint(c0), __float_as_uint(c1), 0x7632);
+            float l0, l1;
+            fma_x2(l0, l1, __uint_as_float(first << 16), __uint_as_float(first & 0xffff0000u),
+                   -1.0f, -1.0f, p0, p1);
+            hi[e / 2] = first;
+            lo[e / 2] = pack_bf16x2(l0, l1);
+          }
+          tc::st8(sc + k * 32 + h * 8, hi);
+          tc::st8(sc + k * 32 + 16 + h * 8, lo);
         }
-        uint32_t half[8];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) half[e] = q < 2 ? hi[q * 8 + e] : lo[(q - 2) * 8 + e];
-          tc::st8(sc + k * 32 + q * 8, half);
-        }
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if ((r & 31) == 0) mbar_arrive(&c.p_full[stream][k]);
       }
-      sum += sum1;
-      l += sum;
-      tc::wait_st();
-      tc::fence_before();
-      mbar_arrive(&c.p_full[stream]);
+      l += sum + sum1;
     }
     if (ok && !wait(&c.o_full[stream], segs++)) ok = false;
     seq += n;
@@ -720,9 +727,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
       mbar_init(&c.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&c.q_full[i], 128);
+      mbar_init(&c.q_full[i], kSoftWarps);
       mbar_init(&c.s_full[i], 1);
-      mbar_init(&c.p_full[i], 128);
+      for (int k = 0; k < 4; ++k) mbar_init(&c.p_full[i][k], kSoftWarps);
       mbar_init(&c.o_full[i], 1);
     }
     mbar_init(&c.fin, 1);
@@ -744,7 +751,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
     const int stream = warp / kSoftWarps;
     if (stream < S::NT) soft_role<D>(x, run, c, base, wait, tmem, stream);
   } else if (warp < kMmaWarp) {
-    if (!copy_role<D, Q8>(x, run, c, ring, wait)) cp_async_wait<0>();
+    copy_role<D, Q8>(x, run, c, ring, wait);
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     mma_role<D>(x, run, c, smem_addr(base), smem_addr(ring), wait, tmem);
     // every product that was issued ends before tensor memory is given back
