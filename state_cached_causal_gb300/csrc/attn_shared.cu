@@ -124,6 +124,10 @@ __device__ __forceinline__ Group group_of(const AttnArgs& a, int g) {
   return r;
 }
 
+// A unit has kAhead more places on the line than tiles, before its first: a segment's
+// start (Q, the first copies) takes a block as long as so many tiles.
+constexpr int kAhead = 2;
+
 struct Run {
   int64_t p, end, total, grid;
   int64_t line, unit;         // of group g
@@ -139,7 +143,7 @@ __device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) 
   int64_t lines = 0, units = 0;
   for (int g = g0; g < g1; ++g) {
     const Group s = group_of<D>(a, g);
-    lines += s.units * s.tiles;
+    lines += s.units * (s.tiles + kAhead);
     units += s.units;
     if (blockIdx.x == 0 &&
         !attn_group_ok(a, a.cu_groups[g], a.cu_groups[g + 1], a.prefix_lens[g]))
@@ -170,7 +174,7 @@ __device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) 
     for (int g = g0; g < g1; ++g) {
       const Group s = group_of<D>(a, g);
       x.rec[g] = Rec{l, fits && s.units > 0 ? (int32_t)u : -1, s.tiles};
-      l += s.units * s.tiles, u += s.units;
+      l += s.units * (s.tiles + kAhead), u += s.units;
     }
   }
   r.total = fits ? ls : 0;
@@ -182,8 +186,8 @@ __device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) 
     int g = g0;
     for (;; ++g) {
       const Group s = group_of<D>(a, g);
-      if (r.p < li + s.units * s.tiles) break;
-      li += s.units * s.tiles, ui += s.units;
+      if (r.p < li + s.units * (s.tiles + kAhead)) break;
+      li += s.units * (s.tiles + kAhead), ui += s.units;
     }
     sm[0] = g, sm[1] = li, sm[2] = ui;
   }
@@ -194,33 +198,43 @@ __device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) 
 
 // One segment: tiles [j0, j1) of a unit: rows [row0, row0 + rows) of group g and kv head h.
 struct Seg {
-  Group g;
-  int h, j0, j1, rows;
-  int64_t row0, slot;
+  int first, prefix;          // the group's first request, and its prefix
+  int h, j0, j1, rows, row0;
+  int64_t slot;
   bool pair;                  // two row tiles on the same positions
 };
+// The run's next segment; false behind the last.
 template <int D>
-__device__ __forceinline__ Seg segment(const PrefixArgs& x, Run& r) {
+__device__ __forceinline__ bool segment(const PrefixArgs& x, Run& r, Seg& s) {
   using S = Shape<D>;
-  Seg s;
-  s.g = group_of<D>(x.a, r.g);
-  while (r.p >= r.line + s.g.units * s.g.tiles) {       // (groups without units, too)
-    r.line += s.g.units * s.g.tiles;
-    r.unit += s.g.units;
-    s.g = group_of<D>(x.a, ++r.g);
+  while (r.p < r.end) {
+    Group g = group_of<D>(x.a, r.g);
+    while (r.p >= r.line + g.units * (g.tiles + kAhead)) {     // (groups without units, too)
+      r.line += g.units * (g.tiles + kAhead);
+      r.unit += g.units;
+      g = group_of<D>(x.a, ++r.g);
+    }
+    const int64_t rel = r.p - r.line;
+    const int per = g.tiles + kAhead;
+    // (a 64-bit division takes a hundred instructions)
+    const int u = rel <= INT32_MAX ? (int)((uint32_t)rel / (uint32_t)per) : (int)(rel / per);
+    const int off = (int)(rel - (int64_t)u * per);
+    const int take = (int)min((int64_t)(per - off), r.end - r.p);
+    r.p += take;
+    s.j0 = max(off - kAhead, 0);
+    s.j1 = off + take - kAhead;
+    if (s.j1 <= s.j0) continue;
+    const int mt = u / x.a.Hkv;
+    s.first = g.first, s.prefix = g.prefix;
+    s.h = u - mt * x.a.Hkv;
+    s.row0 = mt * S::kRowsU;
+    s.rows = min(S::kRowsU, (int)g.rows - s.row0);
+    s.pair = S::NT == 2 && s.rows > 128;
+    // from one segment to the next the unit's number or the block's rises
+    s.slot = r.unit + u + blockIdx.x;
+    return true;
   }
-  const int64_t rel = r.p - r.line, u = rel / s.g.tiles;
-  s.j0 = (int)(rel - u * s.g.tiles);
-  s.j1 = (int)min((int64_t)s.g.tiles, s.j0 + (r.end - r.p));
-  const int64_t mt = u / x.a.Hkv;
-  s.h = (int)(u - mt * x.a.Hkv);
-  s.row0 = mt * S::kRowsU;
-  s.rows = (int)min((int64_t)S::kRowsU, s.g.rows - s.row0);
-  s.pair = S::NT == 2 && s.rows > 128;
-  // from one segment to the next the unit's number or the block's rises
-  s.slot = r.unit + u + blockIdx.x;
-  r.p += s.j1 - s.j0;
-  return s;
+  return false;
 }
 
 // ---- copies ---------------------------------------------------------------------
@@ -245,10 +259,17 @@ __device__ __forceinline__ uint32_t place(int r, int u) {
   return (u >> 3) * PANEL + r * 128 + (((u & 7) ^ (r & 7)) << 4);
 }
 
-// A lane's row of an item: where its values begin (-1: none, zeros), and its scale.
+// What the copies know of an item, from the lane that has its row on.
+struct Piece {
+  int page;             // as the table has it
+  int tok, h;           // token of the page, kv head
+  int seq;              // the tile's number, as masks are kept by
+  bool isv, there;      // V; false: behind the last item
+  bool row;             // the lane has a row of the prefix
+};
 struct Row {
-  int64_t at;
-  float f;
+  int64_t at;           // where its values begin (-1: none, zeros)
+  float f;              // their scale
 };
 
 template <int D, bool Q8>
@@ -261,119 +282,122 @@ __device__ __forceinline__ bool copy_role(const PrefixArgs& x, Run run, Ctl& c,
   constexpr int kPer = 32 / kLanes, kPasses = kRowsW / kPer;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kCopyWarp0;
   const int sub = lane / kLanes, u = lane % kLanes;
-  int it = 0, seq = 0;                      // items, tiles of earlier segments
-  auto acquire = [&]() {
-    return wait(&c.empty[it % S::kStages], (it / S::kStages & 1) ^ 1);
-  };
-  while (run.p < run.end) {
-    const Seg s = segment<D>(x, run);
-    const int n = s.j1 - s.j0;
-    const bool two = S::NT == 2 && !s.pair;
-    const int32_t* const tab = a.table + (int64_t)s.g.first * a.table_rs;
-    const int64_t head = (int64_t)s.h * a.s_head;
-    auto pos_of = [&](const Item& m) { return (s.j0 + m.tile) * S::kN + w * kRowsW + lane; };
-    // the lane's row of item i: its page
-    auto look = [&](int i) {
-      const int pos = pos_of(item_of(i, n, two));
-      return i < 2 * n && lane < kRowsW && pos < s.g.prefix
-                 ? tab[a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size]
-                 : -1;
-    };
-    // and where that is
-    auto row_of = [&](int i, int page) {
-      const Item m = item_of(i, n, two);
-      const int pos = pos_of(m);
-      const bool in = i < 2 * n && lane < kRowsW && pos < s.g.prefix;
-      Row r = {-1, 0.0f};
-      if (!in) return r;
-      if ((uint32_t)page >= (uint32_t)a.num_pages) {
-        if (!m.isv) flag_error(a.dev_err, CCONV_DERR_PAGE);
-        return r;
-      }
-      const int tok = a.page_shift >= 0 ? pos & (a.page_size - 1) : pos % a.page_size;
-      r.at = page * a.s_page + tok * a.s_tok + head;
-      if constexpr (Q8)
-        r.f = q8_scale((m.isv ? a.vsc : a.ksc)[page * a.c_page + tok * a.c_tok +
-                                               (int64_t)s.h * a.c_head]);
-      return r;
-    };
-    auto note = [&](const Item& m, const Row& r) {
-      if (m.isv) return;
-      const uint32_t mask = __ballot_sync(0xffffffffu, r.at >= 0);
-      if (lane == 0) c.mask[(seq + m.tile) % kMasks][w] = mask;
-    };
-    if constexpr (!Q8) {
-      int page = look(0), next = look(1);
-#pragma unroll 1
-      for (int i = 0; i < 2 * n; ++i, ++it) {
-        const Item m = item_of(i, n, two);
-        const Row row = row_of(i, page);
-        const char* const base = m.isv ? a.vc : a.kc;
-        page = next;
-        next = look(i + 2);
-        if (!acquire()) return false;
-        note(m, row);
-        const uint32_t dst = smem_addr(ring) + it % S::kStages * S::kStage;
-#pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-          const int r = p * kPer + sub;
-          const int64_t at = __shfl_sync(0xffffffffu, row.at, r);
-          cp_async16(dst + place<S::kPanel>(w * kRowsW + r, u),
-                     base + (at >= 0 ? at * 2 + u * 16 : 0), at >= 0);
-        }
-        // (arrives when the thread's copies have; the products' warp orders them
-        // before its own reads)
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                         smem_addr(&c.full[it % S::kStages]))
-                     : "memory");
-      }
-    } else {
-      // An item's values are requested while the one before it is converted, their
-      // scales an item earlier, its pages another one.
-      uint4 v[kPasses];
-      auto fetch = [&](const Item& m, const Row& row) {
-        const char* const base = m.isv ? a.vc : a.kc;
-#pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-          const int64_t at = __shfl_sync(0xffffffffu, row.at, p * kPer + sub);
-          v[p] = at >= 0 ? ldg16(base + at + u * 16) : make_uint4(0u, 0u, 0u, 0u);
-        }
-      };
-      int page0 = look(0), page1 = look(1), page2 = look(2);
-      Row row = row_of(0, page0), next = row_of(1, page1);
-      fetch(item_of(0, n, two), row);
-#pragma unroll 1
-      for (int i = 0; i < 2 * n; ++i, ++it) {
-        const Item m = item_of(i, n, two);
-        const Row after = row_of(i + 2, page2);
-        page2 = look(i + 3);
-        if (!acquire()) return false;
-        note(m, row);
-        unsigned char* const dst = ring + it % S::kStages * S::kStage;
-#pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-          const int r = p * kPer + sub;
-          const float k = __shfl_sync(0xffffffffu, row.f, r);
-          uint32_t o[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float y[4];
-            unpack_e4m3x4((&v[p].x)[e], y);
-            o[2 * e] = pack_bf16x2(y[0] * k, y[1] * k);
-            o[2 * e + 1] = pack_bf16x2(y[2] * k, y[3] * k);
-          }
-          *reinterpret_cast<uint4*>(dst + place<S::kPanel>(w * kRowsW + r, 2 * u)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(dst + place<S::kPanel>(w * kRowsW + r, 2 * u + 1)) =
-              make_uint4(o[4], o[5], o[6], o[7]);
-        }
-        fence_proxy_async();
-        mbar_arrive(&c.full[it % S::kStages]);
-        row = next, next = after;
-        if (i + 1 < 2 * n) fetch(item_of(i + 1, n, two), row);
-      }
+  // The items one after the other, over the run's segments: pages are looked up, and
+  // scales and (in 8 bits) values requested, some items before they are needed.
+  Seg s;
+  int i = 0, n = 0, seq = 0;
+  bool more = true;
+  auto next = [&]() {
+    Piece p = {-1, 0, 0, 0, false, false, false};
+    if (more && i == 2 * n) {
+      seq += n;
+      i = 0;
+      more = segment<D>(x, run, s);
+      n = more ? s.j1 - s.j0 : 0;
     }
-    seq += n;
+    if (!more) return p;
+    const Item m = item_of(i++, n, S::NT == 2 && !s.pair);
+    const int pos = (s.j0 + m.tile) * S::kN + w * kRowsW + lane;
+    p.h = s.h;
+    p.seq = seq + m.tile;
+    p.isv = m.isv;
+    p.there = true;
+    if (lane < kRowsW && pos < s.prefix) {
+      const int at = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
+      p.tok = a.page_shift >= 0 ? pos & (a.page_size - 1) : pos - at * a.page_size;
+      p.row = true;
+      p.page = a.table[(int64_t)s.first * a.table_rs + at];
+    }
+    return p;
+  };
+  auto row_of = [&](const Piece& p) {
+    Row r = {-1, 0.0f};
+    if (p.row && (uint32_t)p.page >= (uint32_t)a.num_pages) {
+      if (!p.isv) flag_error(a.dev_err, CCONV_DERR_PAGE);
+    } else if (p.row) {
+      r.at = p.page * a.s_page + p.tok * a.s_tok + (int64_t)p.h * a.s_head;
+      if constexpr (Q8)
+        r.f = q8_scale((p.isv ? a.vsc : a.ksc)[p.page * a.c_page + p.tok * a.c_tok +
+                                               (int64_t)p.h * a.c_head]);
+    }
+    return r;
+  };
+  auto note = [&](const Piece& p, const Row& row) {
+    if (p.isv) return;
+    const uint32_t mask = __ballot_sync(0xffffffffu, row.at >= 0);
+    if (lane == 0) c.mask[p.seq % kMasks][w] = mask;
+  };
+  if constexpr (!Q8) {
+    Piece now = next(), then = next();
+#pragma unroll 1
+    for (int it = 0; now.there; ++it) {
+      const int st = it % S::kStages;
+      const Row row = row_of(now);
+      const Piece after = next();
+      const char* const base = now.isv ? a.vc : a.kc;
+      if (!wait(&c.empty[st], (it / S::kStages & 1) ^ 1)) return false;
+      note(now, row);
+      const uint32_t dst = smem_addr(ring) + st * S::kStage;
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int r = p * kPer + sub;
+        const int64_t at = __shfl_sync(0xffffffffu, row.at, r);
+        cp_async16(dst + place<S::kPanel>(w * kRowsW + r, u),
+                   base + (at >= 0 ? at * 2 + u * 16 : 0), at >= 0);
+      }
+      // (arrives when the thread's copies have; the products' warp orders them before
+      // its own reads)
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                       smem_addr(&c.full[st]))
+                   : "memory");
+      now = then, then = after;
+    }
+  } else {
+    // An item's values are requested while the one before it is converted, their
+    // scales an item earlier, its pages another one.
+    uint4 v[kPasses];
+    auto fetch = [&](const Piece& p, const Row& row) {
+      const char* const base = p.isv ? a.vc : a.kc;
+#pragma unroll
+      for (int k = 0; k < kPasses; ++k) {
+        const int64_t at = __shfl_sync(0xffffffffu, row.at, k * kPer + sub);
+        v[k] = at >= 0 ? ldg16(base + at + u * 16) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    Piece now = next(), then = next(), later = next();
+    Row row = row_of(now), row1 = row_of(then);
+    fetch(now, row);
+#pragma unroll 1
+    for (int it = 0; now.there; ++it) {
+      const int st = it % S::kStages;
+      const Row row2 = row_of(later);
+      const Piece after = next();
+      if (!wait(&c.empty[st], (it / S::kStages & 1) ^ 1)) return false;
+      note(now, row);
+      unsigned char* const dst = ring + st * S::kStage;
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int r = p * kPer + sub;
+        const float k = __shfl_sync(0xffffffffu, row.f, r);
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float y[4];
+          unpack_e4m3x4((&v[p].x)[e], y);
+          o[2 * e] = pack_bf16x2(y[0] * k, y[1] * k);
+          o[2 * e + 1] = pack_bf16x2(y[2] * k, y[3] * k);
+        }
+        *reinterpret_cast<uint4*>(dst + place<S::kPanel>(w * kRowsW + r, 2 * u)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + place<S::kPanel>(w * kRowsW + r, 2 * u + 1)) =
+            make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      fence_proxy_async();
+      mbar_arrive(&c.full[st]);
+      now = then, then = later, later = after;
+      row = row1, row1 = row2;
+      fetch(now, row);
+    }
   }
   return true;
 }
@@ -441,8 +465,8 @@ __device__ __forceinline__ bool mma_role(const PrefixArgs& x, Run run, Ctl& c, u
     if (tc::elect()) tc::commit(&c.empty[i % S::kStages]);
     __syncwarp();
   };
-  while (run.p < run.end) {
-    const Seg s = segment<D>(x, run);
+  Seg s;
+  while (segment<D>(x, run, s)) {
     const int n = s.j1 - s.j0;
     if (!wait(&c.q_full[0], segs[0]++)) return false;
     if (s.pair && !wait(&c.q_full[1], segs[1]++)) return false;
@@ -538,46 +562,53 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
   const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
   int tiles_done = 0, segs = 0, seq = 0;
   bool ok = true;
-  while (run.p < run.end) {
-    const Seg s = segment<D>(x, run);
+  auto valid_of = [&](const Seg& s) { return s.rows - (s.pair ? stream * 128 : 0); };
+  // A segment's Q (the even and the odd tiles of one row tile share the first stream's):
+  // of the warp's 32 rows lane i knows where row i begins.
+  auto load_q = [&](const Seg& s) {
+    if (stream > 0 && !s.pair) return;
+    unsigned char* const to = q_all + stream * S::kQ;
+    const int lane = r & 31, w = r >> 5;
+    int64_t mine = -1;
+    if (r < valid_of(s)) {
+      const uint32_t R = (uint32_t)(s.row0 + stream * 128 + r), b = R / (uint32_t)rows_all;
+      const uint32_t k = R - b * (uint32_t)rows_all, tok = k / (uint32_t)a.G;
+      mine = ((int64_t)(s.first + (int)b) * a.q_len + tok) * a.q_rs +
+             (int64_t)(s.h * a.G + (int)(k - tok * a.G)) * D;
+    }
+    constexpr int kLanes = D / 8, kPer = 32 / kLanes, kBatch = 8;
+#pragma unroll 1
+    for (int p0 = 0; p0 < 32 / kPer; p0 += kBatch) {
+      uint4 v[kBatch];
+#pragma unroll
+      for (int p = 0; p < kBatch; ++p) {
+        const int64_t at = __shfl_sync(0xffffffffu, mine, (p0 + p) * kPer + lane / kLanes);
+        v[p] = at >= 0 ? ldg16(a.q + at * 2 + lane % kLanes * 16) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int p = 0; p < kBatch; ++p) {
+        v[p].x ^= flip, v[p].y ^= flip, v[p].z ^= flip, v[p].w ^= flip;
+        const int row = w * 32 + (p0 + p) * kPer + lane / kLanes;
+        *reinterpret_cast<uint4*>(to + place<S::kPanelQ>(row, lane % kLanes)) = v[p];
+      }
+    }
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c.q_full[stream]);
+  };
+  Seg s;
+  bool more = segment<D>(x, run, s);
+  if (more) load_q(s);
+  while (more) {
     const int n = s.j1 - s.j0;
     const bool two = S::NT == 2 && !s.pair;
-    const int step = two ? 2 : 1, t_first = two ? stream : 0;
+    const int step = two ? 2 : 1, t_first = two ? stream : 0, valid = valid_of(s);
     if (!ok || t_first >= n) {              // (given up, or no tile for this stream)
       empty_part<D>(x, s, stream);
       seq += n;
+      more = segment<D>(x, run, s);
+      if (more && ok) load_q(s);
       continue;
-    }
-    const int valid = s.rows - (two ? 0 : stream * 128);
-    if (!two || stream == 0) {
-      // the warp's 32 rows: lane i knows where row i begins
-      unsigned char* const to = q_all + stream * S::kQ;
-      const int lane = r & 31, w = r >> 5;
-      int64_t mine = -1;
-      if (r < valid) {
-        const int64_t R = s.row0 + stream * 128 + r, b = R / rows_all;
-        const int k = (int)(R - b * rows_all);
-        mine = ((s.g.first + b) * a.q_len + k / a.G) * a.q_rs + (int64_t)(s.h * a.G + k % a.G) * D;
-      }
-      constexpr int kLanes = D / 8, kPer = 32 / kLanes, kBatch = 8;
-#pragma unroll 1
-      for (int p0 = 0; p0 < 32 / kPer; p0 += kBatch) {
-        uint4 v[kBatch];
-#pragma unroll
-        for (int p = 0; p < kBatch; ++p) {
-          const int64_t at = __shfl_sync(0xffffffffu, mine, (p0 + p) * kPer + lane / kLanes);
-          v[p] = at >= 0 ? ldg16(a.q + at * 2 + lane % kLanes * 16) : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int p = 0; p < kBatch; ++p) {
-          v[p].x ^= flip, v[p].y ^= flip, v[p].z ^= flip, v[p].w ^= flip;
-          const int row = w * 32 + (p0 + p) * kPer + lane / kLanes;
-          *reinterpret_cast<uint4*>(to + place<S::kPanelQ>(row, lane % kLanes)) = v[p];
-        }
-      }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c.q_full[stream]);
     }
     const bool idle = (r & ~31) >= valid;    // no row of this warp's: nobody reads its sums
     float m = -INFINITY, l = 0.0f;          // (m: what the weights are relative to)
@@ -687,20 +718,24 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
     seq += n;
     if (!ok) {
       empty_part<D>(x, s, stream);
+      more = segment<D>(x, run, s);
       continue;
     }
     tc::fence_after();
+    // (every product with this Q has ended with the sums: the next one's scores are
+    // made while these are stored)
     const int64_t row = s.slot * S::kRowsU + stream * 128 + r;
-    const bool mine = r < valid;
+    more = segment<D>(x, run, s);
+    if (more) load_q(s);
     float* const o = x.po + row * D;
 #pragma unroll 1
-    for (int k = 0; k < (idle ? 0 : D); k += 16) {
-      uint32_t v[16];
-      tc::ld16(oc + k, v);
+    for (int k = 0; k < (idle ? 0 : D); k += 32) {
+      uint32_t v[32];
+      tc::ld32(oc + k, v);
       tc::wait_ld(v);
-      if (mine)
+      if (r < valid)
 #pragma unroll
-        for (int e = 0; e < 16; e += 4)
+        for (int e = 0; e < 32; e += 4)
           *reinterpret_cast<uint4*>(o + k + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
     }
     tc::fence_before();           // (before this stream's next sums begin)
@@ -776,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
 template <int D, int W>
 __global__ void __launch_bounds__(256) attn_shared_join_kernel(const PrefixArgs x, const int n) {
   using S = Shape<D>;
-  constexpr int kPairs = D / 64, kAhead = D == 256 ? 4 : 8, kRowsB = 8 / W;
+  constexpr int kPairs = D / 64, kBatch = D == 256 ? 4 : 8, kRowsB = 8 / W;
   const AttnArgs& a = x.a;
   __shared__ float sums[W > 1 ? 8 : 1][W > 1 ? D + 2 : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % W;
@@ -816,7 +851,7 @@ __global__ void __launch_bounds__(256) attn_shared_join_kernel(const PrefixArgs 
   if (g >= 0) {
     if (rec.unit < 0) return;                     // (groups that overlap: reported)
     const int64_t R = (int64_t)(b - s.first) * rows_all + rr, mt = R / S::kRowsU;
-    const int64_t u = mt * a.Hkv + h, line = rec.line + u * s.tiles;
+    const int64_t u = mt * a.Hkv + h, line = rec.line + u * (s.tiles + kAhead) + kAhead;
     const int64_t grid = min((int64_t)x.grid, total);
     const int p0 = attn_block_of(line, total, grid);
     const int p1 = attn_block_of(line + s.tiles - 1, total, grid);
@@ -848,11 +883,11 @@ __global__ void __launch_bounds__(256) attn_shared_join_kernel(const PrefixArgs 
     // (a row of NaN scores has a sum without a maximum)
     l += ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.0f) : f * ml.y;
     const int end = min(32, mine - i0);
-    for (int k0 = 0; k0 < end; k0 += kAhead) {
-      float2 v[kAhead][kPairs];
-      float wk[kAhead];
+    for (int k0 = 0; k0 < end; k0 += kBatch) {
+      float2 v[kBatch][kPairs];
+      float wk[kBatch];
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q) {
+      for (int q = 0; q < kBatch; ++q) {
         wk[q] = __shfl_sync(0xffffffffu, f, (k0 + q) & 31);
         const bool in = k0 + q < end && wk[q] != 0.0f;      // (empty parts are not written)
         const float* p = in ? values((i0 + k0 + q) * W + w0) : nullptr;
@@ -862,7 +897,7 @@ __global__ void __launch_bounds__(256) attn_shared_join_kernel(const PrefixArgs 
                        : make_float2(0.0f, 0.0f);
       }
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q)
+      for (int q = 0; q < kBatch; ++q)
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
           acc[j][0] = fmaf(wk[q], v[q][j].x, acc[j][0]);
