@@ -465,46 +465,56 @@ __device__ __forceinline__ bool mma_role(const PrefixArgs& x, Run run, Ctl& c, u
     if (tc::elect()) tc::commit(&c.empty[i % S::kStages]);
     __syncwarp();
   };
+  // (read from one lane, as below: the products take their operands from uniform
+  // registers, where the compiler keeps what it knows to be the same in the warp)
+  auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
   Seg s;
-  while (segment<D>(x, run, s)) {
-    const int n = s.j1 - s.j0;
+  while (same(segment<D>(x, run, s))) {
+    const int n = same(s.j1 - s.j0);
+    const bool pair = same(s.pair);
     if (!wait(&c.q_full[0], segs[0]++)) return false;
-    if (s.pair && !wait(&c.q_full[1], segs[1]++)) return false;
+    if (pair && !wait(&c.q_full[1], segs[1]++)) return false;
     if (!filled(it)) return false;
     tc::fence_after();
-    if (s.pair || S::NT == 1) {
-      const int streams = s.pair ? 2 : 1;
-      for (int k = 0; k < streams; ++k) scores(k, k, it);
+    if (pair || S::NT == 1) {
+      scores(0, 0, it);
+      if (pair) scores(1, 1, it);
       release(it++);
 #pragma unroll 1
       for (int t = 0; t < n; ++t) {             // items: V of tile t, K of the next
         const bool more = t + 1 < n;
-        if (!filled(it)) return false;
-        for (int k = 0; k < streams; ++k) {
-          if (!values(k, it, t == 0, !more)) return false;
-          if (k + 1 == streams) release(it);
-          if (more) {
-            if (k == 0 && !filled(it + 1)) return false;
-            scores(k, k, it + 1);
-          }
+        if (!filled(it) || !values(0, it, t == 0, !more)) return false;
+        if (more) {
+          if (!filled(it + 1)) return false;
+          scores(0, 0, it + 1);
         }
-        ++it;
-        if (more) release(it++);
+        if (pair && !values(1, it, t == 0, !more)) return false;
+        release(it++);
+        if (more) {
+          if (pair) scores(1, 1, it);
+          release(it++);
+        }
       }
     } else {
-      for (int t = 0; t < min(n, 2); ++t) {
+      scores(0, 0, it);
+      release(it++);
+      if (n > 1) {
         if (!filled(it)) return false;
-        scores(t, 0, it);
+        scores(1, 0, it);
         release(it++);
       }
 #pragma unroll 1
-      for (int t = 0; t < n; ++t) {
-        if (!filled(it) || !values(t & 1, it, t < 2, t + 2 >= n)) return false;
-        release(it++);
-        if (t + 2 < n) {
-          if (!filled(it)) return false;
-          scores(t & 1, 0, it);
+      for (int t = 0; t < n; t += 2) {          // a tile of each stream
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (t + k >= n) break;
+          if (!filled(it) || !values(k, it, t == 0, t + k + 2 >= n)) return false;
           release(it++);
+          if (t + k + 2 < n) {
+            if (!filled(it)) return false;
+            scores(k, 0, it);
+            release(it++);
+          }
         }
       }
     }
