@@ -573,20 +573,23 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
   int tiles_done = 0, segs = 0, seq = 0;
   bool ok = true;
   auto valid_of = [&](const Seg& s) { return s.rows - (s.pair ? stream * 128 : 0); };
-  // A segment's Q (the even and the odd tiles of one row tile share the first stream's):
-  // of the warp's 32 rows lane i knows where row i begins.
-  auto load_q = [&](const Seg& s) {
-    if (stream > 0 && !s.pair) return;
-    unsigned char* const to = q_all + stream * S::kQ;
-    const int lane = r & 31, w = r >> 5;
+  // Where row r of a segment's Q begins (-1: no row; the even and the odd tiles of one
+  // row tile share the first stream's).
+  auto q_row = [&](const Seg& s) {
     int64_t mine = -1;
-    if (r < valid_of(s)) {
+    if (r < valid_of(s) && (stream == 0 || s.pair)) {
       const uint32_t R = (uint32_t)(s.row0 + stream * 128 + r), b = R / (uint32_t)rows_all;
       const uint32_t k = R - b * (uint32_t)rows_all, tok = k / (uint32_t)a.G;
       mine = ((int64_t)(s.first + (int)b) * a.q_len + tok) * a.q_rs +
              (int64_t)(s.h * a.G + (int)(k - tok * a.G)) * D;
     }
-    constexpr int kLanes = D / 8, kPer = 32 / kLanes, kBatch = 8;
+    return mine;
+  };
+  // Q of the warp's 32 rows, of which lane i knows where row i begins.
+  unsigned char* const q_mine = q_all + stream * S::kQ;
+  const int lane = r & 31, w = r >> 5;
+  auto load_q = [&](int64_t mine) {
+    constexpr int kLanes = D / 8, kPer = 32 / kLanes, kBatch = D == 64 ? 8 : 16;
 #pragma unroll 1
     for (int p0 = 0; p0 < 32 / kPer; p0 += kBatch) {
       uint4 v[kBatch];
@@ -599,25 +602,31 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
       for (int p = 0; p < kBatch; ++p) {
         v[p].x ^= flip, v[p].y ^= flip, v[p].z ^= flip, v[p].w ^= flip;
         const int row = w * 32 + (p0 + p) * kPer + lane / kLanes;
-        *reinterpret_cast<uint4*>(to + place<S::kPanelQ>(row, lane % kLanes)) = v[p];
+        *reinterpret_cast<uint4*>(q_mine + place<S::kPanelQ>(row, lane % kLanes)) = v[p];
       }
     }
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(&c.q_full[stream]);
   };
-  Seg s;
-  bool more = segment<D>(x, run, s);
-  if (more) load_q(s);
+  Seg s, next;
+  bool more = segment<D>(x, run, next);
+  int64_t q_at = more ? q_row(next) : -1;
   while (more) {
+    s = next;
     const int n = s.j1 - s.j0;
     const bool two = S::NT == 2 && !s.pair;
     const int step = two ? 2 : 1, t_first = two ? stream : 0, valid = valid_of(s);
+    if (ok && (stream == 0 || s.pair)) load_q(q_at);
+    // the next segment's rows of Q come to the L2 meanwhile
+    more = segment<D>(x, run, next);
+    q_at = more ? q_row(next) : -1;
+    if (q_at >= 0)
+      for (int k = 0; k < D * 2; k += 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + q_at * 2 + k));
     if (!ok || t_first >= n) {              // (given up, or no tile for this stream)
       empty_part<D>(x, s, stream);
       seq += n;
-      more = segment<D>(x, run, s);
-      if (more && ok) load_q(s);
       continue;
     }
     const bool idle = (r & ~31) >= valid;    // no row of this warp's: nobody reads its sums
@@ -728,28 +737,37 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
     seq += n;
     if (!ok) {
       empty_part<D>(x, s, stream);
-      more = segment<D>(x, run, s);
       continue;
     }
     tc::fence_after();
-    // (every product with this Q has ended with the sums: the next one's scores are
-    // made while these are stored)
-    const int64_t row = s.slot * S::kRowsU + stream * 128 + r;
-    more = segment<D>(x, run, s);
-    if (more) load_q(s);
-    float* const o = x.po + row * D;
+    // Sums go out by whole lines, 32 columns at a time, through the place of the warp's
+    // rows of Q (every product with this Q has ended with the sums): a row a thread
+    // writes 32 lines an instruction, which took 4 us.
+    const int64_t row0 = s.slot * S::kRowsU + stream * 128 + w * 32;
+    const int rows = min(max(valid - w * 32, 0), 32);
 #pragma unroll 1
     for (int k = 0; k < (idle ? 0 : D); k += 32) {
       uint32_t v[32];
       tc::ld32(oc + k, v);
       tc::wait_ld(v);
-      if (r < valid)
+      unsigned char* const at = q_mine + (k / 32 % (D / 64)) * S::kPanelQ + w * 32 * 128;
+      __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<uint4*>(o + k + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+      for (int e = 0; e < 8; ++e)
+        *reinterpret_cast<uint4*>(at + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+            make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int rr = e * 4 + (lane >> 3), u = lane & 7;
+        const uint4 o = *reinterpret_cast<const uint4*>(at + rr * 128 + ((u ^ (rr & 7)) << 4));
+        if (rr < rows)
+          *reinterpret_cast<uint4*>(x.po + (row0 + rr) * D + k + u * 4) = o;
+      }
     }
+    __syncwarp();
     tc::fence_before();           // (before this stream's next sums begin)
-    x.ps[row] = make_float2(m * 0.6931471805599453f, l);
+    x.ps[row0 + lane] = make_float2(m * 0.6931471805599453f, l);
   }
   return ok;
 }
@@ -923,7 +941,7 @@ __global__ void __launch_bounds__(256) attn_shared_join_kernel(const PrefixArgs 
       *reinterpret_cast<float2*>(&sums[warp][j * 64 + lane * 2]) =
           make_float2(acc[j][0], acc[j][1]);
     if (lane == 0) sums[warp][D] = l;
-    __syncthreads();
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / W), "n"(W * 32) : "memory");   // the row's
     if (w0 != 0) return;
 #pragma unroll
     for (int k = 1; k < W; ++k) {
@@ -995,8 +1013,9 @@ template <int D>
 cudaError_t launch_shared_join(const PrefixArgs& x, cudaStream_t st) {
   const int n = x.a.B * x.a.Hq * x.a.q_len;
   // a warp a row where that fills the GPU, else a block's eight
-  return n >= 4096 ? attn_launch_beside(attn_shared_join_kernel<D, 1>, x, n, (n + 7) / 8, 256, 0, st)
-                   : attn_launch_beside(attn_shared_join_kernel<D, 8>, x, n, n, 256, 0, st);
+  return n >= 8192   ? attn_launch_beside(attn_shared_join_kernel<D, 1>, x, n, (n + 7) / 8, 256, 0, st)
+         : n >= 2048 ? attn_launch_beside(attn_shared_join_kernel<D, 2>, x, n, (n + 3) / 4, 256, 0, st)
+                     : attn_launch_beside(attn_shared_join_kernel<D, 8>, x, n, n, 256, 0, st);
 }
 
 // What both entry points check and do; a's cache is set.
