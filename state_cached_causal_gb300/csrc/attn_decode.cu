@@ -423,7 +423,7 @@ int decode(AttnArgs& a, int D, bool q8, const void* q, int64_t q_row_stride,
     return CCONV_ERR_INVALID;
   const int sms = mix_sm_count();
   if (sms <= 0) return CCONV_ERR_LAUNCH;
-  const AttnPlan p = attn_plan(dtype, sms, num_seqs, 1 + n_spec, num_q_heads / a.Hkv, a.Hkv, D);
+  const AttnPlan p = attn_plan(dtype, q8, sms, num_seqs, 1 + n_spec, num_q_heads / a.Hkv, a.Hkv, D);
   if (!workspace || !mix_aligned16(workspace) || workspace_bytes < p.bytes)
     return CCONV_ERR_INVALID;
   attn_fill(a, p, D, q8 ? 1 : 2, q, q_row_stride, block_table, block_table_row_stride, table_width,
@@ -462,9 +462,10 @@ extern "C" int64_t attn_decode_workspace_bytes(int32_t num_seqs, int32_t n_spec,
   const int sms = mix_sm_count();
   if (sms <= 0) return CCONV_ERR_LAUNCH;
   int64_t most = 0;
+  // (a cache in 8 bits has no larger grid)
   for (const int dtype : {CCONV_DTYPE_F32, CCONV_DTYPE_BF16})
-    most = std::max(most, attn_plan(dtype, sms, num_seqs, 1 + n_spec, num_q_heads / num_kv_heads,
-                               num_kv_heads, head_dim).bytes);
+    most = std::max(most, attn_plan(dtype, false, sms, num_seqs, 1 + n_spec,
+                                    num_q_heads / num_kv_heads, num_kv_heads, head_dim).bytes);
   return most;
 }
 

@@ -49,9 +49,10 @@ struct AttnArgs {
 };
 
 // Blocks of the bf16 kernels that an SM holds at once, by their registers and
-// shared memory (50 to 218 KB).
-__host__ __device__ constexpr int attn_mma_blocks(int D, int rows) {
-  return D * rows >= 4096 ? 1 : D * rows >= 2048 ? 2 : 3;
+// shared memory (50 to 218 KB). A block of the kernel over a cache in 8 bits has a
+// warp more.
+__host__ __device__ constexpr int attn_mma_blocks(int D, int rows, bool q8) {
+  return D * rows >= 4096 ? 1 : D * rows >= 2048 || q8 ? 2 : 3;
 }
 
 // Length of request b; -1 for one that is skipped.
@@ -240,7 +241,8 @@ struct AttnPlan {
   int hw, rblocks, rows, units, grid;
   int64_t meta_bytes, bytes;
 };
-inline AttnPlan attn_plan(int dtype, int sms, int64_t B, int q_len, int G, int Hkv, int D) {
+inline AttnPlan attn_plan(int dtype, bool q8, int sms, int64_t B, int q_len, int G, int Hkv,
+                          int D) {
   AttnPlan p;
   const int rows = G * q_len;
   p.hw = 1;
@@ -251,7 +253,7 @@ inline AttnPlan attn_plan(int dtype, int sms, int64_t B, int q_len, int G, int H
     // row tiles whose sums fit in registers
     p.rows = rows <= 16 || D == 256 ? 16 : 32;
     p.hw = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
-    p.grid = sms * attn_mma_blocks(D, p.rows);
+    p.grid = sms * attn_mma_blocks(D, p.rows, q8);
   }
   p.grid = std::min(p.grid, kAttnMaxGrid);
   p.rblocks = (rows + p.rows - 1) / p.rows;

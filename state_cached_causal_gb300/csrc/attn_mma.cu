@@ -523,7 +523,7 @@ cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
   int stages = D == 64 ? 4 : 3;
   // as many as let the grid's blocks of an SM all be there (228 KB, less what the
   // kernel has besides)
-  const int most = 228 * 1024 / attn_mma_blocks(D, MT * 16) - 3 * 1024;
+  const int most = 228 * 1024 / attn_mma_blocks(D, MT * 16, false) - 3 * 1024;
   while (stages > 2 && stages * stage + std::max(join, q) > most) --stages;
   const int smem = stages * stage + std::max(join, q);
   static std::atomic<uint64_t> full;

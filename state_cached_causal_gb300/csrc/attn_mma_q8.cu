@@ -16,10 +16,10 @@
 //   No spread of the scales then costs range. Weights are fp16, 2^15 times as large,
 //   so that those from 2^-29 of the largest on have all 11 bits. That is one rounding
 //   more than none: 2^-12 of a result, whose own is 2^-9.
-// - Scales are bytes that lie elsewhere; the copying warp reads those of a tile into
-//   registers while the tile before it is issued (their page a tile earlier still),
-//   and puts them beside the tile.
-// - A tile is 128 rows, two groups of 16 a warp, so that it has as many bytes.
+// - Scales are bytes that lie elsewhere; a warp of their own reads them into registers,
+//   two tiles before they are needed, and puts them beside the tile. (With the copies
+//   in one warp that warp's instructions were what bounded the kernel.)
+// - A tile is 128 rows, 32 a warp, so that it has as many bytes.
 #include "attn_decode.cuh"
 #include "q8.cuh"
 #include "tc.cuh"
@@ -30,9 +30,9 @@ namespace cconv {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kThreads = (kWarps + 1) * 32;   // and one warp that loads
+constexpr int kThreads = (kWarps + 2) * 32;   // and a warp for the copies, one for scales
 constexpr int kTile = 128;          // rows of a tile (positions x heads); 32 a warp
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 4;
 constexpr long long kWaitClocks = 4000000000LL;   // seconds; a copy takes microseconds
 constexpr float kLift = 15.0f;      // log2 of what weights are multiplied by
 
@@ -89,7 +89,7 @@ __device__ __noinline__ void settle(uint64_t* full, int stages, int st, int ph, 
 // MT row tiles of 16. Q stays in registers where it fits beside the sums, else
 // in shared memory.
 template <int D, int MT, bool SHARED>
-__global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16))
+__global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16, true))
     attn_mma_q8_kernel(const AttnArgs a, const int stages) {
   constexpr bool kQRegs = MT == 1;
   constexpr int kQPitch = D * 2 + 16;
@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16))
   __shared__ int64_t scan[kThreads + 4];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], met;
   __shared__ __align__(16) unsigned char there[kMaxStages][kTile];   // positions that hold a token
-  __shared__ __align__(16) unsigned char scales[kMaxStages][2][kTile];   // of K and V, head by head
+  // of K: its rows' powers of two; of V: their exponents; head by head
+  __shared__ __align__(16) float scales[kMaxStages][2][kTile];
   __shared__ float row_x[kWarps][MT * 16];          // powers of two of Q's rows
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // position x of a tile lies at off(x) of its place: rows of a group side by side
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16))
   unsigned char* const sq = behind + warp * (MT * 16 * kQPitch);
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], 2);
       mbar_init(&empty[i], kWarps);
     }
     mbar_init(&met, kWarps);
@@ -139,48 +140,17 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16))
       const AttnSeg s = attn_segment<SHARED>(a, tpos, run);
       attn_advance(a, s, run);
       const int32_t* tab = a.table + (int64_t)s.b * a.table_rs;
-      const int head0 = s.unit / a.rblocks * a.hw;
-      const char* const src0 = (isv ? a.vc : a.kc) + (int64_t)(head0 + piece) * a.s_head;
+      const char* const src0 = (isv ? a.vc : a.kc) +
+                               (int64_t)(s.unit / a.rblocks * a.hw + piece) * a.s_head;
       // page of position pos, as the table has it
       auto look = [&](int pos, bool in) {
         return in && pos < s.len ? tab[a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size]
                                  : -1;
       };
-      auto token = [&](int pos) {
-        return a.page_shift >= 0 ? pos & (a.page_size - 1) : pos % a.page_size;
-      };
-      // scales: the lane has rows lane + 32 i of a tile, row r being position r % tpos of
-      // head r / tpos
-      const int r_mask = tpos - 1;
-      int spage[4];
-      uint32_t sc[4][2];
-      auto look_scales = [&](int j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          spage[i] = look(s.base + j * tpos + ((lane + 32 * i) & r_mask), j < s.j1);
-      };
-      auto load_scales = [&](int j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = lane + 32 * i;
-          sc[i][0] = sc[i][1] = 127;
-          if ((uint32_t)spage[i] < (uint32_t)a.num_pages) {
-            const int64_t at = spage[i] * a.c_page +
-                               token(s.base + j * tpos + (r & r_mask)) * a.c_tok +
-                               (int64_t)(head0 + r / tpos) * a.c_head;
-            sc[i][0] = a.ksc[at];
-            sc[i][1] = a.vsc[at];
-          }
-        }
-      };
-      look_scales(s.j0);
-      load_scales(s.j0);
-      look_scales(s.j0 + 1);
       int ahead = look(s.base + s.j0 * tpos + pl0, pl0 < tpos);
       for (int j = s.j0; j < s.j1; ++j) {
         const uint32_t place = st * 2 * half_stage;
         const int t0 = s.base + j * tpos;
-        if (!wait_bar(&empty[st], ph, a.dev_err)) return settle(full, stages, st, ph, a.dev_err);
         int pl = pl0;
         for (int p = 0; p < tpos; p += dpl, pl += dpl) {       // (p: of lane 0)
           const int pos = t0 + pl, page = ahead;
@@ -192,6 +162,8 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16))
             flag_error(a.dev_err, CCONV_DERR_PAGE);
             held = 0;
           }
+          if (p == 0 && !wait_bar(&empty[st], ph, a.dev_err))
+            return settle(full, stages, st, ph, a.dev_err);
           if (in) {
             // (positions before the request's first one are left out, too)
             const int skip = SHARED ? min(max(s.start - pos, 0), held) : 0;
@@ -199,10 +171,11 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16))
               for (int k = 0; k < group; ++k) there[st][pl + k] = k >= skip && k < held;
             unsigned char* const dst = dst0 + place + off(pl);
             if (held > skip) {
+              const int tok = a.page_shift >= 0 ? pos & (a.page_size - 1) : pos % a.page_size;
               const uint32_t n = (held - skip) * bytes;
               mbar_expect(&full[st], n);
-              bulk_load(dst + skip * bytes,
-                        src0 + page * a.s_page + (token(pos) + skip) * a.s_tok, n, &full[st]);
+              bulk_load(dst + skip * bytes, src0 + page * a.s_page + (tok + skip) * a.s_tok, n,
+                        &full[st]);
             }
             if (isv && held - skip < group) {
               for (uint32_t i = 0; i < group * bytes; i += 16)
@@ -212,20 +185,75 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16))
             }
           }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          scales[st][0][lane + 32 * i] = (unsigned char)sc[i][0];
-          scales[st][1][lane + 32 * i] = (unsigned char)sc[i][1];
-        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);
         if (++st == stages) st = 0, ph ^= 1;
-        load_scales(j + 1);             // (behind the segment: none)
-        look_scales(j + 2);
       }
     }
     if (SHARED && blockIdx.x == 0)        // (as in attn_mma.cu)
       asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  if (warp == kWarps + 1) {
+    // ---- scales: lane l has rows l, l + 32, .. of a tile, row r being position r % tpos
+    // of head r / tpos. Those of a tile are requested two tiles before it, their pages
+    // looked up one before that.
+    int st = 0, ph = 1;
+    while (run.p < run.end) {
+      const AttnSeg s = attn_segment<SHARED>(a, tpos, run);
+      attn_advance(a, s, run);
+      const int32_t* tab = a.table + (int64_t)s.b * a.table_rs;
+      const int head = s.unit / a.rblocks * a.hw;
+      int page[4];
+      auto look = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int pos = s.base + j * tpos + ((lane + 32 * i) & (tpos - 1));
+          page[i] = j < s.j1 && pos < s.len
+                        ? tab[a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size]
+                        : -1;
+        }
+      };
+      struct Bytes {
+        uint32_t k[4], v[4];
+      };
+      auto load = [&](int j) {
+        Bytes c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = lane + 32 * i, pos = s.base + j * tpos + (r & (tpos - 1));
+          c.k[i] = c.v[i] = 127;
+          if ((uint32_t)page[i] < (uint32_t)a.num_pages) {
+            const int tok = a.page_shift >= 0 ? pos & (a.page_size - 1) : pos % a.page_size;
+            const int64_t at =
+                page[i] * a.c_page + tok * a.c_tok + (int64_t)(head + r / tpos) * a.c_head;
+            c.k[i] = a.ksc[at];
+            c.v[i] = a.vsc[at];
+          }
+        }
+        return c;
+      };
+      look(s.j0);
+      Bytes c0 = load(s.j0);
+      look(s.j0 + 1);
+      Bytes c1 = load(s.j0 + 1);
+      look(s.j0 + 2);
+#pragma unroll 1
+      for (int j = s.j0; j < s.j1; ++j) {
+        const Bytes c2 = load(j + 2);
+        look(j + 3);
+        if (!wait_bar(&empty[st], ph, a.dev_err)) return settle(full, stages, st, ph, a.dev_err);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          scales[st][0][lane + 32 * i] = q8_scale(c0.k[i]);
+          scales[st][1][lane + 32 * i] = (float)c0.v[i] - 127.0f;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+        if (++st == stages) st = 0, ph ^= 1;
+        c0 = c1, c1 = c2;
+      }
+    }
     return;
   }
   int stage = 0, phase = 0, meets = 0;
@@ -336,162 +364,199 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16))
       const uint32_t place = smem_addr(attn_dyn) + stage * 2 * half_stage + hl * D;
       const int cur = stage;
       if (++stage == stages) stage = 0, phase ^= 1;
-#pragma unroll 1
-      for (int p0 = p_warp; p0 < p_warp + 32; p0 += 16) {
-        const uint32_t kb = place + off(p0), vb = kb + half_stage;
-        const unsigned char* const tr = there[cur] + p0;
-        const unsigned char* const ksb = scales[cur][0] + hl * tpos + p0;
-        const unsigned char* const vsb = scales[cur][1] + hl * tpos + p0;
-        // ---- scores of 16 positions: two n-tiles of 8
-        float s[MT][2][4] = {};
-        const uint32_t ka =
-            kb + off((lane & 7) + ((lane >> 4) << 3)) + ((lane >> 3) & 1) * 16;
+      const uint32_t kb = place + off(p_warp), vb = kb + half_stage;
+      const unsigned char* const tr = there[cur] + p_warp;
+      const float* const ks = scales[cur][0] + hl * tpos + p_warp;
+      const float* const vs = scales[cur][1] + hl * tpos + p_warp;
+      // ---- scores of the warp's 32 positions: four n-tiles of 8
+      float s[MT][4][4] = {};
+      const uint32_t ka = kb + off((lane & 7) + ((lane >> 4) << 3)) + ((lane >> 3) & 1) * 16;
+      const uint32_t step16 = off(16);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ks += 2) {
-          uint32_t b[4];               // positions 0-7: bytes 0-15, 16-31; positions 8-15: the same
-          tc::ldmatrix4(b, ka + ks * 16);
+      for (int d = 0; d < D / 16; d += 2) {
+        uint32_t b[2][4];              // positions 0-7: bytes 0-15, 16-31; positions 8-15: the same
+        tc::ldmatrix4(b[0], ka + d * 16);
+        tc::ldmatrix4(b[1], ka + step16 + d * 16);
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const uint32_t b0 = e4m3x2_to_f16x2(b[t]), b1 = e4m3x2_to_f16x2(b[t] >> 16);
-            const uint32_t b2 = e4m3x2_to_f16x2(b[2 + t]), b3 = e4m3x2_to_f16x2(b[2 + t] >> 16);
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const uint32_t b0 = e4m3x2_to_f16x2(b[g][t]), b1 = e4m3x2_to_f16x2(b[g][t] >> 16);
+            const uint32_t b2 = e4m3x2_to_f16x2(b[g][2 + t]),
+                           b3 = e4m3x2_to_f16x2(b[g][2 + t] >> 16);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
               if constexpr (kQRegs) {
-                tc::mma16h(s[mt][0], q[mt][ks + t], b0, b1);
-                tc::mma16h(s[mt][1], q[mt][ks + t], b2, b3);
+                tc::mma16h(s[mt][2 * g], q[mt][d + t], b0, b1);
+                tc::mma16h(s[mt][2 * g + 1], q[mt][d + t], b2, b3);
               } else {
                 uint32_t qa[4];
                 tc::ldmatrix4(qa, smem_addr(sq) + (mt * 16 + (lane & 15)) * kQPitch +
-                                      (ks + t) * 32 + (lane >> 4) * 16);
-                tc::mma16h(s[mt][0], qa, b0, b1);
-                tc::mma16h(s[mt][1], qa, b2, b3);
+                                      (d + t) * 32 + (lane >> 4) * 16);
+                tc::mma16h(s[mt][2 * g], qa, b0, b1);
+                tc::mma16h(s[mt][2 * g + 1], qa, b2, b3);
               }
             }
           }
-        }
-        // the powers of two of the lane's four positions: q0 + {0, 1, 8, 9}
-        const int q0 = (lane & 3) * 2;
-        float kf[4], ve[4];
+      }
+      // the powers of two of the lane's eight positions: q0 + 8 n + {0, 1}
+      const int q0 = (lane & 3) * 2;
+      float ve[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int x = q0 + (i >> 1) * 8 + (i & 1);
-          kf[i] = q8_scale(ksb[x]);
-          ve[i] = (float)vsb[x] - 127.0f;
-        }
+      for (int n = 0; n < 4; ++n) {
+        const float2 kf = *reinterpret_cast<const float2*>(ks + q0 + 8 * n);
+        const float2 e = *reinterpret_cast<const float2*>(vs + q0 + 8 * n);
+        ve[2 * n] = e.x;
+        ve[2 * n + 1] = e.y;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            s[mt][i >> 2][i & 3] = s[mt][i >> 2][i & 3] * kf[(i >> 2) * 2 + (i & 1)] *
-                                   rf[mt][(i >> 1) & 1];
-        // ---- masks, running maxima, weights
-        const int pos0 = sg.base + j * tpos + p0;      // the first position
-        // Draft tokens' positions are hidden from the rows before them by a weight of
-        // zero, which a NaN among their values would get through: such values (`wild`)
-        // are kept out of the product and added to the rows that see them.
-        const int x0 = max(0, sg.len - a.q_len + 1 - pos0), x1 = min(16, sg.len - pos0);
-        bool wild = false;
-        if (x0 < x1) {
-          for (int x = x0; x < x1; ++x)
-            for (int i = lane; i < D / 4; i += 32)
-              wild |= nan_bytes(lds32(vb + off(x) + i * 4)) != 0;
-          wild = __any_sync(0xffffffffu, wild);
-        }
-        const uint4 all = *reinterpret_cast<const uint4*>(tr);
-        if (pos0 + 15 > sg.len - a.q_len ||
-            (all.x & all.y & all.z & all.w) != 0x01010101u) {
+          for (int i = 0; i < 4; ++i) s[mt][n][i] *= (i & 1 ? kf.y : kf.x);
+      }
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[mt][i >> 2][i & 3] *= rf[mt][(i >> 1) & 1];
+      // ---- masks, running maxima, weights
+      const int pos0 = sg.base + j * tpos + p_warp;    // the first position
+      // Draft tokens' positions are hidden from the rows before them by a weight of
+      // zero, which a NaN among their values would get through: such values (`wild`)
+      // are kept out of the product and added to the rows that see them.
+      const int x0 = max(0, sg.len - a.q_len + 1 - pos0), x1 = min(32, sg.len - pos0);
+      bool wild = false;
+      if (x0 < x1) {
+        for (int x = x0; x < x1; ++x)
+          for (int i = lane; i < D / 4; i += 32)
+            wild |= nan_bytes(lds32(vb + off(x) + i * 4)) != 0;
+        wild = __any_sync(0xffffffffu, wild);
+      }
+      const uint4 all = *reinterpret_cast<const uint4*>(tr);
+      const uint4 more = *reinterpret_cast<const uint4*>(tr + 16);
+      if (pos0 + 31 > sg.len - a.q_len ||
+          (all.x & all.y & all.z & all.w & more.x & more.y & more.z & more.w) != 0x01010101u) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int r = mt * 16 + half * 8 + (lane >> 2);
+            const int seen = r < rows ? sg.len - a.q_len + 1 + (r0 + r) / a.G : 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int x = q0 + (i >> 1) * 8 + (i & 1);
+              if (!tr[x] || pos0 + x >= seen) s[mt][i >> 1][half * 2 + (i & 1)] = -INFINITY;
+            }
+          }
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        uint32_t pw[2][4];
+        float corr[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float x[8], t[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[i] = s[mt][i >> 1][half * 2 + (i & 1)];
+            t[i] = x[i] + ve[i];
+          }
+          float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
+                           fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+          float tx = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])),
+                           fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, 2));
+          const float mn = fmaxf(m[mt][half], mx), tn = fmaxf(mv[mt][half], tx);
+          const float base = mn == -INFINITY ? 0.0f : mn, tbase = tn == -INFINITY ? 0.0f : tn;
+          corr[half] = tc::ex2(mv[mt][half] - tbase);
+          float sum = 0.0f, more_sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            sum += tc::ex2(x[i] - base);
+            more_sum += tc::ex2(x[i + 1] - base);
+          }
+          l[mt][half] = fmaf(l[mt][half], tc::ex2(m[mt][half] - base), sum + more_sum);
+          m[mt][half] = mn;
+          mv[mt][half] = tn;
+          const float up = tbase - kLift;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            pw[g][half] = pack_f16x2(tc::ex2(t[4 * g] - up), tc::ex2(t[4 * g + 1] - up));
+            pw[g][2 + half] = pack_f16x2(tc::ex2(t[4 * g + 2] - up), tc::ex2(t[4 * g + 3] - up));
+          }
+        }
+        if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            o[mt][n][0] *= corr[0];
+            o[mt][n][1] *= corr[0];
+            o[mt][n][2] *= corr[1];
+            o[mt][n][3] *= corr[1];
+          }
+        }
+        // ---- weighted values: of 16 dims, the even ones are one n-tile, the odd ones
+        // another
+        const uint32_t va = vb + off(lane & 15) + (lane >> 4) * 16;
+        if (!wild) {
+#pragma unroll
+          for (int n = 0; n < D / 16; n += 2) {
+            uint32_t b[2][4];          // dims 0-15: positions 0-7, 8-15; dims 16-31: the same
+            tc::ldmatrix4_trans(b[0], va + n * 16);
+            tc::ldmatrix4_trans(b[1], va + step16 + n * 16);
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                const uint32_t v0 = __byte_perm(b[g][2 * t], 0u, 0x3120),
+                               v1 = __byte_perm(b[g][2 * t + 1], 0u, 0x3120);
+                tc::mma16h(o[mt][2 * (n + t)], pw[g], e4m3x2_to_f16x2(v0), e4m3x2_to_f16x2(v1));
+                tc::mma16h(o[mt][2 * (n + t) + 1], pw[g], e4m3x2_to_f16x2(v0 >> 16),
+                           e4m3x2_to_f16x2(v1 >> 16));
+              }
+          }
+        } else {
+#pragma unroll 1
+          for (int g = 0; g < 2; ++g) {
+            const uint32_t pg[4] = {g ? pw[1][0] : pw[0][0], g ? pw[1][1] : pw[0][1],
+                                    g ? pw[1][2] : pw[0][2], g ? pw[1][3] : pw[0][3]};
+#pragma unroll
+            for (int n = 0; n < D / 16; n += 2) {
+              uint32_t b[4];
+              tc::ldmatrix4_trans(b, va + g * step16 + n * 16);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {        // positions 16 g + q0 + 8 (i & 1) + {0, 1}
+                const int x = 16 * g + q0 + (i & 1) * 8;
+                const uint32_t hidden =
+                    (x >= x0 ? 0x00ff00ffu : 0u) | (x + 1 >= x0 ? 0xff00ff00u : 0u);
+                b[i] = __byte_perm(b[i], 0u, 0x3120);
+                b[i] &= ~(nan_bytes(b[i]) & hidden);
+              }
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                tc::mma16h(o[mt][2 * (n + t)], pg, e4m3x2_to_f16x2(b[2 * t]),
+                           e4m3x2_to_f16x2(b[2 * t + 1]));
+                tc::mma16h(o[mt][2 * (n + t) + 1], pg, e4m3x2_to_f16x2(b[2 * t] >> 16),
+                           e4m3x2_to_f16x2(b[2 * t + 1] >> 16));
+              }
+            }
+          }
+#pragma unroll 1
+          for (int x = x0; x < x1; ++x)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               const int r = mt * 16 + half * 8 + (lane >> 2);
-              const int seen = r < rows ? sg.len - a.q_len + 1 + (r0 + r) / a.G : 0;
+              if (r >= rows || pos0 + x >= sg.len - a.q_len + 1 + (r0 + r) / a.G) continue;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int x = q0 + (i >> 1) * 8 + (i & 1);
-                if (!tr[x] || pos0 + x >= seen) s[mt][i >> 1][half * 2 + (i & 1)] = -INFINITY;
+              for (int n = 0; n < D / 16; ++n) {     // dims 16 n + 4 c + {0, 1, 2, 3}
+                const uint32_t v = nan_bytes(lds32(vb + off(x) + n * 16 + q0 * 2));
+                const float nan = __uint_as_float(0x7fc00000u);
+                if (v & 0xffu) o[mt][2 * n][half * 2] = nan;
+                if (v & 0xff00u) o[mt][2 * n + 1][half * 2] = nan;
+                if (v & 0xff0000u) o[mt][2 * n][half * 2 + 1] = nan;
+                if (v & 0xff000000u) o[mt][2 * n + 1][half * 2 + 1] = nan;
               }
             }
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          uint32_t pw[4];
-          float corr[2];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const float s0 = s[mt][0][half * 2], s1 = s[mt][0][half * 2 + 1],
-                        s2 = s[mt][1][half * 2], s3 = s[mt][1][half * 2 + 1];
-            const float t0 = s0 + ve[0], t1 = s1 + ve[1], t2 = s2 + ve[2], t3 = s3 + ve[3];
-            float mx = fmaxf(fmaxf(s0, s1), fmaxf(s2, s3)), tx = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, 2));
-            const float mn = fmaxf(m[mt][half], mx), tn = fmaxf(mv[mt][half], tx);
-            const float base = mn == -INFINITY ? 0.0f : mn, tbase = tn == -INFINITY ? 0.0f : tn;
-            corr[half] = tc::ex2(mv[mt][half] - tbase);
-            const float sum = (tc::ex2(s0 - base) + tc::ex2(s1 - base)) +
-                              (tc::ex2(s2 - base) + tc::ex2(s3 - base));
-            l[mt][half] = fmaf(l[mt][half], tc::ex2(m[mt][half] - base), sum);
-            m[mt][half] = mn;
-            mv[mt][half] = tn;
-            const float up = tbase - kLift;
-            pw[half] = pack_f16x2(tc::ex2(t0 - up), tc::ex2(t1 - up));
-            pw[2 + half] = pack_f16x2(tc::ex2(t2 - up), tc::ex2(t3 - up));
-          }
-          if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-              o[mt][n][0] *= corr[0];
-              o[mt][n][1] *= corr[0];
-              o[mt][n][2] *= corr[1];
-              o[mt][n][3] *= corr[1];
-            }
-          }
-          // ---- weighted values: of 16 dims, the even ones are one n-tile, the odd ones
-          // another
-          const uint32_t va = vb + off(lane & 15) + (lane >> 4) * 16;
-#pragma unroll
-          for (int n = 0; n < D / 16; n += 2) {
-            uint32_t b[4];             // dims 0-15: positions 0-7, 8-15; dims 16-31: the same
-            tc::ldmatrix4_trans(b, va + n * 16);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) b[i] = __byte_perm(b[i], 0u, 0x3120);
-            if (wild) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {        // positions q0 + 8 (i & 1) + {0, 1}
-                const int x = q0 + (i & 1) * 8;
-                const uint32_t hidden =
-                    (x >= x0 ? 0x00ff00ffu : 0u) | (x + 1 >= x0 ? 0xff00ff00u : 0u);
-                b[i] &= ~(nan_bytes(b[i]) & hidden);
-              }
-            }
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              tc::mma16h(o[mt][2 * (n + t)], pw, e4m3x2_to_f16x2(b[2 * t]),
-                         e4m3x2_to_f16x2(b[2 * t + 1]));
-              tc::mma16h(o[mt][2 * (n + t) + 1], pw, e4m3x2_to_f16x2(b[2 * t] >> 16),
-                         e4m3x2_to_f16x2(b[2 * t + 1] >> 16));
-            }
-          }
-          if (wild) {
-#pragma unroll 1
-            for (int x = x0; x < x1; ++x)
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const int r = mt * 16 + half * 8 + (lane >> 2);
-                if (r >= rows || pos0 + x >= sg.len - a.q_len + 1 + (r0 + r) / a.G) continue;
-#pragma unroll
-                for (int n = 0; n < D / 16; ++n) {     // dims 16 n + 4 c + {0, 1, 2, 3}
-                  const uint32_t v = nan_bytes(lds32(vb + off(x) + n * 16 + q0 * 2));
-                  const float nan = __uint_as_float(0x7fc00000u);
-                  if (v & 0xffu) o[mt][2 * n][half * 2] = nan;
-                  if (v & 0xff00u) o[mt][2 * n + 1][half * 2] = nan;
-                  if (v & 0xff0000u) o[mt][2 * n][half * 2 + 1] = nan;
-                  if (v & 0xff000000u) o[mt][2 * n + 1][half * 2 + 1] = nan;
-                }
-              }
-          }
         }
       }
       __syncwarp();
@@ -596,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16))
   }
 }
 
-static_assert(kTile == 32 * kWarps, "a warp takes two groups of 16 rows");
+static_assert(kTile == 32 * kWarps, "a warp takes 32 rows");
 
 template <int D, int MT, bool SHARED>
 cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
@@ -607,7 +672,7 @@ cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
   int stages = D == 64 ? 4 : 3;
   // as many as let the grid's blocks of an SM all be there (228 KB, less what the
   // kernel has besides)
-  const int most = 228 * 1024 / attn_mma_blocks(D, MT * 16) - 5 * 1024;
+  const int most = 228 * 1024 / attn_mma_blocks(D, MT * 16, true) - 10 * 1024;
   while (stages > 2 && stages * stage + std::max(join, q) > most) --stages;
   const int smem = stages * stage + std::max(join, q);
   static std::atomic<uint64_t> full;

@@ -126,7 +126,7 @@ __device__ __forceinline__ Group group_of(const AttnArgs& a, int g) {
 
 // A unit has kAhead more places on the line than tiles, before its first: a segment's
 // start (Q, the first copies) takes a block as long as so many tiles.
-constexpr int kAhead = 2;
+constexpr int kAhead = 3;
 
 struct Run {
   int64_t p, end, total, grid;
@@ -970,9 +970,10 @@ struct SharedPlan {
   AttnPlan own;
   int64_t max_units, part, rec, po, ps, bytes;    // offsets in bytes
 };
-SharedPlan shared_plan(int sms, int64_t B, int64_t groups, int q_len, int G, int Hkv, int D) {
+SharedPlan shared_plan(bool q8, int sms, int64_t B, int64_t groups, int q_len, int G, int Hkv,
+                       int D) {
   SharedPlan p;
-  p.own = attn_plan(CCONV_DTYPE_BF16, sms, B, q_len, G, Hkv, D);
+  p.own = attn_plan(CCONV_DTYPE_BF16, q8, sms, B, q_len, G, Hkv, D);
   auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
   const int rows = D == 256 ? 128 : 256;
   p.max_units = groups > 0 ? (B * G * q_len / rows + groups) * Hkv : 0;
@@ -1037,7 +1038,7 @@ int decode_shared(AttnArgs& a, int D, bool q8, const void* q, int64_t q_row_stri
   const int sms = mix_sm_count();
   if (sms <= 0) return CCONV_ERR_LAUNCH;
   const SharedPlan p =
-      shared_plan(sms, num_seqs, num_groups, 1 + n_spec, num_q_heads / a.Hkv, a.Hkv, D);
+      shared_plan(q8, sms, num_seqs, num_groups, 1 + n_spec, num_q_heads / a.Hkv, a.Hkv, D);
   if (!workspace || !mix_aligned16(workspace) || workspace_bytes < p.bytes)
     return CCONV_ERR_INVALID;
   attn_fill(a, p.own, D, q8 ? 1 : 2, q, q_row_stride, block_table, block_table_row_stride,
@@ -1088,7 +1089,8 @@ extern "C" int64_t attn_decode_shared_workspace_bytes(int32_t num_seqs, int32_t 
   if (rc != CCONV_OK) return rc;
   const int sms = mix_sm_count();
   if (sms <= 0) return CCONV_ERR_LAUNCH;
-  return shared_plan(sms, num_seqs, num_groups, 1 + n_spec, num_q_heads / num_kv_heads,
+  // (a cache in 8 bits has no larger grid)
+  return shared_plan(false, sms, num_seqs, num_groups, 1 + n_spec, num_q_heads / num_kv_heads,
                      num_kv_heads, head_dim).bytes;
 }
 
