@@ -251,7 +251,7 @@ inline AttnPlan attn_plan(int dtype, bool q8, int sms, int64_t B, int q_len, int
     p.grid = sms * (D == 64 ? 7 : D == 128 ? 5 : 2);   // blocks that an SM holds at once
   } else {
     // row tiles whose sums fit in registers
-    p.rows = rows <= 16 || D == 256 ? 16 : 32;
+    p.rows = q8 && rows <= 8 ? 8 : rows <= 16 || D == 256 ? 16 : 32;
     p.hw = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
     p.grid = sms * attn_mma_blocks(D, p.rows, q8);
   }

@@ -2,20 +2,26 @@
 // attn_decode.cuh, with the products on the warp-level tensor instruction (m16n8k16).
 //
 // It is built as the kernel over a cache in bf16 (attn_mma.cu: a warp that copies
-// positions into a ring, four that take 16 rows of a tile each), for half the bytes.
+// positions into a ring, four that take their rows of a tile each), for half the bytes.
 // What differs:
+// - The products are the transposed ones, S^T = K Q^T and O^T = V^T P^T, whose narrow
+//   side of 8 is the query rows': with 16 rows on the other side, half of the softmax
+//   and of the sums was of rows that do not exist where a kv head has 4 or 8. The weights
+//   are turned in registers (movmatrix). 256 requests 216 -> WW us.
 // - Values go to the products as fp16, which holds every e4m3 value, by one
 //   instruction a pair. (bf16 would hold them too; that conversion takes four.) The
 //   four bytes that ldmatrix leaves in a lane are two pairs of K's dims, so that Q is
 //   laid out to match, and of V two dims of two positions, whose bytes are brought
-//   beside one another first; the sums' columns then lie four side by side.
+//   beside one another first.
 // - Q as fp16 has the power of two of its row's largest value taken out. Scores are
 //   multiplied by that, by the scale and by their key's power of two.
-// - A value's power of two 2^e goes to its weight: weights are 2^(s + e - M), with M
-//   the running maximum of s + e, beside the running maximum m and sum of 2^(s - m).
-//   No spread of the scales then costs range. Weights are fp16, 2^15 times as large,
-//   so that those from 2^-29 of the largest on have all 11 bits. That is one rounding
-//   more than none: 2^-12 of a result, whose own is 2^-9.
+// - A value's power of two 2^e goes to its weight: weights are 2^(s + e - M + kLift), M
+//   a reference that follows the largest s + e (and is left until that has passed it
+//   by kSlack: lanes then need no more than a vote). The sum of 2^(s - M) is that of the
+//   weights times 2^-e. Where some |e| is over 40 that could leave fp32's range: from
+//   there on ("wide") the sum has a maximum of its own. Weights are fp16: 11 bits from
+//   2^-22 of the largest on, 2^-33 of it at least. That is one rounding more than none:
+//   2^-12 of a result, whose own is 2^-9.
 // - Scales are bytes that lie elsewhere; a warp of their own reads them into registers,
 //   two tiles before they are needed, and puts them beside the tile. (With the copies
 //   in one warp that warp's instructions were what bounded the kernel.)
@@ -34,7 +40,9 @@ constexpr int kThreads = (kWarps + 2) * 32;   // and a warp for the copies, one 
 constexpr int kTile = 128;          // rows of a tile (positions x heads); 32 a warp
 constexpr int kMaxStages = 4;
 constexpr long long kWaitClocks = 4000000000LL;   // seconds; a copy takes microseconds
-constexpr float kLift = 15.0f;      // log2 of what weights are multiplied by
+constexpr float kLift = 8.0f;       // log2 of what weights are multiplied by
+constexpr float kSlack = 7.0f;      // how far the largest may pass the reference (fp16: 2^16)
+constexpr float kMild = 40.0f;      // |e| of values whose sums need no maximum of their own
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
@@ -44,6 +52,19 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Four e4m3 values as fp16 pairs.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
+}
+// An 8 x 8 matrix of 16-bit values, a row's two in a lane, transposed.
+__device__ __forceinline__ uint32_t turn(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 // All ones in the bytes that are NaN.
@@ -86,20 +107,22 @@ __device__ __noinline__ void settle(uint64_t* full, int stages, int st, int ph, 
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// MT row tiles of 16. Q stays in registers where it fits beside the sums, else
-// in shared memory.
-template <int D, int MT, bool SHARED>
-__global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16, true))
+// NT row tiles of 8. Q stays in registers where it fits beside the sums, else in
+// shared memory.
+template <int D, int NT, bool SHARED>
+__global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, NT * 8, true))
     attn_mma_q8_kernel(const AttnArgs a, const int stages) {
-  constexpr bool kQRegs = MT == 1;
-  constexpr int kQPitch = D * 2 + 16;
+  constexpr bool kQRegs = D * NT <= 256;
+  constexpr int kRows = NT * 8, kQPitch = D * 2 + 16;
   extern __shared__ __align__(128) unsigned char attn_dyn[];
   __shared__ int64_t scan[kThreads + 4];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], met;
   __shared__ __align__(16) unsigned char there[kMaxStages][kTile];   // positions that hold a token
-  // of K: its rows' powers of two; of V: their exponents; head by head
-  __shared__ __align__(16) float scales[kMaxStages][2][kTile];
-  __shared__ float row_x[kWarps][MT * 16];          // powers of two of Q's rows
+  // a row's K power of two, V exponent e and 2^-e, head by head; and whether all |e| are
+  // at most kMild
+  __shared__ __align__(16) float4 scales[kMaxStages][kTile];
+  __shared__ bool mild[kMaxStages];
+  __shared__ float row_x[kWarps][kRows];            // powers of two of Q's rows
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // position x of a tile lies at off(x) of its place: rows of a group side by side
   const int rowb = a.hw * D, gs = a.group_shift, group = 1 << gs;
@@ -109,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16, true))
   // behind the ring: the joins of at most two heads, or the warps' own Q before
   unsigned char* const behind = attn_dyn + stages * 2 * half_stage;
   float* const join = reinterpret_cast<float*>(behind);
-  unsigned char* const sq = behind + warp * (MT * 16 * kQPitch);
+  unsigned char* const sq = behind + warp * (kRows * kQPitch);
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&full[i], 2);
@@ -122,7 +145,10 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16, true))
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!attn_split<kThreads, SHARED>(a, tpos, scan, run)) return;
   const int rows_all = a.G * a.q_len;
-  const float sl2 = a.scale * 1.4426950408889634f;
+  // Q carries the scale's sign (and a scale of zero is the least normal number, which
+  // leaves hidden scores at -inf)
+  const float sl2 = fabsf(a.scale) * 1.4426950408889634f;
+  const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
 
   if (warp == kWarps) {
     // ---- loads: lane l has the copies l, l + 32, .. of a tile: K and V of each
@@ -243,11 +269,15 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16, true))
         const Bytes c2 = load(j + 2);
         look(j + 3);
         if (!wait_bar(&empty[st], ph, a.dev_err)) return settle(full, stages, st, ph, a.dev_err);
+bool near = true;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          scales[st][0][lane + 32 * i] = q8_scale(c0.k[i]);
-          scales[st][1][lane + 32 * i] = (float)c0.v[i] - 127.0f;
+          const float e = (float)c0.v[i] - 127.0f;
+          near = near && fabsf(e) <= kMild;
+          scales[st][lane + 32 * i] = make_float4(q8_scale(c0.k[i]), e, q8_factor(c0.v[i]), 0.0f);
         }
+        near = __all_sync(0xffffffffu, near);
+        if (lane == 0) mild[st] = near;
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);
         if (++st == stages) st = 0, ph ^= 1;
@@ -273,9 +303,9 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16, true))
     attn_advance(a, sg, run);
     // the warp's head and its first position of a tile
     const int hl = warp * 32 / tpos, hkv = sg.unit / a.rblocks * a.hw + hl;
-    const int p_warp = warp * 32 % tpos, r0 = sg.unit % a.rblocks * (MT * 16);
-    const int rows = min(MT * 16, rows_all - r0);
-    // ---- Q as left operands: row r is token (r0 + r) / G, head hkv * G + (r0 + r) % G.
+    const int p_warp = warp * 32 % tpos, r0 = sg.unit % a.rblocks * kRows;
+    const int rows = min(kRows, rows_all - r0);
+    // ---- Q as right operands: row r is token (r0 + r) / G, head hkv * G + (r0 + r) % G.
     // Of 16 dims, 4 c + {0, 1} are where the product has 2 c + {0, 1}, and
     // 4 c + {2, 3} where it has 8 + 2 c + {0, 1}: as the bytes of K come.
     auto q_row = [&](int r) {
@@ -283,47 +313,50 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16, true))
       return a.q + (((int64_t)sg.b * a.q_len + rr / a.G) * a.q_rs +
                     (int64_t)(hkv * a.G + rr % a.G) * D) * 2;
     };
-    uint32_t q[kQRegs ? MT : 1][kQRegs ? D / 16 : 1][4];
-    float rf[MT][2];                    // what a row's scores are multiplied by
+    uint32_t q[kQRegs ? NT : 1][kQRegs ? D / 16 : 1][2];
+    float rf[NT][2];                    // what scores of rows 8 nt + 2 c + {0, 1} are multiplied by
     if constexpr (kQRegs) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = nt * 8 + (lane >> 2);
+        const bool in = r < rows && sg.len > 0;
+        const char* p = q_row(in ? r : 0) + (lane & 3) * 8;
+        uint2 raw[D / 16];
+        float m = 0.0f;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int r = mt * 16 + half * 8 + (lane >> 2);
-          const bool in = r < rows && sg.len > 0;
-          const char* p = q_row(in ? r : 0) + (lane & 3) * 8;
-          uint2 raw[D / 16];
-          float m = 0.0f;
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            raw[ks] = in ? *reinterpret_cast<const uint2*>(p + ks * 32) : make_uint2(0u, 0u);
-            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(raw[ks].x << 16)),
-                               fabsf(__uint_as_float(raw[ks].x & 0xffff0000u))));
-            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(raw[ks].y << 16)),
-                               fabsf(__uint_as_float(raw[ks].y & 0xffff0000u))));
-          }
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          float x;
-          const float f = q_factor(m, x);
-          rf[mt][half] = x;
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            q[mt][ks][half] = pack_f16x2(__uint_as_float(raw[ks].x << 16) * f,
-                                         __uint_as_float(raw[ks].x & 0xffff0000u) * f);
-            q[mt][ks][half + 2] = pack_f16x2(__uint_as_float(raw[ks].y << 16) * f,
-                                             __uint_as_float(raw[ks].y & 0xffff0000u) * f);
-          }
+        for (int ks = 0; ks < D / 16; ++ks) {
+          raw[ks] = in ? *reinterpret_cast<const uint2*>(p + ks * 32) : make_uint2(0u, 0u);
+          raw[ks].x ^= flip, raw[ks].y ^= flip;
+          m = fmaxf(m, fmaxf(fabsf(__uint_as_float(raw[ks].x << 16)),
+                             fabsf(__uint_as_float(raw[ks].x & 0xffff0000u))));
+          m = fmaxf(m, fmaxf(fabsf(__uint_as_float(raw[ks].y << 16)),
+                             fabsf(__uint_as_float(raw[ks].y & 0xffff0000u))));
         }
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        float x;
+        const float f = q_factor(m, x);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          rf[nt][i] = __shfl_sync(0xffffffffu, x, ((lane & 3) * 2 + i) * 4);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          q[nt][ks][0] = pack_f16x2(__uint_as_float(raw[ks].x << 16) * f,
+                                    __uint_as_float(raw[ks].x & 0xffff0000u) * f);
+          q[nt][ks][1] = pack_f16x2(__uint_as_float(raw[ks].y << 16) * f,
+                                    __uint_as_float(raw[ks].y & 0xffff0000u) * f);
+        }
+      }
     } else {
       constexpr int kLanes = D / 8;     // of a row, 8 dims each
 #pragma unroll 1
-      for (int i = lane; i < MT * 16 * kLanes; i += 32) {
+      for (int i = lane; i < kRows * kLanes; i += 32) {
         const int r = i / kLanes, u = i % kLanes;
         const bool in = r < rows && sg.len > 0;
+        uint4 raw = in ? ldg16(q_row(r) + u * 16) : make_uint4(0u, 0u, 0u, 0u);
+        raw.x ^= flip, raw.y ^= flip, raw.z ^= flip, raw.w ^= flip;
         float f[8];
-        unpack16<__nv_bfloat16>(in ? ldg16(q_row(r) + u * 16) : make_uint4(0u, 0u, 0u, 0u), f);
+        unpack16<__nv_bfloat16>(raw, f);
         float m = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
@@ -340,84 +373,94 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16, true))
       }
       __syncwarp();
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
-          rf[mt][half] = row_x[warp][mt * 16 + half * 8 + (lane >> 2)];
+        for (int i = 0; i < 2; ++i) rf[nt][i] = row_x[warp][nt * 8 + (lane & 3) * 2 + i];
     }
+    // positions that a row sees, and its factor
+    int seen[NT][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) rf[mt][half] = ldexpf(sl2, (int)rf[mt][half]);
-    // maxima of scores (m) and of scores with their value's power of two (mv)
-    float m[MT][2], mv[MT][2], l[MT][2], o[MT][D / 8][4];
+      for (int i = 0; i < 2; ++i) {
+        rf[nt][i] = fmaxf(ldexpf(sl2, (int)rf[nt][i]), 0x1p-126f);
+        const int r = nt * 8 + (lane & 3) * 2 + i;
+        seen[nt][i] = r < rows ? sg.len - a.q_len + 1 + (r0 + r) / a.G : 0;
+      }
+    // Of rows 8 nt + 2 c + {0, 1}: the reference of scores with their value's power of two
+    // (mv), the lane's sum, and the sums of values at dims 16 n + 2 (lane / 4) + {0, 1}:
+    // o[nt][n][row + 2 dim]. Once `wide`, m is the maximum of the scores themselves, and l
+    // is relative to it; before, l is relative to mv - kLift.
+    float m[NT][2], mv[NT][2], l[NT][2], o[NT][D / 16][4];
+    bool wide = false;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      m[mt][0] = m[mt][1] = mv[mt][0] = mv[mt][1] = -INFINITY;
-      l[mt][0] = l[mt][1] = 0.0f;
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = mv[nt][0] = mv[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.0f;
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.0f;
+      for (int n = 0; n < D / 16; ++n) o[nt][n][0] = o[nt][n][1] = o[nt][n][2] = o[nt][n][3] = 0.0f;
     }
     for (int j = sg.j0; j < sg.j1; ++j) {
       if (!wait_bar(&full[stage], phase, a.dev_err))
         return settle(full, stages, stage, phase, a.dev_err);
-      const uint32_t place = smem_addr(attn_dyn) + stage * 2 * half_stage + hl * D;
+      const uint32_t kb = smem_addr(attn_dyn) + stage * 2 * half_stage + hl * D + off(p_warp);
+      const uint32_t vb = kb + half_stage;
       const int cur = stage;
-      if (++stage == stages) stage = 0, phase ^= 1;
-      const uint32_t kb = place + off(p_warp), vb = kb + half_stage;
       const unsigned char* const tr = there[cur] + p_warp;
-      const float* const ks = scales[cur][0] + hl * tpos + p_warp;
-      const float* const vs = scales[cur][1] + hl * tpos + p_warp;
-      // ---- scores of the warp's 32 positions: four n-tiles of 8
-      float s[MT][4][4] = {};
-      const uint32_t ka = kb + off((lane & 7) + ((lane >> 4) << 3)) + ((lane >> 3) & 1) * 16;
+      const float4* const sc = scales[cur] + hl * tpos + p_warp + (lane >> 2);
+      if (++stage == stages) stage = 0, phase ^= 1;
+      // ---- scores of the warp's 32 positions, two tiles of 16: s[nt][g][row + 2 h] is that
+      // of position 16 g + 8 h + lane / 4
+      float s[NT][2][4] = {};
       const uint32_t step16 = off(16);
+      const uint32_t ka = kb + off(lane & 15) + (lane >> 4) * 16;
 #pragma unroll
       for (int d = 0; d < D / 16; d += 2) {
-        uint32_t b[2][4];              // positions 0-7: bytes 0-15, 16-31; positions 8-15: the same
+        uint32_t b[2][4];              // bytes 0-15: positions 0-7, 8-15; bytes 16-31: the same
         tc::ldmatrix4(b[0], ka + d * 16);
         tc::ldmatrix4(b[1], ka + step16 + d * 16);
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 2; ++t) {
+          uint32_t kf[2][4];
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const uint32_t b0 = e4m3x2_to_f16x2(b[g][t]), b1 = e4m3x2_to_f16x2(b[g][t] >> 16);
-            const uint32_t b2 = e4m3x2_to_f16x2(b[g][2 + t]),
-                           b3 = e4m3x2_to_f16x2(b[g][2 + t] >> 16);
+            e4m3x4_to_f16(b[g][2 * t], kf[g][0], kf[g][2]);
+            e4m3x4_to_f16(b[g][2 * t + 1], kf[g][1], kf[g][3]);
+          }
+          if constexpr (kQRegs) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              if constexpr (kQRegs) {
-                tc::mma16h(s[mt][2 * g], q[mt][d + t], b0, b1);
-                tc::mma16h(s[mt][2 * g + 1], q[mt][d + t], b2, b3);
-              } else {
-                uint32_t qa[4];
-                tc::ldmatrix4(qa, smem_addr(sq) + (mt * 16 + (lane & 15)) * kQPitch +
-                                      (d + t) * 32 + (lane >> 4) * 16);
-                tc::mma16h(s[mt][2 * g], qa, b0, b1);
-                tc::mma16h(s[mt][2 * g + 1], qa, b2, b3);
+            for (int nt = 0; nt < NT; ++nt) {
+              tc::mma16h(s[nt][0], kf[0], q[nt][d + t][0], q[nt][d + t][1]);
+              tc::mma16h(s[nt][1], kf[1], q[nt][d + t][0], q[nt][d + t][1]);
+            }
+          } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; nt += 2) {
+              uint32_t qb[4];          // rows 0-7: k 0-7, 8-15; rows 8-15: the same
+              tc::ldmatrix4(qb, smem_addr(sq) +
+                                    (nt * 8 + (lane & 7) + ((lane >> 4) << 3)) * kQPitch +
+                                    (d + t) * 32 + ((lane >> 3) & 1) * 16);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                tc::mma16h(s[nt + e][0], kf[0], qb[2 * e], qb[2 * e + 1]);
+                tc::mma16h(s[nt + e][1], kf[1], qb[2 * e], qb[2 * e + 1]);
               }
             }
           }
+        }
       }
-      // the powers of two of the lane's eight positions: q0 + 8 n + {0, 1}
-      const int q0 = (lane & 3) * 2;
-      float ve[8];
+      // the scales of the lane's four positions: 8 i + lane / 4
+      float4 f[4];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float2 kf = *reinterpret_cast<const float2*>(ks + q0 + 8 * n);
-        const float2 e = *reinterpret_cast<const float2*>(vs + q0 + 8 * n);
-        ve[2 * n] = e.x;
-        ve[2 * n + 1] = e.y;
+      for (int i = 0; i < 4; ++i) {
+        f[i] = sc[8 * i];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[mt][n][i] *= (i & 1 ? kf.y : kf.x);
+        for (int nt = 0; nt < NT; ++nt) {
+          s[nt][i >> 1][(i & 1) * 2] *= f[i].x;
+          s[nt][i >> 1][(i & 1) * 2 + 1] *= f[i].x;
+        }
       }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[mt][i >> 2][i & 3] *= rf[mt][(i >> 1) & 1];
-      // ---- masks, running maxima, weights
+      // ---- masks, references, weights
       const int pos0 = sg.base + j * tpos + p_warp;    // the first position
       // Draft tokens' positions are hidden from the rows before them by a weight of
       // zero, which a NaN among their values would get through: such values (`wild`)
@@ -435,148 +478,153 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16, true))
       if (pos0 + 31 > sg.len - a.q_len ||
           (all.x & all.y & all.z & all.w & more.x & more.y & more.z & more.w) != 0x01010101u) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int i = 0; i < 4; ++i) {
+          const int x = 8 * i + (lane >> 2);
+          const bool held = tr[x];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int r = mt * 16 + half * 8 + (lane >> 2);
-            const int seen = r < rows ? sg.len - a.q_len + 1 + (r0 + r) / a.G : 0;
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int x = q0 + (i >> 1) * 8 + (i & 1);
-              if (!tr[x] || pos0 + x >= seen) s[mt][i >> 1][half * 2 + (i & 1)] = -INFINITY;
-            }
+            for (int k = 0; k < 2; ++k)
+              if (!held || pos0 + x >= seen[nt][k]) s[nt][i >> 1][(i & 1) * 2 + k] = -INFINITY;
+        }
+      }
+      if (!wide && !mild[cur]) {
+        wide = true;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            m[nt][k] = mv[nt][k];
+            l[nt][k] *= exp2f(-kLift);
           }
       }
+      uint32_t pt[NT][4];               // weights of positions 8 i .. 8 i + 7 as right operands
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        uint32_t pw[2][4];
-        float corr[2];
+      for (int nt = 0; nt < NT; ++nt) {
+        float t[4][2];
+        bool rises = false;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float x[8], t[8];
+        for (int k = 0; k < 2; ++k) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[i] = s[mt][i >> 1][half * 2 + (i & 1)];
-            t[i] = x[i] + ve[i];
+          for (int i = 0; i < 4; ++i)
+            t[i][k] = fmaf(s[nt][i >> 1][(i & 1) * 2 + k], rf[nt][k], f[i].y);
+          const float top = fmaxf(fmaxf(t[0][k], t[1][k]), fmaxf(t[2][k], t[3][k]));
+          rises = rises || top > mv[nt][k] + kSlack || (mv[nt][k] == -INFINITY && top > mv[nt][k]);
+        }
+        if (__any_sync(0xffffffffu, rises)) {
+          float corr[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float top = fmaxf(fmaxf(t[0][k], t[1][k]), fmaxf(t[2][k], t[3][k]));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float mn = fmaxf(mv[nt][k], top);
+            corr[k] = mn == -INFINITY ? 1.0f : tc::ex2(mv[nt][k] - mn);
+            mv[nt][k] = mn;
+            if (!wide) l[nt][k] *= corr[k];
           }
-          float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
-                           fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-          float tx = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])),
-                           fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, 2));
-          const float mn = fmaxf(m[mt][half], mx), tn = fmaxf(mv[mt][half], tx);
-          const float base = mn == -INFINITY ? 0.0f : mn, tbase = tn == -INFINITY ? 0.0f : tn;
-          corr[half] = tc::ex2(mv[mt][half] - tbase);
-          float sum = 0.0f, more_sum = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            sum += tc::ex2(x[i] - base);
-            more_sum += tc::ex2(x[i + 1] - base);
-          }
-          l[mt][half] = fmaf(l[mt][half], tc::ex2(m[mt][half] - base), sum + more_sum);
-          m[mt][half] = mn;
-          mv[mt][half] = tn;
-          const float up = tbase - kLift;
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            pw[g][half] = pack_f16x2(tc::ex2(t[4 * g] - up), tc::ex2(t[4 * g + 1] - up));
-            pw[g][2 + half] = pack_f16x2(tc::ex2(t[4 * g + 2] - up), tc::ex2(t[4 * g + 3] - up));
+          for (int n = 0; n < D / 16; ++n) {
+            o[nt][n][0] *= corr[0];
+            o[nt][n][1] *= corr[1];
+            o[nt][n][2] *= corr[0];
+            o[nt][n][3] *= corr[1];
           }
         }
-        if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
+        if (wide) {
 #pragma unroll
-          for (int n = 0; n < D / 8; ++n) {
-            o[mt][n][0] *= corr[0];
-            o[mt][n][1] *= corr[0];
-            o[mt][n][2] *= corr[1];
-            o[mt][n][3] *= corr[1];
+          for (int k = 0; k < 2; ++k) {
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = s[nt][i >> 1][(i & 1) * 2 + k] * rf[nt][k];
+            float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float mn = fmaxf(m[nt][k], top), base = mn == -INFINITY ? 0.0f : mn;
+            l[nt][k] = fmaf(l[nt][k], tc::ex2(m[nt][k] - base),
+                            (tc::ex2(x[0] - base) + tc::ex2(x[1] - base)) +
+                                (tc::ex2(x[2] - base) + tc::ex2(x[3] - base)));
+            m[nt][k] = mn;
           }
         }
-        // ---- weighted values: of 16 dims, the even ones are one n-tile, the odd ones
-        // another
-        const uint32_t va = vb + off(lane & 15) + (lane >> 4) * 16;
-        if (!wild) {
+        const float up[2] = {mv[nt][0] == -INFINITY ? 0.0f : mv[nt][0] - kLift,
+                             mv[nt][1] == -INFINITY ? 0.0f : mv[nt][1] - kLift};
 #pragma unroll
-          for (int n = 0; n < D / 16; n += 2) {
-            uint32_t b[2][4];          // dims 0-15: positions 0-7, 8-15; dims 16-31: the same
-            tc::ldmatrix4_trans(b[0], va + n * 16);
-            tc::ldmatrix4_trans(b[1], va + step16 + n * 16);
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-#pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                const uint32_t v0 = __byte_perm(b[g][2 * t], 0u, 0x3120),
-                               v1 = __byte_perm(b[g][2 * t + 1], 0u, 0x3120);
-                tc::mma16h(o[mt][2 * (n + t)], pw[g], e4m3x2_to_f16x2(v0), e4m3x2_to_f16x2(v1));
-                tc::mma16h(o[mt][2 * (n + t) + 1], pw[g], e4m3x2_to_f16x2(v0 >> 16),
-                           e4m3x2_to_f16x2(v1 >> 16));
-              }
+        for (int i = 0; i < 4; ++i) {
+          const float w0 = tc::ex2(t[i][0] - up[0]), w1 = tc::ex2(t[i][1] - up[1]);
+          if (!wide) {
+            l[nt][0] = fmaf(w0, f[i].z, l[nt][0]);
+            l[nt][1] = fmaf(w1, f[i].z, l[nt][1]);
           }
-        } else {
-#pragma unroll 1
+          pt[nt][i] = turn(pack_f16x2(w0, w1));
+        }
+      }
+      // ---- weighted values: of 16 dims, the even ones are rows 0-7 of a left operand, the
+      // odd ones rows 8-15
+      const uint32_t va = vb + off(lane & 15) + (lane >> 4) * 16;
+#pragma unroll
+      for (int n = 0; n < D / 16; n += 2) {
+        uint32_t b[2][4];              // dims 0-15: positions 0-7, 8-15; dims 16-31: the same
+        tc::ldmatrix4_trans(b[0], va + n * 16);
+        tc::ldmatrix4_trans(b[1], va + step16 + n * 16);
+        if (wild) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {      // positions 16 (i / 4) + 8 (i & 1) + 2 c + {0, 1}
+            const int x = (i >> 2) * 16 + (i & 1) * 8 + (lane & 3) * 2;
+            const uint32_t hidden = (x >= x0 ? 0x0000ffffu : 0u) | (x + 1 >= x0 ? 0xffff0000u : 0u);
+            b[i >> 2][i & 3] &= ~(nan_bytes(b[i >> 2][i & 3]) & hidden);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const uint32_t pg[4] = {g ? pw[1][0] : pw[0][0], g ? pw[1][1] : pw[0][1],
-                                    g ? pw[1][2] : pw[0][2], g ? pw[1][3] : pw[0][3]};
+            uint32_t v[4];
+            e4m3x4_to_f16(__byte_perm(b[g][2 * t], 0u, 0x3120), v[0], v[1]);
+            e4m3x4_to_f16(__byte_perm(b[g][2 * t + 1], 0u, 0x3120), v[2], v[3]);
 #pragma unroll
-            for (int n = 0; n < D / 16; n += 2) {
-              uint32_t b[4];
-              tc::ldmatrix4_trans(b, va + g * step16 + n * 16);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {        // positions 16 g + q0 + 8 (i & 1) + {0, 1}
-                const int x = 16 * g + q0 + (i & 1) * 8;
-                const uint32_t hidden =
-                    (x >= x0 ? 0x00ff00ffu : 0u) | (x + 1 >= x0 ? 0xff00ff00u : 0u);
-                b[i] = __byte_perm(b[i], 0u, 0x3120);
-                b[i] &= ~(nan_bytes(b[i]) & hidden);
-              }
-#pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                tc::mma16h(o[mt][2 * (n + t)], pg, e4m3x2_to_f16x2(b[2 * t]),
-                           e4m3x2_to_f16x2(b[2 * t + 1]));
-                tc::mma16h(o[mt][2 * (n + t) + 1], pg, e4m3x2_to_f16x2(b[2 * t] >> 16),
-                           e4m3x2_to_f16x2(b[2 * t + 1] >> 16));
-              }
-            }
+            for (int nt = 0; nt < NT; ++nt)
+              tc::mma16h(o[nt][n + t], v, pt[nt][2 * g], pt[nt][2 * g + 1]);
           }
+      }
+      if (wild) {
 #pragma unroll 1
-          for (int x = x0; x < x1; ++x)
+        for (int x = x0; x < x1; ++x)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int r = mt * 16 + half * 8 + (lane >> 2);
-              if (r >= rows || pos0 + x >= sg.len - a.q_len + 1 + (r0 + r) / a.G) continue;
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int n = 0; n < D / 16; ++n) {     // dims 16 n + 4 c + {0, 1, 2, 3}
-                const uint32_t v = nan_bytes(lds32(vb + off(x) + n * 16 + q0 * 2));
+            for (int k = 0; k < 2; ++k) {
+              if (pos0 + x >= seen[nt][k]) continue;
+#pragma unroll
+              for (int n = 0; n < D / 16; ++n) {     // dims 16 n + 2 (lane / 4) + {0, 1}
+                const uint32_t v = nan_bytes(lds32(vb + off(x) + n * 16 + (lane >> 3) * 4)) >>
+                                   (lane >> 2 & 1) * 16;
                 const float nan = __uint_as_float(0x7fc00000u);
-                if (v & 0xffu) o[mt][2 * n][half * 2] = nan;
-                if (v & 0xff00u) o[mt][2 * n + 1][half * 2] = nan;
-                if (v & 0xff0000u) o[mt][2 * n][half * 2 + 1] = nan;
-                if (v & 0xff000000u) o[mt][2 * n + 1][half * 2 + 1] = nan;
+                if (v & 0xffu) o[nt][n][k] = nan;
+                if (v & 0xff00u) o[nt][n][2 + k] = nan;
               }
             }
-        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[cur]);
     }
-    // ---- the row sums over the quad, and sums in units of 2^m again; then the warps of
-    // one head join: those behind the head's first one leave their part in shared
-    // memory, in turn
+    // ---- the row sums over the lanes, and all in units of 2^m; then the warps of one head
+    // join: those behind the head's first one leave their part in shared memory, in turn
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        l[mt][half] += __shfl_xor_sync(0xffffffffu, l[mt][half], 1);
-        l[mt][half] += __shfl_xor_sync(0xffffffffu, l[mt][half], 2);
-        const float f = m[mt][half] == -INFINITY ? 1.0f
-                                                 : exp2f(mv[mt][half] - m[mt][half] - kLift);
+      for (int k = 0; k < 2; ++k) {
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          o[mt][n][half * 2] *= f;
-          o[mt][n][half * 2 + 1] *= f;
+        for (int d = 4; d < 32; d <<= 1) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], d);
+        if (!wide) {
+          m[nt][k] = mv[nt][k];
+          l[nt][k] *= exp2f(-kLift);
+        }
+        const float g = m[nt][k] == -INFINITY ? 1.0f : exp2f(mv[nt][k] - m[nt][k] - kLift);
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          o[nt][n][k] *= g;
+          o[nt][n][2 + k] *= g;
         }
       }
     const int per = kWarps >> hw_shift;              // warps of a head
@@ -584,74 +632,69 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16, true))
     if (!kQRegs && per > 1 && !meet()) return settle(full, stages, stage, phase, a.dev_err);
 #pragma unroll 1
     for (int w = 1; w < per; ++w) {
-      float* const so = join + (warp / per) * (MT * 16 * (D + 4));
+      float* const so = join + (warp / per) * (kRows * (D + 4));
       if (warp % per == w) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            float* p = so + (mt * 16 + half * 8 + (lane >> 2)) * (D + 4) + (lane & 3) * 2;
+          for (int k = 0; k < 2; ++k) {
+            float* p = so + (nt * 8 + (lane & 3) * 2 + k) * (D + 4);
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-              *reinterpret_cast<float2*>(p + n * 8) =
-                  make_float2(o[mt][n][half * 2], o[mt][n][half * 2 + 1]);
-            if ((lane & 3) == 0) {
-              p[D] = m[mt][half];
-              p[D + 1] = l[mt][half];
+            for (int n = 0; n < D / 16; ++n)
+              *reinterpret_cast<float2*>(p + n * 16 + (lane >> 2) * 2) =
+                  make_float2(o[nt][n][k], o[nt][n][2 + k]);
+            if (lane < 4) {
+              p[D] = m[nt][k];
+              p[D + 1] = l[nt][k];
             }
           }
       }
       if (!meet()) return settle(full, stages, stage, phase, a.dev_err);
       if (warp % per == 0) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const float* row = so + (mt * 16 + half * 8 + (lane >> 2)) * (D + 4);
+          for (int k = 0; k < 2; ++k) {
+            const float* row = so + (nt * 8 + (lane & 3) * 2 + k) * (D + 4);
             const float mo = row[D], lo = row[D + 1];
-            const float mm = fmaxf(m[mt][half], mo), base = mm == -INFINITY ? 0.0f : mm;
-            const float f = tc::ex2(m[mt][half] - base), fo = tc::ex2(mo - base);
-            m[mt][half] = mm;
-            l[mt][half] = fmaf(l[mt][half], f, lo * fo);
+            const float mm = fmaxf(m[nt][k], mo), base = mm == -INFINITY ? 0.0f : mm;
+            const float g = tc::ex2(m[nt][k] - base), go = tc::ex2(mo - base);
+            m[nt][k] = mm;
+            l[nt][k] = fmaf(l[nt][k], g, lo * go);
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-              const float2 v = *reinterpret_cast<const float2*>(row + n * 8 + (lane & 3) * 2);
-              o[mt][n][half * 2] = fmaf(o[mt][n][half * 2], f, v.x * fo);
-              o[mt][n][half * 2 + 1] = fmaf(o[mt][n][half * 2 + 1], f, v.y * fo);
+            for (int n = 0; n < D / 16; ++n) {
+              const float2 v = *reinterpret_cast<const float2*>(row + n * 16 + (lane >> 2) * 2);
+              o[nt][n][k] = fmaf(o[nt][n][k], g, v.x * go);
+              o[nt][n][2 + k] = fmaf(o[nt][n][2 + k], g, v.y * go);
             }
           }
       }
       if (!meet()) return settle(full, stages, stage, phase, a.dev_err);
     }
     if (sg.len < 0 || warp % per != 0) continue;
-    float* const part = attn_part<SHARED>(a, sg, D) + (warp / per) * (MT * 16) * (D + 2);
+    float* const part = attn_part<SHARED>(a, sg, D) + (warp / per) * kRows * (D + 2);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int r = mt * 16 + half * 8 + (lane >> 2), c = (lane & 3) * 4;
+      for (int k = 0; k < 2; ++k) {
+        const int r = nt * 8 + (lane & 3) * 2 + k, c = (lane >> 2) * 2;
         if (r >= rows) continue;
-        const float ll = l[mt][half], mn = m[mt][half] * 0.6931471805599453f;   // natural
+        const float ll = l[nt][k], mn = m[nt][k] * 0.6931471805599453f;   // natural
         if (sg.whole) {
           const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
           const int64_t tok = (int64_t)sg.b * a.q_len + (r0 + r) / a.G;
           const int h = hkv * a.G + (r0 + r) % a.G;
           char* p = a.out + (tok * a.out_rs + (int64_t)h * D + c) * 2;
 #pragma unroll
-          for (int n = 0; n < D / 16; ++n) {
-            const float *e = o[mt][2 * n] + half * 2, *d = o[mt][2 * n + 1] + half * 2;
-            *reinterpret_cast<uint2*>(p + n * 32) = make_uint2(
-                pack_bf16x2(e[0] * inv, d[0] * inv), pack_bf16x2(e[1] * inv, d[1] * inv));
-          }
+          for (int n = 0; n < D / 16; ++n)
+            *reinterpret_cast<uint32_t*>(p + n * 32) =
+                pack_bf16x2(o[nt][n][k] * inv, o[nt][n][2 + k] * inv);
           if (a.lse && c == 0) a.lse[tok * a.Hq + h] = ll != 0.0f ? mn + logf(ll) : -INFINITY;
         } else {
           float* p = part + r * (D + 2);
 #pragma unroll
-          for (int n = 0; n < D / 16; ++n) {
-            const float *e = o[mt][2 * n] + half * 2, *d = o[mt][2 * n + 1] + half * 2;
-            *reinterpret_cast<float2*>(p + n * 16 + c) = make_float2(e[0], d[0]);
-            *reinterpret_cast<float2*>(p + n * 16 + c + 2) = make_float2(e[1], d[1]);
-          }
+          for (int n = 0; n < D / 16; ++n)
+            *reinterpret_cast<float2*>(p + n * 16 + c) = make_float2(o[nt][n][k], o[nt][n][2 + k]);
           if (c == 0) {
             p[D] = mn;
             p[D + 1] = ll;
@@ -663,44 +706,48 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, MT * 16, true))
 
 static_assert(kTile == 32 * kWarps, "a warp takes 32 rows");
 
-template <int D, int MT, bool SHARED>
+template <int D, int NT, bool SHARED>
 cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
   // the ring, and behind it the joins (none with a head a warp) or the warps' Q
   const int tpos = kTile / a.hw, stage = 2 * (tpos * a.hw * D + (tpos >> a.group_shift) * 16);
-  const int join = (a.hw == 4 ? 0 : a.hw) * MT * 16 * (D + 4) * 4;
-  const int q = MT == 1 ? 0 : kWarps * MT * 16 * (D * 2 + 16);
+  const int join = (a.hw == 4 ? 0 : a.hw) * NT * 8 * (D + 4) * 4;
+  const int q = D * NT <= 256 ? 0 : kWarps * NT * 8 * (D * 2 + 16);
   int stages = D == 64 ? 4 : 3;
   // as many as let the grid's blocks of an SM all be there (228 KB, less what the
   // kernel has besides)
-  const int most = 228 * 1024 / attn_mma_blocks(D, MT * 16, true) - 10 * 1024;
+  const int most = 228 * 1024 / attn_mma_blocks(D, NT * 8, true) - 13 * 1024;
   while (stages > 2 && stages * stage + std::max(join, q) > most) --stages;
   const int smem = stages * stage + std::max(join, q);
   static std::atomic<uint64_t> full;
-  const void* const f = reinterpret_cast<const void*>(attn_mma_q8_kernel<D, MT, SHARED>);
+  const void* const f = reinterpret_cast<const void*>(attn_mma_q8_kernel<D, NT, SHARED>);
   const cudaError_t e = mix_full_smem(f, full);
   if (e != cudaSuccess) return e;
   if constexpr (!SHARED) {
-    attn_mma_q8_kernel<D, MT, SHARED><<<grid, kThreads, smem, st>>>(a, stages);
+    attn_mma_q8_kernel<D, NT, SHARED><<<grid, kThreads, smem, st>>>(a, stages);
     return cudaGetLastError();
   } else {
-    return attn_launch_beside(attn_mma_q8_kernel<D, MT, SHARED>, a, stages, grid, kThreads, smem,
+    return attn_launch_beside(attn_mma_q8_kernel<D, NT, SHARED>, a, stages, grid, kThreads, smem,
                               st);
   }
 }
 
-template <bool SHARED>
+template <int NT, bool SHARED>
 cudaError_t launch_d(const AttnArgs& a, int D, int grid, cudaStream_t st) {
-  if (a.rows == 16)
-    return D == 64    ? launch<64, 1, SHARED>(a, grid, st)
-           : D == 128 ? launch<128, 1, SHARED>(a, grid, st)
-                      : launch<256, 1, SHARED>(a, grid, st);
-  return D == 64 ? launch<64, 2, SHARED>(a, grid, st) : launch<128, 2, SHARED>(a, grid, st);
+  return D == 64    ? launch<64, NT, SHARED>(a, grid, st)
+         : D == 128 ? launch<128, NT, SHARED>(a, grid, st)
+                    : launch<256, NT < 2 ? NT : 2, SHARED>(a, grid, st);   // (16 rows at most)
+}
+template <bool SHARED>
+cudaError_t launch_rows(const AttnArgs& a, int D, int grid, cudaStream_t st) {
+  return a.rows == 8    ? launch_d<1, SHARED>(a, D, grid, st)
+         : a.rows == 16 ? launch_d<2, SHARED>(a, D, grid, st)
+                        : launch_d<4, SHARED>(a, D, grid, st);
 }
 
 }  // namespace
 
 cudaError_t attn_launch_mma_q8(const AttnArgs& a, int D, int grid, bool shared, cudaStream_t st) {
-  return shared ? launch_d<true>(a, D, grid, st) : launch_d<false>(a, D, grid, st);
+  return shared ? launch_rows<true>(a, D, grid, st) : launch_rows<false>(a, D, grid, st);
 }
 
 }  // namespace cconv
