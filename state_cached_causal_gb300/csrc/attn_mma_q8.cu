@@ -109,18 +109,19 @@ __device__ __noinline__ void settle(uint64_t* full, int stages, int st, int ph, 
 
 // NT row tiles of 8. Q stays in registers where it fits beside the sums, else in
 // shared memory.
+__host__ __device__ constexpr bool q_in_regs(int D, int NT) { return D * NT <= 256; }
 template <int D, int NT, bool SHARED>
 __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, NT * 8, true))
     attn_mma_q8_kernel(const AttnArgs a, const int stages) {
-  constexpr bool kQRegs = D * NT <= 256;
+  constexpr bool kQRegs = q_in_regs(D, NT);
   constexpr int kRows = NT * 8, kQPitch = D * 2 + 16;
   extern __shared__ __align__(128) unsigned char attn_dyn[];
   __shared__ int64_t scan[kThreads + 4];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], met;
   __shared__ __align__(16) unsigned char there[kMaxStages][kTile];   // positions that hold a token
-  // a row's K power of two, V exponent e and 2^-e, head by head; and whether all |e| are
-  // at most kMild
-  __shared__ __align__(16) float4 scales[kMaxStages][kTile];
+  // a row's K power of two and V exponent e, head by head; and whether all |e| are at
+  // most kMild
+  __shared__ __align__(16) float2 scales[kMaxStages][kTile];
   __shared__ bool mild[kMaxStages];
   __shared__ float row_x[kWarps][kRows];            // powers of two of Q's rows
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -274,7 +275,7 @@ bool near = true;
         for (int i = 0; i < 4; ++i) {
           const float e = (float)c0.v[i] - 127.0f;
           near = near && fabsf(e) <= kMild;
-          scales[st][lane + 32 * i] = make_float4(q8_scale(c0.k[i]), e, q8_factor(c0.v[i]), 0.0f);
+          scales[st][lane + 32 * i] = make_float2(q8_scale(c0.k[i]), e);
         }
         near = __all_sync(0xffffffffu, near);
         if (lane == 0) mild[st] = near;
@@ -349,7 +350,7 @@ bool near = true;
       }
     } else {
       constexpr int kLanes = D / 8;     // of a row, 8 dims each
-#pragma unroll 1
+#pragma unroll 8
       for (int i = lane; i < kRows * kLanes; i += 32) {
         const int r = i / kLanes, u = i % kLanes;
         const bool in = r < rows && sg.len > 0;
@@ -377,16 +378,15 @@ bool near = true;
 #pragma unroll
         for (int i = 0; i < 2; ++i) rf[nt][i] = row_x[warp][nt * 8 + (lane & 3) * 2 + i];
     }
-    // positions that a row sees, and its factor
-    int seen[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        rf[nt][i] = fmaxf(ldexpf(sl2, (int)rf[nt][i]), 0x1p-126f);
-        const int r = nt * 8 + (lane & 3) * 2 + i;
-        seen[nt][i] = r < rows ? sg.len - a.q_len + 1 + (r0 + r) / a.G : 0;
-      }
+      for (int i = 0; i < 2; ++i) rf[nt][i] = fmaxf(ldexpf(sl2, (int)rf[nt][i]), 0x1p-126f);
+    // positions that row 8 nt + 2 c + i sees
+    auto seen = [&](int nt, int i) {
+      const int r = nt * 8 + (lane & 3) * 2 + i;
+      return r < rows ? sg.len - a.q_len + 1 + (r0 + r) / a.G : 0;
+    };
     // Of rows 8 nt + 2 c + {0, 1}: the reference of scores with their value's power of two
     // (mv), the lane's sum, and the sums of values at dims 16 n + 2 (lane / 4) + {0, 1}:
     // o[nt][n][row + 2 dim]. Once `wide`, m is the maximum of the scores themselves, and l
@@ -407,7 +407,7 @@ bool near = true;
       const uint32_t vb = kb + half_stage;
       const int cur = stage;
       const unsigned char* const tr = there[cur] + p_warp;
-      const float4* const sc = scales[cur] + hl * tpos + p_warp + (lane >> 2);
+      const float2* const sc = scales[cur] + hl * tpos + p_warp + (lane >> 2);
       if (++stage == stages) stage = 0, phase ^= 1;
       // ---- scores of the warp's 32 positions, two tiles of 16: s[nt][g][row + 2 h] is that
       // of position 16 g + 8 h + lane / 4
@@ -415,49 +415,43 @@ bool near = true;
       const uint32_t step16 = off(16);
       const uint32_t ka = kb + off(lane & 15) + (lane >> 4) * 16;
 #pragma unroll
-      for (int d = 0; d < D / 16; d += 2) {
-        uint32_t b[2][4];              // bytes 0-15: positions 0-7, 8-15; bytes 16-31: the same
-        tc::ldmatrix4(b[0], ka + d * 16);
-        tc::ldmatrix4(b[1], ka + step16 + d * 16);
+      for (int d = 0; d < D / 16; d += 2)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          uint32_t kf[2][4];
+        for (int g = 0; g < 2; ++g) {
+          uint32_t b[4];               // bytes 0-15: positions 0-7, 8-15; bytes 16-31: the same
+          tc::ldmatrix4(b, ka + g * step16 + d * 16);
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            e4m3x4_to_f16(b[g][2 * t], kf[g][0], kf[g][2]);
-            e4m3x4_to_f16(b[g][2 * t + 1], kf[g][1], kf[g][3]);
-          }
-          if constexpr (kQRegs) {
+          for (int t = 0; t < 2; ++t) {
+            uint32_t kf[4];
+            e4m3x4_to_f16(b[2 * t], kf[0], kf[2]);
+            e4m3x4_to_f16(b[2 * t + 1], kf[1], kf[3]);
+            if constexpr (kQRegs) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              tc::mma16h(s[nt][0], kf[0], q[nt][d + t][0], q[nt][d + t][1]);
-              tc::mma16h(s[nt][1], kf[1], q[nt][d + t][0], q[nt][d + t][1]);
-            }
-          } else {
+              for (int nt = 0; nt < NT; ++nt)
+                tc::mma16h(s[nt][g], kf, q[nt][d + t][0], q[nt][d + t][1]);
+            } else {
 #pragma unroll
-            for (int nt = 0; nt < NT; nt += 2) {
-              uint32_t qb[4];          // rows 0-7: k 0-7, 8-15; rows 8-15: the same
-              tc::ldmatrix4(qb, smem_addr(sq) +
-                                    (nt * 8 + (lane & 7) + ((lane >> 4) << 3)) * kQPitch +
-                                    (d + t) * 32 + ((lane >> 3) & 1) * 16);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                tc::mma16h(s[nt + e][0], kf[0], qb[2 * e], qb[2 * e + 1]);
-                tc::mma16h(s[nt + e][1], kf[1], qb[2 * e], qb[2 * e + 1]);
+              for (int nt = 0; nt < NT; nt += 2) {
+                uint32_t qb[4];        // rows 0-7: k 0-7, 8-15; rows 8-15: the same
+                tc::ldmatrix4(qb, smem_addr(sq) +
+                                      (nt * 8 + (lane & 7) + ((lane >> 4) << 3)) * kQPitch +
+                                      (d + t) * 32 + ((lane >> 3) & 1) * 16);
+                tc::mma16h(s[nt][g], kf, qb[0], qb[1]);
+                tc::mma16h(s[nt + 1][g], kf, qb[2], qb[3]);
               }
             }
           }
         }
-      }
       // the scales of the lane's four positions: 8 i + lane / 4
-      float4 f[4];
+      float e[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        f[i] = sc[8 * i];
+        const float2 f = sc[8 * i];
+        e[i] = f.y;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          s[nt][i >> 1][(i & 1) * 2] *= f[i].x;
-          s[nt][i >> 1][(i & 1) * 2 + 1] *= f[i].x;
+          s[nt][i >> 1][(i & 1) * 2] *= f.x;
+          s[nt][i >> 1][(i & 1) * 2 + 1] *= f.x;
         }
       }
       // ---- masks, references, weights
@@ -478,15 +472,16 @@ bool near = true;
       if (pos0 + 31 > sg.len - a.q_len ||
           (all.x & all.y & all.z & all.w & more.x & more.y & more.z & more.w) != 0x01010101u) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int x = 8 * i + (lane >> 2);
-          const bool held = tr[x];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int k = 0; k < 2; ++k) {
+            const int sees = seen(nt, k);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              if (!held || pos0 + x >= seen[nt][k]) s[nt][i >> 1][(i & 1) * 2 + k] = -INFINITY;
-        }
+            for (int i = 0; i < 4; ++i) {
+              const int x = 8 * i + (lane >> 2);
+              if (!tr[x] || pos0 + x >= sees) s[nt][i >> 1][(i & 1) * 2 + k] = -INFINITY;
+            }
+          }
       }
       if (!wide && !mild[cur]) {
         wide = true;
@@ -498,24 +493,28 @@ bool near = true;
             l[nt][k] *= exp2f(-kLift);
           }
       }
-      uint32_t pt[NT][4];               // weights of positions 8 i .. 8 i + 7 as right operands
+      // scores with their value's power of two, and whether one passes its reference too far
+      bool rises = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float t[4][2];
-        bool rises = false;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
+          float top = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            t[i][k] = fmaf(s[nt][i >> 1][(i & 1) * 2 + k], rf[nt][k], f[i].y);
-          const float top = fmaxf(fmaxf(t[0][k], t[1][k]), fmaxf(t[2][k], t[3][k]));
+          for (int i = 0; i < 4; ++i) {
+            float& t = s[nt][i >> 1][(i & 1) * 2 + k];
+            t = fmaf(t, rf[nt][k], e[i]);
+            top = fmaxf(top, t);
+          }
           rises = rises || top > mv[nt][k] + kSlack || (mv[nt][k] == -INFINITY && top > mv[nt][k]);
         }
-        if (__any_sync(0xffffffffu, rises)) {
+      if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
           float corr[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float top = fmaxf(fmaxf(t[0][k], t[1][k]), fmaxf(t[2][k], t[3][k]));
+            float top = fmaxf(fmaxf(s[nt][0][k], s[nt][0][2 + k]), fmaxf(s[nt][1][k], s[nt][1][2 + k]));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             const float mn = fmaxf(mv[nt][k], top);
@@ -531,12 +530,15 @@ bool near = true;
             o[nt][n][3] *= corr[1];
           }
         }
-        if (wide) {
+      }
+      if (wide) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float x[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = s[nt][i >> 1][(i & 1) * 2 + k] * rf[nt][k];
+            for (int i = 0; i < 4; ++i) x[i] = s[nt][i >> 1][(i & 1) * 2 + k] - e[i];
             float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -546,15 +548,22 @@ bool near = true;
                                 (tc::ex2(x[2] - base) + tc::ex2(x[3] - base)));
             m[nt][k] = mn;
           }
-        }
+      }
+      uint32_t pt[NT][4];               // weights of positions 8 i .. 8 i + 7 as right operands
+      float inv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) inv[i] = wide ? 0.0f : tc::ex2(-e[i]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
         const float up[2] = {mv[nt][0] == -INFINITY ? 0.0f : mv[nt][0] - kLift,
                              mv[nt][1] == -INFINITY ? 0.0f : mv[nt][1] - kLift};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float w0 = tc::ex2(t[i][0] - up[0]), w1 = tc::ex2(t[i][1] - up[1]);
+          const float w0 = tc::ex2(s[nt][i >> 1][(i & 1) * 2] - up[0]),
+                      w1 = tc::ex2(s[nt][i >> 1][(i & 1) * 2 + 1] - up[1]);
           if (!wide) {
-            l[nt][0] = fmaf(w0, f[i].z, l[nt][0]);
-            l[nt][1] = fmaf(w1, f[i].z, l[nt][1]);
+            l[nt][0] = fmaf(w0, inv[i], l[nt][0]);
+            l[nt][1] = fmaf(w1, inv[i], l[nt][1]);
           }
           pt[nt][i] = turn(pack_f16x2(w0, w1));
         }
@@ -563,30 +572,30 @@ bool near = true;
       // odd ones rows 8-15
       const uint32_t va = vb + off(lane & 15) + (lane >> 4) * 16;
 #pragma unroll
-      for (int n = 0; n < D / 16; n += 2) {
-        uint32_t b[2][4];              // dims 0-15: positions 0-7, 8-15; dims 16-31: the same
-        tc::ldmatrix4_trans(b[0], va + n * 16);
-        tc::ldmatrix4_trans(b[1], va + step16 + n * 16);
-        if (wild) {
+      for (int n = 0; n < D / 16; n += 2)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {      // positions 16 (i / 4) + 8 (i & 1) + 2 c + {0, 1}
-            const int x = (i >> 2) * 16 + (i & 1) * 8 + (lane & 3) * 2;
-            const uint32_t hidden = (x >= x0 ? 0x0000ffffu : 0u) | (x + 1 >= x0 ? 0xffff0000u : 0u);
-            b[i >> 2][i & 3] &= ~(nan_bytes(b[i >> 2][i & 3]) & hidden);
+        for (int g = 0; g < 2; ++g) {
+          uint32_t b[4];               // dims 0-15: positions 0-7, 8-15; dims 16-31: the same
+          tc::ldmatrix4_trans(b, va + g * step16 + n * 16);
+          if (wild) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {      // positions 16 g + 8 (i & 1) + 2 c + {0, 1}
+              const int x = g * 16 + (i & 1) * 8 + (lane & 3) * 2;
+              const uint32_t hidden =
+                  (x >= x0 ? 0x0000ffffu : 0u) | (x + 1 >= x0 ? 0xffff0000u : 0u);
+              b[i] &= ~(nan_bytes(b[i]) & hidden);
+            }
           }
-        }
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
+          for (int t = 0; t < 2; ++t) {
             uint32_t v[4];
-            e4m3x4_to_f16(__byte_perm(b[g][2 * t], 0u, 0x3120), v[0], v[1]);
-            e4m3x4_to_f16(__byte_perm(b[g][2 * t + 1], 0u, 0x3120), v[2], v[3]);
+            e4m3x4_to_f16(__byte_perm(b[2 * t], 0u, 0x3120), v[0], v[1]);
+            e4m3x4_to_f16(__byte_perm(b[2 * t + 1], 0u, 0x3120), v[2], v[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               tc::mma16h(o[nt][n + t], v, pt[nt][2 * g], pt[nt][2 * g + 1]);
           }
-      }
+        }
       if (wild) {
 #pragma unroll 1
         for (int x = x0; x < x1; ++x)
@@ -594,7 +603,7 @@ bool near = true;
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              if (pos0 + x >= seen[nt][k]) continue;
+              if (pos0 + x >= seen(nt, k)) continue;
 #pragma unroll
               for (int n = 0; n < D / 16; ++n) {     // dims 16 n + 2 (lane / 4) + {0, 1}
                 const uint32_t v = nan_bytes(lds32(vb + off(x) + n * 16 + (lane >> 3) * 4)) >>
@@ -711,11 +720,11 @@ cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
   // the ring, and behind it the joins (none with a head a warp) or the warps' Q
   const int tpos = kTile / a.hw, stage = 2 * (tpos * a.hw * D + (tpos >> a.group_shift) * 16);
   const int join = (a.hw == 4 ? 0 : a.hw) * NT * 8 * (D + 4) * 4;
-  const int q = D * NT <= 256 ? 0 : kWarps * NT * 8 * (D * 2 + 16);
+  const int q = q_in_regs(D, NT) ? 0 : kWarps * NT * 8 * (D * 2 + 16);
   int stages = D == 64 ? 4 : 3;
   // as many as let the grid's blocks of an SM all be there (228 KB, less what the
   // kernel has besides)
-  const int most = 228 * 1024 / attn_mma_blocks(D, NT * 8, true) - 13 * 1024;
+  const int most = 228 * 1024 / attn_mma_blocks(D, NT * 8, true) - 8 * 1024;
   while (stages > 2 && stages * stage + std::max(join, q) > most) --stages;
   const int smem = stages * stage + std::max(join, q);
   static std::atomic<uint64_t> full;
