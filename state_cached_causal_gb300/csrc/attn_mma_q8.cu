@@ -457,20 +457,23 @@ bool near = true;
       // ---- masks, references, weights
       const int pos0 = sg.base + j * tpos + p_warp;    // the first position
       // Draft tokens' positions are hidden from the rows before them by a weight of
-      // zero, which a NaN among their values would get through: such values (`wild`)
-      // are kept out of the product and added to the rows that see them.
+      // zero, which a NaN among their values would get through: the rows that see such
+      // values (`wild`) get a NaN, and they become zero.
       const int x0 = max(0, sg.len - a.q_len + 1 - pos0), x1 = min(32, sg.len - pos0);
       bool wild = false;
-      if (x0 < x1) {
+      if (__builtin_expect(x0 < x1, 0)) {
+#pragma unroll 1
         for (int x = x0; x < x1; ++x)
+#pragma unroll 1
           for (int i = lane; i < D / 4; i += 32)
             wild |= nan_bytes(lds32(vb + off(x) + i * 4)) != 0;
         wild = __any_sync(0xffffffffu, wild);
       }
       const uint4 all = *reinterpret_cast<const uint4*>(tr);
       const uint4 more = *reinterpret_cast<const uint4*>(tr + 16);
-      if (pos0 + 31 > sg.len - a.q_len ||
-          (all.x & all.y & all.z & all.w & more.x & more.y & more.z & more.w) != 0x01010101u) {
+      if (__builtin_expect(pos0 + 31 > sg.len - a.q_len ||
+                               (all.x & all.y & all.z & all.w & more.x & more.y & more.z &
+                                more.w) != 0x01010101u, 0)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -483,7 +486,7 @@ bool near = true;
             }
           }
       }
-      if (!wide && !mild[cur]) {
+      if (__builtin_expect(!wide && !mild[cur], 0)) {
         wide = true;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -508,7 +511,7 @@ bool near = true;
           }
           rises = rises || top > mv[nt][k] + kSlack || (mv[nt][k] == -INFINITY && top > mv[nt][k]);
         }
-      if (__any_sync(0xffffffffu, rises)) {
+      if (__builtin_expect(__any_sync(0xffffffffu, rises), 0)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float corr[2];
@@ -531,7 +534,7 @@ bool near = true;
           }
         }
       }
-      if (wide) {
+      if (__builtin_expect(wide, 0)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -568,35 +571,7 @@ bool near = true;
           pt[nt][i] = turn(pack_f16x2(w0, w1));
         }
       }
-      // ---- weighted values: of 16 dims, the even ones are rows 0-7 of a left operand, the
-      // odd ones rows 8-15
-      const uint32_t va = vb + off(lane & 15) + (lane >> 4) * 16;
-#pragma unroll
-      for (int n = 0; n < D / 16; n += 2)
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint32_t b[4];               // dims 0-15: positions 0-7, 8-15; dims 16-31: the same
-          tc::ldmatrix4_trans(b, va + g * step16 + n * 16);
-          if (wild) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {      // positions 16 g + 8 (i & 1) + 2 c + {0, 1}
-              const int x = g * 16 + (i & 1) * 8 + (lane & 3) * 2;
-              const uint32_t hidden =
-                  (x >= x0 ? 0x0000ffffu : 0u) | (x + 1 >= x0 ? 0xffff0000u : 0u);
-              b[i] &= ~(nan_bytes(b[i]) & hidden);
-            }
-          }
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            uint32_t v[4];
-            e4m3x4_to_f16(__byte_perm(b[2 * t], 0u, 0x3120), v[0], v[1]);
-            e4m3x4_to_f16(__byte_perm(b[2 * t + 1], 0u, 0x3120), v[2], v[3]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              tc::mma16h(o[nt][n + t], v, pt[nt][2 * g], pt[nt][2 * g + 1]);
-          }
-        }
-      if (wild) {
+      if (__builtin_expect(wild, 0)) {
 #pragma unroll 1
         for (int x = x0; x < x1; ++x)
 #pragma unroll
@@ -613,7 +588,37 @@ bool near = true;
                 if (v & 0xff00u) o[nt][n][2 + k] = nan;
               }
             }
+              __syncwarp();
+        // (these positions' values of this head are this warp's alone)
+#pragma unroll 1
+        for (int x = x0; x < x1; ++x)
+          for (int i = lane; i < D / 4; i += 32) {
+            const uint32_t v = lds32(vb + off(x) + i * 4);
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(vb + off(x) + i * 4), "r"(v & ~nan_bytes(v))
+                         : "memory");
+          }
+        fence_proxy_async();          // before a later copy into the same place
+        __syncwarp();
       }
+      // ---- weighted values: of 16 dims, the even ones are rows 0-7 of a left operand, the
+      // odd ones rows 8-15
+      const uint32_t va = vb + off(lane & 15) + (lane >> 4) * 16;
+#pragma unroll
+      for (int n = 0; n < D / 16; n += 2)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          uint32_t b[4];               // dims 0-15: positions 0-7, 8-15; dims 16-31: the same
+          tc::ldmatrix4_trans(b, va + g * step16 + n * 16);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            uint32_t v[4];
+            e4m3x4_to_f16(__byte_perm(b[2 * t], 0u, 0x3120), v[0], v[1]);
+            e4m3x4_to_f16(__byte_perm(b[2 * t + 1], 0u, 0x3120), v[2], v[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              tc::mma16h(o[nt][n + t], v, pt[nt][2 * g], pt[nt][2 * g + 1]);
+          }
+        }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[cur]);
     }
