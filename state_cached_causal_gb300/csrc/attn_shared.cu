@@ -106,9 +106,27 @@ struct Wait {
 
 // ---- the line -------------------------------------------------------------------
 
+// Places of a unit on the line: kAhead before its first tile (a segment's start -- Q,
+// the first copies -- takes a block as long as so many), then two a tile where two row
+// tiles take it, else one. A block takes the tiles whose first place is in its run, and
+// no run is shorter than two.
+constexpr int kAhead = 5;
+
 struct Group {
   int first, prefix, tiles;
   int64_t rows, units;        // rows of a kv head; units 0 without a prefix or requests
+  int64_t full;               // units of two whole row tiles, which come first
+  int per, wide;              // places of one of the others, and of a tile of it
+
+  __device__ __forceinline__ int per_full() const { return 2 * tiles + kAhead; }
+  __device__ __forceinline__ int64_t places() const {
+    return full * per_full() + (units - full) * per;
+  }
+  // the place of a unit's tile 0, and those of a tile
+  __device__ __forceinline__ int64_t place_of(int64_t unit) const {
+    return kAhead + (unit < full ? unit * per_full() : full * per_full() + (unit - full) * per);
+  }
+  __device__ __forceinline__ int tile_places(int64_t unit) const { return unit < full ? 2 : wide; }
 };
 template <int D>
 __device__ __forceinline__ Group group_of(const AttnArgs& a, int g) {
@@ -120,13 +138,17 @@ __device__ __forceinline__ Group group_of(const AttnArgs& a, int g) {
   r.prefix = ok ? p : 0;
   r.tiles = (r.prefix + S::kN - 1) / S::kN;
   r.rows = ok ? (int64_t)(end - r.first) * (a.G * a.q_len) : 0;
-  r.units = r.tiles > 0 ? (r.rows + S::kRowsU - 1) / S::kRowsU * a.Hkv : 0;
+  const int64_t blocks = (r.rows + S::kRowsU - 1) / S::kRowsU;     // of rows
+  r.units = r.tiles > 0 ? blocks * a.Hkv : 0;
+  r.full = S::NT == 2 && r.units > 0 ? r.units - a.Hkv : 0;
+  r.wide = S::NT == 2 && r.rows - (blocks - 1) * S::kRowsU > 128 ? 2 : 1;
+  r.per = r.wide * r.tiles + kAhead;
   return r;
 }
-
-// A unit has kAhead more places on the line than tiles, before its first: a segment's
-// start (Q, the first copies) takes a block as long as so many tiles.
-constexpr int kAhead = 3;
+// Blocks that have a run.
+__device__ __forceinline__ int64_t runs_of(int64_t grid, int64_t total) {
+  return min(grid, total / 2);
+}
 
 struct Run {
   int64_t p, end, total, grid;
@@ -143,7 +165,7 @@ __device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) 
   int64_t lines = 0, units = 0;
   for (int g = g0; g < g1; ++g) {
     const Group s = group_of<D>(a, g);
-    lines += s.units * (s.tiles + kAhead);
+    lines += s.places();
     units += s.units;
     if (blockIdx.x == 0 &&
         !attn_group_ok(a, a.cu_groups[g], a.cu_groups[g + 1], a.prefix_lens[g]))
@@ -174,11 +196,11 @@ __device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) 
     for (int g = g0; g < g1; ++g) {
       const Group s = group_of<D>(a, g);
       x.rec[g] = Rec{l, fits && s.units > 0 ? (int32_t)u : -1, s.tiles};
-      l += s.units * (s.tiles + kAhead), u += s.units;
+      l += s.places(), u += s.units;
     }
   }
   r.total = fits ? ls : 0;
-  r.grid = min((int64_t)gridDim.x, r.total);
+  r.grid = runs_of(gridDim.x, r.total);
   r.p = blockIdx.x < r.grid ? blockIdx.x * r.total / r.grid : r.total;
   r.end = blockIdx.x < r.grid ? (blockIdx.x + 1) * r.total / r.grid : r.total;
   __syncthreads();
@@ -186,8 +208,8 @@ __device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) 
     int g = g0;
     for (;; ++g) {
       const Group s = group_of<D>(a, g);
-      if (r.p < li + s.units * (s.tiles + kAhead)) break;
-      li += s.units * (s.tiles + kAhead), ui += s.units;
+      if (r.p < li + s.places()) break;
+      li += s.places(), ui += s.units;
     }
     sm[0] = g, sm[1] = li, sm[2] = ui;
   }
@@ -209,21 +231,25 @@ __device__ __forceinline__ bool segment(const PrefixArgs& x, Run& r, Seg& s) {
   using S = Shape<D>;
   while (r.p < r.end) {
     Group g = group_of<D>(x.a, r.g);
-    while (r.p >= r.line + g.units * (g.tiles + kAhead)) {     // (groups without units, too)
-      r.line += g.units * (g.tiles + kAhead);
+    while (r.p >= r.line + g.places()) {      // (groups without units, too)
+      r.line += g.places();
       r.unit += g.units;
       g = group_of<D>(x.a, ++r.g);
     }
-    const int64_t rel = r.p - r.line;
-    const int per = g.tiles + kAhead;
+    int64_t rel = r.p - r.line;
+    const bool whole = rel < g.full * g.per_full();
+    if (!whole) rel -= g.full * g.per_full();
+    const int per = whole ? g.per_full() : g.per, wide = whole ? 2 : g.wide;
     // (a 64-bit division takes a hundred instructions)
-    const int u = rel <= INT32_MAX ? (int)((uint32_t)rel / (uint32_t)per) : (int)(rel / per);
+    int u = rel <= INT32_MAX ? (int)((uint32_t)rel / (uint32_t)per) : (int)(rel / per);
     const int off = (int)(rel - (int64_t)u * per);
     const int take = (int)min((int64_t)(per - off), r.end - r.p);
     r.p += take;
-    s.j0 = max(off - kAhead, 0);
-    s.j1 = off + take - kAhead;
+    // (wide is 1 or 2)
+    s.j0 = max(off - kAhead + wide - 1, 0) >> (wide - 1);
+    s.j1 = max(off + take - kAhead + wide - 1, 0) >> (wide - 1);
     if (s.j1 <= s.j0) continue;
+    if (!whole) u += (int)g.full;
     const int mt = u / x.a.Hkv;
     s.first = g.first, s.prefix = g.prefix;
     s.h = u - mt * x.a.Hkv;
@@ -410,7 +436,7 @@ constexpr int kColS = 0, kColO = 256;      // of tensor memory: scores of both s
 // that its first pass read last.
 template <int N>
 __host__ __device__ constexpr int chunk_at(int j) {
-  return N == 64 ? 1 - j : j < 2 ? 3 - j : j - 2;
+  return N / 32 - 1 - j;
 }
 
 template <int D>
@@ -655,7 +681,7 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
       // ---- the largest score
       uint32_t v[2][32];                  // scores; of the last two chunks behind this pass
       float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < S::kN / 32; k += 2) {
         tc::ld32(sc + k * 32, v[0]);
         tc::ld32(sc + k * 32 + 32, v[1]);
@@ -693,14 +719,20 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
       const float base = m == -INFINITY ? 0.0f : -m;
       // ---- weights, in place of the scores: of 32 positions first terms, then second
       float sum = 0.0f, sum1 = 0.0f;
+#pragma unroll 1
+      for (int k0 = S::kN / 32 - 2; k0 >= 0; k0 -= 2) {
+        // (rolled: with all of a tile unrolled the roles' code was fetched more slowly
+        // than it ran)
+        if (k0 + 2 < S::kN / 32) {
+          tc::ld32(sc + k0 * 32 + 32, v[1]);
+          tc::ld32(sc + k0 * 32, v[0]);
+          tc::wait_ld(v[1]);
+          tc::wait_ld(v[0]);
+        }
 #pragma unroll
-      for (int j = 0; j < S::kN / 32; ++j) {
-        const int k = chunk_at<S::kN>(j);
-        uint32_t(&now)[32] = v[1 - (j & 1)];
-        if (j >= 2) tc::wait_ld(now);
-        // (the other buffer is free from the second chunk on)
-        if (j >= 1 && j + 1 < S::kN / 32)
-          tc::ld32(sc + chunk_at<S::kN>(j + 1 < S::kN / 32 ? j + 1 : j) * 32, v[j & 1]);
+        for (int j = 0; j < 2; ++j) {
+        const int k = k0 + 1 - j;
+        uint32_t(&now)[32] = v[1 - j];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t hi[8], lo[8];
@@ -730,6 +762,7 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
         tc::fence_before();
         __syncwarp();
         if ((r & 31) == 0) mbar_arrive(&c.p_full[stream][k]);
+        }
       }
       l += sum + sum1;
     }
@@ -879,10 +912,10 @@ __global__ void __launch_bounds__(256) attn_shared_join_kernel(const PrefixArgs 
   if (g >= 0) {
     if (rec.unit < 0) return;                     // (groups that overlap: reported)
     const int64_t R = (int64_t)(b - s.first) * rows_all + rr, mt = R / S::kRowsU;
-    const int64_t u = mt * a.Hkv + h, line = rec.line + u * (s.tiles + kAhead) + kAhead;
-    const int64_t grid = min((int64_t)x.grid, total);
+    const int64_t u = mt * a.Hkv + h, line = rec.line + s.place_of(u);
+    const int64_t grid = runs_of(x.grid, total);
     const int p0 = attn_block_of(line, total, grid);
-    const int p1 = attn_block_of(line + s.tiles - 1, total, grid);
+    const int p1 = attn_block_of(line + (int64_t)(s.tiles - 1) * s.tile_places(u), total, grid);
     two = S::NT == 2 && s.rows - mt * S::kRowsU <= 128;
     shared = (p1 - p0 + 1) * (two ? 2 : 1);
     slot = (rec.unit + u + p0) * S::kRowsU + R % S::kRowsU;
