@@ -1048,7 +1048,7 @@ cudaError_t launch_shared_join(const PrefixArgs& x, cudaStream_t st) {
   const int n = x.a.B * x.a.Hq * x.a.q_len;
   // a warp a row where that fills the GPU, else a block's eight
   return n >= 8192   ? attn_launch_beside(attn_shared_join_kernel<D, 1>, x, n, (n + 7) / 8, 256, 0, st)
-         : n >= 2048 ? attn_launch_beside(attn_shared_join_kernel<D, 2>, x, n, (n + 3) / 4, 256, 0, st)
+         : n >= 2048 ? attn_launch_beside(attn_shared_join_kernel<D, 1>, x, n, (n + 7) / 8, 256, 0, st)
                      : attn_launch_beside(attn_shared_join_kernel<D, 8>, x, n, n, 256, 0, st);
 }
 

@@ -8,13 +8,14 @@ namespace cconv {
 namespace {
 
 constexpr int kReadThreads = 256;
+constexpr int kUnits = 4;         // of a thread, requested together
 
 struct ReadArgs {
   const char *kc, *vc;
   int64_t s_page, s_tok, s_head;
   const uint8_t *ksc, *vsc;
   int64_t c_page, c_tok, c_head;
-  int32_t page_size, Hkv;
+  int32_t page_size, page_shift, Hkv;
   int64_t num_slots;
   const int32_t* slots;
   int32_t T;
@@ -26,41 +27,71 @@ struct ReadArgs {
 template <typename T, int D>
 __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a) {
   constexpr int V = Elem<T>::V, E = Elem<T>::bytes, UPR = D / V;    // units a row
-  const int64_t per = (int64_t)2 * a.Hkv * UPR, n = a.T * per;
-  for (int64_t i = (int64_t)blockIdx.x * kReadThreads + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * kReadThreads) {
-    const int64_t t = i / per;
-    int r = (int)(i - t * per);
-    const bool isv = r >= a.Hkv * UPR;
-    if (isv) r -= a.Hkv * UPR;
-    const int h = r / UPR, u = r % UPR, slot = a.slots[t];
-    if (slot < 0 || slot >= a.num_slots) {
-      if (slot >= 0) flag_error(a.dev_err, CCONV_DERR_POSITION);
-      continue;
-    }
-    const int page = slot / a.page_size, tok = slot - page * a.page_size;
-    const char* const src = (isv ? a.vc : a.kc) + page * a.s_page + tok * a.s_tok +
-                            h * a.s_head + u * V;
-    const float f = q8_scale((isv ? a.vsc : a.ksc)[page * a.c_page + tok * a.c_tok +
-                                                   h * a.c_head]);
-    float x[V];
+  const uint32_t per = 2 * a.Hkv * UPR;                             // units of a token
+  // a block's tokens at a time: units of 16 bytes for kUnits a thread, or one token
+  const int tokens = max(1u, kReadThreads * kUnits / per);
+#pragma unroll 1
+  for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < a.T; t0 += (int64_t)gridDim.x * tokens) {
+    const uint32_t n = (uint32_t)min((int64_t)tokens, a.T - t0) * per;
+#pragma unroll 1
+    for (uint32_t j0 = threadIdx.x; j0 < n; j0 += kReadThreads * kUnits) {
+      // slots, then values and scales, of all units before the first is stored
+      int slot[kUnits];
+      uint32_t raw[kUnits][V / 4], byte[kUnits];
+      char* dst[kUnits];
 #pragma unroll
-    for (int e = 0; e < V; e += 4) {
-      float y[4];
-      unpack_e4m3x4(*reinterpret_cast<const uint32_t*>(src + e), y);
+      for (int k = 0; k < kUnits; ++k) {
+        const uint32_t j = j0 + k * kReadThreads;
+        slot[k] = j < n ? a.slots[t0 + j / per] : -1;
+      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[e + j] = y[j] * f;
+      for (int k = 0; k < kUnits; ++k) {
+        const uint32_t j = j0 + k * kReadThreads, t = j / per;
+        uint32_t r = j - t * per;
+        const bool isv = r >= per / 2;
+        if (isv) r -= per / 2;
+        const int h = r / UPR, u = r % UPR;
+        if (slot[k] >= a.num_slots) {
+          flag_error(a.dev_err, CCONV_DERR_POSITION);
+          slot[k] = -1;
+        }
+        if (slot[k] < 0) continue;
+        const int page = a.page_shift >= 0 ? slot[k] >> a.page_shift : slot[k] / a.page_size;
+        const int tok = slot[k] - page * a.page_size;
+        const char* const src = (isv ? a.vc : a.kc) + page * a.s_page + tok * a.s_tok +
+                                h * a.s_head + u * V;
+        if constexpr (V == 8) {
+          const uint2 w = __ldcs(reinterpret_cast<const uint2*>(src));
+          raw[k][0] = w.x, raw[k][V / 4 - 1] = w.y;
+        } else {
+          raw[k][0] = __ldcs(reinterpret_cast<const uint32_t*>(src));
+        }
+        byte[k] = (isv ? a.vsc : a.ksc)[page * a.c_page + tok * a.c_tok + h * a.c_head];
+        dst[k] = (isv ? a.vo + (t0 + t) * a.vo_rs * E : a.ko + (t0 + t) * a.ko_rs * E) +
+                 (int64_t)r * 16;
+      }
+#pragma unroll
+      for (int k = 0; k < kUnits; ++k) {
+        if (slot[k] < 0) continue;
+        const float f = q8_scale(byte[k]);
+        float x[V];
+#pragma unroll
+        for (int e = 0; e < V; e += 4) {
+          float y[4];
+          unpack_e4m3x4(raw[k][e / 4], y);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[e + i] = y[i] * f;
+        }
+        stg16(dst[k], pack16<T>(x));
+      }
     }
-    char* const dst = isv ? a.vo + t * a.vo_rs * E : a.ko + t * a.ko_rs * E;
-    stg16(dst + (int64_t)r * 16, pack16<T>(x));
   }
 }
 
 template <typename T>
 cudaError_t launch_read(const ReadArgs& a, int D, int sms, cudaStream_t st) {
-  const int64_t n = (int64_t)a.T * 2 * a.Hkv * (D / Elem<T>::V);
-  const unsigned grid =
-      (unsigned)std::min<int64_t>((n + kReadThreads - 1) / kReadThreads, (int64_t)sms * 8);
+  const int64_t n = (int64_t)a.T * 2 * a.Hkv * (D / Elem<T>::V), per = kReadThreads * kUnits;
+  const unsigned grid = (unsigned)std::min<int64_t>((n + per - 1) / per, (int64_t)sms * 64);
   if (D == 64)
     kv_read_kernel<T, 64><<<grid, kReadThreads, 0, st>>>(a);
   else if (D == 128)
@@ -98,6 +129,9 @@ extern "C" int kv_cache_read_q8(kv_cache_q8_t cache, const int32_t* slot_mapping
   a.vsc = cache.v_scale;
   a.c_page = cache.c_page, a.c_tok = cache.c_token, a.c_head = cache.c_head;
   a.page_size = cache.page_size;
+  a.page_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if (cache.page_size == 1 << s) a.page_shift = s;
   a.Hkv = cache.num_kv_heads;
   a.num_slots = (int64_t)cache.num_pages * cache.page_size;
   a.slots = slot_mapping;
