@@ -126,10 +126,15 @@ def test_both_marshallings_reach_the_library(in_c, monkeypatch):
         monkeypatch.setattr(ops, "_fast", None)
     norm, read, attn, q8, i = _calls()
     attn = dict(attn, workspace=torch.zeros(1 << 26, dtype=U8), lse=torch.zeros(4, 4))
+    groups = dict(cu_groups=i(3), prefix_lens=i(2))
+    shared = dict(attn, q=attn["q"].bfloat16(), out=attn["out"].bfloat16(), **groups)
+    plain = {k: v for k, v in shared.items() if not k.endswith("_scale")}
+    plain.update(k_cache=torch.zeros(5, 16, 2, 64).bfloat16(), v_cache=torch.zeros(5, 16, 2, 64).bfloat16())
     try:
-        for fn, call in (("attn_norm_rope_cache_q8", norm), ("kv_cache_read_q8", read), ("attn_decode_q8", attn)):
+        for fn, call in (("attn_norm_rope_cache_q8", norm), ("kv_cache_read_q8", read), ("attn_decode_q8", attn),
+                         ("attn_decode_shared_q8", shared), ("attn_decode_shared", plain)):
             for scales in (q8["k_scale"], q8["k_scale"].view(torch.float8_e8m0fnu)):
-                call = dict(call, k_scale=scales, dev_err=i(1))
+                call = dict(call, dev_err=i(1), **(dict(k_scale=scales) if "k_scale" in call else {}))
                 tensors = [n for n, t in call.items() if torch.is_tensor(t)]
                 here = {n: _Placed(t) if n in tensors else t for n, t in call.items()}
                 with pytest.raises(ops.CConvError, match=fn):
@@ -141,3 +146,125 @@ def test_both_marshallings_reach_the_library(in_c, monkeypatch):
                 assert not seen
     finally:
         ops._load_fast(lib)
+
+
+# ---- attention of groups that share a prefix ----------------------------------------
+
+def _kv(c):
+    return ops.KvCache(c.k, c.v, c.s_page, c.s_token, c.s_head, c.num_pages, c.page_size, c.num_kv_heads,
+                       c.head_dim, 1)
+
+
+SHARED = [(dict(q=None), -1), (dict(qs=128), -1), (dict(o=FAKE + 2), -1), (dict(os=513), -1), (dict(bt=None), -1),
+          (dict(bts=4), -1), (dict(w=-1), -1), (dict(w=2 ** 28, bts=2 ** 28), -1), (dict(sl=None), -1),
+          (dict(cu=None), -1), (dict(pl=None), -1), (dict(G=-1), -1), (dict(G=4), -1), (dict(B=-1, G=0), -1),
+          (dict(B=2 ** 30), -1), (dict(ns=-1), -1), (dict(ns=8), -2), (dict(hq=5), -1), (dict(hq=0), -1),
+          (dict(hq=34, ns=3), -2), (dict(dt=0), -2), (dict(dt=4), -1), (dict(B=0, G=0), 0), (dict(), -3),
+          (dict(G=0, cu=None, pl=None), -3)]
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("kw,want", SHARED)
+@no_gpu
+def test_shared_arguments(lib, kw, want, q8):
+    a = dict(q=FAKE, qs=512, c=cache(), bt=FAKE, bts=5, w=5, sl=FAKE, B=3, cu=FAKE, pl=FAKE, G=2, ns=0, hq=4, dt=1,
+             o=FAKE, os=512, lse=None, ws=FAKE, wsb=1 << 40)
+    a.update(kw)
+    c = a["c"] if q8 else _kv(a["c"])
+    if not q8 and a["dt"] == 0:
+        c.dtype = 0
+    fn = lib.attn_decode_shared_q8 if q8 else lib.attn_decode_shared
+    assert fn(a["q"], a["qs"], c, a["bt"], a["bts"], a["w"], a["sl"], a["B"], a["cu"], a["pl"], a["G"], a["ns"],
+              a["hq"], 0.1, a["dt"], a["o"], a["os"], a["lse"], a["ws"], a["wsb"], None, None) == want
+
+
+@pytest.mark.parametrize("kw,want", BAD_CACHE)
+@no_gpu
+def test_shared_caches(lib, kw, want):
+    for q8 in (True, False):
+        if not q8 and kw["c"].k == FAKE and kw["c"].v == FAKE and want == -1 and (
+                not kw["c"].k_scale or not kw["c"].v_scale or min(kw["c"].c_page, kw["c"].c_token,
+                                                                   kw["c"].c_head) <= 0):
+            continue                                    # (only scales are wrong)
+        c = kw["c"] if q8 else _kv(kw["c"])
+        if not q8 and c.s_token == 8:
+            continue                                    # (16 bytes of bf16)
+        fn = lib.attn_decode_shared_q8 if q8 else lib.attn_decode_shared
+        assert fn(FAKE, 512, c, FAKE, 5, 5, FAKE, 3, FAKE, FAKE, 2, 0, 4, 0.1, 1, FAKE, 512, None, FAKE, 1 << 40,
+                  None, None) == want
+
+
+@no_gpu
+def test_shared_workspace_sizes_are_checked(lib):
+    f = lib.attn_decode_shared_workspace_bytes
+    assert f(-1, 0, 0, 4, 2, 128) == -1 and f(1, 0, 0, 5, 2, 128) == -1 and f(2, 3, 0, 4, 2, 128) == -1
+    assert f(2, -1, 0, 4, 2, 128) == -1 and f(1, 0, 9, 4, 2, 128) == -2 and f(1, 1, 0, 4, 2, 80) == -2
+
+
+def test_shared_binding_checks(monkeypatch):
+    _, _, attn, q8, i = _calls()
+    plain = {k: v for k, v in _two()[2].items()}
+    bf = lambda t: t.bfloat16() if t.dtype == torch.float32 else t      # noqa: E731
+    plain = {k: bf(v) if torch.is_tensor(v) else v for k, v in plain.items()}
+    attn = {k: bf(v) if torch.is_tensor(v) and k in ("q", "out") else v for k, v in attn.items()}
+    groups = dict(cu_groups=i(3), prefix_lens=i(2))
+    for fn, call in ((ops.attn_decode_shared, {**plain, **groups}), (ops.attn_decode_shared_q8, {**attn, **groups})):
+        for bad, err in ((dict(cu_groups=i(3).long()), TypeError), (dict(prefix_lens=i(2).float()), TypeError),
+                         (dict(cu_groups=i(2)), ValueError), (dict(cu_groups=i(4)), ValueError),
+                         (dict(cu_groups=i(6)[::2]), ValueError), (dict(prefix_lens=i(2, 2)[:, 0]), ValueError),
+                         (dict(seq_lens=i(4).long()), TypeError), (dict(block_table=i(3, 3)), ValueError),
+                         (dict(dev_err=i(0)), ValueError), (dict(workspace=torch.zeros(64, 64, dtype=U8).t()),
+                                                            ValueError)):
+            with pytest.raises(err):
+                fn(**{**call, **bad})
+        with pytest.raises(ValueError, match="must live on the GPU"):
+            fn(**call)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["norm", "read", "attn", "attn32", "shared", "shared8"])
+def test_both_marshallings_agree(what, monkeypatch):
+    """The C module serves these calls, and Python's marshalling gives the same results."""
+    from tests import _q8
+    from tests.test_attn_shared import Case
+    ops.load()
+    if ops._fast is None:
+        pytest.skip("the C module is not built")
+    dev, dt = torch.device("cuda"), torch.float32 if what == "attn32" else torch.bfloat16
+    c = _q8.case(3, [40, 7, 100], 4, 2, 64, 16, 1, dt)
+    q, kc, vc, ks, vs, table, lens = c
+    sh = Case(4, [(40, [50, 60, 41])], 4, 2, 64, 16, 1, what == "shared8")
+    cos = torch.randn(32, 64, device=dev)
+    i = lambda *v: torch.tensor(v, dtype=torch.int32, device=dev)       # noqa: E731
+    rows = torch.randn(3, 2, 64, device=dev).to(dt)
+
+    def call():
+        caches = [t.view(U8).clone() for t in (kc, vc, ks, vs)]
+        k, v = (t.view(F8) for t in caches[:2])
+        out, lse = torch.zeros_like(q, memory_format=torch.contiguous_format), torch.zeros(3, 4, device=dev)
+        back = [torch.zeros(3, 2, 64, device=dev, dtype=dt) for _ in range(2)]
+        if what == "norm":
+            ops.attn_norm_rope_cache_q8(q, rows, rows, None, rows[0, 0] * 0 + 1, 1e-6, cos, i(1, 2, 3), True, k, v,
+                                        *caches[2:], i(5, -1, 30), out)
+        elif what == "read":
+            ops.kv_cache_read_q8(k, v, *caches[2:], i(3, -1, 17), *back)
+        elif what.startswith("shared"):
+            out = torch.zeros_like(sh.q, memory_format=torch.contiguous_format)
+            sh.call(out, lse)
+        else:
+            ops.attn_decode_q8(q, k, v, *caches[2:], table, lens, 0, 0.125, out, lse)
+        torch.cuda.synchronize()
+        return [*caches, out, lse, *back]
+
+    served, real = [], ops._fast
+
+    class Spy:
+        def __getattr__(self, n):
+            return lambda *x: served.append(getattr(real, n)(*x)) or served[-1]
+
+    monkeypatch.setattr(ops, "_fast", Spy())
+    one = call()
+    assert served == [0]
+    monkeypatch.setattr(ops, "_fast", None)
+    for a, b in zip(one, call()):
+        assert torch.equal(a, b)
