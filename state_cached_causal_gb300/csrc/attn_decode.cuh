@@ -44,8 +44,11 @@ struct AttnArgs {
   int32_t* dev_err;
   const uint8_t *ksc, *vsc;   // scales of a cache in 8 bits
   int64_t c_page, c_tok, c_head;
-  const int32_t *cu_groups, *prefix_lens;   // of attn_decode_shared (attn_shared.cu)
-  int32_t groups;
+  // of attn_decode_shared (attn_shared.cu): groups, rows of a unit and positions of a
+  // tile of a prefix, positions of a tile of the rest; SMs, and what a place of the
+  // prefixes' line and a tile of the rest cost an SM, in sixteenths of a microsecond
+  const int32_t *cu_groups, *prefix_lens;
+  int32_t groups, unit_rows, prefix_tile, own_tile, sms, place_cost, tile_cost;
 };
 
 // Blocks of the bf16 kernels that an SM holds at once, by their registers and
@@ -106,6 +109,56 @@ __device__ __forceinline__ int attn_tiles(const AttnArgs& a, int b, int tile) {
   return n <= 0 ? 1 : (n + tile - 1) / tile;
 }
 
+// ---- prefixes on their line, and the SMs of the two kernels of attn_decode_shared ----
+
+// Places of a unit (attn_shared.cu) on the line: kAhead before its first tile (a
+// segment's start -- Q, the first copies -- takes a block as long as so many), then two
+// a tile where two row tiles take it, else one. A block takes the tiles whose first
+// place is in its run, and no run is shorter than two.
+constexpr int kAhead = 5;
+
+struct AttnGroup {
+  int first, prefix, tiles;
+  int64_t rows, units;        // rows of a kv head; units 0 without a prefix or requests
+  int64_t full;               // units of two whole row tiles, which come first
+  int per, wide;              // places of one of the others, and of a tile of it
+
+  __device__ __forceinline__ int per_full() const { return 2 * tiles + kAhead; }
+  __device__ __forceinline__ int64_t places() const {
+    return full * per_full() + (units - full) * per;
+  }
+  // the place of a unit's tile 0, and those of a tile
+  __device__ __forceinline__ int64_t place_of(int64_t unit) const {
+    return kAhead + (unit < full ? unit * per_full() : full * per_full() + (unit - full) * per);
+  }
+  __device__ __forceinline__ int tile_places(int64_t unit) const { return unit < full ? 2 : wide; }
+};
+__device__ __forceinline__ AttnGroup attn_group_of(const AttnArgs& a, int g) {
+  AttnGroup r;
+  r.first = a.cu_groups[g];
+  const int end = a.cu_groups[g + 1], p = a.prefix_lens[g];
+  const bool ok = attn_group_ok(a, r.first, end, p), two = a.unit_rows > 128;
+  r.prefix = ok ? p : 0;
+  r.tiles = (r.prefix + a.prefix_tile - 1) / a.prefix_tile;
+  r.rows = ok ? (int64_t)(end - r.first) * (a.G * a.q_len) : 0;
+  const int64_t blocks = (r.rows + a.unit_rows - 1) / a.unit_rows;     // of rows
+  r.units = r.tiles > 0 ? blocks * a.Hkv : 0;
+  r.full = two && r.units > 0 ? r.units - a.Hkv : 0;
+  r.wide = two && r.rows - (blocks - 1) * a.unit_rows > 128 ? 2 : 1;
+  r.per = r.wide * r.tiles + kAhead;
+  return r;
+}
+
+// The SMs that take the prefixes, the others taking the rest meanwhile: as the work of
+// both is, by what an SM needs for it. Every block of both kernels comes to the same
+// number. (One after the other on all SMs: 256 requests 153 us, groups in 8 bits 110.)
+__device__ __forceinline__ int attn_prefix_sms(const AttnArgs& a, int64_t places, int64_t tiles) {
+  if (places == 0) return 0;
+  const int64_t pc = places * a.place_cost, tc = tiles * a.tile_cost;
+  const int64_t own = (a.sms * tc + pc + tc - 1) / (pc + tc);
+  return a.sms - (int)min(max(own, (int64_t)2), (int64_t)a.sms * 5 / 8);
+}
+
 // The block's run [p, end) of the line and the request that p lies in.
 struct AttnRun {
   int64_t p, end, total;
@@ -142,9 +195,22 @@ __device__ __forceinline__ bool attn_split(const AttnArgs& a, int tile, int64_t 
   incl += base;
   const int64_t units = a.units;
   r.total = sum * units;
+  int64_t blocks = gridDim.x;
+  if constexpr (SHARED) {
+    int64_t places = 0;
+    for (int g = tid; g < a.groups; g += THREADS) places += attn_group_of(a, g).places();
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) places += __shfl_xor_sync(0xffffffffu, places, d);
+    if ((tid & 31) == 0) sm[THREADS / 32 + (tid >> 5)] = places;
+    __syncthreads();
+    places = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) places += sm[THREADS / 32 + w];
+    blocks = blocks / a.sms * (a.sms - attn_prefix_sms(a, places, r.total));
+  }
   // no run is empty: where there are fewer tiles than blocks, the blocks past
   // the tiles' number have none
-  r.grid = min((int64_t)gridDim.x, r.total);
+  r.grid = min(blocks, r.total);
   r.p = blockIdx.x < r.grid ? blockIdx.x * r.total / r.grid : r.total;
   r.end = blockIdx.x < r.grid ? (blockIdx.x + 1) * r.total / r.grid : r.total;
   __syncthreads();

@@ -14,7 +14,7 @@
 // time, so that K and V come from memory once and from the L2 for the others. A
 // block's warps:
 // - four copy K and V of a tile, row by row wherever its page lies, into a ring in the
-//   128-byte swizzle (from 8 bits: converted to bf16 on the way, exactly);
+//   128-byte swizzle (from 8 bits: by way of a place of bytes, converted to bf16, exactly);
 // - one issues the products on tcgen05: scores S = Q K^T into tensor memory, then
 //   O += P V with P from tensor memory, O in tensor memory;
 // - two times four are a softmax each, a row a thread: maximum and weights of a tile of
@@ -52,14 +52,14 @@ struct Rec {          // a group's place on the line and among the units (-1: no
 
 struct PrefixArgs {
   AttnArgs a;
-  Rec* rec;           // [groups + 1]: of each group, and the line's length
+  Rec* rec;           // [groups + 1]: of each group; the line's length and its runs
   float* po;          // [units + grid][NT * 128][D]: weighted values
   float2* ps;         // [units + grid][NT * 128]: maximum (natural), sum
   int64_t max_units;
   int32_t grid;
 };
 
-template <int D>
+template <int D, bool Q8 = false>
 struct Shape {
   static constexpr int NT = D == 256 ? 1 : 2;            // streams
   static constexpr int kRowsU = 128 * NT;                // rows of a unit
@@ -68,13 +68,14 @@ struct Shape {
   static constexpr int kPanel = kN * 128;                // 64 dims of a tile
   static constexpr int kQ = D / 64 * kPanelQ;
   static constexpr int kStage = D / 64 * kPanel;
-  static constexpr int kStages = D == 64 ? 8 : 5;
+  static constexpr int kRaw = Q8 ? 4 : 0;                // items of bytes on their way
+  static constexpr int kStages = (D == 64 ? 8 : 5) - kRaw / 2;
 };
 
 struct Ctl {
   uint64_t full[8], empty[8];
   uint64_t q_full[2], s_full[2], p_full[2][4], o_full[2], fin;
-  int64_t scan[2 * (kThreads / 32) + 4];
+  int64_t scan[3 * (kThreads / 32)];
   uint32_t mask[kMasks][kCopyWarps];
   uint32_t tmem;
   int dead;
@@ -106,48 +107,9 @@ struct Wait {
 
 // ---- the line -------------------------------------------------------------------
 
-// Places of a unit on the line: kAhead before its first tile (a segment's start -- Q,
-// the first copies -- takes a block as long as so many), then two a tile where two row
-// tiles take it, else one. A block takes the tiles whose first place is in its run, and
-// no run is shorter than two.
-constexpr int kAhead = 5;
-
-struct Group {
-  int first, prefix, tiles;
-  int64_t rows, units;        // rows of a kv head; units 0 without a prefix or requests
-  int64_t full;               // units of two whole row tiles, which come first
-  int per, wide;              // places of one of the others, and of a tile of it
-
-  __device__ __forceinline__ int per_full() const { return 2 * tiles + kAhead; }
-  __device__ __forceinline__ int64_t places() const {
-    return full * per_full() + (units - full) * per;
-  }
-  // the place of a unit's tile 0, and those of a tile
-  __device__ __forceinline__ int64_t place_of(int64_t unit) const {
-    return kAhead + (unit < full ? unit * per_full() : full * per_full() + (unit - full) * per);
-  }
-  __device__ __forceinline__ int tile_places(int64_t unit) const { return unit < full ? 2 : wide; }
-};
-template <int D>
-__device__ __forceinline__ Group group_of(const AttnArgs& a, int g) {
-  using S = Shape<D>;
-  Group r;
-  r.first = a.cu_groups[g];
-  const int end = a.cu_groups[g + 1], p = a.prefix_lens[g];
-  const bool ok = attn_group_ok(a, r.first, end, p);
-  r.prefix = ok ? p : 0;
-  r.tiles = (r.prefix + S::kN - 1) / S::kN;
-  r.rows = ok ? (int64_t)(end - r.first) * (a.G * a.q_len) : 0;
-  const int64_t blocks = (r.rows + S::kRowsU - 1) / S::kRowsU;     // of rows
-  r.units = r.tiles > 0 ? blocks * a.Hkv : 0;
-  r.full = S::NT == 2 && r.units > 0 ? r.units - a.Hkv : 0;
-  r.wide = S::NT == 2 && r.rows - (blocks - 1) * S::kRowsU > 128 ? 2 : 1;
-  r.per = r.wide * r.tiles + kAhead;
-  return r;
-}
 // Blocks that have a run.
-__device__ __forceinline__ int64_t runs_of(int64_t grid, int64_t total) {
-  return min(grid, total / 2);
+__device__ __forceinline__ int64_t runs_of(int64_t sms, int64_t total) {
+  return min(sms, total / 2);
 }
 
 struct Run {
@@ -164,13 +126,17 @@ __device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) 
   const int g0 = min(a.groups, tid * per), g1 = min(a.groups, g0 + per);
   int64_t lines = 0, units = 0;
   for (int g = g0; g < g1; ++g) {
-    const Group s = group_of<D>(a, g);
+    const AttnGroup s = attn_group_of(a, g);
     lines += s.places();
     units += s.units;
     if (blockIdx.x == 0 &&
         !attn_group_ok(a, a.cu_groups[g], a.cu_groups[g + 1], a.prefix_lens[g]))
       flag_error(a.dev_err, CCONV_DERR_GROUP);
   }
+  int64_t own = 0;            // tiles of the requests' own positions
+  for (int b = tid; b < a.B; b += kThreads) own += attn_tiles<true>(a, b, a.own_tile);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) own += __shfl_xor_sync(0xffffffffu, own, d);
   int64_t li = lines, ui = units;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -178,36 +144,38 @@ __device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) 
     if ((tid & 31) >= d) li += l, ui += u;
   }
   constexpr int kWarps = kThreads / 32;
-  if ((tid & 31) == 31) sm[tid >> 5] = li, sm[kWarps + (tid >> 5)] = ui;
+  if ((tid & 31) == 31)
+    sm[tid >> 5] = li, sm[kWarps + (tid >> 5)] = ui, sm[2 * kWarps + (tid >> 5)] = own;
   __syncthreads();
+  own = 0;
   int64_t lb = 0, ub = 0, ls = 0, us = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < (tid >> 5)) lb += sm[w], ub += sm[kWarps + w];
-    ls += sm[w], us += sm[kWarps + w];
+    ls += sm[w], us += sm[kWarps + w], own += sm[2 * kWarps + w];
   }
   li += lb - lines, ui += ub - units;         // before this thread's groups
   // (groups that overlap may have more rows than the call: none is taken then)
   const bool fits = us <= x.max_units;
+  r.total = fits ? ls : 0;
+  r.grid = runs_of(attn_prefix_sms(a, ls, own * a.units), r.total);
   if (blockIdx.x == 0) {
     if (!fits && tid == 0) flag_error(a.dev_err, CCONV_DERR_GROUP);
-    if (tid == 0) x.rec[a.groups] = Rec{fits ? ls : 0, -1, 0};      // the line's length
+    if (tid == 0) x.rec[a.groups] = Rec{r.total, (int32_t)r.grid, 0};
     int64_t l = li, u = ui;
     for (int g = g0; g < g1; ++g) {
-      const Group s = group_of<D>(a, g);
+      const AttnGroup s = attn_group_of(a, g);
       x.rec[g] = Rec{l, fits && s.units > 0 ? (int32_t)u : -1, s.tiles};
       l += s.places(), u += s.units;
     }
   }
-  r.total = fits ? ls : 0;
-  r.grid = runs_of(gridDim.x, r.total);
   r.p = blockIdx.x < r.grid ? blockIdx.x * r.total / r.grid : r.total;
   r.end = blockIdx.x < r.grid ? (blockIdx.x + 1) * r.total / r.grid : r.total;
   __syncthreads();
   if (lines > 0 && r.p >= li && r.p < li + lines) {
     int g = g0;
     for (;; ++g) {
-      const Group s = group_of<D>(a, g);
+      const AttnGroup s = attn_group_of(a, g);
       if (r.p < li + s.places()) break;
       li += s.places(), ui += s.units;
     }
@@ -230,11 +198,11 @@ template <int D>
 __device__ __forceinline__ bool segment(const PrefixArgs& x, Run& r, Seg& s) {
   using S = Shape<D>;
   while (r.p < r.end) {
-    Group g = group_of<D>(x.a, r.g);
+    AttnGroup g = attn_group_of(x.a, r.g);
     while (r.p >= r.line + g.places()) {      // (groups without units, too)
       r.line += g.places();
       r.unit += g.units;
-      g = group_of<D>(x.a, ++r.g);
+      g = attn_group_of(x.a, ++r.g);
     }
     int64_t rel = r.p - r.line;
     const bool whole = rel < g.full * g.per_full();
@@ -300,8 +268,9 @@ struct Row {
 
 template <int D, bool Q8>
 __device__ __forceinline__ bool copy_role(const PrefixArgs& x, Run run, Ctl& c,
-                                          unsigned char* ring, const Wait& wait) {
-  using S = Shape<D>;
+                                          unsigned char* ring, unsigned char* raw,
+                                          const Wait& wait) {
+  using S = Shape<D, Q8>;
   const AttnArgs& a = x.a;
   constexpr int kRowsW = S::kN / kCopyWarps;            // rows of a warp: lane r has row r's
   constexpr int kRowBytes = D * (Q8 ? 1 : 2), kLanes = kRowBytes / 16;   // of a row
@@ -379,37 +348,46 @@ __device__ __forceinline__ bool copy_role(const PrefixArgs& x, Run run, Ctl& c,
       now = then, then = after;
     }
   } else {
-    // An item's values are requested while the one before it is converted, their
-    // scales an item earlier, its pages another one.
-    uint4 v[kPasses];
-    auto fetch = [&](const Piece& p, const Row& row) {
+    // An item's bytes come by copies of the thread that converts them, to a place of its
+    // own, three items ahead; pages are looked up an item before that. (With the bytes
+    // of one item on their way, in registers, the copies' latency was what a tile took.)
+    const uint32_t mine = smem_addr(raw) + (threadIdx.x - kCopyWarp0 * 32) * 16;
+    auto issue = [&](const Piece& p, int it) {
+      const Row row = row_of(p);
       const char* const base = p.isv ? a.vc : a.kc;
 #pragma unroll
       for (int k = 0; k < kPasses; ++k) {
         const int64_t at = __shfl_sync(0xffffffffu, row.at, k * kPer + sub);
-        v[k] = at >= 0 ? ldg16(base + at + u * 16) : make_uint4(0u, 0u, 0u, 0u);
+        cp_async16(mine + (it % S::kRaw * kPasses + k) * (kCopyWarps * 512),
+                   base + (at >= 0 ? at + u * 16 : 0), at >= 0);
       }
+      cp_async_commit();
+      return row;
     };
-    Piece now = next(), then = next(), later = next();
-    Row row = row_of(now), row1 = row_of(then);
-    fetch(now, row);
+    Piece p0 = next(), p1 = next(), p2 = next(), p3 = next();
+    Row r0 = issue(p0, 0), r1 = issue(p1, 1), r2 = issue(p2, 2);
 #pragma unroll 1
-    for (int it = 0; now.there; ++it) {
+    for (int it = 0; p0.there; ++it) {
       const int st = it % S::kStages;
-      const Row row2 = row_of(later);
-      const Piece after = next();
+      const Row r3 = issue(p3, it + 3);
+      const Piece p4 = next();
+      cp_async_wait<3>();
       if (!wait(&c.empty[st], (it / S::kStages & 1) ^ 1)) return false;
-      note(now, row);
+      note(p0, r0);
       unsigned char* const dst = ring + st * S::kStage;
 #pragma unroll
       for (int p = 0; p < kPasses; ++p) {
         const int r = p * kPer + sub;
-        const float k = __shfl_sync(0xffffffffu, row.f, r);
-        uint32_t o[8];
+        const float k = __shfl_sync(0xffffffffu, r0.f, r);
+        uint32_t v[4], o[8];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "r"(mine + (it % S::kRaw * kPasses + p) * (kCopyWarps * 512))
+                     : "memory");
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float y[4];
-          unpack_e4m3x4((&v[p].x)[e], y);
+          unpack_e4m3x4(v[e], y);
           o[2 * e] = pack_bf16x2(y[0] * k, y[1] * k);
           o[2 * e + 1] = pack_bf16x2(y[2] * k, y[3] * k);
         }
@@ -420,9 +398,8 @@ __device__ __forceinline__ bool copy_role(const PrefixArgs& x, Run run, Ctl& c,
       }
       fence_proxy_async();
       mbar_arrive(&c.full[st]);
-      now = then, then = later, later = after;
-      row = row1, row1 = row2;
-      fetch(now, row);
+      p0 = p1, p1 = p2, p2 = p3, p3 = p4;
+      r0 = r1, r1 = r2, r2 = r3;
     }
   }
   return true;
@@ -439,10 +416,10 @@ __host__ __device__ constexpr int chunk_at(int j) {
   return N / 32 - 1 - j;
 }
 
-template <int D>
+template <int D, bool Q8>
 __device__ __forceinline__ bool mma_role(const PrefixArgs& x, Run run, Ctl& c, uint32_t q_addr,
                                          uint32_t ring, const Wait& wait, uint32_t tmem) {
-  using S = Shape<D>;
+  using S = Shape<D, Q8>;
   constexpr uint32_t kIdS = tc::idesc(128, S::kN), kIdO = tc::idesc(128, D, false, true);
   const uint64_t q0 = tc::desc_sw128(q_addr, 16);
   const uint64_t k0 = tc::desc_sw128(ring, 16), v0 = tc::desc_sw128(ring, S::kPanel);
@@ -807,11 +784,12 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
 
 template <int D, bool Q8>
 __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixArgs x) {
-  using S = Shape<D>;
+  using S = Shape<D, Q8>;
   extern __shared__ __align__(1024) unsigned char shared_dyn[];
   unsigned char* const base = shared_dyn + ((1024u - (smem_addr(shared_dyn) & 1023u)) & 1023u);
   unsigned char* const ring = base + S::NT * S::kQ;
-  Ctl& c = *reinterpret_cast<Ctl*>(ring + S::kStages * S::kStage);
+  unsigned char* const raw = ring + S::kStages * S::kStage;
+  Ctl& c = *reinterpret_cast<Ctl*>(raw + S::kRaw * S::kStage / 2);
   const int tid = threadIdx.x;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -847,10 +825,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
     const int stream = warp / kSoftWarps;
     if (stream < S::NT) soft_role<D>(x, run, c, base, wait, tmem, stream);
   } else if (warp < kMmaWarp) {
-    copy_role<D, Q8>(x, run, c, ring, wait);
+    copy_role<D, Q8>(x, run, c, ring, raw, wait);
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
-    mma_role<D>(x, run, c, smem_addr(base), smem_addr(ring), wait, tmem);
+    mma_role<D, Q8>(x, run, c, smem_addr(base), smem_addr(ring), wait, tmem);
     // every product that was issued ends before tensor memory is given back
     if (tc::elect()) tc::commit(&c.fin);
     __syncwarp();
@@ -889,16 +867,12 @@ __global__ void __launch_bounds__(256) attn_shared_join_kernel(const PrefixArgs 
   const int unit = h / a.hw * a.rblocks + rr / a.rows;
   const int64_t bu = (int64_t)b * a.units + unit;
   const int g = attn_start(a, b) > 0 ? attn_group(a, b) : -1;
-  Group s = {};
-  if (g >= 0) s = group_of<D>(a, g);
+  AttnGroup s = {};
+  if (g >= 0) s = attn_group_of(a, g);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 c = *reinterpret_cast<const int2*>(a.meta + bu * 2);
-  Rec rec = {};
-  int64_t total = 0;
-  if (g >= 0) {
-    rec = x.rec[g];
-    total = x.rec[a.groups].line;
-  }
+  Rec rec = {}, all = {};
+  if (g >= 0) rec = x.rec[g], all = x.rec[a.groups];
   // own positions
   if (!attn_joins(c.x, c.y, a.grid)) return;
   const int64_t one = (int64_t)a.hw * a.rows * (D + 2);
@@ -913,9 +887,9 @@ __global__ void __launch_bounds__(256) attn_shared_join_kernel(const PrefixArgs 
     if (rec.unit < 0) return;                     // (groups that overlap: reported)
     const int64_t R = (int64_t)(b - s.first) * rows_all + rr, mt = R / S::kRowsU;
     const int64_t u = mt * a.Hkv + h, line = rec.line + s.place_of(u);
-    const int64_t grid = runs_of(x.grid, total);
-    const int p0 = attn_block_of(line, total, grid);
-    const int p1 = attn_block_of(line + (int64_t)(s.tiles - 1) * s.tile_places(u), total, grid);
+    const int p0 = attn_block_of(line, all.line, all.unit);
+    const int p1 =
+        attn_block_of(line + (int64_t)(s.tiles - 1) * s.tile_places(u), all.line, all.unit);
     two = S::NT == 2 && s.rows - mt * S::kRowsU <= 128;
     shared = (p1 - p0 + 1) * (two ? 2 : 1);
     slot = (rec.unit + u + p0) * S::kRowsU + R % S::kRowsU;
@@ -1032,8 +1006,9 @@ int check_shared(int32_t num_seqs, int32_t num_groups, int32_t n_spec, int32_t H
 
 template <int D, bool Q8>
 cudaError_t launch_prefix(const PrefixArgs& x, cudaStream_t st) {
-  using S = Shape<D>;
-  constexpr int smem = 1024 + S::NT * S::kQ + S::kStages * S::kStage + (int)sizeof(Ctl);
+  using S = Shape<D, Q8>;
+  constexpr int smem = 1024 + S::NT * S::kQ + S::kStages * S::kStage + S::kRaw * S::kStage / 2 +
+                       (int)sizeof(Ctl);
   static_assert(smem <= 227 * 1024, "shared memory of a block");
   static std::atomic<uint64_t> full;
   const cudaError_t e =
@@ -1083,6 +1058,14 @@ int decode_shared(AttnArgs& a, int D, bool q8, const void* q, int64_t q_row_stri
   a.cu_groups = cu_groups;
   a.prefix_lens = prefix_lens;
   a.groups = num_groups;
+  a.unit_rows = D == 256 ? 128 : 256;
+  a.prefix_tile = D == 256 ? 64 : 128;
+  a.own_tile = (q8 ? 128 : 64) / a.hw;
+  a.sms = sms;
+  // measured for heads of 128: a place 1.15 us; a tile of a block, of which an SM has two,
+  // 1 us (8 bits and 16 rows 1.75 us)
+  a.place_cost = D == 256 ? 32 : D == 128 ? 18 : 12;
+  a.tile_cost = (q8 && a.rows > 8 ? 14 : 8) * D / 128 + 1;
   PrefixArgs x;
   x.a = a;
   x.rec = reinterpret_cast<Rec*>(ws + p.rec);

@@ -60,7 +60,7 @@ def test_the_shared_kernel():
     assert soft.count("empty_part<D>(x, s, stream);") == 2 and soft.count("x.ps[row0 + lane] =") == 1
 
 
-K = int(re.search(r"constexpr int kAhead = (\d+);", source("attn_shared.cu")).group(1))
+K = int(re.search(r"constexpr int kAhead = (\d+);", source("attn_decode.cuh")).group(1))
 
 
 def split(groups, hkv, streams, grid):
