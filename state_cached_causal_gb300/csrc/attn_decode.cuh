@@ -45,10 +45,12 @@ struct AttnArgs {
   const uint8_t *ksc, *vsc;   // scales of a cache in 8 bits
   int64_t c_page, c_tok, c_head;
   // of attn_decode_shared (attn_shared.cu): groups, rows of a unit and positions of a
-  // tile of a prefix, positions of a tile of the rest; SMs, and what a place of the
-  // prefixes' line and a tile of the rest cost an SM, in sixteenths of a microsecond
+  // tile of a prefix, positions of a tile of the rest; places of a segment's start, of a
+  // tile of two row tiles; SMs, and what a place of the prefixes' line and a tile of the
+  // rest cost an SM, in sixteenths of a microsecond
   const int32_t *cu_groups, *prefix_lens;
-  int32_t groups, unit_rows, prefix_tile, own_tile, sms, place_cost, tile_cost;
+  int32_t groups, unit_rows, prefix_tile, own_tile, start_places, pair_places;
+  int32_t sms, place_cost, tile_cost;
 };
 
 // Blocks of the bf16 kernels that an SM holds at once, by their registers and
@@ -111,27 +113,23 @@ __device__ __forceinline__ int attn_tiles(const AttnArgs& a, int b, int tile) {
 
 // ---- prefixes on their line, and the SMs of the two kernels of attn_decode_shared ----
 
-// Places of a unit (attn_shared.cu) on the line: kAhead before its first tile (a
-// segment's start -- Q, the first copies -- takes a block as long as so many), then two
-// a tile where two row tiles take it, else one. A block takes the tiles whose first
+// Places of a unit (attn_shared.cu) on the line: start_places before its first tile (a
+// segment's start -- Q, the first copies -- takes a block as long), then pair_places (1
+// or 2) a tile where two row tiles take it, else one. A block takes the tiles whose first
 // place is in its run, and no run is shorter than two.
-constexpr int kAhead = 5;
-
 struct AttnGroup {
   int first, prefix, tiles;
   int64_t rows, units;        // rows of a kv head; units 0 without a prefix or requests
   int64_t full;               // units of two whole row tiles, which come first
-  int per, wide;              // places of one of the others, and of a tile of it
+  int per_full, per, wide;    // places of one of these, of another, and of a tile of that
+  int start, pair;
 
-  __device__ __forceinline__ int per_full() const { return 2 * tiles + kAhead; }
-  __device__ __forceinline__ int64_t places() const {
-    return full * per_full() + (units - full) * per;
-  }
+  __device__ __forceinline__ int64_t places() const { return full * per_full + (units - full) * per; }
   // the place of a unit's tile 0, and those of a tile
   __device__ __forceinline__ int64_t place_of(int64_t unit) const {
-    return kAhead + (unit < full ? unit * per_full() : full * per_full() + (unit - full) * per);
+    return start + (unit < full ? unit * per_full : full * per_full + (unit - full) * per);
   }
-  __device__ __forceinline__ int tile_places(int64_t unit) const { return unit < full ? 2 : wide; }
+  __device__ __forceinline__ int tile_places(int64_t unit) const { return unit < full ? pair : wide; }
 };
 __device__ __forceinline__ AttnGroup attn_group_of(const AttnArgs& a, int g) {
   AttnGroup r;
@@ -144,18 +142,26 @@ __device__ __forceinline__ AttnGroup attn_group_of(const AttnArgs& a, int g) {
   const int64_t blocks = (r.rows + a.unit_rows - 1) / a.unit_rows;     // of rows
   r.units = r.tiles > 0 ? blocks * a.Hkv : 0;
   r.full = two && r.units > 0 ? r.units - a.Hkv : 0;
-  r.wide = two && r.rows - (blocks - 1) * a.unit_rows > 128 ? 2 : 1;
-  r.per = r.wide * r.tiles + kAhead;
+  r.start = a.start_places;
+  r.pair = a.pair_places;
+  r.wide = two && r.rows - (blocks - 1) * a.unit_rows > 128 ? r.pair : 1;
+  r.per = r.wide * r.tiles + r.start;
+  r.per_full = r.pair * r.tiles + r.start;
   return r;
 }
 
 // The SMs that take the prefixes, the others taking the rest meanwhile: as the work of
-// both is, by what an SM needs for it. Every block of both kernels comes to the same
-// number. (One after the other on all SMs: 256 requests 153 us, groups in 8 bits 110.)
-__device__ __forceinline__ int attn_prefix_sms(const AttnArgs& a, int64_t places, int64_t tiles) {
+// both is, by what an SM needs for it. `places` of the prefixes, `positions` of all
+// requests that lie behind them (or so: a request that does not see its prefix whole
+// counts as if it did); every block of both kernels comes to the same number. (One
+// after the other on all SMs: 256 requests 153 us against 148, groups in 8 bits 110
+// against 87.)
+__device__ __forceinline__ int attn_prefix_sms(const AttnArgs& a, int64_t places,
+                                               int64_t positions) {
   if (places == 0) return 0;
+  const int64_t tiles = (max(positions, (int64_t)0) / a.own_tile + a.B / 2) * a.units;
   const int64_t pc = places * a.place_cost, tc = tiles * a.tile_cost;
-  const int64_t own = (a.sms * tc + pc + tc - 1) / (pc + tc);
+  const int64_t own = (a.sms * tc + pc + tc - 1) / max(pc + tc, (int64_t)1);
   return a.sms - (int)min(max(own, (int64_t)2), (int64_t)a.sms * 5 / 8);
 }
 
@@ -177,6 +183,22 @@ __device__ __forceinline__ bool attn_split(const AttnArgs& a, int tile, int64_t 
   const int per = (a.B + THREADS - 1) / THREADS;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   int64_t mine = 0;
+  constexpr int kW = THREADS / 32;
+  if constexpr (SHARED) {           // before the requests' own: their loads run together
+    int64_t places = 0, positions = 0;
+    for (int b = tid; b < a.B; b += THREADS) positions += max(attn_len(a, b), 0);
+    for (int g = tid; g < a.groups; g += THREADS) {
+      const AttnGroup s = attn_group_of(a, g);
+      places += s.places();
+      positions -= s.rows / (a.G * a.q_len) * s.prefix;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      places += __shfl_xor_sync(0xffffffffu, places, d);
+      positions += __shfl_xor_sync(0xffffffffu, positions, d);
+    }
+    if ((tid & 31) == 0) sm[kW + (tid >> 5)] = places, sm[2 * kW + (tid >> 5)] = positions;
+  }
   for (int b = b0; b < b1; ++b) mine += attn_tiles<SHARED>(a, b, tile);
   int64_t incl = mine;
 #pragma unroll
@@ -188,7 +210,7 @@ __device__ __forceinline__ bool attn_split(const AttnArgs& a, int tile, int64_t 
   __syncthreads();
   int64_t base = 0, sum = 0;
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
+  for (int w = 0; w < kW; ++w) {
     if (w < (tid >> 5)) base += sm[w];
     sum += sm[w];
   }
@@ -197,16 +219,10 @@ __device__ __forceinline__ bool attn_split(const AttnArgs& a, int tile, int64_t 
   r.total = sum * units;
   int64_t blocks = gridDim.x;
   if constexpr (SHARED) {
-    int64_t places = 0;
-    for (int g = tid; g < a.groups; g += THREADS) places += attn_group_of(a, g).places();
+    int64_t places = 0, positions = 0;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) places += __shfl_xor_sync(0xffffffffu, places, d);
-    if ((tid & 31) == 0) sm[THREADS / 32 + (tid >> 5)] = places;
-    __syncthreads();
-    places = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) places += sm[THREADS / 32 + w];
-    blocks = blocks / a.sms * (a.sms - attn_prefix_sms(a, places, r.total));
+    for (int w = 0; w < kW; ++w) places += sm[kW + w], positions += sm[2 * kW + w];
+    blocks = blocks / a.sms * (a.sms - attn_prefix_sms(a, places, positions));
   }
   // no run is empty: where there are fewer tiles than blocks, the blocks past
   // the tiles' number have none

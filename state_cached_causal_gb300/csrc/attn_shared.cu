@@ -124,17 +124,17 @@ __device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) 
   const AttnArgs& a = x.a;
   const int tid = threadIdx.x, per = (a.groups + kThreads - 1) / kThreads;
   const int g0 = min(a.groups, tid * per), g1 = min(a.groups, g0 + per);
-  int64_t lines = 0, units = 0;
+  int64_t lines = 0, units = 0, own = 0;      // own: positions behind the prefixes
+  for (int b = tid; b < a.B; b += kThreads) own += max(attn_len(a, b), 0);
   for (int g = g0; g < g1; ++g) {
     const AttnGroup s = attn_group_of(a, g);
     lines += s.places();
     units += s.units;
+    own -= s.rows / (a.G * a.q_len) * s.prefix;
     if (blockIdx.x == 0 &&
         !attn_group_ok(a, a.cu_groups[g], a.cu_groups[g + 1], a.prefix_lens[g]))
       flag_error(a.dev_err, CCONV_DERR_GROUP);
   }
-  int64_t own = 0;            // tiles of the requests' own positions
-  for (int b = tid; b < a.B; b += kThreads) own += attn_tiles<true>(a, b, a.own_tile);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) own += __shfl_xor_sync(0xffffffffu, own, d);
   int64_t li = lines, ui = units;
@@ -158,7 +158,7 @@ __device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) 
   // (groups that overlap may have more rows than the call: none is taken then)
   const bool fits = us <= x.max_units;
   r.total = fits ? ls : 0;
-  r.grid = runs_of(attn_prefix_sms(a, ls, own * a.units), r.total);
+  r.grid = runs_of(attn_prefix_sms(a, ls, own), r.total);
   if (blockIdx.x == 0) {
     if (!fits && tid == 0) flag_error(a.dev_err, CCONV_DERR_GROUP);
     if (tid == 0) x.rec[a.groups] = Rec{r.total, (int32_t)r.grid, 0};
@@ -205,17 +205,17 @@ __device__ __forceinline__ bool segment(const PrefixArgs& x, Run& r, Seg& s) {
       g = attn_group_of(x.a, ++r.g);
     }
     int64_t rel = r.p - r.line;
-    const bool whole = rel < g.full * g.per_full();
-    if (!whole) rel -= g.full * g.per_full();
-    const int per = whole ? g.per_full() : g.per, wide = whole ? 2 : g.wide;
+    const bool whole = rel < g.full * g.per_full;
+    if (!whole) rel -= g.full * g.per_full;
+    const int per = whole ? g.per_full : g.per, wide = whole ? g.pair : g.wide;
     // (a 64-bit division takes a hundred instructions)
     int u = rel <= INT32_MAX ? (int)((uint32_t)rel / (uint32_t)per) : (int)(rel / per);
     const int off = (int)(rel - (int64_t)u * per);
     const int take = (int)min((int64_t)(per - off), r.end - r.p);
     r.p += take;
     // (wide is 1 or 2)
-    s.j0 = max(off - kAhead + wide - 1, 0) >> (wide - 1);
-    s.j1 = max(off + take - kAhead + wide - 1, 0) >> (wide - 1);
+    s.j0 = max(off - g.start + wide - 1, 0) >> (wide - 1);
+    s.j1 = max(off + take - g.start + wide - 1, 0) >> (wide - 1);
     if (s.j1 <= s.j0) continue;
     if (!whole) u += (int)g.full;
     const int mt = u / x.a.Hkv;
@@ -1062,10 +1062,13 @@ int decode_shared(AttnArgs& a, int D, bool q8, const void* q, int64_t q_row_stri
   a.prefix_tile = D == 256 ? 64 : 128;
   a.own_tile = (q8 ? 128 : 64) / a.hw;
   a.sms = sms;
-  // measured for heads of 128: a place 1.15 us; a tile of a block, of which an SM has two,
-  // 1 us (8 bits and 16 rows 1.75 us)
-  a.place_cost = D == 256 ? 32 : D == 128 ? 18 : 12;
-  a.tile_cost = (q8 && a.rows > 8 ? 14 : 8) * D / 128 + 1;
+  // Measured for heads of 128: a tile of two row tiles 2.5 us, of one 1.6; from 8 bits,
+  // whose conversion bounds it, 2.8 either way; a start 8 to 10 us. A tile of the rest
+  // takes an SM 0.9 us, about as many as its share of the memory's bandwidth allows.
+  a.start_places = q8 ? 3 : 8;
+  a.pair_places = q8 ? 1 : 2;
+  a.place_cost = (q8 ? 44 : 22) * (D == 64 ? 5 : 8) / 8;
+  a.tile_cost = (q8 && a.rows == 8 ? 13 : 15) * D / 128;
   PrefixArgs x;
   x.a = a;
   x.rec = reinterpret_cast<Rec*>(ws + p.rec);

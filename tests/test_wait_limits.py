@@ -60,18 +60,15 @@ def test_the_shared_kernel():
     assert soft.count("empty_part<D>(x, s, stream);") == 2 and soft.count("x.ps[row0 + lane] =") == 1
 
 
-K = int(re.search(r"constexpr int kAhead = (\d+);", source("attn_decode.cuh")).group(1))
-
-
-def split(groups, hkv, streams, grid):
+def split(groups, hkv, streams, grid, K, pair):
     """(rows of a kv head, tiles) of each group -> the tiles that each block takes, and their parts' places."""
     R, unit, base, info = 128 * streams, 0, 0, []
     for rows, tiles in groups:
         blocks = -(-rows // R)
         units = blocks * hkv if tiles > 0 else 0
         full = units - hkv if streams == 2 and units > 0 else 0
-        wide = 2 if streams == 2 and rows - (blocks - 1) * R > 128 else 1
-        per, per_full = wide * tiles + K, 2 * tiles + K
+        wide = pair if streams == 2 and rows - (blocks - 1) * R > 128 else 1
+        per, per_full = wide * tiles + K, pair * tiles + K
         info.append((base, unit, units, full, wide, per, per_full, tiles))
         base += full * per_full + (units - full) * per
         unit += units
@@ -86,7 +83,7 @@ def split(groups, hkv, streams, grid):
             rel = p - b
             whole = rel < full * per_full
             rel -= 0 if whole else full * per_full
-            one, w = (per_full, 2) if whole else (per, wide)
+            one, w = (per_full, pair) if whole else (per, wide)
             u, off = rel // one, rel % one
             take = min(one - off, end - p)
             p += take
@@ -105,14 +102,14 @@ def split(groups, hkv, streams, grid):
     return taken, info
 
 
-@pytest.mark.parametrize("streams", [1, 2])
-def test_every_tile_of_a_prefix_is_taken_once(streams):
+@pytest.mark.parametrize("streams,start,pair", [(1, 8, 2), (2, 8, 2), (2, 3, 1)])
+def test_every_tile_of_a_prefix_is_taken_once(streams, start, pair):
     """And the parts of a unit are those of neighbouring blocks, each of which has tiles of it."""
-    r = random.Random(streams)
+    r = random.Random(streams + start)
     for _ in range(1500):
         groups = [(r.choice([0, 1, 4, 100, 128, 129, 256, 257, 600, 1000]), r.choice([0, 0, 1, 2, 3, 8, 30, 200]))
                   for _ in range(r.randint(1, 9))]
-        taken, info = split(groups, r.choice([1, 2, 4]), streams, r.choice([3, 10, 152]))
+        taken, info = split(groups, r.choice([1, 2, 4]), streams, r.choice([3, 10, 152]), start, pair)
         assert len(taken) == sum(i[2] * i[7] for i in info)
         for g, i in enumerate(info):
             for u in range(i[2]):
