@@ -417,10 +417,11 @@ inline void attn_fill(AttnArgs& a, const AttnPlan& p, int D, int bytes, const vo
   a.dev_err = dev_err;
 }
 
-// Launches a kernel of the shared form beside the end of the one before it.
+// Launches a kernel of the shared form, beside the call's kernel before it if there is one
+// (any other that lets its successor start early may still be writing what this reads).
 template <typename K, typename A>
-cudaError_t attn_launch_beside(K kernel, const A& a, int more, int grid, int threads, int smem,
-                               cudaStream_t st) {
+cudaError_t attn_launch_beside(bool beside, K kernel, const A& a, int more, int grid, int threads,
+                               int smem, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3((unsigned)threads);
@@ -430,7 +431,7 @@ cudaError_t attn_launch_beside(K kernel, const A& a, int more, int grid, int thr
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = beside ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, a, more);
 }
 

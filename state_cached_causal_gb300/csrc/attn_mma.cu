@@ -534,7 +534,8 @@ cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
     attn_mma_kernel<D, MT, SHARED><<<grid, kThreads, smem, st>>>(a, stages);
     return cudaGetLastError();
   } else {
-    return attn_launch_beside(attn_mma_kernel<D, MT, SHARED>, a, stages, grid, kThreads, smem, st);
+    return attn_launch_beside(a.groups > 0, attn_mma_kernel<D, MT, SHARED>, a, stages, grid,
+                              kThreads, smem, st);
   }
 }
 

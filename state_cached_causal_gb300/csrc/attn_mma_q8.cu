@@ -7,7 +7,7 @@
 // - The products are the transposed ones, S^T = K Q^T and O^T = V^T P^T, whose narrow
 //   side of 8 is the query rows': with 16 rows on the other side, half of the softmax
 //   and of the sums was of rows that do not exist where a kv head has 4 or 8. The weights
-//   are turned in registers (movmatrix). 256 requests 216 -> WW us.
+//   are turned in registers (movmatrix).
 // - Values go to the products as fp16, which holds every e4m3 value, by one
 //   instruction a pair. (bf16 would hold them too; that conversion takes four.) The
 //   four bytes that ldmatrix leaves in a lane are two pairs of K's dims, so that Q is
@@ -26,6 +26,13 @@
 //   two tiles before they are needed, and puts them beside the tile. (With the copies
 //   in one warp that warp's instructions were what bounded the kernel.)
 // - A tile is 128 rows, 32 a warp, so that it has as many bytes.
+//
+// 256 requests of up to 8192 positions, 16 query heads on 4 kv heads of 128 (1.07 GB):
+// 198 us, 5.4 TB/s. It is bound by the bytes, nearly: the copies alone, without the
+// products, take 173 (in bf16 the cache takes 340). With rows as the products' side of
+// 16 and one warp for copies and scales 270; with the scales in their own warp 216.
+// 64 requests of 4 tokens (16 rows a kv head, 127 MB): 53 us, where conversion, softmax
+// and turning the weights are what the warps' issue slots go to.
 #include "attn_decode.cuh"
 #include "q8.cuh"
 #include "tc.cuh"
@@ -740,8 +747,8 @@ cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
     attn_mma_q8_kernel<D, NT, SHARED><<<grid, kThreads, smem, st>>>(a, stages);
     return cudaGetLastError();
   } else {
-    return attn_launch_beside(attn_mma_q8_kernel<D, NT, SHARED>, a, stages, grid, kThreads, smem,
-                              st);
+    return attn_launch_beside(a.groups > 0, attn_mma_q8_kernel<D, NT, SHARED>, a, stages, grid,
+                              kThreads, smem, st);
   }
 }
 

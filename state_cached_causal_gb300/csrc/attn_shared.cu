@@ -3,8 +3,9 @@
 //
 // Three launches. attn_prefix_kernel multiplies a group's prefix once, for the rows of
 // all its requests; the kernels of attn_decode take each request's positions behind
-// it (from attn_start on); attn_shared_join_kernel joins both. The second starts beside
-// the end of the first, whose results it does not need.
+// it (from attn_start on); attn_shared_join_kernel joins both. The second runs beside the
+// first, whose results it does not need: the SMs are divided between the two by their
+// work (attn_prefix_sms).
 //
 // attn_prefix_kernel. The rows of a group and kv head (requests x new tokens x query
 // heads of the kv head) are cut into units of 256 (128 for heads of 256), a unit's
@@ -27,7 +28,14 @@
 // of 256 leave tensor memory for one stream.)
 //
 // With many rows it is bound by the products (scores, and twice the weights'), with few
-// by the bytes of K and V.
+// by the bytes of K and V, from 8 bits by their conversion to bf16 in the copying warps.
+// 16 query heads on 4 kv heads of 128: 256 requests behind 32768 positions, with up to
+// 1024 of their own (338 MB, 70 GFLOP and a half more for the weights' second terms)
+// 146 us; a tile for two row tiles takes a block 2.5 us, 10 TFLOP/s, 0.9 of what cuBLAS
+// keeps up an SM. 8 requests behind 131072 positions 74 us for 270 MB, of which 10 to 13
+// are before the first products (code, page table, copies) and 9 the join; seven groups of
+// 96 requests with 4 tokens, from 8 bits, 86 us. Attended one by one (attn_decode) the
+// first would read 17.5 GB.
 #include "attn_decode.cuh"
 #include "q8.cuh"
 #include "tc.cuh"
@@ -1022,9 +1030,9 @@ template <int D>
 cudaError_t launch_shared_join(const PrefixArgs& x, cudaStream_t st) {
   const int n = x.a.B * x.a.Hq * x.a.q_len;
   // a warp a row where that fills the GPU, else a block's eight
-  return n >= 8192   ? attn_launch_beside(attn_shared_join_kernel<D, 1>, x, n, (n + 7) / 8, 256, 0, st)
-         : n >= 2048 ? attn_launch_beside(attn_shared_join_kernel<D, 1>, x, n, (n + 7) / 8, 256, 0, st)
-                     : attn_launch_beside(attn_shared_join_kernel<D, 8>, x, n, n, 256, 0, st);
+  return n >= 2048
+             ? attn_launch_beside(true, attn_shared_join_kernel<D, 1>, x, n, (n + 7) / 8, 256, 0, st)
+             : attn_launch_beside(true, attn_shared_join_kernel<D, 8>, x, n, n, 256, 0, st);
 }
 
 // What both entry points check and do; a's cache is set.

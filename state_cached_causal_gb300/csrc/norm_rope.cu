@@ -21,7 +21,9 @@
 // latency of a few dependent loads.
 //
 // Into a cache in 8 bits a row's largest magnitude is reduced over the head's lanes
-// as its sum of squares is, and a unit of 16 bytes becomes one of 8 (4 from fp32).
+// as its sum of squares is, and a unit of 16 bytes becomes one of 8 (4 from fp32). The
+// same tokens: 80.7 us for 389 MB, 4.8 TB/s; the second reduction, the conversions and
+// the narrower stores cost the instructions what the bytes save.
 #include "q8.cuh"
 
 namespace cconv {
