@@ -1,16 +1,19 @@
 // Entry point kv_cache_read_q8: rows of a cache in 8 bits as fp32 or bf16.
 //
 // A thread turns 8 bytes (4 for fp32) of a row into the 16 it stores, so that both
-// sides of a warp are whole lines, and has four such units requested before the first
-// is stored: slots, then bytes and scales, depend on one another. 65536 rows of 4 heads
-// of 128 to bf16 (202 MB): 47 us, 4.3 TB/s, of which two thirds are
-// stores (with one unit a thread 56 us).
+// sides of a warp are whole lines. It takes the same unit of one token after the other,
+// so that where that lies in a token is computed once, and has four tokens' bytes and
+// scales requested before the first is stored, and their successors' slots. 65536 rows
+// of 4 heads of 128 to bf16 (202 MB): 41 us, 4.9 TB/s, two thirds of it stores (units
+// dealt out in their order, with two divisions each: 47 us and 81 % of the issue slots;
+// slots not read ahead: 50 us; two or eight tokens, twice the bytes a thread: 40 to 41).
 #include "q8.cuh"
 
 namespace cconv {
 namespace {
 
 constexpr int kReadThreads = 256;
+constexpr int kBlocks = 20;       // an SM (five: 45 us; 64: 45)
 constexpr int kUnits = 4;         // of a thread, requested together
 
 struct ReadArgs {
@@ -28,79 +31,88 @@ struct ReadArgs {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a, const int cols,
+                                                               const uint32_t wide) {
   constexpr int V = Elem<T>::V, E = Elem<T>::bytes, UPR = D / V;    // units a row
-  const uint32_t per = 2 * a.Hkv * UPR;                             // units of a token
-  // a block's tokens at a time: units of 16 bytes for kUnits a thread, or one token
-  const int tokens = max(1u, kReadThreads * kUnits / per);
+  const int per = 2 * a.Hkv * UPR;                                  // units of a token
+  // the thread's unit of every token that it takes: K or V, head and place in that
+  const int rows = blockDim.x / cols, row = threadIdx.x / cols;
+  const uint32_t chunk = blockIdx.x / wide, block = blockIdx.x - chunk * wide;
+  const int j = chunk * cols + threadIdx.x - row * cols;
+  if (j >= per) return;
+  const bool isv = j >= per / 2;
+  const int r = isv ? j - per / 2 : j, h = r / UPR, u = r % UPR;
+  const char* const src0 = (isv ? a.vc : a.kc) + h * a.s_head + u * V;
+  const uint8_t* const scale0 = (isv ? a.vsc : a.ksc) + h * a.c_head;
+  const int64_t rs = (isv ? a.vo_rs : a.ko_rs) * E;
+  char* const dst0 = (isv ? a.vo : a.ko) + (int64_t)r * 16;
+  const int64_t step = (int64_t)rows * kUnits;                      // tokens of a block at a time
+  int32_t next[kUnits];             // slots, read a step ahead
+  auto look = [&](int64_t t0) {
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) next[k] = t0 + k * rows < a.T ? a.slots[t0 + k * rows] : -1;
+  };
+  int64_t t0 = block * step + row;
+  look(t0);
 #pragma unroll 1
-  for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < a.T; t0 += (int64_t)gridDim.x * tokens) {
-    const uint32_t n = (uint32_t)min((int64_t)tokens, a.T - t0) * per;
-#pragma unroll 1
-    for (uint32_t j0 = threadIdx.x; j0 < n; j0 += kReadThreads * kUnits) {
-      // slots, then values and scales, of all units before the first is stored
-      int slot[kUnits];
-      uint32_t raw[kUnits][V / 4], byte[kUnits];
-      char* dst[kUnits];
+  for (; t0 < a.T; t0 += wide * step) {
+    // values and scales of all units before the first is stored
+    int slot[kUnits];
+    uint32_t raw[kUnits][V / 4], byte[kUnits];
 #pragma unroll
-      for (int k = 0; k < kUnits; ++k) {
-        const uint32_t j = j0 + k * kReadThreads;
-        slot[k] = j < n ? a.slots[t0 + j / per] : -1;
+    for (int k = 0; k < kUnits; ++k) slot[k] = next[k];
+    look(t0 + wide * step);
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      if (slot[k] >= a.num_slots) {
+        flag_error(a.dev_err, CCONV_DERR_POSITION);
+        slot[k] = -1;
       }
-#pragma unroll
-      for (int k = 0; k < kUnits; ++k) {
-        const uint32_t j = j0 + k * kReadThreads, t = j / per;
-        uint32_t r = j - t * per;
-        const bool isv = r >= per / 2;
-        if (isv) r -= per / 2;
-        const int h = r / UPR, u = r % UPR;
-        if (slot[k] >= a.num_slots) {
-          flag_error(a.dev_err, CCONV_DERR_POSITION);
-          slot[k] = -1;
-        }
-        if (slot[k] < 0) continue;
-        const int page = a.page_shift >= 0 ? slot[k] >> a.page_shift : slot[k] / a.page_size;
-        const int tok = slot[k] - page * a.page_size;
-        const char* const src = (isv ? a.vc : a.kc) + page * a.s_page + tok * a.s_tok +
-                                h * a.s_head + u * V;
-        if constexpr (V == 8) {
-          const uint2 w = __ldcs(reinterpret_cast<const uint2*>(src));
-          raw[k][0] = w.x, raw[k][V / 4 - 1] = w.y;
-        } else {
-          raw[k][0] = __ldcs(reinterpret_cast<const uint32_t*>(src));
-        }
-        byte[k] = (isv ? a.vsc : a.ksc)[page * a.c_page + tok * a.c_tok + h * a.c_head];
-        dst[k] = (isv ? a.vo + (t0 + t) * a.vo_rs * E : a.ko + (t0 + t) * a.ko_rs * E) +
-                 (int64_t)r * 16;
+      if (slot[k] < 0) continue;
+      const int page = a.page_shift >= 0 ? slot[k] >> a.page_shift : slot[k] / a.page_size;
+      const int tok = slot[k] - page * a.page_size;
+      const char* const src = src0 + page * a.s_page + tok * a.s_tok;
+      if constexpr (V == 8) {
+        const uint2 w = __ldcs(reinterpret_cast<const uint2*>(src));
+        raw[k][0] = w.x, raw[k][V / 4 - 1] = w.y;
+      } else {
+        raw[k][0] = __ldcs(reinterpret_cast<const uint32_t*>(src));
       }
+      byte[k] = scale0[page * a.c_page + tok * a.c_tok];
+    }
 #pragma unroll
-      for (int k = 0; k < kUnits; ++k) {
-        if (slot[k] < 0) continue;
-        const float f = q8_scale(byte[k]);
-        float x[V];
+    for (int k = 0; k < kUnits; ++k) {
+      if (slot[k] < 0) continue;
+      const float f = q8_scale(byte[k]);
+      float x[V];
 #pragma unroll
-        for (int e = 0; e < V; e += 4) {
-          float y[4];
-          unpack_e4m3x4(raw[k][e / 4], y);
+      for (int e = 0; e < V; e += 4) {
+        float y[4];
+        unpack_e4m3x4(raw[k][e / 4], y);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[e + i] = y[i] * f;
-        }
-        stg16(dst[k], pack16<T>(x));
+        for (int i = 0; i < 4; ++i) x[e + i] = y[i] * f;
       }
+      stg16(dst0 + (t0 + k * rows) * rs, pack16<T>(x));
     }
   }
 }
 
 template <typename T>
 cudaError_t launch_read(const ReadArgs& a, int D, int sms, cudaStream_t st) {
-  const int64_t n = (int64_t)a.T * 2 * a.Hkv * (D / Elem<T>::V), per = kReadThreads * kUnits;
-  const unsigned grid = (unsigned)std::min<int64_t>((n + per - 1) / per, (int64_t)sms * 64);
+  const int per = 2 * a.Hkv * (D / Elem<T>::V);       // at most 2^28 (the caller checks)
+  // a block takes all units of some tokens, or of one token as many as it has threads
+  const int cols = std::min(per, kReadThreads), rows = kReadThreads / cols;
+  const int chunks = (per + cols - 1) / cols;
+  const int64_t most = ((int64_t)a.T + rows * kUnits - 1) / (rows * kUnits);
+  const unsigned wide = (unsigned)std::min<int64_t>(most, std::max(sms * kBlocks / chunks, 1));
+  const unsigned grid = wide * chunks;
+  const int threads = cols * rows;
   if (D == 64)
-    kv_read_kernel<T, 64><<<grid, kReadThreads, 0, st>>>(a);
+    kv_read_kernel<T, 64><<<grid, threads, 0, st>>>(a, cols, wide);
   else if (D == 128)
-    kv_read_kernel<T, 128><<<grid, kReadThreads, 0, st>>>(a);
+    kv_read_kernel<T, 128><<<grid, threads, 0, st>>>(a, cols, wide);
   else
-    kv_read_kernel<T, 256><<<grid, kReadThreads, 0, st>>>(a);
+    kv_read_kernel<T, 256><<<grid, threads, 0, st>>>(a, cols, wide);
   return cudaGetLastError();
 }
 

@@ -158,6 +158,22 @@ def test_rows_come_back(dtype, hkv, D, T):
     assert (wide[:, :, hkv * D:] == 7).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("hkv,D,page,T", [(20, 256, 16, 41), (9, 128, 24, 200), (33, 64, 16, 7), (17, 64, 5, 130),
+                                          (1, 64, 16, 200001), (4, 128, 16, 70001)])
+def test_many_heads_and_many_rows_come_back(dtype, hkv, D, page, T):
+    """More units of a token than a block has threads, and more rows than a launch's blocks take at a time."""
+    g = synth.generator(T, DEV)
+    pages = 33
+    kc, vc, ks, vs = cache_pair(g, (pages, page, hkv, D), heads_first=False, spread=20)
+    slots = torch.randint(0, pages * page, (T,), generator=g, device=DEV, dtype=torch.int32)
+    ko, vo = (torch.full((T, hkv, D), 7.0, device=DEV, dtype=dtype) for _ in range(2))
+    ops.kv_cache_read_q8(kc, vc, ks, vs, slots, ko, vo)
+    for got, c, s in ((ko, kc, ks), (vo, vc, vs)):
+        rows = values(c.cpu(), s.cpu()).to(dtype).to(DEV).flatten(0, 1)          # powers of two: exact in bf16 too
+        assert torch.equal(got, rows[slots.long()])
+
+
 def test_what_is_written_comes_back():
     c = case(11, 50, 4, 2, 128, 64, BF16)
     kc, vc, ks, vs = cache_pair(synth.generator(8, DEV), tuple(c["kc"].shape))
