@@ -13,24 +13,26 @@
 // there are few tokens a token's heads are spread over several warps.
 //
 // Four groups of query heads have their loads in flight together, beside the
-// first group of keys and values, and four blocks an SM take the tokens one after
-// the other, the next token's position and slot read ahead. 33024 tokens of
-// 16 + 4 + 4 heads of 128 in bf16: 75.9 us for 422 MB, 5.6 TB/s (keys after the
-// queries, values after the keys: 78.7 us; three blocks, whose 168 registers
-// spill nothing: 78.1 us; one unit a lane: 98.7 us). 61 tokens: 3.0 us, the
-// latency of a few dependent loads.
+// first group of keys and values, and three blocks an SM take the tokens one after
+// the other, the next token's position and slot read ahead and its queries asked
+// into the L2. 33024 tokens of 16 + 4 + 4 heads of 128 in bf16: 73.0 us for 422 MB,
+// 5.8 TB/s (without that prefetch 78.0 us, and 75.9 with four blocks, whose 128
+// registers spill a little; four with it 77.7; keys and values prefetched, too, no
+// better; keys after the queries, values after the keys: 78.7 us; one unit a lane:
+// 98.7 us). 61 tokens: 3.0 us, the latency of a few dependent loads.
 //
 // Into a cache in 8 bits a row's largest magnitude is reduced over the head's lanes
 // as its sum of squares is, and a unit of 16 bytes becomes one of 8 (4 from fp32). The
-// same tokens: 80.7 us for 389 MB, 4.8 TB/s; the second reduction, the conversions and
-// the narrower stores cost the instructions what the bytes save.
+// same tokens: 75.1 us for 389 MB, 5.2 TB/s (four blocks without the prefetch 80.5; the
+// 8 bytes in one store instead of two: the same): the second reduction, the
+// conversions and the narrower stores cost the instructions what the bytes save.
 #include "q8.cuh"
 
 namespace cconv {
 namespace {
 
 constexpr int kNrThreads = 128;
-constexpr int kNrBlocks = 4;    // of an SM
+constexpr int kNrBlocks = 3;    // of an SM
 constexpr int kUnroll = 4;      // groups of heads whose loads are in flight together
 
 struct NrArgs {
@@ -88,6 +90,9 @@ __global__ void __launch_bounds__(kNrThreads, kNrBlocks) norm_rope_kernel(const 
     if (t < a.T) {                // the next token's, while this one is worked on
       pos = a.pos[t];
       slot = a.slots[t];
+      if (a.parts == 1)           // its queries to the L2, whose latency it then waits for
+        for (int at = lane * 128; at < a.Hq * (D * E); at += 32 * 128)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + t * a.q_rs * E + at));
     }
     if (p < 0 || p >= a.max_pos || sl >= a.num_slots) {
       if (part == 0 && lane == 0) flag_error(a.dev_err, CCONV_DERR_POSITION);
