@@ -153,16 +153,18 @@ __device__ __forceinline__ AttnGroup attn_group_of(const AttnArgs& a, int g) {
 // The SMs that take the prefixes, the others taking the rest meanwhile: as the work of
 // both is, by what an SM needs for it. `places` of the prefixes, `positions` of all
 // requests that lie behind them (or so: a request that does not see its prefix whole
-// counts as if it did); every block of both kernels comes to the same number. (One
-// after the other on all SMs: 256 requests 153 us against 148, groups in 8 bits 110
-// against 87.)
+// counts as if it did); every block of both kernels comes to the same number. (One after
+// the other on all SMs: 256 requests behind a long document 153 us against 146, groups in
+// 8 bits 103 to 110 against 86, 64 requests whose own 8192 positions are most of the work
+// 126 against 116, 96 behind 1024 positions 67 against 57. With at most 5/8 of the SMs
+// for the rest those 64 took 157.)
 __device__ __forceinline__ int attn_prefix_sms(const AttnArgs& a, int64_t places,
                                                int64_t positions) {
   if (places == 0) return 0;
   const int64_t tiles = (max(positions, (int64_t)0) / a.own_tile + a.B / 2) * a.units;
   const int64_t pc = places * a.place_cost, tc = tiles * a.tile_cost;
   const int64_t own = (a.sms * tc + pc + tc - 1) / max(pc + tc, (int64_t)1);
-  return a.sms - (int)min(max(own, (int64_t)2), (int64_t)a.sms * 5 / 8);
+  return a.sms - (int)min(max(own, (int64_t)2), (int64_t)a.sms * 15 / 16);
 }
 
 // The block's run [p, end) of the line and the request that p lies in.

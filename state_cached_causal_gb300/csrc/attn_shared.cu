@@ -34,7 +34,7 @@
 // 146 us; a tile for two row tiles takes a block 2.5 us, 10 TFLOP/s, 0.9 of what cuBLAS
 // keeps up an SM. 8 requests behind 131072 positions 74 us for 270 MB, of which 10 to 13
 // are before the first products (code, page table, copies) and 9 the join; seven groups of
-// 96 requests with 4 tokens, from 8 bits, 86 us. Attended one by one (attn_decode) the
+// 96 requests with 4 tokens, from 8 bits, 87 us. Attended one by one (attn_decode) the
 // first would read 17.5 GB.
 #include "attn_decode.cuh"
 #include "q8.cuh"
