@@ -7,6 +7,7 @@ import ctypes
 import pytest
 import torch
 
+from state_cached_causal_gb300 import ops
 from tests import test_attn_shared as shared
 
 pytestmark = pytest.mark.gpu
@@ -56,3 +57,28 @@ def test_only_the_calls_own_kernels_run_beside_one_another(q8, groups):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_calls_at_once_on_two_streams():
+    """Each with a workspace of its own; results are those of a call alone."""
+    cases = [shared.Case(32, [(3000, [3001 + 5 * i for i in range(70)])], 16, 4, 128, 16, 1, False),
+             shared.Case(33, [(900, [950, 1300]), (2000, [2100] * 9)], 16, 4, 128, 16, 2, True)]
+    outs, want, spaces = [], [], []
+    for c in cases:
+        outs.append(torch.zeros(c.q.shape, device=shared.DEV, dtype=torch.bfloat16))
+        n = ops.attn_decode_shared_workspace_bytes(len(c.lens), len(c.prefix), c.n - 1, 16, 4, 128)
+        spaces.append(torch.empty(n, dtype=torch.uint8, device=shared.DEV))
+        c.call(outs[-1], workspace=spaces[-1])
+        torch.cuda.synchronize()
+        want.append(outs[-1].clone())
+        outs[-1].zero_()
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    err = torch.zeros(1, dtype=torch.int32, device=shared.DEV)
+    for _ in range(20):
+        for c, out, ws, st in zip(cases, outs, spaces, streams):
+            c.call(out, workspace=ws, stream=st, err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    for out, w in zip(outs, want):
+        assert torch.equal(out, w)
