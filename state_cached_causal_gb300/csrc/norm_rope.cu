@@ -19,7 +19,8 @@
 // 5.8 TB/s (without that prefetch 78.0 us, and 75.9 with four blocks, whose 128
 // registers spill a little; four with it 77.7; keys and values prefetched, too, no
 // better; keys after the queries, values after the keys: 78.7 us; one unit a lane:
-// 98.7 us). 61 tokens: 3.0 us, the latency of a few dependent loads.
+// 98.7 us). 61 tokens: 3.0 us, the latency of a few dependent loads. (Four blocks took
+// 2000 to 2400 tokens 8 % faster, in one turn, and other numbers up to 10 % slower.)
 //
 // Into a cache in 8 bits a row's largest magnitude is reduced over the head's lanes
 // as its sum of squares is, and a unit of 16 bytes becomes one of 8 (4 from fp32). The
@@ -336,10 +337,11 @@ int norm_rope(NrArgs& a, int D, bool q8, const void* q, int64_t q_row_stride, co
   a.Hq = num_q_heads;
   a.qo = static_cast<char*>(q_out);
   a.dev_err = dev_err;
-  // several warps a token while there are fewer than 16 warps an SM: 1, 2, 4 or 8,
-  // so that a block's four warps, and the grid's, fall into whole tokens
+  // several warps a token while that leaves all of them at work at once (1000 tokens with
+  // two, more than that: 5.9 us, not 4.7): 1, 2, 4 or 8, so that a block's four warps,
+  // and the grid's, fall into whole tokens
   a.parts = 1;
-  while (a.parts < 8 && (int64_t)num_tokens * a.parts * 2 <= (int64_t)sms * 16) a.parts *= 2;
+  while (a.parts < 8 && (int64_t)num_tokens * a.parts * 2 <= (int64_t)sms * (kNrBlocks * kNrThreads / 32)) a.parts *= 2;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool pairs = interleaved != 0;
   cudaError_t err;
