@@ -1,5 +1,6 @@
 // Paged attention of new tokens: work split, partial results and arguments
-// shared by the kernels of attn_decode (attn_decode.cu, attn_mma.cu).
+// shared by the kernels of attn_decode (attn_decode.cu, attn_mma.cu), of attn_decode_q8
+// (attn_mma_q8.cu) and of the shared form (attn_shared.cu).
 //
 // A unit is a request with a group of `hw` kv heads (and a block of `rows` query
 // rows of each); its cached tokens are cut into tiles of `tile` positions. All
