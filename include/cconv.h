@@ -697,8 +697,11 @@ CCONV_API int kv_cache_read_q8(kv_cache_q8_t cache, const int32_t* slot_mapping,
  * k and v the values that the cache's bytes and scales stand for. Arguments,
  * workspace (attn_decode_workspace_bytes) and errors as attn_decode. The bf16
  * kernel multiplies the bytes as they are, as fp16 (exact), q as fp16 with a power
- * of two a row (exact but for values 2^-38 below the row's largest), and takes the
- * softmax weights, times their row's power of two, as fp16 (11 bits).
+ * of two a row (exact down to 2^-38 of the row's largest value), and takes the
+ * softmax weights, times their row's power of two, as fp16: 11 bits where that
+ * product is 2^-22 of its largest or more, fewer below, none from 2^-33 on. (Its
+ * largest over rows of v as they are when each has the least power of two that its
+ * values allow, rows of zeros aside: any scale byte may stand with any values.)
  */
 CCONV_API int attn_decode_q8(const void* q, int64_t q_row_stride, kv_cache_q8_t cache,
                    const int32_t* block_table, int64_t block_table_row_stride,

@@ -21,7 +21,9 @@
 //   weights times 2^-e. Where some |e| is over 40 that could leave fp32's range: from
 //   there on ("wide") the sum has a maximum of its own. Weights are fp16: 11 bits from
 //   2^-22 of the largest on, 2^-33 of it at least. That is one rounding more than none:
-//   2^-12 of a result, whose own is 2^-9.
+//   2^-12 of a result, whose own is 2^-9. That holds for powers of two that are the
+//   least ones of their rows. Others are allowed, so that a tile which raises the reference
+//   is looked through first, and brought into that form (`fill_row`).
 // - Scales are bytes that lie elsewhere; a warp of their own reads them into registers,
 //   two tiles before they are needed, and puts them beside the tile. (With the copies
 //   in one warp that warp's instructions were what bounded the kernel.)
@@ -104,6 +106,64 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, int phase, int32_t* err)
   }
   __syncwarp();
   return true;
+}
+
+// Whether one of a row's D values has the magnitude that the largest one has where the
+// scale is the least one: 224 and above (and none is NaN).
+template <int D>
+__device__ __noinline__ bool row_full(uint32_t addr) {
+  uint32_t full = 0u, nan = 0u;
+#pragma unroll
+  for (int i = 0; i < D; i += 64) {
+    uint32_t v[16];
+#pragma unroll
+    for (int k = 0; k < 16; k += 4)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v[k]), "=r"(v[k + 1]), "=r"(v[k + 2]), "=r"(v[k + 3])
+                   : "r"(addr + i + k * 4)
+                   : "memory");
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      full |= (v[k] & 0x7f7f7f7fu) + 0x0a0a0a0au;       // (0x76 is 224)
+      nan |= (v[k] & 0x7f7f7f7fu) + 0x01010101u;
+    }
+  }
+  return (full & 0x80808080u) != 0u && (nan & 0x80808080u) == 0u;
+}
+// A row of `bytes` e4m3 values: if none is as large as above, they are multiplied by the
+// power of two 2^x that brings the largest finite one there, and x is returned; kNothing
+// for a row of zeros, 0 for any other.
+constexpr float kNothing = 300.0f;
+__device__ __noinline__ float fill_row(uint32_t addr, int bytes) {
+  uint32_t most = 0u;
+#pragma unroll 1
+  for (int i = 0; i < bytes; i += 4) {
+    const uint32_t v = lds32(addr + i);
+    most = __vmaxu4(most, v & 0x7f7f7f7fu & ~nan_bytes(v));
+  }
+  most = __vmaxu4(most, most >> 16);
+  const uint32_t b = max(most & 0xffu, most >> 8 & 0xffu);
+  if (b >= 0x76u) return 0.0f;
+  if (b == 0u) return kNothing;
+  // 2^(e - 7) (1 + f / 8), below 2^-6 too; 448 is that of e = 15 and f = 6
+  const int j = 31 - __clz(b), e = b < 8u ? j - 2 : (int)(b >> 3);
+  const uint32_t f = (b < 8u ? b << (3 - j) : b) & 7u;
+  const int x = (f < 7u ? 15 : 14) - e;
+  const uint32_t x0 = (uint32_t)(x / 2 + 15) << 10, x1 = (uint32_t)(x - x / 2 + 15) << 10;
+#pragma unroll 1
+  for (int i = 0; i < bytes; i += 4) {
+    uint32_t h[2], r[2];
+    e4m3x4_to_f16(lds32(addr + i), h[0], h[1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      asm("{\n\t.reg .b16 y;\n\t.reg .b32 a, x;\n\tmov.b32 x, {%2, %2};\n\t"
+          "mul.rn.f16x2 a, %1, x;\n\tmov.b32 x, {%3, %3};\n\tmul.rn.f16x2 a, a, x;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f16x2 y, a;\n\tcvt.u32.u16 %0, y;\n\t}"
+          : "=r"(r[k])
+          : "r"(h[k]), "h"((uint16_t)x0), "h"((uint16_t)x1));
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr + i), "r"(r[0] | r[1] << 16) : "memory");
+  }
+  return (float)x;
 }
 
 // What a warp that gives a wait up leaves the kernel by, so that no copy lands
@@ -277,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, attn_mma_blocks(D, NT * 8, true))
         const Bytes c2 = load(j + 2);
         look(j + 3);
         if (!wait_bar(&empty[st], ph, a.dev_err)) return settle(full, stages, st, ph, a.dev_err);
-bool near = true;
+        bool near = true;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float e = (float)c0.v[i] - 127.0f;
@@ -493,16 +553,7 @@ bool near = true;
             }
           }
       }
-      if (__builtin_expect(!wide && !mild[cur], 0)) {
-        wide = true;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            m[nt][k] = mv[nt][k];
-            l[nt][k] *= exp2f(-kLift);
-          }
-      }
+      bool far = !mild[cur];
       // scores with their value's power of two, and whether one passes its reference too far
       bool rises = false;
 #pragma unroll
@@ -518,7 +569,44 @@ bool near = true;
           }
           rises = rises || top > mv[nt][k] + kSlack || (mv[nt][k] == -INFINITY && top > mv[nt][k]);
         }
-      if (__builtin_expect(__any_sync(0xffffffffu, rises), 0)) {
+      rises = __any_sync(0xffffffffu, rises);
+      if (__builtin_expect(rises, 0)) {
+        // The reference stands for the largest products with values, so it follows powers
+        // of two that are the least ones of their rows. A tile that raises it is brought
+        // into that form (lane l has position l; these are this warp's alone): a row of
+        // zeros, or of the smallest bytes, under a large power of two would otherwise
+        // raise it past the weights of all others.
+        const uint32_t mine = vb + off(lane);
+        const bool low = !row_full<D>(mine) && tr[lane];
+        if (__any_sync(0xffffffffu, low)) {
+          const float up = low ? fill_row(mine, D) : 0.0f;
+          fence_proxy_async();        // before a later copy into the same place
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = __shfl_sync(0xffffffffu, up, 8 * i + (lane >> 2));
+            e[i] -= x;
+            far = far || fabsf(e[i]) > kMild;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              s[nt][i >> 1][(i & 1) * 2] -= x;
+              s[nt][i >> 1][(i & 1) * 2 + 1] -= x;
+            }
+          }
+          far = __any_sync(0xffffffffu, far);
+        }
+      }
+      if (__builtin_expect(!wide && far, 0)) {
+        wide = true;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            m[nt][k] = mv[nt][k];
+            l[nt][k] *= exp2f(-kLift);
+          }
+      }
+      if (__builtin_expect(rises, 0)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float corr[2];
@@ -595,7 +683,7 @@ bool near = true;
                 if (v & 0xff00u) o[nt][n][2 + k] = nan;
               }
             }
-              __syncwarp();
+        __syncwarp();
         // (these positions' values of this head are this warp's alone)
 #pragma unroll 1
         for (int x = x0; x < x1; ++x)
