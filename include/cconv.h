@@ -721,9 +721,11 @@ CCONV_API int attn_decode_q8(const void* q, int64_t q_row_stride, kv_cache_q8_t 
  *                before the first group and behind the last are attended as by
  *                attn_decode.
  *   prefix_lens  int32 [num_groups]: the first prefix_lens[g] positions are the
- *                same for all of group g, in the same pages or in copies: those of
- *                the block table of its first request are read. Any length,
- *                whole pages or not; 0 for no prefix.
+ *                same for all of group g, in the same pages or in copies. They are
+ *                read through the block table of the first request that sees all
+ *                of them, once (an entry of that which is out of range: of the
+ *                group's first request). Any length, whole pages or not; 0 for no
+ *                prefix.
  *   seq_lens     as attn_decode, the prefix included. A request of which some row
  *                does not see the whole prefix (seq_lens[s] - n_spec <
  *                prefix_lens[g]) attends over its own block table alone.

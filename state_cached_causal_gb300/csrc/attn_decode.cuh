@@ -62,15 +62,16 @@ __host__ __device__ constexpr int attn_mma_blocks(int D, int rows, bool q8) {
 }
 
 // Length of request b; -1 for one that is skipped.
-__device__ __forceinline__ int attn_len(const AttnArgs& a, int b) {
+__host__ __device__ __forceinline__ int attn_len(const AttnArgs& a, int b) {
   const int n = a.seq_lens[b];
   return (n < 0 || n > (int64_t)a.table_width * a.page_size) ? -1 : n;
 }
 
 // attn_decode_shared: the group that request b is of (-1: none), and the prefix of
 // group g (0 where its bounds or its prefix are out of range).
-__device__ __forceinline__ int attn_group(const AttnArgs& a, int b) {
+__host__ __device__ __forceinline__ int attn_group(const AttnArgs& a, int b) {
   int lo = 0, hi = a.groups;              // the last group that begins at b or before
+#pragma unroll 1
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (a.cu_groups[mid] <= b)
@@ -81,21 +82,26 @@ __device__ __forceinline__ int attn_group(const AttnArgs& a, int b) {
   const int g = lo - 1;
   return g >= 0 && a.cu_groups[g + 1] > b ? g : -1;
 }
-__device__ __forceinline__ bool attn_group_ok(const AttnArgs& a, int first, int end, int prefix) {
+__host__ __device__ __forceinline__ bool attn_group_ok(const AttnArgs& a, int first, int end, int prefix) {
   return first >= 0 && first <= end && end <= a.B && prefix >= 0 &&
          prefix <= (int64_t)a.table_width * a.page_size;
 }
-__device__ __forceinline__ int attn_prefix(const AttnArgs& a, int g) {
+__host__ __device__ __forceinline__ int attn_prefix(const AttnArgs& a, int g) {
   const int first = a.cu_groups[g], end = a.cu_groups[g + 1], p = a.prefix_lens[g];
   return attn_group_ok(a, first, end, p) ? p : 0;
 }
 // The positions of request b that the shared kernel takes (the rest begins there):
 // its group's prefix if all its rows see the whole of that, else none.
-__device__ __forceinline__ int attn_start(const AttnArgs& a, int b) {
+__host__ __device__ __forceinline__ int attn_start(const AttnArgs& a, int b) {
   const int g = attn_group(a, b);
   if (g < 0) return 0;
   const int p = attn_prefix(a, g);
   return attn_len(a, b) - (a.q_len - 1) >= p ? p : 0;
+}
+// The positions of request b that lie behind that.
+__host__ __device__ __forceinline__ int attn_behind(const AttnArgs& a, int b) {
+  const int n = attn_len(a, b);
+  return n > 0 ? n - attn_start(a, b) : 0;
 }
 
 // The position that tile 0 of request b begins at, and its tiles: at least one (an
@@ -120,28 +126,34 @@ __device__ __forceinline__ int attn_tiles(const AttnArgs& a, int b, int tile) {
 // place is in its run, and no run is shorter than two.
 struct AttnGroup {
   int first, prefix, tiles;
-  int64_t rows, units;        // rows of a kv head; units 0 without a prefix or requests
+  int lead;                   // the first request that sees the prefix whole (-1: none)
+  int64_t rows, units;        // rows of a kv head; units 0 without a prefix or a lead
   int64_t full;               // units of two whole row tiles, which come first
   int per_full, per, wide;    // places of one of these, of another, and of a tile of that
   int start, pair;
 
-  __device__ __forceinline__ int64_t places() const { return full * per_full + (units - full) * per; }
+  __host__ __device__ __forceinline__ int64_t places() const { return full * per_full + (units - full) * per; }
   // the place of a unit's tile 0, and those of a tile
   __device__ __forceinline__ int64_t place_of(int64_t unit) const {
     return start + (unit < full ? unit * per_full : full * per_full + (unit - full) * per);
   }
   __device__ __forceinline__ int tile_places(int64_t unit) const { return unit < full ? pair : wide; }
 };
-__device__ __forceinline__ AttnGroup attn_group_of(const AttnArgs& a, int g) {
+__host__ __device__ __forceinline__ AttnGroup attn_group_of(const AttnArgs& a, int g) {
   AttnGroup r;
   r.first = a.cu_groups[g];
   const int end = a.cu_groups[g + 1], p = a.prefix_lens[g];
   const bool ok = attn_group_ok(a, r.first, end, p), two = a.unit_rows > 128;
   r.prefix = ok ? p : 0;
   r.tiles = (r.prefix + a.prefix_tile - 1) / a.prefix_tile;
+  r.lead = ok ? r.first : end;
+  if (r.tiles > 0)
+#pragma unroll 1
+    while (r.lead < end && attn_len(a, r.lead) - (a.q_len - 1) < r.prefix) ++r.lead;
+  if (r.lead >= end) r.lead = -1;
   r.rows = ok ? (int64_t)(end - r.first) * (a.G * a.q_len) : 0;
   const int64_t blocks = (r.rows + a.unit_rows - 1) / a.unit_rows;     // of rows
-  r.units = r.tiles > 0 ? blocks * a.Hkv : 0;
+  r.units = r.tiles > 0 && r.lead >= 0 ? blocks * a.Hkv : 0;
   r.full = two && r.units > 0 ? r.units - a.Hkv : 0;
   r.start = a.start_places;
   r.pair = a.pair_places;
@@ -153,19 +165,28 @@ __device__ __forceinline__ AttnGroup attn_group_of(const AttnArgs& a, int g) {
 
 // The SMs that take the prefixes, the others taking the rest meanwhile: as the work of
 // both is, by what an SM needs for it. `places` of the prefixes, `positions` of all
-// requests that lie behind them (or so: a request that does not see its prefix whole
-// counts as if it did); every block of both kernels comes to the same number. (One after
+// requests that lie behind what they see of them; every block of both kernels comes to
+// the same number. (With every request counted as if it saw its prefix, 64 of 4000
+// positions in a group whose prefix is 4096 took 1149 us, where attn_decode takes 90. One after
 // the other on all SMs: 256 requests behind a long document 153 us against 146, groups in
 // 8 bits 103 to 110 against 86, 64 requests whose own 8192 positions are most of the work
 // 126 against 116, 96 behind 1024 positions 67 against 57. With at most 5/8 of the SMs
 // for the rest those 64 took 157.)
-__device__ __forceinline__ int attn_prefix_sms(const AttnArgs& a, int64_t places,
+__host__ __device__ __forceinline__ int attn_prefix_sms(const AttnArgs& a, int64_t places,
                                                int64_t positions) {
   if (places == 0) return 0;
   const int64_t tiles = (max(positions, (int64_t)0) / a.own_tile + a.B / 2) * a.units;
   const int64_t pc = places * a.place_cost, tc = tiles * a.tile_cost;
   const int64_t own = (a.sms * tc + pc + tc - 1) / max(pc + tc, (int64_t)1);
   return a.sms - (int)min(max(own, (int64_t)2), (int64_t)a.sms * 15 / 16);
+}
+
+// Requests what the counts below read, all at once (a group's prefix would wait for the
+// search among the groups).
+__device__ __forceinline__ void attn_warm(const AttnArgs& a) {
+  const int g = min((int)threadIdx.x, a.groups - 1), b = min((int)threadIdx.x, a.B - 1);
+  if (g >= 0)
+    asm volatile("" ::"r"(a.cu_groups[g]), "r"(a.prefix_lens[g]), "r"(a.seq_lens[b]));
 }
 
 // The block's run [p, end) of the line and the request that p lies in.
@@ -187,13 +208,15 @@ __device__ __forceinline__ bool attn_split(const AttnArgs& a, int tile, int64_t 
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   int64_t mine = 0;
   constexpr int kW = THREADS / 32;
-  if constexpr (SHARED) {           // before the requests' own: their loads run together
+  if constexpr (SHARED) {
     int64_t places = 0, positions = 0;
-    for (int b = tid; b < a.B; b += THREADS) positions += max(attn_len(a, b), 0);
-    for (int g = tid; g < a.groups; g += THREADS) {
-      const AttnGroup s = attn_group_of(a, g);
-      places += s.places();
-      positions -= s.rows / (a.G * a.q_len) * s.prefix;
+    attn_warm(a);
+#pragma unroll 1
+    for (int g = tid; g < a.groups; g += THREADS) places += attn_group_of(a, g).places();
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      mine += attn_tiles<true>(a, b, tile);
+      positions += attn_behind(a, b);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
@@ -202,7 +225,8 @@ __device__ __forceinline__ bool attn_split(const AttnArgs& a, int tile, int64_t 
     }
     if ((tid & 31) == 0) sm[kW + (tid >> 5)] = places, sm[2 * kW + (tid >> 5)] = positions;
   }
-  for (int b = b0; b < b1; ++b) mine += attn_tiles<SHARED>(a, b, tile);
+  if constexpr (!SHARED)
+    for (int b = b0; b < b1; ++b) mine += attn_tiles<false>(a, b, tile);
   int64_t incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {

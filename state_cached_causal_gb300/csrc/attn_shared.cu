@@ -133,12 +133,14 @@ __device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) 
   const int tid = threadIdx.x, per = (a.groups + kThreads - 1) / kThreads;
   const int g0 = min(a.groups, tid * per), g1 = min(a.groups, g0 + per);
   int64_t lines = 0, units = 0, own = 0;      // own: positions behind the prefixes
-  for (int b = tid; b < a.B; b += kThreads) own += max(attn_len(a, b), 0);
+  attn_warm(a);
+#pragma unroll 1
+  for (int b = tid; b < a.B; b += kThreads) own += attn_behind(a, b);
+#pragma unroll 1
   for (int g = g0; g < g1; ++g) {
     const AttnGroup s = attn_group_of(a, g);
     lines += s.places();
     units += s.units;
-    own -= s.rows / (a.G * a.q_len) * s.prefix;
     if (blockIdx.x == 0 &&
         !attn_group_ok(a, a.cu_groups[g], a.cu_groups[g + 1], a.prefix_lens[g]))
       flag_error(a.dev_err, CCONV_DERR_GROUP);
@@ -197,6 +199,7 @@ __device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) 
 // One segment: tiles [j0, j1) of a unit: rows [row0, row0 + rows) of group g and kv head h.
 struct Seg {
   int first, prefix;          // the group's first request, and its prefix
+  int lead;                   // the request whose table names the prefix
   int h, j0, j1, rows, row0;
   int64_t slot;
   bool pair;                  // two row tiles on the same positions
@@ -227,7 +230,7 @@ __device__ __forceinline__ bool segment(const PrefixArgs& x, Run& r, Seg& s) {
     if (s.j1 <= s.j0) continue;
     if (!whole) u += (int)g.full;
     const int mt = u / x.a.Hkv;
-    s.first = g.first, s.prefix = g.prefix;
+    s.first = g.first, s.prefix = g.prefix, s.lead = g.lead;
     s.h = u - mt * x.a.Hkv;
     s.row0 = mt * S::kRowsU;
     s.rows = min(S::kRowsU, (int)g.rows - s.row0);
@@ -264,7 +267,8 @@ __device__ __forceinline__ uint32_t place(int r, int u) {
 // What the copies know of an item, from the lane that has its row on.
 struct Piece {
   int page;             // as the table has it
-  int tok, h;           // token of the page, kv head
+  int pos, h;           // position, kv head
+  int first;            // the group's first request, if the table is another's, else -1
   int seq;              // the tile's number, as masks are kept by
   bool isv, there;      // V; false: behind the last item
   bool row;             // the lane has a row of the prefix
@@ -290,8 +294,11 @@ __device__ __forceinline__ bool copy_role(const PrefixArgs& x, Run run, Ctl& c,
   Seg s;
   int i = 0, n = 0, seq = 0;
   bool more = true;
+  auto page_at = [&](int pos) {
+    return a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
+  };
   auto next = [&]() {
-    Piece p = {-1, 0, 0, 0, false, false, false};
+    Piece p = {-1, 0, 0, -1, 0, false, false, false};
     if (more && i == 2 * n) {
       seq += n;
       i = 0;
@@ -300,27 +307,31 @@ __device__ __forceinline__ bool copy_role(const PrefixArgs& x, Run run, Ctl& c,
     }
     if (!more) return p;
     const Item m = item_of(i++, n, S::NT == 2 && !s.pair);
-    const int pos = (s.j0 + m.tile) * S::kN + w * kRowsW + lane;
+    p.pos = (s.j0 + m.tile) * S::kN + w * kRowsW + lane;
     p.h = s.h;
     p.seq = seq + m.tile;
     p.isv = m.isv;
     p.there = true;
-    if (lane < kRowsW && pos < s.prefix) {
-      const int at = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
-      p.tok = a.page_shift >= 0 ? pos & (a.page_size - 1) : pos - at * a.page_size;
+    if (lane < kRowsW && p.pos < s.prefix) {
       p.row = true;
-      p.page = a.table[(int64_t)s.first * a.table_rs + at];
+      p.first = s.lead != s.first ? s.first : -1;
+      p.page = a.table[(int64_t)s.lead * a.table_rs + page_at(p.pos)];
     }
     return p;
   };
   auto row_of = [&](const Piece& p) {
     Row r = {-1, 0.0f};
-    if (p.row && (uint32_t)p.page >= (uint32_t)a.num_pages) {
+    int page = p.page;
+    if (p.row && (uint32_t)page >= (uint32_t)a.num_pages && p.first >= 0)
+      page = a.table[(int64_t)p.first * a.table_rs + page_at(p.pos)];
+    if (p.row && (uint32_t)page >= (uint32_t)a.num_pages) {
       if (!p.isv) flag_error(a.dev_err, CCONV_DERR_PAGE);
     } else if (p.row) {
-      r.at = p.page * a.s_page + p.tok * a.s_tok + (int64_t)p.h * a.s_head;
+      const int tok =
+          a.page_shift >= 0 ? p.pos & (a.page_size - 1) : p.pos - page_at(p.pos) * a.page_size;
+      r.at = page * a.s_page + tok * a.s_tok + (int64_t)p.h * a.s_head;
       if constexpr (Q8)
-        r.f = q8_scale((p.isv ? a.vsc : a.ksc)[p.page * a.c_page + p.tok * a.c_tok +
+        r.f = q8_scale((p.isv ? a.vsc : a.ksc)[page * a.c_page + tok * a.c_tok +
                                                (int64_t)p.h * a.c_head]);
     }
     return r;

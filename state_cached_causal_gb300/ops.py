@@ -813,8 +813,8 @@ def attn_decode_shared(q, k_cache, v_cache, block_table, seq_lens, cu_groups, pr
     attn_decode_shared in cconv.h).
 
     cu_groups: int32 [groups + 1], group g holds requests cu_groups[g] to cu_groups[g + 1] - 1;
-    prefix_lens: int32 [groups], the positions that it shares, read through the block table of its
-    first request; workspace: attn_decode_shared_workspace_bytes() or None (allocated for the
+    prefix_lens: int32 [groups], the positions that it shares, read through the block table of the
+    first of its requests that sees all of them; workspace: attn_decode_shared_workspace_bytes() or None (allocated for the
     call). The rest as attn_decode, in bf16.
     """
     if stream is None and (_lib or load()) and _fast is not None and _served(
