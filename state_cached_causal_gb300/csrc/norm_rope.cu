@@ -13,28 +13,30 @@
 // there are few tokens a token's heads are spread over several warps.
 //
 // Four groups of query heads have their loads in flight together, beside the
-// first group of keys and values, and three blocks an SM take the tokens one after
-// the other, the next token's position and slot read ahead and its queries asked
-// into the L2. 33024 tokens of 16 + 4 + 4 heads of 128 in bf16: 73.0 us for 422 MB,
-// 5.8 TB/s (without that prefetch 78.0 us, and 75.9 with four blocks, whose 128
-// registers spill a little; four with it 77.7; keys and values prefetched, too, no
-// better; keys after the queries, values after the keys: 78.7 us; one unit a lane:
-// 98.7 us). 61 tokens: 3.0 us, the latency of a few dependent loads. (Four blocks took
-// 2000 to 2400 tokens 8 % faster, in one turn, and other numbers up to 10 % slower.)
+// first group of keys and values, and the blocks' warps take the tokens one after the
+// other, the next token's position and slot read ahead. 33024 tokens of 16 + 4 + 4
+// heads of 128 in bf16: 73.0 us for 422 MB, 5.8 TB/s (keys after the queries, values
+// after the keys: 5 % more; one unit a lane: 30 % more). 61 tokens: 3.0 us, the latency
+// of a few dependent loads.
+//
+// An SM holds three blocks or four (`blocks_of`). Three spill nothing in bf16 and are 3
+// to 15 % faster for as many steps; four have fewer steps in turn for some numbers of
+// tokens, and then are faster: 2100 tokens of the heads above 8.6 us where three take
+// 10.0, in fp32 11.4 and 14.3; 16000 in fp32 62.9 and 66.6.
 //
 // Into a cache in 8 bits a row's largest magnitude is reduced over the head's lanes
 // as its sum of squares is, and a unit of 16 bytes becomes one of 8 (4 from fp32). The
-// same tokens: 75.1 us for 389 MB, 5.2 TB/s (four blocks without the prefetch 80.5; the
-// 8 bytes in one store instead of two: the same): the second reduction, the
-// conversions and the narrower stores cost the instructions what the bytes save.
+// same tokens: 75.1 us for 389 MB, 5.2 TB/s (the 8 bytes in one store instead of two: the
+// same): the second reduction, the conversions and the narrower stores cost the
+// instructions what the bytes save.
 #include "q8.cuh"
 
 namespace cconv {
 namespace {
 
 constexpr int kNrThreads = 128;
-constexpr int kNrBlocks = 3;    // of an SM
 constexpr int kUnroll = 4;      // groups of heads whose loads are in flight together
+constexpr int kBatch = 32 * 2 * 16 * kUnroll;   // bytes of queries that a warp loads together
 
 struct NrArgs {
   const char *q, *k, *v;
@@ -51,14 +53,15 @@ struct NrArgs {
   const int32_t* slots;
   int32_t T, Hq, Hkv;
   int32_t parts;      // warps a token
+  bool ahead;         // the next token's queries are asked into the L2
   char* qo;
   int32_t* dev_err;
   uint8_t *ksc, *vsc;   // of a cache in 8 bits
   int64_t c_page, c_tok, c_head;
 };
 
-template <typename T, int D, bool PAIRS, bool Q8>
-__global__ void __launch_bounds__(kNrThreads, kNrBlocks) norm_rope_kernel(const NrArgs a) {
+template <typename T, int D, bool PAIRS, bool Q8, int BLOCKS>
+__global__ void __launch_bounds__(kNrThreads, BLOCKS) norm_rope_kernel(const NrArgs a) {
   constexpr int V = Elem<T>::V, E = Elem<T>::bytes;
   constexpr int LPH = D / V / 2;              // lanes a head, two units each
   constexpr int HPW = 32 / LPH;               // heads a warp at a time
@@ -91,7 +94,7 @@ __global__ void __launch_bounds__(kNrThreads, kNrBlocks) norm_rope_kernel(const 
     if (t < a.T) {                // the next token's, while this one is worked on
       pos = a.pos[t];
       slot = a.slots[t];
-      if (a.parts == 1)           // its queries to the L2, whose latency it then waits for
+      if (BLOCKS == 3 && a.ahead) // its queries to the L2, whose latency it then waits for
         for (int at = lane * 128; at < a.Hq * (D * E); at += 32 * 128)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + t * a.q_rs * E + at));
     }
@@ -279,23 +282,68 @@ __global__ void __launch_bounds__(kNrThreads, kNrBlocks) norm_rope_kernel(const 
   }
 }
 
-template <typename T, int D, bool Q8>
-cudaError_t launch_nr(const NrArgs& a, bool pairs, int sms, cudaStream_t st) {
-  const int64_t warps = (int64_t)a.T * a.parts, per = kNrThreads / 32;
+// Warps of a token, for `slots` of them at work at once: several while that leaves all of
+// them at work at once, 1, 2, 4 or 8, so that a block's four warps, and the grid's, fall
+// into whole tokens.
+int parts_of(int64_t tokens, int64_t slots) {
+  int p = 1;
+  while (p < 8 && tokens * p * 2 <= slots) p *= 2;
+  return p;
+}
+// The blocks of an SM: four where a warp then has fewer steps in turn, tokens one after
+// the other and batches of its share of a token's queries. (With three: 1000 tokens in
+// fp32, whose 8 KB of queries are two batches, 8.4 us where four blocks, with twice the
+// warps a token, take 7.2.) `ahead`: tokens in turn ask for the next one's queries, in bf16
+// where those are a batch at most, and queries, keys and values three quarters of one. With four
+// turns or more that is worth three blocks: 16000 tokens 37.1 us (four blocks 38.7, three
+// without 39.2), into 8 bits 38.8 (41.7, 40.6), of 16 + 4 heads of 64 (3 KB) 26.4 (27.7,
+// 28.1). Queries of several batches, shorter rows, and fp32 are slower with it: 14000 tokens
+// of 32 + 8 heads of 128 65.2 us, four blocks 59.9; 33024 of 8 + 1 49.1, four blocks 48.1.
+// For as many steps three are faster in bf16, and in fp32, which spills with neither, for
+// rows of several batches or where four would take more warps a token (else 2 to 7 % slower).
+int blocks_of(const NrArgs& a, int D, int e, int sms, bool& ahead) {
+  const int64_t row = (int64_t)a.Hq * D * e, batches = (row + kBatch - 1) / kBatch;
+  int64_t turns = 0;
+  int p = 0;
+  auto steps = [&](int blocks) {
+    const int64_t slots = (int64_t)sms * blocks * (kNrThreads / 32);
+    p = parts_of(a.T, slots);
+    turns = (a.T * (int64_t)p + slots - 1) / slots;
+    return turns * ((batches + p - 1) / p);
+  };
+  const int64_t four = steps(4);
+  const int p4 = p;
+  const int64_t three = steps(3);
+  ahead = e == 2 && row <= kBatch && row + 2LL * a.Hkv * D * e >= kBatch * 3 / 4 && turns > 1;
+  if (e == 4 && four == three && p == p4 && (turns == 1 || batches == 1)) return 4;
+  return four < three && !(ahead && turns >= 4) ? 4 : 3;
+}
+
+template <typename T, int D, bool Q8, int BLOCKS>
+cudaError_t launch_nr(NrArgs& a, bool pairs, int sms, cudaStream_t st) {
+  const int64_t per = kNrThreads / 32;
+  a.parts = parts_of(a.T, sms * BLOCKS * per);
   const unsigned grid =
-      (unsigned)std::min<int64_t>((warps + per - 1) / per, (int64_t)sms * kNrBlocks);
+      (unsigned)std::min<int64_t>(((int64_t)a.T * a.parts + per - 1) / per, (int64_t)sms * BLOCKS);
   if (pairs)
-    norm_rope_kernel<T, D, true, Q8><<<grid, kNrThreads, 0, st>>>(a);
+    norm_rope_kernel<T, D, true, Q8, BLOCKS><<<grid, kNrThreads, 0, st>>>(a);
   else
-    norm_rope_kernel<T, D, false, Q8><<<grid, kNrThreads, 0, st>>>(a);
+    norm_rope_kernel<T, D, false, Q8, BLOCKS><<<grid, kNrThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
+template <typename T, bool Q8, int BLOCKS>
+cudaError_t launch_nr_d(NrArgs& a, int D, bool pairs, int sms, cudaStream_t st) {
+  if (D == 64) return launch_nr<T, 64, Q8, BLOCKS>(a, pairs, sms, st);
+  if (D == 128) return launch_nr<T, 128, Q8, BLOCKS>(a, pairs, sms, st);
+  return launch_nr<T, 256, Q8, BLOCKS>(a, pairs, sms, st);
+}
+
 template <typename T, bool Q8>
-cudaError_t launch_nr_d(const NrArgs& a, int D, bool pairs, int sms, cudaStream_t st) {
-  if (D == 64) return launch_nr<T, 64, Q8>(a, pairs, sms, st);
-  if (D == 128) return launch_nr<T, 128, Q8>(a, pairs, sms, st);
-  return launch_nr<T, 256, Q8>(a, pairs, sms, st);
+cudaError_t launch_nr_b(NrArgs& a, int D, bool pairs, int sms, cudaStream_t st) {
+  return blocks_of(a, D, Elem<T>::bytes, sms, a.ahead) == 4
+             ? launch_nr_d<T, Q8, 4>(a, D, pairs, sms, st)
+             : launch_nr_d<T, Q8, 3>(a, D, pairs, sms, st);
 }
 
 // What both entry points check and fill in; a's cache, and D, are set.
@@ -337,20 +385,15 @@ int norm_rope(NrArgs& a, int D, bool q8, const void* q, int64_t q_row_stride, co
   a.Hq = num_q_heads;
   a.qo = static_cast<char*>(q_out);
   a.dev_err = dev_err;
-  // several warps a token while that leaves all of them at work at once (1000 tokens with
-  // two, more than that: 5.9 us, not 4.7): 1, 2, 4 or 8, so that a block's four warps,
-  // and the grid's, fall into whole tokens
-  a.parts = 1;
-  while (a.parts < 8 && (int64_t)num_tokens * a.parts * 2 <= (int64_t)sms * (kNrBlocks * kNrThreads / 32)) a.parts *= 2;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool pairs = interleaved != 0;
   cudaError_t err;
   if (dtype == CCONV_DTYPE_F32)
-    err = q8 ? launch_nr_d<float, true>(a, D, pairs, sms, st)
-             : launch_nr_d<float, false>(a, D, pairs, sms, st);
+    err = q8 ? launch_nr_b<float, true>(a, D, pairs, sms, st)
+             : launch_nr_b<float, false>(a, D, pairs, sms, st);
   else
-    err = q8 ? launch_nr_d<__nv_bfloat16, true>(a, D, pairs, sms, st)
-             : launch_nr_d<__nv_bfloat16, false>(a, D, pairs, sms, st);
+    err = q8 ? launch_nr_b<__nv_bfloat16, true>(a, D, pairs, sms, st)
+             : launch_nr_b<__nv_bfloat16, false>(a, D, pairs, sms, st);
   return err == cudaSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
 }
 
