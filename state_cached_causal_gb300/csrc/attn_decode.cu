@@ -462,10 +462,10 @@ extern "C" int64_t attn_decode_workspace_bytes(int32_t num_seqs, int32_t n_spec,
   const int sms = mix_sm_count();
   if (sms <= 0) return CCONV_ERR_LAUNCH;
   int64_t most = 0;
-  // (a cache in 8 bits has no larger grid)
   for (const int dtype : {CCONV_DTYPE_F32, CCONV_DTYPE_BF16})
-    most = std::max(most, attn_plan(dtype, false, sms, num_seqs, 1 + n_spec,
-                                    num_q_heads / num_kv_heads, num_kv_heads, head_dim).bytes);
+    for (const bool q8 : {false, true})
+      most = std::max(most, attn_plan(dtype, q8, sms, num_seqs, 1 + n_spec,
+                                      num_q_heads / num_kv_heads, num_kv_heads, head_dim).bytes);
   return most;
 }
 

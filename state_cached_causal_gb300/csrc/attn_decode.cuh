@@ -55,10 +55,10 @@ struct AttnArgs {
 };
 
 // Blocks of the bf16 kernels that an SM holds at once, by their registers and
-// shared memory (50 to 218 KB). A block of the kernel over a cache in 8 bits has a
-// warp more.
+// shared memory (50 to 218 KB; with heads of 256 two places of the ring are over half of
+// it already). A block of the kernel over a cache in 8 bits has a warp more.
 __host__ __device__ constexpr int attn_mma_blocks(int D, int rows, bool q8) {
-  return D * rows >= 4096 ? 1 : D * rows >= 2048 || q8 ? 2 : 3;
+  return D == 256 || D * rows >= 4096 ? 1 : D * rows >= 2048 || q8 ? 2 : 3;
 }
 
 // Length of request b; -1 for one that is skipped.

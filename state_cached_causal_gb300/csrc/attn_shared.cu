@@ -1127,9 +1127,11 @@ extern "C" int64_t attn_decode_shared_workspace_bytes(int32_t num_seqs, int32_t 
   if (rc != CCONV_OK) return rc;
   const int sms = mix_sm_count();
   if (sms <= 0) return CCONV_ERR_LAUNCH;
-  // (a cache in 8 bits has no larger grid)
-  return shared_plan(false, sms, num_seqs, num_groups, 1 + n_spec, num_q_heads / num_kv_heads,
-                     num_kv_heads, head_dim).bytes;
+  int64_t most = 0;
+  for (const bool q8 : {false, true})
+    most = std::max(most, shared_plan(q8, sms, num_seqs, num_groups, 1 + n_spec,
+                                      num_q_heads / num_kv_heads, num_kv_heads, head_dim).bytes);
+  return most;
 }
 
 extern "C" int attn_decode_shared(const void* q, int64_t q_row_stride, kv_cache_t cache,
