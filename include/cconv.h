@@ -723,9 +723,9 @@ CCONV_API int attn_decode_q8(const void* q, int64_t q_row_stride, kv_cache_q8_t 
  *   prefix_lens  int32 [num_groups]: the first prefix_lens[g] positions are the
  *                same for all of group g, in the same pages or in copies. They are
  *                read through the block table of the first request that sees all
- *                of them, once (an entry of that which is out of range: of the
- *                group's first request). Any length, whole pages or not; 0 for no
- *                prefix.
+ *                of them, once (where that does not name a page of position 0: of
+ *                the group's first request). Any length, whole pages or not; 0 for
+ *                no prefix.
  *   seq_lens     as attn_decode, the prefix included. A request of which some row
  *                does not see the whole prefix (seq_lens[s] - n_spec <
  *                prefix_lens[g]) attends over its own block table alone.

@@ -139,6 +139,8 @@ struct AttnGroup {
   }
   __device__ __forceinline__ int tile_places(int64_t unit) const { return unit < full ? pair : wide; }
 };
+// (LED: it is known that there is a lead, which is not looked for)
+template <bool LED = false>
 __host__ __device__ __forceinline__ AttnGroup attn_group_of(const AttnArgs& a, int g) {
   AttnGroup r;
   r.first = a.cu_groups[g];
@@ -147,7 +149,7 @@ __host__ __device__ __forceinline__ AttnGroup attn_group_of(const AttnArgs& a, i
   r.prefix = ok ? p : 0;
   r.tiles = (r.prefix + a.prefix_tile - 1) / a.prefix_tile;
   r.lead = ok ? r.first : end;
-  if (r.tiles > 0)
+  if (!LED && r.tiles > 0)
 #pragma unroll 1
     while (r.lead < end && attn_len(a, r.lead) - (a.q_len - 1) < r.prefix) ++r.lead;
   if (r.lead >= end) r.lead = -1;
@@ -181,14 +183,6 @@ __host__ __device__ __forceinline__ int attn_prefix_sms(const AttnArgs& a, int64
   return a.sms - (int)min(max(own, (int64_t)2), (int64_t)a.sms * 15 / 16);
 }
 
-// Requests what the counts below read, all at once (a group's prefix would wait for the
-// search among the groups).
-__device__ __forceinline__ void attn_warm(const AttnArgs& a) {
-  const int g = min((int)threadIdx.x, a.groups - 1), b = min((int)threadIdx.x, a.B - 1);
-  if (g >= 0)
-    asm volatile("" ::"r"(a.cu_groups[g]), "r"(a.prefix_lens[g]), "r"(a.seq_lens[b]));
-}
-
 // The block's run [p, end) of the line and the request that p lies in.
 struct AttnRun {
   int64_t p, end, total;
@@ -210,7 +204,6 @@ __device__ __forceinline__ bool attn_split(const AttnArgs& a, int tile, int64_t 
   constexpr int kW = THREADS / 32;
   if constexpr (SHARED) {
     int64_t places = 0, positions = 0;
-    attn_warm(a);
 #pragma unroll 1
     for (int g = tid; g < a.groups; g += THREADS) places += attn_group_of(a, g).places();
 #pragma unroll 1

@@ -123,7 +123,7 @@ __device__ __forceinline__ int64_t runs_of(int64_t sms, int64_t total) {
 struct Run {
   int64_t p, end, total, grid;
   int64_t line, unit;         // of group g
-  int g;
+  int g, lead;                // (its first request that sees the prefix)
 };
 
 // As attn_split, over the groups. The first block notes every group for the join.
@@ -133,7 +133,6 @@ __device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) 
   const int tid = threadIdx.x, per = (a.groups + kThreads - 1) / kThreads;
   const int g0 = min(a.groups, tid * per), g1 = min(a.groups, g0 + per);
   int64_t lines = 0, units = 0, own = 0;      // own: positions behind the prefixes
-  attn_warm(a);
 #pragma unroll 1
   for (int b = tid; b < a.B; b += kThreads) own += attn_behind(a, b);
 #pragma unroll 1
@@ -186,13 +185,14 @@ __device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) 
     int g = g0;
     for (;; ++g) {
       const AttnGroup s = attn_group_of(a, g);
+      sm[3] = s.lead;
       if (r.p < li + s.places()) break;
       li += s.places(), ui += s.units;
     }
     sm[0] = g, sm[1] = li, sm[2] = ui;
   }
   __syncthreads();
-  r.g = (int)sm[0], r.line = sm[1], r.unit = sm[2];
+  r.g = (int)sm[0], r.line = sm[1], r.unit = sm[2], r.lead = (int)sm[3];
   return r.p < r.end;
 }
 
@@ -209,11 +209,12 @@ template <int D>
 __device__ __forceinline__ bool segment(const PrefixArgs& x, Run& r, Seg& s) {
   using S = Shape<D>;
   while (r.p < r.end) {
-    AttnGroup g = attn_group_of(x.a, r.g);
+    AttnGroup g = attn_group_of<true>(x.a, r.g);
     while (r.p >= r.line + g.places()) {      // (groups without units, too)
       r.line += g.places();
       r.unit += g.units;
       g = attn_group_of(x.a, ++r.g);
+      r.lead = g.lead;
     }
     int64_t rel = r.p - r.line;
     const bool whole = rel < g.full * g.per_full;
@@ -230,7 +231,7 @@ __device__ __forceinline__ bool segment(const PrefixArgs& x, Run& r, Seg& s) {
     if (s.j1 <= s.j0) continue;
     if (!whole) u += (int)g.full;
     const int mt = u / x.a.Hkv;
-    s.first = g.first, s.prefix = g.prefix, s.lead = g.lead;
+    s.first = g.first, s.prefix = g.prefix, s.lead = r.lead;
     s.h = u - mt * x.a.Hkv;
     s.row0 = mt * S::kRowsU;
     s.rows = min(S::kRowsU, (int)g.rows - s.row0);
@@ -267,8 +268,7 @@ __device__ __forceinline__ uint32_t place(int r, int u) {
 // What the copies know of an item, from the lane that has its row on.
 struct Piece {
   int page;             // as the table has it
-  int pos, h;           // position, kv head
-  int first;            // the group's first request, if the table is another's, else -1
+  int tok, h;           // token of the page, kv head
   int seq;              // the tile's number, as masks are kept by
   bool isv, there;      // V; false: behind the last item
   bool row;             // the lane has a row of the prefix
@@ -294,44 +294,40 @@ __device__ __forceinline__ bool copy_role(const PrefixArgs& x, Run run, Ctl& c,
   Seg s;
   int i = 0, n = 0, seq = 0;
   bool more = true;
-  auto page_at = [&](int pos) {
-    return a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
-  };
   auto next = [&]() {
-    Piece p = {-1, 0, 0, -1, 0, false, false, false};
+    Piece p = {-1, 0, 0, 0, false, false, false};
     if (more && i == 2 * n) {
       seq += n;
       i = 0;
       more = segment<D>(x, run, s);
       n = more ? s.j1 - s.j0 : 0;
+      if (more && s.lead != s.first &&
+          (uint32_t)a.table[(int64_t)s.lead * a.table_rs] >= (uint32_t)a.num_pages)
+        s.lead = s.first;
     }
     if (!more) return p;
     const Item m = item_of(i++, n, S::NT == 2 && !s.pair);
-    p.pos = (s.j0 + m.tile) * S::kN + w * kRowsW + lane;
+    const int pos = (s.j0 + m.tile) * S::kN + w * kRowsW + lane;
     p.h = s.h;
     p.seq = seq + m.tile;
     p.isv = m.isv;
     p.there = true;
-    if (lane < kRowsW && p.pos < s.prefix) {
+    if (lane < kRowsW && pos < s.prefix) {
+      const int at = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
+      p.tok = a.page_shift >= 0 ? pos & (a.page_size - 1) : pos - at * a.page_size;
       p.row = true;
-      p.first = s.lead != s.first ? s.first : -1;
-      p.page = a.table[(int64_t)s.lead * a.table_rs + page_at(p.pos)];
+      p.page = a.table[(int64_t)s.lead * a.table_rs + at];
     }
     return p;
   };
   auto row_of = [&](const Piece& p) {
     Row r = {-1, 0.0f};
-    int page = p.page;
-    if (p.row && (uint32_t)page >= (uint32_t)a.num_pages && p.first >= 0)
-      page = a.table[(int64_t)p.first * a.table_rs + page_at(p.pos)];
-    if (p.row && (uint32_t)page >= (uint32_t)a.num_pages) {
+    if (p.row && (uint32_t)p.page >= (uint32_t)a.num_pages) {
       if (!p.isv) flag_error(a.dev_err, CCONV_DERR_PAGE);
     } else if (p.row) {
-      const int tok =
-          a.page_shift >= 0 ? p.pos & (a.page_size - 1) : p.pos - page_at(p.pos) * a.page_size;
-      r.at = page * a.s_page + tok * a.s_tok + (int64_t)p.h * a.s_head;
+      r.at = p.page * a.s_page + p.tok * a.s_tok + (int64_t)p.h * a.s_head;
       if constexpr (Q8)
-        r.f = q8_scale((p.isv ? a.vsc : a.ksc)[page * a.c_page + tok * a.c_tok +
+        r.f = q8_scale((p.isv ? a.vsc : a.ksc)[p.page * a.c_page + p.tok * a.c_tok +
                                                (int64_t)p.h * a.c_head]);
     }
     return r;
@@ -887,7 +883,7 @@ __global__ void __launch_bounds__(256) attn_shared_join_kernel(const PrefixArgs 
   const int64_t bu = (int64_t)b * a.units + unit;
   const int g = attn_start(a, b) > 0 ? attn_group(a, b) : -1;
   AttnGroup s = {};
-  if (g >= 0) s = attn_group_of(a, g);
+  if (g >= 0) s = attn_group_of<true>(a, g);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 c = *reinterpret_cast<const int2*>(a.meta + bu * 2);
   Rec rec = {}, all = {};

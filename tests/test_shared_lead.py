@@ -64,7 +64,7 @@ def test_no_request_sees_the_prefix(q8):
 @pytest.mark.gpu
 @both
 def test_pages_that_only_the_first_request_names(q8):
-    """As where later tables begin behind the prefix: an entry that is out of range is the first request's."""
+    """As where later tables begin behind the prefix: the first request's table is read."""
     c = Case(4, [(203, [20, 230, 250])], 8, 2, 128, 16, 1, q8)      # (tables of 1 and 2 name no page of the prefix)
     assert c.check() == 0
     c.table[0, 4] = c.table[1, 4] = -1                              # nobody does
