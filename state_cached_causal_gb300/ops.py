@@ -24,7 +24,8 @@ DERR_SLOT_RANGE, DERR_CU_SEQLENS, DERR_NUM_ACCEPTED, DERR_TIMEOUT = 1, 2, 4, 8
 DERR_ROW_INDEX, DERR_CHECKPOINT = 16, 32
 DERR_POSITION, DERR_PAGE, DERR_SEQ_LEN, DERR_GROUP = 64, 128, 256, 512
 
-_F8, _F8_SCALE = torch.float8_e4m3fn, torch.float8_e8m0fnu    # of a cache in 8 bits
+# of a cache in 8 bits (None on a PyTorch without them)
+_F8, _F8_SCALE = (getattr(torch, t, None) for t in ("float8_e4m3fn", "float8_e8m0fnu"))
 
 _lock = threading.Lock()
 _lib = None
@@ -159,8 +160,10 @@ def _load_fast(lib):
         raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     except (ImportError, AttributeError):
         return None
-    mod.init(lib._handle, (torch.float32, torch.bfloat16, torch.int32, torch.uint8, torch.bool,
-                           _F8, _F8_SCALE), raw, lambda beside, n: beside.new_empty(n, dtype=torch.uint8), device)
+    types = (torch.float32, torch.bfloat16, torch.int32, torch.uint8, torch.bool)
+    if _F8 is not None and _F8_SCALE is not None:
+        types += (_F8, _F8_SCALE)
+    mod.init(lib._handle, types, raw, lambda beside, n: beside.new_empty(n, dtype=torch.uint8), device)
     return mod
 
 
@@ -586,7 +589,7 @@ def _cache(k_cache, v_cache, dtype):
 def _cache_q8(k_cache, v_cache, k_scale, v_scale):
     """(shape, strides, scale strides) of an 8-bit cache's four views."""
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype is not _F8:
+        if t.dtype is not _F8:          # (nothing is where there is no such type)
             raise TypeError(f"{name} must be float8_e4m3fn")
     for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
         if t.dtype not in (torch.uint8, _F8_SCALE):
