@@ -15,9 +15,9 @@
 
 #include "cconv.h"
 
-enum { F32 = 0, BF16 = 1, I32 = 2, U8 = 3, F8 = 5, F8S = 6, MIN_DT = 5, NDT = 7 };
-/* float32, bfloat16, int32, uint8, bool, and of a cache in 8 bits float8_e4m3fn,
- * float8_e8m0fnu (taken as uint8); bool too is taken as uint8 */
+enum { F32 = 0, BF16 = 1, I32 = 2, U8 = 3, B8 = 4, F8 = 5, F8S = 6, MIN_DT = 5, NDT = 7 };
+/* float32, bfloat16, int32, uint8, bool (flags may be either), and of a cache in 8 bits
+ * float8_e4m3fn, float8_e8m0fnu (scales may be that or uint8) */
 static PyObject* dtypes[NDT];
 static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device;
 static PyObject* raw_stream; /* device index -> cudaStream_t as an int */
@@ -78,7 +78,7 @@ static int get(PyObject* o, Ten* t, int* dev) {
   PyObject* d = PyObject_GetAttr(o, s_dtype);
   if (!d) return 0;
   for (int i = 0; i < NDT; ++i)
-    if (d == dtypes[i]) t->dt = i == 4 || i == F8S ? U8 : i;
+    if (d == dtypes[i]) t->dt = i;
   Py_DECREF(d);
   if (t->dt < 0) return 0;
   PyObject* c = PyObject_CallMethodNoArgs(o, s_get_device);
@@ -116,6 +116,13 @@ static int need(PyObject* o, Ten* t, int dt, int* dev) {
 /* An optional one. */
 static int maybe(PyObject* o, Ten* t, int dt, int* dev) {
   return get(o, t, dev) && (t->nd < 0 || t->dt == dt);
+}
+/* Optional flags; required scales of a cache in 8 bits. */
+static int flags(PyObject* o, Ten* t, int* dev) {
+  return get(o, t, dev) && (t->nd < 0 || t->dt == U8 || t->dt == B8);
+}
+static int scales(PyObject* o, Ten* t, int* dev) {
+  return get(o, t, dev) && t->nd >= 0 && (t->dt == U8 || t->dt == F8S);
 }
 
 /* [rows, heads, dim] with contiguous rows; *rs = row stride. */
@@ -200,7 +207,7 @@ static PyObject* f_fwd(PyObject* self, PyObject* const* x, Py_ssize_t n) {
   const double scale = PyFloat_AsDouble(x[11]);
   const long l2 = PyObject_IsTrue(x[13]);
   if (PyErr_Occurred() || !need(x[8], &idx, I32, &g.dev) || !need(x[9], &cu, I32, &g.dev) ||
-      !maybe(x[10], &hi, U8, &g.dev) || !flat(&idx) || !flat(&cu) || cu.n[0] != idx.n[0] + 1 ||
+      !flags(x[10], &hi, &g.dev) || !flat(&idx) || !flat(&cu) || cu.n[0] != idx.n[0] + 1 ||
       (hi.nd >= 0 && (!flat(&hi) || hi.n[0] < idx.n[0])))
     return not_plain();
   Ten q;
@@ -230,7 +237,7 @@ static PyObject* f_upd(PyObject* self, PyObject* const* x, Py_ssize_t n) {
   const double scale = PyFloat_AsDouble(x[12]);
   const long l2 = PyObject_IsTrue(x[14]);
   if (PyErr_Occurred() || !need(x[8], &idx, I32, &g.dev) || !maybe(x[10], &acc, I32, &g.dev) ||
-      !maybe(x[11], &hi, U8, &g.dev) || idx.nd < 1 || idx.nd > 2 || ns < 0)
+      !flags(x[11], &hi, &g.dev) || idx.nd < 1 || idx.nd > 2 || ns < 0)
     return not_plain();
   const int64_t B = idx.n[0], w = idx.nd == 2 ? idx.n[1] : 1;
   if (w != 1 + ns || (idx.nd == 2 && w > 1 && idx.s[1] != 1) || (B > 1 && idx.s[0] != w) ||
@@ -263,7 +270,7 @@ static int cache(PyObject* ko, PyObject* vo, int dt, kv_cache_t* c, int* dev) {
 static int cache_q8(PyObject* const* x, kv_cache_q8_t* c, int* dev) {
   kv_cache_t p;
   Ten k, v;
-  if (!cache(x[0], x[1], F8, &p, dev) || !need(x[2], &k, U8, dev) || !need(x[3], &v, U8, dev) ||
+  if (!cache(x[0], x[1], F8, &p, dev) || !scales(x[2], &k, dev) || !scales(x[3], &v, dev) ||
       k.nd != 3 || v.nd != 3)
     return 0;
   const int64_t n[3] = {p.num_pages, p.page_size, p.num_kv_heads};
