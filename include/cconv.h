@@ -645,7 +645,7 @@ CCONV_API int64_t attn_decode_workspace_bytes(int32_t num_seqs, int32_t n_spec,
  * sign, 4 bits of exponent, 3 of fraction; no infinities, 0x7f and 0xff are NaN)
  * and, for each row of head_dim values, the power of two that multiplies them:
  * scale byte b stands for 2^(b - 127), 1 <= b <= 254. k_scale and v_scale are
- * [page, token of the page, kv head] views of the same strides (in bytes, any).
+ * [page, token of the page, kv head] views of the same strides (in bytes, positive).
  */
 typedef struct kv_cache_q8 {
   void* k;           /* 16-byte aligned */
@@ -663,7 +663,8 @@ typedef struct kv_cache_q8 {
  * The rows of k (after norm and rotation, in fp32) and of v are rounded once,
  * from fp32 to e4m3 (nearest even): with m the largest finite |x| of a row,
  *   e = the least integer with m <= 448 * 2^e, at least -126;
- *   value = e4m3(x * 2^-e),  scale byte = e + 127.
+ *   value = e4m3(x * 2^-e),  scale byte = e + 127
+ * (and 240 * 2^120, not 2^128, where |x| is 1.9375 * 2^127 or more).
  * A power of two costs no precision over m / 448 (e4m3 values have a step that
  * goes with their size) and multiplies without a rounding when it is read.
  * Infinities and NaN are stored as NaN, and do not enter m.
@@ -683,7 +684,8 @@ CCONV_API int attn_norm_rope_cache_q8(const void* q, int64_t q_row_stride, const
  * kv_cache_read_q8 -- rows of a cache in 8 bits as fp32 or bf16: k_out[t] and
  * v_out[t] [num_kv_heads * head_dim] are the keys and values of cache row
  * slot_mapping[t] = page * page_size + token of the page (fp32: exact; bf16: exact
- * but for magnitudes under 2^-126). Rows may be named more than once. A negative
+ * but for magnitudes under 2^-126; values of 2^128 and more, which
+ * attn_norm_rope_cache_q8 does not write, as infinity). Rows may be named more than once. A negative
  * slot leaves its rows of k_out and v_out as they are; one beyond the cache does
  * too, and sets CCONV_DERR_POSITION. head_dim is 64, 128 or 256.
  */

@@ -153,6 +153,9 @@ __global__ void __launch_bounds__(kNrThreads, BLOCKS) norm_rope_kernel(const NrA
       const uint32_t byte = q8_byte(m);
       const float f = q8_factor(byte);
       if (!in) return;
+      if (byte >= kQ8Top)
+#pragma unroll
+        for (int e = 0; e < V; ++e) x0[e] = q8_top(x0[e]), x1[e] = q8_top(x1[e]);
 #pragma unroll
       for (int e = 0; e < V; e += 4) {
         *reinterpret_cast<uint32_t*>(dst + b0 + e) =

@@ -60,4 +60,12 @@ __device__ __forceinline__ float q8_in(float x) {
   return fabsf(x) == __uint_as_float(0x7f800000u) ? __uint_as_float(0x7fc00000u) : x;
 }
 
+// Rows of this byte hold values that would be rounded to 2^128: they become the largest
+// one below that, 240 * 2^120.
+constexpr uint32_t kQ8Top = 127 + 120;
+__device__ __forceinline__ float q8_top(float x) {
+  const float top = __uint_as_float(0x7f700000u);
+  return x > top ? top : x < -top ? -top : x;
+}
+
 }  // namespace cconv
