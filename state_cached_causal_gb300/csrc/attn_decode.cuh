@@ -134,10 +134,10 @@ struct AttnGroup {
 
   __host__ __device__ __forceinline__ int64_t places() const { return full * per_full + (units - full) * per; }
   // the place of a unit's tile 0, and those of a tile
-  __device__ __forceinline__ int64_t place_of(int64_t unit) const {
+  __host__ __device__ __forceinline__ int64_t place_of(int64_t unit) const {
     return start + (unit < full ? unit * per_full : full * per_full + (unit - full) * per);
   }
-  __device__ __forceinline__ int tile_places(int64_t unit) const { return unit < full ? pair : wide; }
+  __host__ __device__ __forceinline__ int tile_places(int64_t unit) const { return unit < full ? pair : wide; }
 };
 // (LED: it is known that there is a lead, which is not looked for)
 template <bool LED = false>
@@ -269,7 +269,7 @@ __device__ __forceinline__ bool attn_split(const AttnArgs& a, int tile, int64_t 
 }
 
 // The block of the grid whose run holds this tile of the line.
-__device__ __forceinline__ int attn_block_of(int64_t tile, int64_t total, int64_t grid) {
+__host__ __device__ __forceinline__ int attn_block_of(int64_t tile, int64_t total, int64_t grid) {
   return (int)(((tile + 1) * grid - 1) / total);
 }
 

@@ -36,7 +36,7 @@
 // are before the first products (code, page table, copies) and 9 the join; seven groups of
 // 96 requests with 4 tokens, from 8 bits, 87 us. Attended one by one (attn_decode) the
 // first would read 17.5 GB.
-#include "attn_decode.cuh"
+#include "attn_line.cuh"
 #include "q8.cuh"
 #include "tc.cuh"
 
@@ -115,20 +115,9 @@ struct Wait {
 
 // ---- the line -------------------------------------------------------------------
 
-// Blocks that have a run.
-__device__ __forceinline__ int64_t runs_of(int64_t sms, int64_t total) {
-  return min(sms, total / 2);
-}
-
-struct Run {
-  int64_t p, end, total, grid;
-  int64_t line, unit;         // of group g
-  int g, lead;                // (its first request that sees the prefix)
-};
-
 // As attn_split, over the groups. The first block notes every group for the join.
 template <int D>
-__device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) {
+__device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, LineRun& r) {
   const AttnArgs& a = x.a;
   const int tid = threadIdx.x, per = (a.groups + kThreads - 1) / kThreads;
   const int g0 = min(a.groups, tid * per), g1 = min(a.groups, g0 + per);
@@ -167,7 +156,7 @@ __device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) 
   // (groups that overlap may have more rows than the call: none is taken then)
   const bool fits = us <= x.max_units;
   r.total = fits ? ls : 0;
-  r.grid = runs_of(attn_prefix_sms(a, ls, own), r.total);
+  r.grid = line_runs(attn_prefix_sms(a, ls, own), r.total);
   if (blockIdx.x == 0) {
     if (!fits && tid == 0) flag_error(a.dev_err, CCONV_DERR_GROUP);
     if (tid == 0) x.rec[a.groups] = Rec{r.total, (int32_t)r.grid, 0};
@@ -194,53 +183,6 @@ __device__ __forceinline__ bool split(const PrefixArgs& x, int64_t* sm, Run& r) 
   __syncthreads();
   r.g = (int)sm[0], r.line = sm[1], r.unit = sm[2], r.lead = (int)sm[3];
   return r.p < r.end;
-}
-
-// One segment: tiles [j0, j1) of a unit: rows [row0, row0 + rows) of group g and kv head h.
-struct Seg {
-  int first, prefix;          // the group's first request, and its prefix
-  int lead;                   // the request whose table names the prefix
-  int h, j0, j1, rows, row0;
-  int64_t slot;
-  bool pair;                  // two row tiles on the same positions
-};
-// The run's next segment; false behind the last.
-template <int D>
-__device__ __forceinline__ bool segment(const PrefixArgs& x, Run& r, Seg& s) {
-  using S = Shape<D>;
-  while (r.p < r.end) {
-    AttnGroup g = attn_group_of<true>(x.a, r.g);
-    while (r.p >= r.line + g.places()) {      // (groups without units, too)
-      r.line += g.places();
-      r.unit += g.units;
-      g = attn_group_of(x.a, ++r.g);
-      r.lead = g.lead;
-    }
-    int64_t rel = r.p - r.line;
-    const bool whole = rel < g.full * g.per_full;
-    if (!whole) rel -= g.full * g.per_full;
-    const int per = whole ? g.per_full : g.per, wide = whole ? g.pair : g.wide;
-    // (a 64-bit division takes a hundred instructions)
-    int u = rel <= INT32_MAX ? (int)((uint32_t)rel / (uint32_t)per) : (int)(rel / per);
-    const int off = (int)(rel - (int64_t)u * per);
-    const int take = (int)min((int64_t)(per - off), r.end - r.p);
-    r.p += take;
-    // (wide is 1 or 2)
-    s.j0 = max(off - g.start + wide - 1, 0) >> (wide - 1);
-    s.j1 = max(off + take - g.start + wide - 1, 0) >> (wide - 1);
-    if (s.j1 <= s.j0) continue;
-    if (!whole) u += (int)g.full;
-    const int mt = u / x.a.Hkv;
-    s.first = g.first, s.prefix = g.prefix, s.lead = r.lead;
-    s.h = u - mt * x.a.Hkv;
-    s.row0 = mt * S::kRowsU;
-    s.rows = min(S::kRowsU, (int)g.rows - s.row0);
-    s.pair = S::NT == 2 && s.rows > 128;
-    // from one segment to the next the unit's number or the block's rises
-    s.slot = r.unit + u + blockIdx.x;
-    return true;
-  }
-  return false;
 }
 
 // ---- copies ---------------------------------------------------------------------
@@ -279,7 +221,7 @@ struct Row {
 };
 
 template <int D, bool Q8>
-__device__ __forceinline__ bool copy_role(const PrefixArgs& x, Run run, Ctl& c,
+__device__ __forceinline__ bool copy_role(const PrefixArgs& x, LineRun run, Ctl& c,
                                           unsigned char* ring, unsigned char* raw,
                                           const Wait& wait) {
   using S = Shape<D, Q8>;
@@ -291,7 +233,7 @@ __device__ __forceinline__ bool copy_role(const PrefixArgs& x, Run run, Ctl& c,
   const int sub = lane / kLanes, u = lane % kLanes;
   // The items one after the other, over the run's segments: pages are looked up, and
   // scales and (in 8 bits) values requested, some items before they are needed.
-  Seg s;
+  LineSeg s;
   int i = 0, n = 0, seq = 0;
   bool more = true;
   auto next = [&]() {
@@ -299,7 +241,7 @@ __device__ __forceinline__ bool copy_role(const PrefixArgs& x, Run run, Ctl& c,
     if (more && i == 2 * n) {
       seq += n;
       i = 0;
-      more = segment<D>(x, run, s);
+      more = line_segment<Shape<D>::kRowsU>(x.a, blockIdx.x, run, s);
       n = more ? s.j1 - s.j0 : 0;
       if (more && s.lead != s.first &&
           (uint32_t)a.table[(int64_t)s.lead * a.table_rs] >= (uint32_t)a.num_pages)
@@ -432,7 +374,7 @@ __host__ __device__ constexpr int chunk_at(int j) {
 }
 
 template <int D, bool Q8>
-__device__ __forceinline__ bool mma_role(const PrefixArgs& x, Run run, Ctl& c, uint32_t q_addr,
+__device__ __forceinline__ bool mma_role(const PrefixArgs& x, LineRun run, Ctl& c, uint32_t q_addr,
                                          uint32_t ring, const Wait& wait, uint32_t tmem) {
   using S = Shape<D, Q8>;
   constexpr uint32_t kIdS = tc::idesc(128, S::kN), kIdO = tc::idesc(128, D, false, true);
@@ -486,8 +428,8 @@ __device__ __forceinline__ bool mma_role(const PrefixArgs& x, Run run, Ctl& c, u
   // (read from one lane, as below: the products take their operands from uniform
   // registers, where the compiler keeps what it knows to be the same in the warp)
   auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
-  Seg s;
-  while (same(segment<D>(x, run, s))) {
+  LineSeg s;
+  while (same(line_segment<Shape<D>::kRowsU>(x.a, blockIdx.x, run, s))) {
     const int n = same(s.j1 - s.j0);
     const bool pair = same(s.pair);
     if (!wait(&c.q_full[0], segs[0]++)) return false;
@@ -544,7 +486,7 @@ __device__ __forceinline__ bool mma_role(const PrefixArgs& x, Run run, Ctl& c, u
 
 // Writes the statistics of a part without positions.
 template <int D>
-__device__ __forceinline__ void empty_part(const PrefixArgs& x, const Seg& s, int stream) {
+__device__ __forceinline__ void empty_part(const PrefixArgs& x, const LineSeg& s, int stream) {
   using S = Shape<D>;
   const int r = threadIdx.x & 127;
   x.ps[s.slot * S::kRowsU + stream * 128 + r] = make_float2(-INFINITY, 0.0f);
@@ -577,7 +519,7 @@ __device__ __noinline__ void hide(uint32_t sc, const uint32_t (&keep)[N / 32]) {
 }
 
 template <int D>
-__device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, unsigned char* q_all,
+__device__ __forceinline__ bool soft_role(const PrefixArgs& x, LineRun run, Ctl& c, unsigned char* q_all,
                                           const Wait& wait, uint32_t tmem, int stream) {
   using S = Shape<D>;
   const AttnArgs& a = x.a;
@@ -590,10 +532,10 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
   const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
   int tiles_done = 0, segs = 0, seq = 0;
   bool ok = true;
-  auto valid_of = [&](const Seg& s) { return s.rows - (s.pair ? stream * 128 : 0); };
+  auto valid_of = [&](const LineSeg& s) { return s.rows - (s.pair ? stream * 128 : 0); };
   // Where row r of a segment's Q begins (-1: no row; the even and the odd tiles of one
   // row tile share the first stream's).
-  auto q_row = [&](const Seg& s) {
+  auto q_row = [&](const LineSeg& s) {
     int64_t mine = -1;
     if (r < valid_of(s) && (stream == 0 || s.pair)) {
       const uint32_t R = (uint32_t)(s.row0 + stream * 128 + r), b = R / (uint32_t)rows_all;
@@ -627,8 +569,8 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
     __syncwarp();
     if (lane == 0) mbar_arrive(&c.q_full[stream]);
   };
-  Seg s, next;
-  bool more = segment<D>(x, run, next);
+  LineSeg s, next;
+  bool more = line_segment<Shape<D>::kRowsU>(x.a, blockIdx.x, run, next);
   int64_t q_at = more ? q_row(next) : -1;
   while (more) {
     s = next;
@@ -637,7 +579,7 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, Run run, Ctl& c, 
     const int step = two ? 2 : 1, t_first = two ? stream : 0, valid = valid_of(s);
     if (ok && (stream == 0 || s.pair)) load_q(q_at);
     // the next segment's rows of Q come to the L2 meanwhile
-    more = segment<D>(x, run, next);
+    more = line_segment<Shape<D>::kRowsU>(x.a, blockIdx.x, run, next);
     q_at = more ? q_row(next) : -1;
     if (q_at >= 0)
       for (int k = 0; k < D * 2; k += 128)
@@ -808,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
   const int tid = threadIdx.x;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Run run;
+  LineRun run;
   if (!split<D>(x, c.scan, run)) return;
   if (tid == 0) {
     for (int i = 0; i < S::kStages; ++i) {
