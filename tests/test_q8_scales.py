@@ -101,6 +101,24 @@ def test_a_sink_without_a_value(dtype, hq, hkv, D, place, byte):
     assert check(q.to(dtype), *c[1:], 1, scale=30.0 / D) == 0
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@heads
+def test_sinks_each_above_the_one_before(dtype, hq, hkv, D):
+    """Positions without a value whose scores rise by 2^14 from one to the next: none of them takes the others' weights
+    away, however many there are."""
+    c = case(9, [200], hq, hkv, D, 16, 1, dtype)
+    c[3][c[3] != 255] -= 4                          # (the others' scores: 0 +- 2)
+    q = (c[0].abs() + 0.5).to(dtype)
+    for j, (k, byte) in zip((10, 40, 72, 104, 136, 168), ((0x70, 118), (0x78, 118), (0x7c, 118), (0x78, 119), (0x7a, 119),
+                                                        (0x7c, 119))):
+        at = row(c, c[5], 0, j)                     # 128, 256, 384, 512, 640, 768 times 2^-9
+        c[1].view(torch.uint8)[at] = k
+        c[3][at] = byte
+        c[2].view(torch.uint8)[at] = 0
+        c[4][at] = 119
+    assert check(q, *c[1:], 1, scale=30.0 / D) == 0
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_behind_a_shared_prefix(D):
     c = Case(7, [(100, [140, 190, 101])], 8, 2, D, 16, 1, True)
