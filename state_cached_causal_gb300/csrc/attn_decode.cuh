@@ -82,7 +82,8 @@ __host__ __device__ __forceinline__ int attn_group(const AttnArgs& a, int b) {
   const int g = lo - 1;
   return g >= 0 && a.cu_groups[g + 1] > b ? g : -1;
 }
-__host__ __device__ __forceinline__ bool attn_group_ok(const AttnArgs& a, int first, int end, int prefix) {
+__host__ __device__ __forceinline__ bool attn_group_ok(const AttnArgs& a, int first, int end,
+                                                       int prefix) {
   return first >= 0 && first <= end && end <= a.B && prefix >= 0 &&
          prefix <= (int64_t)a.table_width * a.page_size;
 }
@@ -132,12 +133,16 @@ struct AttnGroup {
   int per_full, per, wide;    // places of one of these, of another, and of a tile of that
   int start, pair;
 
-  __host__ __device__ __forceinline__ int64_t places() const { return full * per_full + (units - full) * per; }
+  __host__ __device__ __forceinline__ int64_t places() const {
+    return full * per_full + (units - full) * per;
+  }
   // the place of a unit's tile 0, and those of a tile
   __host__ __device__ __forceinline__ int64_t place_of(int64_t unit) const {
     return start + (unit < full ? unit * per_full : full * per_full + (unit - full) * per);
   }
-  __host__ __device__ __forceinline__ int tile_places(int64_t unit) const { return unit < full ? pair : wide; }
+  __host__ __device__ __forceinline__ int tile_places(int64_t unit) const {
+    return unit < full ? pair : wide;
+  }
 };
 // (LED: it is known that there is a lead, which is not looked for)
 template <bool LED = false>
@@ -168,14 +173,14 @@ __host__ __device__ __forceinline__ AttnGroup attn_group_of(const AttnArgs& a, i
 // The SMs that take the prefixes, the others taking the rest meanwhile: as the work of
 // both is, by what an SM needs for it. `places` of the prefixes, `positions` of all
 // requests that lie behind what they see of them; every block of both kernels comes to
-// the same number. (With every request counted as if it saw its prefix, 64 of 4000
-// positions in a group whose prefix is 4096 took 1149 us, where attn_decode takes 90. One after
-// the other on all SMs: 256 requests behind a long document 153 us against 146, groups in
-// 8 bits 103 to 110 against 86, 64 requests whose own 8192 positions are most of the work
-// 126 against 116, 96 behind 1024 positions 67 against 57. With at most 5/8 of the SMs
-// for the rest those 64 took 157.)
+// the same number. (Each request counts what it sees: 64 of 4000 positions in a group
+// whose prefix is 4096 take 112 us, and took 1149 counted as if they saw it. One after the
+// other on all SMs: 256 requests behind a long document 153 us against 146, groups in 8 bits
+// 103 to 110 against 86, 64 requests whose own 8192 positions are most of the work 126
+// against 116, 96 behind 1024 positions 67 against 57. With at most 5/8 of the SMs for the
+// rest those 64 took 157.)
 __host__ __device__ __forceinline__ int attn_prefix_sms(const AttnArgs& a, int64_t places,
-                                               int64_t positions) {
+                                                        int64_t positions) {
   if (places == 0) return 0;
   const int64_t tiles = (max(positions, (int64_t)0) / a.own_tile + a.B / 2) * a.units;
   const int64_t pc = places * a.place_cost, tc = tiles * a.tile_cost;

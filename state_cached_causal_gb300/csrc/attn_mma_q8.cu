@@ -33,8 +33,9 @@
 // 198 us, 5.4 TB/s. It is bound by the bytes, nearly: the copies alone, without the
 // products, take 173 (in bf16 the cache takes 340). With rows as the products' side of
 // 16 and one warp for copies and scales 270; with the scales in their own warp 216.
-// 64 requests of 4 tokens (16 rows a kv head, 127 MB): 53 us, where conversion, softmax
-// and turning the weights are what the warps' issue slots go to.
+// 64 requests of 4 tokens (16 rows a kv head, 127 MB): 54 us: twice the softmax and the
+// products a byte, whose latencies eight computing warps an SM do not hide (issue slots
+// 37 %, and some of a warp's values spilled at 168 registers).
 #include "attn_decode.cuh"
 #include "q8.cuh"
 #include "tc.cuh"

@@ -34,7 +34,7 @@
 // 146 us; a tile for two row tiles takes a block 2.5 us, 10 TFLOP/s, 0.9 of what cuBLAS
 // keeps up an SM. 8 requests behind 131072 positions 74 us for 270 MB, of which 10 to 13
 // are before the first products (code, page table, copies) and 9 the join; seven groups of
-// 96 requests with 4 tokens, from 8 bits, 87 us. Attended one by one (attn_decode) the
+// 96 requests with 4 tokens, from 8 bits, 95 us. Attended one by one (attn_decode) the
 // first would read 17.5 GB.
 #include "attn_line.cuh"
 #include "q8.cuh"
@@ -519,8 +519,9 @@ __device__ __noinline__ void hide(uint32_t sc, const uint32_t (&keep)[N / 32]) {
 }
 
 template <int D>
-__device__ __forceinline__ bool soft_role(const PrefixArgs& x, LineRun run, Ctl& c, unsigned char* q_all,
-                                          const Wait& wait, uint32_t tmem, int stream) {
+__device__ __forceinline__ bool soft_role(const PrefixArgs& x, LineRun run, Ctl& c,
+                                          unsigned char* q_all, const Wait& wait, uint32_t tmem,
+                                          int stream) {
   using S = Shape<D>;
   const AttnArgs& a = x.a;
   const int r = threadIdx.x & 127, rows_all = a.G * a.q_len;
@@ -665,37 +666,37 @@ __device__ __forceinline__ bool soft_role(const PrefixArgs& x, LineRun run, Ctl&
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-        const int k = k0 + 1 - j;
-        uint32_t(&now)[32] = v[1 - j];
+          const int k = k0 + 1 - j;
+          uint32_t(&now)[32] = v[1 - j];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t hi[8], lo[8];
+          for (int h = 0; h < 2; ++h) {
+            uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const uint32_t* w = now + h * 16 + e;
-            float p0, p1;
-            fma_x2(p0, p1, __uint_as_float(w[0]), __uint_as_float(w[1]), sl2, sl2, base, base);
-            p0 = tc::ex2(p0);
-            p1 = tc::ex2(p1);
-            fma_x2(sum, sum1, p0, p1, 1.0f, 1.0f, sum, sum1);
-            // The first term is cut a little below the weight, so that the second is above
-            // zero: terms of zero times an infinite value would make NaN.
-            float c0, c1;
-            mul_x2(c0, c1, p0, p1, 0.99609375f, 0.99609375f);
-            const uint32_t first = __byte_perm(__float_as_uint(c0), __float_as_uint(c1), 0x7632);
-            float l0, l1;
-            fma_x2(l0, l1, __uint_as_float(first << 16), __uint_as_float(first & 0xffff0000u),
-                   -1.0f, -1.0f, p0, p1);
-            hi[e / 2] = first;
-            lo[e / 2] = pack_bf16x2(l0, l1);
+            for (int e = 0; e < 16; e += 2) {
+              const uint32_t* w = now + h * 16 + e;
+              float p0, p1;
+              fma_x2(p0, p1, __uint_as_float(w[0]), __uint_as_float(w[1]), sl2, sl2, base, base);
+              p0 = tc::ex2(p0);
+              p1 = tc::ex2(p1);
+              fma_x2(sum, sum1, p0, p1, 1.0f, 1.0f, sum, sum1);
+              // The first term is cut a little below the weight, so that the second is above
+              // zero: terms of zero times an infinite value would make NaN.
+              float c0, c1;
+              mul_x2(c0, c1, p0, p1, 0.99609375f, 0.99609375f);
+              const uint32_t first = __byte_perm(__float_as_uint(c0), __float_as_uint(c1), 0x7632);
+              float l0, l1;
+              fma_x2(l0, l1, __uint_as_float(first << 16), __uint_as_float(first & 0xffff0000u),
+                     -1.0f, -1.0f, p0, p1);
+              hi[e / 2] = first;
+              lo[e / 2] = pack_bf16x2(l0, l1);
+            }
+            tc::st8(sc + k * 32 + h * 8, hi);
+            tc::st8(sc + k * 32 + 16 + h * 8, lo);
           }
-          tc::st8(sc + k * 32 + h * 8, hi);
-          tc::st8(sc + k * 32 + 16 + h * 8, lo);
-        }
-        tc::wait_st();
-        tc::fence_before();
-        __syncwarp();
-        if ((r & 31) == 0) mbar_arrive(&c.p_full[stream][k]);
+          tc::wait_st();
+          tc::fence_before();
+          __syncwarp();
+          if ((r & 31) == 0) mbar_arrive(&c.p_full[stream][k]);
         }
       }
       l += sum + sum1;
@@ -1020,8 +1021,12 @@ int decode_shared(AttnArgs& a, int D, bool q8, const void* q, int64_t q_row_stri
   a.own_tile = (q8 ? 128 : 64) / a.hw;
   a.sms = sms;
   // Measured for heads of 128: a tile of two row tiles 2.5 us, of one 1.6; from 8 bits,
-  // whose conversion bounds it, 2.8 either way; a start 8 to 10 us. A tile of the rest
-  // takes an SM 0.9 us, about as many as its share of the memory's bandwidth allows.
+  // whose conversion bounds it, 2.8 either way; a start 8 to 10 us. A tile of the rest of up
+  // to 8 rows takes an SM 0.9 us, about as many as its share of the memory's bandwidth
+  // allows. (One of 16 rows over 8 bits takes 1.3 to 1.7, but mixed calls are no faster for
+  // it: seven groups with 4 tokens 89 us, with 20 here 109, with 24 102, 64 requests mostly
+  // behind their prefix 76, 87 and 98. With 32 rows, and heads of 64 and 256, they would be:
+  // 200 us with 15, 147 with 32 for heads of 256.)
   a.start_places = q8 ? 3 : 8;
   a.pair_places = q8 ? 1 : 2;
   a.place_cost = (q8 ? 44 : 22) * (D == 64 ? 5 : 8) / 8;

@@ -4,9 +4,11 @@
 // sides of a warp are whole lines. It takes the same unit of one token after the other,
 // so that where that lies in a token is computed once, and has four tokens' bytes and
 // scales requested before the first is stored, and their successors' slots. 65536 rows
-// of 4 heads of 128 to bf16 (202 MB): 41 us, 4.9 TB/s, two thirds of it stores (units
-// dealt out in their order, with two divisions each: 47 us and 81 % of the issue slots;
-// slots not read ahead: 50 us; two or eight tokens, twice the bytes a thread: 40 to 41).
+// of 4 heads of 128 to bf16 (202 MB): 41 us, 4.9 TB/s, two thirds of it stores. The issue
+// slots bound it, at 68 %, more than HBM, at 49 %: two conversions, two multiplications and
+// a pack for two values. (Units dealt out in their order, with two divisions each: 47 us and
+// 81 % of the issue slots; slots not read ahead: 50 us; two or eight tokens, twice the bytes
+// a thread: 40 to 41.)
 #include "q8.cuh"
 
 namespace cconv {
